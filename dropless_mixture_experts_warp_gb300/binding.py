@@ -20,6 +20,9 @@ STATUS_NAMES = {0: "MOE_OK", 1: "MOE_ERR_INVALID_ARG", 2: "MOE_ERR_UNSUPPORTED",
                 4: "MOE_ERR_WORKSPACE", 5: "MOE_ERR_CUDA", 6: "MOE_ERR_TIMEOUT", 7: "MOE_ERR_INVARIANT",
                 8: "MOE_ERR_SCRATCH_LIMIT"}
 SCORE = {"softmax": 0, "sigmoid": 1}
+TYPE = {"bf16": 0, "fp32": 1}
+GATE = {"none": 0, "channel": 1, "token": 2}
+GATE_ACT = {"identity": 0, "sigmoid": 1}
 PREC = {"bf16": 0, "mxfp8": 1, "mxfp8-w4": 2}
 
 
@@ -35,6 +38,19 @@ class moe_dims(ctypes.Structure):
                 ("score", ctypes.c_int32), ("prec", ctypes.c_int32)]
 
 
+class moe_norm_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("stream_type", ctypes.c_int32),
+                ("weight_type", ctypes.c_int32), ("gate", ctypes.c_int32), ("gate_act", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float), ("alpha", ctypes.c_float),
+                ("beta", ctypes.c_float)]
+
+
+def make_norm_dims(T, d, stream="bf16", weights="fp32", gate="none", gate_act="identity", eps=1e-6,
+                   weight_offset=0.0, alpha=1.0, beta=1.0) -> moe_norm_dims:
+    return moe_norm_dims(T, d, TYPE[stream], TYPE[weights], GATE[gate], GATE_ACT[gate_act], eps, weight_offset,
+                         alpha, beta)
+
+
 def make_dims(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> moe_dims:
     return moe_dims(T, d, f, E, k, f_shared, SCORE[score] if isinstance(score, str) else score,
                     PREC[prec] if isinstance(prec, str) else prec)
@@ -43,6 +59,7 @@ def make_dims(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> moe_di
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _D = ctypes.POINTER(moe_dims)
+_N = ctypes.POINTER(moe_norm_dims)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -98,6 +115,12 @@ SIGNATURES = {
     "moe_mx4_quantize_cols": (ctypes.c_int32, [_P, _I, ctypes.c_int64, _I, _P, _P, _P, _P, _P]),
     "moe_grouped_mlp_fwd_mx": (ctypes.c_int32, [_D] + [_P] * 7),
     "moe_grouped_mlp_bwd_mx": (ctypes.c_int32, [_D] + [_P] * 11),
+    "moe_norm_check_dims": (ctypes.c_int32, [_N]),
+    "moe_norm_workspace_size": (ctypes.c_size_t, [_N]),
+    "moe_norm_fwd": (ctypes.c_int32, [_N] + [_P] * 4),
+    "moe_norm_bwd": (ctypes.c_int32, [_N] + [_P] * 8),
+    "moe_merge_fwd": (ctypes.c_int32, [_N] + [_P] * 8),
+    "moe_merge_bwd": (ctypes.c_int32, [_N] + [_P] * 14),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -133,6 +156,16 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def check_tensor(t, dtype, shape, device):
+    """Raise ValueError unless t (None passes) is a contiguous tensor of this dtype and shape on `device`: the
+    entry points see only its address."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} with strides {tuple(t.stride())} on {t.device}")
 
 
 def _call(name: str, *args):
@@ -411,3 +444,34 @@ def moe_shared_mlp_bwd_mx(dims, wq_s, mx_ws_s, gu_s, dy, dx_s, dw_gu_s, dw_d_s, 
 def moe_gemm_bf16_pair(A, B, C, M, N, K, a_layout, b_layout, dev_status, stream=None):
     return _call("moe_gemm_bf16_pair", _ptr(A), _ptr(B), _ptr(C), M, N, K, a_layout, b_layout,
                  _ptr(dev_status), _stream(stream))
+
+
+# ------------------------------------------------------------------ around the layer
+
+def moe_norm_check_dims(dims: moe_norm_dims) -> int:
+    return lib().moe_norm_check_dims(_d(dims))
+
+
+def moe_norm_workspace_size(dims: moe_norm_dims) -> int:
+    return lib().moe_norm_workspace_size(_d(dims))
+
+
+def moe_norm_fwd(dims, h, w, x, stream=None):
+    return _call("moe_norm_fwd", _d(dims), _ptr(h), _ptr(w), _ptr(x), _stream(stream))
+
+
+def moe_norm_bwd(dims, dx, h, w, dh_add, dh, dw, workspace, stream=None):
+    return _call("moe_norm_bwd", _d(dims), _ptr(dx), _ptr(h), _ptr(w), _ptr(dh_add), _ptr(dh), _ptr(dw),
+                 _ptr(workspace), _stream(stream))
+
+
+def moe_merge_fwd(dims, h, y, w_post, gate, w_next, h_out, x_next, stream=None):
+    return _call("moe_merge_fwd", _d(dims), _ptr(h), _ptr(y), _ptr(w_post), _ptr(gate), _ptr(w_next), _ptr(h_out),
+                 _ptr(x_next), _stream(stream))
+
+
+def moe_merge_bwd(dims, dh_out, dx_next, h_out, y, w_post, gate, w_next, dh, dy, dw_post, dgate, dw_next,
+                  workspace, stream=None):
+    return _call("moe_merge_bwd", _d(dims), _ptr(dh_out), _ptr(dx_next), _ptr(h_out), _ptr(y), _ptr(w_post),
+                 _ptr(gate), _ptr(w_next), _ptr(dh), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_next),
+                 _ptr(workspace), _stream(stream))

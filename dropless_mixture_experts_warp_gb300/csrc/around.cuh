@@ -1,0 +1,64 @@
+// Shared pieces of the operators around the layer (block norms, balance loss, optimiser):
+// 8-element vectors in bf16 or fp32 and sums over the threads that share a row.
+#pragma once
+
+#include "common.cuh"
+
+namespace moe {
+
+void count_launch();
+int num_sms();
+
+inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
+
+// Eight consecutive elements, widened to fp32 / rounded once from it.
+__device__ __forceinline__ void load8(const moe_bf16* p, float (&v)[8]) {
+  const uint4 q = *reinterpret_cast<const uint4*>(p);
+  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
+  v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8_as(const void* p, int type, long long at, float (&v)[8]) {
+  if (type == MOE_TYPE_BF16) load8(static_cast<const moe_bf16*>(p) + at, v);
+  else load8(static_cast<const float*>(p) + at, v);
+}
+__device__ __forceinline__ void store8(moe_bf16* p, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(p) =
+      make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// Sums of N values over a warp (WARP) or over the block, in a fixed order; every thread
+// gets them.  `buf`: 32 * N floats of shared memory that the previous sum did not use (two
+// buffers taken in turn need one barrier a sum).
+template <bool WARP, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], float* buf) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+  }
+  if (WARP) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+  if (lane == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) buf[warp * N + i] = s[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) s[i] = lane < warps ? buf[lane * N + i] : 0.0f;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+  }
+}
+
+}  // namespace moe

@@ -526,6 +526,78 @@ moe_status moe_gemm_bf16(const moe_bf16* A, const moe_bf16* B, moe_bf16* C, int3
                          int32_t N, int32_t K, int32_t a_layout, int32_t b_layout,
                          int32_t* dev_status, void* stream);
 
+/*
+ * ---------------------------------------------------------------- around the layer
+ * What a training step computes next to the layer: the norms and the residual merge of
+ * the block the layer sits in, the router's balance loss, and the optimiser step.  The
+ * conventions at the top of this file hold (caller-owned device memory, asynchronous on
+ * `stream`, host-checked arguments, no allocation, 16-byte-aligned pointers).  Repeated
+ * calls on the same inputs give the same bits: no sum depends on the order of atomics.
+ */
+enum { MOE_TYPE_BF16 = 0, MOE_TYPE_FP32 = 1 };
+enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2 };
+enum { MOE_GATE_IDENTITY = 0, MOE_GATE_SIGMOID = 1 };
+
+typedef struct moe_norm_dims {
+  int32_t T;           /* tokens (rows), 0 allowed */
+  int32_t d;           /* width: a multiple of 8, at most 16384 */
+  int32_t stream_type; /* MOE_TYPE_*: the residual stream and its gradient (h, h_out, dh_out, dh) */
+  int32_t weight_type; /* MOE_TYPE_*: the norm weights and the channel gate */
+  int32_t gate;        /* MOE_GATE_* */
+  int32_t gate_act;    /* MOE_GATE_IDENTITY or MOE_GATE_SIGMOID, applied to the gate */
+  float eps;           /* added to the mean square, > 0 */
+  float weight_offset; /* added to every norm weight (1 for weights stored around 0) */
+  float alpha;         /* scale of the residual stream in the merge */
+  float beta;          /* scale of the block's branch in the merge */
+} moe_norm_dims;
+
+/* Validates the struct against the limits above.  Host only. */
+moe_status moe_norm_check_dims(const moe_norm_dims* dims);
+
+/* Bytes of scratch of moe_norm_bwd and moe_merge_bwd (the column sums' partials). */
+size_t moe_norm_workspace_size(const moe_norm_dims* dims);
+
+/*
+ * The norm before a block, over each row h[t] of d elements:
+ *   r = 1 / sqrt(mean(h^2) + eps);  x = h * r * (w + weight_offset)
+ *   h [T][d] stream type, w [d] weight type, x [T][d] bf16.
+ * bwd:  n = dx * (w + weight_offset);  hh = h * r
+ *   dh = dh_add + r * (n - hh * mean(n * hh));  dw[j] = sum_t dx[t][j] * hh[t][j]
+ *   dx [T][d] bf16, dh_add [T][d] stream type or NULL (= 0; may be dh itself: the
+ *   gradient that reaches h around the block), dh [T][d] stream type, dw [d] fp32
+ *   (written, not added to; 0 when T = 0), workspace >= moe_norm_workspace_size bytes.
+ * All arithmetic is fp32; each output is rounded once.
+ */
+moe_status moe_norm_fwd(const moe_norm_dims* dims, const void* h, const void* w, moe_bf16* x, void* stream);
+moe_status moe_norm_bwd(const moe_norm_dims* dims, const moe_bf16* dx, const void* h, const void* w,
+                        const void* dh_add, void* dh, float* dw, void* workspace, void* stream);
+
+/*
+ * The merge after a block: the norm of its output y, the gate, the scaled residual and,
+ * in the same pass, the next block's norm:
+ *   z = y * r(y) * (w_post + weight_offset)          (w_post NULL: z = y)
+ *   h_out = alpha * h + beta * a * z,   a = 1, act(gate[j]) or act(gate[t])
+ *   x_next = h_out * r(h_out) * (w_next + weight_offset)
+ *   h [T][d] stream type, y [T][d] bf16, w_post [d], gate [d] weight type (CHANNEL),
+ *   [T] fp32 (TOKEN) or NULL (NONE), w_next [d] and x_next [T][d] bf16 both NULL for no
+ *   next norm, h_out [T][d] stream type (may be h itself).  x_next is the norm of h_out
+ *   before its rounding to the stream type.
+ * bwd: from the gradients dh_out [T][d] (stream type; NULL = 0) and dx_next [T][d] bf16
+ *   (NULL exactly when w_next is NULL; then dh_out is required):
+ *   D = dh_out + the gradient of x_next's norm (as moe_norm_bwd, of the given h_out)
+ *   dh = alpha * D (stream type; may be dh_out itself);  dy (bf16) = the gradient of
+ *   beta * a * z by y
+ *   dw_next [d], dw_post [d] fp32: given exactly when their weight is;
+ *   dgate fp32, [d] (CHANNEL) or [T] (TOKEN), by the gate before its activation; NULL
+ *   exactly when the gate is NONE.  Column sums are 0 when T = 0.
+ *   h_out is read only with w_next (else it may be NULL), y only with w_post or a gate.
+ */
+moe_status moe_merge_fwd(const moe_norm_dims* dims, const void* h, const moe_bf16* y, const void* w_post,
+                         const void* gate, const void* w_next, void* h_out, moe_bf16* x_next, void* stream);
+moe_status moe_merge_bwd(const moe_norm_dims* dims, const void* dh_out, const moe_bf16* dx_next, const void* h_out,
+                         const moe_bf16* y, const void* w_post, const void* gate, const void* w_next, void* dh,
+                         moe_bf16* dy, float* dw_post, float* dgate, float* dw_next, void* workspace, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,93 @@
+"""Plain float64 forms of the operators around the layer (NumPy), for the tests.
+
+Each gradient follows its formula; beside every result stands its majorant: the same
+expression with every term taken by its absolute value, the scale of what rounding in fp32
+can do to it.
+"""
+from __future__ import annotations
+
+import numpy as np
+
+U32 = 2.0 ** -24        # fp32: half a step, relative
+HALF_STEP = {"bf16": 2.0 ** -8, "fp32": U32}
+
+
+def _act(g, sigmoid):
+    """act(g) and its derivative."""
+    if not sigmoid:
+        return g, np.ones_like(g)
+    a = 1.0 / (1.0 + np.exp(-g))
+    return a, a * (1.0 - a)
+
+
+def rms(h, eps):
+    return 1.0 / np.sqrt((h * h).mean(axis=1, keepdims=True) + eps)
+
+
+def norm_fwd(h, w, eps, offset=0.0):
+    return h * rms(h, eps) * (w + offset)
+
+
+def _norm_grad(g, h, w, eps, offset):
+    """Gradients of norm_fwd by h and w for the output gradient g, and their majorants."""
+    r = rms(h, eps)
+    n, hh = g * (w + offset), h * r
+    dh = r * (n - hh * (n * hh).mean(axis=1, keepdims=True))
+    m = r * (abs(n) + abs(hh) * abs(n * hh).mean(axis=1, keepdims=True))
+    return dh, m, (g * hh).sum(axis=0), abs(g * hh).sum(axis=0)
+
+
+def norm_bwd(dx, h, w, eps, offset=0.0, dh_add=None):
+    dh, m, dw, mw = _norm_grad(dx, h, w, eps, offset)
+    if dh_add is not None:
+        dh, m = dh + dh_add, m + abs(dh_add)
+    return {"dh": (dh, m), "dw": (dw, mw)}
+
+
+def _gate(gate, kind, sigmoid):
+    if kind == "none":
+        return 1.0, 0.0
+    a, da = _act(gate, sigmoid)
+    return (a[None, :], da[None, :]) if kind == "channel" else (a[:, None], da[:, None])
+
+
+def merge_fwd(h, y, w_post, gate, w_next, *, eps, kind="none", sigmoid=False, offset=0.0, alpha=1.0, beta=1.0):
+    z = y if w_post is None else norm_fwd(y, w_post, eps, offset)
+    a, _ = _gate(gate, kind, sigmoid)
+    out = alpha * h + beta * a * z
+    m = abs(alpha * h) + abs(beta * a * z)
+    res = {"h_out": (out, m)}
+    if w_next is not None:
+        r = rms(out, eps)
+        x = out * r * (w_next + offset)
+        # an error of m * u in the stream reaches x through the element and through r
+        mx = m * r * abs(w_next + offset) + abs(x) * (1.0 + r * r * (m * abs(out)).mean(axis=1, keepdims=True))
+        res["x"] = (x, mx)
+    return res
+
+
+def merge_bwd(dh_out, dx, h_out, y, w_post, gate, w_next, *, eps, kind="none", sigmoid=False, offset=0.0, alpha=1.0,
+              beta=1.0):
+    res = {}
+    T, d = (dh_out if dh_out is not None else dx).shape
+    D = np.zeros((T, d)) if dh_out is None else dh_out
+    m = abs(D)
+    if w_next is not None:
+        more, mm, dw, mw = _norm_grad(dx, h_out, w_next, eps, offset)
+        D, m = D + more, m + mm
+        res["dw_next"] = (dw, mw)
+    res["dh"] = (alpha * D, abs(alpha) * m)
+    a, da = _gate(gate, kind, sigmoid)
+    dz, mz = beta * a * D, abs(beta * a) * m
+    z = y
+    if w_post is not None:
+        z = norm_fwd(y, w_post, eps, offset)
+        dy, _, dw, _ = _norm_grad(dz, y, w_post, eps, offset)
+        _, md, _, mw = _norm_grad(mz, abs(y), abs(w_post + offset), eps, 0.0)
+        res["dy"], res["dw_post"] = (dy, md), (dw, mw)
+    else:
+        res["dy"] = (dz, mz)
+    if kind != "none":
+        axis = 0 if kind == "channel" else 1
+        res["dgate"] = ((beta * da * D * z).sum(axis=axis), (abs(beta * da * z) * m).sum(axis=axis))
+    return res

@@ -1,0 +1,68 @@
+"""Refusals of the operators around the layer: found on the host, before anything is launched (CPU)."""
+import pytest
+
+
+@pytest.fixture(scope="module")
+def B():
+    from dropless_mixture_experts_warp_gb300 import build, binding
+    build.build()
+    return binding
+
+
+P = 1 << 12     # an aligned address that nothing reads
+
+
+def status(B, fn, *args):
+    before = B.moe_launch_count()
+    with pytest.raises(B.MoeError) as e:
+        getattr(B, fn)(*args, stream=0)
+    assert B.moe_launch_count() == before
+    return e.value.status
+
+
+def test_norm_dims(B):
+    good = dict(T=4, d=64)
+    assert B.moe_norm_check_dims(B.make_norm_dims(**good)) == 0
+    for bad, want in [(dict(T=-1), 1), (dict(d=0), 1), (dict(d=68), 2), (dict(d=16392), 2), (dict(eps=0.0), 1),
+                      (dict(eps=float("nan")), 1)]:
+        dims = B.make_norm_dims(**{**good, **bad})
+        assert B.moe_norm_check_dims(dims) == want, bad
+        assert B.moe_norm_workspace_size(dims) == 0
+        assert status(B, "moe_norm_fwd", dims, P, P, P) == want
+    for field, value in [("stream_type", 2), ("weight_type", -1), ("gate", 3), ("gate_act", 2)]:
+        dims = B.make_norm_dims(**good)
+        setattr(dims, field, value)
+        assert B.moe_norm_check_dims(dims) == 1, field
+
+
+def test_norm_and_merge_arguments(B):
+    dims = B.make_norm_dims(4, 64)
+    assert status(B, "moe_norm_fwd", dims, None, P, P) == 1
+    assert status(B, "moe_norm_fwd", dims, P + 8, P, P) == 3
+    assert status(B, "moe_norm_bwd", dims, P, P, P, None, P, None, P) == 1
+    assert status(B, "moe_norm_bwd", dims, P, P, P, None, P, P, None) == 4
+    assert status(B, "moe_norm_bwd", dims, P, P, P, P + 2, P, P, P) == 3
+    # h, y, w_post, gate, w_next, h_out, x_next
+    assert status(B, "moe_merge_fwd", dims, P, P, P, P, P, P, P) == 1          # a gate without a gate kind
+    assert status(B, "moe_merge_fwd", dims, P, P, P, None, None, P, P) == 1    # x_next without w_next
+    assert status(B, "moe_merge_fwd", dims, P, P, P, None, P, P, None) == 1    # w_next without x_next
+    assert status(B, "moe_merge_fwd", dims, P, P, P, None, P, P, P + 4) == 3
+    # dh_out, dx_next, h_out, y, w_post, gate, w_next, dh, dy, dw_post, dgate, dw_next, workspace
+    ok = [P, P, P, P, P, None, P, P, P, P, None, P, P]
+
+    def bwd(dims, **change):
+        names = ["dh_out", "dx_next", "h_out", "y", "w_post", "gate", "w_next", "dh", "dy", "dw_post", "dgate", "dw_next",
+                 "workspace"]
+        return status(B, "moe_merge_bwd", dims, *[change.get(n, v) for n, v in zip(names, ok)])
+
+    assert bwd(dims, dw_post=None) == 1
+    assert bwd(dims, w_next=None) == 1
+    assert bwd(dims, dx_next=None) == 1
+    assert bwd(dims, h_out=None) == 1
+    assert bwd(dims, dgate=P) == 1
+    assert bwd(dims, y=None) == 1
+    assert bwd(dims, workspace=None) == 4
+    assert bwd(dims, dy=P + 8) == 3
+    assert bwd(dims, w_next=None, dw_next=None, dx_next=None, dh_out=None) == 1   # no gradient at all
+    for gate in ("channel", "token"):
+        assert bwd(B.make_norm_dims(4, 64, gate=gate), gate=P) == 1            # no dgate
