@@ -51,6 +51,15 @@ def make_norm_dims(T, d, stream="bf16", weights="fp32", gate="none", gate_act="i
                          alpha, beta)
 
 
+class moe_balance_dims(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("k", ctypes.c_int32), ("score", ctypes.c_int32),
+                ("S", ctypes.c_int32), ("coef", ctypes.c_float), ("z_coef", ctypes.c_float)]
+
+
+def make_balance_dims(T, E, k, score="softmax", sequences=1, coef=1.0, z_coef=0.0) -> moe_balance_dims:
+    return moe_balance_dims(T, E, k, SCORE[score], sequences, coef, z_coef)
+
+
 def make_dims(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> moe_dims:
     return moe_dims(T, d, f, E, k, f_shared, SCORE[score] if isinstance(score, str) else score,
                     PREC[prec] if isinstance(prec, str) else prec)
@@ -60,6 +69,7 @@ _P = ctypes.c_void_p
 _I = ctypes.c_int32
 _D = ctypes.POINTER(moe_dims)
 _N = ctypes.POINTER(moe_norm_dims)
+_L = ctypes.POINTER(moe_balance_dims)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -121,6 +131,10 @@ SIGNATURES = {
     "moe_norm_bwd": (ctypes.c_int32, [_N] + [_P] * 8),
     "moe_merge_fwd": (ctypes.c_int32, [_N] + [_P] * 8),
     "moe_merge_bwd": (ctypes.c_int32, [_N] + [_P] * 14),
+    "moe_balance_check_dims": (ctypes.c_int32, [_L]),
+    "moe_balance_workspace_size": (ctypes.c_size_t, [_L]),
+    "moe_balance_fwd": (ctypes.c_int32, [_L] + [_P] * 11),
+    "moe_balance_bwd": (ctypes.c_int32, [_L] + [_P] * 6 + [_I, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -475,3 +489,24 @@ def moe_merge_bwd(dims, dh_out, dx_next, h_out, y, w_post, gate, w_next, dh, dy,
     return _call("moe_merge_bwd", _d(dims), _ptr(dh_out), _ptr(dx_next), _ptr(h_out), _ptr(y), _ptr(w_post),
                  _ptr(gate), _ptr(w_next), _ptr(dh), _ptr(dy), _ptr(dw_post), _ptr(dgate), _ptr(dw_next),
                  _ptr(workspace), _stream(stream))
+
+
+def moe_balance_check_dims(dims: moe_balance_dims) -> int:
+    return lib().moe_balance_check_dims(_d(dims))
+
+
+def moe_balance_workspace_size(dims: moe_balance_dims) -> int:
+    return lib().moe_balance_workspace_size(_d(dims))
+
+
+def moe_balance_fwd(dims, logits, topk_idx, seq_offsets, mask, losses, counts, prob_mean, seq_tokens, workspace,
+                    dev_status, stream=None):
+    return _call("moe_balance_fwd", _d(dims), _ptr(logits), _ptr(topk_idx), _ptr(seq_offsets), _ptr(mask),
+                 _ptr(losses), _ptr(counts), _ptr(prob_mean), _ptr(seq_tokens), _ptr(workspace), _ptr(dev_status),
+                 _stream(stream))
+
+
+def moe_balance_bwd(dims, logits, seq_offsets, mask, counts, seq_tokens, grad_losses, accumulate, d_logits,
+                    stream=None):
+    return _call("moe_balance_bwd", _d(dims), _ptr(logits), _ptr(seq_offsets), _ptr(mask), _ptr(counts),
+                 _ptr(seq_tokens), _ptr(grad_losses), int(accumulate), _ptr(d_logits), _stream(stream))

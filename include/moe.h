@@ -598,6 +598,57 @@ moe_status moe_merge_bwd(const moe_norm_dims* dims, const void* dh_out, const mo
                          const moe_bf16* y, const void* w_post, const void* gate, const void* w_next, void* dh,
                          moe_bf16* dy, float* dw_post, float* dgate, float* dw_next, void* workspace, void* stream);
 
+/*
+ * Balance loss of the router, per-expert counts and the router's z-loss, over S
+ * sequences of tokens (S = 1: the whole batch).  With the tokens t of sequence s that
+ * `mask` keeps, n_s their number, S' the sequences with n_s > 0, N = sum n_s:
+ *   p = softmax of the E logits of a token, or sigmoid(l) / sum sigmoid(l)
+ *   counts[s][e] = kept tokens of s that selected e;   f = E * counts / (k * n_s)
+ *   prob_mean[s][e] = sum_t p[t][e] / n_s  (0 where n_s = 0)
+ *   losses[0] = coef / S' * sum_s sum_e f * prob_mean
+ *   losses[1] = z_coef / N * sum_t logsumexp(l[t])^2
+ * A logit of -inf is an expert out of reach (p = 0, no gradient); a kept token with
+ * nothing but -inf has p = 0 and adds 0 to both losses; a masked token's logits are
+ * never used (NaN or infinities there change nothing).
+ */
+typedef struct moe_balance_dims {
+  int32_t T;     /* tokens, 0 allowed */
+  int32_t E;     /* experts, 1 .. 1024 */
+  int32_t k;     /* experts per token, 1 .. min(E, 32) */
+  int32_t score; /* MOE_SCORE_* */
+  int32_t S;     /* sequences, 1 .. 65535 */
+  float coef;    /* balance loss coefficient */
+  float z_coef;  /* z-loss coefficient */
+} moe_balance_dims;
+
+moe_status moe_balance_check_dims(const moe_balance_dims* dims);
+size_t moe_balance_workspace_size(const moe_balance_dims* dims);
+
+/*
+ *   logits [T][E] fp32, topk_idx [T][k] int32 (as moe_route_topk leaves them);
+ *   seq_offsets [S+1] int32 ascending, from 0 to T (NULL only when S = 1);
+ *   mask [T] uint8, 0 = padding (NULL: every token counts);
+ *   losses [2] fp32, counts [S][E] int32, prob_mean [S][E] fp32, seq_tokens [S] int32
+ *   (= n_s), workspace >= moe_balance_workspace_size bytes.
+ * dev_status gets MOE_ERR_INVARIANT for an expert index outside [0, E) (not counted)
+ * and for seq_offsets that are not ascending from 0 to T.
+ */
+moe_status moe_balance_fwd(const moe_balance_dims* dims, const float* logits, const int32_t* topk_idx,
+                           const int32_t* seq_offsets, const uint8_t* mask, float* losses, int32_t* counts,
+                           float* prob_mean, int32_t* seq_tokens, void* workspace, int32_t* dev_status,
+                           void* stream);
+
+/*
+ * Gradient of grad_losses[0] * losses[0] + grad_losses[1] * losses[1] by the logits (f
+ * is a constant: counts have no gradient).  counts and seq_tokens from the forward;
+ * grad_losses [2] fp32 on the device or NULL (= 1, 1); d_logits [T][E] fp32 is added to
+ * when accumulate is not 0 (after moe_route_topk_bwd wrote the router's own gradient;
+ * masked tokens then keep theirs), else written (0 for masked tokens).
+ */
+moe_status moe_balance_bwd(const moe_balance_dims* dims, const float* logits, const int32_t* seq_offsets,
+                           const uint8_t* mask, const int32_t* counts, const int32_t* seq_tokens,
+                           const float* grad_losses, int32_t accumulate, float* d_logits, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

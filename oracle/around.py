@@ -91,3 +91,65 @@ def merge_bwd(dh_out, dx, h_out, y, w_post, gate, w_next, *, eps, kind="none", s
         axis = 0 if kind == "channel" else 1
         res["dgate"] = ((beta * da * D * z).sum(axis=axis), (abs(beta * da * z) * m).sum(axis=axis))
     return res
+
+
+# ------------------------------------------------------------------ balance loss
+
+def probabilities(l, score):
+    """[T, E] logits -> p: the softmax of the scores' logarithms (log sigmoid(l) = -log(1 + e^-l), or l itself); a
+    row of -inf gives p = 0."""
+    g = l if score == "softmax" else -np.logaddexp(0.0, -l)
+    top = g.max(axis=1, keepdims=True)
+    e = np.exp(g - np.where(np.isneginf(top), 0.0, top))
+    s = e.sum(axis=1, keepdims=True)
+    return np.divide(e, s, out=np.zeros_like(e), where=s > 0)
+
+
+def logsumexp(l):
+    top = l.max(axis=1)
+    top = np.where(np.isneginf(top), 0.0, top)
+    s = np.exp(l - top[:, None]).sum(axis=1)
+    return np.where(s > 0, top + np.log(np.where(s > 0, s, 1.0)), 0.0)
+
+
+def balance_fwd(l, idx, offsets, mask, k, score, coef, z_coef):
+    E, S = l.shape[1], len(offsets) - 1
+    counts, mean, n = np.zeros((S, E), np.int64), np.zeros((S, E)), np.zeros(S, np.int64)
+    loss, z = 0.0, 0.0
+    for s in range(S):
+        t = np.arange(offsets[s], offsets[s + 1])
+        if mask is not None:
+            t = t[mask[t] != 0]
+        n[s] = len(t)
+        if not len(t):
+            continue
+        counts[s] = np.bincount(idx[t].ravel(), minlength=E)
+        mean[s] = probabilities(l[t], score).mean(axis=0)
+        loss += (E * counts[s] / (k * n[s]) * mean[s]).sum()
+        z += (logsumexp(l[t]) ** 2).sum()
+    return {"losses": np.array([coef * loss / max(1, (n > 0).sum()), z_coef * z / max(1, n.sum())]), "counts": counts,
+            "prob_mean": mean, "seq_tokens": n}
+
+
+def balance_bwd(l, offsets, mask, counts, n, k, score, coef, z_coef, grad=(1.0, 1.0)):
+    """Gradient by the logits and its majorant."""
+    out, maj = np.zeros_like(l), np.zeros_like(l)
+    E = l.shape[1]
+    for s in range(len(offsets) - 1):
+        t = np.arange(offsets[s], offsets[s + 1])
+        if mask is not None:
+            t = t[mask[t] != 0]
+        if not len(t):
+            continue
+        x = l[t]
+        p, q = probabilities(x, score), probabilities(x, "softmax")
+        f = E * counts[s] / (k * n[s])
+        g = grad[0] * coef / (n > 0).sum() / n[s]
+        m = (f * p).sum(axis=1, keepdims=True)
+        d, md = g * p * (f - m), abs(g) * p * (f + m)
+        if score == "sigmoid":
+            with np.errstate(over="ignore"):
+                d, md = d / (1 + np.exp(x)), md / (1 + np.exp(x))
+        zz = grad[1] * z_coef * 2 / n.sum() * logsumexp(x)[:, None] * q
+        out[t], maj[t] = d + zz, md + abs(zz)
+    return out, maj

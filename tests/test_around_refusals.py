@@ -66,3 +66,27 @@ def test_norm_and_merge_arguments(B):
     assert bwd(dims, w_next=None, dw_next=None, dx_next=None, dh_out=None) == 1   # no gradient at all
     for gate in ("channel", "token"):
         assert bwd(B.make_norm_dims(4, 64, gate=gate), gate=P) == 1            # no dgate
+
+
+def test_balance_dims_and_arguments(B):
+    good = dict(T=64, E=8, k=2)
+    assert B.moe_balance_check_dims(B.make_balance_dims(**good)) == 0
+    for bad, want in [(dict(T=-1), 1), (dict(E=0), 1), (dict(k=9), 1), (dict(k=0), 1), (dict(E=64, k=33), 1),
+                      (dict(sequences=0), 1), (dict(E=1025), 2), (dict(sequences=65536), 2),
+                      (dict(coef=float("inf")), 1), (dict(z_coef=float("nan")), 1)]:
+        dims = B.make_balance_dims(**{**good, **bad})
+        assert B.moe_balance_check_dims(dims) == want, bad
+        assert B.moe_balance_workspace_size(dims) == 0
+    one, two = B.make_balance_dims(**good), B.make_balance_dims(sequences=2, **good)
+    # logits, topk_idx, seq_offsets, mask, losses, counts, prob_mean, seq_tokens, workspace, dev_status
+    assert status(B, "moe_balance_fwd", one, None, P, None, None, P, P, P, P, P, P) == 1
+    assert status(B, "moe_balance_fwd", one, P, P, None, None, None, P, P, P, P, P) == 1
+    assert status(B, "moe_balance_fwd", one, P, P, None, None, P, P, P, P, P, None) == 1
+    assert status(B, "moe_balance_fwd", one, P, P, None, None, P, P, P, P, None, P) == 4
+    assert status(B, "moe_balance_fwd", one, P + 4, P, None, None, P, P, P, P, P, P) == 3
+    assert status(B, "moe_balance_fwd", two, P, P, None, None, P, P, P, P, P, P) == 1
+    # logits, seq_offsets, mask, counts, seq_tokens, grad_losses, accumulate, d_logits
+    assert status(B, "moe_balance_bwd", one, P, None, None, None, P, None, 1, P) == 1
+    assert status(B, "moe_balance_bwd", one, P, None, None, P, P, None, 1, None) == 1
+    assert status(B, "moe_balance_bwd", two, P, None, None, P, P, None, 1, P) == 1
+    assert status(B, "moe_balance_bwd", one, P, None, None, P, P, None, 1, P + 8) == 3

@@ -61,3 +61,28 @@ def test_merge_gradients_are_the_differences(kind, sigmoid, post):
     assert set(got) == set(wanted)
     for name, x in wanted.items():
         assert abs(got[name][0] - differences(both, x, gg)).max() < TOL, name
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_balance_gradient_is_the_difference(score):
+    rng = np.random.default_rng(3)
+    T, E, k = 12, 6, 2
+    l = rng.standard_normal((T, E))
+    idx = np.argsort(-l, axis=1)[:, :k].copy()
+    mask = np.ones(T, np.uint8)
+    mask[[4, 11]] = 0
+    offsets = np.array([0, 5, 5, 12])
+    fwd = oa.balance_fwd(l, idx, offsets, mask, k, score, 0.7, 0.3)
+    assert fwd["seq_tokens"].tolist() == [4, 0, 6] and fwd["counts"].sum() == k * 10
+    grad = (1.5, 0.5)
+    got, _ = oa.balance_bwd(l, offsets, mask, fwd["counts"], fwd["seq_tokens"], k, score, 0.7, 0.3, grad)
+    f = lambda: oa.balance_fwd(l, idx, offsets, mask, k, score, 0.7, 0.3)["losses"]  # noqa: E731
+    assert abs(got - differences(f, l, np.array(grad))).max() < TOL
+
+
+def test_balance_of_an_even_router_is_the_coefficient():
+    """Uniform probabilities: sum f P = (1 / E) sum f = 1, whatever the counts."""
+    l = np.zeros((8, 4))
+    idx = np.arange(8)[:, None] % 4
+    fwd = oa.balance_fwd(l, idx, np.array([0, 8]), None, 1, "softmax", 0.25, 1.0)
+    assert np.allclose(fwd["losses"], [0.25, np.log(4.0) ** 2])
