@@ -60,6 +60,18 @@ def make_balance_dims(T, E, k, score="softmax", sequences=1, coef=1.0, z_coef=0.
     return moe_balance_dims(T, E, k, SCORE[score], sequences, coef, z_coef)
 
 
+class moe_adamw_tensor(ctypes.Structure):
+    _fields_ = [("w", ctypes.c_void_p), ("w16", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p),
+                ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("weight_decay", ctypes.c_float), ("grad_type", ctypes.c_int32)]
+
+
+class moe_adamw_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int32), ("seed", ctypes.c_uint32),
+                ("bits", ctypes.c_int32)]
+
+
 def make_dims(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> moe_dims:
     return moe_dims(T, d, f, E, k, f_shared, SCORE[score] if isinstance(score, str) else score,
                     PREC[prec] if isinstance(prec, str) else prec)
@@ -70,6 +82,8 @@ _I = ctypes.c_int32
 _D = ctypes.POINTER(moe_dims)
 _N = ctypes.POINTER(moe_norm_dims)
 _L = ctypes.POINTER(moe_balance_dims)
+_T = ctypes.POINTER(moe_adamw_tensor)
+_PP = ctypes.POINTER(ctypes.c_void_p)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -135,6 +149,8 @@ SIGNATURES = {
     "moe_balance_workspace_size": (ctypes.c_size_t, [_L]),
     "moe_balance_fwd": (ctypes.c_int32, [_L] + [_P] * 11),
     "moe_balance_bwd": (ctypes.c_int32, [_L] + [_P] * 6 + [_I, _P, _P]),
+    "moe_adamw_step": (ctypes.c_int32, [ctypes.POINTER(moe_adamw_hyper), _T, _I, _P, _P]),
+    "moe_adamw_values": (ctypes.c_int32, [_T, _I, _I, _PP, _PP, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -510,3 +526,14 @@ def moe_balance_bwd(dims, logits, seq_offsets, mask, counts, seq_tokens, grad_lo
                     stream=None):
     return _call("moe_balance_bwd", _d(dims), _ptr(logits), _ptr(seq_offsets), _ptr(mask), _ptr(counts),
                  _ptr(seq_tokens), _ptr(grad_losses), int(accumulate), _ptr(d_logits), _stream(stream))
+
+
+def moe_adamw_step(hyper, tensors, count, control=None, stream=None):
+    """hyper: a moe_adamw_hyper; tensors: a ctypes array of `count` moe_adamw_tensor."""
+    return _call("moe_adamw_step", None if hyper is None else ctypes.byref(hyper), tensors, count, _ptr(control),
+                 _stream(stream))
+
+
+def moe_adamw_values(tensors, count, out_type, m_out, v_out, stream=None):
+    """m_out, v_out: ctypes arrays of `count` device pointers."""
+    return _call("moe_adamw_values", tensors, count, out_type, m_out, v_out, _stream(stream))

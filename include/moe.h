@@ -649,6 +649,70 @@ moe_status moe_balance_bwd(const moe_balance_dims* dims, const float* logits, co
                            const uint8_t* mask, const int32_t* counts, const int32_t* seq_tokens,
                            const float* grad_losses, int32_t accumulate, float* d_logits, void* stream);
 
+/*
+ * AdamW step over a list of tensors, each of n elements (any n >= 0):
+ *   g = grad_scale * grad;  m = beta1 m + (1 - beta1) g;  v = beta2 v + (1 - beta2) g^2
+ *   w = w - lr * (m / (1 - beta1^t) / (sqrt(v / (1 - beta2^t)) + eps) + weight_decay * w)
+ *   w16 = bf16(w)
+ * in fp32, with the new m and v before they are stored.
+ * bits = 32: m and v are fp32 [n].
+ * bits = 8: 128 consecutive elements share fp32 scales (m_scale, v_scale
+ *   [ceil(n / 128)], the largest |m| and the largest v of the block);  m is int8,
+ *   m = m_scale * sign(c) * (c / 127)^2;  v is uint8, v = v_scale * (c / 255)^4.  Codes
+ *   between two representable values are drawn so that their mean is the value (a
+ *   moment that moves by less than a code's width a step still moves); v > 0 never
+ *   becomes 0.  All-zero codes and scales are the state of step 0.  The draws come
+ *   from the seed, the step, the tensor's number and the element's index:
+ *     mix(x): x ^= x >> 16; x *= 0x6A09E667; x ^= x >> 15; x *= 0xBB67AE85; x ^= x >> 16
+ *     key = mix(mix(mix(seed) + t) + tensor * 0x6A09E667 + (i >> 32) * 0xBB67AE85)
+ *     u = mix((i mod 2^32) * 0x9E3779B9 + key)         (32-bit arithmetic throughout)
+ *   u's low 16 bits draw m's code, its high 16 bits v's: with k the code below and
+ *   x_k < x < x_{k+1} the block's shares, the upper one where (bits + 1/2) / 2^16 <
+ *   (x - x_k) / (x_{k+1} - x_k).
+ *   A scale below fp32's smallest normal number stores the block's moment as 0.
+ * Gradients that are not finite reach the state (of the whole block of 128 with bits =
+ * 8): a caller that checks for them sets `skip`.
+ */
+typedef struct moe_adamw_tensor {
+  float* w;            /* [n] fp32 weights, updated */
+  moe_bf16* w16;       /* [n] bf16 copy of the new weights, or NULL */
+  const void* grad;    /* [n] grad_type */
+  void* m;             /* [n] fp32 or int8 */
+  void* v;             /* [n] fp32 or uint8 */
+  float* m_scale;      /* bits = 8, else NULL */
+  float* v_scale;
+  int64_t n;
+  float weight_decay;
+  int32_t grad_type;   /* MOE_TYPE_* */
+} moe_adamw_tensor;
+
+/* What a step may take from device memory instead of the host, so that a captured step
+ * can be replayed with new values. */
+typedef struct moe_adamw_control {
+  float grad_scale; /* multiplies every gradient (clipping, loss scale) */
+  float lr_scale;   /* multiplies lr */
+  int32_t step;     /* t, >= 1 */
+  int32_t skip;     /* not 0: nothing is changed */
+} moe_adamw_control;
+
+typedef struct moe_adamw_hyper {
+  double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0 */
+  int32_t step;                 /* t, >= 1 (not used with a control) */
+  uint32_t seed;                /* bits = 8 */
+  int32_t bits;                 /* 32 or 8 */
+} moe_adamw_hyper;
+
+/* tensors: HOST array of `count` (read before the call returns); control: DEVICE, or
+ * NULL (scales 1, hyper->step, no skip). */
+moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* tensors, int32_t count,
+                          const moe_adamw_control* control, void* stream);
+
+/* The values that 8-bit states stand for (checkpoints, statistics): for each tensor its m
+ * into m_out[i] and its v into v_out[i] (HOST arrays of `count` device pointers, [n] of
+ * out_type; w, w16 and grad of the tensors are not used). */
+moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int32_t out_type, void* const* m_out,
+                            void* const* v_out, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

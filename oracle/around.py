@@ -153,3 +153,64 @@ def balance_bwd(l, offsets, mask, counts, n, k, score, coef, z_coef, grad=(1.0, 
         zz = grad[1] * z_coef * 2 / n.sum() * logsumexp(x)[:, None] * q
         out[t], maj[t] = d + zz, md + abs(zz)
     return out, maj
+
+
+# ------------------------------------------------------------------ AdamW
+
+ADAM_BLOCK = 128
+
+
+def adamw(w, g, m, v, *, t, lr, beta1, beta2, eps, wd, grad_scale=1.0):
+    """One step in float64: new w, m, v."""
+    g = grad_scale * g
+    m = beta1 * m + (1 - beta1) * g
+    v = beta2 * v + (1 - beta2) * g * g
+    w = w - lr * (m / (1 - beta1 ** t) / (np.sqrt(v / (1 - beta2 ** t)) + eps) + wd * w)
+    return w, m, v
+
+
+def _mix(x):
+    x = x.astype(np.uint32)
+    x ^= x >> np.uint32(16)
+    x *= np.uint32(0x6A09E667)
+    x ^= x >> np.uint32(15)
+    x *= np.uint32(0xBB67AE85)
+    return x ^ (x >> np.uint32(16))
+
+
+def adamw_draws(seed, t, tensor, n, first=0):
+    """The two numbers in (0, 1) that draw the codes of elements first .. first + n of a tensor."""
+    i = np.arange(first, first + n, dtype=np.uint64)
+    low, high = i.astype(np.uint32), (i >> np.uint64(32)).astype(np.uint32)
+    with np.errstate(over="ignore"):
+        base = _mix(_mix(np.array([seed], np.uint32)) + np.uint32(t))
+        key = _mix(base + np.array([tensor], np.uint32) * np.uint32(0x6A09E667) + high * np.uint32(0xBB67AE85))
+        u = _mix(low * np.uint32(0x9E3779B9) + key)
+    return ((u & np.uint32(0xFFFF)) + 0.5) / 65536, ((u >> np.uint32(16)) + 0.5) / 65536
+
+
+def block_scales(x):
+    """Largest |x| of each block of 128 (the last may be shorter); 0 below fp32's normal numbers."""
+    pad = np.zeros(-(-len(x) // ADAM_BLOCK) * ADAM_BLOCK)
+    pad[:len(x)] = abs(x)
+    s = pad.reshape(-1, ADAM_BLOCK).max(axis=1)
+    return np.where(s < np.finfo(np.float32).tiny, 0.0, s)
+
+
+def encode(x, scales, draws, top, power):
+    """Codes of x (signed for power 2, unsigned for power 4), and the distance of the draw from the border between
+    the two codes around x, as a share of their distance."""
+    s = np.repeat(scales, ADAM_BLOCK)[:len(x)]
+    share = np.divide(abs(x), s, out=np.zeros_like(x), where=s > 0)
+    k = np.floor(np.minimum(share, 1.0) ** (1.0 / power) * top * (1 + 1e-13))
+    lo, hi = (k / top) ** power, ((k + 1) / top) ** power
+    chance = (share - lo) / (hi - lo)
+    code = np.minimum(k + (draws < chance), top)
+    if power == 4:
+        code = np.where(share > 0, np.maximum(code, 1), code)
+    return (np.sign(x) * code).astype(np.int64), abs(draws - chance)
+
+
+def decode(code, scales, top, power):
+    s = np.repeat(scales, ADAM_BLOCK)[:len(code)]
+    return np.sign(code) * s * (abs(code) / top) ** power

@@ -90,3 +90,55 @@ def test_balance_dims_and_arguments(B):
     assert status(B, "moe_balance_bwd", one, P, None, None, P, P, None, 1, None) == 1
     assert status(B, "moe_balance_bwd", two, P, None, None, P, P, None, 1, P) == 1
     assert status(B, "moe_balance_bwd", one, P, None, None, P, P, None, 1, P + 8) == 3
+
+
+def test_adamw_arguments(B):
+    import ctypes
+
+    def step(change=None, hyper=None, count=2, bits=32):
+        h = B.moe_adamw_hyper(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1, seed=0, bits=bits)
+        for k, v in (hyper or {}).items():
+            setattr(h, k, v)
+        t = (B.moe_adamw_tensor * 2)()
+        for i in range(2):
+            t[i] = B.moe_adamw_tensor(P, P, P, P, P, P if bits == 8 else None, P if bits == 8 else None, 100, 0.1, 0)
+        for k, v in (change or {}).items():
+            setattr(t[1], k, v)
+        return status(B, "moe_adamw_step", h, t, count, None)
+
+    for field, value, want in [("w", None, 1), ("grad", None, 1), ("m", None, 1), ("v", None, 1), ("n", -1, 1),
+                               ("grad_type", 2, 1), ("m_scale", P, 1), ("weight_decay", float("inf"), 1),
+                               ("w", P + 4, 3), ("w16", P + 2, 3), ("grad", P + 8, 3), ("m", P + 1, 3)]:
+        assert step({field: value}) == want, field
+    for field, value, want in [("m_scale", None, 1), ("v_scale", None, 1), ("v_scale", P + 2, 3), ("v", P + 4, 3)]:
+        assert step({field: value}, bits=8) == want, field
+    for field, value in [("lr", -1.0), ("lr", float("nan")), ("beta1", 1.0), ("beta2", -0.1), ("eps", 0.0), ("step", 0),
+                         ("bits", 16)]:
+        assert step(hyper={field: value}) == 1, field
+    assert step(count=-1) == 1
+    h = B.moe_adamw_hyper(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1, seed=0, bits=32)
+    assert status(B, "moe_adamw_step", h, None, 1, None) == 1
+    assert status(B, "moe_adamw_step", None, None, 0, None) == 1
+    t = (B.moe_adamw_tensor * 1)(B.moe_adamw_tensor(None, None, None, P, P, P, P, 100, 0.0, 0))
+    out = lambda p: (ctypes.c_void_p * 1)(p)  # noqa: E731
+    assert status(B, "moe_adamw_values", t, 1, 2, out(P), out(P)) == 1
+    assert status(B, "moe_adamw_values", t, 1, 0, out(None), out(P)) == 1
+    assert status(B, "moe_adamw_values", t, 1, 0, out(P), out(P + 4)) == 3
+    t[0].m_scale = None
+    assert status(B, "moe_adamw_values", t, 1, 0, out(P), out(P)) == 1
+
+
+def test_adamw_plan_refuses_tensors_that_do_not_fit(B):
+    import torch
+    from dropless_mixture_experts_warp_gb300 import optim
+    w = torch.zeros(8, 16)
+    good = dict(weights=[w], grads=[w.clone()])
+    p = optim.plan(**good, bits=8)
+    assert p.m[0].dtype == torch.int8 and p.v_scale[0].shape == (1,)
+    for bad in (dict(grads=[w.half()]), dict(grads=[w[:4]]), dict(grads=[w.t()]), dict(grads=[]), dict(copies=[w]),
+                dict(bits=16), dict(weights=[w.bfloat16()]), dict(m=[w.double()]), dict(weight_decay=[0.0, 0.0]),
+                dict(m_scale=[torch.zeros(1)]), dict(bits=8, m_scale=[torch.zeros(2)])):
+        with pytest.raises(ValueError):
+            optim.plan(**{**good, **bad})
+    with pytest.raises(ValueError):
+        optim.values(optim.plan(**good))

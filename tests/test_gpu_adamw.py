@@ -1,0 +1,209 @@
+"""AdamW steps over lists of tensors against the float64 form, 32-bit and 8-bit states (GPU)."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import around as oa
+from tests.gpu_util import need_gpu
+
+pytestmark = pytest.mark.gpu
+
+U = oa.U32
+HYPER = dict(lr=1e-2, beta1=0.9, beta2=0.95, eps=1e-8)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def gpu():
+    need_gpu()
+
+
+def tensors(sizes, seed=0, scale=1e-2):
+    rng = np.random.default_rng(seed)
+    out = []
+    for n in sizes:
+        w, g = rng.standard_normal(n), rng.standard_normal(n) * scale
+        m, v = rng.standard_normal(n) * scale, (rng.standard_normal(n) * scale) ** 2
+        out.append(dict(w=w, g=g, m=m, v=v))
+    return out
+
+
+def cuda(x, kind=torch.float32):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(kind).cuda()
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def close(got, ref, majorant, terms, half=0.0):
+    """Within `terms` roundings of 2^-24 on the majorant and one of `half` on the value."""
+    assert np.all(abs(got - ref) <= half * abs(ref) + (1 + half) * terms * U * majorant + 1e-37)
+
+
+def check_step(before, w, m, v, wd, t, got_w, got_m, got_v, gs=1.0, lr_scale=1.0):
+    """Four roundings make m, five v; the update's root, quotients and bias corrections (each within 2 units, the
+    corrections of 1 - beta^t from the device's step within 8) and v's error under the root: 32 on the update."""
+    h = {**HYPER, "lr": HYPER["lr"] * lr_scale}
+    w1, m1, v1 = oa.adamw(w, before["g64"], m, v, t=t, wd=wd, grad_scale=gs, **h)
+    g = gs * before["g64"]
+    mm = HYPER["beta1"] * abs(m) + (1 - HYPER["beta1"]) * abs(g)
+    vm = HYPER["beta2"] * v + (1 - HYPER["beta2"]) * g * g
+    if got_m is not None:
+        close(got_m, m1, mm, 8)
+        close(got_v, v1, vm, 8)
+    update = mm / (1 - HYPER["beta1"] ** t) / (np.sqrt(v1 / (1 - HYPER["beta2"] ** t)) + HYPER["eps"])
+    close(got_w, w1, abs(w) + h["lr"] * (update + wd * abs(w)), 32)
+    return m1, v1, mm, vm
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [127, 128, 129, 4095, 4096, 4097], [5000, 1, 70001, 12],
+                                   list(range(1, 250))])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_32_bit(sizes, grad):
+    from dropless_mixture_experts_warp_gb300 import optim
+    ts = tensors(sizes)
+    ws, gs = [cuda(t["w"]) for t in ts], [cuda(t["g"], grad) for t in ts]
+    copies = [None if i % 3 == 1 else torch.zeros_like(w, dtype=torch.bfloat16) for i, w in enumerate(ws)]
+    decay = [0.1 * (i % 2) for i in range(len(ts))]
+    ms, vs = [cuda(t["m"]) for t in ts], [cuda(t["v"]) for t in ts]
+    p = optim.plan(ws, gs, copies=copies, weight_decay=decay, m=ms, v=vs)
+    old = [[f64(x) for x in (w, m, v)] for w, m, v in zip(ws, ms, vs)]
+    optim.step(p, step=7, **HYPER)
+    for i, t in enumerate(ts):
+        t["g64"] = f64(gs[i])
+        check_step(t, *old[i], decay[i], 7, f64(ws[i]), f64(ms[i]), f64(vs[i]))
+        if copies[i] is not None:
+            assert torch.equal(copies[i], ws[i].bfloat16())
+
+
+@pytest.mark.parametrize("sizes", [[1], [0, 3, 0], [127, 128, 129, 4095, 4096, 4097], [5000, 1, 70001, 12],
+                                   list(range(1, 250))])
+@pytest.mark.parametrize("grad", [torch.bfloat16, torch.float32])
+def test_8_bit(sizes, grad):
+    """Codes equal the definition's, except where a draw lies within fp32's roundings of the border between two."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    ts = tensors(sizes, 1)
+    ws, gs = [cuda(t["w"]) for t in ts], [cuda(t["g"], grad) for t in ts]
+    copies = [torch.zeros_like(w, dtype=torch.bfloat16) for w in ws]
+    rng = np.random.default_rng(2)
+    ms = [cuda(rng.integers(-127, 128, n), torch.int8) for n in sizes]
+    vs = [cuda(rng.integers(0, 256, n), torch.uint8) for n in sizes]
+    sm = [cuda(1e-2 * (0.5 + rng.random(-(-n // 128)))) for n in sizes]
+    sv = [cuda(1e-4 * (0.5 + rng.random(-(-n // 128)))) for n in sizes]
+    p = optim.plan(ws, gs, copies=copies, bits=8, weight_decay=0.1, m=ms, v=vs, m_scale=sm, v_scale=sv)
+    old = [(f64(ws[i]), oa.decode(f64(ms[i]), f64(sm[i]), 127, 2), oa.decode(f64(vs[i]), f64(sv[i]), 255, 4))
+           for i in range(len(sizes))]
+    optim.step(p, step=5, seed=123, **HYPER)
+    mv, vv = optim.values(p, dtype=torch.float32)
+    mb, vb = optim.values(p)
+    for i, t in enumerate(ts):
+        t["g64"] = f64(gs[i])
+        m1, v1, mm, vm = check_step(t, *old[i], 0.1, 5, f64(ws[i]), None, None)
+        assert torch.equal(copies[i], ws[i].bfloat16())
+        for x, maj, s, code, draw, top, power, val, low in ((m1, mm, sm, ms, 0, 127, 2, mv, mb), (v1, vm, sv, vs, 1, 255, 4, vv, vb)):
+            scales = f64(s[i])
+            ref = oa.block_scales(x)
+            # 16 roundings: the decoded state's 5, the moment's 5 and their products
+            limit = 16 * U * oa.block_scales(maj)
+            assert np.all(abs(scales - ref) <= limit)
+            draws = oa.adamw_draws(123, 5, i, sizes[i])[draw]
+            want, margin = oa.encode(x, ref, draws, top, power)
+            got = code[i].cpu().numpy().astype(np.int64)
+            # the share's roundings (24 of them) over the width of a code there, times the block's largest majorant
+            k = np.maximum(abs(want) - 1, 0)
+            width = ((k + 1) / top) ** power - (k / top) ** power
+            rep = np.repeat(np.divide(oa.block_scales(maj), ref, out=np.ones_like(ref), where=ref > 0), 128)[:sizes[i]]
+            near = margin <= 24 * U * rep / width
+            assert np.array_equal(got[~near], want[~near])
+            assert np.all(abs(got - want) <= 1)
+            close(f64(val[i]), oa.decode(got, scales, top, power), abs(oa.decode(got, scales, top, power)), 8)
+            assert torch.equal(low[i], val[i].bfloat16())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_steps_from_zero_train(bits):
+    """100 steps on a quadratic: both kinds of state bring the loss down to the same order, step for step repeatable."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    target = torch.linspace(-1, 1, 1000, device="cuda")
+    runs = []
+    for _ in range(2):
+        w, g = torch.zeros(1000, device="cuda"), torch.zeros(1000, device="cuda")
+        p = optim.plan([w], [g], bits=bits)
+        for t in range(1, 101):
+            torch.sub(w, target, out=g)
+            optim.step(p, lr=2e-2, step=t, seed=11)
+        runs.append(w.clone())
+    assert torch.equal(runs[0], runs[1])
+    assert float((runs[0] - target).square().mean()) < 0.05 * float(target.square().mean())
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_control_and_capture(bits):
+    """A captured step replayed with new values in device memory is the step with those values; skip changes nothing."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    sizes = [300, 4097]
+    ts = tensors(sizes, 3)
+
+    def fresh():
+        ws, gs = [cuda(t["w"]) for t in ts], [cuda(t["g"]) for t in ts]
+        return optim.plan(ws, gs, copies=[torch.zeros_like(w, dtype=torch.bfloat16) for w in ws], bits=bits)
+
+    state = lambda p: p.weights + p.copies + p.m + p.v + ((p.m_scale + p.v_scale) if bits == 8 else [])  # noqa: E731
+    p, c = fresh(), optim.Control()
+    start = [x.clone() for x in state(p)]
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        optim.step(p, step=0, seed=5, control=c, **HYPER)
+    for x, y in zip(state(p), start):
+        assert torch.equal(x, y)               # capturing runs nothing
+    c.skip.fill_(1)
+    p.grads[0].fill_(float("nan"))
+    g.replay()
+    for x, y in zip(state(p), start):
+        assert torch.equal(x, y)
+    p.grads[0].copy_(cuda(ts[0]["g"]))
+    c.skip.fill_(0)
+    old = [[f64(w), np.zeros(n), np.zeros(n)] for w, n in zip(p.weights, sizes)]
+    for t, gs, ls in ((1, 0.5, 1.0), (2, 2.0, 0.25)):
+        c.step.fill_(t)
+        c.grad_scale.fill_(gs)
+        c.lr_scale.fill_(ls)
+        g.replay()
+        if bits == 8:
+            ms, vs = optim.values(p, dtype=torch.float32)
+        else:
+            ms, vs = p.m, p.v
+        for i, x in enumerate(ts):
+            x["g64"] = f64(p.grads[i])
+            exact = bits == 32
+            check_step(x, *old[i], 0.0, t, f64(p.weights[i]), f64(ms[i]) if exact else None, f64(vs[i]) if exact else None,
+                       gs=gs, lr_scale=ls)
+            old[i] = [f64(p.weights[i]), f64(ms[i]), f64(vs[i])]
+
+
+def test_blocks_of_zeros_and_of_numbers_fp32_cannot_scale():
+    from dropless_mixture_experts_warp_gb300 import optim
+    w = torch.ones(384, device="cuda")
+    g = torch.zeros(384, device="cuda")
+    g[128:256] = 1e-38                          # m below the smallest normal number, v below any
+    g[256:] = 1e-15                             # v = 5e-32 (a normal number)
+    p = optim.plan([w], [g], bits=8)
+    for t in (1, 2):
+        optim.step(p, step=t, **HYPER)
+    assert torch.isfinite(w).all() and torch.equal(w[:128], torch.ones(128, device="cuda"))
+    assert torch.count_nonzero(p.m[0][:256]) == 0 and p.m_scale[0][:2].tolist() == [0.0, 0.0]
+    assert torch.all(p.v[0][256:] == 255) and torch.all(p.m[0][256:] == 127)
+
+
+def test_side_stream():
+    from dropless_mixture_experts_warp_gb300 import optim
+    ts = tensors([9000], 4)
+    out = []
+    for stream in (None, torch.cuda.Stream()):
+        w, g = cuda(ts[0]["w"]), cuda(ts[0]["g"])
+        p = optim.plan([w], [g], bits=8)
+        torch.cuda.synchronize()
+        optim.step(p, step=1, stream=stream, **HYPER)
+        torch.cuda.synchronize()
+        out.append((w, p.m[0], p.v[0], p.m_scale[0], p.v_scale[0]))
+    assert all(torch.equal(a, b) for a, b in zip(*out))

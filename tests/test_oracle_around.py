@@ -86,3 +86,59 @@ def test_balance_of_an_even_router_is_the_coefficient():
     idx = np.arange(8)[:, None] % 4
     fwd = oa.balance_fwd(l, idx, np.array([0, 8]), None, 1, "softmax", 0.25, 1.0)
     assert np.allclose(fwd["losses"], [0.25, np.log(4.0) ** 2])
+
+
+@pytest.mark.parametrize("top,power", [(127, 2), (255, 4)])
+def test_codes_have_the_value_as_their_mean(top, power):
+    """Over 4000 draws the mean of the decoded value is within 5 standard errors (at most half a code's width each)."""
+    rng = np.random.default_rng(4)
+    x = rng.random(128) ** 3 * 2.5e-4
+    if power == 2:
+        x *= rng.choice([-1.0, 1.0], 128)
+    s = oa.block_scales(x)
+    assert s[0] == abs(x).max()
+    got = np.stack([oa.decode(oa.encode(x, s, oa.adamw_draws(seed, 3, 1, 128)[power // 4], top, power)[0], s, top, power)
+                    for seed in range(4000)])
+    k = (abs(x) / s[0]) ** (1 / power) * top
+    width = s[0] * (((np.floor(k) + 1) / top) ** power - (np.floor(k) / top) ** power)
+    # codes of v below 1 are raised to 1: only shares above that are unbiased
+    fair = k >= 1 if power == 4 else k >= 0
+    assert fair.sum() > 100
+    assert np.all(abs(got.mean(axis=0) - x)[fair] <= 5 * 0.5 * width[fair] / np.sqrt(4000) + 1e-12 * s[0])
+    assert np.all(abs(got - x)[:, fair] <= width[fair] * (1 + 1e-9))
+    if power == 4:
+        assert np.all(got > 0)
+    assert oa.encode(np.zeros(128), np.zeros(1), np.full(128, 0.5), top, power)[0].max() == 0
+
+
+def test_draws_are_even_and_do_not_follow_each_other():
+    """The 16-bit draws of neighbouring elements, steps, tensors and seeds: means, variances and correlations within
+    5 standard errors."""
+    n = 1 << 16
+    sets = [oa.adamw_draws(*a, n) for a in [(0, 1, 0), (0, 2, 0), (0, 1, 1), (1, 1, 0)]] + [oa.adamw_draws(0, 1, 0, n, 1 << 32)]
+    flat = [u for pair in sets for u in pair]
+    for u in flat:
+        assert abs(u.mean() - 0.5) < 5 * (1 / 12) ** 0.5 / n ** 0.5
+        assert abs(u.var() - 1 / 12) < 5 * (1 / 180) ** 0.5 / n ** 0.5
+        assert abs(np.corrcoef(u[:-1], u[1:])[0, 1]) < 5 / n ** 0.5
+    for i, a in enumerate(flat):
+        for b in flat[:i]:
+            assert abs(np.corrcoef(a, b)[0, 1]) < 5 / n ** 0.5
+
+
+def test_8_bit_moments_follow_the_32_bit_ones():
+    """A moment that moves by less than a code's width a step still decays: after 2000 steps of gradients 30 times
+    smaller the mean over 512 elements is within 10% (each element's noise is under half a code: 1/15 of v at code
+    60, and 512 of them average)."""
+    rng = np.random.default_rng(6)
+    n, beta2 = 512, 0.999
+    v = np.full(n, 1.0)
+    s, code = np.ones(n // 128), np.full(n, 255)
+    for t in range(1, 2001):
+        g2 = (rng.standard_normal(n) / 30) ** 2
+        v = beta2 * v + (1 - beta2) * g2
+        new = beta2 * oa.decode(code, s, 255, 4) + (1 - beta2) * g2
+        s = oa.block_scales(new)
+        code = oa.encode(new, s, oa.adamw_draws(9, t, 0, n)[1], 255, 4)[0]
+    assert v.mean() < 0.2
+    assert abs(oa.decode(code, s, 255, 4).mean() / v.mean() - 1) < 0.1
