@@ -1,17 +1,24 @@
 // Block norms: the norm before a block, the merge after it (norm of its output, gate,
 // scaled residual, the next block's norm) and their gradients.  Every kernel reads each
-// row of its inputs once, keeps it in registers between the sums over the row and the
-// outputs, and does its arithmetic in fp32; all are bound by HBM bandwidth.
+// row of its inputs once, keeps it in shared memory and registers between the sums over
+// the row and the outputs, and does its arithmetic in fp32; all are bound by HBM.
+//
+// One block an SM, its threads in groups that each have a row: tpr threads (a multiple of
+// 32) with UPT units of U columns each, a unit being 16 bytes of the stream (8 or 16 of a
+// bf16 array).  Groups walk the rows worker, worker + workers, ...; a row's units arrive by
+// asynchronous copies in the group's ring of `stages` rows in shared memory, each thread
+// copying and reading its own units only, so that the next rows are on their way while one
+// is computed.  The weights are shared by the block's rows: as fp32, offsets added and
+// gates activated, in shared memory where that has room beside two rows a group.
 #include "around.cuh"
 
 namespace moe {
 
 constexpr int NORM_MAX_D = 16384;
-// Rows in progress at once in the backward, each with its own partial column sums:
-// blocks of a row each, or (narrow rows) warps of a row each.
-constexpr int NORM_BLOCK_WORKERS = 304;
-constexpr int NORM_WARP_WORKERS = 2432;
-constexpr int NORM_WARP_VECTORS = 64;  // rows of up to 64 8-element vectors take one warp
+constexpr int NORM_SMEM = 226 * 1024;  // dynamic shared memory of a block, its static buffers aside
+constexpr int NORM_MAX_SMS = 160;      // blocks at most
+constexpr int NORM_FWD_THREADS = 1024;
+constexpr int NORM_BWD_THREADS = 512;  // 128 registers a thread: the column sums of three weights
 
 struct NormArgs {
   int T, d;
@@ -33,307 +40,577 @@ struct NormArgs {
   float* part;          // [worker][3][d] partial sums of dw_next, dw_post, dgate
 };
 
+enum { RING_D, RING_H, RING_DX, RING_Y, RING_ARRAYS };
+enum { W_NEXT, W_POST, W_GATE, W_SLOPE, W_ARRAYS };
+
+// How the threads and the shared memory of a block are split.
+struct NormPlan {
+  int grid, groups, tpr;
+  int off[RING_ARRAYS];   // each array's place in a ring row (-1: not read)
+  int weight[W_ARRAYS];   // each weight's place, in floats (-1: read from global memory)
+  int row_bytes, weight_bytes, stages;
+};
+
 __device__ __forceinline__ float gate_act(float g, int sigmoid) { return sigmoid ? 1.0f / (1.0f + __expf(-g)) : g; }
 
-// One row per block (or per warp).  MERGE: h_out and, with w_next, its norm; else the
-// norm of h.
-template <typename ST, int VPT, bool MERGE, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) norm_fwd_kernel(const NormArgs a) {
-  __shared__ float buf[2][32];
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const long long row = WARP ? static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  if (row >= a.T) return;
-  const int nvec = a.d >> 3;
-  const long long base = row * a.d;
-  const float inv_d = 1.0f / static_cast<float>(a.d);
-  float h[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = tid + i * tpr;
-    if (v < nvec) load8(static_cast<const ST*>(a.h) + base + v * 8, h[i]);
-    else
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = 0.0f;
-  }
-  if (MERGE) {
-    float y[VPT][8];
-    float s[1] = {0.0f};
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-      if (v < nvec) load8(a.y + base + v * 8, y[i]);
-      else
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(y[i][j], y[i][j], s[0]);
-    }
-    float r = 1.0f;
-    if (a.w_post) {
-      row_sums<WARP, 1>(s, buf[0]);
-      r = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
-    }
-    float g = a.beta;
-    if (a.gate_kind == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-      if (v >= nvec) continue;
-      float w[8];
-      if (a.w_post) {
-        load8_as(a.w_post, a.weight_type, v * 8, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] = y[i][j] * r * (w[j] + a.offset);
-      }
-      if (a.gate_kind == MOE_GATE_CHANNEL) {
-        load8_as(a.gate, a.weight_type, v * 8, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[i][j] *= gate_act(w[j], a.gate_sigmoid);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[i][j] = fmaf(g, y[i][j], a.alpha * h[i][j]);
-      store8(static_cast<ST*>(a.h_out) + base + v * 8, h[i]);
-    }
-    if (!a.w_next) return;
-  }
-  float s[1] = {0.0f};
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) s[0] = fmaf(h[i][j], h[i][j], s[0]);
-  row_sums<WARP, 1>(s, buf[1]);
-  const float r = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
-#pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = tid + i * tpr;
-    if (v >= nvec) continue;
-    float w[8];
-    load8_as(a.w_next, a.weight_type, v * 8, w);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) w[j] = h[i][j] * r * (w[j] + a.offset);
-    store8(a.x + base + v * 8, w);
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+// Until the oldest of `stages` open groups of copies has arrived.
+__device__ __forceinline__ void copy_wait_oldest(int stages) {
+  switch (stages) {
+    case 1: copy_wait<0>(); break;
+    case 2: copy_wait<1>(); break;
+    case 3: copy_wait<2>(); break;
+    default: copy_wait<3>(); break;
   }
 }
 
-// Gradients.  A worker (block or warp) takes rows worker, worker + workers, ...; a thread
-// keeps its columns' sums over the worker's rows in registers and writes them as the
-// worker's partial sums, which norm_reduce_kernel adds in worker order.
+// Units of U columns as U / 2 pairs.
+template <int U>
+__device__ __forceinline__ void unpack(const moe_bf16* p, f32x2 (&v)[U / 2]) {
+  if (U == 8) {
+    const uint4 q = *reinterpret_cast<const uint4*>(p);
+    v[0] = pair(bf16_lo(q.x), bf16_hi(q.x));
+    v[1] = pair(bf16_lo(q.y), bf16_hi(q.y));
+    v[U / 2 - 2] = pair(bf16_lo(q.z), bf16_hi(q.z));
+    v[U / 2 - 1] = pair(bf16_lo(q.w), bf16_hi(q.w));
+  } else {
+    const uint2 q = *reinterpret_cast<const uint2*>(p);
+    v[0] = pair(bf16_lo(q.x), bf16_hi(q.x));
+    v[1] = pair(bf16_lo(q.y), bf16_hi(q.y));
+  }
+}
+template <int U>
+__device__ __forceinline__ void unpack(const float* p, f32x2 (&v)[U / 2]) {
+#pragma unroll
+  for (int j = 0; j < U / 4; ++j) {
+    const ulonglong2 q = reinterpret_cast<const ulonglong2*>(p)[j];
+    v[2 * j] = q.x;
+    v[2 * j + 1] = q.y;
+  }
+}
+template <int U>
+__device__ __forceinline__ void pack(moe_bf16* p, const f32x2 (&v)[U / 2]) {
+  uint32_t w[U / 2];
+#pragma unroll
+  for (int j = 0; j < U / 2; ++j) {
+    const float2 f = unpair(v[j]);
+    w[j] = pack_bf16(f.x, f.y);
+  }
+  if (U == 8) *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[U / 2 - 2], w[U / 2 - 1]);
+  else *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+template <int U>
+__device__ __forceinline__ void pack(float* p, const f32x2 (&v)[U / 2]) {
+#pragma unroll
+  for (int j = 0; j < U / 4; ++j) reinterpret_cast<ulonglong2*>(p)[j] = make_ulonglong2(v[2 * j], v[2 * j + 1]);
+}
+template <int U>
+__device__ __forceinline__ void fill(f32x2 (&v)[U / 2], float x) {
+#pragma unroll
+  for (int j = 0; j < U / 2; ++j) v[j] = pair(x, x);
+}
+
+// What a weight array holds for the kernels: weight + offset, the activated gate, its slope.
+__device__ __forceinline__ float weight_value(const NormArgs& a, int kind, float w) {
+  if (kind == W_NEXT || kind == W_POST) return w + a.offset;
+  const float g = gate_act(w, a.gate_sigmoid);
+  return kind == W_GATE ? g : g * (1.0f - g);
+}
+template <int U>
+__device__ __forceinline__ void global_weights(const NormArgs& a, int kind, int u, f32x2 (&v)[U / 2]) {
+  const void* w = kind == W_NEXT ? a.w_next : kind == W_POST ? a.w_post : a.gate;
+  if (a.weight_type == MOE_TYPE_BF16) unpack<U>(static_cast<const moe_bf16*>(w) + u * U, v);
+  else unpack<U>(static_cast<const float*>(w) + u * U, v);
+#pragma unroll
+  for (int j = 0; j < U / 2; ++j) {
+    const float2 f = unpair(v[j]);
+    v[j] = pair(weight_value(a, kind, f.x), weight_value(a, kind, f.y));
+  }
+}
+// Unit u of a weight array.  In shared memory a unit's 16-byte pieces lie `units` apart: at
+// 32-byte strides every access would take two passes.
+template <int U>
+__device__ __forceinline__ void weights(const NormArgs& a, const NormPlan& plan, const float* smem, int kind, int units,
+                                        int u, f32x2 (&v)[U / 2]) {
+  if (plan.weight[kind] >= 0) {
+    const float* w = smem + plan.weight[kind];
+#pragma unroll
+    for (int j = 0; j < U / 4; ++j) {
+      const ulonglong2 q = *reinterpret_cast<const ulonglong2*>(w + (j * units + u) * 4);
+      v[2 * j] = q.x;
+      v[2 * j + 1] = q.y;
+    }
+  } else {
+    global_weights<U>(a, kind, u, v);
+  }
+}
+// Copies the weights that have a place into shared memory (the caller synchronises).
+template <int U>
+__device__ __forceinline__ void stage_weights(const NormArgs& a, const NormPlan& plan, float* smem, int units) {
+#pragma unroll
+  for (int kind = 0; kind < W_ARRAYS; ++kind) {
+    if (plan.weight[kind] < 0) continue;
+    for (int u = threadIdx.x; u < units; u += blockDim.x) {
+      f32x2 v[U / 2];
+      global_weights<U>(a, kind, u, v);
+#pragma unroll
+      for (int j = 0; j < U / 4; ++j)
+        *reinterpret_cast<ulonglong2*>(smem + plan.weight[kind] + (j * units + u) * 4) = make_ulonglong2(v[2 * j], v[2 * j + 1]);
+    }
+  }
+}
+
+// Sums over the threads of a group, in a fixed order.  Two buffers taken in turn need one
+// barrier a sum: whoever writes a buffer again has passed the barrier of the other, which
+// its readers reach after reading.
+struct GroupSums {
+  float* buf;   // the group's 2 * 3 * (tpr / 32) floats
+  int tpr, group, tid, flip;
+  template <int N>
+  __device__ __forceinline__ void operator()(float (&s)[N]) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+    }
+    if (tpr == 32) return;
+    const int warps = tpr >> 5, lane = tid & 31;
+    float* b = buf + flip * 3 * warps;
+    flip ^= 1;
+    if (lane == 0) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) b[i * warps + (tid >> 5)] = s[i];
+    }
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = lane < warps ? b[i * warps + lane] : 0.0f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+    }
+  }
+};
+
+__device__ __forceinline__ float sum_pair(f32x2 v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
+}
+
+// MERGE: h_out and, with w_next, its norm; else the norm of h.
+template <typename ST, int UPT, bool MERGE>
+__global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float buf[2 * 3 * 32];
+  constexpr int U = 16 / sizeof(ST);
+  const int tpr = plan.tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
+  const int worker = group * gridDim.x + blockIdx.x, workers = plan.groups * gridDim.x;
+  const int units = a.d / U;
+  const float inv_d = 1.0f / static_cast<float>(a.d);
+  GroupSums sums{buf + group * 2 * 3 * (tpr >> 5), tpr, group, tid, 0};
+  const float* s_w = reinterpret_cast<const float*>(smem);
+  uint8_t* my_ring = smem + plan.weight_bytes + group * plan.stages * plan.row_bytes;
+  auto fetch = [&](long long row, int stage) {
+    if (row < a.T) {
+      const uint32_t dst = smem_u32(my_ring + stage * plan.row_bytes);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (u >= units) continue;
+        const long long at = row * a.d + u * U;
+        copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
+        if (MERGE) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
+      }
+    }
+    copy_commit();
+  };
+  // one group of copies a row: `stages` of them are open when a row's turn comes
+  for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
+  stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
+  __syncthreads();
+  const bool post = MERGE && a.w_post != nullptr, next = a.w_next != nullptr;
+  const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
+  const f32x2 alpha = pair(a.alpha, a.alpha);
+  int stage = 0;
+  for (long long row = worker; row < a.T; row += workers) {
+    const uint8_t* at = my_ring + stage * plan.row_bytes;
+    const long long base = row * a.d;
+    copy_wait_oldest(plan.stages);
+    f32x2 h[UPT][U / 2];
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      const int u = tid + i * tpr;
+      if (u < units) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
+      else fill<U>(h[i], 0.0f);
+    }
+    if (MERGE) {
+      f32x2 y[UPT][U / 2], ss = pair(0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (u < units) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y[i]);
+        else fill<U>(y[i], 0.0f);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) ss = fma2(y[i][j], y[i][j], ss);
+      }
+      float g = a.beta;
+      if (a.gate_kind == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
+      if (post) {
+        float s[1] = {sum_pair(ss)};
+        sums(s);
+        g *= 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+      }
+      const f32x2 g2 = pair(g, g);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (u >= units) continue;
+        f32x2 w[U / 2];
+        if (post) {
+          weights<U>(a, plan, s_w, W_POST, units, u, w);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
+        }
+        if (channel) {
+          weights<U>(a, plan, s_w, W_GATE, units, u, w);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) h[i][j] = fma2(g2, y[i][j], mul2(alpha, h[i][j]));
+        pack<U>(static_cast<ST*>(a.h_out) + base + u * U, h[i]);
+      }
+    }
+    f32x2 ss = pair(0.0f, 0.0f);
+#pragma unroll
+    for (int i = 0; i < UPT; ++i)
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) ss = fma2(h[i][j], h[i][j], ss);
+    // every value that the ring held was used above: the row's place is free
+    fetch(row + static_cast<long long>(plan.stages) * workers, stage);
+    stage = stage + 1 == plan.stages ? 0 : stage + 1;
+    if (!next) continue;
+    float s[1] = {sum_pair(ss)};
+    sums(s);
+    const float r = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+    const f32x2 r2 = pair(r, r);
+#pragma unroll
+    for (int i = 0; i < UPT; ++i) {
+      const int u = tid + i * tpr;
+      if (u >= units) continue;
+      f32x2 w[U / 2];
+      weights<U>(a, plan, s_w, W_NEXT, units, u, w);
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) w[j] = mul2(mul2(h[i][j], r2), w[j]);
+      pack<U>(a.x + base + u * U, w);
+    }
+  }
+}
+
+// Gradients.  A thread keeps its columns' sums over the worker's rows in registers and
+// writes them as the worker's partial sums, which norm_reduce_kernel adds in worker order.
 //   D = d_stream + r (n - h r^2 mean(n h)),  n = dx (w_next + offset)
 //   dz = beta a D,  q = dz (w_post + offset),  dy = r (q - y r^2 mean(q y))
-template <typename ST, int VPT, bool MERGE, bool WARP>
-__global__ void __launch_bounds__(WARP ? 256 : 512) norm_bwd_kernel(const NormArgs a) {
-  __shared__ float buf[2][3 * 32];
-  const int tpr = WARP ? 32 : blockDim.x;
-  const int tid = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int per = WARP ? (blockDim.x >> 5) : 1;
-  const int worker = WARP ? blockIdx.x * per + (threadIdx.x >> 5) : blockIdx.x;
-  const int workers = gridDim.x * per;
-  const int nvec = a.d >> 3;
+// What a call lacks (weights, gate) takes its neutral value, a unit at a time: a choice for
+// each element made 86 instructions an element.
+template <typename ST, int UPT, bool MERGE>
+__global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float buf[2 * 3 * 32];
+  constexpr int U = 16 / sizeof(ST);
+  const int tpr = plan.tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
+  const int worker = group * gridDim.x + blockIdx.x, workers = plan.groups * gridDim.x;
+  const int units = a.d / U;
   const float inv_d = 1.0f / static_cast<float>(a.d);
+  GroupSums sums{buf + group * 2 * 3 * (tpr >> 5), tpr, group, tid, 0};
+  const float* s_w = reinterpret_cast<const float*>(smem);
+  uint8_t* my_ring = smem + plan.weight_bytes + group * plan.stages * plan.row_bytes;
+  auto fetch = [&](long long row, int stage) {
+    if (row < a.T) {
+      const uint32_t dst = smem_u32(my_ring + stage * plan.row_bytes);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (u >= units) continue;
+        const long long at = row * a.d + u * U;
+        if (plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
+        if (plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
+        if (plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
+        if (MERGE && plan.off[RING_Y] >= 0) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
+      }
+    }
+    copy_commit();
+  };
+  for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
+  stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
+  __syncthreads();
   const bool next = a.w_next != nullptr, post = MERGE && a.w_post != nullptr;
   const int gate = MERGE ? a.gate_kind : MOE_GATE_NONE;
-  const bool need_y = post || gate != MOE_GATE_NONE;
-  float dw_next[VPT][8], dw_post[VPT][8], dgate[VPT][8];
-#pragma unroll
-  for (int i = 0; i < VPT; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw_next[i][j] = dw_post[i][j] = dgate[i][j] = 0.0f;
+  const bool channel = gate == MOE_GATE_CHANNEL, token = gate == MOE_GATE_TOKEN;
+  const bool slope = channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
 
-  int flip = 0;  // the buffer of the next sum over the row
+  f32x2 dw_next[UPT][U / 2], dw_post[UPT][U / 2], dgate[UPT][U / 2];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    fill<U>(dw_next[i], 0.0f);
+    fill<U>(dw_post[i], 0.0f);
+    fill<U>(dgate[i], 0.0f);
+  }
+  int stage = 0;
   for (long long row = worker; row < a.T; row += workers) {
     const long long base = row * a.d;
-    float D[VPT][8], h[VPT][8], n[VPT][8], y[VPT][8];
-    float s[3] = {0.0f, 0.0f, 0.0f};  // sums of h^2, n h, y^2
+    const uint8_t* at = my_ring + stage * plan.row_bytes;
+    const ST* r_d = reinterpret_cast<const ST*>(at + plan.off[RING_D]);
+    const ST* r_h = reinterpret_cast<const ST*>(at + plan.off[RING_H]);
+    const moe_bf16* r_dx = reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]);
+    const moe_bf16* r_y = reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]);
+    copy_wait_oldest(plan.stages);
+    const f32x2 zero = pair(0.0f, 0.0f);
+    f32x2 shh = zero, snh = zero, syy = zero;
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) D[i][j] = h[i][j] = n[i][j] = y[i][j] = 0.0f;
-      if (v >= nvec) continue;
-      if (a.d_stream) load8(static_cast<const ST*>(a.d_stream) + base + v * 8, D[i]);
+    for (int i = 0; i < UPT; ++i) {
+      const int u = tid + i * tpr;
+      if (u >= units) continue;
       if (next) {
-        load8(static_cast<const ST*>(a.h) + base + v * 8, h[i]);
-        load8(a.dx + base + v * 8, n[i]);
-      }
-      if (MERGE && need_y) load8(a.y + base + v * 8, y[i]);
-    }
-    if (next) {
+        f32x2 h[U / 2], n[U / 2], w[U / 2];
+        unpack<U>(r_h + u * U, h);
+        unpack<U>(r_dx + u * U, n);
+        weights<U>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * tpr;
-        if (v >= nvec) continue;
-        float w[8];
-        load8_as(a.w_next, a.weight_type, v * 8, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s[0] = fmaf(h[i][j], h[i][j], s[0]);
-          s[1] = fmaf(n[i][j] * (w[j] + a.offset), h[i][j], s[1]);
+        for (int j = 0; j < U / 2; ++j) {
+          shh = fma2(h[j], h[j], shh);
+          snh = fma2(mul2(n[j], w[j]), h[j], snh);
         }
       }
-    }
-    if (post) {
+      if (post) {
+        f32x2 y[U / 2];
+        unpack<U>(r_y + u * U, y);
 #pragma unroll
-      for (int i = 0; i < VPT; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[2] = fmaf(y[i][j], y[i][j], s[2]);
-    }
-    row_sums<WARP, 3>(s, buf[flip]);
-    flip ^= 1;
-    if (next) {
-      const float r = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
-      const float c = r * r * s[1] * inv_d;
-#pragma unroll
-      for (int i = 0; i < VPT; ++i) {
-        const int v = tid + i * tpr;
-        if (v >= nvec) continue;
-        float w[8];
-        load8_as(a.w_next, a.weight_type, v * 8, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          dw_next[i][j] = fmaf(n[i][j], h[i][j] * r, dw_next[i][j]);
-          D[i][j] = fmaf(r, n[i][j] * (w[j] + a.offset) - h[i][j] * c, D[i][j]);
-        }
+        for (int j = 0; j < U / 2; ++j) syy = fma2(y[j], y[j], syy);
       }
     }
-    float out[VPT][8];
-#pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-      if (v >= nvec) continue;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) out[i][j] = MERGE ? a.alpha * D[i][j] : D[i][j];
-      store8(static_cast<ST*>(a.dh) + base + v * 8, out[i]);
-    }
-    if (!MERGE) continue;
+    float s[3] = {sum_pair(shh), sum_pair(snh), sum_pair(syy)};
+    sums(s);
+    const float r = next ? 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps)) : 0.0f;
+    const float c = -r * r * s[1] * inv_d;
     const float ry = post ? 1.0f / sqrtf(fmaf(s[2], inv_d, a.eps)) : 1.0f;
     float tg = a.beta, tact = 1.0f;  // beta * a for the row
-    if (gate == MOE_GATE_TOKEN) {
+    if (token) {
       tact = gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
       tg *= tact;
     }
-    float s2[2] = {0.0f, 0.0f};  // sums of q y, D z
+    const f32x2 r2 = pair(r, r), c2 = pair(c, c), ry2 = pair(ry, ry), tg2 = pair(tg, tg), alpha = pair(a.alpha, a.alpha);
+    f32x2 sqy = zero, sdz = zero;
+    f32x2 q[UPT][U / 2];
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-      if (v >= nvec) continue;
-      float wp[8], wg[8];
-      if (post) load8_as(a.w_post, a.weight_type, v * 8, wp);
-      if (gate == MOE_GATE_CHANNEL) load8_as(a.gate, a.weight_type, v * 8, wg);
+    for (int i = 0; i < UPT; ++i) {
+      const int u = tid + i * tpr;
+      if (u >= units) continue;
+      f32x2 D[U / 2];
+      if (a.d_stream) unpack<U>(r_d + u * U, D);
+      else fill<U>(D, 0.0f);
+      if (next) {
+        f32x2 h[U / 2], n[U / 2], w[U / 2];
+        unpack<U>(r_h + u * U, h);
+        unpack<U>(r_dx + u * U, n);
+        weights<U>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float w = post ? wp[j] + a.offset : 1.0f;
-        const float yh = y[i][j] * ry;
-        const float Dv = D[i][j];
-        float dz = tg * Dv;
-        if (gate == MOE_GATE_CHANNEL) {
-          const float act = gate_act(wg[j], a.gate_sigmoid);
-          const float slope = a.gate_sigmoid ? act * (1.0f - act) : 1.0f;
-          dgate[i][j] = fmaf(dz * slope, yh * w, dgate[i][j]);
-          dz *= act;
-        } else if (gate == MOE_GATE_TOKEN) {
-          s2[1] = fmaf(Dv, yh * w, s2[1]);
+        for (int j = 0; j < U / 2; ++j) {
+          dw_next[i][j] = fma2(n[j], mul2(h[j], r2), dw_next[i][j]);
+          D[j] = fma2(r2, fma2(h[j], c2, mul2(n[j], w[j])), D[j]);
         }
-        dw_post[i][j] = fmaf(dz, yh, dw_post[i][j]);
-        const float q = dz * w;
-        s2[0] = fmaf(q, y[i][j], s2[0]);
-        D[i][j] = q;
+      }
+      f32x2 o[U / 2];
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) o[j] = MERGE ? mul2(alpha, D[j]) : D[j];
+      pack<U>(static_cast<ST*>(a.dh) + base + u * U, o);
+      if (MERGE) {
+        f32x2 y[U / 2], wp[U / 2], wg[U / 2], ds[U / 2];
+        if (has_y) unpack<U>(r_y + u * U, y);
+        else fill<U>(y, 0.0f);
+        if (post) weights<U>(a, plan, s_w, W_POST, units, u, wp);
+        else fill<U>(wp, 1.0f);
+        if (channel) weights<U>(a, plan, s_w, W_GATE, units, u, wg);
+        else fill<U>(wg, 1.0f);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) q[i][j] = ds[j] = mul2(tg2, D[j]);
+        if (slope) {
+          f32x2 sl[U / 2];
+          weights<U>(a, plan, s_w, W_SLOPE, units, u, sl);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) ds[j] = mul2(ds[j], sl[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) {
+          const f32x2 yh = mul2(y[j], ry2), z = mul2(yh, wp[j]);
+          dgate[i][j] = fma2(ds[j], z, dgate[i][j]);
+          sdz = fma2(D[j], z, sdz);
+          const f32x2 dz = mul2(q[i][j], wg[j]);
+          dw_post[i][j] = fma2(dz, yh, dw_post[i][j]);
+          q[i][j] = mul2(dz, wp[j]);
+          sqy = fma2(q[i][j], y[j], sqy);
+        }
       }
     }
-    float c = 0.0f;
-    if (post || gate == MOE_GATE_TOKEN) {
-      row_sums<WARP, 2>(s2, buf[flip]);
-      flip ^= 1;
-      c = ry * ry * s2[0] * inv_d;
-      if (gate == MOE_GATE_TOKEN && tid == 0)
-        a.dgate_rows[row] = a.beta * s2[1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
-    }
+    if (MERGE) {
+      if (post || token) {
+        float s2[2] = {sum_pair(sqy), sum_pair(sdz)};
+        sums(s2);
+        if (token && tid == 0)
+          a.dgate_rows[row] = a.beta * s2[1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
+        const float cy = -ry * ry * s2[0] * inv_d;
+        if (post) {
+          const f32x2 cy2 = pair(cy, cy);
 #pragma unroll
-    for (int i = 0; i < VPT; ++i) {
-      const int v = tid + i * tpr;
-      if (v >= nvec) continue;
-      float o[8];
+          for (int i = 0; i < UPT; ++i) {
+            const int u = tid + i * tpr;
+            if (u >= units) continue;
+            f32x2 y[U / 2];
+            unpack<U>(r_y + u * U, y);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] = post ? ry * (D[i][j] - y[i][j] * c) : D[i][j];
-      store8(a.dy + base + v * 8, o);
+            for (int j = 0; j < U / 2; ++j) q[i][j] = mul2(ry2, fma2(y[j], cy2, q[i][j]));
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (u < units) pack<U>(a.dy + base + u * U, q[i]);
+      }
     }
+    // every value of the row was used above: its place in the ring is free
+    fetch(row + static_cast<long long>(plan.stages) * workers, stage);
+    stage = stage + 1 == plan.stages ? 0 : stage + 1;
   }
   float* part = a.part + static_cast<long long>(worker) * 3 * a.d;
 #pragma unroll
-  for (int i = 0; i < VPT; ++i) {
-    const int v = tid + i * tpr;
-    if (v >= nvec) continue;
-    if (next) store8(part + v * 8, dw_next[i]);
-    if (post) store8(part + a.d + v * 8, dw_post[i]);
-    if (gate == MOE_GATE_CHANNEL) store8(part + 2 * a.d + v * 8, dgate[i]);
+  for (int i = 0; i < UPT; ++i) {
+    const int u = tid + i * tpr;
+    if (u >= units) continue;
+    if (next) pack<U>(part + u * U, dw_next[i]);
+    if (post) pack<U>(part + a.d + u * U, dw_post[i]);
+    if (channel) pack<U>(part + 2 * a.d + u * U, dgate[i]);
   }
 }
 
-// Column sums of the workers' partial sums, in worker order within each of the 8 lanes of
-// a column, then over the lanes.  blockIdx.y picks the sum; a NULL output is skipped.
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restrict__ part, int workers, int d,
-                                                          float* __restrict__ o0, float* __restrict__ o1,
-                                                          float* __restrict__ o2) {
-  __shared__ float4 buf[8][32];
+// Column sums of the workers' partial sums: 32 threads a column, each adding every 32nd
+// worker in order, then the 32 in order.  blockIdx.y picks the sum; a NULL output is skipped.
+constexpr int REDUCE_GROUPS = 32;
+__global__ void __launch_bounds__(32 * REDUCE_GROUPS) norm_reduce_kernel(const float* __restrict__ part, int workers, int d,
+                                                                         float* __restrict__ o0, float* __restrict__ o1,
+                                                                         float* __restrict__ o2) {
+  __shared__ float4 buf[REDUCE_GROUPS][32];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   if (!out) return;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < d) {
-#pragma unroll 4
-    for (int w = grp; w < workers; w += 8) {
+#pragma unroll 8
+    for (int w = grp; w < workers; w += REDUCE_GROUPS) {
       const float4 p = *reinterpret_cast<const float4*>(part + (static_cast<long long>(w) * 3 + blockIdx.y) * d + c);
       s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
     }
   }
   buf[grp][lane] = s;
   __syncthreads();
-  if (grp == 0 && c < d) {
-    for (int g = 1; g < 8; ++g) {
-      const float4 p = buf[g][lane];
-      s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
-    }
-    *reinterpret_cast<float4*>(out + c) = s;
+  // thread (grp, lane): column grp of the 32 lanes' 128, by shuffles over the groups
+  const float* cols = reinterpret_cast<const float*>(buf);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int col = grp * 4 + k;
+    float v = cols[lane * 128 + col];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0 && blockIdx.x * 128 + col < d) out[blockIdx.x * 128 + col] = v;
   }
 }
 
 // ------------------------------------------------------------------ launchers
 
-static int norm_workers(int d) { return (d >> 3) <= NORM_WARP_VECTORS ? NORM_WARP_WORKERS : NORM_BLOCK_WORKERS; }
+// Units of a thread: 16 columns (narrow rows: 8; beyond 8192 columns 32), so that a row has
+// at most 512 threads and its column sums stay in registers.
+static int norm_cols(int d) { return d <= 256 ? 8 : d <= 8192 ? 16 : 32; }
 
-// Threads of a block that shares a row of nvec vectors, VPT of them a thread.
-static int row_threads(int nvec, int vpt) { return ((nvec + vpt - 1) / vpt + 31) / 32 * 32; }
+// The plan for rows of d columns; used[] tells the arrays and weights of the call.
+static NormPlan norm_plan(int T, int d, int stream_size, int max_threads, const bool (&rows)[RING_ARRAYS],
+                          const bool (&w)[W_ARRAYS]) {
+  NormPlan p{};
+  p.tpr = ((d + norm_cols(d) - 1) / norm_cols(d) + 31) / 32 * 32;
+  p.groups = max_threads / p.tpr;
+  if (p.tpr > 32 && p.groups > 15) p.groups = 15;  // named barriers 1 .. 15
+  const int size[RING_ARRAYS] = {stream_size, stream_size, 2, 2};
+  for (int i = 0; i < RING_ARRAYS; ++i) {
+    p.off[i] = rows[i] ? p.row_bytes : -1;
+    if (rows[i]) p.row_bytes += d * size[i];
+  }
+  // groups as far as each has room for two rows (one row fits always: 16384 columns take at
+  // most 192 KB), then the weights, then up to four rows a group
+  while (p.groups > 1 && 2 * p.groups * p.row_bytes > NORM_SMEM) --p.groups;
+  const int row = p.groups * p.row_bytes;
+  p.stages = 2 * row <= NORM_SMEM ? 2 : 1;
+  for (int k = 0; k < W_ARRAYS; ++k) {
+    const bool fits = w[k] && p.stages * row + p.weight_bytes + d * 4 <= NORM_SMEM;
+    p.weight[k] = fits ? p.weight_bytes / 4 : -1;
+    if (fits) p.weight_bytes += d * 4;
+  }
+  while (p.stages > 1 && p.stages < 4 && (p.stages + 1) * row + p.weight_bytes <= NORM_SMEM) ++p.stages;
+  const int sms = num_sms() < NORM_MAX_SMS ? num_sms() : NORM_MAX_SMS;
+  p.grid = T < sms ? T : sms;
+  return p;
+}
 
-template <typename ST, bool MERGE>
-static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
-  if (a.T == 0) return cudaSuccess;
-  const int nvec = a.d >> 3;
-  if (nvec <= NORM_WARP_VECTORS) norm_fwd_kernel<ST, 2, MERGE, true><<<(a.T + 7) / 8, 256, 0, s>>>(a);
-  else if (nvec <= 1024) norm_fwd_kernel<ST, 2, MERGE, false><<<a.T, row_threads(nvec, 2), 0, s>>>(a);
-  else norm_fwd_kernel<ST, 4, MERGE, false><<<a.T, row_threads(nvec, 4), 0, s>>>(a);
+template <typename K>
+static cudaError_t launch_rows(K kern, const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM);
+  if (err != cudaSuccess) return err;
+  kern<<<p.grid, p.groups * p.tpr, p.weight_bytes + p.groups * p.stages * p.row_bytes, s>>>(a, p);
   count_launch();
   return cudaGetLastError();
 }
 
 template <typename ST, bool MERGE>
+static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
+  if (a.T == 0) return cudaSuccess;
+  constexpr int SZ = sizeof(ST), U = 16 / SZ;
+  const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
+  const NormPlan p = norm_plan(a.T, a.d, SZ, NORM_FWD_THREADS, {false, true, false, MERGE},
+                               {a.w_next != nullptr, a.w_post != nullptr, channel, false});
+  switch (norm_cols(a.d)) {
+    case 8: return launch_rows(norm_fwd_kernel<ST, 8 / U, MERGE>, a, p, s);
+    case 16: return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE>, a, p, s);
+    default: return launch_rows(norm_fwd_kernel<ST, 32 / U, MERGE>, a, p, s);
+  }
+}
+
+template <typename ST, bool MERGE>
 static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_post, float* dgate_cols, cudaStream_t s) {
-  const int nvec = a.d >> 3;
+  constexpr int SZ = sizeof(ST), U = 16 / SZ;
+  const bool next = a.w_next, post = MERGE && a.w_post, channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
   int workers = 0;
   if (a.T > 0) {
-    if (nvec <= NORM_WARP_VECTORS) {
-      const int grid = min((a.T + 7) / 8, NORM_WARP_WORKERS / 8);
-      workers = grid * 8;
-      norm_bwd_kernel<ST, 2, MERGE, true><<<grid, 256, 0, s>>>(a);
-    } else {
-      workers = min(a.T, NORM_BLOCK_WORKERS);
-      if (nvec <= 1024) norm_bwd_kernel<ST, 2, MERGE, false><<<workers, row_threads(nvec, 2), 0, s>>>(a);
-      else norm_bwd_kernel<ST, 4, MERGE, false><<<workers, row_threads(nvec, 4), 0, s>>>(a);
+    const NormPlan p = norm_plan(a.T, a.d, SZ, NORM_BWD_THREADS,
+                                 {a.d_stream != nullptr, next, next, post || (MERGE && a.gate_kind != MOE_GATE_NONE)},
+                                 {next, post, channel, channel && a.gate_sigmoid});
+    workers = p.grid * p.groups;
+    cudaError_t err;
+    switch (norm_cols(a.d)) {
+      case 8: err = launch_rows(norm_bwd_kernel<ST, 8 / U, MERGE>, a, p, s); break;
+      case 16: err = launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE>, a, p, s); break;
+      default: err = launch_rows(norm_bwd_kernel<ST, 32 / U, MERGE>, a, p, s); break;
     }
-    count_launch();
+    if (err != cudaSuccess) return err;
   }
   if (dw_next || dw_post || dgate_cols) {
-    norm_reduce_kernel<<<dim3((a.d + 127) / 128, 3), 256, 0, s>>>(a.part, workers, a.d, dw_next, dw_post, dgate_cols);
+    norm_reduce_kernel<<<dim3((a.d + 127) / 128, 3), 32 * REDUCE_GROUPS, 0, s>>>(a.part, workers, a.d, dw_next, dw_post,
+                                                                                 dgate_cols);
     count_launch();
   }
   return cudaGetLastError();
@@ -368,7 +645,8 @@ moe_status moe_norm_check_dims(const moe_norm_dims* dims) {
 
 size_t moe_norm_workspace_size(const moe_norm_dims* dims) {
   if (moe_norm_check_dims(dims) != MOE_OK) return 0;
-  return static_cast<size_t>(norm_workers(dims->d)) * 3 * dims->d * sizeof(float);
+  const int tpr = ((dims->d + norm_cols(dims->d) - 1) / norm_cols(dims->d) + 31) / 32 * 32;
+  return static_cast<size_t>(NORM_MAX_SMS) * (NORM_BWD_THREADS / tpr) * 3 * dims->d * sizeof(float);
 }
 
 moe_status moe_norm_fwd(const moe_norm_dims* dims, const void* h, const void* w, moe_bf16* x, void* stream) {
