@@ -10,6 +10,9 @@
 // copying and reading its own units only, so that the next rows are on their way while one
 // is computed.  The weights are shared by the block's rows: as fp32, offsets added and
 // gates activated, in shared memory where that has room beside two rows a group.
+//
+// FAST variants know at compile time what a call usually has: every weight present and in
+// shared memory, every unit inside the row, the kind of gate GATE.
 #include "around.cuh"
 
 namespace moe {
@@ -42,6 +45,7 @@ struct NormArgs {
 
 enum { RING_D, RING_H, RING_DX, RING_Y, RING_ARRAYS };
 enum { W_NEXT, W_POST, W_GATE, W_SLOPE, W_ARRAYS };
+constexpr int GATE_SLOPE = 3;  // a sigmoid channel gate, for the backward's variants
 
 // How the threads and the shared memory of a block are split.
 struct NormPlan {
@@ -136,10 +140,10 @@ __device__ __forceinline__ void global_weights(const NormArgs& a, int kind, int 
 }
 // Unit u of a weight array.  In shared memory a unit's 16-byte pieces lie `units` apart: at
 // 32-byte strides every access would take two passes.
-template <int U>
+template <int U, bool STAGED>
 __device__ __forceinline__ void weights(const NormArgs& a, const NormPlan& plan, const float* smem, int kind, int units,
                                         int u, f32x2 (&v)[U / 2]) {
-  if (plan.weight[kind] >= 0) {
+  if (STAGED || plan.weight[kind] >= 0) {
     const float* w = smem + plan.weight[kind];
 #pragma unroll
     for (int j = 0; j < U / 4; ++j) {
@@ -167,37 +171,51 @@ __device__ __forceinline__ void stage_weights(const NormArgs& a, const NormPlan&
   }
 }
 
-// Sums over the threads of a group, in a fixed order.  Two buffers taken in turn need one
-// barrier a sum: whoever writes a buffer again has passed the barrier of the other, which
-// its readers reach after reading.
+// Sums of N values over the threads of a group, in a fixed order; every thread gets them.
+// Lanes give half of the values away while they add (N = 3: 12 shuffles instead of 30).
+// Two buffers taken in turn need one barrier a sum: whoever writes a buffer again has
+// passed the barrier of the other, which its readers reach after reading.
+constexpr int ROW_WARPS = 16;  // of a group, at most
 struct GroupSums {
-  float* buf;   // the group's 2 * 3 * (tpr / 32) floats
+  float* buf;   // the group's 2 * 3 * tpr / 32 floats
   int tpr, group, tid, flip;
   template <int N>
   __device__ __forceinline__ void operator()(float (&s)[N]) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
+    constexpr unsigned ALL = 0xffffffffu;
+    constexpr int SPLIT = N == 1 ? 1 : N == 2 ? 2 : 4, WIDTH = 32 / SPLIT;
+    const int lane = tid & 31;
+    float v = s[0];
+    if (N == 2) {
+      const bool up = lane & 16;
+      v = (up ? s[N - 1] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[N - 1], 16);
+    } else if (N == 3) {
+      const bool up = lane & 16, odd = lane & 8;
+      const float x = (up ? s[N - 1] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[N - 1], 16);
+      const float y = (up ? 0.0f : s[N / 2]) + __shfl_xor_sync(ALL, up ? s[N / 2] : 0.0f, 16);
+      v = (odd ? y : x) + __shfl_xor_sync(ALL, odd ? x : y, 8);
     }
-    if (tpr == 32) return;
-    const int warps = tpr >> 5, lane = tid & 31;
-    float* b = buf + flip * 3 * warps;
-    flip ^= 1;
-    if (lane == 0) {
 #pragma unroll
-      for (int i = 0; i < N; ++i) b[i * warps + (tid >> 5)] = s[i];
+    for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(ALL, v, off);
+    const int value = lane / WIDTH;
+    if (tpr > 32) {
+      const int warps = tpr >> 5, first = lane & (WIDTH - 1);
+      float* b = buf + flip * 3 * warps;
+      flip ^= 1;
+      if (first == 0 && value < N) b[value * warps + (tid >> 5)] = v;
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+      const float* r = b + (value < N ? value : 0) * warps;
+      v = first < warps ? r[first] : 0.0f;
+      if (WIDTH < ROW_WARPS) v += first + WIDTH < warps ? r[first + WIDTH] : 0.0f;
+#pragma unroll
+      for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(ALL, v, off);
     }
-    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
 #pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = lane < warps ? b[i * warps + lane] : 0.0f;
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], off);
-    }
+    for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(ALL, v, i * WIDTH);
   }
 };
+
+// 1 / sqrt(mean + eps) of a sum of squares; within 2 units.
+__device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
 
 __device__ __forceinline__ float sum_pair(f32x2 v) {
   const float2 f = unpair(v);
@@ -205,7 +223,7 @@ __device__ __forceinline__ float sum_pair(f32x2 v) {
 }
 
 // MERGE: h_out and, with w_next, its norm; else the norm of h.
-template <typename ST, int UPT, bool MERGE>
+template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
 __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * 3 * 32];
@@ -223,7 +241,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (u >= units) continue;
+        if (!FAST && u >= units) continue;
         const long long at = row * a.d + u * U;
         copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
         if (MERGE) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
@@ -235,8 +253,9 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
-  const bool post = MERGE && a.w_post != nullptr, next = a.w_next != nullptr;
-  const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
+  const int gate = !MERGE ? MOE_GATE_NONE : FAST ? GATE : a.gate_kind;
+  const bool post = MERGE && (FAST || a.w_post != nullptr), next = FAST || a.w_next != nullptr;
+  const bool channel = gate == MOE_GATE_CHANNEL;
   const f32x2 alpha = pair(a.alpha, a.alpha);
   int stage = 0;
   for (long long row = worker; row < a.T; row += workers) {
@@ -247,7 +266,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (u < units) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
+      if (FAST || u < units) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
       else fill<U>(h[i], 0.0f);
     }
     if (MERGE) {
@@ -255,31 +274,31 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (u < units) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y[i]);
+        if (FAST || u < units) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y[i]);
         else fill<U>(y[i], 0.0f);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) ss = fma2(y[i][j], y[i][j], ss);
       }
       float g = a.beta;
-      if (a.gate_kind == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
+      if (gate == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
       if (post) {
         float s[1] = {sum_pair(ss)};
         sums(s);
-        g *= 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+        g *= inv_rms(s[0], inv_d, a.eps);
       }
       const f32x2 g2 = pair(g, g);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (u >= units) continue;
+        if (!FAST && u >= units) continue;
         f32x2 w[U / 2];
         if (post) {
-          weights<U>(a, plan, s_w, W_POST, units, u, w);
+          weights<U, FAST>(a, plan, s_w, W_POST, units, u, w);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
         }
         if (channel) {
-          weights<U>(a, plan, s_w, W_GATE, units, u, w);
+          weights<U, FAST>(a, plan, s_w, W_GATE, units, u, w);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
         }
@@ -299,14 +318,14 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
     if (!next) continue;
     float s[1] = {sum_pair(ss)};
     sums(s);
-    const float r = 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps));
+    const float r = inv_rms(s[0], inv_d, a.eps);
     const f32x2 r2 = pair(r, r);
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (u >= units) continue;
+      if (!FAST && u >= units) continue;
       f32x2 w[U / 2];
-      weights<U>(a, plan, s_w, W_NEXT, units, u, w);
+      weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
       for (int j = 0; j < U / 2; ++j) w[j] = mul2(mul2(h[i][j], r2), w[j]);
       pack<U>(a.x + base + u * U, w);
@@ -318,9 +337,8 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 // writes them as the worker's partial sums, which norm_reduce_kernel adds in worker order.
 //   D = d_stream + r (n - h r^2 mean(n h)),  n = dx (w_next + offset)
 //   dz = beta a D,  q = dz (w_post + offset),  dy = r (q - y r^2 mean(q y))
-// What a call lacks (weights, gate) takes its neutral value, a unit at a time: a choice for
-// each element made 86 instructions an element.
-template <typename ST, int UPT, bool MERGE>
+// What a call lacks (weights, gate) takes its neutral value, a unit at a time.
+template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
 __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * 3 * 32];
@@ -338,12 +356,12 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (u >= units) continue;
+        if (!FAST && u >= units) continue;
         const long long at = row * a.d + u * U;
-        if (plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
-        if (plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
-        if (plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
-        if (MERGE && plan.off[RING_Y] >= 0) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
+        if (FAST || plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
+        if (FAST || plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
+        if (FAST || plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
+        if (MERGE && (FAST || plan.off[RING_Y] >= 0)) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
       }
     }
     copy_commit();
@@ -351,10 +369,10 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
-  const bool next = a.w_next != nullptr, post = MERGE && a.w_post != nullptr;
-  const int gate = MERGE ? a.gate_kind : MOE_GATE_NONE;
+  const bool next = FAST || a.w_next != nullptr, post = MERGE && (FAST || a.w_post != nullptr);
+  const int gate = !MERGE ? MOE_GATE_NONE : !FAST ? a.gate_kind : GATE == GATE_SLOPE ? MOE_GATE_CHANNEL : GATE;
   const bool channel = gate == MOE_GATE_CHANNEL, token = gate == MOE_GATE_TOKEN;
-  const bool slope = channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
+  const bool slope = FAST ? GATE == GATE_SLOPE : channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
 
   f32x2 dw_next[UPT][U / 2], dw_post[UPT][U / 2], dgate[UPT][U / 2];
 #pragma unroll
@@ -377,12 +395,12 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (u >= units) continue;
+      if (!FAST && u >= units) continue;
       if (next) {
         f32x2 h[U / 2], n[U / 2], w[U / 2];
         unpack<U>(r_h + u * U, h);
         unpack<U>(r_dx + u * U, n);
-        weights<U>(a, plan, s_w, W_NEXT, units, u, w);
+        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) {
           shh = fma2(h[j], h[j], shh);
@@ -398,29 +416,29 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
     }
     float s[3] = {sum_pair(shh), sum_pair(snh), sum_pair(syy)};
     sums(s);
-    const float r = next ? 1.0f / sqrtf(fmaf(s[0], inv_d, a.eps)) : 0.0f;
+    const float r = next ? inv_rms(s[0], inv_d, a.eps) : 0.0f;
     const float c = -r * r * s[1] * inv_d;
-    const float ry = post ? 1.0f / sqrtf(fmaf(s[2], inv_d, a.eps)) : 1.0f;
+    const float ry = post ? inv_rms(s[2], inv_d, a.eps) : 1.0f;
     float tg = a.beta, tact = 1.0f;  // beta * a for the row
     if (token) {
       tact = gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
       tg *= tact;
     }
-    const f32x2 r2 = pair(r, r), c2 = pair(c, c), ry2 = pair(ry, ry), tg2 = pair(tg, tg), alpha = pair(a.alpha, a.alpha);
+    const f32x2 r2 = pair(r, r), c2 = pair(c, c), ry2 = pair(ry, ry), tg2 = pair(tg, tg);
     f32x2 sqy = zero, sdz = zero;
     f32x2 q[UPT][U / 2];
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (u >= units) continue;
+      if (!FAST && u >= units) continue;
       f32x2 D[U / 2];
-      if (a.d_stream) unpack<U>(r_d + u * U, D);
+      if (FAST || a.d_stream) unpack<U>(r_d + u * U, D);
       else fill<U>(D, 0.0f);
       if (next) {
         f32x2 h[U / 2], n[U / 2], w[U / 2];
         unpack<U>(r_h + u * U, h);
         unpack<U>(r_dx + u * U, n);
-        weights<U>(a, plan, s_w, W_NEXT, units, u, w);
+        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) {
           dw_next[i][j] = fma2(n[j], mul2(h[j], r2), dw_next[i][j]);
@@ -429,21 +447,24 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
       }
       f32x2 o[U / 2];
 #pragma unroll
-      for (int j = 0; j < U / 2; ++j) o[j] = MERGE ? mul2(alpha, D[j]) : D[j];
+      for (int j = 0; j < U / 2; ++j) {
+        const float2 f = unpair(D[j]);
+        o[j] = MERGE ? pair(a.alpha * f.x, a.alpha * f.y) : D[j];
+      }
       pack<U>(static_cast<ST*>(a.dh) + base + u * U, o);
       if (MERGE) {
         f32x2 y[U / 2], wp[U / 2], wg[U / 2], ds[U / 2];
         if (has_y) unpack<U>(r_y + u * U, y);
         else fill<U>(y, 0.0f);
-        if (post) weights<U>(a, plan, s_w, W_POST, units, u, wp);
+        if (post) weights<U, FAST>(a, plan, s_w, W_POST, units, u, wp);
         else fill<U>(wp, 1.0f);
-        if (channel) weights<U>(a, plan, s_w, W_GATE, units, u, wg);
+        if (channel) weights<U, FAST>(a, plan, s_w, W_GATE, units, u, wg);
         else fill<U>(wg, 1.0f);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) q[i][j] = ds[j] = mul2(tg2, D[j]);
         if (slope) {
           f32x2 sl[U / 2];
-          weights<U>(a, plan, s_w, W_SLOPE, units, u, sl);
+          weights<U, FAST>(a, plan, s_w, W_SLOPE, units, u, sl);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) ds[j] = mul2(ds[j], sl[j]);
         }
@@ -451,7 +472,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
         for (int j = 0; j < U / 2; ++j) {
           const f32x2 yh = mul2(y[j], ry2), z = mul2(yh, wp[j]);
           dgate[i][j] = fma2(ds[j], z, dgate[i][j]);
-          sdz = fma2(D[j], z, sdz);
+          if (!FAST || token) sdz = fma2(D[j], z, sdz);
           const f32x2 dz = mul2(q[i][j], wg[j]);
           dw_post[i][j] = fma2(dz, yh, dw_post[i][j]);
           q[i][j] = mul2(dz, wp[j]);
@@ -461,17 +482,19 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
     }
     if (MERGE) {
       if (post || token) {
-        float s2[2] = {sum_pair(sqy), sum_pair(sdz)};
+        float s2[FAST && GATE != MOE_GATE_TOKEN ? 1 : 2];
+        s2[0] = sum_pair(sqy);
+        if (!FAST || token) s2[sizeof(s2) / 4 - 1] = sum_pair(sdz);
         sums(s2);
         if (token && tid == 0)
-          a.dgate_rows[row] = a.beta * s2[1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
+          a.dgate_rows[row] = a.beta * s2[sizeof(s2) / 4 - 1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
         const float cy = -ry * ry * s2[0] * inv_d;
         if (post) {
           const f32x2 cy2 = pair(cy, cy);
 #pragma unroll
           for (int i = 0; i < UPT; ++i) {
             const int u = tid + i * tpr;
-            if (u >= units) continue;
+            if (!FAST && u >= units) continue;
             f32x2 y[U / 2];
             unpack<U>(r_y + u * U, y);
 #pragma unroll
@@ -482,7 +505,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (u < units) pack<U>(a.dy + base + u * U, q[i]);
+        if (FAST || u < units) pack<U>(a.dy + base + u * U, q[i]);
       }
     }
     // every value of the row was used above: its place in the ring is free
@@ -493,7 +516,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
   for (int i = 0; i < UPT; ++i) {
     const int u = tid + i * tpr;
-    if (u >= units) continue;
+    if (!FAST && u >= units) continue;
     if (next) pack<U>(part + u * U, dw_next[i]);
     if (post) pack<U>(part + a.d + u * U, dw_post[i]);
     if (channel) pack<U>(part + 2 * a.d + u * U, dgate[i]);
@@ -567,6 +590,14 @@ static NormPlan norm_plan(int T, int d, int stream_size, int max_threads, const 
   return p;
 }
 
+// Whether the FAST variants take the call (see the top of the file).
+static bool norm_fast(const NormPlan& p, const NormArgs& a, bool merge) {
+  if (norm_cols(a.d) != 16 || a.d != p.tpr * 16 || !a.w_next || (merge && !a.w_post)) return false;
+  const bool channel = merge && a.gate_kind == MOE_GATE_CHANNEL;
+  return p.weight[W_NEXT] >= 0 && (!merge || p.weight[W_POST] >= 0) && (!channel || p.weight[W_GATE] >= 0) &&
+         (!(channel && a.gate_sigmoid) || !a.dh || p.weight[W_SLOPE] >= 0);
+}
+
 template <typename K>
 static cudaError_t launch_rows(K kern, const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM);
@@ -583,11 +614,26 @@ static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
   const NormPlan p = norm_plan(a.T, a.d, SZ, NORM_FWD_THREADS, {false, true, false, MERGE},
                                {a.w_next != nullptr, a.w_post != nullptr, channel, false});
-  switch (norm_cols(a.d)) {
-    case 8: return launch_rows(norm_fwd_kernel<ST, 8 / U, MERGE>, a, p, s);
-    case 16: return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE>, a, p, s);
-    default: return launch_rows(norm_fwd_kernel<ST, 32 / U, MERGE>, a, p, s);
+  if (norm_fast(p, a, MERGE)) {
+    if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>, a, p, s);
+    if (channel) return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE>, a, p, s);
+    return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE>, a, p, s);
   }
+  switch (norm_cols(a.d)) {
+    case 8: return launch_rows(norm_fwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
+    case 16: return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
+    default: return launch_rows(norm_fwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
+  }
+}
+
+template <typename ST, bool MERGE>
+static cudaError_t launch_bwd_fast(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  constexpr int U = 16 / sizeof(ST), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
+  constexpr int SL = MERGE ? GATE_SLOPE : MOE_GATE_NONE;
+  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>, a, p, s);
+  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, TK>, a, p, s);
+  if (a.gate_sigmoid) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, SL>, a, p, s);
+  return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, CH>, a, p, s);
 }
 
 template <typename ST, bool MERGE>
@@ -601,10 +647,14 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
                                  {next, post, channel, channel && a.gate_sigmoid});
     workers = p.grid * p.groups;
     cudaError_t err;
-    switch (norm_cols(a.d)) {
-      case 8: err = launch_rows(norm_bwd_kernel<ST, 8 / U, MERGE>, a, p, s); break;
-      case 16: err = launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE>, a, p, s); break;
-      default: err = launch_rows(norm_bwd_kernel<ST, 32 / U, MERGE>, a, p, s); break;
+    if (norm_fast(p, a, MERGE) && a.d_stream) {
+      err = launch_bwd_fast<ST, MERGE>(a, p, s);
+    } else {
+      switch (norm_cols(a.d)) {
+        case 8: err = launch_rows(norm_bwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
+        case 16: err = launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
+        default: err = launch_rows(norm_bwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
+      }
     }
     if (err != cudaSuccess) return err;
   }
