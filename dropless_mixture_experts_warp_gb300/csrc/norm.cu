@@ -18,7 +18,7 @@
 namespace moe {
 
 constexpr int NORM_MAX_D = 16384;
-constexpr int NORM_SMEM = 226 * 1024;  // dynamic shared memory of a block, its static buffers aside
+constexpr int NORM_SMEM = 225 * 1024;  // dynamic shared memory of a block: of the 227 KB, static buffers aside
 constexpr int NORM_MAX_SMS = 160;      // blocks at most
 constexpr int NORM_FWD_THREADS = 1024;
 constexpr int NORM_BWD_THREADS = 512;  // 128 registers a thread: the column sums of three weights
@@ -53,6 +53,8 @@ struct NormPlan {
   int off[RING_ARRAYS];   // each array's place in a ring row (-1: not read)
   int weight[W_ARRAYS];   // each weight's place, in floats (-1: read from global memory)
   int row_bytes, weight_bytes, stages;
+  int smem_bytes;
+  int y_bytes;            // backward: y has a ring of its own, of stages + 1 rows
 };
 
 __device__ __forceinline__ float gate_act(float g, int sigmoid) { return sigmoid ? 1.0f / (1.0f + __expf(-g)) : g; }
@@ -171,46 +173,77 @@ __device__ __forceinline__ void stage_weights(const NormArgs& a, const NormPlan&
   }
 }
 
-// Sums of N values over the threads of a group, in a fixed order; every thread gets them.
-// Lanes give half of the values away while they add (N = 3: 12 shuffles instead of 30).
-// Two buffers taken in turn need one barrier a sum: whoever writes a buffer again has
-// passed the barrier of the other, which its readers reach after reading.
-constexpr int ROW_WARPS = 16;  // of a group, at most
+// Sums of up to 4 values over a warp: lanes give half of the values away while they add (4
+// values: 6 shuffles instead of 20).  The sum of value i stands in lanes i * WIDTH and on.
+template <int N>
+struct SumLanes {
+  static constexpr int WIDTH = N == 1 ? 32 : N == 2 ? 16 : 8;
+};
+template <int N>
+__device__ __forceinline__ float lane_sums(const float* s, int lane) {
+  constexpr unsigned ALL = 0xffffffffu;
+  float v = s[0];
+  if (N == 2) {
+    const bool up = lane & 16;
+    v = (up ? s[1] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[1], 16);
+  } else if (N >= 3) {
+    const bool up = lane & 16, odd = lane & 8;
+    const float last = N == 4 ? s[3] : 0.0f;
+    const float x = (up ? s[2] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[2], 16);
+    const float y = (up ? last : s[1]) + __shfl_xor_sync(ALL, up ? s[1] : last, 16);
+    v = (odd ? y : x) + __shfl_xor_sync(ALL, odd ? x : y, 8);
+  }
+#pragma unroll
+  for (int off = SumLanes<N>::WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(ALL, v, off);
+  return v;
+}
+
+// Sums of N values (at most 8) over the threads of a group, in a fixed order; every thread
+// gets them.  Two buffers taken in turn need one barrier a sum: whoever writes a buffer
+// again has passed the barrier of the other, which its readers reach after reading.
+constexpr int SUMS_MAX = 5;
 struct GroupSums {
-  float* buf;   // the group's 2 * 3 * tpr / 32 floats
+  float* buf;   // the group's 2 * SUMS_MAX * tpr / 32 floats
   int tpr, group, tid, flip;
   template <int N>
+  __device__ __forceinline__ void write(const float* s, float* b) {
+    const int lane = tid & 31, value = lane / SumLanes<N>::WIDTH;
+    const float v = lane_sums<N>(s, lane);
+    if ((lane & (SumLanes<N>::WIDTH - 1)) == 0 && value < N) b[value * (tpr >> 5) + (tid >> 5)] = v;
+  }
+  template <int N>
+  __device__ __forceinline__ void read(float* s, const float* b) {
+    constexpr int WIDTH = SumLanes<N>::WIDTH;
+    const int lane = tid & 31, warps = tpr >> 5, first = lane & (WIDTH - 1), value = lane / WIDTH;
+    const float* r = b + (value < N ? value : 0) * warps;
+    float v = first < warps ? r[first] : 0.0f;
+    if (WIDTH < 16) v += first + WIDTH < warps ? r[first + WIDTH] : 0.0f;  // at most 16 warps a group
+#pragma unroll
+    for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(0xffffffffu, v, i * WIDTH);
+  }
+  template <int N>
+  __device__ __forceinline__ void warp_only(float* s) {
+    const float v = lane_sums<N>(s, tid & 31);
+#pragma unroll
+    for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(0xffffffffu, v, i * SumLanes<N>::WIDTH);
+  }
+  template <int N>
   __device__ __forceinline__ void operator()(float (&s)[N]) {
-    constexpr unsigned ALL = 0xffffffffu;
-    constexpr int SPLIT = N == 1 ? 1 : N == 2 ? 2 : 4, WIDTH = 32 / SPLIT;
-    const int lane = tid & 31;
-    float v = s[0];
-    if (N == 2) {
-      const bool up = lane & 16;
-      v = (up ? s[N - 1] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[N - 1], 16);
-    } else if (N == 3) {
-      const bool up = lane & 16, odd = lane & 8;
-      const float x = (up ? s[N - 1] : s[0]) + __shfl_xor_sync(ALL, up ? s[0] : s[N - 1], 16);
-      const float y = (up ? 0.0f : s[N / 2]) + __shfl_xor_sync(ALL, up ? s[N / 2] : 0.0f, 16);
-      v = (odd ? y : x) + __shfl_xor_sync(ALL, odd ? x : y, 8);
+    constexpr int A = N < 4 ? N : 4, B = N - A;
+    if (tpr == 32) {
+      warp_only<A>(s);
+      if (B) warp_only<B ? B : 1>(s + (B ? A : 0));
+      return;
     }
-#pragma unroll
-    for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(ALL, v, off);
-    const int value = lane / WIDTH;
-    if (tpr > 32) {
-      const int warps = tpr >> 5, first = lane & (WIDTH - 1);
-      float* b = buf + flip * 3 * warps;
-      flip ^= 1;
-      if (first == 0 && value < N) b[value * warps + (tid >> 5)] = v;
-      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
-      const float* r = b + (value < N ? value : 0) * warps;
-      v = first < warps ? r[first] : 0.0f;
-      if (WIDTH < ROW_WARPS) v += first + WIDTH < warps ? r[first + WIDTH] : 0.0f;
-#pragma unroll
-      for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(ALL, v, off);
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] = N == 1 ? v : __shfl_sync(ALL, v, i * WIDTH);
+    float* b = buf + flip * SUMS_MAX * (tpr >> 5);
+    flip ^= 1;
+    write<A>(s, b);
+    if (B) write<B ? B : 1>(s + (B ? A : 0), b + A * (tpr >> 5));
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(tpr) : "memory");
+    read<A>(s, b);
+    if (B) read<B ? B : 1>(s + (B ? A : 0), b + A * (tpr >> 5));
   }
 };
 
@@ -226,13 +259,13 @@ __device__ __forceinline__ float sum_pair(f32x2 v) {
 template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
 __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[2 * 3 * 32];
+  __shared__ float buf[2 * SUMS_MAX * 32];
   constexpr int U = 16 / sizeof(ST);
   const int tpr = plan.tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int worker = group * gridDim.x + blockIdx.x, workers = plan.groups * gridDim.x;
   const int units = a.d / U;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  GroupSums sums{buf + group * 2 * 3 * (tpr >> 5), tpr, group, tid, 0};
+  GroupSums sums{buf + group * 2 * SUMS_MAX * (tpr >> 5), tpr, group, tid, 0};
   const float* s_w = reinterpret_cast<const float*>(smem);
   uint8_t* my_ring = smem + plan.weight_bytes + group * plan.stages * plan.row_bytes;
   auto fetch = [&](long long row, int stage) {
@@ -337,22 +370,27 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 // writes them as the worker's partial sums, which norm_reduce_kernel adds in worker order.
 //   D = d_stream + r (n - h r^2 mean(n h)),  n = dx (w_next + offset)
 //   dz = beta a D,  q = dz (w_post + offset),  dy = r (q - y r^2 mean(q y))
+// Two rows are under way in a group: the sums that D of the next row needs are added up
+// together with those that dy of this row needs, so that a row takes one barrier and its
+// waits are filled with the other row's work (355 us with two barriers a row, for 16384 x
+// 7168 bf16 with everything).  So y has one place more in the ring than the other arrays.
 // What a call lacks (weights, gate) takes its neutral value, a unit at a time.
 template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
 __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float buf[2 * 3 * 32];
+  __shared__ float buf[2 * SUMS_MAX * 32];
   constexpr int U = 16 / sizeof(ST);
   const int tpr = plan.tpr, group = threadIdx.x / tpr, tid = threadIdx.x - group * tpr;
   const int worker = group * gridDim.x + blockIdx.x, workers = plan.groups * gridDim.x;
   const int units = a.d / U;
   const float inv_d = 1.0f / static_cast<float>(a.d);
-  GroupSums sums{buf + group * 2 * 3 * (tpr >> 5), tpr, group, tid, 0};
+  GroupSums sums{buf + group * 2 * SUMS_MAX * (tpr >> 5), tpr, group, tid, 0};
   const float* s_w = reinterpret_cast<const float*>(smem);
-  uint8_t* my_ring = smem + plan.weight_bytes + group * plan.stages * plan.row_bytes;
-  auto fetch = [&](long long row, int stage) {
+  uint8_t* my_ring = smem + plan.weight_bytes + group * (plan.stages * plan.row_bytes + (plan.stages + 1) * plan.y_bytes);
+  uint8_t* my_y = my_ring + plan.stages * plan.row_bytes;
+  auto fetch = [&](long long row, int stage, int y_stage) {
     if (row < a.T) {
-      const uint32_t dst = smem_u32(my_ring + stage * plan.row_bytes);
+      const uint32_t dst = smem_u32(my_ring + stage * plan.row_bytes), dst_y = smem_u32(my_y + y_stage * plan.y_bytes);
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
@@ -361,36 +399,23 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
         if (FAST || plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
         if (FAST || plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
         if (FAST || plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
-        if (MERGE && (FAST || plan.off[RING_Y] >= 0)) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
+        if (MERGE && (FAST || plan.y_bytes > 0)) copy_async<U * 2>(dst_y + u * U * 2, a.y + at);
       }
     }
     copy_commit();
   };
-  for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
+  // one group of copies a row: `stages` of them are open when a row is waited for
+  for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
   const bool next = FAST || a.w_next != nullptr, post = MERGE && (FAST || a.w_post != nullptr);
   const int gate = !MERGE ? MOE_GATE_NONE : !FAST ? a.gate_kind : GATE == GATE_SLOPE ? MOE_GATE_CHANNEL : GATE;
   const bool channel = gate == MOE_GATE_CHANNEL, token = gate == MOE_GATE_TOKEN;
   const bool slope = FAST ? GATE == GATE_SLOPE : channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
+  const f32x2 zero = pair(0.0f, 0.0f);
 
-  f32x2 dw_next[UPT][U / 2], dw_post[UPT][U / 2], dgate[UPT][U / 2];
-#pragma unroll
-  for (int i = 0; i < UPT; ++i) {
-    fill<U>(dw_next[i], 0.0f);
-    fill<U>(dw_post[i], 0.0f);
-    fill<U>(dgate[i], 0.0f);
-  }
-  int stage = 0;
-  for (long long row = worker; row < a.T; row += workers) {
-    const long long base = row * a.d;
-    const uint8_t* at = my_ring + stage * plan.row_bytes;
-    const ST* r_d = reinterpret_cast<const ST*>(at + plan.off[RING_D]);
-    const ST* r_h = reinterpret_cast<const ST*>(at + plan.off[RING_H]);
-    const moe_bf16* r_dx = reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]);
-    const moe_bf16* r_y = reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]);
-    copy_wait_oldest(plan.stages);
-    const f32x2 zero = pair(0.0f, 0.0f);
+  // A row's sums of h^2, n h and y^2.
+  auto first_sums = [&](const uint8_t* at, const uint8_t* y_at, float& hh, float& nh, float& yy) {
     f32x2 shh = zero, snh = zero, syy = zero;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
@@ -398,8 +423,8 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
       if (!FAST && u >= units) continue;
       if (next) {
         f32x2 h[U / 2], n[U / 2], w[U / 2];
-        unpack<U>(r_h + u * U, h);
-        unpack<U>(r_dx + u * U, n);
+        unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h);
+        unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]) + u * U, n);
         weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) {
@@ -409,97 +434,139 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
       }
       if (post) {
         f32x2 y[U / 2];
-        unpack<U>(r_y + u * U, y);
+        unpack<U>(reinterpret_cast<const moe_bf16*>(y_at) + u * U, y);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) syy = fma2(y[j], y[j], syy);
       }
     }
-    float s[3] = {sum_pair(shh), sum_pair(snh), sum_pair(syy)};
+    hh = sum_pair(shh);
+    nh = sum_pair(snh);
+    yy = sum_pair(syy);
+  };
+
+  f32x2 dw_next[UPT][U / 2], dw_post[UPT][U / 2], dgate[UPT][U / 2];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    fill<U>(dw_next[i], 0.0f);
+    fill<U>(dw_post[i], 0.0f);
+    fill<U>(dgate[i], 0.0f);
+  }
+  int stage = 0, y_stage = 0;
+  float hh = 0.0f, nh = 0.0f, yy = 0.0f;  // of the row, over all its columns
+  if (worker < a.T) {
+    copy_wait_oldest(plan.stages);
+    float s[3];
+    first_sums(my_ring, my_y, s[0], s[1], s[2]);
     sums(s);
-    const float r = next ? inv_rms(s[0], inv_d, a.eps) : 0.0f;
-    const float c = -r * r * s[1] * inv_d;
-    const float ry = post ? inv_rms(s[2], inv_d, a.eps) : 1.0f;
+    hh = s[0];
+    nh = s[1];
+    yy = s[2];
+  }
+  for (long long row = worker; row < a.T; row += workers) {
+    const long long base = row * a.d;
+    const uint8_t* at = my_ring + stage * plan.row_bytes;
+    const moe_bf16* r_y = reinterpret_cast<const moe_bf16*>(my_y + y_stage * plan.y_bytes);
+    const float r = next ? inv_rms(hh, inv_d, a.eps) : 0.0f;
+    const float c = -r * r * nh * inv_d;
+    const float ry = post ? inv_rms(yy, inv_d, a.eps) : 1.0f;
     float tg = a.beta, tact = 1.0f;  // beta * a for the row
     if (token) {
       tact = gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
       tg *= tact;
     }
-    const f32x2 r2 = pair(r, r), c2 = pair(c, c), ry2 = pair(ry, ry), tg2 = pair(tg, tg);
     f32x2 sqy = zero, sdz = zero;
     f32x2 q[UPT][U / 2];
+    {
+      const f32x2 r2 = pair(r, r), c2 = pair(c, c), ry2 = pair(ry, ry), tg2 = pair(tg, tg);
 #pragma unroll
-    for (int i = 0; i < UPT; ++i) {
-      const int u = tid + i * tpr;
-      if (!FAST && u >= units) continue;
-      f32x2 D[U / 2];
-      if (FAST || a.d_stream) unpack<U>(r_d + u * U, D);
-      else fill<U>(D, 0.0f);
-      if (next) {
-        f32x2 h[U / 2], n[U / 2], w[U / 2];
-        unpack<U>(r_h + u * U, h);
-        unpack<U>(r_dx + u * U, n);
-        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (!FAST && u >= units) continue;
+        f32x2 D[U / 2];
+        if (FAST || a.d_stream) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_D]) + u * U, D);
+        else fill<U>(D, 0.0f);
+        if (next) {
+          f32x2 h[U / 2], n[U / 2], w[U / 2];
+          unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h);
+          unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]) + u * U, n);
+          weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+#pragma unroll
+          for (int j = 0; j < U / 2; ++j) {
+            dw_next[i][j] = fma2(n[j], mul2(h[j], r2), dw_next[i][j]);
+            D[j] = fma2(r2, fma2(h[j], c2, mul2(n[j], w[j])), D[j]);
+          }
+        }
+        f32x2 o[U / 2];
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) {
-          dw_next[i][j] = fma2(n[j], mul2(h[j], r2), dw_next[i][j]);
-          D[j] = fma2(r2, fma2(h[j], c2, mul2(n[j], w[j])), D[j]);
+          const float2 f = unpair(D[j]);
+          o[j] = MERGE ? pair(a.alpha * f.x, a.alpha * f.y) : D[j];
         }
-      }
-      f32x2 o[U / 2];
+        pack<U>(static_cast<ST*>(a.dh) + base + u * U, o);
+        if (MERGE) {
+          f32x2 y[U / 2], wp[U / 2], wg[U / 2], ds[U / 2];
+          if (has_y) unpack<U>(r_y + u * U, y);
+          else fill<U>(y, 0.0f);
+          if (post) weights<U, FAST>(a, plan, s_w, W_POST, units, u, wp);
+          else fill<U>(wp, 1.0f);
+          if (channel) weights<U, FAST>(a, plan, s_w, W_GATE, units, u, wg);
+          else fill<U>(wg, 1.0f);
 #pragma unroll
-      for (int j = 0; j < U / 2; ++j) {
-        const float2 f = unpair(D[j]);
-        o[j] = MERGE ? pair(a.alpha * f.x, a.alpha * f.y) : D[j];
-      }
-      pack<U>(static_cast<ST*>(a.dh) + base + u * U, o);
-      if (MERGE) {
-        f32x2 y[U / 2], wp[U / 2], wg[U / 2], ds[U / 2];
-        if (has_y) unpack<U>(r_y + u * U, y);
-        else fill<U>(y, 0.0f);
-        if (post) weights<U, FAST>(a, plan, s_w, W_POST, units, u, wp);
-        else fill<U>(wp, 1.0f);
-        if (channel) weights<U, FAST>(a, plan, s_w, W_GATE, units, u, wg);
-        else fill<U>(wg, 1.0f);
+          for (int j = 0; j < U / 2; ++j) q[i][j] = ds[j] = mul2(tg2, D[j]);
+          if (slope) {
+            f32x2 sl[U / 2];
+            weights<U, FAST>(a, plan, s_w, W_SLOPE, units, u, sl);
 #pragma unroll
-        for (int j = 0; j < U / 2; ++j) q[i][j] = ds[j] = mul2(tg2, D[j]);
-        if (slope) {
-          f32x2 sl[U / 2];
-          weights<U, FAST>(a, plan, s_w, W_SLOPE, units, u, sl);
+            for (int j = 0; j < U / 2; ++j) ds[j] = mul2(ds[j], sl[j]);
+          }
 #pragma unroll
-          for (int j = 0; j < U / 2; ++j) ds[j] = mul2(ds[j], sl[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < U / 2; ++j) {
-          const f32x2 yh = mul2(y[j], ry2), z = mul2(yh, wp[j]);
-          dgate[i][j] = fma2(ds[j], z, dgate[i][j]);
-          if (!FAST || token) sdz = fma2(D[j], z, sdz);
-          const f32x2 dz = mul2(q[i][j], wg[j]);
-          dw_post[i][j] = fma2(dz, yh, dw_post[i][j]);
-          q[i][j] = mul2(dz, wp[j]);
-          sqy = fma2(q[i][j], y[j], sqy);
+          for (int j = 0; j < U / 2; ++j) {
+            const f32x2 yh = mul2(y[j], ry2), z = mul2(yh, wp[j]);
+            dgate[i][j] = fma2(ds[j], z, dgate[i][j]);
+            if (!FAST || token) sdz = fma2(D[j], z, sdz);
+            const f32x2 dz = mul2(q[i][j], wg[j]);
+            dw_post[i][j] = fma2(dz, yh, dw_post[i][j]);
+            q[i][j] = mul2(dz, wp[j]);
+            sqy = fma2(q[i][j], y[j], sqy);
+          }
         }
       }
     }
+    // the row's D, h and dx were used above and y of the row before in its dy: their places
+    // are free for the row `stages` further on
+    const int y_after = y_stage + plan.stages > plan.stages ? y_stage - 1 : plan.stages;
+    fetch(row + static_cast<long long>(plan.stages) * workers, stage, y_after);
+    stage = stage + 1 == plan.stages ? 0 : stage + 1;
+    y_stage = y_stage == plan.stages ? 0 : y_stage + 1;
+    float s[!MERGE ? 2 : FAST && GATE != MOE_GATE_TOKEN ? 4 : 5] = {};
+    if (row + workers < a.T) {
+      copy_wait_oldest(plan.stages);
+      float y2;
+      first_sums(my_ring + stage * plan.row_bytes, my_y + y_stage * plan.y_bytes, s[0], s[1], y2);
+      if (MERGE) s[MERGE ? 2 : 0] = y2;
+    }
     if (MERGE) {
-      if (post || token) {
-        float s2[FAST && GATE != MOE_GATE_TOKEN ? 1 : 2];
-        s2[0] = sum_pair(sqy);
-        if (!FAST || token) s2[sizeof(s2) / 4 - 1] = sum_pair(sdz);
-        sums(s2);
-        if (token && tid == 0)
-          a.dgate_rows[row] = a.beta * s2[sizeof(s2) / 4 - 1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
-        const float cy = -ry * ry * s2[0] * inv_d;
-        if (post) {
-          const f32x2 cy2 = pair(cy, cy);
+      s[MERGE ? 3 : 0] = sum_pair(sqy);
+      if (!FAST || token) s[sizeof(s) / 4 - 1] = sum_pair(sdz);
+    }
+    sums(s);
+    hh = s[0];
+    nh = s[1];
+    if (MERGE) {
+      yy = s[MERGE ? 2 : 0];
+      if (token && tid == 0)
+        a.dgate_rows[row] = a.beta * s[sizeof(s) / 4 - 1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
+      if (post) {
+        const float cy = -ry * ry * s[MERGE ? 3 : 0] * inv_d;
+        const f32x2 cy2 = pair(cy, cy), ry2 = pair(ry, ry);
 #pragma unroll
-          for (int i = 0; i < UPT; ++i) {
-            const int u = tid + i * tpr;
-            if (!FAST && u >= units) continue;
-            f32x2 y[U / 2];
-            unpack<U>(r_y + u * U, y);
+        for (int i = 0; i < UPT; ++i) {
+          const int u = tid + i * tpr;
+          if (!FAST && u >= units) continue;
+          f32x2 y[U / 2];
+          unpack<U>(r_y + u * U, y);
 #pragma unroll
-            for (int j = 0; j < U / 2; ++j) q[i][j] = mul2(ry2, fma2(y[j], cy2, q[i][j]));
-          }
+          for (int j = 0; j < U / 2; ++j) q[i][j] = mul2(ry2, fma2(y[j], cy2, q[i][j]));
         }
       }
 #pragma unroll
@@ -508,9 +575,6 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
         if (FAST || u < units) pack<U>(a.dy + base + u * U, q[i]);
       }
     }
-    // every value of the row was used above: its place in the ring is free
-    fetch(row + static_cast<long long>(plan.stages) * workers, stage);
-    stage = stage + 1 == plan.stages ? 0 : stage + 1;
   }
   float* part = a.part + static_cast<long long>(worker) * 3 * a.d;
 #pragma unroll
@@ -563,28 +627,30 @@ __global__ void __launch_bounds__(32 * REDUCE_GROUPS) norm_reduce_kernel(const f
 static int norm_cols(int d) { return d <= 256 ? 8 : d <= 8192 ? 16 : 32; }
 
 // The plan for rows of d columns; used[] tells the arrays and weights of the call.
-static NormPlan norm_plan(int T, int d, int stream_size, int max_threads, const bool (&rows)[RING_ARRAYS],
+static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&rows)[RING_ARRAYS],
                           const bool (&w)[W_ARRAYS]) {
   NormPlan p{};
   p.tpr = ((d + norm_cols(d) - 1) / norm_cols(d) + 31) / 32 * 32;
-  p.groups = max_threads / p.tpr;
+  p.groups = (bwd ? NORM_BWD_THREADS : NORM_FWD_THREADS) / p.tpr;
   if (p.tpr > 32 && p.groups > 15) p.groups = 15;  // named barriers 1 .. 15
   const int size[RING_ARRAYS] = {stream_size, stream_size, 2, 2};
   for (int i = 0; i < RING_ARRAYS; ++i) {
-    p.off[i] = rows[i] ? p.row_bytes : -1;
-    if (rows[i]) p.row_bytes += d * size[i];
+    const bool apart = bwd && i == RING_Y;
+    p.off[i] = rows[i] && !apart ? p.row_bytes : -1;
+    if (rows[i]) (apart ? p.y_bytes : p.row_bytes) += d * size[i];
   }
+  auto ring = [&](int stages) { return p.groups * (stages * p.row_bytes + (p.y_bytes ? (stages + 1) * p.y_bytes : 0)); };
   // groups as far as each has room for two rows (one row fits always: 16384 columns take at
-  // most 192 KB), then the weights, then up to four rows a group
-  while (p.groups > 1 && 2 * p.groups * p.row_bytes > NORM_SMEM) --p.groups;
-  const int row = p.groups * p.row_bytes;
-  p.stages = 2 * row <= NORM_SMEM ? 2 : 1;
+  // most 224 KB), then the weights, then up to four rows a group
+  while (p.groups > 1 && ring(2) > NORM_SMEM) --p.groups;
+  p.stages = ring(2) <= NORM_SMEM ? 2 : 1;
   for (int k = 0; k < W_ARRAYS; ++k) {
-    const bool fits = w[k] && p.stages * row + p.weight_bytes + d * 4 <= NORM_SMEM;
+    const bool fits = w[k] && ring(p.stages) + p.weight_bytes + d * 4 <= NORM_SMEM;
     p.weight[k] = fits ? p.weight_bytes / 4 : -1;
     if (fits) p.weight_bytes += d * 4;
   }
-  while (p.stages > 1 && p.stages < 4 && (p.stages + 1) * row + p.weight_bytes <= NORM_SMEM) ++p.stages;
+  while (p.stages > 1 && p.stages < 4 && ring(p.stages + 1) + p.weight_bytes <= NORM_SMEM) ++p.stages;
+  p.smem_bytes = ring(p.stages) + p.weight_bytes;
   const int sms = num_sms() < NORM_MAX_SMS ? num_sms() : NORM_MAX_SMS;
   p.grid = T < sms ? T : sms;
   return p;
@@ -602,7 +668,7 @@ template <typename K>
 static cudaError_t launch_rows(K kern, const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM);
   if (err != cudaSuccess) return err;
-  kern<<<p.grid, p.groups * p.tpr, p.weight_bytes + p.groups * p.stages * p.row_bytes, s>>>(a, p);
+  kern<<<p.grid, p.groups * p.tpr, p.smem_bytes, s>>>(a, p);
   count_launch();
   return cudaGetLastError();
 }
@@ -612,7 +678,7 @@ static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
   constexpr int SZ = sizeof(ST), U = 16 / SZ;
   const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
-  const NormPlan p = norm_plan(a.T, a.d, SZ, NORM_FWD_THREADS, {false, true, false, MERGE},
+  const NormPlan p = norm_plan(a.T, a.d, SZ, false, {false, true, false, MERGE},
                                {a.w_next != nullptr, a.w_post != nullptr, channel, false});
   if (norm_fast(p, a, MERGE)) {
     if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>, a, p, s);
@@ -642,7 +708,7 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
   const bool next = a.w_next, post = MERGE && a.w_post, channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
   int workers = 0;
   if (a.T > 0) {
-    const NormPlan p = norm_plan(a.T, a.d, SZ, NORM_BWD_THREADS,
+    const NormPlan p = norm_plan(a.T, a.d, SZ, true,
                                  {a.d_stream != nullptr, next, next, post || (MERGE && a.gate_kind != MOE_GATE_NONE)},
                                  {next, post, channel, channel && a.gate_sigmoid});
     workers = p.grid * p.groups;
