@@ -1,13 +1,19 @@
 // Balance loss of the router over ragged sequences, per-expert counts, the z-loss, and
 // their gradient by the logits.
+//
+// A token's E logits lie over the G lanes of a group, PLV vectors of VEC a lane (16 logits a
+// lane up to 512 experts: a token's sums then take few shuffles a logit, and a warp has
+// several tokens under way).  Exponentials are 2^x of the scaled argument, which the maximum
+// keeps at or below 0: their relative error is at most |l - max| 2^-24 + 2^-22.
 #include "around.cuh"
 
 namespace moe {
 
 constexpr int BAL_MAX_E = 1024;
 constexpr int BAL_MAX_S = 65535;
-constexpr int BAL_CHUNK = 128;  // tokens of a forward block
-constexpr int BAL_WARPS = 8;
+constexpr int BAL_MAX_T = 1 << 30;
+constexpr int BAL_THREADS = 256;
+constexpr int JOIN_COLS = 32;  // experts of a join block
 
 struct BalanceArgs {
   int T, E, k, S;
@@ -17,6 +23,7 @@ struct BalanceArgs {
   const int32_t* seq_offsets;  // NULL: one sequence of T tokens
   const uint8_t* mask;
   // forward
+  int chunk;           // tokens of a block
   float* losses;
   int32_t* counts;
   float* prob_mean;
@@ -28,9 +35,11 @@ struct BalanceArgs {
   int32_t* part_c;     // [slots][E]
   float* part_z;       // [slots] sums of logsumexp^2
   int32_t* part_n;     // [slots] kept tokens
-  float* seq_loss;     // [S][2] a sequence's sum f P and sum logsumexp^2
+  float* seq_loss;     // [S][join blocks a sequence] sums f P
+  float* seq_z;        // [S] sums of logsumexp^2
   int32_t* counter;
   // backward
+  int run;             // tokens of a group
   const int32_t* counts_in;
   const int32_t* tokens_in;
   const float* grad_losses;
@@ -38,223 +47,362 @@ struct BalanceArgs {
   float* d_logits;
 };
 
-// Start of sequence s, whatever the array holds inside [0, T].
-__device__ __forceinline__ int seq_at(const BalanceArgs& a, int s) {
-  if (!a.seq_offsets) return s == 0 ? 0 : a.T;
-  return min(max(a.seq_offsets[s], 0), a.T);
-}
-
-// The last sequence that starts at or before token t (0 if none does).
-__device__ __forceinline__ int seq_of(const BalanceArgs& a, int t) {
-  int lo = 0, hi = a.S - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (seq_at(a, mid) <= t) lo = mid;
-    else hi = mid - 1;
+// Starts of the sequences, whatever the array holds inside [0, T]; up to SEQ_TABLE of them
+// are read into shared memory at once, so that a search does not wait for memory at each step.
+constexpr int SEQ_TABLE = 512;
+struct Sequences {
+  const int32_t* offsets;
+  int T, S;
+  const int* table;
+  // The caller synchronises the block before the first use.
+  __device__ __forceinline__ Sequences(const BalanceArgs& a, int* shared)
+      : offsets(a.seq_offsets), T(a.T), S(a.S), table(a.seq_offsets && a.S <= SEQ_TABLE ? shared : nullptr) {
+    if (table)
+      for (int i = threadIdx.x; i <= S; i += blockDim.x) shared[i] = min(max(offsets[i], 0), T);
   }
-  return lo;
-}
+  __device__ __forceinline__ int at(int s) const {
+    if (table) return table[s];
+    if (!offsets) return s == 0 ? 0 : T;
+    return min(max(offsets[s], 0), T);
+  }
+  // The last sequence that starts at or before token t (0 if none does).
+  __device__ __forceinline__ int of(int t) const {
+    int lo = 0, hi = S - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (at(mid) <= t) lo = mid;
+      else hi = mid - 1;
+    }
+    return lo;
+  }
+};
 
-__device__ __forceinline__ float warp_max(float v) {
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+  for (int off = G / 2; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
   return v;
 }
-__device__ __forceinline__ float warp_sum(float v) {
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  for (int off = G / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   return v;
 }
 
-// A row of E logits over the lanes of a warp: expert lane + 32 c in slot c.
-template <int PL>
-__device__ __forceinline__ void load_row(const float* row, int E, int lane, float (&l)[PL]) {
+constexpr float LOG2E = 1.4426950408889634f;
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// A lane's logits (or other [T][E] values) of one token; `fill` where the row ends, and
+// everywhere where `there` is false.
+template <int VEC, int G, int PLV>
+__device__ __forceinline__ void load_row(const float* row, int E, int gl, bool there, float fill, float (&l)[VEC * PLV]) {
 #pragma unroll
-  for (int c = 0; c < PL; ++c) l[c] = lane + 32 * c < E ? row[lane + 32 * c] : -INFINITY;
+  for (int i = 0; i < PLV; ++i) {
+    const int e = (gl + G * i) * VEC;
+    if (VEC == 4) {
+      float4 q = make_float4(fill, fill, fill, fill);
+      if (there && e < E) q = *reinterpret_cast<const float4*>(row + e);
+      l[4 * i] = q.x; l[4 * i + 1] = q.y; l[4 * i + 2] = q.z; l[4 * i + 3] = q.w;
+    } else {
+      l[i] = there && e < E ? row[e] : fill;
+    }
+  }
 }
 
 // The row's largest logit.
-template <int PL>
-__device__ __forceinline__ float row_top(const float (&l)[PL]) {
+template <int G, int N>
+__device__ __forceinline__ float row_top(const float (&l)[N]) {
   float top = l[0];
 #pragma unroll
-  for (int c = 1; c < PL; ++c) top = fmaxf(top, l[c]);
-  return warp_max(top);
+  for (int c = 1; c < N; ++c) top = fmaxf(top, l[c]);
+  return group_max<G>(top);
 }
 
-// Softmax of the row and its logsumexp; p = 0 and lse = 0 for a row of -inf.
-template <int PL>
-__device__ __forceinline__ void row_softmax(const float (&l)[PL], float top, float (&p)[PL], float& lse) {
+// Softmax of the row, not yet divided by its sum, the sum's inverse and the logsumexp; all 0
+// for a row of -inf.  (A NaN reaches the sum through its own exponential.)
+template <int G, int N>
+__device__ __forceinline__ void row_softmax(const float (&l)[N], float top, bool with_lse, float (&p)[N], float& inv, float& lse) {
   if (top == -INFINITY) top = 0.0f;
   float sum = 0.0f;
 #pragma unroll
-  for (int c = 0; c < PL; ++c) {
-    p[c] = expf(l[c] - top);
+  for (int c = 0; c < N; ++c) {
+    p[c] = exp2_fast((l[c] - top) * LOG2E);  // the difference first: logits near fp32's lowest
     sum += p[c];
   }
-  sum = warp_sum(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int c = 0; c < PL; ++c) p[c] *= inv;
-  lse = sum == 0.0f ? 0.0f : top + logf(sum);
+  sum = group_sum<G>(sum);
+  inv = sum == 0.0f ? 0.0f : rcp_fast(sum);
+  lse = with_lse && sum != 0.0f ? top + logf(sum) : 0.0f;
 }
 
-// p = sigmoid(l) / sum, each sigmoid taken times e^-c with c = min(top, 0): 1 / (e^c +
-// e^(c - l)).  The largest is then at least 1/2, so that a row of far negative logits,
-// whose sigmoids fp32 cannot hold, keeps its shares.  p = 0 for a row of -inf.
-template <int PL>
-__device__ __forceinline__ void row_sigmoid(const float (&l)[PL], float top, float (&p)[PL]) {
+// p = sigmoid(l), each taken times e^-c with c = min(top, 0): 1 / (e^c + e^(c - l)), and the
+// inverse of their sum.  The largest is then at least 1/2, so that a row of far negative
+// logits, whose sigmoids fp32 cannot hold, keeps its shares; the inverse is 0 for a row of
+// -inf.  rest = 1 - sigmoid(l) = e^(c - l) p, without the cancellation of the difference.
+template <int G, int N>
+__device__ __forceinline__ void row_sigmoid(const float (&l)[N], float top, float (&p)[N], float& inv, float (*rest)[N]) {
   const float c0 = top == -INFINITY ? 0.0f : fminf(top, 0.0f);
-  const float ec = expf(c0);
+  const float ec = exp2_fast(c0 * LOG2E);
   float sum = 0.0f;
 #pragma unroll
-  for (int c = 0; c < PL; ++c) {
-    p[c] = 1.0f / (ec + expf(c0 - l[c]));
+  for (int c = 0; c < N; ++c) {
+    const float e = exp2_fast((c0 - l[c]) * LOG2E);
+    p[c] = rcp_fast(ec + e);
     sum += p[c];
+    if (rest) (*rest)[c] = fminf(e * p[c], 1.0f);  // inf * 0 where l is far below the top: 1
   }
-  sum = warp_sum(sum);
-  const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-#pragma unroll
-  for (int c = 0; c < PL; ++c) p[c] *= inv;
+  sum = group_sum<G>(sum);
+  inv = sum == 0.0f ? 0.0f : rcp_fast(sum);
 }
 
-// A block takes a chunk of tokens, sequence by sequence: its warps take the tokens in
-// turn and keep the sums of p in registers; the counts are integer sums in shared memory.
-template <int PL, bool SIGMOID>
-__global__ void __launch_bounds__(BAL_WARPS * 32) balance_fwd_kernel(const BalanceArgs a) {
-  __shared__ float s_p[BAL_WARPS][PL * 32];
-  __shared__ int s_c[PL * 32];
-  __shared__ float s_z[BAL_WARPS];
-  __shared__ int s_n[BAL_WARPS];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c0 = blockIdx.x * BAL_CHUNK, c1 = min(a.T, c0 + BAL_CHUNK);
-  for (int s = seq_of(a, c0); s < a.S; ++s) {
-    const int b = max(c0, seq_at(a, s)), e = min(c1, seq_at(a, s + 1));
-    if (seq_at(a, s) >= c1) break;
+// A block takes a chunk of tokens, sequence by sequence: its groups take the tokens in turn
+// and keep the sums of p in registers; the counts are integer sums in shared memory.  A
+// single block with a single sequence writes the results itself.
+template <int VEC, int G, int PLV, bool SIGMOID>
+__global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceArgs a) {
+  constexpr int N = VEC * PLV, GROUPS = BAL_THREADS / G, WARP_COLS = N * G;
+  __shared__ float s_p[BAL_THREADS / 32][WARP_COLS];
+  __shared__ int s_c[WARP_COLS];
+  __shared__ float s_z[BAL_THREADS / 32];
+  __shared__ int s_n[BAL_THREADS / 32];
+  __shared__ float buf[32];
+  __shared__ int s_off[SEQ_TABLE + 1];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G, group = threadIdx.x / G;
+  const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+  const Sequences seqs(a, s_off);
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;  // of the join's blocks
+  __syncthreads();
+  for (int s = seqs.of(c0); s < a.S; ++s) {
+    const int start = seqs.at(s);
+    if (start >= c1) break;
+    const int b = max(c0, start), e = min(c1, seqs.at(s + 1));
     if (b >= e) continue;
-    for (int i = threadIdx.x; i < PL * 32; i += blockDim.x) s_c[i] = 0;
-    __syncthreads();
-    float acc[PL], z = 0.0f;
+    for (int i = threadIdx.x; i < WARP_COLS; i += BAL_THREADS) s_c[i] = 0;
+    float acc[N], z = 0.0f, l[N];
     int n = 0;
 #pragma unroll
-    for (int c = 0; c < PL; ++c) acc[c] = 0.0f;
-    for (int t = b + warp; t < e; t += BAL_WARPS) {
-      if (a.mask && !a.mask[t]) continue;
-      ++n;
-      float l[PL], p[PL], lse = 0.0f;
-      load_row(a.logits + static_cast<long long>(t) * a.E, a.E, lane, l);
-      const float top = row_top(l);
-      if (!SIGMOID || a.z_coef != 0.0f) row_softmax(l, top, p, lse);
-      if (SIGMOID) row_sigmoid(l, top, p);
-      if (a.z_coef != 0.0f) z = fmaf(lse, lse, z);
-#pragma unroll
-      for (int c = 0; c < PL; ++c) acc[c] += p[c];
-      if (lane < a.k) {
-        const int x = a.topk_idx[static_cast<long long>(t) * a.k + lane];
-        if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
-        else set_status(a.status, MOE_ERR_INVARIANT);
-      }
+    for (int c = 0; c < N; ++c) acc[c] = 0.0f;
+    // a token's mask is read two tokens ahead, its logits one: neither waits for the other
+    auto kept = [&](int t) { return t < e && (!a.mask || a.mask[t]); };
+    int t = b + group;
+    bool keep = kept(t), keep_next = kept(t + GROUPS);
+    load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, keep, -INFINITY, l);
+    __syncthreads();
+    for (int i = threadIdx.x; i < (e - b) * a.k; i += BAL_THREADS) {
+      if (a.mask && !a.mask[b + i / a.k]) continue;
+      const int x = a.topk_idx[static_cast<long long>(b) * a.k + i];
+      if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
+      else set_status(a.status, MOE_ERR_INVARIANT);
     }
+    for (int done = b; done < e; done += GROUPS) {  // a token of every group
+      const int tn = t + GROUPS;
+      const bool keep_after = kept(tn + GROUPS);
+      float next[N];
+      load_row<VEC, G, PLV>(a.logits + static_cast<long long>(tn) * a.E, a.E, gl, keep_next, -INFINITY, next);
+      float p[N], inv, lse = 0.0f;
+      const float top = row_top<G>(l);
+      if (!SIGMOID || a.z_coef != 0.0f) row_softmax<G>(l, top, a.z_coef != 0.0f, p, inv, lse);
+      if (SIGMOID) row_sigmoid<G>(l, top, p, inv, static_cast<float (*)[N]>(nullptr));
+      z = fmaf(lse, lse, z);
+      n += keep;
 #pragma unroll
-    for (int c = 0; c < PL; ++c) s_p[warp][lane + 32 * c] = acc[c];
+      for (int c = 0; c < N; ++c) {
+        acc[c] = fmaf(p[c], inv, acc[c]);
+        l[c] = next[c];
+      }
+      t = tn;
+      keep = keep_next;
+      keep_next = keep_after;
+    }
+    // the warp's groups, then the block's warps, in order
+#pragma unroll
+    for (int off = G; off < 32; off <<= 1) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) acc[c] += __shfl_xor_sync(0xffffffffu, acc[c], off);
+      z += __shfl_xor_sync(0xffffffffu, z, off);
+      n += __shfl_xor_sync(0xffffffffu, n, off);
+    }
+    if (lane < G) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) s_p[warp][(gl + G * (c / VEC)) * VEC + c % VEC] = acc[c];
+    }
     if (lane == 0) {
       s_z[warp] = z;
       s_n[warp] = n;
     }
     __syncthreads();
+    float zs = 0.0f;
+    int ns = 0;
+#pragma unroll
+    for (int w = 0; w < BAL_THREADS / 32; ++w) {
+      zs += s_z[w];
+      ns += s_n[w];
+    }
+    const bool whole = gridDim.x == 1 && a.S == 1;
+    const float inv_n = ns > 0 ? 1.0f / static_cast<float>(ns) : 0.0f;
+    const float fs = inv_n * static_cast<float>(a.E) / static_cast<float>(a.k);
     const long long slot = blockIdx.x + s;
-    for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
+    float sum[1] = {0.0f};
+    for (int i = threadIdx.x; i < a.E; i += BAL_THREADS) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < BAL_WARPS; ++w) v += s_p[w][i];
-      a.part_p[slot * a.E + i] = v;
-      a.part_c[slot * a.E + i] = s_c[i];
-    }
-    if (threadIdx.x == 0) {
-      float zs = 0.0f;
-      int ns = 0;
-      for (int w = 0; w < BAL_WARPS; ++w) {
-        zs += s_z[w];
-        ns += s_n[w];
+      for (int w = 0; w < BAL_THREADS / 32; ++w) v += s_p[w][i];
+      if (whole) {
+        a.counts[i] = s_c[i];
+        a.prob_mean[i] = v * inv_n;
+        sum[0] = fmaf(static_cast<float>(s_c[i]) * fs, v * inv_n, sum[0]);
+      } else {
+        a.part_p[slot * a.E + i] = v;
+        a.part_c[slot * a.E + i] = s_c[i];
       }
-      a.part_z[slot] = zs;
-      a.part_n[slot] = ns;
+    }
+    if (whole) row_sums<false, 1>(sum, buf);
+    if (threadIdx.x == 0) {
+      if (whole) {
+        a.seq_tokens[0] = ns;
+        a.losses[0] = a.coef * sum[0];
+        a.losses[1] = a.z_coef * zs * inv_n;
+      } else {
+        a.part_z[slot] = zs;
+        a.part_n[slot] = ns;
+      }
     }
     __syncthreads();
   }
+  if (gridDim.x == 1 && a.S == 1 && a.seq_offsets && threadIdx.x == 0 && (a.seq_offsets[0] != 0 || a.seq_offsets[1] != a.T))
+    set_status(a.status, MOE_ERR_INVARIANT);
 }
 
-// A block per sequence adds its parts in token order; the last block to finish turns the
-// sequences' sums into the losses, in sequence order.
+// Block (x, s) adds the parts of sequence s for 32 experts: 32 threads an expert's four,
+// each every 32nd part in token order, then the 32 in order.  The last block to finish turns
+// the sums into the losses.
 __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) {
+  __shared__ float4 s_p[32][8];
+  __shared__ int4 s_c[32][8];
   __shared__ float buf[32 * 2];
+  __shared__ float buf4[32 * 4];
   __shared__ int s_last;
-  const int s = blockIdx.x;
-  const int b = seq_at(a, s), e = seq_at(a, s + 1);
-  if (threadIdx.x == 0 && a.seq_offsets) {
+  const int s = blockIdx.y;
+  const int b = a.seq_offsets ? min(max(a.seq_offsets[s], 0), a.T) : 0;
+  const int e = a.seq_offsets ? min(max(a.seq_offsets[s + 1], 0), a.T) : a.T;
+  if (threadIdx.x == 0 && blockIdx.x == 0 && a.seq_offsets) {
     const int x = a.seq_offsets[s], y = a.seq_offsets[s + 1];
     if (x > y || (s == 0 && x != 0) || (s == a.S - 1 && y != a.T)) set_status(a.status, MOE_ERR_INVARIANT);
   }
   int first = 0, last = -1;  // slots
   if (b < e) {
-    first = b / BAL_CHUNK + s;
-    last = (e - 1) / BAL_CHUNK + s;
+    first = b / a.chunk + s;
+    last = (e - 1) / a.chunk + s;
   }
-  int n = 0;
-  float z = 0.0f;
-  for (int i = first; i <= last; ++i) {
-    n += a.part_n[i];
-    z += a.part_z[i];
+  // n in two parts, whose sums over at most 320 chunks fp32 holds exactly
+  float nz[3] = {0.0f, 0.0f, 0.0f};
+  for (int i = first + static_cast<int>(threadIdx.x); i <= last; i += 256) {
+    const int c = a.part_n[i];
+    nz[0] += static_cast<float>(c & 0xFFF);
+    nz[1] += static_cast<float>(c >> 12);
+    nz[2] += a.part_z[i];
   }
+  const int col = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  const int x = blockIdx.x * JOIN_COLS + col * 4;
+  float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  int4 c = make_int4(0, 0, 0, 0);
+  const bool vec = a.E % 4 == 0;
+  for (int j = first + grp; j <= last; j += 32) {
+    const float* pp = a.part_p + static_cast<long long>(j) * a.E + x;
+    const int* pc = a.part_c + static_cast<long long>(j) * a.E + x;
+    if (vec) {
+      if (x < a.E) {
+        const float4 q = *reinterpret_cast<const float4*>(pp);
+        const int4 d = *reinterpret_cast<const int4*>(pc);
+        p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
+        c.x += d.x; c.y += d.y; c.z += d.z; c.w += d.w;
+      }
+    } else {
+      if (x < a.E) { p.x += pp[0]; c.x += pc[0]; }
+      if (x + 1 < a.E) { p.y += pp[1]; c.y += pc[1]; }
+      if (x + 2 < a.E) { p.z += pp[2]; c.z += pc[2]; }
+      if (x + 3 < a.E) { p.w += pp[3]; c.w += pc[3]; }
+    }
+  }
+  s_p[grp][col] = p;
+  s_c[grp][col] = c;
+  __shared__ float buf3[32 * 3];
+  row_sums<false, 3>(nz, buf3);  // and the parts are in shared memory
+  const int n = static_cast<int>(nz[0]) + (static_cast<int>(nz[1]) << 12);
   const float inv_n = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
   const float fs = inv_n * static_cast<float>(a.E) / static_cast<float>(a.k);
   float sum[1] = {0.0f};
-  for (int i = threadIdx.x; i < a.E; i += blockDim.x) {
-    float p = 0.0f;
-    int c = 0;
-    for (int j = first; j <= last; ++j) {
-      p += a.part_p[static_cast<long long>(j) * a.E + i];
-      c += a.part_c[static_cast<long long>(j) * a.E + i];
+  if (threadIdx.x < JOIN_COLS) {
+    const int i = blockIdx.x * JOIN_COLS + threadIdx.x;
+    float v = 0.0f;
+    int k = 0;
+#pragma unroll
+    for (int g = 0; g < 32; ++g) {
+      v += reinterpret_cast<const float*>(s_p[g])[threadIdx.x];
+      k += reinterpret_cast<const int*>(s_c[g])[threadIdx.x];
     }
-    a.counts[static_cast<long long>(s) * a.E + i] = c;
-    a.prob_mean[static_cast<long long>(s) * a.E + i] = p * inv_n;
-    sum[0] = fmaf(static_cast<float>(c) * fs, p * inv_n, sum[0]);
-  }
-  row_sums<false, 1>(sum, buf);
-  if (threadIdx.x == 0) {
-    a.seq_tokens[s] = n;
-    a.seq_loss[2 * s] = sum[0];
-    a.seq_loss[2 * s + 1] = z;
-    __threadfence();
-    s_last = atomicAdd(a.counter, 1) == static_cast<int>(gridDim.x) - 1;
+    if (i < a.E) {
+      a.counts[static_cast<long long>(s) * a.E + i] = k;
+      a.prob_mean[static_cast<long long>(s) * a.E + i] = v * inv_n;
+      sum[0] = static_cast<float>(k) * fs * (v * inv_n);
+    }
+    row_sums<true, 1>(sum, buf);
+    if (threadIdx.x == 0) {
+      a.seq_loss[static_cast<long long>(s) * gridDim.x + blockIdx.x] = sum[0];
+      if (blockIdx.x == 0) {
+        a.seq_tokens[s] = n;
+        a.seq_z[s] = nz[2];
+      }
+      __threadfence();
+      s_last = atomicAdd(a.counter, 1) == static_cast<int>(gridDim.x * gridDim.y) - 1;
+    }
   }
   __syncthreads();
   if (!s_last) return;
   __threadfence();
   float t[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // losses, sequences and tokens that count
-  __shared__ float buf4[32 * 4];
-  for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
-    const int c = __ldcg(&a.seq_tokens[i]);
-    t[0] += __ldcg(&a.seq_loss[2 * i]);
-    t[1] += __ldcg(&a.seq_loss[2 * i + 1]);
-    t[2] += c > 0 ? 1.0f : 0.0f;
-    t[3] += static_cast<float>(c);
+  for (int i = threadIdx.x; i < a.S; i += 256) {
+    const int k = __ldcg(&a.seq_tokens[i]);
+    t[1] += __ldcg(&a.seq_z[i]);
+    t[2] += k > 0 ? 1.0f : 0.0f;
+    t[3] += static_cast<float>(k);
   }
+  for (long long i = threadIdx.x; i < static_cast<long long>(a.S) * gridDim.x; i += 256) t[0] += __ldcg(&a.seq_loss[i]);
   row_sums<false, 4>(t, buf4);
   if (threadIdx.x == 0) {
     a.losses[0] = t[2] > 0.0f ? a.coef * t[0] / t[2] : 0.0f;
-    a.losses[1] = t[3] > 0.0f ? a.z_coef * t[1] / t[3] : 0.0f;
+    a.losses[1] = t[3] > 0.0f && a.z_coef != 0.0f ? a.z_coef * t[1] / t[3] : 0.0f;
   }
 }
 
-// A warp takes a run of consecutive tokens.  dl_j = g0 coef / (S' n_s) p_j (f_j - sum f p)
+// A group takes a run of consecutive tokens.  dl_j = g0 coef / (S' n_s) p_j (f_j - sum f p)
 // [(1 - sigmoid(l_j)) for sigmoid scores] + g1 z_coef 2 / N lse softmax(l)_j.
-template <int PL, bool SIGMOID>
-__global__ void __launch_bounds__(256) balance_bwd_kernel(const BalanceArgs a, int run) {
+template <int VEC, int G, int PLV, bool SIGMOID>
+__global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceArgs a) {
+  constexpr int N = VEC * PLV;
   __shared__ float buf[32 * 2];
-  const int lane = threadIdx.x & 31;
-  float tot[2] = {0.0f, 0.0f};  // sequences and tokens that count
-  for (int i = threadIdx.x; i < a.S; i += blockDim.x) {
+  __shared__ int s_off[SEQ_TABLE + 1];
+  const int gl = threadIdx.x % G;
+  const long long t0 = (static_cast<long long>(blockIdx.x) * (BAL_THREADS / G) + threadIdx.x / G) * a.run;
+  const int t1 = static_cast<int>(min(static_cast<long long>(a.T), t0 + a.run));
+  auto kept = [&](long long t) { return t < t1 && (!a.mask || a.mask[t]); };
+  // the first token's values are on their way while the totals are added up
+  float l[N], old[N];
+  bool keep = kept(t0), keep_next = a.run > 1 && kept(t0 + 1);
+  load_row<VEC, G, PLV>(a.logits + t0 * a.E, a.E, gl, keep, -INFINITY, l);
+  load_row<VEC, G, PLV>(a.d_logits + t0 * a.E, a.E, gl, keep && a.accumulate, 0.0f, old);
+  const Sequences seqs(a, s_off);  // the sum's barrier is its
+  float tot[2] = {0.0f, 0.0f};     // sequences and tokens that count
+  for (int i = threadIdx.x; i < a.S; i += BAL_THREADS) {
     const int c = a.tokens_in[i];
     tot[0] += c > 0 ? 1.0f : 0.0f;
     tot[1] += static_cast<float>(c);
@@ -262,53 +410,80 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(const BalanceArgs a, i
   row_sums<false, 2>(tot, buf);
   const float g0 = (a.grad_losses ? a.grad_losses[0] : 1.0f) * a.coef / fmaxf(tot[0], 1.0f);
   const float g1 = (a.grad_losses ? a.grad_losses[1] : 1.0f) * a.z_coef * 2.0f / fmaxf(tot[1], 1.0f);
-  const long long t0 = (static_cast<long long>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * run;
-  if (t0 >= a.T) return;
-  const int t1 = static_cast<int>(min(static_cast<long long>(a.T), t0 + run));
-  int s = seq_of(a, static_cast<int>(t0));
+  int s = t0 < a.T ? seqs.of(static_cast<int>(t0)) : 0;
   int end = -1;
-  float f[PL], gs = 0.0f;
-  for (int t = static_cast<int>(t0); t < t1; ++t) {
-    if (t >= end) {  // first token of the run, or of a sequence
-      while (s + 1 < a.S && seq_at(a, s + 1) <= t) ++s;
-      end = s + 1 < a.S ? seq_at(a, s + 1) : a.T;
+  float f[N], gs = 0.0f;
+#pragma unroll
+  for (int c = 0; c < N; ++c) f[c] = 0.0f;
+  for (int step = 0; step < a.run; ++step) {
+    const long long t = t0 + step;
+    if (t < t1 && t >= end) {  // first token of the run, or of a sequence
+      while (s + 1 < a.S && seqs.at(s + 1) <= t) ++s;
+      end = s + 1 < a.S ? seqs.at(s + 1) : a.T;
       const int n = a.tokens_in[s];
       const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
       gs = g0 * inv;
       const float fs = inv * static_cast<float>(a.E) / static_cast<float>(a.k);
 #pragma unroll
-      for (int c = 0; c < PL; ++c)
-        f[c] = lane + 32 * c < a.E ? static_cast<float>(a.counts_in[static_cast<long long>(s) * a.E + lane + 32 * c]) * fs : 0.0f;
+      for (int c = 0; c < N; ++c) {
+        const int i = (gl + G * (c / VEC)) * VEC + c % VEC;
+        f[c] = i < a.E ? static_cast<float>(a.counts_in[static_cast<long long>(s) * a.E + i]) * fs : 0.0f;
+      }
     }
-    float* out = a.d_logits + static_cast<long long>(t) * a.E;
-    if (a.mask && !a.mask[t]) {
-      if (!a.accumulate)
-        for (int i = lane; i < a.E; i += 32) out[i] = 0.0f;
-      continue;
+    __syncwarp();
+    const bool keep_after = step + 2 < a.run && kept(t + 2);
+    float l_next[N], old_next[N];
+    load_row<VEC, G, PLV>(a.logits + (t + 1) * a.E, a.E, gl, keep_next, -INFINITY, l_next);
+    load_row<VEC, G, PLV>(a.d_logits + (t + 1) * a.E, a.E, gl, keep_next && a.accumulate, 0.0f, old_next);
+    const float top = row_top<G>(l);
+    float p[N], inv, lse, q_inv, d[N];
+    if (!SIGMOID) {
+      row_softmax<G>(l, top, a.z_coef != 0.0f, p, inv, lse);
+      float m = 0.0f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) m = fmaf(f[c], p[c], m);
+      m = group_sum<G>(m) * inv;
+      const float gp = gs * inv, gz = g1 * lse * inv;
+#pragma unroll
+      for (int c = 0; c < N; ++c) d[c] = p[c] * fmaf(gp, f[c] - m, gz);
+    } else {
+      float rest[N];
+      row_sigmoid<G>(l, top, p, inv, &rest);
+      float m = 0.0f;
+#pragma unroll
+      for (int c = 0; c < N; ++c) m = fmaf(f[c], p[c], m);
+      m = group_sum<G>(m) * inv;
+      const float gp = gs * inv;
+#pragma unroll
+      for (int c = 0; c < N; ++c) d[c] = gp * p[c] * (f[c] - m) * rest[c];
+      if (a.z_coef != 0.0f) {
+        row_softmax<G>(l, top, true, p, q_inv, lse);
+        const float gz = g1 * lse * q_inv;
+#pragma unroll
+        for (int c = 0; c < N; ++c) d[c] = fmaf(gz, p[c], d[c]);
+      }
     }
-    float l[PL], p[PL], q[PL], lse = 0.0f;
-    load_row(a.logits + static_cast<long long>(t) * a.E, a.E, lane, l);
-    const float top = row_top(l);
-    if (!SIGMOID || a.z_coef != 0.0f) row_softmax(l, top, q, lse);
-    else
+    if (t < t1 && (keep || !a.accumulate)) {
+      float* out = a.d_logits + t * a.E;
 #pragma unroll
-      for (int c = 0; c < PL; ++c) q[c] = 0.0f;
-    if (SIGMOID) row_sigmoid(l, top, p);
-    else
+      for (int i = 0; i < PLV; ++i) {
+        const int e = (gl + G * i) * VEC;
+        if (e >= a.E) continue;
+        if (VEC == 4) {
+          const float4 v = make_float4(old[4 * i] + d[4 * i], old[VEC * i + VEC / 3] + d[VEC * i + VEC / 3],
+                                       old[VEC * i + VEC / 2] + d[VEC * i + VEC / 2], old[VEC * i + VEC - 1] + d[VEC * i + VEC - 1]);
+          *reinterpret_cast<float4*>(out + e) = keep ? v : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        } else {
+          out[e] = keep ? old[i] + d[i] : 0.0f;
+        }
+      }
+    }
+    keep = keep_next;
+    keep_next = keep_after;
 #pragma unroll
-      for (int c = 0; c < PL; ++c) p[c] = q[c];
-    float m = 0.0f;
-#pragma unroll
-    for (int c = 0; c < PL; ++c) m = fmaf(f[c], p[c], m);
-    m = warp_sum(m);
-#pragma unroll
-    for (int c = 0; c < PL; ++c) {
-      const int i = lane + 32 * c;
-      if (i >= a.E) continue;
-      float d = gs * p[c] * (f[c] - m);
-      if (SIGMOID) d *= 1.0f / (1.0f + expf(l[c]));
-      d = fmaf(g1 * lse, q[c], d);
-      out[i] = a.accumulate ? out[i] + d : d;
+    for (int c = 0; c < N; ++c) {
+      l[c] = l_next[c];
+      old[c] = old_next[c];
     }
   }
 }
@@ -317,12 +492,30 @@ __global__ void __launch_bounds__(256) balance_bwd_kernel(const BalanceArgs a, i
 
 static size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
-static long long balance_slots(const moe_balance_dims& m) {
-  return (static_cast<long long>(m.T) + BAL_CHUNK - 1) / BAL_CHUNK + m.S;
+// Lanes of a token's group.
+static int balance_lanes(int E) {
+  if (E % 4 != 0) return 32;
+  int g = 1;
+  while (g < 32 && g * 16 < E) g *= 2;
+  return g;
+}
+
+// Tokens of a forward block: about two blocks an SM (counted as 160 whatever the GPU, as
+// the workspace's size goes by it), each group with at least one token; up to four a group
+// stay in one block, whose results then need no join.
+static int balance_chunk(const moe_balance_dims& m) {
+  const int groups = BAL_THREADS / balance_lanes(m.E);
+  if (m.T <= 4 * groups) return 4 * groups;
+  const long long per = (static_cast<long long>(m.T) + 319) / 320;
+  return static_cast<int>((per + groups - 1) / groups * groups);
+}
+static long long balance_chunks(const moe_balance_dims& m) {
+  const int chunk = balance_chunk(m);
+  return (static_cast<long long>(m.T) + chunk - 1) / chunk;
 }
 
 static size_t balance_carve(const moe_balance_dims& m, void* ws, BalanceArgs* a) {
-  const size_t slots = balance_slots(m);
+  const size_t slots = balance_chunks(m) + m.S, joins = (m.E + JOIN_COLS - 1) / JOIN_COLS;
   uint8_t* p = static_cast<uint8_t*>(ws);
   size_t at = 0;
   auto take = [&](size_t bytes) {
@@ -335,7 +528,8 @@ static size_t balance_carve(const moe_balance_dims& m, void* ws, BalanceArgs* a)
   uint8_t* pc = take(slots * m.E * 4);
   uint8_t* pz = take(slots * 4);
   uint8_t* pn = take(slots * 4);
-  uint8_t* sl = take(static_cast<size_t>(m.S) * 8);
+  uint8_t* sl = take(static_cast<size_t>(m.S) * joins * 4);
+  uint8_t* sz = take(static_cast<size_t>(m.S) * 4);
   if (a) {
     a->counter = reinterpret_cast<int32_t*>(counter);
     a->part_p = reinterpret_cast<float*>(pp);
@@ -343,6 +537,7 @@ static size_t balance_carve(const moe_balance_dims& m, void* ws, BalanceArgs* a)
     a->part_z = reinterpret_cast<float*>(pz);
     a->part_n = reinterpret_cast<int32_t*>(pn);
     a->seq_loss = reinterpret_cast<float*>(sl);
+    a->seq_z = reinterpret_cast<float*>(sz);
   }
   return at;
 }
@@ -353,47 +548,68 @@ static BalanceArgs balance_args(const moe_balance_dims& m) {
   return a;
 }
 
-template <int PL>
-static void launch_fwd(const BalanceArgs& a, bool sigmoid, int grid, cudaStream_t s) {
-  if (sigmoid) balance_fwd_kernel<PL, true><<<grid, BAL_WARPS * 32, 0, s>>>(a);
-  else balance_fwd_kernel<PL, false><<<grid, BAL_WARPS * 32, 0, s>>>(a);
+using BalanceKernel = void (*)(BalanceArgs);
+
+template <bool SIGMOID>
+static BalanceKernel pick_fwd(int E) {
+  if (E % 4 != 0) {
+    if (E <= 128) return balance_fwd_kernel<1, 32, 4, SIGMOID>;
+    if (E <= 512) return balance_fwd_kernel<1, 32, 16, SIGMOID>;
+    return balance_fwd_kernel<1, 32, 32, SIGMOID>;
+  }
+  switch (balance_lanes(E)) {
+    case 1: return balance_fwd_kernel<4, 1, 4, SIGMOID>;
+    case 2: return balance_fwd_kernel<4, 2, 4, SIGMOID>;
+    case 4: return balance_fwd_kernel<4, 4, 4, SIGMOID>;
+    case 8: return balance_fwd_kernel<4, 8, 4, SIGMOID>;
+    case 16: return balance_fwd_kernel<4, 16, 4, SIGMOID>;
+    default: return E <= 512 ? balance_fwd_kernel<4, 32, 4, SIGMOID> : balance_fwd_kernel<4, 32, 8, SIGMOID>;
+  }
 }
-template <int PL>
-static void launch_bwd(const BalanceArgs& a, bool sigmoid, int grid, int run, cudaStream_t s) {
-  if (sigmoid) balance_bwd_kernel<PL, true><<<grid, 256, 0, s>>>(a, run);
-  else balance_bwd_kernel<PL, false><<<grid, 256, 0, s>>>(a, run);
+template <bool SIGMOID>
+static BalanceKernel pick_bwd(int E) {
+  if (E % 4 != 0) {
+    if (E <= 128) return balance_bwd_kernel<1, 32, 4, SIGMOID>;
+    if (E <= 512) return balance_bwd_kernel<1, 32, 16, SIGMOID>;
+    return balance_bwd_kernel<1, 32, 32, SIGMOID>;
+  }
+  switch (balance_lanes(E)) {
+    case 1: return balance_bwd_kernel<4, 1, 4, SIGMOID>;
+    case 2: return balance_bwd_kernel<4, 2, 4, SIGMOID>;
+    case 4: return balance_bwd_kernel<4, 4, 4, SIGMOID>;
+    case 8: return balance_bwd_kernel<4, 8, 4, SIGMOID>;
+    case 16: return balance_bwd_kernel<4, 16, 4, SIGMOID>;
+    default: return E <= 512 ? balance_bwd_kernel<4, 32, 4, SIGMOID> : balance_bwd_kernel<4, 32, 8, SIGMOID>;
+  }
 }
 
-static cudaError_t launch_balance_fwd(const BalanceArgs& a, bool sigmoid, cudaStream_t s) {
-  cudaError_t err = cudaMemsetAsync(a.counter, 0, 4, s);
-  if (err != cudaSuccess) return err;
-  if (a.T > 0) {
-    const int grid = (a.T + BAL_CHUNK - 1) / BAL_CHUNK;
-    if (a.E <= 32) launch_fwd<1>(a, sigmoid, grid, s);
-    else if (a.E <= 64) launch_fwd<2>(a, sigmoid, grid, s);
-    else if (a.E <= 128) launch_fwd<4>(a, sigmoid, grid, s);
-    else if (a.E <= 256) launch_fwd<8>(a, sigmoid, grid, s);
-    else if (a.E <= 512) launch_fwd<16>(a, sigmoid, grid, s);
-    else launch_fwd<32>(a, sigmoid, grid, s);
+static cudaError_t launch_balance_fwd(BalanceArgs a, const moe_balance_dims& m, cudaStream_t s) {
+  cudaError_t err;
+  a.chunk = balance_chunk(m);
+  const long long chunks = balance_chunks(m);
+  if (chunks > 0) {
+    const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_fwd<true>(a.E) : pick_fwd<false>(a.E);
+    kern<<<static_cast<unsigned>(chunks), BAL_THREADS, 0, s>>>(a);
     count_launch();
     if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    if (chunks == 1 && a.S == 1) return cudaSuccess;
+  } else if ((err = cudaMemsetAsync(a.counter, 0, 4, s)) != cudaSuccess) {
+    return err;
   }
-  balance_join_kernel<<<a.S, 256, 0, s>>>(a);
+  balance_join_kernel<<<dim3((a.E + JOIN_COLS - 1) / JOIN_COLS, a.S), 256, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
 
-static cudaError_t launch_balance_bwd(const BalanceArgs& a, bool sigmoid, cudaStream_t s) {
+static cudaError_t launch_balance_bwd(BalanceArgs a, const moe_balance_dims& m, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  const long long warps = static_cast<long long>(num_sms()) * 32;
-  const int run = static_cast<int>((a.T + warps - 1) / warps);
-  const int grid = static_cast<int>((a.T + 8ll * run - 1) / (8ll * run));
-  if (a.E <= 32) launch_bwd<1>(a, sigmoid, grid, run, s);
-  else if (a.E <= 64) launch_bwd<2>(a, sigmoid, grid, run, s);
-  else if (a.E <= 128) launch_bwd<4>(a, sigmoid, grid, run, s);
-  else if (a.E <= 256) launch_bwd<8>(a, sigmoid, grid, run, s);
-  else if (a.E <= 512) launch_bwd<16>(a, sigmoid, grid, run, s);
-  else launch_bwd<32>(a, sigmoid, grid, run, s);
+  const int groups = BAL_THREADS / balance_lanes(a.E);
+  // up to 32 warps an SM, each with the groups of BAL_THREADS / 8 of a block
+  const long long most = static_cast<long long>(num_sms()) * 4 * groups;
+  a.run = static_cast<int>((a.T + most - 1) / most);
+  const long long grid = (a.T + static_cast<long long>(groups) * a.run - 1) / (static_cast<long long>(groups) * a.run);
+  const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_bwd<true>(a.E) : pick_bwd<false>(a.E);
+  kern<<<static_cast<unsigned>(grid), BAL_THREADS, 0, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -410,7 +626,7 @@ moe_status moe_balance_check_dims(const moe_balance_dims* dims) {
   if (m.T < 0 || m.E <= 0 || m.k <= 0 || m.k > m.E || m.k > 32 || m.S <= 0) return MOE_ERR_INVALID_ARG;
   if (m.score != MOE_SCORE_SOFTMAX && m.score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
   if (!isfinite(m.coef) || !isfinite(m.z_coef)) return MOE_ERR_INVALID_ARG;
-  if (m.E > BAL_MAX_E || m.S > BAL_MAX_S) return MOE_ERR_UNSUPPORTED;
+  if (m.E > BAL_MAX_E || m.S > BAL_MAX_S || m.T > BAL_MAX_T) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -436,7 +652,7 @@ moe_status moe_balance_fwd(const moe_balance_dims* dims, const float* logits, co
   balance_carve(*dims, workspace, &a);
   a.logits = logits; a.topk_idx = topk_idx; a.seq_offsets = seq_offsets; a.mask = mask; a.losses = losses;
   a.counts = counts; a.prob_mean = prob_mean; a.seq_tokens = seq_tokens; a.status = dev_status;
-  return status_of(launch_balance_fwd(a, dims->score == MOE_SCORE_SIGMOID, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_balance_fwd(a, *dims, static_cast<cudaStream_t>(stream)));
 }
 
 moe_status moe_balance_bwd(const moe_balance_dims* dims, const float* logits, const int32_t* seq_offsets,
@@ -451,7 +667,7 @@ moe_status moe_balance_bwd(const moe_balance_dims* dims, const float* logits, co
   BalanceArgs a = balance_args(*dims);
   a.logits = logits; a.seq_offsets = seq_offsets; a.mask = mask; a.counts_in = counts; a.tokens_in = seq_tokens;
   a.grad_losses = grad_losses; a.accumulate = accumulate; a.d_logits = d_logits;
-  return status_of(launch_balance_bwd(a, dims->score == MOE_SCORE_SIGMOID, static_cast<cudaStream_t>(stream)));
+  return status_of(launch_balance_bwd(a, *dims, static_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

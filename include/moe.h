@@ -612,7 +612,7 @@ moe_status moe_merge_bwd(const moe_norm_dims* dims, const void* dh_out, const mo
  * never used (NaN or infinities there change nothing).
  */
 typedef struct moe_balance_dims {
-  int32_t T;     /* tokens, 0 allowed */
+  int32_t T;     /* tokens, 0 .. 2^30 */
   int32_t E;     /* experts, 1 .. 1024 */
   int32_t k;     /* experts per token, 1 .. min(E, 32) */
   int32_t score; /* MOE_SCORE_* */
