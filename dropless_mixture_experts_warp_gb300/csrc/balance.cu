@@ -178,36 +178,58 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
   __shared__ int s_off[SEQ_TABLE + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G, group = threadIdx.x / G;
   const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+  // The chunk's first tokens are on their way before their sequences are known.  A token's
+  // mask is read two tokens ahead, its logits and its first choice a lane one ahead.
+  auto kept = [&](int t, int e) { return t < e && (!a.mask || a.mask[t]); };
+  auto choice = [&](int t, bool there) { return there && gl < a.k ? a.topk_idx[static_cast<long long>(t) * a.k + gl] : -1; };
+  int t = c0 + group, x;
+  bool keep = kept(t, c1), keep_next = kept(t + GROUPS, c1);
+  float l[N];
+  load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, t < c1, -INFINITY, l);
+  x = choice(t, t < c1);
   const Sequences seqs(a, s_off);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;  // of the join's blocks
   __syncthreads();
+  launch_dependents();
+  bool fresh = true;
   for (int s = seqs.of(c0); s < a.S; ++s) {
     const int start = seqs.at(s);
     if (start >= c1) break;
     const int b = max(c0, start), e = min(c1, seqs.at(s + 1));
     if (b >= e) continue;
     for (int i = threadIdx.x; i < WARP_COLS; i += BAL_THREADS) s_c[i] = 0;
-    float acc[N], z = 0.0f, l[N];
+    if (fresh && b == c0) {  // what was read above is this part's, as far as that goes
+      keep = keep && t < e;
+      keep_next = keep_next && t + GROUPS < e;
+    } else {
+      t = b + group;
+      keep = kept(t, e);
+      keep_next = kept(t + GROUPS, e);
+      load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, keep, -INFINITY, l);
+      x = choice(t, keep);
+    }
+    fresh = false;
+    if (!keep) {
+#pragma unroll
+      for (int c = 0; c < N; ++c) l[c] = -INFINITY;
+    }
+    float acc[N], z = 0.0f;
     int n = 0;
 #pragma unroll
     for (int c = 0; c < N; ++c) acc[c] = 0.0f;
-    // a token's mask is read two tokens ahead, its logits one: neither waits for the other
-    auto kept = [&](int t) { return t < e && (!a.mask || a.mask[t]); };
-    int t = b + group;
-    bool keep = kept(t), keep_next = kept(t + GROUPS);
-    load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, keep, -INFINITY, l);
     __syncthreads();
-    for (int i = threadIdx.x; i < (e - b) * a.k; i += BAL_THREADS) {
-      if (a.mask && !a.mask[b + i / a.k]) continue;
-      const int x = a.topk_idx[static_cast<long long>(b) * a.k + i];
-      if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
-      else set_status(a.status, MOE_ERR_INVARIANT);
-    }
     for (int done = b; done < e; done += GROUPS) {  // a token of every group
       const int tn = t + GROUPS;
-      const bool keep_after = kept(tn + GROUPS);
+      const bool keep_after = kept(tn + GROUPS, e);
       float next[N];
       load_row<VEC, G, PLV>(a.logits + static_cast<long long>(tn) * a.E, a.E, gl, keep_next, -INFINITY, next);
+      const int x_next = choice(tn, keep_next);
+      for (int j = gl; keep && j < a.k; j += G) {
+        if (j != gl) x = a.topk_idx[static_cast<long long>(t) * a.k + j];
+        if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
+        else set_status(a.status, MOE_ERR_INVARIANT);
+      }
+      __syncwarp();
       float p[N], inv, lse = 0.0f;
       const float top = row_top<G>(l);
       if (!SIGMOID || a.z_coef != 0.0f) row_softmax<G>(l, top, a.z_coef != 0.0f, p, inv, lse);
@@ -219,6 +241,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
         acc[c] = fmaf(p[c], inv, acc[c]);
         l[c] = next[c];
       }
+      x = x_next;
       t = tn;
       keep = keep_next;
       keep_next = keep_after;
@@ -292,6 +315,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   __shared__ float buf4[32 * 4];
   __shared__ int s_last;
   const int s = blockIdx.y;
+  wait_for_previous();
   const int b = a.seq_offsets ? min(max(a.seq_offsets[s], 0), a.T) : 0;
   const int e = a.seq_offsets ? min(max(a.seq_offsets[s + 1], 0), a.T) : a.T;
   if (threadIdx.x == 0 && blockIdx.x == 0 && a.seq_offsets) {
@@ -596,16 +620,14 @@ static cudaError_t launch_balance_fwd(BalanceArgs a, const moe_balance_dims& m, 
   } else if ((err = cudaMemsetAsync(a.counter, 0, 4, s)) != cudaSuccess) {
     return err;
   }
-  balance_join_kernel<<<dim3((a.E + JOIN_COLS - 1) / JOIN_COLS, a.S), 256, 0, s>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(balance_join_kernel, dim3((a.E + JOIN_COLS - 1) / JOIN_COLS, a.S), dim3(256), s, a);
 }
 
 static cudaError_t launch_balance_bwd(BalanceArgs a, const moe_balance_dims& m, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
   const int groups = BAL_THREADS / balance_lanes(a.E);
-  // up to 32 warps an SM, each with the groups of BAL_THREADS / 8 of a block
-  const long long most = static_cast<long long>(num_sms()) * 4 * groups;
+  // one wave of the two blocks that an SM holds
+  const long long most = static_cast<long long>(num_sms()) * 2 * groups;
   a.run = static_cast<int>((a.T + most - 1) / most);
   const long long grid = (a.T + static_cast<long long>(groups) * a.run - 1) / (static_cast<long long>(groups) * a.run);
   const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_bwd<true>(a.E) : pick_bwd<false>(a.E);

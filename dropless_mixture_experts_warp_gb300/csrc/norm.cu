@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
     fill<U>(dw_post[i], 0.0f);
     fill<U>(dgate[i], 0.0f);
   }
+  launch_dependents();
   int stage = 0, y_stage = 0;
   float hh = 0.0f, nh = 0.0f, yy = 0.0f;  // of the row, over all its columns
   if (worker < a.T) {
@@ -595,6 +596,7 @@ __global__ void __launch_bounds__(32 * REDUCE_GROUPS) norm_reduce_kernel(const f
                                                                          float* __restrict__ o2) {
   __shared__ float4 buf[REDUCE_GROUPS][32];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
+  wait_for_previous();
   if (!out) return;
   const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
   const int c = (blockIdx.x * 32 + lane) * 4;
@@ -725,11 +727,10 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
     if (err != cudaSuccess) return err;
   }
   if (dw_next || dw_post || dgate_cols) {
-    norm_reduce_kernel<<<dim3((a.d + 127) / 128, 3), 32 * REDUCE_GROUPS, 0, s>>>(a.part, workers, a.d, dw_next, dw_post,
-                                                                                 dgate_cols);
-    count_launch();
+    return launch_early(norm_reduce_kernel, dim3((a.d + 127) / 128, 3), dim3(32 * REDUCE_GROUPS), s,
+                        static_cast<const float*>(a.part), workers, a.d, dw_next, dw_post, dgate_cols);
   }
-  return cudaGetLastError();
+  return cudaSuccess;
 }
 
 static NormArgs norm_args(const moe_norm_dims& m) {
