@@ -9,6 +9,7 @@ namespace moe {
 constexpr int ADAM_BLOCK = 128;         // elements that share a scale: a warp's step, 4 a lane
 constexpr int ADAM_TENSORS = 96;        // tensors of one launch (their descriptors are its arguments)
 constexpr int ADAM_THREADS = 256;
+constexpr int BLOCKS_32 = 5, BLOCKS_8 = 3, BLOCKS_VALUES = 8;  // of a kernel on an SM
 
 struct AdamTensor {
   float* w;
@@ -163,7 +164,7 @@ __device__ __forceinline__ int tensor_of(const A& a, long long unit) {
 }
 
 // fp32 states.  A unit of elements a block, four consecutive ones a thread.
-__global__ void __launch_bounds__(ADAM_THREADS) adamw_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_32) adamw_kernel(const __grid_constant__ AdamArgs a) {
   AdamScalars sc;
   int step;
   if (!adam_scalars(a, sc, step)) return;
@@ -433,7 +434,7 @@ __device__ __forceinline__ void adam8_unit(const Unit8& c, const AdamTensor& t, 
     step8<G16, true>(c, t, i + lane * 4, fetch8<G16>(t, i + lane * 4));
 }
 
-__global__ void __launch_bounds__(ADAM_THREADS, 3) adamw8_kernel(const __grid_constant__ AdamArgs a) {
+__global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __grid_constant__ AdamArgs a) {
   __shared__ Slot8 rings[ADAM_THREADS / 32][RING8];
   Slot8* const ring = rings[threadIdx.x >> 5];
   AdamScalars sc;
@@ -479,7 +480,7 @@ struct AdamValueArgs {
 
 // The values of 8-bit states.
 template <typename OT>
-__global__ void __launch_bounds__(ADAM_THREADS) adamw_values_kernel(const __grid_constant__ AdamValueArgs a) {
+__global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_VALUES) adamw_values_kernel(const __grid_constant__ AdamValueArgs a) {
   for (long long unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
     const AdamValue& t = a.t[tensor_of(a, unit)];
     const long long start = (unit - t.first) * a.chunk;
@@ -529,16 +530,24 @@ __global__ void __launch_bounds__(ADAM_THREADS) adamw_values_kernel(const __grid
 }
 
 static long long adam_units(long long n, int chunk) { return (n + chunk - 1) / chunk; }
-// Units of 32768 elements, or, where those would leave the SMs less than eight blocks each,
+// Units of 16384 elements, or, where those would leave the SMs less than eight blocks each,
 // smaller ones (2.2M elements of 95 tensors: 2048; 16.4 us with 8192, 12.7 us with 4096).
 static int adam_chunk(long long total) {
-  int chunk = 32768;
+  int chunk = 16384;
   while (chunk > 2048 && total < static_cast<long long>(chunk) * num_sms() * 8) chunk /= 2;
   return chunk;
 }
-static int adam_grid(long long units) {
-  const long long most = static_cast<long long>(num_sms()) * 8;
+// The blocks that the SMs hold at once (the kernels' launch bounds): a second, partial wave
+// would leave SMs idle at its end.
+static int adam_grid(long long units, int per_sm) {
+  const long long most = static_cast<long long>(num_sms()) * per_sm;
   return static_cast<int>(units < most ? units : most);
+}
+template <typename A>
+static cudaError_t launch_adam(void (*kern)(A), int grid, const A& a, cudaStream_t s) {
+  kern<<<grid, ADAM_THREADS, 0, s>>>(a);
+  count_launch();
+  return cudaGetLastError();
 }
 
 }  // namespace moe
@@ -608,10 +617,8 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
       a.units += adam_units(t.n, a.chunk);
     }
     if (a.units == 0) continue;
-    if (eight) adamw8_kernel<<<adam_grid(a.units), ADAM_THREADS, 0, s>>>(a);
-    else adamw_kernel<<<adam_grid(a.units), ADAM_THREADS, 0, s>>>(a);
-    count_launch();
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = eight ? launch_adam(adamw8_kernel, adam_grid(a.units, BLOCKS_8), a, s)
+                                  : launch_adam(adamw_kernel, adam_grid(a.units, BLOCKS_32), a, s);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
@@ -642,10 +649,9 @@ moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int3
       a.units += adam_units(t.n, a.chunk);
     }
     if (a.units == 0) continue;
-    if (out_type == MOE_TYPE_BF16) adamw_values_kernel<moe_bf16><<<adam_grid(a.units), ADAM_THREADS, 0, s>>>(a);
-    else adamw_values_kernel<float><<<adam_grid(a.units), ADAM_THREADS, 0, s>>>(a);
-    count_launch();
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = out_type == MOE_TYPE_BF16
+                                ? launch_adam(adamw_values_kernel<moe_bf16>, adam_grid(a.units, BLOCKS_VALUES), a, s)
+                                : launch_adam(adamw_values_kernel<float>, adam_grid(a.units, BLOCKS_VALUES), a, s);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
