@@ -9,7 +9,7 @@ namespace moe {
 constexpr int ADAM_BLOCK = 128;         // elements that share a scale: a warp's step, 4 a lane
 constexpr int ADAM_TENSORS = 96;        // tensors of one launch (their descriptors are its arguments)
 constexpr int ADAM_THREADS = 256;
-constexpr int BLOCKS_32 = 5, BLOCKS_8 = 3, BLOCKS_VALUES = 8;  // of a kernel on an SM
+constexpr int BLOCKS_32 = 5, BLOCKS_8 = 2, BLOCKS_VALUES = 8;  // of a kernel on an SM
 
 struct AdamTensor {
   float* w;
@@ -95,10 +95,12 @@ __device__ __forceinline__ float rcp_fast(float x) {
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float below_zero(float x) {  // 1 or 0
-  float r;
-  asm("set.lt.f32.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(x));
-  return r;
+// 0xFF in the bytes of the four that are negative.
+__device__ __forceinline__ uint32_t sign_bytes(float a, float b, float c, float d) {
+  uint32_t lo, hi;
+  asm("prmt.b32 %0, %1, %2, 0xFB;" : "=r"(lo) : "r"(__float_as_uint(a)), "r"(__float_as_uint(b)));
+  asm("prmt.b32 %0, %1, %2, 0xFB;" : "=r"(hi) : "r"(__float_as_uint(c)), "r"(__float_as_uint(d)));
+  return __byte_perm(lo, hi, 0x5410);
 }
 // max |a|, |b|, |c|; NaN if one of them is.
 __device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
@@ -107,29 +109,29 @@ __device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
   return d;
 }
 
-// Codes of two shares x of the scale (x = |m| / s, below 1) as floats: the largest k with
-// (k / 127)^2 <= x, or k + 1 with the chance that makes the mean x: y = 127^2 x lies between
-// k^2 and k^2 + 2 k + 1, and the upper one is drawn where u (2 k + 1) + k^2 - y < 0.  An
-// approximate root that falls on the other side of a k changes nothing: the draw then
-// decides for k in either case.
-__device__ __forceinline__ f32x2 encode2_m(f32x2 x, f32x2 root, f32x2 u) {
-  const f32x2 t = fma2_down(root, pair(127.0f, 127.0f), pair(TWO23, TWO23));
-  const f32x2 k = add2(t, pair(-TWO23, -TWO23));
+// Codes of two shares x of the scale (x = |m| / s, below 1): k = the largest with
+// (k / 127)^2 <= x, in the low byte of t, or k + 1 where e < 0, with the chance that makes the
+// mean x: y = 127^2 x lies between k^2 and k^2 + 2 k + 1, and e = u (2 k + 1) + k^2 - y.  An
+// approximate root that falls on the other side of a k changes nothing: the draw then decides
+// for k in either case.
+__device__ __forceinline__ void encode2_m(f32x2 x, f32x2 root, f32x2 u, float2& t, float2& e) {
+  const f32x2 t2 = fma2_down(root, pair(127.0f, 127.0f), pair(TWO23, TWO23));
+  const f32x2 k = add2(t2, pair(-TWO23, -TWO23));
   const f32x2 d = fma2(k, k, mul2(x, pair(-16129.0f, -16129.0f)));
   const f32x2 n = fma2(k, pair(0x1p-15f, 0x1p-15f), pair(0x1p-16f, 0x1p-16f));  // u comes times 2^16
-  const float2 e = unpair(fma2(u, n, d));
-  return add2(k, pair(below_zero(e.x), below_zero(e.y)));
+  t = unpair(t2);
+  e = unpair(fma2(u, n, d));
 }
 // The same for x = v / s and fourth powers, k^4 .. (k + 1)^4 = k^4 + (2 k + 1) ((k + 1)^2 + k^2);
 // 255 x^(1/4) = root * scale, from a root that the step has already.
-__device__ __forceinline__ f32x2 encode2_v(f32x2 x, f32x2 root, float scale, f32x2 u) {
-  const f32x2 t = fma2_down(root, pair(scale, scale), pair(TWO23, TWO23));
-  const f32x2 k = add2(t, pair(-TWO23, -TWO23)), k1 = add2(k, pair(1.0f, 1.0f));
+__device__ __forceinline__ void encode2_v(f32x2 x, f32x2 root, float scale, f32x2 u, float2& t, float2& e) {
+  const f32x2 t2 = fma2_down(root, pair(scale, scale), pair(TWO23, TWO23));
+  const f32x2 k = add2(t2, pair(-TWO23, -TWO23)), k1 = add2(k, pair(1.0f, 1.0f));
   const f32x2 k2 = mul2(k, k);
   const f32x2 d = fma2(k2, k2, mul2(x, pair(-4228250625.0f, -4228250625.0f)));
   const f32x2 n = mul2(fma2(k, pair(0x1p-15f, 0x1p-15f), pair(0x1p-16f, 0x1p-16f)), fma2(k1, k1, k2));
-  const float2 e = unpair(fma2(u, n, d));
-  return add2(k, pair(below_zero(e.x), below_zero(e.y)));
+  t = unpair(t2);
+  e = unpair(fma2(u, n, d));
 }
 
 struct AdamScalars {
@@ -280,90 +282,113 @@ struct Unit8 {
   uint32_t key;
 };
 
-// The step of four elements, and its stores.
-template <bool G16, bool TAIL>
-__device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long long i, const Block8& x) {
-  f32x2 g[2], m[2], v[2], w[2] = {pair(x.w.x, x.w.y), pair(x.w.z, x.w.w)};
-  if (G16) {
-    g[0] = pair(bf16_lo(x.g16.x), bf16_hi(x.g16.x));
-    g[1] = pair(bf16_lo(x.g16.y), bf16_hi(x.g16.y));
-  } else {
-    g[0] = pair(x.g32.x, x.g32.y);
-    g[1] = pair(x.g32.z, x.g32.w);
-  }
-  decode4_m(x.m, x.ms * c.b1, m);
-  decode4_v(x.v, x.vs * c.b2, v);
-  f32x2 root[2];  // v^(1/4)
-  float2 am[2], av[2];
+// The step of four elements in each of H blocks of 128 that follow each other, and its
+// stores.  Two blocks go through each stage together: their chains of roots and sums over
+// the warp fill each other's waits.
+template <bool G16, bool TAIL, int H>
+__device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long long i, const Block8 (&x)[H]) {
+  f32x2 m[H][2], v[H][2], w[H][2], root[H][2];  // root = v^(1/4)
+  float ms[H], vs[H];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    m[j] = fma2(g[j], pair(c.c1, c.c1), m[j]);
-    const f32x2 h = mul2(g[j], pair(c.c2, c.c2));
-    v[j] = fma2(h, h, v[j]);
-    am[j] = unpair(m[j]);
-    av[j] = unpair(v[j]);
-    const float2 r = make_float2(sqrt_fast(av[j].x), sqrt_fast(av[j].y));
-    const float2 den = unpair(fma2(pair(r.x, r.y), pair(c.root_bc2, c.root_bc2), pair(c.eps, c.eps)));
-    const f32x2 update = mul2(m[j], pair(rcp_fast(den.x), rcp_fast(den.y)));
-    w[j] = fma2(update, pair(c.rate, c.rate), mul2(w[j], pair(c.decay, c.decay)));
-    root[j] = pair(sqrt_fast(r.x), sqrt_fast(r.y));
+  for (int h = 0; h < H; ++h) {
+    f32x2 g[2];
+    w[h][0] = pair(x[h].w.x, x[h].w.y);
+    w[h][1] = pair(x[h].w.z, x[h].w.w);
+    if (G16) {
+      g[0] = pair(bf16_lo(x[h].g16.x), bf16_hi(x[h].g16.x));
+      g[1] = pair(bf16_lo(x[h].g16.y), bf16_hi(x[h].g16.y));
+    } else {
+      g[0] = pair(x[h].g32.x, x[h].g32.y);
+      g[1] = pair(x[h].g32.z, x[h].g32.w);
+    }
+    decode4_m(x[h].m, x[h].ms * c.b1, m[h]);
+    decode4_v(x[h].v, x[h].vs * c.b2, v[h]);
+    float2 am[2], av[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      m[h][j] = fma2(g[j], pair(c.c1, c.c1), m[h][j]);
+      const f32x2 q = mul2(g[j], pair(c.c2, c.c2));
+      v[h][j] = fma2(q, q, v[h][j]);
+      am[j] = unpair(m[h][j]);
+      av[j] = unpair(v[h][j]);
+      const float2 r = make_float2(sqrt_fast(av[j].x), sqrt_fast(av[j].y));
+      const float2 den = unpair(fma2(pair(r.x, r.y), pair(c.root_bc2, c.root_bc2), pair(c.eps, c.eps)));
+      const f32x2 update = mul2(m[h][j], pair(rcp_fast(den.x), rcp_fast(den.y)));
+      w[h][j] = fma2(update, pair(c.rate, c.rate), mul2(w[h][j], pair(c.decay, c.decay)));
+      root[h][j] = pair(sqrt_fast(r.x), sqrt_fast(r.y));
+    }
+    ms[h] = absmax3_nan(absmax3_nan(am[0].x, am[0].y, am[1].x), am[1].y, am[1].y);
+    vs[h] = absmax3_nan(absmax3_nan(av[0].x, av[0].y, av[1].x), av[1].y, av[1].y);
   }
   // elements past the end hold 0: they do not raise a maximum (bits of non-negative floats
   // order as the numbers do; a NaN is the largest)
-  const float lm = absmax3_nan(absmax3_nan(am[0].x, am[0].y, am[1].x), am[1].y, am[1].y);
-  const float lv = absmax3_nan(absmax3_nan(av[0].x, av[0].y, av[1].x), av[1].y, av[1].y);
-  float ms = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lm)));
-  float vs = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(lv)));
-  if (ms < 1.17549435e-38f) ms = 0.0f;
-  if (vs < 1.17549435e-38f) vs = 0.0f;
-  // Inverses a little below (rcp is within 2^-23): shares stay under 1, the codes within a
-  // byte without a clamp, and the largest value still draws its own code but for 2^-15 or so.
-  const float im = ms > 0.0f ? rcp_fast(ms) * (1.0f - 0x1p-22f) : 0.0f;
-  const float iv = vs > 0.0f ? rcp_fast(vs) * (1.0f - 0x1p-22f) : 0.0f;
-  const float rs = 255.0f * sqrt_fast(sqrt_fast(iv));  // 255 (v / s)^(1/4) = root * rs
-  f32x2 cm[2], cv[2];
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const uint32_t at = static_cast<uint32_t>(i) + 2 * j;
-    const uint32_t h0 = adam_mix(at * 0x9E3779B9u + c.key), h1 = adam_mix((at + 1) * 0x9E3779B9u + c.key);
-    const float2 sm = make_float2(fabsf(am[j].x) * im, fabsf(am[j].y) * im);
-    const float2 k = unpair(encode2_m(pair(sm.x, sm.y), pair(sqrt_fast(sm.x), sqrt_fast(sm.y)), draws(h0, h1, false)));
-    // 256 +- the code: its low byte is the code in two's complement
-    cm[j] = add2(pair(copysignf(k.x, am[j].x), copysignf(k.y, am[j].y)), pair(TWO23 + 256.0f, TWO23 + 256.0f));
-    cv[j] = add2(encode2_v(mul2(v[j], pair(iv, iv)), root[j], rs, draws(h0, h1, true)), pair(TWO23, TWO23));
+  for (int h = 0; h < H; ++h) {
+    ms[h] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(ms[h])));
+    vs[h] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(vs[h])));
   }
-  const float2 m0 = unpair(cm[0]), m1 = unpair(cm[1]), v0 = unpair(cv[0]), v1 = unpair(cv[1]);
-  const uint32_t wm = low_bytes(m0.x, m0.y, m1.x, m1.y);
-  uint32_t wv = low_bytes(v0.x, v0.y, v1.x, v1.y);
-  if ((wv - 0x01010101u) & ~wv & 0x80808080u) {  // a code 0, seldom: no v > 0 becomes 0
-    const float vs4[4] = {av[0].x, av[0].y, av[1].x, av[1].y};
+  uint32_t wm[H], wv[H];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (vs4[j] > 0.0f && vs > 0.0f && !((wv >> (8 * j)) & 0xFFu)) wv |= 1u << (8 * j);
-  }
-  const float2 w0 = unpair(w[0]), w1 = unpair(w[1]);
-  const uint2 w16 = make_uint2(pack_bf16(w0.x, w0.y), pack_bf16(w1.x, w1.y));
-  if ((threadIdx.x & 31) == 0) {
-    t.m_scale[i / ADAM_BLOCK] = ms;
-    t.v_scale[i / ADAM_BLOCK] = vs;
-  }
-  uint8_t* const tm = static_cast<uint8_t*>(t.m) + i;
-  uint8_t* const tv = static_cast<uint8_t*>(t.v) + i;
-  if (!TAIL || i + 4 <= t.n) {
-    *reinterpret_cast<float4*>(t.w + i) = make_float4(w0.x, w0.y, w1.x, w1.y);
-    if (t.w16) *reinterpret_cast<uint2*>(t.w16 + i) = w16;
-    *reinterpret_cast<uint32_t*>(tm) = wm;
-    *reinterpret_cast<uint32_t*>(tv) = wv;
-  } else {
-    const float ws[3] = {w0.x, w0.y, w1.x};
-    const uint32_t hs[3] = {w16.x, w16.x >> 16, w16.y};
+  for (int h = 0; h < H; ++h) {
+    if (ms[h] < 1.17549435e-38f) ms[h] = 0.0f;
+    if (vs[h] < 1.17549435e-38f) vs[h] = 0.0f;
+    // Inverses a little below (rcp is within 2^-23): shares stay under 1, the codes within a
+    // byte without a clamp, and the largest value still draws its own code but for 2^-15 or so.
+    const float im = ms[h] > 0.0f ? rcp_fast(ms[h]) * (1.0f - 0x1p-22f) : 0.0f;
+    const float iv = vs[h] > 0.0f ? rcp_fast(vs[h]) * (1.0f - 0x1p-22f) : 0.0f;
+    const float rs = 255.0f * sqrt_fast(sqrt_fast(iv));  // 255 (v / s)^(1/4) = root * rs
+    float2 am[2], tm[2], em[2], tv[2], ev[2];
 #pragma unroll
-    for (int j = 0; j < 3; ++j) {
-      if (i + j >= t.n) continue;
-      t.w[i + j] = ws[j];
-      if (t.w16) t.w16[i + j] = static_cast<moe_bf16>(hs[j]);
-      tm[j] = static_cast<uint8_t>(wm >> (8 * j));
-      tv[j] = static_cast<uint8_t>(wv >> (8 * j));
+    for (int j = 0; j < 2; ++j) {
+      const uint32_t at = static_cast<uint32_t>(i) + h * ADAM_BLOCK + 2 * j;
+      const uint32_t h0 = adam_mix(at * 0x9E3779B9u + c.key), h1 = adam_mix((at + 1) * 0x9E3779B9u + c.key);
+      am[j] = unpair(m[h][j]);
+      const float2 sm = make_float2(fabsf(am[j].x) * im, fabsf(am[j].y) * im);
+      encode2_m(pair(sm.x, sm.y), pair(sqrt_fast(sm.x), sqrt_fast(sm.y)), draws(h0, h1, false), tm[j], em[j]);
+      encode2_v(mul2(v[h][j], pair(iv, iv)), root[h][j], rs, draws(h0, h1, true), tv[j], ev[j]);
+    }
+    // four codes at a time as bytes: k or k + 1 (at most 127 and 255), then m's sign, whose
+    // two's complement is added without a carry between bytes
+    wm[h] = low_bytes(tm[0].x, tm[0].y, tm[1].x, tm[1].y) + (sign_bytes(em[0].x, em[0].y, em[1].x, em[1].y) & 0x01010101u);
+    wv[h] = low_bytes(tv[0].x, tv[0].y, tv[1].x, tv[1].y) + (sign_bytes(ev[0].x, ev[0].y, ev[1].x, ev[1].y) & 0x01010101u);
+    const uint32_t neg = sign_bytes(am[0].x, am[0].y, am[1].x, am[1].y);
+    wm[h] ^= neg;
+    wm[h] = ((wm[h] & 0x7F7F7F7Fu) + (neg & 0x01010101u)) ^ (wm[h] & 0x80808080u);
+  }
+#pragma unroll
+  for (int h = 0; h < H; ++h) {
+    if ((wv[h] - 0x01010101u) & ~wv[h] & 0x80808080u) {  // a code 0, seldom: no v > 0 becomes 0
+      const float2 v0 = unpair(v[h][0]), v1 = unpair(v[h][1]);
+      const float vs4[4] = {v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (vs4[j] > 0.0f && vs[h] > 0.0f && !((wv[h] >> (8 * j)) & 0xFFu)) wv[h] |= 1u << (8 * j);
+    }
+    const long long k = i + h * ADAM_BLOCK;
+    const float2 w0 = unpair(w[h][0]), w1 = unpair(w[h][1]);
+    const uint2 w16 = make_uint2(pack_bf16(w0.x, w0.y), pack_bf16(w1.x, w1.y));
+    if ((threadIdx.x & 31) == 0) {
+      t.m_scale[k / ADAM_BLOCK] = ms[h];
+      t.v_scale[k / ADAM_BLOCK] = vs[h];
+    }
+    uint8_t* const pm = static_cast<uint8_t*>(t.m) + k;
+    uint8_t* const pv = static_cast<uint8_t*>(t.v) + k;
+    if (!TAIL || k + 4 <= t.n) {
+      *reinterpret_cast<float4*>(t.w + k) = make_float4(w0.x, w0.y, w1.x, w1.y);
+      if (t.w16) *reinterpret_cast<uint2*>(t.w16 + k) = w16;
+      *reinterpret_cast<uint32_t*>(pm) = wm[h];
+      *reinterpret_cast<uint32_t*>(pv) = wv[h];
+    } else {
+      const float ws[3] = {w0.x, w0.y, w1.x};
+      const uint32_t hs[3] = {w16.x, w16.x >> 16, w16.y};
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        if (k + j >= t.n) continue;
+        t.w[k + j] = ws[j];
+        if (t.w16) t.w16[k + j] = static_cast<moe_bf16>(hs[j]);
+        pm[j] = static_cast<uint8_t>(wm[h] >> (8 * j));
+        pv[j] = static_cast<uint8_t>(wv[h] >> (8 * j));
+      }
     }
   }
 }
@@ -378,7 +403,8 @@ struct Slot8 {
   uint32_t v[2][32];
   float scale[2][2];  // [m, v][block]
 };
-constexpr int RING8 = 2;  // pairs on their way: with one block (16 KB an SM) the loads' latency was all of the time
+constexpr int RING8 = 4;  // pairs on their way
+constexpr int RING8_BYTES = ADAM_THREADS / 32 * RING8 * sizeof(Slot8);
 
 template <bool G16>
 __device__ __forceinline__ void fetch8_async(const AdamTensor& t, long long i, Slot8& slot, int lane) {
@@ -413,30 +439,32 @@ __device__ __forceinline__ void adam8_unit(const Unit8& c, const AdamTensor& t, 
     __syncwarp();
     const long long i = i0 + static_cast<long long>(b) * PAIR;
     const Slot8& s = ring[slot];
+    Block8 x[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      Block8 x;
-      x.w = s.w[h][lane];
-      if (G16) x.g16 = *reinterpret_cast<const uint2*>(&s.g[h][lane]);
-      else x.g32 = s.g[h][lane];
-      x.m = s.m[h][lane];
-      x.v = s.v[h][lane];
-      x.ms = s.scale[0][h];
-      x.vs = s.scale[1][h];
-      step8<G16, false>(c, t, i + h * ADAM_BLOCK, x);
+      x[h].w = s.w[h][lane];
+      if (G16) x[h].g16 = *reinterpret_cast<const uint2*>(&s.g[h][lane]);
+      else x[h].g32 = s.g[h][lane];
+      x[h].m = s.m[h][lane];
+      x[h].v = s.v[h][lane];
+      x[h].ms = s.scale[0][h];
+      x[h].vs = s.scale[1][h];
     }
+    step8<G16, false, 2>(c, t, i, x);
     __syncwarp();  // every lane has used the slot
     fetch(b + RING8 * WARPS, slot);
     slot = (slot + 1) % RING8;
   }
   copy_wait<0>();
-  for (long long i = start + static_cast<long long>(pairs) * PAIR; warp == pairs % WARPS && i < stop; i += ADAM_BLOCK)
-    step8<G16, true>(c, t, i + lane * 4, fetch8<G16>(t, i + lane * 4));
+  for (long long i = start + static_cast<long long>(pairs) * PAIR; warp == pairs % WARPS && i < stop; i += ADAM_BLOCK) {
+    const Block8 x[1] = {fetch8<G16>(t, i + lane * 4)};
+    step8<G16, true, 1>(c, t, i + lane * 4, x);
+  }
 }
 
 __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __grid_constant__ AdamArgs a) {
-  __shared__ Slot8 rings[ADAM_THREADS / 32][RING8];
-  Slot8* const ring = rings[threadIdx.x >> 5];
+  extern __shared__ Slot8 rings[];
+  Slot8* const ring = rings + (threadIdx.x >> 5) * RING8;
   AdamScalars sc;
   int step;
   if (!adam_scalars(a, sc, step)) return;
@@ -544,8 +572,12 @@ static int adam_grid(long long units, int per_sm) {
   return static_cast<int>(units < most ? units : most);
 }
 template <typename A>
-static cudaError_t launch_adam(void (*kern)(A), int grid, const A& a, cudaStream_t s) {
-  kern<<<grid, ADAM_THREADS, 0, s>>>(a);
+static cudaError_t launch_adam(void (*kern)(A), int grid, const A& a, cudaStream_t s, int smem = 0) {
+  if (smem > 0) {
+    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (err != cudaSuccess) return err;
+  }
+  kern<<<grid, ADAM_THREADS, smem, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -617,7 +649,7 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
       a.units += adam_units(t.n, a.chunk);
     }
     if (a.units == 0) continue;
-    const cudaError_t err = eight ? launch_adam(adamw8_kernel, adam_grid(a.units, BLOCKS_8), a, s)
+    const cudaError_t err = eight ? launch_adam(adamw8_kernel, adam_grid(a.units, BLOCKS_8), a, s, RING8_BYTES)
                                   : launch_adam(adamw_kernel, adam_grid(a.units, BLOCKS_32), a, s);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
   }
