@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __
   const uint32_t base = adam_mix(adam_mix(a.seed) + static_cast<uint32_t>(step));
   for (long long unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
     const int at = tensor_of(a, unit);
-    const AdamTensor& t = a.t[at];
+    const AdamTensor t = a.t[at];  // in registers: read from the arguments, 22 more loads a pair
     const long long start = (unit - t.first) * a.chunk;
     const long long stop = min(t.n, start + a.chunk);
     c.decay = 1.0f - sc.lr * t.weight_decay;
