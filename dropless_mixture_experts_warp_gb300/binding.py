@@ -172,9 +172,7 @@ def lib() -> ctypes.CDLL:
 
 
 def _ptr(x) -> Optional[int]:
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or x.__class__ is int:
         return x
     return x.data_ptr()
 

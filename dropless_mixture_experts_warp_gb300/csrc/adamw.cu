@@ -571,13 +571,13 @@ static int adam_grid(long long units, int per_sm) {
   const long long most = static_cast<long long>(num_sms()) * per_sm;
   return static_cast<int>(units < most ? units : most);
 }
-template <typename A>
-static cudaError_t launch_adam(void (*kern)(A), int grid, const A& a, cudaStream_t s, int smem = 0) {
-  if (smem > 0) {
-    const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+template <auto KERN, int SMEM = 0, typename A>
+static cudaError_t launch_adam(int grid, const A& a, cudaStream_t s) {
+  if (SMEM > 0) {
+    const cudaError_t err = allow_smem<KERN>(SMEM);
     if (err != cudaSuccess) return err;
   }
-  kern<<<grid, ADAM_THREADS, smem, s>>>(a);
+  KERN<<<grid, ADAM_THREADS, SMEM, s>>>(a);
   count_launch();
   return cudaGetLastError();
 }
@@ -649,8 +649,8 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
       a.units += adam_units(t.n, a.chunk);
     }
     if (a.units == 0) continue;
-    const cudaError_t err = eight ? launch_adam(adamw8_kernel, adam_grid(a.units, BLOCKS_8), a, s, RING8_BYTES)
-                                  : launch_adam(adamw_kernel, adam_grid(a.units, BLOCKS_32), a, s);
+    const cudaError_t err = eight ? launch_adam<adamw8_kernel, RING8_BYTES>(adam_grid(a.units, BLOCKS_8), a, s)
+                                  : launch_adam<adamw_kernel>(adam_grid(a.units, BLOCKS_32), a, s);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;
@@ -682,8 +682,8 @@ moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int3
     }
     if (a.units == 0) continue;
     const cudaError_t err = out_type == MOE_TYPE_BF16
-                                ? launch_adam(adamw_values_kernel<moe_bf16>, adam_grid(a.units, BLOCKS_VALUES), a, s)
-                                : launch_adam(adamw_values_kernel<float>, adam_grid(a.units, BLOCKS_VALUES), a, s);
+                                ? launch_adam<adamw_values_kernel<moe_bf16>>(adam_grid(a.units, BLOCKS_VALUES), a, s)
+                                : launch_adam<adamw_values_kernel<float>>(adam_grid(a.units, BLOCKS_VALUES), a, s);
     if (err != cudaSuccess) return MOE_ERR_CUDA;
   }
   return MOE_OK;

@@ -2,12 +2,29 @@
 // 8-element vectors in bf16 or fp32 and sums over the threads that share a row.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 
 namespace moe {
 
 void count_launch();
 int num_sms();
+
+// Allows kernel KERN `bytes` of dynamic shared memory, once a device (asked at every call it
+// costs a launch 0.5 us).
+template <auto KERN>
+static cudaError_t allow_smem(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t err = cudaGetDevice(&dev);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  err = cudaFuncSetAttribute(KERN, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_release);
+  return err;
+}
 
 inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }

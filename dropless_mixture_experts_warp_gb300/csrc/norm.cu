@@ -20,7 +20,7 @@ namespace moe {
 constexpr int NORM_MAX_D = 16384;
 constexpr int NORM_SMEM = 225 * 1024;  // dynamic shared memory of a block: of the 227 KB, static buffers aside
 constexpr int NORM_MAX_SMS = 160;      // blocks at most
-constexpr int NORM_FWD_THREADS = 1024;
+constexpr int NORM_FWD_THREADS = 640;  // 96 registers a thread: with 1024 threads and 64, spills cost 12 % (two rows under way)
 constexpr int NORM_BWD_THREADS = 512;  // 128 registers a thread: the column sums of three weights
 
 struct NormArgs {
@@ -247,7 +247,10 @@ __device__ __forceinline__ float sum_pair(f32x2 v) {
   return f.x + f.y;
 }
 
-// MERGE: h_out and, with w_next, its norm; else the norm of h.
+// MERGE: h_out and, with w_next, its norm; else the norm of h.  Two rows are under way in a
+// group: the sum that the next row's first norm needs (of y^2, or of h^2) is added up
+// together with this row's sum of h_out^2, so that a row takes one barrier and its waits are
+// filled with the other row's work.
 template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
 __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
@@ -274,76 +277,93 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
     }
     copy_commit();
   };
-  // one group of copies a row: `stages` of them are open when a row's turn comes
+  // one group of copies a row: `stages` of them are open when a row is waited for
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
   const int gate = !MERGE ? MOE_GATE_NONE : FAST ? GATE : a.gate_kind;
   const bool post = MERGE && (FAST || a.w_post != nullptr), next = FAST || a.w_next != nullptr;
   const bool channel = gate == MOE_GATE_CHANNEL;
-  const f32x2 alpha = pair(a.alpha, a.alpha);
-  int stage = 0;
-  for (long long row = worker; row < a.T; row += workers) {
-    const uint8_t* at = my_ring + stage * plan.row_bytes;
-    const long long base = row * a.d;
-    copy_wait_oldest(plan.stages);
-    f32x2 h[UPT][U / 2];
+
+  // A row's sum of y^2 (MERGE) or h^2, this thread's part.
+  auto first_sum = [&](const uint8_t* at) {
+    f32x2 ss = pair(0.0f, 0.0f);
+    if (MERGE && !post) return 0.0f;
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (FAST || u < units) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
-      else fill<U>(h[i], 0.0f);
+      if (!FAST && u >= units) continue;
+      f32x2 v[U / 2];
+      if (MERGE) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, v);
+      else unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, v);
+#pragma unroll
+      for (int j = 0; j < U / 2; ++j) ss = fma2(v[j], v[j], ss);
     }
-    if (MERGE) {
-      f32x2 y[UPT][U / 2], ss = pair(0.0f, 0.0f);
+    return sum_pair(ss);
+  };
+  int stage = 0;
+  float first = 0.0f;  // the row's first sum, over all its columns
+  if (worker < a.T) {
+    copy_wait_oldest(plan.stages);
+    float s[1] = {first_sum(my_ring)};
+    sums(s);
+    first = s[0];
+  }
+  for (long long row = worker; row < a.T; row += workers) {
+    const uint8_t* at = my_ring + stage * plan.row_bytes;
+    const long long base = row * a.d;
+    const float r1 = inv_rms(first, inv_d, a.eps);
+    float g = MERGE ? a.beta : r1;
+    if (gate == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
+    if (post) g *= r1;
+    const f32x2 g2 = pair(g, g);
+    f32x2 h[UPT][U / 2], ss = pair(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int u = tid + i * tpr;
-        if (FAST || u < units) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y[i]);
-        else fill<U>(y[i], 0.0f);
-#pragma unroll
-        for (int j = 0; j < U / 2; ++j) ss = fma2(y[i][j], y[i][j], ss);
-      }
-      float g = a.beta;
-      if (gate == MOE_GATE_TOKEN) g *= gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
-      if (post) {
-        float s[1] = {sum_pair(ss)};
-        sums(s);
-        g *= inv_rms(s[0], inv_d, a.eps);
-      }
-      const f32x2 g2 = pair(g, g);
-#pragma unroll
-      for (int i = 0; i < UPT; ++i) {
-        const int u = tid + i * tpr;
-        if (!FAST && u >= units) continue;
-        f32x2 w[U / 2];
+    for (int i = 0; i < UPT; ++i) {
+      const int u = tid + i * tpr;
+      if (!FAST && u >= units) continue;
+      f32x2 w[U / 2];
+      unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
+      if (MERGE) {
+        f32x2 y[U / 2];
+        unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y);
         if (post) {
           weights<U, FAST>(a, plan, s_w, W_POST, units, u, w);
 #pragma unroll
-          for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
+          for (int j = 0; j < U / 2; ++j) y[j] = mul2(y[j], w[j]);
         }
         if (channel) {
           weights<U, FAST>(a, plan, s_w, W_GATE, units, u, w);
 #pragma unroll
-          for (int j = 0; j < U / 2; ++j) y[i][j] = mul2(y[i][j], w[j]);
+          for (int j = 0; j < U / 2; ++j) y[j] = mul2(y[j], w[j]);
         }
 #pragma unroll
-        for (int j = 0; j < U / 2; ++j) h[i][j] = fma2(g2, y[i][j], mul2(alpha, h[i][j]));
+        for (int j = 0; j < U / 2; ++j) {
+          const float2 f = unpair(h[i][j]);
+          h[i][j] = fma2(g2, y[j], pair(a.alpha * f.x, a.alpha * f.y));
+          ss = fma2(h[i][j], h[i][j], ss);
+        }
         pack<U>(static_cast<ST*>(a.h_out) + base + u * U, h[i]);
+      } else {
+        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+#pragma unroll
+        for (int j = 0; j < U / 2; ++j) w[j] = mul2(mul2(h[i][j], g2), w[j]);
+        pack<U>(a.x + base + u * U, w);
       }
     }
-    f32x2 ss = pair(0.0f, 0.0f);
-#pragma unroll
-    for (int i = 0; i < UPT; ++i)
-#pragma unroll
-      for (int j = 0; j < U / 2; ++j) ss = fma2(h[i][j], h[i][j], ss);
-    // every value that the ring held was used above: the row's place is free
+    // every value of the row was used above: its place in the ring is free
     fetch(row + static_cast<long long>(plan.stages) * workers, stage);
     stage = stage + 1 == plan.stages ? 0 : stage + 1;
-    if (!next) continue;
-    float s[1] = {sum_pair(ss)};
+    float s[MERGE ? 2 : 1] = {};
+    if (row + workers < a.T) {
+      copy_wait_oldest(plan.stages);
+      s[0] = first_sum(my_ring + stage * plan.row_bytes);
+    }
+    if (MERGE) s[MERGE ? 1 : 0] = sum_pair(ss);
     sums(s);
-    const float r = inv_rms(s[0], inv_d, a.eps);
+    first = s[0];
+    if (!MERGE || !next) continue;
+    const float r = inv_rms(s[MERGE ? 1 : 0], inv_d, a.eps);
     const f32x2 r2 = pair(r, r);
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
@@ -580,37 +600,38 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
   }
 }
 
-// Column sums of the workers' partial sums: 32 threads a column, each adding every 32nd
-// worker in order, then the 32 in order.  blockIdx.y picks the sum; a NULL output is skipped.
-constexpr int REDUCE_GROUPS = 32;
-__global__ void __launch_bounds__(32 * REDUCE_GROUPS) norm_reduce_kernel(const float* __restrict__ part, int workers, int d,
-                                                                         float* __restrict__ o0, float* __restrict__ o1,
-                                                                         float* __restrict__ o2) {
-  __shared__ float4 buf[REDUCE_GROUPS][32];
+// Column sums of the workers' partial sums, 32 columns a block: 32 threads a column, each
+// adding every 32nd worker in order, then the 32 in order.  blockIdx.y picks the sum; a NULL
+// output is skipped.
+constexpr int REDUCE_COLS = 32;
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restrict__ part, int workers, int d,
+                                                          float* __restrict__ o0, float* __restrict__ o1,
+                                                          float* __restrict__ o2) {
+  __shared__ float buf[32][REDUCE_COLS + 1];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   wait_for_previous();
   if (!out) return;
-  const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
-  const int c = (blockIdx.x * 32 + lane) * 4;
+  const int quad = threadIdx.x & 7, grp = threadIdx.x >> 3;
+  const int c = blockIdx.x * REDUCE_COLS + quad * 4;
   float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (c < d) {
 #pragma unroll 8
-    for (int w = grp; w < workers; w += REDUCE_GROUPS) {
+    for (int w = grp; w < workers; w += 32) {
       const float4 p = *reinterpret_cast<const float4*>(part + (static_cast<long long>(w) * 3 + blockIdx.y) * d + c);
       s.x += p.x; s.y += p.y; s.z += p.z; s.w += p.w;
     }
   }
-  buf[grp][lane] = s;
+  float* b = &buf[grp][quad * 4];
+  b[0] = s.x; b[1] = s.y; b[2] = s.z; b[3] = s.w;
   __syncthreads();
-  // thread (grp, lane): column grp of the 32 lanes' 128, by shuffles over the groups
-  const float* cols = reinterpret_cast<const float*>(buf);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int col = grp * 4 + k;
-    float v = cols[lane * 128 + col];
+    const int col = warp * 4 + k;
+    float v = buf[lane][col];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0 && blockIdx.x * 128 + col < d) out[blockIdx.x * 128 + col] = v;
+    if (lane == 0 && blockIdx.x * REDUCE_COLS + col < d) out[blockIdx.x * REDUCE_COLS + col] = v;
   }
 }
 
@@ -658,11 +679,11 @@ static bool norm_fast(const NormPlan& p, const NormArgs& a, bool merge) {
          (!(channel && a.gate_sigmoid) || !a.dh || p.weight[W_SLOPE] >= 0);
 }
 
-template <typename K>
-static cudaError_t launch_rows(K kern, const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_SMEM);
+template <auto KERN>
+static cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  const cudaError_t err = allow_smem<KERN>(NORM_SMEM);
   if (err != cudaSuccess) return err;
-  kern<<<p.grid, p.groups * p.tpr, p.smem_bytes, s>>>(a, p);
+  KERN<<<p.grid, p.groups * p.tpr, p.smem_bytes, s>>>(a, p);
   count_launch();
   return cudaGetLastError();
 }
@@ -675,14 +696,14 @@ static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   const NormPlan p = norm_plan(a.T, a.d, SZ, false, {false, true, false, MERGE},
                                {a.w_next != nullptr, a.w_post != nullptr, channel, false});
   if (norm_fast(p, a, MERGE)) {
-    if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>, a, p, s);
-    if (channel) return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE>, a, p, s);
-    return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE>, a, p, s);
+    if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>>(a, p, s);
+    if (channel) return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE>>(a, p, s);
+    return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE>>(a, p, s);
   }
   switch (norm_cols(a.d)) {
-    case 8: return launch_rows(norm_fwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
-    case 16: return launch_rows(norm_fwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
-    default: return launch_rows(norm_fwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>, a, p, s);
+    case 8: return launch_rows<norm_fwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
+    case 16: return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
+    default: return launch_rows<norm_fwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
   }
 }
 
@@ -690,10 +711,10 @@ template <typename ST, bool MERGE>
 static cudaError_t launch_bwd_fast(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   constexpr int U = 16 / sizeof(ST), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
   constexpr int SL = MERGE ? GATE_SLOPE : MOE_GATE_NONE;
-  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>, a, p, s);
-  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, TK>, a, p, s);
-  if (a.gate_sigmoid) return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, SL>, a, p, s);
-  return launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, true, CH>, a, p, s);
+  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>>(a, p, s);
+  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, TK>>(a, p, s);
+  if (a.gate_sigmoid) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, SL>>(a, p, s);
+  return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, CH>>(a, p, s);
 }
 
 template <typename ST, bool MERGE>
@@ -711,15 +732,15 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
       err = launch_bwd_fast<ST, MERGE>(a, p, s);
     } else {
       switch (norm_cols(a.d)) {
-        case 8: err = launch_rows(norm_bwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
-        case 16: err = launch_rows(norm_bwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
-        default: err = launch_rows(norm_bwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>, a, p, s); break;
+        case 8: err = launch_rows<norm_bwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
+        case 16: err = launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
+        default: err = launch_rows<norm_bwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
       }
     }
     if (err != cudaSuccess) return err;
   }
   if (dw_next || dw_post || dgate_cols) {
-    return launch_early(norm_reduce_kernel, dim3((a.d + 127) / 128, 3), dim3(32 * REDUCE_GROUPS), s,
+    return launch_early(norm_reduce_kernel, dim3((a.d + REDUCE_COLS - 1) / REDUCE_COLS, 3), dim3(256), s,
                         static_cast<const float*>(a.part), workers, a.d, dw_next, dw_post, dgate_cols);
   }
   return cudaSuccess;
