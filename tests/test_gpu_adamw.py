@@ -207,3 +207,57 @@ def test_side_stream():
         torch.cuda.synchronize()
         out.append((w, p.m[0], p.v[0], p.m_scale[0], p.v_scale[0]))
     assert all(torch.equal(a, b) for a, b in zip(*out))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_large_tensors(bits):
+    """Units of several blocks a warp: sampled elements (whole blocks of 128) of 21M against the definition."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    n = 21_000_001
+    g = torch.Generator("cuda").manual_seed(8)
+    r = lambda: torch.randn(n, device="cuda", generator=g)  # noqa: E731
+    w, grad = r(), r().mul_(1e-2).bfloat16()
+    small = torch.randn(77, device="cuda", generator=g)
+    ws, gs = [w, small], [grad, torch.full((77,), 1e-2, device="cuda")]
+    if bits == 32:
+        p = optim.plan(ws, gs, weight_decay=0.1, m=[r().mul_(1e-2), torch.zeros(77, device="cuda")],
+                       v=[r().mul_(1e-2).square_(), torch.zeros(77, device="cuda")])
+    else:
+        blocks = -(-n // 128)
+        p = optim.plan(ws, gs, weight_decay=0.1, bits=8)
+        p.m[0].copy_(torch.randint(-127, 128, (n,), device="cuda", generator=g))
+        p.v[0].copy_(torch.randint(0, 256, (n,), device="cuda", generator=g))
+        p.m_scale[0].copy_(torch.rand(blocks, device="cuda", generator=g) * 1e-2 + 1e-3)
+        p.v_scale[0].copy_(torch.rand(blocks, device="cuda", generator=g) * 1e-4 + 1e-6)
+    pick = np.unique(np.concatenate([np.arange(64), np.random.default_rng(1).integers(0, n // 128, 3000), [n // 128]]))
+    at = np.minimum((pick[:, None] * 128 + np.arange(128)), n - 1)
+    inside = (pick[:, None] * 128 + np.arange(128)) < n
+    take = lambda t: f64(t[torch.from_numpy(at.ravel()).cuda()]).reshape(at.shape) * inside  # noqa: E731
+    rows = lambda t: f64(t[torch.from_numpy(pick).cuda()])  # noqa: E731
+    old_w, g64 = take(w), take(grad)
+    if bits == 32:
+        old_m, old_v = take(p.m[0]), take(p.v[0])
+    else:
+        k, q = take(p.m[0]), take(p.v[0])
+        old_m = rows(p.m_scale[0])[:, None] * np.sign(k) * (k / 127) ** 2
+        old_v = rows(p.v_scale[0])[:, None] * (q / 255) ** 4
+    optim.step(p, step=3, seed=77, **HYPER)
+    exact = bits == 32
+    m1, v1, mm, vm = check_step({"g64": g64}, old_w, old_m, old_v, 0.1, 3, take(w), take(p.m[0]) if exact else None,
+                                take(p.v[0]) if exact else None)
+    if exact:
+        return
+    draws = [oa.adamw_draws(77, 3, 0, n)[i][at.ravel()].reshape(at.shape) for i in (0, 1)]
+    for x, maj, code, scale, u, top, power in ((m1, mm, p.m[0], p.m_scale[0], draws[0], 127, 2),
+                                               (v1, vm, p.v[0], p.v_scale[0], draws[1], 255, 4)):
+        s = (abs(x) * inside).max(axis=1)
+        big = maj.max(axis=1)
+        assert np.all(abs(rows(scale) - s) <= 16 * U * big)
+        want, margin = oa.encode((x * inside).ravel(), s, u.ravel(), top, power)
+        want, margin = want.reshape(at.shape), margin.reshape(at.shape)
+        got = take(code)
+        low = np.maximum(abs(want) - 1, 0)
+        width = ((low + 1) / top) ** power - (low / top) ** power
+        near = margin <= 24 * U * (big / s)[:, None] / width
+        assert np.array_equal(got[~near], want[~near])
+        assert np.all(abs(got - want) <= 1)

@@ -194,3 +194,11 @@ def test_side_stream_and_graph():
         g.replay()
     torch.cuda.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(want, (b.losses, b.counts, b.prob_mean, d)))
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,S,masked", [(14000, 256, 8, 6, True), (6500, 1000, 4, 1, False), (4000, 301, 8, 3, True),
+                                            (90000, 16, 2, 600, True), (12000, 512, 8, 2, False), (25000, 127, 6, 30, True)])
+def test_many_tokens(T, E, k, S, masked, score):
+    """Several tokens a group and several groups a block's part; more sequences than the table in shared memory."""
+    run(*case(T, E, k, S, masked), score, k)

@@ -187,3 +187,38 @@ def test_tensors_that_do_not_fit_are_refused():
         block.norm_forward(b, h, w.bfloat16())
     with pytest.raises(ValueError):
         block.merge_forward(b, h, h, gate=w[:32], w_next=w)
+
+
+# More rows than are under way at once, so that every group takes several: each kernel variant by its width
+# (a warp, part of a block, a block a row; weights in shared memory or not; units that end inside the row)
+LONG = [(5300, 512), (5000, 264), (1300, 1040), (1100, 4096), (950, 7168), (620, 8200), (330, 16384)]
+
+
+@pytest.mark.parametrize("T,d", LONG)
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_many_rows(T, d, stream):
+    from dropless_mixture_experts_warp_gb300 import block
+    i = inputs(T, d, stream, "fp32", 2)
+    (h, h64), (y, y64), (w, w64), (wp, wp64), (dx, dx64), (dh, dh64) = (i[n] for n in ("h", "y", "w", "w_post", "dx", "dh"))
+    b = block.allocate(block.dims_of(T, d, stream=stream))
+    x = oa.norm_fwd(h64, w64, 1e-6)
+    check("x", block.norm_forward(b, h, w), (x, abs(x)), "bf16", ROW)
+    ref = oa.norm_bwd(dx64, h64, w64, 1e-6, 0.0, dh64)
+    block.norm_backward(b, dx, h, w, dh_add=dh)
+    check("dh", b.dh, ref["dh"], stream, ROW)
+    check("dw", b.dw, ref["dw"], "fp32", T + ROW)
+    for gate, act in (("none", "identity"), ("channel", "identity"), ("channel", "sigmoid"), ("token", "sigmoid")):
+        b = block.allocate(block.dims_of(T, d, stream=stream, gate=gate, gate_act=act))
+        opt = dict(eps=1e-6, kind=gate, sigmoid=act == "sigmoid")
+        g, g64 = i[gate]
+        ref = oa.merge_fwd(h64, y64, wp64, g64, w64, **opt)
+        block.merge_forward(b, h, y, w_post=wp, gate=g, w_next=w)
+        check("h_out", b.h_out, ref["h_out"], stream, ROW)
+        check("x", b.x, ref["x"], "bf16", 2 * ROW)
+        ref = oa.merge_bwd(dh64, dx64, h64, y64, wp64, g64, w64, **opt)
+        block.merge_backward(b, dh, dx, h, y, w_post=wp, gate=g, w_next=w)
+        got = {"dh": b.dh, "dy": b.dy, "dw_post": b.dw_post, "dgate": b.dgate, "dw_next": b.dw}
+        terms = {"dh": ROW, "dy": 3 * ROW, "dw_next": T + ROW, "dw_post": T + 2 * ROW,
+                 "dgate": (d if gate == "token" else T) + 3 * ROW}
+        for n in ref:
+            check(f"{gate} {act} {n}", got[n], ref[n], {"dh": stream, "dy": "bf16"}.get(n, "fp32"), terms[n])
