@@ -102,44 +102,65 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return r;
 }
 
-// A lane's logits (or other [T][E] values) of one token; `fill` where the row ends, and
-// everywhere where `there` is false.
+// A lane's logits (or other [T][E] values) of one token, in pairs; `fill` where the row ends,
+// and everywhere where `there` is false.
 template <int VEC, int G, int PLV>
-__device__ __forceinline__ void load_row(const float* row, int E, int gl, bool there, float fill, float (&l)[VEC * PLV]) {
+__device__ __forceinline__ void load_row(const float* row, int E, int gl, bool there, float fill, f32x2 (&l)[VEC * PLV / 2]) {
+  if (VEC == 4) {
 #pragma unroll
-  for (int i = 0; i < PLV; ++i) {
-    const int e = (gl + G * i) * VEC;
-    if (VEC == 4) {
+    for (int i = 0; i < PLV; ++i) {
+      const int e = (gl + G * i) * VEC;
       float4 q = make_float4(fill, fill, fill, fill);
       if (there && e < E) q = *reinterpret_cast<const float4*>(row + e);
-      l[4 * i] = q.x; l[4 * i + 1] = q.y; l[4 * i + 2] = q.z; l[4 * i + 3] = q.w;
-    } else {
-      l[i] = there && e < E ? row[e] : fill;
+      l[VEC / 2 * i] = pair(q.x, q.y);
+      l[VEC / 2 * i + VEC / 4] = pair(q.z, q.w);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < PLV; i += 2) {
+      const int e = gl + G * i;
+      l[i / 2] = pair(there && e < E ? row[e] : fill, there && e + G < E ? row[e + G] : fill);
     }
   }
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+__device__ __forceinline__ float sum_pair(f32x2 v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
+}
+
 // The row's largest logit.
-template <int G, int N>
-__device__ __forceinline__ float row_top(const float (&l)[N]) {
-  float top = l[0];
+template <int G, int M>
+__device__ __forceinline__ float row_top(const f32x2 (&l)[M]) {
+  const float2 f = unpair(l[0]);
+  float top = fmaxf(f.x, f.y);
 #pragma unroll
-  for (int c = 1; c < N; ++c) top = fmaxf(top, l[c]);
+  for (int c = 1; c < M; ++c) {
+    const float2 v = unpair(l[c]);
+    top = max3(top, v.x, v.y);
+  }
   return group_max<G>(top);
 }
 
 // Softmax of the row, not yet divided by its sum, the sum's inverse and the logsumexp; all 0
 // for a row of -inf.  (A NaN reaches the sum through its own exponential.)
-template <int G, int N>
-__device__ __forceinline__ void row_softmax(const float (&l)[N], float top, bool with_lse, float (&p)[N], float& inv, float& lse) {
+template <int G, int M>
+__device__ __forceinline__ void row_softmax(const f32x2 (&l)[M], float top, bool with_lse, f32x2 (&p)[M], float& inv, float& lse) {
   if (top == -INFINITY) top = 0.0f;
-  float sum = 0.0f;
+  f32x2 sums = pair(0.0f, 0.0f);
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
-    p[c] = exp2_fast((l[c] - top) * LOG2E);  // the difference first: logits near fp32's lowest
-    sum += p[c];
+  for (int c = 0; c < M; ++c) {
+    // the difference first: logits near fp32's lowest
+    const float2 x = unpair(mul2(add2(l[c], pair(-top, -top)), pair(LOG2E, LOG2E)));
+    p[c] = pair(exp2_fast(x.x), exp2_fast(x.y));
+    sums = add2(sums, p[c]);
   }
-  sum = group_sum<G>(sum);
+  const float sum = group_sum<G>(sum_pair(sums));
   inv = sum == 0.0f ? 0.0f : rcp_fast(sum);
   lse = with_lse && sum != 0.0f ? top + logf(sum) : 0.0f;
 }
@@ -148,19 +169,24 @@ __device__ __forceinline__ void row_softmax(const float (&l)[N], float top, bool
 // inverse of their sum.  The largest is then at least 1/2, so that a row of far negative
 // logits, whose sigmoids fp32 cannot hold, keeps its shares; the inverse is 0 for a row of
 // -inf.  rest = 1 - sigmoid(l) = e^(c - l) p, without the cancellation of the difference.
-template <int G, int N>
-__device__ __forceinline__ void row_sigmoid(const float (&l)[N], float top, float (&p)[N], float& inv, float (*rest)[N]) {
+template <int G, int M>
+__device__ __forceinline__ void row_sigmoid(const f32x2 (&l)[M], float top, f32x2 (&p)[M], float& inv, f32x2 (*rest)[M]) {
   const float c0 = top == -INFINITY ? 0.0f : fminf(top, 0.0f);
   const float ec = exp2_fast(c0 * LOG2E);
-  float sum = 0.0f;
+  f32x2 sums = pair(0.0f, 0.0f);
 #pragma unroll
-  for (int c = 0; c < N; ++c) {
-    const float e = exp2_fast((c0 - l[c]) * LOG2E);
-    p[c] = rcp_fast(ec + e);
-    sum += p[c];
-    if (rest) (*rest)[c] = fminf(e * p[c], 1.0f);  // inf * 0 where l is far below the top: 1
+  for (int c = 0; c < M; ++c) {
+    const float2 x = unpair(mul2(fma2(l[c], pair(-1.0f, -1.0f), pair(c0, c0)), pair(LOG2E, LOG2E)));
+    const f32x2 e = pair(exp2_fast(x.x), exp2_fast(x.y));
+    const float2 den = unpair(add2(e, pair(ec, ec)));
+    p[c] = pair(rcp_fast(den.x), rcp_fast(den.y));
+    sums = add2(sums, p[c]);
+    if (rest) {
+      const float2 q = unpair(mul2(e, p[c]));
+      (*rest)[c] = pair(fminf(q.x, 1.0f), fminf(q.y, 1.0f));  // inf * 0 where l is far below the top: 1
+    }
   }
-  sum = group_sum<G>(sum);
+  const float sum = group_sum<G>(sum_pair(sums));
   inv = sum == 0.0f ? 0.0f : rcp_fast(sum);
 }
 
@@ -169,7 +195,7 @@ __device__ __forceinline__ void row_sigmoid(const float (&l)[N], float top, floa
 // single block with a single sequence writes the results itself.
 template <int VEC, int G, int PLV, bool SIGMOID>
 __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceArgs a) {
-  constexpr int N = VEC * PLV, GROUPS = BAL_THREADS / G, WARP_COLS = N * G;
+  constexpr int N = VEC * PLV, M = N / 2, GROUPS = BAL_THREADS / G, WARP_COLS = N * G;
   __shared__ float s_p[BAL_THREADS / 32][WARP_COLS];
   __shared__ int s_c[WARP_COLS];
   __shared__ float s_z[BAL_THREADS / 32];
@@ -184,7 +210,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
   auto choice = [&](int t, bool there) { return there && gl < a.k ? a.topk_idx[static_cast<long long>(t) * a.k + gl] : -1; };
   int t = c0 + group, x;
   bool keep = kept(t, c1), keep_next = kept(t + GROUPS, c1);
-  float l[N];
+  f32x2 l[M];
   load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, t < c1, -INFINITY, l);
   x = choice(t, t < c1);
   const Sequences seqs(a, s_off);
@@ -211,17 +237,18 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
     fresh = false;
     if (!keep) {
 #pragma unroll
-      for (int c = 0; c < N; ++c) l[c] = -INFINITY;
+      for (int c = 0; c < M; ++c) l[c] = pair(-INFINITY, -INFINITY);
     }
-    float acc[N], z = 0.0f;
+    f32x2 acc2[M];
+    float z = 0.0f;
     int n = 0;
 #pragma unroll
-    for (int c = 0; c < N; ++c) acc[c] = 0.0f;
+    for (int c = 0; c < M; ++c) acc2[c] = pair(0.0f, 0.0f);
     __syncthreads();
     for (int done = b; done < e; done += GROUPS) {  // a token of every group
       const int tn = t + GROUPS;
       const bool keep_after = kept(tn + GROUPS, e);
-      float next[N];
+      f32x2 next[M];
       load_row<VEC, G, PLV>(a.logits + static_cast<long long>(tn) * a.E, a.E, gl, keep_next, -INFINITY, next);
       const int x_next = choice(tn, keep_next);
       for (int j = gl; keep && j < a.k; j += G) {
@@ -230,21 +257,29 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
         else set_status(a.status, MOE_ERR_INVARIANT);
       }
       __syncwarp();
-      float p[N], inv, lse = 0.0f;
+      f32x2 p[M];
+      float inv, lse = 0.0f;
       const float top = row_top<G>(l);
       if (!SIGMOID || a.z_coef != 0.0f) row_softmax<G>(l, top, a.z_coef != 0.0f, p, inv, lse);
-      if (SIGMOID) row_sigmoid<G>(l, top, p, inv, static_cast<float (*)[N]>(nullptr));
+      if (SIGMOID) row_sigmoid<G>(l, top, p, inv, static_cast<f32x2 (*)[M]>(nullptr));
       z = fmaf(lse, lse, z);
       n += keep;
 #pragma unroll
-      for (int c = 0; c < N; ++c) {
-        acc[c] = fmaf(p[c], inv, acc[c]);
+      for (int c = 0; c < M; ++c) {
+        acc2[c] = fma2(p[c], pair(inv, inv), acc2[c]);
         l[c] = next[c];
       }
       x = x_next;
       t = tn;
       keep = keep_next;
       keep_next = keep_after;
+    }
+    float acc[N];
+#pragma unroll
+    for (int c = 0; c < M; ++c) {
+      const float2 f = unpair(acc2[c]);
+      acc[2 * c] = f.x;
+      acc[2 * c + 1] = f.y;
     }
     // the warp's groups, then the block's warps, in order
 #pragma unroll
@@ -412,7 +447,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
 // [(1 - sigmoid(l_j)) for sigmoid scores] + g1 z_coef 2 / N lse softmax(l)_j.
 template <int VEC, int G, int PLV, bool SIGMOID>
 __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceArgs a) {
-  constexpr int N = VEC * PLV;
+  constexpr int N = VEC * PLV, M = N / 2;
   __shared__ float buf[32 * 2];
   __shared__ int s_off[SEQ_TABLE + 1];
   const int gl = threadIdx.x % G;
@@ -420,7 +455,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceA
   const int t1 = static_cast<int>(min(static_cast<long long>(a.T), t0 + a.run));
   auto kept = [&](long long t) { return t < t1 && (!a.mask || a.mask[t]); };
   // the first token's values are on their way while the totals are added up
-  float l[N], old[N];
+  f32x2 l[M], old[M];
   bool keep = kept(t0), keep_next = a.run > 1 && kept(t0 + 1);
   load_row<VEC, G, PLV>(a.logits + t0 * a.E, a.E, gl, keep, -INFINITY, l);
   load_row<VEC, G, PLV>(a.d_logits + t0 * a.E, a.E, gl, keep && a.accumulate, 0.0f, old);
@@ -436,9 +471,10 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceA
   const float g1 = (a.grad_losses ? a.grad_losses[1] : 1.0f) * a.z_coef * 2.0f / fmaxf(tot[1], 1.0f);
   int s = t0 < a.T ? seqs.of(static_cast<int>(t0)) : 0;
   int end = -1;
-  float f[N], gs = 0.0f;
+  f32x2 f[M];
+  float gs = 0.0f;
 #pragma unroll
-  for (int c = 0; c < N; ++c) f[c] = 0.0f;
+  for (int c = 0; c < M; ++c) f[c] = pair(0.0f, 0.0f);
   for (int step = 0; step < a.run; ++step) {
     const long long t = t0 + step;
     if (t < t1 && t >= end) {  // first token of the run, or of a sequence
@@ -448,64 +484,68 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceA
       const float inv = n > 0 ? 1.0f / static_cast<float>(n) : 0.0f;
       gs = g0 * inv;
       const float fs = inv * static_cast<float>(a.E) / static_cast<float>(a.k);
-#pragma unroll
-      for (int c = 0; c < N; ++c) {
+      const int32_t* counts = a.counts_in + static_cast<long long>(s) * a.E;
+      auto at = [&](int c) {
         const int i = (gl + G * (c / VEC)) * VEC + c % VEC;
-        f[c] = i < a.E ? static_cast<float>(a.counts_in[static_cast<long long>(s) * a.E + i]) * fs : 0.0f;
-      }
+        return i < a.E ? static_cast<float>(counts[i]) * fs : 0.0f;
+      };
+#pragma unroll
+      for (int c = 0; c < M; ++c) f[c] = pair(at(2 * c), at(2 * c + 1));
     }
     __syncwarp();
     const bool keep_after = step + 2 < a.run && kept(t + 2);
-    float l_next[N], old_next[N];
+    f32x2 l_next[M], old_next[M];
     load_row<VEC, G, PLV>(a.logits + (t + 1) * a.E, a.E, gl, keep_next, -INFINITY, l_next);
     load_row<VEC, G, PLV>(a.d_logits + (t + 1) * a.E, a.E, gl, keep_next && a.accumulate, 0.0f, old_next);
     const float top = row_top<G>(l);
-    float p[N], inv, lse, q_inv, d[N];
+    f32x2 p[M], d[M], m2 = pair(0.0f, 0.0f);
+    float inv, lse, q_inv;
     if (!SIGMOID) {
       row_softmax<G>(l, top, a.z_coef != 0.0f, p, inv, lse);
-      float m = 0.0f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) m = fmaf(f[c], p[c], m);
-      m = group_sum<G>(m) * inv;
-      const float gp = gs * inv, gz = g1 * lse * inv;
+      for (int c = 0; c < M; ++c) m2 = fma2(f[c], p[c], m2);
+      const float m = group_sum<G>(sum_pair(m2)) * inv, gp = gs * inv, gz = g1 * lse * inv;
 #pragma unroll
-      for (int c = 0; c < N; ++c) d[c] = p[c] * fmaf(gp, f[c] - m, gz);
+      for (int c = 0; c < M; ++c) d[c] = mul2(p[c], fma2(pair(gp, gp), add2(f[c], pair(-m, -m)), pair(gz, gz)));
     } else {
-      float rest[N];
+      f32x2 rest[M];
       row_sigmoid<G>(l, top, p, inv, &rest);
-      float m = 0.0f;
 #pragma unroll
-      for (int c = 0; c < N; ++c) m = fmaf(f[c], p[c], m);
-      m = group_sum<G>(m) * inv;
-      const float gp = gs * inv;
+      for (int c = 0; c < M; ++c) m2 = fma2(f[c], p[c], m2);
+      const float m = group_sum<G>(sum_pair(m2)) * inv, gp = gs * inv;
 #pragma unroll
-      for (int c = 0; c < N; ++c) d[c] = gp * p[c] * (f[c] - m) * rest[c];
+      for (int c = 0; c < M; ++c) d[c] = mul2(mul2(mul2(p[c], pair(gp, gp)), add2(f[c], pair(-m, -m))), rest[c]);
       if (a.z_coef != 0.0f) {
         row_softmax<G>(l, top, true, p, q_inv, lse);
         const float gz = g1 * lse * q_inv;
 #pragma unroll
-        for (int c = 0; c < N; ++c) d[c] = fmaf(gz, p[c], d[c]);
+        for (int c = 0; c < M; ++c) d[c] = fma2(pair(gz, gz), p[c], d[c]);
       }
     }
     if (t < t1 && (keep || !a.accumulate)) {
       float* out = a.d_logits + t * a.E;
 #pragma unroll
-      for (int i = 0; i < PLV; ++i) {
-        const int e = (gl + G * i) * VEC;
-        if (e >= a.E) continue;
-        if (VEC == 4) {
-          const float4 v = make_float4(old[4 * i] + d[4 * i], old[VEC * i + VEC / 3] + d[VEC * i + VEC / 3],
-                                       old[VEC * i + VEC / 2] + d[VEC * i + VEC / 2], old[VEC * i + VEC - 1] + d[VEC * i + VEC - 1]);
-          *reinterpret_cast<float4*>(out + e) = keep ? v : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        } else {
-          out[e] = keep ? old[i] + d[i] : 0.0f;
+      for (int c = 0; c < M; ++c) d[c] = keep ? add2(old[c], d[c]) : pair(0.0f, 0.0f);
+      if (VEC == 4) {
+#pragma unroll
+        for (int i = 0; i < PLV; ++i) {
+          const int e = (gl + G * i) * VEC;
+          if (e < a.E) *reinterpret_cast<ulonglong2*>(out + e) = make_ulonglong2(d[VEC / 2 * i], d[VEC / 2 * i + VEC / 4]);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < PLV; i += 2) {
+          const int e = gl + G * i;
+          const float2 v = unpair(d[i / 2]);
+          if (e < a.E) out[e] = v.x;
+          if (e + G < a.E) out[e + G] = v.y;
         }
       }
     }
     keep = keep_next;
     keep_next = keep_after;
 #pragma unroll
-    for (int c = 0; c < N; ++c) {
+    for (int c = 0; c < M; ++c) {
       l[c] = l_next[c];
       old[c] = old_next[c];
     }
