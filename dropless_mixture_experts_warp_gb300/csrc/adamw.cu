@@ -56,13 +56,13 @@ __device__ __forceinline__ float byte_at_two23(uint32_t word, int j) {
 }
 // Four codes from one word: m's (two's complement bytes) or v's.
 __device__ __forceinline__ void decode4_m(uint32_t word, float s, f32x2 (&v)[2]) {
+  constexpr float SCALE = 1.0f / 16129.0f;
   word ^= 0x80808080u;
-  const float t = s * (1.0f / 16129.0f);
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const f32x2 c = add2(pair(byte_at_two23(word, 2 * j), byte_at_two23(word, 2 * j + 1)), pair(-TWO23 - 128.0f, -TWO23 - 128.0f));
     const float2 f = unpair(c);
-    v[j] = mul2(pair(f.x * fabsf(f.x), f.y * fabsf(f.y)), pair(t, t));
+    v[j] = mul2(mul2(pair(f.x * fabsf(f.x), f.y * fabsf(f.y)), pair(SCALE, SCALE)), pair(s, s));
   }
 }
 __device__ __forceinline__ void decode4_v(uint32_t word, float s, f32x2 (&v)[2]) {
@@ -109,26 +109,39 @@ __device__ __forceinline__ float absmax3_nan(float a, float b, float c) {
   return d;
 }
 
-// Codes of two shares x of the scale (x = |m| / s, below 1): k = the largest with
-// (k / 127)^2 <= x, in the low byte of t, or k + 1 where e < 0, with the chance that makes the
-// mean x: y = 127^2 x lies between k^2 and k^2 + 2 k + 1, and e = u (2 k + 1) + k^2 - y.  An
-// approximate root that falls on the other side of a k changes nothing: the draw then decides
-// for k in either case.
-__device__ __forceinline__ void encode2_m(f32x2 x, f32x2 root, f32x2 u, float2& t, float2& e) {
+// 1 / s times `top` as a sum of two floats, for products that are exact to some 2^-40.
+struct Inverse {
+  float hi, lo;
+};
+__device__ __forceinline__ Inverse inverse(float s, float r, float top) {  // r = about 1 / s
+  const float hi = top * r;
+  return {hi, fmaf(-hi, s, top) * r};
+}
+
+// Codes of two |m| of a block with the scale s: with y = 127^2 |m| / s, k = the largest with
+// k^2 <= y, in the low byte of t, or k + 1 where e < 0, with the chance that makes the mean
+// right: y lies between k^2 and k^2 + 2 k + 1, and e = u (2 k + 1) + k^2 - y.  An approximate
+// root that falls on the other side of a k changes nothing: the draw then decides for k in
+// either case.  k^2 - y is a difference of near numbers: y comes as |m| (hi + lo), whose
+// rounding against k^2 is less than a 2^-24th of the codes' distance; with y rounded once a
+// code in 10^5 was another.
+__device__ __forceinline__ void encode2_m(f32x2 m, f32x2 root, Inverse inv, f32x2 u, float2& t, float2& e) {
   const f32x2 t2 = fma2_down(root, pair(127.0f, 127.0f), pair(TWO23, TWO23));
   const f32x2 k = add2(t2, pair(-TWO23, -TWO23));
-  const f32x2 d = fma2(k, k, mul2(x, pair(-16129.0f, -16129.0f)));
+  const f32x2 d = fma2(m, pair(-inv.lo, -inv.lo), fma2(m, pair(-inv.hi, -inv.hi), mul2(k, k)));
   const f32x2 n = fma2(k, pair(0x1p-15f, 0x1p-15f), pair(0x1p-16f, 0x1p-16f));  // u comes times 2^16
   t = unpair(t2);
   e = unpair(fma2(u, n, d));
 }
-// The same for x = v / s and fourth powers, k^4 .. (k + 1)^4 = k^4 + (2 k + 1) ((k + 1)^2 + k^2);
-// 255 x^(1/4) = root * scale, from a root that the step has already.
-__device__ __forceinline__ void encode2_v(f32x2 x, f32x2 root, float scale, f32x2 u, float2& t, float2& e) {
+// The same for v, y = 255^4 v / s and fourth powers, k^4 .. (k + 1)^4 = k^4 + (2 k + 1) ((k + 1)^2
+// + k^2); y^(1/4) = root * scale, from a root that the step has already.  k^4 takes 32 bits, so
+// the product v hi is split into its rounding and the rest.
+__device__ __forceinline__ void encode2_v(f32x2 v, f32x2 root, float scale, Inverse inv, f32x2 u, float2& t, float2& e) {
   const f32x2 t2 = fma2_down(root, pair(scale, scale), pair(TWO23, TWO23));
   const f32x2 k = add2(t2, pair(-TWO23, -TWO23)), k1 = add2(k, pair(1.0f, 1.0f));
-  const f32x2 k2 = mul2(k, k);
-  const f32x2 d = fma2(k2, k2, mul2(x, pair(-4228250625.0f, -4228250625.0f)));
+  const f32x2 k2 = mul2(k, k), ny = mul2(v, pair(-inv.hi, -inv.hi));
+  const f32x2 rest = fma2(v, pair(inv.lo, inv.lo), fma2(v, pair(inv.hi, inv.hi), ny));
+  const f32x2 d = fma2(rest, pair(-1.0f, -1.0f), fma2(k2, k2, ny));
   const f32x2 n = mul2(fma2(k, pair(0x1p-15f, 0x1p-15f), pair(0x1p-16f, 0x1p-16f)), fma2(k1, k1, k2));
   t = unpair(t2);
   e = unpair(fma2(u, n, d));
@@ -277,7 +290,7 @@ __device__ __forceinline__ Block8 fetch8(const AdamTensor& t, long long i) {
 
 // What is the same for a unit's elements.
 struct Unit8 {
-  float c1, c2, b1, b2;        // m = b1 m + c1 g, v = b2 v + (c2 g)^2
+  float gs, b1, b2, c1, c2;    // m = b1 m + c1 g, v = b2 v + c2 g^2
   float root_bc2, eps, rate, decay;
   uint32_t key;
 };
@@ -301,14 +314,15 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
       g[0] = pair(x[h].g32.x, x[h].g32.y);
       g[1] = pair(x[h].g32.z, x[h].g32.w);
     }
-    decode4_m(x[h].m, x[h].ms * c.b1, m[h]);
-    decode4_v(x[h].v, x[h].vs * c.b2, v[h]);
+    decode4_m(x[h].m, x[h].ms, m[h]);
+    decode4_v(x[h].v, x[h].vs, v[h]);
     float2 am[2], av[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      m[h][j] = fma2(g[j], pair(c.c1, c.c1), m[h][j]);
-      const f32x2 q = mul2(g[j], pair(c.c2, c.c2));
-      v[h][j] = fma2(q, q, v[h][j]);
+      // each operation rounded: the codes then do not depend on how a compiler joins them
+      g[j] = mul2(g[j], pair(c.gs, c.gs));
+      m[h][j] = add2(mul2(m[h][j], pair(c.b1, c.b1)), mul2(g[j], pair(c.c1, c.c1)));
+      v[h][j] = add2(mul2(v[h][j], pair(c.b2, c.b2)), mul2(mul2(g[j], g[j]), pair(c.c2, c.c2)));
       am[j] = unpair(m[h][j]);
       av[j] = unpair(v[h][j]);
       const float2 r = make_float2(sqrt_fast(av[j].x), sqrt_fast(av[j].y));
@@ -332,10 +346,24 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
   for (int h = 0; h < H; ++h) {
     if (ms[h] < 1.17549435e-38f) ms[h] = 0.0f;
     if (vs[h] < 1.17549435e-38f) vs[h] = 0.0f;
-    // Inverses a little below (rcp is within 2^-23): shares stay under 1, the codes within a
-    // byte without a clamp, and the largest value still draws its own code but for 2^-15 or so.
-    const float im = ms[h] > 0.0f ? rcp_fast(ms[h]) * (1.0f - 0x1p-22f) : 0.0f;
-    const float iv = vs[h] > 0.0f ? rcp_fast(vs[h]) * (1.0f - 0x1p-22f) : 0.0f;
+    // what the codes are made of; scales whose inverses would leave fp32's range, and their
+    // moments, times 2^60
+    float sm = ms[h], sv = vs[h];
+    if (fminf(sm, sv) < 0x1p-60f) {
+      const float fm = sm < 0x1p-60f ? 0x1p60f : 1.0f, fv = sv < 0x1p-60f ? 0x1p60f : 1.0f;
+      sm *= fm;
+      sv *= fv;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        m[h][j] = mul2(m[h][j], pair(fm, fm));
+        v[h][j] = mul2(v[h][j], pair(fv, fv));
+        const float2 f = unpair(v[h][j]);
+        root[h][j] = pair(sqrt_fast(sqrt_fast(f.x)), sqrt_fast(sqrt_fast(f.y)));
+      }
+    }
+    const float im = sm > 0.0f ? rcp_fast(sm) : 0.0f, iv = sv > 0.0f ? rcp_fast(sv) : 0.0f;
+    const Inverse em2 = sm > 0.0f ? inverse(sm, im, 16129.0f) : Inverse{0.0f, 0.0f};
+    const Inverse ev4 = sv > 0.0f ? inverse(sv, iv, 4228250625.0f) : Inverse{0.0f, 0.0f};
     const float rs = 255.0f * sqrt_fast(sqrt_fast(iv));  // 255 (v / s)^(1/4) = root * rs
     float2 am[2], tm[2], em[2], tv[2], ev[2];
 #pragma unroll
@@ -343,9 +371,10 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
       const uint32_t at = static_cast<uint32_t>(i) + h * ADAM_BLOCK + 2 * j;
       const uint32_t h0 = adam_mix(at * 0x9E3779B9u + c.key), h1 = adam_mix((at + 1) * 0x9E3779B9u + c.key);
       am[j] = unpair(m[h][j]);
-      const float2 sm = make_float2(fabsf(am[j].x) * im, fabsf(am[j].y) * im);
-      encode2_m(pair(sm.x, sm.y), pair(sqrt_fast(sm.x), sqrt_fast(sm.y)), draws(h0, h1, false), tm[j], em[j]);
-      encode2_v(mul2(v[h][j], pair(iv, iv)), root[h][j], rs, draws(h0, h1, true), tv[j], ev[j]);
+      const float2 ab = make_float2(fabsf(am[j].x), fabsf(am[j].y));
+      const f32x2 root_m = pair(sqrt_fast(ab.x * im), sqrt_fast(ab.y * im));
+      encode2_m(pair(ab.x, ab.y), root_m, em2, draws(h0, h1, false), tm[j], em[j]);
+      encode2_v(v[h][j], root[h][j], rs, ev4, draws(h0, h1, true), tv[j], ev[j]);
     }
     // four codes at a time as bytes: k or k + 1 (at most 127 and 255), then m's sign, whose
     // two's complement is added without a carry between bytes
@@ -469,8 +498,9 @@ __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __
   int step;
   if (!adam_scalars(a, sc, step)) return;
   Unit8 c;
-  c.c1 = a.keep1 * sc.gs;
-  c.c2 = sqrtf(a.keep2) * sc.gs;
+  c.gs = sc.gs;
+  c.c1 = a.keep1;
+  c.c2 = a.keep2;
   c.b1 = a.beta1;
   c.b2 = a.beta2;
   c.root_bc2 = sqrtf(sc.inv_bc2);

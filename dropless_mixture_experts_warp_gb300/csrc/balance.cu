@@ -350,7 +350,6 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   __shared__ float buf4[32 * 4];
   __shared__ int s_last;
   const int s = blockIdx.y;
-  wait_for_previous();
   const int b = a.seq_offsets ? min(max(a.seq_offsets[s], 0), a.T) : 0;
   const int e = a.seq_offsets ? min(max(a.seq_offsets[s + 1], 0), a.T) : a.T;
   if (threadIdx.x == 0 && blockIdx.x == 0 && a.seq_offsets) {
@@ -362,6 +361,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
     first = b / a.chunk + s;
     last = (e - 1) / a.chunk + s;
   }
+  wait_for_previous();
   // n in two parts, whose sums over at most 320 chunks fp32 holds exactly
   float nz[3] = {0.0f, 0.0f, 0.0f};
   for (int i = first + static_cast<int>(threadIdx.x); i <= last; i += 256) {

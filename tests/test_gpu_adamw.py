@@ -261,3 +261,28 @@ def test_large_tensors(bits):
         near = margin <= 24 * U * (big / s)[:, None] / width
         assert np.array_equal(got[~near], want[~near])
         assert np.all(abs(got - want) <= 1)
+
+
+@pytest.mark.parametrize("scale", [1e-17, 1e-10, 1e15])
+def test_8_bit_at_far_scales(scale):
+    """Codes follow the definition where the inverse of a scale, or a share's product, would leave fp32's range."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    n = 4096
+    rng = np.random.default_rng(12)
+    w, g = torch.zeros(n, device="cuda"), cuda(rng.standard_normal(n) * scale * 10.0 ** rng.uniform(-3, 0, n))
+    p = optim.plan([w], [g], bits=8)
+    optim.step(p, step=1, seed=4, **HYPER)
+    g64 = f64(g)
+    m1, v1 = (1 - HYPER["beta1"]) * g64, (1 - HYPER["beta2"]) * g64 ** 2
+    for x, code, scales, u, top, power in ((m1, p.m[0], p.m_scale[0], 0, 127, 2), (v1, p.v[0], p.v_scale[0], 1, 255, 4)):
+        ref = oa.block_scales(x)
+        assert np.all(abs(f64(scales) - ref) <= 8 * U * ref)
+        want, margin = oa.encode(x, ref, oa.adamw_draws(4, 1, 0, n)[u], top, power)
+        got = code.cpu().numpy().astype(np.int64)
+        low = np.maximum(abs(want) - 1, 0)
+        # the roundings are relative to the value; a v below fp32's normal numbers is rounded to 2^-149, or to 0
+        largest = np.repeat(ref, 128)
+        width = ((low + 1) / top) ** power - (low / top) ** power
+        near = (margin <= (24 * U * abs(x) + 2.0 ** -149) / largest / width) | ((x != 0) & (abs(x) < 2.0 ** -149))
+        assert np.array_equal(got[~near], want[~near]) and np.all(abs(got - want) <= 1)
+        assert near.mean() < 0.2
