@@ -31,6 +31,7 @@ struct AdamArgs {
   int base;         // number of tensors[0] in the caller's list
   long long units;
   float lr, beta1, beta2, keep1, keep2, eps;  // keep = 1 - beta
+  float one;                                  // 1
   float inv_bc1, inv_bc2;                     // 1 / (1 - beta^t)
   float log_beta1, log_beta2;
   uint32_t seed;
@@ -291,7 +292,7 @@ __device__ __forceinline__ Block8 fetch8(const AdamTensor& t, long long i) {
 // What is the same for a unit's elements.
 struct Unit8 {
   float gs, b1, b2, c1, c2;    // m = b1 m + c1 g, v = b2 v + c2 g^2
-  float root_bc2, eps, rate, decay;
+  float one, root_bc2, eps, rate, decay;
   uint32_t key;
 };
 
@@ -319,10 +320,13 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
     float2 am[2], av[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      // each operation rounded: the codes then do not depend on how a compiler joins them
+      // Each operation rounded: the codes then do not depend on how a compiler joins them.  (A
+      // packed product and sum are joined for all their .rn; a product by 1 is not, where 1 is
+      // an argument.)
+      const f32x2 one = pair(c.one, c.one);
       g[j] = mul2(g[j], pair(c.gs, c.gs));
-      m[h][j] = add2(mul2(m[h][j], pair(c.b1, c.b1)), mul2(g[j], pair(c.c1, c.c1)));
-      v[h][j] = add2(mul2(v[h][j], pair(c.b2, c.b2)), mul2(mul2(g[j], g[j]), pair(c.c2, c.c2)));
+      m[h][j] = fma2(mul2(m[h][j], pair(c.b1, c.b1)), one, mul2(g[j], pair(c.c1, c.c1)));
+      v[h][j] = fma2(mul2(v[h][j], pair(c.b2, c.b2)), one, mul2(mul2(g[j], g[j]), pair(c.c2, c.c2)));
       am[j] = unpair(m[h][j]);
       av[j] = unpair(v[h][j]);
       const float2 r = make_float2(sqrt_fast(av[j].x), sqrt_fast(av[j].y));
@@ -498,6 +502,7 @@ __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __
   int step;
   if (!adam_scalars(a, sc, step)) return;
   Unit8 c;
+  c.one = a.one;
   c.gs = sc.gs;
   c.c1 = a.keep1;
   c.c2 = a.keep2;
@@ -654,6 +659,7 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
   a.keep1 = static_cast<float>(1.0 - h.beta1);
   a.keep2 = static_cast<float>(1.0 - h.beta2);
   a.eps = static_cast<float>(h.eps);
+  a.one = 1.0f;
   a.log_beta1 = static_cast<float>(std::log(h.beta1));
   a.log_beta2 = static_cast<float>(std::log(h.beta2));
   if (!control) {
