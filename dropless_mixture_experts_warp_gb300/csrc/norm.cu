@@ -11,8 +11,10 @@
 // is computed.  The weights are shared by the block's rows: as fp32, offsets added and
 // gates activated, in shared memory where that has room beside two rows a group.
 //
-// FAST variants know at compile time what a call usually has: every weight present and in
-// shared memory, every unit inside the row, the kind of gate GATE.
+// KNOWN variants know at compile time what a call usually has: every weight, the gradient of
+// the stream, the kind of gate GATE (one choice after the other at run time: 355 us instead
+// of 449 for the gradients of a 16384 x 7168 merge when they came); EXACT ones also that the
+// weights are in shared memory and the row's units fill the threads.
 #include "around.cuh"
 
 namespace moe {
@@ -54,6 +56,7 @@ struct NormPlan {
   int weight[W_ARRAYS];   // each weight's place, in floats (-1: read from global memory)
   int row_bytes, weight_bytes, stages;
   int smem_bytes;
+  bool join;              // backward: the groups' column sums are added in the block
   int y_bytes;            // backward: y has a ring of its own, of stages + 1 rows
 };
 
@@ -251,7 +254,7 @@ __device__ __forceinline__ float sum_pair(f32x2 v) {
 // group: the sum that the next row's first norm needs (of y^2, or of h^2) is added up
 // together with this row's sum of h_out^2, so that a row takes one barrier and its waits are
 // filled with the other row's work.
-template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
+template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE>
 __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * SUMS_MAX * 32];
@@ -269,7 +272,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (!FAST && u >= units) continue;
+        if (!EXACT && u >= units) continue;
         const long long at = row * a.d + u * U;
         copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
         if (MERGE) copy_async<U * 2>(dst + plan.off[RING_Y] + u * U * 2, a.y + at);
@@ -281,8 +284,8 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
-  const int gate = !MERGE ? MOE_GATE_NONE : FAST ? GATE : a.gate_kind;
-  const bool post = MERGE && (FAST || a.w_post != nullptr), next = FAST || a.w_next != nullptr;
+  const int gate = !MERGE ? MOE_GATE_NONE : KNOWN ? GATE : a.gate_kind;
+  const bool post = MERGE && (KNOWN || a.w_post != nullptr), next = KNOWN || a.w_next != nullptr;
   const bool channel = gate == MOE_GATE_CHANNEL;
 
   // A row's sum of y^2 (MERGE) or h^2, this thread's part.
@@ -292,7 +295,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (!FAST && u >= units) continue;
+      if (!EXACT && u >= units) continue;
       f32x2 v[U / 2];
       if (MERGE) unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, v);
       else unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, v);
@@ -321,19 +324,19 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (!FAST && u >= units) continue;
+      if (!EXACT && u >= units) continue;
       f32x2 w[U / 2];
       unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h[i]);
       if (MERGE) {
         f32x2 y[U / 2];
         unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_Y]) + u * U, y);
         if (post) {
-          weights<U, FAST>(a, plan, s_w, W_POST, units, u, w);
+          weights<U, EXACT>(a, plan, s_w, W_POST, units, u, w);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) y[j] = mul2(y[j], w[j]);
         }
         if (channel) {
-          weights<U, FAST>(a, plan, s_w, W_GATE, units, u, w);
+          weights<U, EXACT>(a, plan, s_w, W_GATE, units, u, w);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) y[j] = mul2(y[j], w[j]);
         }
@@ -345,7 +348,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
         }
         pack<U>(static_cast<ST*>(a.h_out) + base + u * U, h[i]);
       } else {
-        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+        weights<U, EXACT>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) w[j] = mul2(mul2(h[i][j], g2), w[j]);
         pack<U>(a.x + base + u * U, w);
@@ -368,9 +371,9 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (!FAST && u >= units) continue;
+      if (!EXACT && u >= units) continue;
       f32x2 w[U / 2];
-      weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+      weights<U, EXACT>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
       for (int j = 0; j < U / 2; ++j) w[j] = mul2(mul2(h[i][j], r2), w[j]);
       pack<U>(a.x + base + u * U, w);
@@ -387,7 +390,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 // waits are filled with the other row's work (355 us with two barriers a row, for 16384 x
 // 7168 bf16 with everything).  So y has one place more in the ring than the other arrays.
 // What a call lacks (weights, gate) takes its neutral value, a unit at a time.
-template <typename ST, int UPT, bool MERGE, bool FAST, int GATE>
+template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE>
 __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * SUMS_MAX * 32];
@@ -406,12 +409,12 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (!FAST && u >= units) continue;
+        if (!EXACT && u >= units) continue;
         const long long at = row * a.d + u * U;
-        if (FAST || plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
-        if (FAST || plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
-        if (FAST || plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
-        if (MERGE && (FAST || plan.y_bytes > 0)) copy_async<U * 2>(dst_y + u * U * 2, a.y + at);
+        if (KNOWN || plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
+        if (KNOWN || plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
+        if (KNOWN || plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
+        if (MERGE && (KNOWN || plan.y_bytes > 0)) copy_async<U * 2>(dst_y + u * U * 2, a.y + at);
       }
     }
     copy_commit();
@@ -420,10 +423,10 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
-  const bool next = FAST || a.w_next != nullptr, post = MERGE && (FAST || a.w_post != nullptr);
-  const int gate = !MERGE ? MOE_GATE_NONE : !FAST ? a.gate_kind : GATE == GATE_SLOPE ? MOE_GATE_CHANNEL : GATE;
+  const bool next = KNOWN || a.w_next != nullptr, post = MERGE && (KNOWN || a.w_post != nullptr);
+  const int gate = !MERGE ? MOE_GATE_NONE : !KNOWN ? a.gate_kind : GATE == GATE_SLOPE ? MOE_GATE_CHANNEL : GATE;
   const bool channel = gate == MOE_GATE_CHANNEL, token = gate == MOE_GATE_TOKEN;
-  const bool slope = FAST ? GATE == GATE_SLOPE : channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
+  const bool slope = KNOWN ? GATE == GATE_SLOPE : channel && a.gate_sigmoid, has_y = post || gate != MOE_GATE_NONE;
   const f32x2 zero = pair(0.0f, 0.0f);
 
   // A row's sums of h^2, n h and y^2.
@@ -432,12 +435,12 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
     for (int i = 0; i < UPT; ++i) {
       const int u = tid + i * tpr;
-      if (!FAST && u >= units) continue;
+      if (!EXACT && u >= units) continue;
       if (next) {
         f32x2 h[U / 2], n[U / 2], w[U / 2];
         unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h);
         unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]) + u * U, n);
-        weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+        weights<U, EXACT>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
         for (int j = 0; j < U / 2; ++j) {
           shh = fma2(h[j], h[j], shh);
@@ -494,15 +497,15 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (!FAST && u >= units) continue;
+        if (!EXACT && u >= units) continue;
         f32x2 D[U / 2];
-        if (FAST || a.d_stream) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_D]) + u * U, D);
+        if (KNOWN || a.d_stream) unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_D]) + u * U, D);
         else fill<U>(D, 0.0f);
         if (next) {
           f32x2 h[U / 2], n[U / 2], w[U / 2];
           unpack<U>(reinterpret_cast<const ST*>(at + plan.off[RING_H]) + u * U, h);
           unpack<U>(reinterpret_cast<const moe_bf16*>(at + plan.off[RING_DX]) + u * U, n);
-          weights<U, FAST>(a, plan, s_w, W_NEXT, units, u, w);
+          weights<U, EXACT>(a, plan, s_w, W_NEXT, units, u, w);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) {
             dw_next[i][j] = fma2(n[j], mul2(h[j], r2), dw_next[i][j]);
@@ -520,15 +523,15 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
           f32x2 y[U / 2], wp[U / 2], wg[U / 2], ds[U / 2];
           if (has_y) unpack<U>(r_y + u * U, y);
           else fill<U>(y, 0.0f);
-          if (post) weights<U, FAST>(a, plan, s_w, W_POST, units, u, wp);
+          if (post) weights<U, EXACT>(a, plan, s_w, W_POST, units, u, wp);
           else fill<U>(wp, 1.0f);
-          if (channel) weights<U, FAST>(a, plan, s_w, W_GATE, units, u, wg);
+          if (channel) weights<U, EXACT>(a, plan, s_w, W_GATE, units, u, wg);
           else fill<U>(wg, 1.0f);
 #pragma unroll
           for (int j = 0; j < U / 2; ++j) q[i][j] = ds[j] = mul2(tg2, D[j]);
           if (slope) {
             f32x2 sl[U / 2];
-            weights<U, FAST>(a, plan, s_w, W_SLOPE, units, u, sl);
+            weights<U, EXACT>(a, plan, s_w, W_SLOPE, units, u, sl);
 #pragma unroll
             for (int j = 0; j < U / 2; ++j) ds[j] = mul2(ds[j], sl[j]);
           }
@@ -536,7 +539,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
           for (int j = 0; j < U / 2; ++j) {
             const f32x2 yh = mul2(y[j], ry2), z = mul2(yh, wp[j]);
             dgate[i][j] = fma2(ds[j], z, dgate[i][j]);
-            if (!FAST || token) sdz = fma2(D[j], z, sdz);
+            if (!KNOWN || token) sdz = fma2(D[j], z, sdz);
             const f32x2 dz = mul2(q[i][j], wg[j]);
             dw_post[i][j] = fma2(dz, yh, dw_post[i][j]);
             q[i][j] = mul2(dz, wp[j]);
@@ -551,7 +554,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
     fetch(row + static_cast<long long>(plan.stages) * workers, stage, y_after);
     stage = stage + 1 == plan.stages ? 0 : stage + 1;
     y_stage = y_stage == plan.stages ? 0 : y_stage + 1;
-    float s[!MERGE ? 2 : FAST && GATE != MOE_GATE_TOKEN ? 4 : 5] = {};
+    float s[!MERGE ? 2 : KNOWN && GATE != MOE_GATE_TOKEN ? 4 : 5] = {};
     if (row + workers < a.T) {
       copy_wait_oldest(plan.stages);
       float y2;
@@ -560,7 +563,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
     }
     if (MERGE) {
       s[MERGE ? 3 : 0] = sum_pair(sqy);
-      if (!FAST || token) s[sizeof(s) / 4 - 1] = sum_pair(sdz);
+      if (!KNOWN || token) s[sizeof(s) / 4 - 1] = sum_pair(sdz);
     }
     sums(s);
     hh = s[0];
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
         for (int i = 0; i < UPT; ++i) {
           const int u = tid + i * tpr;
-          if (!FAST && u >= units) continue;
+          if (!EXACT && u >= units) continue;
           f32x2 y[U / 2];
           unpack<U>(r_y + u * U, y);
 #pragma unroll
@@ -585,15 +588,52 @@ __global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormAr
 #pragma unroll
       for (int i = 0; i < UPT; ++i) {
         const int u = tid + i * tpr;
-        if (FAST || u < units) pack<U>(a.dy + base + u * U, q[i]);
+        if (EXACT || u < units) pack<U>(a.dy + base + u * U, q[i]);
       }
     }
+  }
+  // the groups' column sums, added in order through the rings' room where that suffices
+  const bool wanted[3] = {next, post, channel};
+  if (plan.join) {
+    copy_wait<0>();
+    __syncthreads();
+    float* room = reinterpret_cast<float*>(smem + plan.weight_bytes);
+    const int stride = plan.groups * a.d;
+    int k = 0;
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+      if (!wanted[which]) continue;
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (!EXACT && u >= units) continue;
+        pack<U>(room + k * stride + group * a.d + u * U, which == 0 ? dw_next[i] : which == 1 ? dw_post[i] : dgate[i]);
+      }
+      ++k;
+    }
+    __syncthreads();
+    k = 0;
+#pragma unroll
+    for (int which = 0; which < 3; ++which) {
+      if (!wanted[which]) continue;
+      float* part = a.part + (static_cast<long long>(blockIdx.x) * 3 + which) * a.d;
+      for (int c = threadIdx.x * 4; c < a.d; c += blockDim.x * 4) {
+        float4 v = *reinterpret_cast<const float4*>(room + k * stride + c);
+        for (int g = 1; g < plan.groups; ++g) {
+          const float4 p = *reinterpret_cast<const float4*>(room + k * stride + g * a.d + c);
+          v.x += p.x; v.y += p.y; v.z += p.z; v.w += p.w;
+        }
+        *reinterpret_cast<float4*>(part + c) = v;
+      }
+      ++k;
+    }
+    return;
   }
   float* part = a.part + static_cast<long long>(worker) * 3 * a.d;
 #pragma unroll
   for (int i = 0; i < UPT; ++i) {
     const int u = tid + i * tpr;
-    if (!FAST && u >= units) continue;
+    if (!EXACT && u >= units) continue;
     if (next) pack<U>(part + u * U, dw_next[i]);
     if (post) pack<U>(part + a.d + u * U, dw_post[i]);
     if (channel) pack<U>(part + 2 * a.d + u * U, dgate[i]);
@@ -648,6 +688,10 @@ static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&
   p.tpr = ((d + norm_cols(d) - 1) / norm_cols(d) + 31) / 32 * 32;
   p.groups = (bwd ? NORM_BWD_THREADS : NORM_FWD_THREADS) / p.tpr;
   if (p.tpr > 32 && p.groups > 15) p.groups = 15;  // named barriers 1 .. 15
+  const int sms = num_sms() < NORM_MAX_SMS ? num_sms() : NORM_MAX_SMS;
+  p.grid = T < sms ? T : sms;
+  const int each = (T + p.grid - 1) / p.grid;  // rows of a block
+  if (p.groups > each) p.groups = each;
   const int size[RING_ARRAYS] = {stream_size, stream_size, 2, 2};
   for (int i = 0; i < RING_ARRAYS; ++i) {
     const bool apart = bwd && i == RING_Y;
@@ -666,14 +710,14 @@ static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&
   }
   while (p.stages > 1 && p.stages < 4 && ring(p.stages + 1) + p.weight_bytes <= NORM_SMEM) ++p.stages;
   p.smem_bytes = ring(p.stages) + p.weight_bytes;
-  const int sms = num_sms() < NORM_MAX_SMS ? num_sms() : NORM_MAX_SMS;
-  p.grid = T < sms ? T : sms;
+  p.join = bwd && p.groups > 1 && p.groups * (w[W_NEXT] + w[W_POST] + w[W_GATE]) * d * 4 <= ring(p.stages);
   return p;
 }
 
-// Whether the FAST variants take the call (see the top of the file).
-static bool norm_fast(const NormPlan& p, const NormArgs& a, bool merge) {
-  if (norm_cols(a.d) != 16 || a.d != p.tpr * 16 || !a.w_next || (merge && !a.w_post)) return false;
+// Whether the KNOWN and the EXACT variants take the call (see the top of the file).
+static bool norm_known(const NormArgs& a, bool merge) { return norm_cols(a.d) == 16 && a.w_next && (!merge || a.w_post); }
+static bool norm_exact(const NormPlan& p, const NormArgs& a, bool merge) {
+  if (a.d != p.tpr * 16) return false;
   const bool channel = merge && a.gate_kind == MOE_GATE_CHANNEL;
   return p.weight[W_NEXT] >= 0 && (!merge || p.weight[W_POST] >= 0) && (!channel || p.weight[W_GATE] >= 0) &&
          (!(channel && a.gate_sigmoid) || !a.dh || p.weight[W_SLOPE] >= 0);
@@ -688,6 +732,14 @@ static cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_
   return cudaGetLastError();
 }
 
+template <typename ST, bool MERGE, bool EXACT>
+static cudaError_t launch_fwd_known(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  constexpr int N = 16 / (16 / sizeof(ST)), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
+  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE>>(a, p, s);
+  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, TK>>(a, p, s);
+  return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, CH>>(a, p, s);
+}
+
 template <typename ST, bool MERGE>
 static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
@@ -695,26 +747,23 @@ static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
   const NormPlan p = norm_plan(a.T, a.d, SZ, false, {false, true, false, MERGE},
                                {a.w_next != nullptr, a.w_post != nullptr, channel, false});
-  if (norm_fast(p, a, MERGE)) {
-    if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>>(a, p, s);
-    if (channel) return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE>>(a, p, s);
-    return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, true, MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE>>(a, p, s);
-  }
+  if (norm_known(a, MERGE))
+    return norm_exact(p, a, MERGE) ? launch_fwd_known<ST, MERGE, true>(a, p, s) : launch_fwd_known<ST, MERGE, false>(a, p, s);
   switch (norm_cols(a.d)) {
-    case 8: return launch_rows<norm_fwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
-    case 16: return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
-    default: return launch_rows<norm_fwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s);
+    case 8: return launch_rows<norm_fwd_kernel<ST, 8 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
+    case 16: return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
+    default: return launch_rows<norm_fwd_kernel<ST, 32 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
   }
 }
 
-template <typename ST, bool MERGE>
-static cudaError_t launch_bwd_fast(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-  constexpr int U = 16 / sizeof(ST), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
+template <typename ST, bool MERGE, bool EXACT>
+static cudaError_t launch_bwd_known(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  constexpr int N = 16 / (16 / sizeof(ST)), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
   constexpr int SL = MERGE ? GATE_SLOPE : MOE_GATE_NONE;
-  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, MOE_GATE_NONE>>(a, p, s);
-  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, TK>>(a, p, s);
-  if (a.gate_sigmoid) return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, SL>>(a, p, s);
-  return launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, true, CH>>(a, p, s);
+  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE>>(a, p, s);
+  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, TK>>(a, p, s);
+  if (a.gate_sigmoid) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, SL>>(a, p, s);
+  return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, CH>>(a, p, s);
 }
 
 template <typename ST, bool MERGE>
@@ -726,15 +775,15 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
     const NormPlan p = norm_plan(a.T, a.d, SZ, true,
                                  {a.d_stream != nullptr, next, next, post || (MERGE && a.gate_kind != MOE_GATE_NONE)},
                                  {next, post, channel, channel && a.gate_sigmoid});
-    workers = p.grid * p.groups;
+    workers = p.join ? p.grid : p.grid * p.groups;
     cudaError_t err;
-    if (norm_fast(p, a, MERGE) && a.d_stream) {
-      err = launch_bwd_fast<ST, MERGE>(a, p, s);
+    if (norm_known(a, MERGE) && a.d_stream) {
+      err = norm_exact(p, a, MERGE) ? launch_bwd_known<ST, MERGE, true>(a, p, s) : launch_bwd_known<ST, MERGE, false>(a, p, s);
     } else {
       switch (norm_cols(a.d)) {
-        case 8: err = launch_rows<norm_bwd_kernel<ST, 8 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
-        case 16: err = launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
-        default: err = launch_rows<norm_bwd_kernel<ST, 32 / U, MERGE, false, MOE_GATE_NONE>>(a, p, s); break;
+        case 8: err = launch_rows<norm_bwd_kernel<ST, 8 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
+        case 16: err = launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
+        default: err = launch_rows<norm_bwd_kernel<ST, 32 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
       }
     }
     if (err != cudaSuccess) return err;
