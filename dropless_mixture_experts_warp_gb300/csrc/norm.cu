@@ -12,18 +12,22 @@
 // gates activated, in shared memory where that has room beside two rows a group.
 //
 // KNOWN variants know at compile time what a call usually has: every weight, the gradient of
-// the stream, the kind of gate GATE (one choice after the other at run time: 355 us instead
-// of 449 for the gradients of a 16384 x 7168 merge when they came); EXACT ones also that the
-// weights are in shared memory and the row's units fill the threads.
+// the stream, the kind of gate GATE (asked element by element at run time these choices took
+// half of the instructions); EXACT ones also that the weights are in shared memory and that
+// the row's units fill the threads.
 #include "around.cuh"
+
+#include <algorithm>
 
 namespace moe {
 
 constexpr int NORM_MAX_D = 16384;
 constexpr int NORM_SMEM = 225 * 1024;  // dynamic shared memory of a block: of the 227 KB, static buffers aside
 constexpr int NORM_MAX_SMS = 160;      // blocks at most
-constexpr int NORM_FWD_THREADS = 640;  // 96 registers a thread: with 1024 threads and 64, spills cost 12 % (two rows under way)
-constexpr int NORM_BWD_THREADS = 512;  // 128 registers a thread: the column sums of three weights
+// Threads of a block: the forward of the merge needs 96 registers a thread (spills with 64
+// cost 12 %), the backward those of three weights' column sums, 128 with 16 columns a thread.
+constexpr int norm_fwd_threads(bool merge) { return merge ? 640 : 1024; }
+constexpr int norm_bwd_threads(int cols) { return cols == 8 ? 768 : 512; }
 
 struct NormArgs {
   int T, d;
@@ -51,7 +55,8 @@ constexpr int GATE_SLOPE = 3;  // a sigmoid channel gate, for the backward's var
 
 // How the threads and the shared memory of a block are split.
 struct NormPlan {
-  int grid, groups, tpr;
+  int grid, groups, tpr, cols;
+  bool staged;            // every weight has a place
   int off[RING_ARRAYS];   // each array's place in a ring row (-1: not read)
   int weight[W_ARRAYS];   // each weight's place, in floats (-1: read from global memory)
   int row_bytes, weight_bytes, stages;
@@ -125,10 +130,13 @@ __device__ __forceinline__ float weight_value(const NormArgs& a, int kind, float
   return kind == W_GATE ? g : g * (1.0f - g);
 }
 template <int U>
-__device__ __forceinline__ void global_weights(const NormArgs& a, int kind, int u, f32x2 (&v)[U / 2]) {
+__device__ __forceinline__ void raw_weights(const NormArgs& a, int kind, int u, f32x2 (&v)[U / 2]) {
   const void* w = kind == W_NEXT ? a.w_next : kind == W_POST ? a.w_post : a.gate;
   if (a.weight_type == MOE_TYPE_BF16) unpack<U>(static_cast<const moe_bf16*>(w) + u * U, v);
   else unpack<U>(static_cast<const float*>(w) + u * U, v);
+}
+template <int U>
+__device__ __forceinline__ void weight_values(const NormArgs& a, int kind, f32x2 (&v)[U / 2]) {
 #pragma unroll
   for (int j = 0; j < U / 2; ++j) {
     const float2 f = unpair(v[j]);
@@ -149,21 +157,29 @@ __device__ __forceinline__ void weights(const NormArgs& a, const NormPlan& plan,
       v[2 * j + 1] = q.y;
     }
   } else {
-    global_weights<U>(a, kind, u, v);
+    raw_weights<U>(a, kind, u, v);
+    weight_values<U>(a, kind, v);
   }
 }
-// Copies the weights that have a place into shared memory (the caller synchronises).
+// Copies the weights that have a place into shared memory (the caller synchronises).  All
+// arrays' loads come before the first use of one: they wait for memory together.
 template <int U>
 __device__ __forceinline__ void stage_weights(const NormArgs& a, const NormPlan& plan, float* smem, int units) {
+  for (int u = threadIdx.x; u < units; u += blockDim.x) {
+    f32x2 v[W_ARRAYS][U / 2];
 #pragma unroll
-  for (int kind = 0; kind < W_ARRAYS; ++kind) {
-    if (plan.weight[kind] < 0) continue;
-    for (int u = threadIdx.x; u < units; u += blockDim.x) {
-      f32x2 v[U / 2];
-      global_weights<U>(a, kind, u, v);
+    for (int kind = 0; kind < W_SLOPE; ++kind)
+      if (plan.weight[kind] >= 0 || (kind == W_GATE && plan.weight[W_SLOPE] >= 0)) raw_weights<U>(a, kind, u, v[kind]);
+#pragma unroll
+    for (int j = 0; j < U / 2; ++j) v[W_SLOPE][j] = v[W_GATE][j];
+#pragma unroll
+    for (int kind = 0; kind < W_ARRAYS; ++kind) {
+      if (plan.weight[kind] < 0) continue;
+      weight_values<U>(a, kind, v[kind]);
 #pragma unroll
       for (int j = 0; j < U / 4; ++j)
-        *reinterpret_cast<ulonglong2*>(smem + plan.weight[kind] + (j * units + u) * 4) = make_ulonglong2(v[2 * j], v[2 * j + 1]);
+        *reinterpret_cast<ulonglong2*>(smem + plan.weight[kind] + (j * units + u) * 4) =
+            make_ulonglong2(v[kind][2 * j], v[kind][2 * j + 1]);
     }
   }
 }
@@ -197,6 +213,7 @@ __device__ __forceinline__ float lane_sums(const float* s, int lane) {
 // gets them.  Two buffers taken in turn need one barrier a sum: whoever writes a buffer
 // again has passed the barrier of the other, which its readers reach after reading.
 constexpr int SUMS_MAX = 5;
+constexpr int MAX_WARPS = 24;  // of a group
 struct GroupSums {
   float* buf;   // the group's 2 * SUMS_MAX * tpr / 32 floats
   int tpr, group, tid, flip;
@@ -212,7 +229,8 @@ struct GroupSums {
     const int lane = tid & 31, warps = tpr >> 5, first = lane & (WIDTH - 1), value = lane / WIDTH;
     const float* r = b + (value < N ? value : 0) * warps;
     float v = first < warps ? r[first] : 0.0f;
-    if (WIDTH < 16) v += first + WIDTH < warps ? r[first + WIDTH] : 0.0f;  // at most 16 warps a group
+#pragma unroll
+    for (int more = WIDTH; more < MAX_WARPS; more += WIDTH) v += first + more < warps ? r[first + more] : 0.0f;
 #pragma unroll
     for (int off = WIDTH / 2; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
 #pragma unroll
@@ -255,7 +273,7 @@ __device__ __forceinline__ float sum_pair(f32x2 v) {
 // together with this row's sum of h_out^2, so that a row takes one barrier and its waits are
 // filled with the other row's work.
 template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE>
-__global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
+__global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * SUMS_MAX * 32];
   constexpr int U = 16 / sizeof(ST);
@@ -391,7 +409,7 @@ __global__ void __launch_bounds__(NORM_FWD_THREADS) norm_fwd_kernel(const NormAr
 // 7168 bf16 with everything).  So y has one place more in the ring than the other arrays.
 // What a call lacks (weights, gate) takes its neutral value, a unit at a time.
 template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE>
-__global__ void __launch_bounds__(NORM_BWD_THREADS) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
+__global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(sizeof(ST)))) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * SUMS_MAX * 32];
   constexpr int U = 16 / sizeof(ST);
@@ -677,16 +695,16 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
 
 // ------------------------------------------------------------------ launchers
 
-// Units of a thread: 16 columns (narrow rows: 8; beyond 8192 columns 32), so that a row has
-// at most 512 threads and its column sums stay in registers.
-static int norm_cols(int d) { return d <= 256 ? 8 : d <= 8192 ? 16 : 32; }
+static int row_threads(int d, int cols) { return ((d + cols - 1) / cols + 31) / 32 * 32; }
 
-// The plan for rows of d columns; used[] tells the arrays and weights of the call.
-static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&rows)[RING_ARRAYS],
-                          const bool (&w)[W_ARRAYS]) {
+// The plan for rows of d columns with `cols` a thread and up to max_threads a block; rows[]
+// and w[] tell the arrays and weights of the call.
+static NormPlan norm_plan_for(int T, int d, int cols, int stream_size, bool bwd, int max_threads, const bool (&rows)[RING_ARRAYS],
+                              const bool (&w)[W_ARRAYS]) {
   NormPlan p{};
-  p.tpr = ((d + norm_cols(d) - 1) / norm_cols(d) + 31) / 32 * 32;
-  p.groups = (bwd ? NORM_BWD_THREADS : NORM_FWD_THREADS) / p.tpr;
+  p.cols = cols;
+  p.tpr = row_threads(d, cols);
+  p.groups = max_threads / p.tpr;
   if (p.tpr > 32 && p.groups > 15) p.groups = 15;  // named barriers 1 .. 15
   const int sms = num_sms() < NORM_MAX_SMS ? num_sms() : NORM_MAX_SMS;
   p.grid = T < sms ? T : sms;
@@ -703,10 +721,12 @@ static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&
   // most 224 KB), then the weights, then up to four rows a group
   while (p.groups > 1 && ring(2) > NORM_SMEM) --p.groups;
   p.stages = ring(2) <= NORM_SMEM ? 2 : 1;
+  p.staged = true;
   for (int k = 0; k < W_ARRAYS; ++k) {
     const bool fits = w[k] && ring(p.stages) + p.weight_bytes + d * 4 <= NORM_SMEM;
     p.weight[k] = fits ? p.weight_bytes / 4 : -1;
     if (fits) p.weight_bytes += d * 4;
+    else if (w[k]) p.staged = false;
   }
   while (p.stages > 1 && p.stages < 4 && ring(p.stages + 1) + p.weight_bytes <= NORM_SMEM) ++p.stages;
   p.smem_bytes = ring(p.stages) + p.weight_bytes;
@@ -714,15 +734,24 @@ static NormPlan norm_plan(int T, int d, int stream_size, bool bwd, const bool (&
   return p;
 }
 
-// Whether the KNOWN and the EXACT variants take the call (see the top of the file).
-static bool norm_known(const NormArgs& a, bool merge) { return norm_cols(a.d) == 16 && a.w_next && (!merge || a.w_post); }
-static bool norm_exact(const NormPlan& p, const NormArgs& a, bool merge) {
-  if (a.d != p.tpr * 16) return false;
-  const bool channel = merge && a.gate_kind == MOE_GATE_CHANNEL;
-  return p.weight[W_NEXT] >= 0 && (!merge || p.weight[W_POST] >= 0) && (!channel || p.weight[W_GATE] >= 0) &&
-         (!(channel && a.gate_sigmoid) || !a.dh || p.weight[W_SLOPE] >= 0);
+// Columns of a thread: 16 where that fills the block (narrow rows: 8, beyond 8192 columns 32).
+static NormPlan norm_fwd_plan(int T, int d, int stream_size, bool merge, const bool (&rows)[RING_ARRAYS], const bool (&w)[W_ARRAYS]) {
+  return norm_plan_for(T, d, d <= 256 ? 8 : d <= 8192 ? 16 : 32, stream_size, false, norm_fwd_threads(merge), rows, w);
+}
+// In the backward 8 also where 16 leave most of the block without threads (4472 columns: one
+// group of 288) or more groups' rings leave no room for the weights (4096 columns of an fp32
+// stream: two groups of 256, weights read from global memory for each row).
+static NormPlan norm_bwd_plan(int T, int d, int stream_size, const bool (&rows)[RING_ARRAYS], const bool (&w)[W_ARRAYS]) {
+  if (d > 8192) return norm_plan_for(T, d, 32, stream_size, true, norm_bwd_threads(32), rows, w);
+  const NormPlan wide = norm_plan_for(T, d, 16, stream_size, true, norm_bwd_threads(16), rows, w);
+  if (row_threads(d, 8) > norm_bwd_threads(8)) return wide;
+  if (d > 256 && wide.staged && norm_bwd_threads(16) / wide.tpr * wide.tpr >= 384) return wide;
+  const NormPlan narrow = norm_plan_for(T, d, 8, stream_size, true, norm_bwd_threads(8), rows, w);
+  return wide.staged && !narrow.staged ? wide : narrow;
 }
 
+// Whether the KNOWN variants take the call (see the top of the file).
+static bool norm_known(const NormPlan& p, const NormArgs& a, bool merge) { return p.cols < 32 && a.w_next && (!merge || a.w_post); }
 template <auto KERN>
 static cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   const cudaError_t err = allow_smem<KERN>(NORM_SMEM);
@@ -732,33 +761,38 @@ static cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_
   return cudaGetLastError();
 }
 
-template <typename ST, bool MERGE, bool EXACT>
+template <typename ST, int COLS, bool MERGE, bool EXACT>
 static cudaError_t launch_fwd_known(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-  constexpr int N = 16 / (16 / sizeof(ST)), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
+  constexpr int N = COLS * sizeof(ST) / 16, CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
   if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE>>(a, p, s);
   if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, TK>>(a, p, s);
   return launch_rows<norm_fwd_kernel<ST, N, MERGE, true, EXACT, CH>>(a, p, s);
 }
 
+template <typename ST, int COLS, bool MERGE>
+static cudaError_t launch_fwd_cols(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  if (COLS == 16 && norm_known(p, a, MERGE)) {
+    constexpr int C = COLS == 16 ? 16 : 8;
+    // where one row fills the block (16384 x 7168: 139 us, 164 without); with two groups or
+    // more the guarded form is faster (16384 x 4096: 87 us, 95 with)
+    constexpr bool EXACT = MERGE && sizeof(ST) == 2 && C == 16;
+    return p.staged && a.d == p.tpr * COLS && 2 * p.tpr > norm_fwd_threads(MERGE) ? launch_fwd_known<ST, C, MERGE, EXACT>(a, p, s) : launch_fwd_known<ST, C, MERGE, false>(a, p, s);
+  }
+  return launch_rows<norm_fwd_kernel<ST, COLS * static_cast<int>(sizeof(ST)) / 16, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
+}
+
 template <typename ST, bool MERGE>
 static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  constexpr int SZ = sizeof(ST), U = 16 / SZ;
-  const bool channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
-  const NormPlan p = norm_plan(a.T, a.d, SZ, false, {false, true, false, MERGE},
-                               {a.w_next != nullptr, a.w_post != nullptr, channel, false});
-  if (norm_known(a, MERGE))
-    return norm_exact(p, a, MERGE) ? launch_fwd_known<ST, MERGE, true>(a, p, s) : launch_fwd_known<ST, MERGE, false>(a, p, s);
-  switch (norm_cols(a.d)) {
-    case 8: return launch_rows<norm_fwd_kernel<ST, 8 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
-    case 16: return launch_rows<norm_fwd_kernel<ST, 16 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
-    default: return launch_rows<norm_fwd_kernel<ST, 32 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
-  }
+  const NormPlan p = norm_fwd_plan(a.T, a.d, sizeof(ST), MERGE, {false, true, false, MERGE},
+                                   {a.w_next != nullptr, a.w_post != nullptr, MERGE && a.gate_kind == MOE_GATE_CHANNEL, false});
+  return p.cols == 8 ? launch_fwd_cols<ST, 8, MERGE>(a, p, s)
+                     : p.cols == 16 ? launch_fwd_cols<ST, 16, MERGE>(a, p, s) : launch_fwd_cols<ST, 32, MERGE>(a, p, s);
 }
 
-template <typename ST, bool MERGE, bool EXACT>
+template <typename ST, int COLS, bool MERGE, bool EXACT>
 static cudaError_t launch_bwd_known(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
-  constexpr int N = 16 / (16 / sizeof(ST)), CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
+  constexpr int N = COLS * sizeof(ST) / 16, CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
   constexpr int SL = MERGE ? GATE_SLOPE : MOE_GATE_NONE;
   if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE>>(a, p, s);
   if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, TK>>(a, p, s);
@@ -766,26 +800,28 @@ static cudaError_t launch_bwd_known(const NormArgs& a, const NormPlan& p, cudaSt
   return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, CH>>(a, p, s);
 }
 
+template <typename ST, int COLS, bool MERGE>
+static cudaError_t launch_bwd_cols(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
+  if (COLS < 32 && norm_known(p, a, MERGE) && a.d_stream) {
+    constexpr int C = COLS < 32 ? COLS : 16;
+    // (16384 x 7168 bf16: 221 us, 276 without; the fp32 stream's and the 8-column forms spill)
+    constexpr bool EXACT = sizeof(ST) == 2 && C == 16;
+    return p.staged && a.d == p.tpr * COLS ? launch_bwd_known<ST, C, MERGE, EXACT>(a, p, s) : launch_bwd_known<ST, C, MERGE, false>(a, p, s);
+  }
+  return launch_rows<norm_bwd_kernel<ST, COLS * static_cast<int>(sizeof(ST)) / 16, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
+}
+
 template <typename ST, bool MERGE>
 static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_post, float* dgate_cols, cudaStream_t s) {
-  constexpr int SZ = sizeof(ST), U = 16 / SZ;
   const bool next = a.w_next, post = MERGE && a.w_post, channel = MERGE && a.gate_kind == MOE_GATE_CHANNEL;
   int workers = 0;
   if (a.T > 0) {
-    const NormPlan p = norm_plan(a.T, a.d, SZ, true,
-                                 {a.d_stream != nullptr, next, next, post || (MERGE && a.gate_kind != MOE_GATE_NONE)},
-                                 {next, post, channel, channel && a.gate_sigmoid});
+    const NormPlan p = norm_bwd_plan(a.T, a.d, sizeof(ST),
+                                     {a.d_stream != nullptr, next, next, post || (MERGE && a.gate_kind != MOE_GATE_NONE)},
+                                     {next, post, channel, channel && a.gate_sigmoid});
     workers = p.join ? p.grid : p.grid * p.groups;
-    cudaError_t err;
-    if (norm_known(a, MERGE) && a.d_stream) {
-      err = norm_exact(p, a, MERGE) ? launch_bwd_known<ST, MERGE, true>(a, p, s) : launch_bwd_known<ST, MERGE, false>(a, p, s);
-    } else {
-      switch (norm_cols(a.d)) {
-        case 8: err = launch_rows<norm_bwd_kernel<ST, 8 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
-        case 16: err = launch_rows<norm_bwd_kernel<ST, 16 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
-        default: err = launch_rows<norm_bwd_kernel<ST, 32 / U, MERGE, false, false, MOE_GATE_NONE>>(a, p, s); break;
-      }
-    }
+    const cudaError_t err = p.cols == 8 ? launch_bwd_cols<ST, 8, MERGE>(a, p, s)
+                                        : p.cols == 16 ? launch_bwd_cols<ST, 16, MERGE>(a, p, s) : launch_bwd_cols<ST, 32, MERGE>(a, p, s);
     if (err != cudaSuccess) return err;
   }
   if (dw_next || dw_post || dgate_cols) {
@@ -824,8 +860,9 @@ moe_status moe_norm_check_dims(const moe_norm_dims* dims) {
 
 size_t moe_norm_workspace_size(const moe_norm_dims* dims) {
   if (moe_norm_check_dims(dims) != MOE_OK) return 0;
-  const int tpr = ((dims->d + norm_cols(dims->d) - 1) / norm_cols(dims->d) + 31) / 32 * 32;
-  return static_cast<size_t>(NORM_MAX_SMS) * (NORM_BWD_THREADS / tpr) * 3 * dims->d * sizeof(float);
+  // blocks times the most groups of a block, as if none added their sums in the block
+  const int d = dims->d, most = std::max({1, norm_bwd_threads(8) / row_threads(d, 8), norm_bwd_threads(16) / row_threads(d, 16)});
+  return static_cast<size_t>(NORM_MAX_SMS) * most * 3 * d * sizeof(float);
 }
 
 moe_status moe_norm_fwd(const moe_norm_dims* dims, const void* h, const void* w, moe_bf16* x, void* stream) {
