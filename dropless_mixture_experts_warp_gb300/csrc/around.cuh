@@ -1,5 +1,5 @@
 // Shared pieces of the operators around the layer (block norms, balance loss, optimiser):
-// 8-element vectors in bf16 or fp32 and sums over the threads that share a row.
+// launches, asynchronous copies, arithmetic on pairs, sums over a block.
 #pragma once
 
 #include <atomic>
@@ -11,8 +11,8 @@ namespace moe {
 void count_launch();
 int num_sms();
 
-// Allows kernel KERN `bytes` of dynamic shared memory, once a device (asked at every call it
-// costs a launch 0.5 us).
+// Allows kernel KERN `bytes` of dynamic shared memory, once a device (at every call it would
+// cost a launch 0.5 us; after a cudaDeviceReset the launch fails, and the call says so).
 template <auto KERN>
 static cudaError_t allow_smem(int bytes) {
   static std::atomic<uint64_t> done{0};
@@ -61,7 +61,7 @@ template <int N>
 __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // Two fp32 values in a register pair, and arithmetic on both in one instruction (rounded
-// as two scalar ones).
+// as two scalar ones, except that a mul2 whose only use is an add2 may become one fma2).
 using f32x2 = unsigned long long;
 __device__ __forceinline__ f32x2 pair(float x, float y) {
   f32x2 r;
@@ -95,20 +95,7 @@ __device__ __forceinline__ f32x2 fma2_down(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
-// Eight consecutive elements, widened to fp32 / rounded once from it.
-__device__ __forceinline__ void load8(const moe_bf16* p, float (&v)[8]) {
-  const uint4 q = *reinterpret_cast<const uint4*>(p);
-  v[0] = bf16_lo(q.x); v[1] = bf16_hi(q.x); v[2] = bf16_lo(q.y); v[3] = bf16_hi(q.y);
-  v[4] = bf16_lo(q.z); v[5] = bf16_hi(q.z); v[6] = bf16_lo(q.w); v[7] = bf16_hi(q.w);
-}
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8_as(const void* p, int type, long long at, float (&v)[8]) {
-  if (type == MOE_TYPE_BF16) load8(static_cast<const moe_bf16*>(p) + at, v);
-  else load8(static_cast<const float*>(p) + at, v);
-}
+// Eight consecutive elements, rounded once from fp32.
 __device__ __forceinline__ void store8(moe_bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
