@@ -31,7 +31,7 @@ def test_norms():
         t[rows] = torch.randn(len(rows), d, device="cuda", generator=g).bfloat16()
     w = torch.randn(d, device="cuda", generator=g)
     dims = block.dims_of(T, d)
-    # one row more than the outputs' buffers of allocate() would need: only what the calls write
+    # the entry points themselves: allocate() would hold every call's outputs at once
     from dropless_mixture_experts_warp_gb300 import binding as B
     out, dw = torch.empty_like(h), torch.empty(d, device="cuda")
     ws = torch.empty(B.moe_norm_workspace_size(dims), dtype=torch.uint8, device="cuda")
@@ -41,9 +41,11 @@ def test_norms():
     check("x", out[rows], (x, abs(x)), "bf16", 128)
     B.moe_norm_bwd(dims, dx, h, w, None, out, dw, ws)
     check("dh", out[rows], oa.norm_bwd(f64(dx[rows]), f64(h[rows]), f64(w), 1e-6)["dh"], "bf16", 128)
-    B.moe_merge_fwd(dims, h, dx, w, None, w, out, h)       # x over h: rows are read before they are written
-    del dx
-    torch.cuda.synchronize()
+    x_next = torch.empty_like(h)
+    B.moe_merge_fwd(dims, h, dx, w, None, w, out, x_next)
+    ref = oa.merge_fwd(f64(h[rows]), f64(dx[rows]), f64(w), None, f64(w), eps=1e-6)
+    check("h_out", out[rows], ref["h_out"], "bf16", 128)
+    check("x_next", x_next[rows], ref["x"], "bf16", 256)
 
 
 def test_balance():
