@@ -67,16 +67,17 @@ struct NormPlan {
   int smem_bytes;
   bool join;              // backward: the groups' column sums are added in the block
   int y_bytes;            // backward: y has a ring of its own, of stages + 1 rows
+  bool late_y;            // or, for two stages, of two
 };
 
 __device__ __forceinline__ float gate_act(float g, int sigmoid) { return sigmoid ? 1.0f / (1.0f + __expf(-g)) : g; }
 
-// Until the oldest of `stages` open groups of copies has arrived.
-__device__ __forceinline__ void copy_wait_oldest(int stages) {
-  switch (stages) {
-    case 1: copy_wait<0>(); break;
-    case 2: copy_wait<1>(); break;
-    case 3: copy_wait<2>(); break;
+// Until at most n (0 .. 3) of the thread's groups of copies are under way.
+__device__ __forceinline__ void copy_wait_but(int n) {
+  switch (n) {
+    case 0: copy_wait<0>(); break;
+    case 1: copy_wait<1>(); break;
+    case 2: copy_wait<2>(); break;
     default: copy_wait<3>(); break;
   }
 }
@@ -329,7 +330,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const
   int stage = 0;
   float first = 0.0f;  // the row's first sum, over all its columns
   if (worker < a.T) {
-    copy_wait_oldest(plan.stages);
+    copy_wait_but(plan.stages - 1);
     float s[1] = {first_sum(my_ring)};
     sums(s);
     first = s[0];
@@ -381,7 +382,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const
     stage = stage + 1 == plan.stages ? 0 : stage + 1;
     float s[MERGE ? 2 : 1] = {};
     if (row + workers < a.T) {
-      copy_wait_oldest(plan.stages);
+      copy_wait_but(plan.stages - 1);
       s[0] = first_sum(my_ring + stage * plan.row_bytes);
     }
     if (MERGE) s[MERGE ? 1 : 0] = sum_pair(ss);
@@ -412,7 +413,7 @@ __global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const
 // waits are filled with the other row's work (355 us with two barriers a row, for 16384 x
 // 7168 bf16 with everything).  So y has one place more in the ring than the other arrays.
 // What a call lacks (weights, gate) takes its neutral value, a unit at a time.
-template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE>
+template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE, bool LATE>
 __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(sizeof(ST)))) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float buf[2 * SUMS_MAX * 32];
@@ -423,8 +424,20 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
   const float inv_d = 1.0f / static_cast<float>(a.d);
   GroupSums sums{buf + group * 2 * SUMS_MAX * (tpr >> 5), tpr, group, tid, 0};
   const float* s_w = reinterpret_cast<const float*>(smem);
-  uint8_t* my_ring = smem + plan.weight_bytes + group * (plan.stages * plan.row_bytes + (plan.stages + 1) * plan.y_bytes);
+  const int last_y = plan.stages - (LATE ? 1 : 0);  // of the places of y
+  uint8_t* my_ring = smem + plan.weight_bytes + group * (plan.stages * plan.row_bytes + (last_y + 1) * plan.y_bytes);
   uint8_t* my_y = my_ring + plan.stages * plan.row_bytes;
+  auto fetch_y = [&](long long row, int y_stage) {
+    if (row < a.T) {
+      const uint32_t dst_y = smem_u32(my_y + y_stage * plan.y_bytes);
+#pragma unroll
+      for (int i = 0; i < UPT; ++i) {
+        const int u = tid + i * tpr;
+        if (EXACT || u < units) copy_async<U * 2>(dst_y + u * U * 2, a.y + row * a.d + u * U);
+      }
+    }
+    copy_commit();
+  };
   auto fetch = [&](long long row, int stage, int y_stage) {
     if (row < a.T) {
       const uint32_t dst = smem_u32(my_ring + stage * plan.row_bytes), dst_y = smem_u32(my_y + y_stage * plan.y_bytes);
@@ -436,13 +449,17 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
         if (KNOWN || plan.off[RING_D] >= 0) copy_async<16>(dst + plan.off[RING_D] + u * 16, static_cast<const ST*>(a.d_stream) + at);
         if (KNOWN || plan.off[RING_H] >= 0) copy_async<16>(dst + plan.off[RING_H] + u * 16, static_cast<const ST*>(a.h) + at);
         if (KNOWN || plan.off[RING_DX] >= 0) copy_async<U * 2>(dst + plan.off[RING_DX] + u * U * 2, a.dx + at);
-        if (MERGE && (KNOWN || plan.y_bytes > 0)) copy_async<U * 2>(dst_y + u * U * 2, a.y + at);
+        if (MERGE && !LATE && (KNOWN || plan.y_bytes > 0)) copy_async<U * 2>(dst_y + u * U * 2, a.y + at);
       }
     }
     copy_commit();
   };
-  // one group of copies a row: `stages` of them are open when a row is waited for
-  for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s, s);
+  // one group of copies a row, or two where LATE (the row's other arrays, its y): those of
+  // `stages` rows are open when a row is waited for
+  for (int s = 0; s < plan.stages; ++s) {
+    fetch(worker + static_cast<long long>(s) * workers, s, s);
+    if (LATE) fetch_y(worker + static_cast<long long>(s) * workers, s);
+  }
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
   __syncthreads();
   const bool next = KNOWN || a.w_next != nullptr, post = MERGE && (KNOWN || a.w_post != nullptr);
@@ -492,7 +509,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
   int stage = 0, y_stage = 0;
   float hh = 0.0f, nh = 0.0f, yy = 0.0f;  // of the row, over all its columns
   if (worker < a.T) {
-    copy_wait_oldest(plan.stages);
+    copy_wait_but(LATE ? 2 : plan.stages - 1);
     float s[3];
     first_sums(my_ring, my_y, s[0], s[1], s[2]);
     sums(s);
@@ -571,14 +588,14 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
       }
     }
     // the row's D, h and dx were used above and y of the row before in its dy: their places
-    // are free for the row `stages` further on
-    const int y_after = y_stage + plan.stages > plan.stages ? y_stage - 1 : plan.stages;
+    // are free for the row `stages` further on (where LATE, this row's y is, below)
+    const int y_after = LATE ? y_stage : y_stage + plan.stages > plan.stages ? y_stage - 1 : plan.stages;
     fetch(row + static_cast<long long>(plan.stages) * workers, stage, y_after);
     stage = stage + 1 == plan.stages ? 0 : stage + 1;
-    y_stage = y_stage == plan.stages ? 0 : y_stage + 1;
+    y_stage = y_stage == last_y ? 0 : y_stage + 1;
     float s[!MERGE ? 2 : KNOWN && GATE != MOE_GATE_TOKEN ? 4 : 5] = {};
     if (row + workers < a.T) {
-      copy_wait_oldest(plan.stages);
+      copy_wait_but(plan.stages - 1);
       float y2;
       first_sums(my_ring + stage * plan.row_bytes, my_y + y_stage * plan.y_bytes, s[0], s[1], y2);
       if (MERGE) s[MERGE ? 2 : 0] = y2;
@@ -612,6 +629,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
         const int u = tid + i * tpr;
         if (EXACT || u < units) pack<U>(a.dy + base + u * U, q[i]);
       }
+      if (LATE) fetch_y(row + static_cast<long long>(plan.stages) * workers, y_after);
     }
   }
   // the groups' column sums, added in order through the rings' room where that suffices
@@ -703,8 +721,8 @@ static int row_threads(int d, int cols) { return ((d + cols - 1) / cols + 31) / 
 
 // The plan for rows of d columns with `cols` a thread and up to max_threads a block; rows[]
 // and w[] tell the arrays and weights of the call.
-static NormPlan norm_plan_for(int T, int d, int cols, int stream_size, bool bwd, int max_threads, const bool (&rows)[RING_ARRAYS],
-                              const bool (&w)[W_ARRAYS]) {
+static NormPlan norm_plan_for(int T, int d, int cols, int stream_size, bool bwd, bool may_late, int max_threads,
+                              const bool (&rows)[RING_ARRAYS], const bool (&w)[W_ARRAYS]) {
   NormPlan p{};
   p.cols = cols;
   p.tpr = row_threads(d, cols);
@@ -720,17 +738,31 @@ static NormPlan norm_plan_for(int T, int d, int cols, int stream_size, bool bwd,
     p.off[i] = rows[i] && !apart ? p.row_bytes : -1;
     if (rows[i]) (apart ? p.y_bytes : p.row_bytes) += d * size[i];
   }
-  auto ring = [&](int stages) { return p.groups * (stages * p.row_bytes + (p.y_bytes ? (stages + 1) * p.y_bytes : 0)); };
+  auto ring = [&](int stages) { return p.groups * (stages * p.row_bytes + (stages + (p.late_y ? 0 : 1)) * p.y_bytes); };
   // groups as far as each has room for two rows (one row fits always: 16384 columns take at
   // most 224 KB), then the weights, then up to four rows a group
   while (p.groups > 1 && ring(2) > NORM_SMEM) --p.groups;
   p.stages = ring(2) <= NORM_SMEM ? 2 : 1;
-  p.staged = true;
+  int wanted = 0;
+  for (int k = 0; k < W_ARRAYS; ++k) wanted += w[k];
+  auto places = [&] { return std::min(wanted, (NORM_SMEM - ring(p.stages)) / (d * 4)); };
+  if (may_late && p.stages == 2 && places() < wanted) {
+    const int before = places();
+    p.late_y = true;
+    p.late_y = places() > before;
+  }
+  int left = places();
+  p.staged = left == wanted;
   for (int k = 0; k < W_ARRAYS; ++k) {
-    const bool fits = w[k] && ring(p.stages) + p.weight_bytes + d * 4 <= NORM_SMEM;
-    p.weight[k] = fits ? p.weight_bytes / 4 : -1;
-    if (fits) p.weight_bytes += d * 4;
-    else if (w[k]) p.staged = false;
+    p.weight[k] = w[k] && left > 0 ? p.weight_bytes / 4 : -1;
+    if (p.weight[k] < 0) continue;
+    p.weight_bytes += d * 4;
+    --left;
+  }
+  if (p.late_y) {
+    p.smem_bytes = ring(p.stages) + p.weight_bytes;
+    p.join = p.groups > 1 && p.groups * (w[W_NEXT] + w[W_POST] + w[W_GATE]) * d * 4 <= ring(p.stages);
+    return p;
   }
   while (p.stages > 1 && p.stages < 4 && ring(p.stages + 1) + p.weight_bytes <= NORM_SMEM) ++p.stages;
   p.smem_bytes = ring(p.stages) + p.weight_bytes;
@@ -740,17 +772,18 @@ static NormPlan norm_plan_for(int T, int d, int cols, int stream_size, bool bwd,
 
 // Columns of a thread: 16 where that fills the block (narrow rows: 8, beyond 8192 columns 32).
 static NormPlan norm_fwd_plan(int T, int d, int stream_size, bool merge, const bool (&rows)[RING_ARRAYS], const bool (&w)[W_ARRAYS]) {
-  return norm_plan_for(T, d, d <= 256 ? 8 : d <= 8192 ? 16 : 32, stream_size, false, norm_fwd_threads(merge), rows, w);
+  return norm_plan_for(T, d, d <= 256 ? 8 : d <= 8192 ? 16 : 32, stream_size, false, false, norm_fwd_threads(merge), rows, w);
 }
 // In the backward 8 also where 16 leave most of the block without threads (4472 columns: one
 // group of 288) or more groups' rings leave no room for the weights (4096 columns of an fp32
 // stream: two groups of 256, weights read from global memory for each row).
 static NormPlan norm_bwd_plan(int T, int d, int stream_size, const bool (&rows)[RING_ARRAYS], const bool (&w)[W_ARRAYS]) {
-  if (d > 8192) return norm_plan_for(T, d, 32, stream_size, true, norm_bwd_threads(32), rows, w);
-  const NormPlan wide = norm_plan_for(T, d, 16, stream_size, true, norm_bwd_threads(16), rows, w);
+  if (d > 8192) return norm_plan_for(T, d, 32, stream_size, true, false, norm_bwd_threads(32), rows, w);
+  const bool known = rows[RING_D] && w[W_NEXT] && w[W_POST];  // the variants that have a LATE form
+  const NormPlan wide = norm_plan_for(T, d, 16, stream_size, true, known, norm_bwd_threads(16), rows, w);
   if (row_threads(d, 8) > norm_bwd_threads(8)) return wide;
   if (d > 256 && wide.staged && norm_bwd_threads(16) / wide.tpr * wide.tpr >= 384) return wide;
-  const NormPlan narrow = norm_plan_for(T, d, 8, stream_size, true, norm_bwd_threads(8), rows, w);
+  const NormPlan narrow = norm_plan_for(T, d, 8, stream_size, true, false, norm_bwd_threads(8), rows, w);
   return wide.staged && !narrow.staged ? wide : narrow;
 }
 
@@ -794,14 +827,14 @@ static cudaError_t launch_norm_fwd(const NormArgs& a, cudaStream_t s) {
                      : p.cols == 16 ? launch_fwd_cols<ST, 16, MERGE>(a, p, s) : launch_fwd_cols<ST, 32, MERGE>(a, p, s);
 }
 
-template <typename ST, int COLS, bool MERGE, bool EXACT>
+template <typename ST, int COLS, bool MERGE, bool EXACT, bool LATE>
 static cudaError_t launch_bwd_known(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   constexpr int N = COLS * sizeof(ST) / 16, CH = MERGE ? MOE_GATE_CHANNEL : MOE_GATE_NONE, TK = MERGE ? MOE_GATE_TOKEN : MOE_GATE_NONE;
   constexpr int SL = MERGE ? GATE_SLOPE : MOE_GATE_NONE;
-  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE>>(a, p, s);
-  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, TK>>(a, p, s);
-  if (a.gate_sigmoid) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, SL>>(a, p, s);
-  return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, CH>>(a, p, s);
+  if (!MERGE || a.gate_kind == MOE_GATE_NONE) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, MOE_GATE_NONE, LATE>>(a, p, s);
+  if (a.gate_kind == MOE_GATE_TOKEN) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, TK, LATE>>(a, p, s);
+  if (a.gate_sigmoid) return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, SL, LATE>>(a, p, s);
+  return launch_rows<norm_bwd_kernel<ST, N, MERGE, true, EXACT, CH, LATE>>(a, p, s);
 }
 
 template <typename ST, int COLS, bool MERGE>
@@ -809,10 +842,12 @@ static cudaError_t launch_bwd_cols(const NormArgs& a, const NormPlan& p, cudaStr
   if (COLS < 32 && norm_known(p, a, MERGE) && a.d_stream) {
     constexpr int C = COLS < 32 ? COLS : 16;
     // (16384 x 7168 bf16: 221 us, 276 without; the fp32 stream's and the 8-column forms spill)
-    constexpr bool EXACT = sizeof(ST) == 2 && C == 16;
-    return p.staged && a.d == p.tpr * COLS ? launch_bwd_known<ST, C, MERGE, EXACT>(a, p, s) : launch_bwd_known<ST, C, MERGE, false>(a, p, s);
+    constexpr bool EXACT = sizeof(ST) == 2 && C == 16, LATE = MERGE && C == 16;
+    const bool exact = p.staged && a.d == p.tpr * COLS;
+    if (p.late_y) return exact ? launch_bwd_known<ST, C, MERGE, EXACT, LATE>(a, p, s) : launch_bwd_known<ST, C, MERGE, false, LATE>(a, p, s);
+    return exact ? launch_bwd_known<ST, C, MERGE, EXACT, false>(a, p, s) : launch_bwd_known<ST, C, MERGE, false, false>(a, p, s);
   }
-  return launch_rows<norm_bwd_kernel<ST, COLS * static_cast<int>(sizeof(ST)) / 16, MERGE, false, false, MOE_GATE_NONE>>(a, p, s);
+  return launch_rows<norm_bwd_kernel<ST, COLS * static_cast<int>(sizeof(ST)) / 16, MERGE, false, false, MOE_GATE_NONE, false>>(a, p, s);
 }
 
 template <typename ST, bool MERGE>
