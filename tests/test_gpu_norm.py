@@ -222,3 +222,11 @@ def test_many_rows(T, d, stream):
                  "dgate": (d if gate == "token" else T) + 3 * ROW}
         for n in ref:
             check(f"{gate} {act} {n}", got[n], ref[n], {"dh": stream, "dy": "bf16"}.get(n, "fp32"), terms[n])
+
+
+# Widths at which the gradients' ring leaves the weights room only with one row of y fewer: units that fill the
+# threads and that do not, and a width at which it does for one of the types alone
+@pytest.mark.parametrize("T,d", [(800, 8192), (700, 7176), (900, 6664)])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+def test_many_rows_of_wide_streams(T, d, stream):
+    test_many_rows(T, d, stream)
