@@ -10,6 +10,7 @@ where the formulas and the 8-bit format are).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 from dataclasses import dataclass
 from typing import List, Optional
@@ -33,6 +34,12 @@ class Plan:
     bits: int
     table: ctypes.Array         # the entry point's descriptors of the above
     hyper: B.moe_adamw_hyper
+    device: torch.device
+    shapes: List[torch.Size]    # of the weights
+
+    def check_device(self):
+        if self.device.type != "cuda":
+            raise ValueError(f"AdamW runs on a GPU: the plan's tensors are on {self.device}")
 
 
 def plan(weights, grads, copies=None, bits=32, weight_decay=0.0, m=None, v=None, m_scale=None, v_scale=None) -> Plan:
@@ -58,6 +65,11 @@ def plan(weights, grads, copies=None, bits=32, weight_decay=0.0, m=None, v=None,
     every = [weights, grads, copies, decay, m, v] + ([m_scale, v_scale] if bits == 8 else [])
     if any(len(x) != n for x in every):
         raise ValueError("as many gradients, copies, decays and states as weights")
+    if any(t is None for x in every if x is not copies for t in x):
+        raise ValueError("only copies may be None")
+    device = weights[0].device if n else torch.device("cuda")
+    if any(w.device != device for w in weights):
+        raise ValueError("weights on more than one device")
     table = (B.moe_adamw_tensor * max(1, n))()
     for i, w in enumerate(weights):
         B.check_tensor(w, torch.float32, w.shape, w.device)
@@ -74,12 +86,14 @@ def plan(weights, grads, copies=None, bits=32, weight_decay=0.0, m=None, v=None,
         t.w16 = None if copies[i] is None else copies[i].data_ptr()
         t.n, t.weight_decay = w.numel(), decay[i]
         t.grad_type = B.TYPE["bf16" if grads[i].dtype == torch.bfloat16 else "fp32"]
-    return Plan(weights, grads, copies, m, v, m_scale, v_scale, bits, table, B.moe_adamw_hyper(bits=bits))
+    return Plan(weights, grads, copies, m, v, m_scale, v_scale, bits, table, B.moe_adamw_hyper(bits=bits), device,
+                [w.shape for w in weights])
 
 
 def step(p: Plan, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, seed=0, control=None, stream=None):
     """Updates p's weights, copies and states.  seed: of the 8-bit states' draws.  control: a Control, whose values
     on the device then take the place of `step` and scale lr and the gradients (for captured steps)."""
+    p.check_device()
     h = p.hyper
     h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed = lr, beta1, beta2, eps, step, seed
     B.moe_adamw_step(h, p.table, len(p.weights), None if control is None else control.raw, stream)
@@ -101,15 +115,16 @@ def values(p: Plan, m_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
     """The moments that p's 8-bit states stand for, as lists of tensors (new ones of `dtype`, or the given)."""
     if p.bits != 8:
         raise ValueError("values: the states are held in fp32 as they are")
-    new = lambda: [torch.empty(w.shape, dtype=dtype, device=w.device) for w in p.weights]  # noqa: E731
-    m_out, v_out = new() if m_out is None else m_out, new() if v_out is None else v_out
+    p.check_device()
+    new = lambda: [torch.empty(s, dtype=dtype, device=p.device) for s in p.shapes]  # noqa: E731
+    m_out, v_out = new() if m_out is None else list(m_out), new() if v_out is None else list(v_out)
     kind = m_out[0].dtype if m_out else dtype
-    if kind not in (torch.bfloat16, torch.float32) or len(m_out) != len(p.weights) or len(v_out) != len(p.weights):
-        raise ValueError("values: one bf16 or fp32 tensor a weight for either moment")
-    for a, b, w in zip(m_out, v_out, p.weights):
-        B.check_tensor(a, kind, w.shape, w.device)
-        B.check_tensor(b, kind, w.shape, w.device)
-    pointers = lambda ts: (ctypes.c_void_p * max(1, len(ts)))(*[t.data_ptr() for t in ts])  # noqa: E731
+    if kind not in (torch.bfloat16, torch.float32):
+        raise ValueError("values: bf16 or fp32 tensors")
+    B.check_tensors(m_out, kind, p.shapes, p.device)
+    B.check_tensors(v_out, kind, p.shapes, p.device)
+    pointers = lambda ts: (ctypes.c_void_p * max(1, len(ts))).from_buffer(  # noqa: E731
+        array.array("Q", [t.data_ptr() for t in ts] or [0]))
     B.moe_adamw_values(p.table, len(p.weights), B.TYPE["bf16" if kind == torch.bfloat16 else "fp32"], pointers(m_out),
                        pointers(v_out), stream)
     return m_out, v_out

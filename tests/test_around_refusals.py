@@ -142,3 +142,31 @@ def test_adamw_plan_refuses_tensors_that_do_not_fit(B):
             optim.plan(**{**good, **bad})
     with pytest.raises(ValueError):
         optim.values(optim.plan(**good))
+
+
+def test_adamw_refuses_tensors_that_are_not_on_one_gpu(B):
+    import torch
+    from dropless_mixture_experts_warp_gb300 import optim
+    w = torch.zeros(8, 16)
+    p = optim.plan([w], [w.clone()], bits=8)
+    for call in (lambda: optim.step(p, lr=1e-3, step=1), lambda: optim.values(p)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+    with pytest.raises(ValueError, match="device"):
+        optim.plan([w, w.to("meta")], [w, w.to("meta")])
+    with pytest.raises(ValueError):
+        optim.plan([w], [None])
+    with pytest.raises(ValueError):
+        optim.plan([w], [w], m=[None])
+
+
+def test_lists_of_tensors_are_checked_one_by_one(B):
+    import torch
+    ts = [torch.zeros(3, 4), torch.zeros(5)]
+    shapes, cpu = [t.shape for t in ts], torch.device("cpu")
+    B.check_tensors(ts, torch.float32, shapes, cpu)
+    B.check_tensors([], torch.float32, [], cpu)
+    for bad in ([ts[0]], [ts[0], None], [ts[1], ts[0]], [ts[0].t().contiguous().t(), ts[1]], [ts[0], ts[1].double()],
+                [ts[0], ts[1].to("meta")]):
+        with pytest.raises(ValueError):
+            B.check_tensors(bad, torch.float32, shapes, cpu)
