@@ -185,6 +185,8 @@ __device__ __forceinline__ int tensor_of(const A& a, long long unit) {
 // fp32 states.  A unit of elements a block, four consecutive ones a thread: wide loads of
 // all arrays before the first use, and enough threads (five blocks an SM) to cover them.
 __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_32) adamw_kernel(const __grid_constant__ AdamArgs a) {
+  wait_for_previous();
+  launch_dependents();
   AdamScalars sc;
   int step;
   if (!adam_scalars(a, sc, step)) return;
@@ -504,6 +506,8 @@ __device__ __forceinline__ void adam8_unit(const Unit8& c, const AdamTensor& t, 
 __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __grid_constant__ AdamArgs a) {
   extern __shared__ Slot8 rings[];
   Slot8* const ring = rings + (threadIdx.x >> 5) * RING8;
+  wait_for_previous();
+  launch_dependents();
   AdamScalars sc;
   int step;
   if (!adam_scalars(a, sc, step)) return;
@@ -550,6 +554,8 @@ struct AdamValueArgs {
 // The values of 8-bit states.
 template <typename OT>
 __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_VALUES) adamw_values_kernel(const __grid_constant__ AdamValueArgs a) {
+  wait_for_previous();
+  launch_dependents();
   for (long long unit = blockIdx.x; unit < a.units; unit += gridDim.x) {
     const AdamValue& t = a.t[tensor_of(a, unit)];
     const long long start = (unit - t.first) * a.chunk;
@@ -618,9 +624,7 @@ static cudaError_t launch_adam(int grid, const A& a, cudaStream_t s) {
     const cudaError_t err = allow_smem<KERN>(SMEM);
     if (err != cudaSuccess) return err;
   }
-  KERN<<<grid, ADAM_THREADS, SMEM, s>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(KERN, dim3(grid), dim3(ADAM_THREADS), SMEM, s, a);
 }
 
 }  // namespace moe

@@ -29,18 +29,23 @@ static cudaError_t allow_smem(int bytes) {
 inline bool ptr_aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
-// A kernel that joins the partial sums of the one before it is launched early: its blocks
-// come up while the other's last ones run and wait there for its end and its writes.
+// Every kernel here is launched early: its blocks come up as the last ones of the kernel
+// before it on the stream (of any origin) leave the SMs, and wait there for that kernel's end
+// and its writes.  It saves a call 2 us (balance of 16384 x 256: 17.1 to 14.8 us, norm of
+// 8121 x 2048: 20.7 to 18.6 us, calls one after another).  A kernel waits before it touches
+// memory and only then lets the next one come up, so that a kernel that has begun knows that
+// everything before its predecessor is done.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... Params, typename... Args>
-static cudaError_t launch_early(void (*kern)(Params...), dim3 grid, dim3 block, cudaStream_t s, Args... args) {
+static cudaError_t launch_early(void (*kern)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, const Args&... args) {
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

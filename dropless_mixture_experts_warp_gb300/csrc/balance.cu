@@ -204,6 +204,8 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
   __shared__ int s_off[SEQ_TABLE + 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gl = lane % G, group = threadIdx.x / G;
   const int c0 = blockIdx.x * a.chunk, c1 = min(a.T, c0 + a.chunk);
+  wait_for_previous();
+  launch_dependents();
   // The chunk's first tokens are on their way before their sequences are known.  A token's
   // mask is read two tokens ahead, its logits and its first choice a lane one ahead.
   auto kept = [&](int t, int e) { return t < e && (!a.mask || a.mask[t]); };
@@ -216,7 +218,6 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
   const Sequences seqs(a, s_off);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;  // of the join's blocks
   __syncthreads();
-  launch_dependents();
   bool fresh = true;
   for (int s = seqs.of(c0); s < a.S; ++s) {
     const int start = seqs.at(s);
@@ -362,6 +363,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
     last = (e - 1) / a.chunk + s;
   }
   wait_for_previous();
+  launch_dependents();
   // n in two parts, whose sums over at most 320 chunks fp32 holds exactly
   float nz[3] = {0.0f, 0.0f, 0.0f};
   for (int i = first + static_cast<int>(threadIdx.x); i <= last; i += 256) {
@@ -454,6 +456,8 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceA
   const long long t0 = (static_cast<long long>(blockIdx.x) * (BAL_THREADS / G) + threadIdx.x / G) * a.run;
   const int t1 = static_cast<int>(min(static_cast<long long>(a.T), t0 + a.run));
   auto kept = [&](long long t) { return t < t1 && (!a.mask || a.mask[t]); };
+  wait_for_previous();
+  launch_dependents();
   // the first token's values are on their way while the totals are added up
   f32x2 l[M], old[M];
   bool keep = kept(t0), keep_next = a.run > 1 && kept(t0 + 1);
@@ -653,14 +657,13 @@ static cudaError_t launch_balance_fwd(BalanceArgs a, const moe_balance_dims& m, 
   const long long chunks = balance_chunks(m);
   if (chunks > 0) {
     const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_fwd<true>(a.E) : pick_fwd<false>(a.E);
-    kern<<<static_cast<unsigned>(chunks), BAL_THREADS, 0, s>>>(a);
-    count_launch();
-    if ((err = cudaGetLastError()) != cudaSuccess) return err;
+    err = launch_early(kern, dim3(static_cast<unsigned>(chunks)), dim3(BAL_THREADS), 0, s, a);
+    if (err != cudaSuccess) return err;
     if (chunks == 1 && a.S == 1) return cudaSuccess;
   } else if ((err = cudaMemsetAsync(a.counter, 0, 4, s)) != cudaSuccess) {
     return err;
   }
-  return launch_early(balance_join_kernel, dim3((a.E + JOIN_COLS - 1) / JOIN_COLS, a.S), dim3(256), s, a);
+  return launch_early(balance_join_kernel, dim3((a.E + JOIN_COLS - 1) / JOIN_COLS, a.S), dim3(256), 0, s, a);
 }
 
 static cudaError_t launch_balance_bwd(BalanceArgs a, const moe_balance_dims& m, cudaStream_t s) {
@@ -671,9 +674,7 @@ static cudaError_t launch_balance_bwd(BalanceArgs a, const moe_balance_dims& m, 
   a.run = static_cast<int>((a.T + most - 1) / most);
   const long long grid = (a.T + static_cast<long long>(groups) * a.run - 1) / (static_cast<long long>(groups) * a.run);
   const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_bwd<true>(a.E) : pick_bwd<false>(a.E);
-  kern<<<static_cast<unsigned>(grid), BAL_THREADS, 0, s>>>(a);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(kern, dim3(static_cast<unsigned>(grid)), dim3(BAL_THREADS), 0, s, a);
 }
 
 }  // namespace moe

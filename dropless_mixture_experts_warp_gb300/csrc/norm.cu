@@ -303,6 +303,8 @@ __global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const
     }
     copy_commit();
   };
+  wait_for_previous();
+  launch_dependents();
   // one group of copies a row: `stages` of them are open when a row is waited for
   for (int s = 0; s < plan.stages; ++s) fetch(worker + static_cast<long long>(s) * workers, s);
   stage_weights<U>(a, plan, reinterpret_cast<float*>(smem), units);
@@ -457,6 +459,8 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
     }
     copy_commit();
   };
+  wait_for_previous();
+  launch_dependents();
   // one group of copies a row, or two where LATE (the row's other arrays, its y): those of
   // `stages` rows are open when a row is waited for
   for (int s = 0; s < plan.stages; ++s) {
@@ -508,7 +512,6 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
     fill<U>(dw_post[i], 0.0f);
     fill<U>(dgate[i], 0.0f);
   }
-  launch_dependents();
   int stage = 0, y_stage = 0;
   float hh = 0.0f, nh = 0.0f, yy = 0.0f;  // of the row, over all its columns
   if (worker < a.T) {
@@ -693,6 +696,7 @@ __global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restric
   __shared__ float buf[32][REDUCE_COLS + 1];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   wait_for_previous();
+  launch_dependents();
   if (!out) return;
   const int quad = threadIdx.x & 7, grp = threadIdx.x >> 3;
   const int c = blockIdx.x * REDUCE_COLS + quad * 4;
@@ -796,9 +800,7 @@ template <auto KERN>
 static cudaError_t launch_rows(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   const cudaError_t err = allow_smem<KERN>(NORM_SMEM);
   if (err != cudaSuccess) return err;
-  KERN<<<p.grid, p.groups * p.tpr, p.smem_bytes, s>>>(a, p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(KERN, dim3(p.grid), dim3(p.groups * p.tpr), p.smem_bytes, s, a, p);
 }
 
 template <typename ST, int COLS, bool MERGE, bool EXACT>
@@ -867,7 +869,7 @@ static cudaError_t launch_norm_bwd(const NormArgs& a, float* dw_next, float* dw_
     if (err != cudaSuccess) return err;
   }
   if (dw_next || dw_post || dgate_cols) {
-    return launch_early(norm_reduce_kernel, dim3((a.d + REDUCE_COLS - 1) / REDUCE_COLS, 3), dim3(256), s,
+    return launch_early(norm_reduce_kernel, dim3((a.d + REDUCE_COLS - 1) / REDUCE_COLS, 3), dim3(256), 0, s,
                         static_cast<const float*>(a.part), workers, a.d, dw_next, dw_post, dgate_cols);
   }
   return cudaSuccess;

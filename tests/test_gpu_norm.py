@@ -230,3 +230,51 @@ def test_many_rows(T, d, stream):
 @pytest.mark.parametrize("stream", ["bf16", "fp32"])
 def test_many_rows_of_wide_streams(T, d, stream):
     test_many_rows(T, d, stream)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_written_just_before_and_on_another_stream(captured):
+    """The kernels come up while what precedes them runs: they read nothing before it is done, be it a slow kernel
+    of their stream, of another that it waits for, or a copy; and what follows may overwrite their inputs."""
+    from dropless_mixture_experts_warp_gb300 import block
+    T, d = 2048, 1024
+    i = inputs(T, d, "bf16", "fp32", 3)
+    (h, _), (w, _), (dx, _) = i["h"], i["w"], i["dx"]
+    b = block.allocate(block.dims_of(T, d))
+    want = block.norm_forward(b, h, w).clone()
+    want_dh, want_dw = block.norm_backward(b, dx, h, w).clone(), b.dw.clone()
+    src, dst, x, dh, dw = (torch.zeros_like(t) for t in (h, dx, want, want_dh, want_dw))
+    side = torch.cuda.Stream()
+
+    def work():
+        here = torch.cuda.current_stream()
+        torch.cuda._sleep(200_000)
+        torch.mul(h, 1.0, out=src)
+        x.copy_(block.norm_forward(b, src, w))
+        src.zero_()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000)
+            src.copy_(h)
+            dst.copy_(dx)
+        here.wait_stream(side)
+        dh.copy_(block.norm_backward(b, dst, src, w))
+        dw.copy_(b.dw)
+        dst.zero_()
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    s.synchronize()
+    if captured:
+        for t in (src, dst, x, dh, dw):
+            t.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            work()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+    assert torch.equal(x, want) and torch.equal(dh, want_dh) and torch.equal(dw, want_dw)
