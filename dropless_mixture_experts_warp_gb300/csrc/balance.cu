@@ -3,7 +3,7 @@
 //
 // A token's E logits lie over the G lanes of a group, PLV vectors of VEC a lane (16 logits a
 // lane up to 512 experts: a token's sums then take few shuffles a logit, and a warp has
-// several tokens under way).  Exponentials are 2^x of the scaled argument, which the maximum
+// several tokens under way; 30001 x 131 over all 32 lanes: 29 us, over 16: 16 us).  Exponentials are 2^x of the scaled argument, which the maximum
 // keeps at or below 0: their relative error is at most |l - max| 2^-24 + 2^-22.
 #include "around.cuh"
 
@@ -194,8 +194,9 @@ __device__ __forceinline__ void row_sigmoid(const f32x2 (&l)[M], float top, f32x
 // and keep the sums of p in registers; the counts are integer sums in shared memory.  A
 // single block with a single sequence writes the results itself.
 template <int VEC, int G, int PLV, bool SIGMOID>
-__global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(BAL_THREADS, VEC * PLV <= 16 ? 2 : 1) balance_fwd_kernel(const BalanceArgs a) {
   constexpr int N = VEC * PLV, M = N / 2, GROUPS = BAL_THREADS / G, WARP_COLS = N * G;
+  constexpr int C = G < 8 ? 8 / G : 1;  // choices of a lane that are read ahead
   __shared__ float s_p[BAL_THREADS / 32][WARP_COLS];
   __shared__ int s_c[WARP_COLS];
   __shared__ float s_z[BAL_THREADS / 32];
@@ -207,14 +208,22 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
   wait_for_previous();
   launch_dependents();
   // The chunk's first tokens are on their way before their sequences are known.  A token's
-  // mask is read two tokens ahead, its logits and its first choice a lane one ahead.
+  // mask is read two tokens ahead, its logits and its first C choices a lane one ahead (one
+  // choice a lane: 11.5 us for 88517 x 16, 7 choices; so 8.7 us).
   auto kept = [&](int t, int e) { return t < e && (!a.mask || a.mask[t]); };
-  auto choice = [&](int t, bool there) { return there && gl < a.k ? a.topk_idx[static_cast<long long>(t) * a.k + gl] : -1; };
-  int t = c0 + group, x;
+  auto choices = [&](int t, bool there, int (&x)[C]) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) x[i] = there && gl + G * i < a.k ? a.topk_idx[static_cast<long long>(t) * a.k + gl + G * i] : -1;
+  };
+  auto count = [&](int x) {
+    if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
+    else set_status(a.status, MOE_ERR_INVARIANT);
+  };
+  int t = c0 + group, x[C];
   bool keep = kept(t, c1), keep_next = kept(t + GROUPS, c1);
   f32x2 l[M];
   load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, t < c1, -INFINITY, l);
-  x = choice(t, t < c1);
+  choices(t, t < c1, x);
   const Sequences seqs(a, s_off);
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.counter = 0;  // of the join's blocks
   __syncthreads();
@@ -233,7 +242,7 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
       keep = kept(t, e);
       keep_next = kept(t + GROUPS, e);
       load_row<VEC, G, PLV>(a.logits + static_cast<long long>(t) * a.E, a.E, gl, keep, -INFINITY, l);
-      x = choice(t, keep);
+      choices(t, keep, x);
     }
     fresh = false;
     if (!keep) {
@@ -251,12 +260,12 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
       const bool keep_after = kept(tn + GROUPS, e);
       f32x2 next[M];
       load_row<VEC, G, PLV>(a.logits + static_cast<long long>(tn) * a.E, a.E, gl, keep_next, -INFINITY, next);
-      const int x_next = choice(tn, keep_next);
-      for (int j = gl; keep && j < a.k; j += G) {
-        if (j != gl) x = a.topk_idx[static_cast<long long>(t) * a.k + j];
-        if (x >= 0 && x < a.E) atomicAdd(&s_c[x], 1);
-        else set_status(a.status, MOE_ERR_INVARIANT);
-      }
+      int x_next[C];
+      choices(tn, keep_next, x_next);
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (keep && gl + G * i < a.k) count(x[i]);
+      for (int j = gl + G * C; keep && j < a.k; j += G) count(a.topk_idx[static_cast<long long>(t) * a.k + j]);
       __syncwarp();
       f32x2 p[M];
       float inv, lse = 0.0f;
@@ -270,7 +279,8 @@ __global__ void __launch_bounds__(BAL_THREADS) balance_fwd_kernel(const BalanceA
         acc2[c] = fma2(p[c], pair(inv, inv), acc2[c]);
         l[c] = next[c];
       }
-      x = x_next;
+#pragma unroll
+      for (int i = 0; i < C; ++i) x[i] = x_next[i];
       t = tn;
       keep = keep_next;
       keep_next = keep_after;
@@ -364,7 +374,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   }
   wait_for_previous();
   launch_dependents();
-  // n in two parts, whose sums over at most 320 chunks fp32 holds exactly
+  // n in two parts, whose sums over at most 300 chunks fp32 holds exactly
   float nz[3] = {0.0f, 0.0f, 0.0f};
   for (int i = first + static_cast<int>(threadIdx.x); i <= last; i += 256) {
     const int c = a.part_n[i];
@@ -377,21 +387,33 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   int4 c = make_int4(0, 0, 0, 0);
   const bool vec = a.E % 4 == 0;
-  for (int j = first + grp; j <= last; j += 32) {
-    const float* pp = a.part_p + static_cast<long long>(j) * a.E + x;
-    const int* pc = a.part_c + static_cast<long long>(j) * a.E + x;
-    if (vec) {
-      if (x < a.E) {
-        const float4 q = *reinterpret_cast<const float4*>(pp);
-        const int4 d = *reinterpret_cast<const int4*>(pc);
-        p.x += q.x; p.y += q.y; p.z += q.z; p.w += q.w;
-        c.x += d.x; c.y += d.y; c.z += d.z; c.w += d.w;
+  constexpr int AHEAD = 4;  // parts that are read together: the 300 of a sequence are ten a thread
+                            // (16385 x 256 one by one: 15.6 us, so 12.6 us)
+  for (int j0 = first + grp; j0 <= last; j0 += 32 * AHEAD) {
+    float4 q[AHEAD];
+    int4 d[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const long long at = static_cast<long long>(j0 + 32 * i) * a.E + x;
+      const int left = j0 + 32 * i <= last ? a.E - x : 0;
+      q[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      d[i] = make_int4(0, 0, 0, 0);
+      if (vec) {
+        if (left > 0) {
+          q[i] = *reinterpret_cast<const float4*>(a.part_p + at);
+          d[i] = *reinterpret_cast<const int4*>(a.part_c + at);
+        }
+      } else {
+        if (left > 0) { q[i].x = a.part_p[at]; d[i].x = a.part_c[at]; }
+        if (left > 1) { q[i].y = a.part_p[at + 1]; d[i].y = a.part_c[at + 1]; }
+        if (left > 2) { q[i].z = a.part_p[at + 2]; d[i].z = a.part_c[at + 2]; }
+        if (left > 3) { q[i].w = a.part_p[at + 3]; d[i].w = a.part_c[at + 3]; }
       }
-    } else {
-      if (x < a.E) { p.x += pp[0]; c.x += pc[0]; }
-      if (x + 1 < a.E) { p.y += pp[1]; c.y += pc[1]; }
-      if (x + 2 < a.E) { p.z += pp[2]; c.z += pc[2]; }
-      if (x + 3 < a.E) { p.w += pp[3]; c.w += pc[3]; }
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      p.x += q[i].x; p.y += q[i].y; p.z += q[i].z; p.w += q[i].w;
+      c.x += d[i].x; c.y += d[i].y; c.z += d[i].z; c.w += d[i].w;
     }
   }
   s_p[grp][col] = p;
@@ -417,7 +439,14 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
       sum[0] = static_cast<float>(k) * fs * (v * inv_n);
     }
     row_sums<true, 1>(sum, buf);
-    if (threadIdx.x == 0) {
+    if (gridDim.x * gridDim.y == 1) {  // all there is
+      if (threadIdx.x == 0) {
+        a.seq_tokens[0] = n;
+        a.losses[0] = a.coef * sum[0];
+        a.losses[1] = a.z_coef != 0.0f ? a.z_coef * nz[2] * inv_n : 0.0f;
+        s_last = 0;
+      }
+    } else if (threadIdx.x == 0) {
       a.seq_loss[static_cast<long long>(s) * gridDim.x + blockIdx.x] = sum[0];
       if (blockIdx.x == 0) {
         a.seq_tokens[s] = n;
@@ -448,7 +477,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
 // A group takes a run of consecutive tokens.  dl_j = g0 coef / (S' n_s) p_j (f_j - sum f p)
 // [(1 - sigmoid(l_j)) for sigmoid scores] + g1 z_coef 2 / N lse softmax(l)_j.
 template <int VEC, int G, int PLV, bool SIGMOID>
-__global__ void __launch_bounds__(BAL_THREADS) balance_bwd_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(BAL_THREADS, VEC * PLV <= 16 ? 2 : 1) balance_bwd_kernel(const BalanceArgs a) {
   constexpr int N = VEC * PLV, M = N / 2;
   __shared__ float buf[32 * 2];
   __shared__ int s_off[SEQ_TABLE + 1];
@@ -562,19 +591,18 @@ static size_t al256(size_t x) { return (x + 255) / 256 * 256; }
 
 // Lanes of a token's group.
 static int balance_lanes(int E) {
-  if (E % 4 != 0) return 32;
   int g = 1;
   while (g < 32 && g * 16 < E) g *= 2;
   return g;
 }
 
-// Tokens of a forward block: about two blocks an SM (counted as 160 whatever the GPU, as
-// the workspace's size goes by it), each group with at least one token; up to four a group
+// Tokens of a forward block: the two blocks that an SM holds (of 150 SMs whatever the GPU, as
+// the workspace's size goes by it: one wave), each group with at least one token; up to four a group
 // stay in one block, whose results then need no join.
 static int balance_chunk(const moe_balance_dims& m) {
   const int groups = BAL_THREADS / balance_lanes(m.E);
   if (m.T <= 4 * groups) return 4 * groups;
-  const long long per = (static_cast<long long>(m.T) + 319) / 320;
+  const long long per = (static_cast<long long>(m.T) + 299) / 300;
   return static_cast<int>((per + groups - 1) / groups * groups);
 }
 static long long balance_chunks(const moe_balance_dims& m) {
@@ -618,37 +646,37 @@ static BalanceArgs balance_args(const moe_balance_dims& m) {
 
 using BalanceKernel = void (*)(BalanceArgs);
 
-template <bool SIGMOID>
+template <int VEC, bool SIGMOID>
 static BalanceKernel pick_fwd(int E) {
-  if (E % 4 != 0) {
-    if (E <= 128) return balance_fwd_kernel<1, 32, 4, SIGMOID>;
-    if (E <= 512) return balance_fwd_kernel<1, 32, 16, SIGMOID>;
-    return balance_fwd_kernel<1, 32, 32, SIGMOID>;
-  }
+  constexpr int PLV = 16 / VEC;
   switch (balance_lanes(E)) {
-    case 1: return balance_fwd_kernel<4, 1, 4, SIGMOID>;
-    case 2: return balance_fwd_kernel<4, 2, 4, SIGMOID>;
-    case 4: return balance_fwd_kernel<4, 4, 4, SIGMOID>;
-    case 8: return balance_fwd_kernel<4, 8, 4, SIGMOID>;
-    case 16: return balance_fwd_kernel<4, 16, 4, SIGMOID>;
-    default: return E <= 512 ? balance_fwd_kernel<4, 32, 4, SIGMOID> : balance_fwd_kernel<4, 32, 8, SIGMOID>;
+    case 1: return balance_fwd_kernel<VEC, 1, PLV, SIGMOID>;
+    case 2: return balance_fwd_kernel<VEC, 2, PLV, SIGMOID>;
+    case 4: return balance_fwd_kernel<VEC, 4, PLV, SIGMOID>;
+    case 8: return balance_fwd_kernel<VEC, 8, PLV, SIGMOID>;
+    case 16: return balance_fwd_kernel<VEC, 16, PLV, SIGMOID>;
+    default: return E <= 512 ? balance_fwd_kernel<VEC, 32, PLV, SIGMOID> : balance_fwd_kernel<VEC, 32, 2 * PLV, SIGMOID>;
   }
 }
-template <bool SIGMOID>
+static BalanceKernel pick_fwd(int E, bool sigmoid) {
+  if (E % 4 != 0) return sigmoid ? pick_fwd<1, true>(E) : pick_fwd<1, false>(E);
+  return sigmoid ? pick_fwd<4, true>(E) : pick_fwd<4, false>(E);
+}
+template <int VEC, bool SIGMOID>
 static BalanceKernel pick_bwd(int E) {
-  if (E % 4 != 0) {
-    if (E <= 128) return balance_bwd_kernel<1, 32, 4, SIGMOID>;
-    if (E <= 512) return balance_bwd_kernel<1, 32, 16, SIGMOID>;
-    return balance_bwd_kernel<1, 32, 32, SIGMOID>;
-  }
+  constexpr int PLV = 16 / VEC;
   switch (balance_lanes(E)) {
-    case 1: return balance_bwd_kernel<4, 1, 4, SIGMOID>;
-    case 2: return balance_bwd_kernel<4, 2, 4, SIGMOID>;
-    case 4: return balance_bwd_kernel<4, 4, 4, SIGMOID>;
-    case 8: return balance_bwd_kernel<4, 8, 4, SIGMOID>;
-    case 16: return balance_bwd_kernel<4, 16, 4, SIGMOID>;
-    default: return E <= 512 ? balance_bwd_kernel<4, 32, 4, SIGMOID> : balance_bwd_kernel<4, 32, 8, SIGMOID>;
+    case 1: return balance_bwd_kernel<VEC, 1, PLV, SIGMOID>;
+    case 2: return balance_bwd_kernel<VEC, 2, PLV, SIGMOID>;
+    case 4: return balance_bwd_kernel<VEC, 4, PLV, SIGMOID>;
+    case 8: return balance_bwd_kernel<VEC, 8, PLV, SIGMOID>;
+    case 16: return balance_bwd_kernel<VEC, 16, PLV, SIGMOID>;
+    default: return E <= 512 ? balance_bwd_kernel<VEC, 32, PLV, SIGMOID> : balance_bwd_kernel<VEC, 32, 2 * PLV, SIGMOID>;
   }
+}
+static BalanceKernel pick_bwd(int E, bool sigmoid) {
+  if (E % 4 != 0) return sigmoid ? pick_bwd<1, true>(E) : pick_bwd<1, false>(E);
+  return sigmoid ? pick_bwd<4, true>(E) : pick_bwd<4, false>(E);
 }
 
 static cudaError_t launch_balance_fwd(BalanceArgs a, const moe_balance_dims& m, cudaStream_t s) {
@@ -656,7 +684,7 @@ static cudaError_t launch_balance_fwd(BalanceArgs a, const moe_balance_dims& m, 
   a.chunk = balance_chunk(m);
   const long long chunks = balance_chunks(m);
   if (chunks > 0) {
-    const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_fwd<true>(a.E) : pick_fwd<false>(a.E);
+    const BalanceKernel kern = pick_fwd(a.E, m.score == MOE_SCORE_SIGMOID);
     err = launch_early(kern, dim3(static_cast<unsigned>(chunks)), dim3(BAL_THREADS), 0, s, a);
     if (err != cudaSuccess) return err;
     if (chunks == 1 && a.S == 1) return cudaSuccess;
@@ -673,7 +701,7 @@ static cudaError_t launch_balance_bwd(BalanceArgs a, const moe_balance_dims& m, 
   const long long most = static_cast<long long>(num_sms()) * 2 * groups;
   a.run = static_cast<int>((a.T + most - 1) / most);
   const long long grid = (a.T + static_cast<long long>(groups) * a.run - 1) / (static_cast<long long>(groups) * a.run);
-  const BalanceKernel kern = m.score == MOE_SCORE_SIGMOID ? pick_bwd<true>(a.E) : pick_bwd<false>(a.E);
+  const BalanceKernel kern = pick_bwd(a.E, m.score == MOE_SCORE_SIGMOID);
   return launch_early(kern, dim3(static_cast<unsigned>(grid)), dim3(BAL_THREADS), 0, s, a);
 }
 

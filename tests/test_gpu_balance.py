@@ -202,3 +202,12 @@ def test_side_stream_and_graph():
 def test_many_tokens(T, E, k, S, masked, score):
     """Several tokens a group and several groups a block's part; more sequences than the table in shared memory."""
     run(*case(T, E, k, S, masked), score, k)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,S,masked", [(9001, 7, 7, 1, True), (5003, 15, 12, 3, True), (16, 16, 16, 2, False),
+                                            (6001, 18, 9, 1, False), (5501, 33, 10, 4, True), (5002, 66, 5, 1, True),
+                                            (4001, 131, 17, 2, False), (2501, 258, 8, 1, True), (9000, 32, 20, 3, True)])
+def test_each_number_of_lanes(T, E, k, S, masked, score):
+    """Widths that are no multiple of four at each group size, and more choices than a group reads ahead."""
+    run(*case(T, E, k, S, masked, 1), score, k)
