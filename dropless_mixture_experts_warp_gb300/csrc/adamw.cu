@@ -185,8 +185,7 @@ __device__ __forceinline__ int tensor_of(const A& a, long long unit) {
 // fp32 states.  A unit of elements a block, four consecutive ones a thread: wide loads of
 // all arrays before the first use, and enough threads (five blocks an SM) to cover them.
 __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_32) adamw_kernel(const __grid_constant__ AdamArgs a) {
-  wait_for_previous();
-  launch_dependents();
+  wait_for_previous();  // (the next kernel's blocks among the last of these: 2562 us for 604M elements, 2545 without)
   AdamScalars sc;
   int step;
   if (!adam_scalars(a, sc, step)) return;

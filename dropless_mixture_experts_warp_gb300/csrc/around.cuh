@@ -34,7 +34,7 @@ inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : 
 // and its writes.  It saves a call 2 us (balance of 16384 x 256: 17.1 to 14.8 us, norm of
 // 8121 x 2048: 20.7 to 18.6 us, calls one after another).  A kernel waits before it touches
 // memory and only then lets the next one come up, so that a kernel that has begun knows that
-// everything before its predecessor is done.
+// everything before its predecessor is done.  (The step of fp32 moments lets nothing come up.)
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... Params, typename... Args>

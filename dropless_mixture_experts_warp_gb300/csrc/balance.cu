@@ -3,8 +3,13 @@
 //
 // A token's E logits lie over the G lanes of a group, PLV vectors of VEC a lane (16 logits a
 // lane up to 512 experts: a token's sums then take few shuffles a logit, and a warp has
-// several tokens under way; 30001 x 131 over all 32 lanes: 29 us, over 16: 16 us).  Exponentials are 2^x of the scaled argument, which the maximum
-// keeps at or below 0: their relative error is at most |l - max| 2^-24 + 2^-22.
+// several tokens under way; 30001 x 131 over all 32 lanes: 29 us, over 16: 16 us).
+// Exponentials are 2^x of the scaled argument, which the maximum keeps at or below 0: their
+// relative error is at most |l - max| 2^-24 + 2^-22.
+//
+// Measured (GB300, in a graph): losses of 393215 x 128, 41 us (5.2 TB/s), of 16384 x 256 13 us
+// (bound by the chain of dependent reads through two kernels); gradients 10.5 us for the
+// latter, 96 us for 393216 x 128 (6.28 TB/s, the rate of memory).
 #include "around.cuh"
 
 namespace moe {
@@ -190,11 +195,15 @@ __device__ __forceinline__ void row_sigmoid(const f32x2 (&l)[M], float top, f32x
   inv = sum == 0.0f ? 0.0f : rcp_fast(sum);
 }
 
+// Blocks of the forward that an SM holds, by their registers (393215 x 128 with two: 55 us, with
+// three 41 us).
+constexpr int balance_fwd_blocks(int vec, int lanes, int E) { return E > 512 ? 1 : vec == 4 && lanes >= 8 ? 3 : 2; }
+
 // A block takes a chunk of tokens, sequence by sequence: its groups take the tokens in turn
 // and keep the sums of p in registers; the counts are integer sums in shared memory.  A
 // single block with a single sequence writes the results itself.
 template <int VEC, int G, int PLV, bool SIGMOID>
-__global__ void __launch_bounds__(BAL_THREADS, VEC * PLV <= 16 ? 2 : 1) balance_fwd_kernel(const BalanceArgs a) {
+__global__ void __launch_bounds__(BAL_THREADS, balance_fwd_blocks(VEC, G, VEC * PLV * G)) balance_fwd_kernel(const BalanceArgs a) {
   constexpr int N = VEC * PLV, M = N / 2, GROUPS = BAL_THREADS / G, WARP_COLS = N * G;
   constexpr int C = G < 8 ? 8 / G : 1;  // choices of a lane that are read ahead
   __shared__ float s_p[BAL_THREADS / 32][WARP_COLS];
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   }
   wait_for_previous();
   launch_dependents();
-  // n in two parts, whose sums over at most 300 chunks fp32 holds exactly
+  // n in two parts, whose sums over at most 450 chunks fp32 holds exactly
   float nz[3] = {0.0f, 0.0f, 0.0f};
   for (int i = first + static_cast<int>(threadIdx.x); i <= last; i += 256) {
     const int c = a.part_n[i];
@@ -387,7 +396,7 @@ __global__ void __launch_bounds__(256) balance_join_kernel(const BalanceArgs a) 
   float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   int4 c = make_int4(0, 0, 0, 0);
   const bool vec = a.E % 4 == 0;
-  constexpr int AHEAD = 4;  // parts that are read together: the 300 of a sequence are ten a thread
+  constexpr int AHEAD = 4;  // parts that are read together: the 300 of one sequence are ten a thread
                             // (16385 x 256 one by one: 15.6 us, so 12.6 us)
   for (int j0 = first + grp; j0 <= last; j0 += 32 * AHEAD) {
     float4 q[AHEAD];
@@ -596,13 +605,14 @@ static int balance_lanes(int E) {
   return g;
 }
 
-// Tokens of a forward block: the two blocks that an SM holds (of 150 SMs whatever the GPU, as
-// the workspace's size goes by it: one wave), each group with at least one token; up to four a group
+// Tokens of a forward block: the blocks that 150 SMs hold (whatever the GPU, as the
+// workspace's size goes by it: one wave), each group with at least one token; up to four a group
 // stay in one block, whose results then need no join.
 static int balance_chunk(const moe_balance_dims& m) {
   const int groups = BAL_THREADS / balance_lanes(m.E);
   if (m.T <= 4 * groups) return 4 * groups;
-  const long long per = (static_cast<long long>(m.T) + 299) / 300;
+  const int blocks = 150 * balance_fwd_blocks(m.E % 4 == 0 ? 4 : 1, balance_lanes(m.E), m.E);
+  const long long per = (static_cast<long long>(m.T) + blocks - 1) / blocks;
   return static_cast<int>((per + groups - 1) / groups * groups);
 }
 static long long balance_chunks(const moe_balance_dims& m) {

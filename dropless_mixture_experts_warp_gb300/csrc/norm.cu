@@ -11,9 +11,9 @@
 // is computed.  The weights are shared by the block's rows: as fp32, offsets added and
 // gates activated, in shared memory where that has room beside two rows a group.
 //
-// Measured (GB300, bf16 stream, 16384 x 7168): the norm 73 us, the merge with everything 141 us
-// (6.68 TB/s, the rate of a copy), its gradients 222 us (6.34 TB/s); fp32 stream, 16384 x 4096:
-// merge 122 us, gradients 213 us (5.67 TB/s).
+// Measured (GB300, bf16 stream, 16384 x 7168): the norm 72 us, the merge with everything 138 us
+// (6.8 TB/s, the rate of a copy), its gradients 222 us (6.35 TB/s); fp32 stream, 16384 x 4096:
+// merge 120 us, gradients 214 us (5.65 TB/s).
 //
 // KNOWN variants know at compile time what a call usually has: every weight, the gradient of
 // the stream, the kind of gate GATE (asked element by element at run time these choices took
