@@ -35,6 +35,10 @@ inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : 
 // 8121 x 2048: 20.7 to 18.6 us, calls one after another).  A kernel waits before it touches
 // memory and only then lets the next one come up, so that a kernel that has begun knows that
 // everything before its predecessor is done.  (The step of fp32 moments lets nothing come up.)
+// The exception is the balance loss's join: it reads the sequence offsets, which its
+// predecessor, the loss's own first kernel, only reads too, and may set the status before it
+// waits.  What a predecessor writes must not be reached through __restrict__ pointers or
+// read-only loads: both say that memory does not change while a kernel is resident.
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... Params, typename... Args>

@@ -688,11 +688,9 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
 
 // Column sums of the workers' partial sums, 32 columns a block: 32 threads a column, each
 // adding every 32nd worker in order, then the 32 in order.  blockIdx.y picks the sum; a NULL
-// output is skipped.
+// output is skipped.  (It is resident while `part` is still being written: plain pointers.)
 constexpr int REDUCE_COLS = 32;
-__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* __restrict__ part, int workers, int d,
-                                                          float* __restrict__ o0, float* __restrict__ o1,
-                                                          float* __restrict__ o2) {
+__global__ void __launch_bounds__(256) norm_reduce_kernel(const float* part, int workers, int d, float* o0, float* o1, float* o2) {
   __shared__ float buf[32][REDUCE_COLS + 1];
   float* out = blockIdx.y == 0 ? o0 : blockIdx.y == 1 ? o1 : o2;
   wait_for_previous();
