@@ -299,7 +299,8 @@ __device__ __forceinline__ Block8 fetch8(const AdamTensor& t, long long i) {
 // What is the same for a unit's elements.
 struct Unit8 {
   float gs, b1, b2, c1, c2;    // m = b1 m + c1 g, v = b2 v + c2 g^2
-  float one, root_bc2, eps, rate, decay;
+  float one, root_bc2, eps;
+  float rate, decay;           // w += rate m / (root_bc2 sqrt(v) + eps) + decay w
   uint32_t key;
 };
 
@@ -339,7 +340,8 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
       const float2 r = make_float2(sqrt_fast(av[j].x), sqrt_fast(av[j].y));
       const float2 den = unpair(fma2(pair(r.x, r.y), pair(c.root_bc2, c.root_bc2), pair(c.eps, c.eps)));
       const f32x2 update = mul2(m[h][j], pair(rcp_fast(den.x), rcp_fast(den.y)));
-      w[h][j] = fma2(update, pair(c.rate, c.rate), mul2(w[h][j], pair(c.decay, c.decay)));
+      // the change first: a factor 1 - lr weight_decay keeps of a small decay what 1 + 2^-24 shows of it
+      w[h][j] = add2(w[h][j], fma2(update, pair(c.rate, c.rate), mul2(w[h][j], pair(c.decay, c.decay))));
       root[h][j] = pair(sqrt_fast(r.x), sqrt_fast(r.y));
     }
     ms[h] = absmax3_nan(absmax3_nan(am[0].x, am[0].y, am[1].x), am[1].y, am[1].y);
@@ -526,7 +528,7 @@ __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_8) adamw8_kernel(const __
     const AdamTensor t = a.t[at];  // in registers: read from the arguments, 22 more loads a pair
     const long long start = (unit - t.first) * a.chunk;
     const long long stop = min(t.n, start + a.chunk);
-    c.decay = 1.0f - sc.lr * t.weight_decay;
+    c.decay = -sc.lr * t.weight_decay;
     // a unit does not cross a multiple of 2^32
     c.key = adam_mix(base + static_cast<uint32_t>(a.base + at) * 0x6A09E667u + static_cast<uint32_t>(start >> 32) * 0xBB67AE85u);
     if (t.grad_bf16) adam8_unit<true>(c, t, start, stop, ring);

@@ -286,3 +286,27 @@ def test_8_bit_at_far_scales(scale):
         near = (margin <= (24 * U * abs(x) + 2.0 ** -149) / largest / width) | ((x != 0) & (abs(x) < 2.0 ** -149))
         assert np.array_equal(got[~near], want[~near]) and np.all(abs(got - want) <= 1)
         assert near.mean() < 0.2
+
+
+@pytest.mark.parametrize("wd", [0.1, 0.02])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_small_decay_is_not_lost_in_rounding(bits, wd):
+    """lr * wd of 1e-7 and 2e-8, near and below the distance of 1 from its neighbours: the drift of the mean weight
+    against the same steps without decay.  Weights lie in [1, 2), so a step rounds each by at most 2^-24, as good as
+    uniformly (the updates spread over several units): two runs of K steps leave the mean of n differences a deviation
+    of 2^-23 / sqrt(12) * sqrt(2 K / n), of which 6 are allowed.  The weights themselves move by less than K lr."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    n, lr, warm, K = 1 << 18, 1e-6, 5, 50
+    start = 1 + torch.rand(n, device="cuda", generator=torch.Generator("cuda").manual_seed(5))
+    ends = []
+    for decay in (wd, 0.0):
+        rng = torch.Generator("cuda").manual_seed(6)
+        w, g = start.clone(), torch.zeros(n, device="cuda")
+        p = optim.plan([w], [g], bits=bits, weight_decay=decay)
+        for t in range(1, warm + K + 1):       # the first steps only fill the moments (step 1 moves by lr exactly)
+            g.normal_(generator=rng).mul_(1e-3)
+            optim.step(p, lr=lr if t > warm else 0.0, step=t, beta1=0.5, beta2=0.95, seed=9)
+        ends.append(w.double())
+    drift = float((ends[0] - ends[1]).mean())
+    want = -K * lr * wd * float(start.double().mean())
+    assert abs(drift - want) <= 6 * 2.0 ** -23 / 12 ** 0.5 * (2 * K / n) ** 0.5 + abs(want) * 2 * K * lr
