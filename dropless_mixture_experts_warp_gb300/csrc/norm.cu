@@ -70,7 +70,19 @@ struct NormPlan {
   bool late_y;            // of stages rows instead, for two stages (the LATE form)
 };
 
-__device__ __forceinline__ float gate_act(float g, int sigmoid) { return sigmoid ? 1.0f / (1.0f + __expf(-g)) : g; }
+// The activated gate and its slope.  With e = exp(-|g|) the sigmoid is 1 / (1 + e) or
+// e / (1 + e) and its slope e / (1 + e)^2, all within a few units of fp32.  (As a (1 - a) the
+// slope would be 17 % off at g = 15 and 0 from 17 on, where a rounds to 1.)
+__device__ __forceinline__ float gate_act(float g, int sigmoid) {
+  if (!sigmoid) return g;
+  const float e = expf(-fabsf(g));
+  return (g < 0.0f ? e : 1.0f) / (1.0f + e);
+}
+__device__ __forceinline__ float gate_slope(float g, int sigmoid) {
+  if (!sigmoid) return 1.0f;
+  const float e = expf(-fabsf(g));
+  return e / ((1.0f + e) * (1.0f + e));
+}
 
 // Until at most n (0 .. 3) of the thread's groups of copies are under way.
 __device__ __forceinline__ void copy_wait_but(int n) {
@@ -131,8 +143,7 @@ __device__ __forceinline__ void fill(f32x2 (&v)[U / 2], float x) {
 // What a weight array holds for the kernels: weight + offset, the activated gate, its slope.
 __device__ __forceinline__ float weight_value(const NormArgs& a, int kind, float w) {
   if (kind == W_NEXT || kind == W_POST) return w + a.offset;
-  const float g = gate_act(w, a.gate_sigmoid);
-  return kind == W_GATE ? g : g * (1.0f - g);
+  return kind == W_GATE ? gate_act(w, a.gate_sigmoid) : gate_slope(w, a.gate_sigmoid);
 }
 template <int U>
 __device__ __forceinline__ void raw_weights(const NormArgs& a, int kind, int u, f32x2 (&v)[U / 2]) {
@@ -530,10 +541,11 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
     const float r = next ? inv_rms(hh, inv_d, a.eps) : 0.0f;
     const float c = -r * r * nh * inv_d;
     const float ry = post ? inv_rms(yy, inv_d, a.eps) : 1.0f;
-    float tg = a.beta, tact = 1.0f;  // beta * a for the row
+    float tg = a.beta, tslope = 1.0f;  // beta * a for the row
     if (token) {
-      tact = gate_act(static_cast<const float*>(a.gate)[row], a.gate_sigmoid);
-      tg *= tact;
+      const float gate = static_cast<const float*>(a.gate)[row];
+      tg *= gate_act(gate, a.gate_sigmoid);
+      tslope = gate_slope(gate, a.gate_sigmoid);
     }
     f32x2 sqy = zero, sdz = zero;
     f32x2 q[UPT][U / 2];
@@ -616,7 +628,7 @@ __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(s
     if (MERGE) {
       yy = s[MERGE ? 2 : 0];
       if (token && tid == 0)
-        a.dgate_rows[row] = a.beta * s[sizeof(s) / 4 - 1] * (a.gate_sigmoid ? tact * (1.0f - tact) : 1.0f);
+        a.dgate_rows[row] = a.beta * s[sizeof(s) / 4 - 1] * tslope;
       if (post) {
         const float cy = -ry * ry * s[MERGE ? 3 : 0] * inv_d;
         const f32x2 cy2 = pair(cy, cy), ry2 = pair(ry, ry);

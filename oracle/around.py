@@ -17,7 +17,7 @@ def _act(g, sigmoid):
     if not sigmoid:
         return g, np.ones_like(g)
     a = 1.0 / (1.0 + np.exp(-g))
-    return a, a * (1.0 - a)
+    return a, a / (1.0 + np.exp(g))    # 1 - a without the cancellation
 
 
 def rms(h, eps):

@@ -278,3 +278,25 @@ def test_inputs_written_just_before_and_on_another_stream(captured):
             g.replay()
         torch.cuda.synchronize()
     assert torch.equal(x, want) and torch.equal(dh, want_dh) and torch.equal(dw, want_dw)
+
+
+@pytest.mark.parametrize("T,d", [(33, 512), (7, 7168), (40, 520), (6, 8200)])
+@pytest.mark.parametrize("stream", ["bf16", "fp32"])
+@pytest.mark.parametrize("gate", ["channel", "token"])
+@pytest.mark.parametrize("post", [True, False])
+def test_gradients_of_gates_far_open_and_far_shut(T, d, stream, gate, post):
+    """The sigmoid's slope where the gate is as good as 1 or 0: e^-|g|, which 1 - sigmoid(g) does not hold in fp32."""
+    from dropless_mixture_experts_warp_gb300 import block
+    b = block.allocate(block.dims_of(T, d, stream=stream, gate=gate, gate_act="sigmoid"))
+    i = inputs(T, d, stream, "fp32", 4)
+    far = np.random.default_rng(T + d).choice([-30.0, -16.0, -0.5, 15.0, 16.0, 17.5, 30.0], d if gate == "channel" else T)
+    g, g64 = dev(far, "fp32")
+    w_post = i["w_post"] if post else (None, None)
+    opt = dict(eps=1e-6, kind=gate, sigmoid=True)
+    ref = oa.merge_fwd(i["h"][1], i["y"][1], w_post[1], g64, i["w"][1], **opt)
+    block.merge_forward(b, i["h"][0], i["y"][0], w_post=w_post[0], gate=g, w_next=i["w"][0])
+    check("h_out", b.h_out, ref["h_out"], stream, ROW)
+    ref = oa.merge_bwd(i["dh"][1], i["dx"][1], i["h"][1], i["y"][1], w_post[1], g64, i["w"][1], **opt)
+    block.merge_backward(b, i["dh"][0], i["dx"][0], i["h"][0], i["y"][0], w_post=w_post[0], gate=g, w_next=i["w"][0])
+    check("dy", b.dy, ref["dy"], "bf16", 3 * ROW)
+    check("dgate", b.dgate, ref["dgate"], "fp32", (d if gate == "token" else T) + 3 * ROW)
