@@ -359,11 +359,12 @@ __device__ __forceinline__ void step8(const Unit8& c, const AdamTensor& t, long 
   for (int h = 0; h < H; ++h) {
     if (ms[h] < 1.17549435e-38f) ms[h] = 0.0f;
     if (vs[h] < 1.17549435e-38f) vs[h] = 0.0f;
-    // what the codes are made of; scales whose inverses would leave fp32's range, and their
-    // moments, times 2^60
+    // what the codes are made of; scales whose inverses would leave fp32's normal numbers at
+    // either end, and their moments, times 2^60 or 2^-60
     float sm = ms[h], sv = vs[h];
-    if (fminf(sm, sv) < 0x1p-60f) {
-      const float fm = sm < 0x1p-60f ? 0x1p60f : 1.0f, fv = sv < 0x1p-60f ? 0x1p60f : 1.0f;
+    if (fminf(sm, sv) < 0x1p-60f || fmaxf(sm, sv) > 0x1p100f) {
+      auto nearer = [](float x) { return x < 0x1p-60f ? 0x1p60f : x > 0x1p100f ? 0x1p-60f : 1.0f; };
+      const float fm = nearer(sm), fv = nearer(sv);
       sm *= fm;
       sv *= fv;
 #pragma unroll

@@ -310,3 +310,28 @@ def test_small_decay_is_not_lost_in_rounding(bits, wd):
     drift = float((ends[0] - ends[1]).mean())
     want = -K * lr * wd * float(start.double().mean())
     assert abs(drift - want) <= 6 * 2.0 ** -23 / 12 ** 0.5 * (2 * K / n) ** 0.5 + abs(want) * 2 * K * lr
+
+
+def test_8_bit_at_scales_near_the_largest_number():
+    """Codes follow the definition where the inverse of a block's scale is below fp32's normal numbers."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    n = 1000
+    rng = np.random.default_rng(13)
+    w, g = torch.zeros(n, device="cuda"), cuda(rng.standard_normal(n) * 1e10)
+    ms, vs = cuda(rng.integers(-127, 128, n), torch.int8), cuda(rng.integers(1, 256, n), torch.uint8)
+    sm, sv = (cuda(3e38 * (0.5 + 0.5 * rng.random(-(-n // 128)))) for _ in range(2))
+    p = optim.plan([w], [g], bits=8, m=[ms], v=[vs], m_scale=[sm], v_scale=[sv])
+    old_m, old_v = oa.decode(f64(ms), f64(sm), 127, 2), oa.decode(f64(vs), f64(sv), 255, 4)
+    optim.step(p, step=3, seed=4, **HYPER)
+    m1, v1, mm, vm = check_step({"g64": f64(g)}, np.zeros(n), old_m, old_v, 0.0, 3, f64(w), None, None)
+    for x, maj, code, scales, u, top, power in ((m1, mm, ms, sm, 0, 127, 2), (v1, vm, vs, sv, 1, 255, 4)):
+        ref = oa.block_scales(x)
+        assert ref.min() > 2.0 ** 126                # the case is what it says
+        assert np.all(abs(f64(scales) - ref) <= 16 * U * oa.block_scales(maj))
+        want, margin = oa.encode(x, ref, oa.adamw_draws(4, 3, 0, n)[u], top, power)
+        got = code.cpu().numpy().astype(np.int64)
+        k = np.maximum(abs(want) - 1, 0)
+        width = ((k + 1) / top) ** power - (k / top) ** power
+        near = margin <= 24 * U * np.repeat(oa.block_scales(maj) / ref, 128)[:n] / width
+        assert np.array_equal(got[~near], want[~near]) and np.all(abs(got - want) <= 1)
+        assert near.mean() < 0.2
