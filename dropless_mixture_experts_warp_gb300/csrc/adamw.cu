@@ -5,11 +5,15 @@
 // rate of a copy), 8-bit states 1.95 ms (5.0 TB/s).
 #include "around.cuh"
 
+#include <cfloat>
 #include <cmath>
 
 namespace moe {
 
 constexpr int ADAM_BLOCK = 128;         // elements that share a scale: a warp's step, 4 a lane
+// The least eps with 8-bit states: they hold no v below fp32's smallest normal number, 2^-126,
+// but an m down to that, so an update may lack its root, which eps has to stand in for.
+constexpr float ADAM_MIN_EPS8 = 0x1p-63f;
 constexpr int ADAM_TENSORS = 96;        // tensors of one launch (their descriptors are its arguments)
 constexpr int ADAM_THREADS = 256;
 constexpr int BLOCKS_32 = 5, BLOCKS_8 = 2, BLOCKS_VALUES = 8;  // of a kernel on an SM
@@ -654,8 +658,10 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
   if (!hyper || count < 0 || (count > 0 && !tensors)) return MOE_ERR_INVALID_ARG;
   const moe_adamw_hyper& h = *hyper;
   if (h.bits != 32 && h.bits != 8) return MOE_ERR_INVALID_ARG;
-  if (!(h.lr >= 0.0) || !std::isfinite(h.lr) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
-      !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !(h.eps > 0.0) || !std::isfinite(h.eps))
+  // lr and eps as the kernels have them, in fp32
+  const float lr = static_cast<float>(h.lr), eps = static_cast<float>(h.eps);
+  if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.beta1 >= 0.0 && h.beta1 < 1.0) ||
+      !(h.beta2 >= 0.0 && h.beta2 < 1.0) || !(eps >= (h.bits == 8 ? ADAM_MIN_EPS8 : FLT_TRUE_MIN)) || !std::isfinite(eps))
     return MOE_ERR_INVALID_ARG;
   if (!control && h.step < 1) return MOE_ERR_INVALID_ARG;
   if (reinterpret_cast<uintptr_t>(control) % 4) return MOE_ERR_ALIGNMENT;
@@ -665,12 +671,12 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
     if (st != MOE_OK) return st;
   }
   AdamArgs a{};
-  a.lr = static_cast<float>(h.lr);
+  a.lr = lr;
   a.beta1 = static_cast<float>(h.beta1);
   a.beta2 = static_cast<float>(h.beta2);
   a.keep1 = static_cast<float>(1.0 - h.beta1);
   a.keep2 = static_cast<float>(1.0 - h.beta2);
-  a.eps = static_cast<float>(h.eps);
+  a.eps = eps;
   a.one = 1.0f;
   a.log_beta1 = static_cast<float>(std::log(h.beta1));
   a.log_beta2 = static_cast<float>(std::log(h.beta2));

@@ -92,7 +92,8 @@ def plan(weights, grads, copies=None, bits=32, weight_decay=0.0, m=None, v=None,
 
 def step(p: Plan, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, seed=0, control=None, stream=None):
     """Updates p's weights, copies and states.  seed: of the 8-bit states' draws.  control: a Control, whose values
-    on the device then take the place of `step` and scale lr and the gradients (for captured steps)."""
+    on the device then take the place of `step` and scale lr and the gradients (for captured steps).  eps: above 0
+    in fp32, and at least 2^-63 with 8-bit states."""
     p.check_device()
     h = p.hyper
     h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed = lr, beta1, beta2, eps, step, seed

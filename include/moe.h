@@ -669,7 +669,8 @@ moe_status moe_balance_bwd(const moe_balance_dims* dims, const float* logits, co
  *   u's low 16 bits draw m's code, its high 16 bits v's: with k the code below and
  *   x_k < x < x_{k+1} the block's shares, the upper one where (bits + 1/2) / 2^16 <
  *   (x - x_k) / (x_{k+1} - x_k).
- *   A scale below fp32's smallest normal number stores the block's moment as 0.
+ *   A scale below fp32's smallest normal number (2^-126) stores the block's moment as 0,
+ *   and a new v below it counts as 0 in the update: eps has to be at least its root, 2^-63.
  * Gradients that are not finite reach the state (of the whole block of 128 with bits =
  * 8): a caller that checks for them sets `skip`.
  */
@@ -696,7 +697,8 @@ typedef struct moe_adamw_control {
 } moe_adamw_control;
 
 typedef struct moe_adamw_hyper {
-  double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0 */
+  double lr, beta1, beta2, eps; /* lr >= 0, 0 <= beta < 1, eps > 0 (bits = 8: >= 2^-63); lr and
+                                 * eps are used, and checked, in fp32 */
   int32_t step;                 /* t, >= 1 (not used with a control) */
   uint32_t seed;                /* bits = 8 */
   int32_t bits;                 /* 32 or 8 */

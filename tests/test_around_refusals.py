@@ -170,3 +170,28 @@ def test_lists_of_tensors_are_checked_one_by_one(B):
                 [ts[0], ts[1].to("meta")]):
         with pytest.raises(ValueError):
             B.check_tensors(bad, torch.float32, shapes, cpu)
+
+
+def test_adamw_eps_and_lr_are_checked_as_the_kernels_have_them(B):
+    """In fp32: an eps that rounds to 0 there would make 0 / 0 of an element without a gradient, and with 8-bit states
+    one below the root of the smallest v that they hold would divide by next to nothing; lr must not become infinite."""
+
+    def step(bits, **hyper):
+        h = B.moe_adamw_hyper(**{**dict(lr=1e-3, beta1=0.9, beta2=0.99, eps=1e-8, step=1, seed=0, bits=bits), **hyper})
+        s = P if bits == 8 else None
+        t = (B.moe_adamw_tensor * 1)(B.moe_adamw_tensor(P, P, P, P, P, s, s, 100, 0.1, 0))
+        return status(B, "moe_adamw_step", h, t, 1, None)
+
+    for bits in (32, 8):
+        for eps in (1e-50, 2.0 ** -151, 1e39, float("inf"), float("nan"), -1e-8):
+            assert step(bits, eps=eps) == 1, (bits, eps)
+        for lr in (1e39, float("inf")):
+            assert step(bits, lr=lr) == 1, (bits, lr)
+    for eps in (1e-40, 1e-38, 1e-20, 2.0 ** -63 * (1 - 2.0 ** -20)):
+        assert step(8, eps=eps) == 1, eps
+    # what is still taken: no tensors, so that nothing is launched
+    before = B.moe_launch_count()
+    for bits, eps in ((32, 1e-40), (32, 1e-45), (8, 2.0 ** -63), (8, 1e-15)):
+        h = B.moe_adamw_hyper(lr=1e-3, beta1=0.9, beta2=0.99, eps=eps, step=1, seed=0, bits=bits)
+        B.moe_adamw_step(h, None, 0, None, stream=0)
+    assert B.moe_launch_count() == before
