@@ -9,6 +9,7 @@ Non-zero statuses raise :class:`MoeError`.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -177,14 +178,38 @@ def _ptr(x) -> Optional[int]:
     return x.data_ptr()
 
 
+@functools.lru_cache(maxsize=None)
+def _torch():
+    """torch, imported once something of it is needed (an import statement at every call costs 0.1 us)."""
+    import torch
+    return torch
+
+
+def _current_device() -> int:
+    return _torch()._C._cuda_getDevice()
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
         # the handle alone: a torch.cuda.Stream object for it costs 3 us a call
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+        return _torch()._C._cuda_getCurrentRawStream(_current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def check_device(device, stream=None):
+    """Raise ValueError unless `device` is the GPU that a call with `stream` (None: the current one) runs on, the
+    current device: a kernel would take the addresses of any other's memory for its own."""
+    index = device.index            # a tensor off the GPUs has none (the type's name alone costs 0.2 us)
+    if index is None and device.type != "cuda":
+        raise ValueError(f"runs on a GPU: the tensors are on {device}")
+    current = _current_device()
+    if index is not None and index != current:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{current}")
+    at = None if stream is None else getattr(stream, "device", None)
+    if at is not None and at.index != current:
+        raise ValueError(f"the stream is of {at}, the current device is cuda:{current}")
 
 
 def check_tensor(t, dtype, shape, device):

@@ -53,9 +53,11 @@ def allocate(dims: B.moe_norm_dims, device="cuda") -> Buffers:
                    workspace=e(B.moe_norm_workspace_size(dims), dt=torch.uint8))
 
 
-def _check(b: Buffers, stream=(), block=(), weights=(), gate=None):
-    """Rows of the stream, rows of the block and weights as the call's dims have them."""
+def _check(b: Buffers, on, stream=(), block=(), weights=(), gate=None):
+    """Rows of the residual stream, rows of the block and weights as the call's dims have them, on the device that a
+    call with the CUDA stream `on` runs on."""
     dm, dev = b.dims, b.x.device
+    B.check_device(dev, on)
     rows, n = (dm.T, dm.d), (dm.d,)
     for t in stream:
         B.check_tensor(t, _DTYPE[dm.stream_type], rows, dev)
@@ -72,21 +74,21 @@ def _check(b: Buffers, stream=(), block=(), weights=(), gate=None):
 
 def norm_forward(b: Buffers, h, w, stream=None):
     """-> b.x"""
-    _check(b, stream=(h,), weights=(w,))
+    _check(b, stream, stream=(h,), weights=(w,))
     B.moe_norm_fwd(b.dims, h, w, b.x, stream)
     return b.x
 
 
 def norm_backward(b: Buffers, dx, h, w, dh_add=None, stream=None):
     """-> b.dh (dh_add, the gradient that reaches h around the block, added to it) and b.dw."""
-    _check(b, stream=(h, dh_add), block=(dx,), weights=(w,))
+    _check(b, stream, stream=(h, dh_add), block=(dx,), weights=(w,))
     B.moe_norm_bwd(b.dims, dx, h, w, dh_add, b.dh, b.dw, b.workspace, stream)
     return b.dh
 
 
 def merge_forward(b: Buffers, h, y, w_post=None, gate=None, w_next=None, stream=None):
     """-> b.h_out, and b.x (the next block's input) where w_next is given."""
-    _check(b, stream=(h,), block=(y,), weights=(w_post, w_next), gate=gate)
+    _check(b, stream, stream=(h,), block=(y,), weights=(w_post, w_next), gate=gate)
     B.moe_merge_fwd(b.dims, h, y, w_post, gate, w_next, b.h_out, None if w_next is None else b.x, stream)
     return b.h_out
 
@@ -94,7 +96,7 @@ def merge_forward(b: Buffers, h, y, w_post=None, gate=None, w_next=None, stream=
 def merge_backward(b: Buffers, dh_out, dx_next, h_out, y, w_post=None, gate=None, w_next=None, stream=None):
     """-> b.dh, b.dy and the gradients of what is given: b.dw_post, b.dgate, b.dw (of w_next).  dh_out (the
     gradient of h_out) may be None where w_next is given, dx_next (of b.x) is None where it is not."""
-    _check(b, stream=(dh_out, h_out), block=(dx_next, y), weights=(w_post, w_next), gate=gate)
+    _check(b, stream, stream=(dh_out, h_out), block=(dx_next, y), weights=(w_post, w_next), gate=gate)
     B.moe_merge_bwd(b.dims, dh_out, dx_next, h_out, y, w_post, gate, w_next, b.dh, b.dy,
                     None if w_post is None else b.dw_post, b.dgate, None if w_next is None else b.dw, b.workspace,
                     stream)

@@ -37,9 +37,8 @@ class Plan:
     device: torch.device
     shapes: List[torch.Size]    # of the weights
 
-    def check_device(self):
-        if self.device.type != "cuda":
-            raise ValueError(f"AdamW runs on a GPU: the plan's tensors are on {self.device}")
+    def check_device(self, stream=None):
+        B.check_device(self.device, stream)
 
 
 def plan(weights, grads, copies=None, bits=32, weight_decay=0.0, m=None, v=None, m_scale=None, v_scale=None) -> Plan:
@@ -94,7 +93,9 @@ def step(p: Plan, lr, step, beta1=0.9, beta2=0.95, eps=1e-8, seed=0, control=Non
     """Updates p's weights, copies and states.  seed: of the 8-bit states' draws.  control: a Control, whose values
     on the device then take the place of `step` and scale lr and the gradients (for captured steps).  eps: above 0
     in fp32, and at least 2^-63 with 8-bit states."""
-    p.check_device()
+    p.check_device(stream)
+    if control is not None and p.weights:
+        B.check_tensor(control.raw, torch.int32, (4,), p.device)
     h = p.hyper
     h.lr, h.beta1, h.beta2, h.eps, h.step, h.seed = lr, beta1, beta2, eps, step, seed
     B.moe_adamw_step(h, p.table, len(p.weights), None if control is None else control.raw, stream)
@@ -116,7 +117,7 @@ def values(p: Plan, m_out=None, v_out=None, dtype=torch.bfloat16, stream=None):
     """The moments that p's 8-bit states stand for, as lists of tensors (new ones of `dtype`, or the given)."""
     if p.bits != 8:
         raise ValueError("values: the states are held in fp32 as they are")
-    p.check_device()
+    p.check_device(stream)
     new = lambda: [torch.empty(s, dtype=dtype, device=p.device) for s in p.shapes]  # noqa: E731
     m_out, v_out = new() if m_out is None else list(m_out), new() if v_out is None else list(v_out)
     kind = m_out[0].dtype if m_out else dtype

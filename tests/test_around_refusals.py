@@ -195,3 +195,45 @@ def test_adamw_eps_and_lr_are_checked_as_the_kernels_have_them(B):
         h = B.moe_adamw_hyper(lr=1e-3, beta1=0.9, beta2=0.99, eps=eps, step=1, seed=0, bits=bits)
         B.moe_adamw_step(h, None, 0, None, stream=0)
     assert B.moe_launch_count() == before
+
+
+def test_buffers_on_another_device_are_refused(B, monkeypatch):
+    """Buffers on the CPU, or on a GPU that is not the current one (here told by a stand-in for its query)."""
+    import dataclasses
+    import types
+
+    import torch
+    from dropless_mixture_experts_warp_gb300 import balance, block, optim
+    bf = torch.bfloat16
+    n = block.allocate(block.dims_of(4, 64), device="cpu")
+    h, w = torch.zeros(4, 64, dtype=bf), torch.ones(64)
+    o = balance.allocate(4, 8, 2, device="cpu")
+    l, idx = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    far = types.SimpleNamespace(device=torch.device("cuda:1"))      # of a tensor its device alone is looked at
+    p = optim.plan([torch.zeros(8)], [torch.zeros(8)], bits=8)
+
+    def calls(n, o, p, **kw):
+        return (lambda: block.norm_forward(n, h, w, **kw), lambda: block.norm_backward(n, h, h, w, **kw),
+                lambda: block.merge_forward(n, h, h, w_next=w, **kw), lambda: block.merge_backward(n, h, h, h, h, w_next=w, **kw),
+                lambda: balance.forward(o, l, idx, **kw), lambda: balance.backward(o, l, l.clone(), **kw),
+                lambda: optim.step(p, lr=1e-3, step=1, **kw), lambda: optim.values(p, **kw))
+
+    before = B.moe_launch_count()
+    for call in calls(n, o, p, stream=0):
+        with pytest.raises(ValueError, match="runs on a GPU"):
+            call()
+    monkeypatch.setattr(B, "_current_device", lambda: 0)
+    away = dataclasses.replace(p, device=torch.device("cuda:1"))
+    for call in calls(dataclasses.replace(n, x=far), dataclasses.replace(o, losses=far), away, stream=0):
+        with pytest.raises(ValueError, match="current device is cuda:0"):
+            call()
+    B.check_device(torch.device("cuda:0"), 0)
+    here = types.SimpleNamespace(device=torch.device("cuda:0"), cuda_stream=0)
+    B.check_device(torch.device("cuda:0"), here)
+    with pytest.raises(ValueError, match="stream"):
+        B.check_device(torch.device("cuda:0"), types.SimpleNamespace(device=torch.device("cuda:1"), cuda_stream=0))
+    # a step's control elsewhere than its tensors
+    near = dataclasses.replace(p, device=torch.device("cuda:0"))
+    with pytest.raises(ValueError, match="expected a contiguous"):
+        optim.step(near, lr=1e-3, step=1, control=optim.Control(device="cpu"), stream=0)
+    assert B.moe_launch_count() == before
