@@ -237,3 +237,25 @@ def test_buffers_on_another_device_are_refused(B, monkeypatch):
     with pytest.raises(ValueError, match="expected a contiguous"):
         optim.step(near, lr=1e-3, step=1, control=optim.Control(device="cpu"), stream=0)
     assert B.moe_launch_count() == before
+
+
+def test_the_balance_gradient_gets_the_forwards_coefficients(B, monkeypatch):
+    """The dims that reach the entry points, without a GPU: both calls replaced."""
+    import torch
+    from dropless_mixture_experts_warp_gb300 import balance
+    seen = []
+    note = lambda dims, *a: seen.append((dims.coef, dims.z_coef))  # noqa: E731
+    monkeypatch.setattr(B, "moe_balance_fwd", note)
+    monkeypatch.setattr(B, "moe_balance_bwd", note)
+    monkeypatch.setattr(B, "check_device", lambda *a: None)
+    o = balance.allocate(4, 8, 2, device="cpu")
+    l, idx = torch.zeros(4, 8), torch.zeros(4, 2, dtype=torch.int32)
+    balance.backward(o, l, l.clone())
+    balance.forward(o, l, idx, coef=0.5, z_coef=0.25)
+    balance.backward(o, l, l.clone())
+    balance.backward(o, l, l.clone(), coef=2.0)
+    balance.backward(o, l, l.clone(), z_coef=0.0)
+    balance.backward(o, l, l.clone())
+    balance.forward(o, l, idx)
+    balance.backward(o, l, l.clone())
+    assert seen == [(1.0, 0.0), (0.5, 0.25), (0.5, 0.25), (2.0, 0.25), (0.5, 0.0), (0.5, 0.25), (1.0, 0.0), (1.0, 0.0)]

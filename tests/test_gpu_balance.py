@@ -211,3 +211,27 @@ def test_many_tokens(T, E, k, S, masked, score):
 def test_each_number_of_lanes(T, E, k, S, masked, score):
     """Widths that are no multiple of four at each group size, and more choices than a group reads ahead."""
     run(*case(T, E, k, S, masked, 1), score, k)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_the_gradient_takes_the_forwards_coefficients(score):
+    """backward() without coefficients is the gradient of the losses that forward() gave; others hold for one call."""
+    from dropless_mixture_experts_warp_gb300 import balance
+    l, idx, offsets, mask = case(300, 24, 3, 4, True, 2)
+    b = balance.allocate(300, 24, 3, score=score, sequences=4)
+    dl, di, do, dm = cuda(l, idx, offsets, mask)
+    at = dict(seq_offsets=do, mask=dm)
+    balance.forward(b, dl, di, coef=COEF, z_coef=Z, **at)
+    ref = oa.balance_fwd(l.astype(np.float64), idx, offsets, mask, 3, score, COEF, Z)
+
+    def bound(wanted_coef, wanted_z, **given):
+        d, m = oa.balance_bwd(l.astype(np.float64), offsets, mask, ref["counts"], ref["seq_tokens"], 3, score,
+                              wanted_coef, wanted_z)
+        out = balance.backward(b, dl, torch.zeros(300, 24, device="cuda"), accumulate=False, **at, **given)
+        check(str(given), out, (d, m), "fp32", 2 * ROW)
+
+    bound(COEF, Z)
+    bound(2.0, Z, coef=2.0)
+    bound(COEF, 0.0, z_coef=0.0)
+    bound(3.0, 0.125, coef=3.0, z_coef=0.125)
+    bound(COEF, Z)
