@@ -175,7 +175,12 @@ def lib() -> ctypes.CDLL:
 def _ptr(x) -> Optional[int]:
     if x is None or x.__class__ is int:
         return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):      # last: asked of every tensor it costs a call up to 0.4 us
+            return x
+        raise
 
 
 @functools.lru_cache(maxsize=None)

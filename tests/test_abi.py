@@ -104,3 +104,20 @@ def test_grouped_routing_and_mxfp8_argument_checks(lib):
     # codes (1 byte) and scales (1/32) of both weights in both orientations
     assert B.moe_mx_weights_size(ok) >= 2 * 3 * 8 * 128 * 128 * (1 + 1 / 32)
     assert B.moe_launch_count() == before
+
+
+def test_addresses_may_be_of_a_class_of_their_own(lib):
+    """Any int is an address: a subclass is passed on as one (here to a refusal of its alignment)."""
+    from dropless_mixture_experts_warp_gb300 import binding as B
+
+    class Address(int):
+        pass
+
+    dims = B.make_dims(256, 128, 64, 8, 2)
+    before = B.moe_launch_count()
+    with pytest.raises(B.MoeError) as e:
+        B.moe_permute(dims, Address(18), *[Address(16)] * 10, stream=Address(0))
+    assert e.value.status == 3
+    with pytest.raises(B.MoeError) as e:
+        B.moe_norm_fwd(B.make_norm_dims(4, 64), Address(24), Address(16), Address(16), stream=0)
+    assert e.value.status == 3 and B.moe_launch_count() == before
