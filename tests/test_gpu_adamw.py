@@ -335,3 +335,76 @@ def test_8_bit_at_scales_near_the_largest_number():
         near = margin <= 24 * U * np.repeat(oa.block_scales(maj) / ref, 128)[:n] / width
         assert np.array_equal(got[~near], want[~near]) and np.all(abs(got - want) <= 1)
         assert near.mean() < 0.2
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("bits", [32, 8])
+def test_gradients_written_just_before_and_on_another_stream(bits, captured):
+    """The step comes up while what precedes it runs: gradients and control values that a slow kernel or another
+    stream's copies write count all the same, and what follows may overwrite them."""
+    from dropless_mixture_experts_warp_gb300 import optim
+    n, wd = 300_001, 0.1
+    t = tensors([n], 9)[0]
+    first, second = cuda(t["g"]), cuda(t["m"])
+
+    def fresh():
+        w, g = cuda(t["w"]), torch.full((n,), 3.0, device="cuda")
+        return optim.plan([w], [g], copies=[torch.zeros_like(w, dtype=torch.bfloat16)], bits=bits, weight_decay=wd), optim.Control()
+
+    state = lambda p: p.weights + p.copies + p.m + p.v + ((p.m_scale + p.v_scale) if bits == 8 else [])  # noqa: E731
+    p, c = fresh()
+    for step, g in ((1, first), (2, second)):
+        p.grads[0].copy_(g)
+        c.step.fill_(step)
+        torch.cuda.synchronize()
+        optim.step(p, step=0, seed=5, control=c, **HYPER)
+        torch.cuda.synchronize()
+    want = [x.clone() for x in state(p)]
+    if bits == 8:
+        want += [x.clone() for x in sum(optim.values(p), [])]
+    p, c = fresh()
+    start = [x.clone() for x in state(p)]
+    got = [torch.zeros_like(x) for x in want]
+    values = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    side = torch.cuda.Stream()
+
+    def fill(step, g):
+        torch.cuda._sleep(200_000)
+        p.grads[0].copy_(g)
+        c.step.fill_(step)
+
+    def work():
+        here = torch.cuda.current_stream()
+        for x, y in zip(state(p), start):
+            x.copy_(y)
+        fill(1, first)
+        optim.step(p, step=0, seed=5, control=c, **HYPER)
+        p.grads[0].fill_(3.0)
+        c.step.fill_(9)
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            fill(2, second)
+        here.wait_stream(side)
+        optim.step(p, step=0, seed=5, control=c, **HYPER)
+        if bits == 8:
+            optim.values(p, values[:1], values[1:])
+        p.grads[0].fill_(3.0)
+        for x, y in zip(got, state(p) + values):
+            x.copy_(y)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    s.synchronize()
+    if captured:
+        for x in got:
+            x.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            work()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))

@@ -235,3 +235,65 @@ def test_the_gradient_takes_the_forwards_coefficients(score):
     bound(COEF, 0.0, z_coef=0.0)
     bound(3.0, 0.125, coef=3.0, z_coef=0.125)
     bound(COEF, Z)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_inputs_written_just_before_and_on_another_stream(captured):
+    """The kernels come up while what precedes them runs, and the forward's second one reads the offsets before it
+    waits: logits, choices, offsets and mask written by a slow kernel or a copy, of the call's stream or of another
+    that it waits for, count all the same, and what follows may overwrite them."""
+    from dropless_mixture_experts_warp_gb300 import balance
+    T, E, k, S = 6000, 64, 6, 5
+    l, idx, offsets, mask = cuda(*case(T, E, k, S, True, 3))
+    b = balance.allocate(T, E, k, sequences=S)
+    outs = lambda: [b.losses, b.counts, b.prob_mean, b.seq_tokens]  # noqa: E731
+    balance.forward(b, l, idx, seq_offsets=offsets, mask=mask, coef=COEF, z_coef=Z)
+    want = [t.clone() for t in outs()]
+    want.append(balance.backward(b, l, torch.zeros_like(l), seq_offsets=offsets, mask=mask).clone())
+    balance.check(b)
+    # what stands in the arrays before: other numbers, all of them in range
+    spare = [torch.zeros_like(l), torch.zeros_like(idx), torch.linspace(0, T, S + 1, device="cuda").int(), torch.ones_like(mask)]
+    src, got = [t.clone() for t in spare], [torch.zeros_like(t) for t in want]
+    side = torch.cuda.Stream()
+
+    def fill():
+        torch.cuda._sleep(200_000)
+        for dst, t in zip(src, (l, idx, offsets, mask)):
+            dst.copy_(t)
+
+    def spoil():
+        for dst, t in zip(src, spare):
+            dst.copy_(t)
+
+    def work():
+        here = torch.cuda.current_stream()
+        d, at = got[-1], dict(seq_offsets=src[2], mask=src[3])
+        fill()
+        balance.forward(b, src[0], src[1], coef=COEF, z_coef=Z, **at)
+        spoil()
+        for t, o in zip(got, outs()):
+            t.copy_(o)
+        d.zero_()
+        side.wait_stream(here)
+        with torch.cuda.stream(side):
+            fill()
+        here.wait_stream(side)
+        balance.backward(b, src[0], d, **at)
+        spoil()
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        work()
+    s.synchronize()
+    if captured:
+        for t in got:
+            t.zero_()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            work()
+        torch.cuda.synchronize()
+        for _ in range(3):
+            g.replay()
+        torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
