@@ -98,11 +98,6 @@ __device__ __forceinline__ float sqrt_fast(float x) {
   asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 // 0xFF in the bytes of the four that are negative.
 __device__ __forceinline__ uint32_t sign_bytes(float a, float b, float c, float d) {
   uint32_t lo, hi;

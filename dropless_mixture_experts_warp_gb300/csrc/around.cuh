@@ -104,6 +104,17 @@ __device__ __forceinline__ f32x2 fma2_down(f32x2 a, f32x2 b, f32x2 c) {
   return r;
 }
 
+__device__ __forceinline__ float sum_pair(f32x2 v) {
+  const float2 f = unpair(v);
+  return f.x + f.y;
+}
+// 1 / x within a unit; 0 where that is below fp32's normal numbers, infinite where x is.
+__device__ __forceinline__ float rcp_fast(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Eight consecutive elements, rounded once from fp32.
 __device__ __forceinline__ void store8(moe_bf16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =

@@ -4,8 +4,11 @@
 // A token's E logits lie over the G lanes of a group, PLV vectors of VEC a lane (16 logits a
 // lane up to 512 experts: a token's sums then take few shuffles a logit, and a warp has
 // several tokens under way; 30001 x 131 over all 32 lanes: 29 us, over 16: 16 us).
-// Exponentials are 2^x of the scaled argument, which the maximum keeps at or below 0: their
-// relative error is at most |l - max| 2^-24 + 2^-22.
+// Exponentials are 2^x of the scaled argument; its difference, its product and log2(e) are each
+// rounded, so their relative error is at most |l - c| 2^-22.8 + 2^-22.  Softmax: c is the row's
+// maximum, and the arguments lie at or below 0.  Sigmoid scores: e^(c - l) with c the smaller
+// of the maximum and 0; in a row without a positive logit the arguments lie at or above 0, and
+// one that overflows makes the share 0.
 //
 // Measured (GB300, in a graph): losses of 393215 x 128, 41 us (5.2 TB/s), of 16384 x 256 13 us
 // (bound by the chain of dependent reads through two kernels); gradients 10.5 us for the
@@ -101,11 +104,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-__device__ __forceinline__ float rcp_fast(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // A lane's logits (or other [T][E] values) of one token, in pairs; `fill` where the row ends,
 // and everywhere where `there` is false.
@@ -133,10 +131,6 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
-}
-__device__ __forceinline__ float sum_pair(f32x2 v) {
-  const float2 f = unpair(v);
-  return f.x + f.y;
 }
 
 // The row's largest logit.

@@ -225,7 +225,7 @@ __device__ __forceinline__ float lane_sums(const float* s, int lane) {
   return v;
 }
 
-// Sums of N values (at most 8) over the threads of a group, in a fixed order; every thread
+// Sums of N values (at most SUMS_MAX) over the threads of a group, in a fixed order; every thread
 // gets them.  Two buffers taken in turn need one barrier a sum: whoever writes a buffer
 // again has passed the barrier of the other, which its readers reach after reading.
 constexpr int SUMS_MAX = 5;
@@ -260,6 +260,7 @@ struct GroupSums {
   }
   template <int N>
   __device__ __forceinline__ void operator()(float (&s)[N]) {
+    static_assert(N <= SUMS_MAX, "more sums than the buffers hold");
     constexpr int A = N < 4 ? N : 4, B = N - A;
     if (tpr == 32) {
       warp_only<A>(s);
@@ -278,11 +279,6 @@ struct GroupSums {
 
 // 1 / sqrt(mean + eps) of a sum of squares; within 2 units.
 __device__ __forceinline__ float inv_rms(float sum, float inv_d, float eps) { return rsqrtf(fmaf(sum, inv_d, eps)); }
-
-__device__ __forceinline__ float sum_pair(f32x2 v) {
-  const float2 f = unpair(v);
-  return f.x + f.y;
-}
 
 // MERGE: h_out and, with w_next, its norm; else the norm of h.  Two rows are under way in a
 // group: the sum that the next row's first norm needs (of y^2, or of h^2) is added up
