@@ -6,7 +6,8 @@
 
 PyTorch only allocates; every step runs in libmoe.so's kernels (moe_norm_*, moe_merge_* of
 include/moe.h, where the formulas are).  One `Buffers` serves one norm or merge of a block;
-its outputs are overwritten by the next call.
+its outputs are overwritten by the next call.  It holds the outputs of either direction of
+both: 16384 x 7168 bf16 take 0.95 GB, of which a norm's forward writes a quarter.
 """
 from __future__ import annotations
 

@@ -2,7 +2,7 @@
 // scale in blocks of 128 elements.  One pass over every array; a launch takes up to 96
 // tensors, whose descriptors are its arguments, in units of elements that the blocks deal
 // out.  604M elements (GB300, bf16 gradients and copy): fp32 states 2.55 ms (6.63 TB/s, the
-// rate of a copy), 8-bit states 1.95 ms (5.0 TB/s).
+// rate of a copy), 8-bit states 1.93 ms (5.05 TB/s).
 #include "around.cuh"
 
 #include <cfloat>
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(ADAM_THREADS, BLOCKS_32) adamw_kernel(const __
 // element about 88 issued instructions (at 16 bytes an element); one at a time with exact
 // roots and conversions it took 158 (3.1 ms for 604M elements), with arithmetic on pairs,
 // approximate roots and quotients of the update (within 2^-22; a v below fp32's normal numbers
-// has the root 0), bytes and floats by permutes 79 (1.95 ms), two thirds of the issue slots:
+// has the root 0), bytes and floats by permutes 79 (1.93 ms), two thirds of the issue slots:
 // four warps a scheduler, as many as two blocks in registers allow, wait for results of the
 // same few pipes.
 struct Block8 {

@@ -11,14 +11,16 @@
 // is computed.  The weights are shared by the block's rows: as fp32, offsets added and
 // gates activated, in shared memory where that has room beside two rows a group.
 //
-// Measured (GB300, bf16 stream, 16384 x 7168): the norm 72 us, the merge with everything 138 us
-// (6.8 TB/s, the rate of a copy), its gradients 222 us (6.35 TB/s); fp32 stream, 16384 x 4096:
-// merge 120 us, gradients 214 us (5.65 TB/s).
+// Measured (GB300, bf16 stream, 16384 x 7168): the norm 73 us, its gradients 142 us; the merge
+// with every weight and a channel gate 138 us (6.8 TB/s, the rate of a copy), its gradients
+// 222 us (6.35 TB/s); fp32 stream, 16384 x 4096: merge 120 us, gradients 215 us (5.65 TB/s).
 //
-// KNOWN variants know at compile time what a call usually has: every weight, the gradient of
-// the stream, the kind of gate GATE (asked element by element at run time these choices took
+// KNOWN variants know at compile time that a call has every weight and the gradient of the
+// stream, and the kind of gate GATE (asked element by element at run time these choices took
 // half of the instructions); EXACT ones also that the weights are in shared memory and that
-// the row's units fill the threads.
+// the row's units fill the threads.  A merge without an output norm, or of more than 8192
+// columns, asks at run time: 16384 x 7168 bf16 with the next norm alone 151 us, gradients
+// 364 us (a copy's rate would be 141 and 176).
 #include "around.cuh"
 
 #include <algorithm>
@@ -422,8 +424,8 @@ __global__ void __launch_bounds__(norm_fwd_threads(MERGE)) norm_fwd_kernel(const
 // waits are filled with the other row's work (355 us with two barriers a row, for 16384 x
 // 7168 bf16 with everything).  So y has one place more in the ring than the others; where
 // that leaves a weight no room (it would come from L2 for each row) LATE takes none more and
-// fetches y when the row that used its place is done (8192 x 7168 fp32 stream: 173 us, 219
-// without; 16384 x 8192 bf16: 287, 316 without).
+// fetches y when the row that used its place is done (8192 x 7168 fp32 stream without a gate:
+// 173 us, 219 without; 16384 x 8192 bf16 with a channel gate: 287, 316 without).
 // What a call lacks (weights, gate) takes its neutral value, a unit at a time.
 template <typename ST, int UPT, bool MERGE, bool KNOWN, bool EXACT, int GATE, bool LATE>
 __global__ void __launch_bounds__(norm_bwd_threads(UPT * 16 / static_cast<int>(sizeof(ST)))) norm_bwd_kernel(const NormArgs a, const NormPlan plan) {
@@ -852,7 +854,9 @@ template <typename ST, int COLS, bool MERGE>
 static cudaError_t launch_bwd_cols(const NormArgs& a, const NormPlan& p, cudaStream_t s) {
   if (COLS < 32 && norm_known(p, a, MERGE) && a.d_stream) {
     constexpr int C = COLS < 32 ? COLS : 16;
-    // (16384 x 7168 bf16: 221 us, 276 without; the fp32 stream's and the 8-column forms spill)
+    // (16384 x 7168 bf16 with a channel gate: 222 us, 276 without.  Not for an fp32 stream and 8
+    // columns, where it spills; the form for a sigmoid channel gate spills 28 bytes in the row loop:
+    // 369 us)
     constexpr bool EXACT = sizeof(ST) == 2 && C == 16, LATE = MERGE && C == 16;
     const bool exact = p.staged && a.d == p.tpr * COLS;
     if (p.late_y) return exact ? launch_bwd_known<ST, C, MERGE, EXACT, LATE>(a, p, s) : launch_bwd_known<ST, C, MERGE, false, LATE>(a, p, s);
