@@ -140,6 +140,11 @@ SIGNATURES = {
     "moe_mx4_quantize_cols": (ctypes.c_int32, [_P, _I, ctypes.c_int64, _I, _P, _P, _P, _P, _P]),
     "moe_grouped_mlp_fwd_mx": (ctypes.c_int32, [_D] + [_P] * 7),
     "moe_grouped_mlp_bwd_mx": (ctypes.c_int32, [_D] + [_P] * 11),
+    "moe_fp8_quantize": (ctypes.c_int32, [_P, ctypes.c_int64, _I] + [_P] * 7),
+    "moe_fp8_quantize_weights": (ctypes.c_int32, [_P, _I, _I, _I] + [_P] * 4),
+    "moe_fp8_gemm": (ctypes.c_int32, [_P, _P, ctypes.c_int64, _I, _P, _P, _I, _I, _I] + [_P] * 4),
+    "moe_fp8_wgrad": (ctypes.c_int32, [_P] * 4 + [ctypes.c_int64, _I, _I, _I] + [_P] * 4),
+    "moe_fp8_swiglu": (ctypes.c_int32, [_P, _P, ctypes.c_int64, _I] + [_P] * 4),
     "moe_norm_check_dims": (ctypes.c_int32, [_N]),
     "moe_norm_workspace_size": (ctypes.c_size_t, [_N]),
     "moe_norm_fwd": (ctypes.c_int32, [_N] + [_P] * 4),
@@ -512,6 +517,31 @@ def moe_shared_mlp_bwd_mx(dims, wq_s, mx_ws_s, gu_s, dy, dx_s, dw_gu_s, dw_d_s, 
 def moe_gemm_bf16_pair(A, B, C, M, N, K, a_layout, b_layout, dev_status, stream=None):
     return _call("moe_gemm_bf16_pair", _ptr(A), _ptr(B), _ptr(C), M, N, K, a_layout, b_layout,
                  _ptr(dev_status), _stream(stream))
+
+
+# ------------------------------------------------------------------ blocks of 128
+
+def moe_fp8_quantize(src, rows, C, row_map, nrows_dev, codes, scales, codes_t, scales_t, stream=None):
+    return _call("moe_fp8_quantize", _ptr(src), rows, C, _ptr(row_map), _ptr(nrows_dev), _ptr(codes), _ptr(scales),
+                 _ptr(codes_t), _ptr(scales_t), _stream(stream))
+
+
+def moe_fp8_quantize_weights(src, E, N, K, codes, codes_t, scales, stream=None):
+    return _call("moe_fp8_quantize_weights", _ptr(src), E, N, K, _ptr(codes), _ptr(codes_t), _ptr(scales), _stream(stream))
+
+
+def moe_fp8_gemm(a, a_scales, rows, K, b, b_scales, b_transposed, N, E, row_offsets, out, dev_status, stream=None):
+    return _call("moe_fp8_gemm", _ptr(a), _ptr(a_scales), rows, K, _ptr(b), _ptr(b_scales), int(b_transposed), N, E,
+                 _ptr(row_offsets), _ptr(out), _ptr(dev_status), _stream(stream))
+
+
+def moe_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, rows, N, K, E, row_offsets, out, dev_status, stream=None):
+    return _call("moe_fp8_wgrad", _ptr(dy_t), _ptr(dy_scales), _ptr(x_t), _ptr(x_scales), rows, N, K, E,
+                 _ptr(row_offsets), _ptr(out), _ptr(dev_status), _stream(stream))
+
+
+def moe_fp8_swiglu(gu, w_rows, rows, f, nrows_dev, codes, scales, stream=None):
+    return _call("moe_fp8_swiglu", _ptr(gu), _ptr(w_rows), rows, f, _ptr(nrows_dev), _ptr(codes), _ptr(scales), _stream(stream))
 
 
 # ------------------------------------------------------------------ around the layer

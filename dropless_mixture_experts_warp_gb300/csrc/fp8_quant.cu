@@ -1,0 +1,347 @@
+// The quantiser of the 8-bit products with blocks of 128: bf16 rows to E4M3 codes with fp32
+// scales, blocks along rows, down columns (codes transposed, the operand of weight gradients)
+// or square (weights); and the SwiGLU between the experts' two products, quantised as it is
+// computed.  All are bound by memory.
+#include "fp8.cuh"
+#include "kernels.h"
+
+namespace moe {
+
+// ------------------------------------------------------------------------ rows
+
+constexpr int QR_ROWS = 4;   // rows under way in a warp
+
+// Eight values of 16 lanes (one block of 128): scale, codes.
+__device__ __forceinline__ uint2 f8_block16(const f32x2 (&v)[4], float amax, float& scale) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  const F8Scale f = f8_scale(amax);
+  scale = f.s;
+  const f32x2 ns = pair(-f.s, -f.s), inv = pair(f.inv, f.inv);
+  return make_uint2(f8_codes4(v[0], v[1], ns, inv), f8_codes4(v[2], v[3], ns, inv));
+}
+
+// A warp takes QR_ROWS rows x 256 columns: 16 lanes of 16 bytes a block, every row's load
+// issued before the first is used.  row_map: row r reads src row row_map[r], zeros where that
+// is negative.
+__global__ void __launch_bounds__(256) f8_rows_kernel(const uint16_t* __restrict__ src, int rows, int C,
+                                                      const int32_t* __restrict__ row_map,
+                                                      const int32_t* __restrict__ nrows_dev, uint8_t* __restrict__ codes,
+                                                      float* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  const int groups = (C + 255) / 256;
+  const long long total = static_cast<long long>((limit + QR_ROWS - 1) / QR_ROWS) * groups;
+  for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8ll) {
+    const int r0 = static_cast<int>(t / groups) * QR_ROWS;
+    const int col = static_cast<int>(t % groups) * 256 + lane * 8;
+    const bool in = col < C;
+    uint4 w[QR_ROWS];
+#pragma unroll
+    for (int i = 0; i < QR_ROWS; ++i) {
+      const int r = r0 + i;
+      const int from = r >= limit ? -1 : (row_map ? row_map[r] : r);
+      w[i] = in && from >= 0 ? *reinterpret_cast<const uint4*>(src + static_cast<long long>(from) * C + col) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < QR_ROWS; ++i) {
+      const uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, w[i].x), w[i].y), w[i].z), w[i].w);
+      const f32x2 v[4] = {bf16_pair(w[i].x), bf16_pair(w[i].y), bf16_pair(w[i].z), bf16_pair(w[i].w)};
+      float s;
+      const uint2 c = f8_block16(v, max_halves(m), s);
+      if (in && r0 + i < limit) {
+        *reinterpret_cast<uint2*>(codes + static_cast<long long>(r0 + i) * C + col) = c;
+        if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * rows + r0 + i] = s;
+      }
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ tiles
+
+constexpr int QT_IN_LD = 128 + 8;     // padded bf16 input rows
+constexpr int QT_LD = 128 + 16;       // padded code rows (bytes)
+constexpr int QT_IN_BYTES = 128 * QT_IN_LD * 2;
+constexpr int QT_SMEM = 2 * QT_IN_BYTES + 2 * 128 * QT_LD + (4 * 128 + 2 * 128 + 8) * 4;
+
+// What a tile kernel writes.  Rows: codes [batch][R][C] and scales; columns: codes_t
+// [batch][C][R_t] (R_t >= R: rows from R on are zeros) and scales_t.  Either may be NULL.
+struct F8Tiles {
+  const uint16_t* src;         // [batch][R][C]
+  const int32_t* row_map;      // batch 1
+  const int32_t* nrows_dev;    // batch 1: 128-row tiles from *nrows_dev on are left out
+  int batch, R, C, R_t;
+  uint8_t* codes;
+  float* scales;               // [ceil(C / 128)][R]; SQUARE: [batch][ceil(R / 128)][ceil(C / 128)]
+  uint8_t* codes_t;
+  float* scales_t;             // [ceil(R / 128)][C]; SQUARE: not used
+};
+
+// 128 x 128 tiles, persistent blocks with the next tile's rows on their way (cp.async) while
+// one is quantised.  A thread holds 32 rows of two columns and 64 columns of one row in
+// registers, as they were loaded from shared memory for the maxima; codes are assembled in
+// shared memory and leave as whole lines.  SQUARE: one scale a tile.
+template <bool SQUARE>
+__global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
+  extern __shared__ __align__(16) uint8_t sm[];
+  uint8_t* ct = sm + 2 * QT_IN_BYTES;              // column codes [128 columns][QT_LD]
+  uint8_t* rt = ct + 128 * QT_LD;                  // row codes [128 rows][QT_LD]
+  float* cmax = reinterpret_cast<float*>(rt + 128 * QT_LD);   // [4][128]
+  float* rmax = cmax + 4 * 128;                    // [2][128]
+  float* tmax = rmax + 2 * 128;                    // [8]
+  const int tid = threadIdx.x;
+  const int limit = p.nrows_dev ? min(p.R, *p.nrows_dev) : p.R;
+  const unsigned ctiles = (p.C + 127) / 128, rtiles = (limit + 127) / 128;
+  const unsigned total = p.batch * rtiles * ctiles;
+
+  auto rows_of = [&](unsigned t, int (&sr)[8]) {
+    const unsigned rti = t < total ? (t / ctiles) % rtiles : 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int r = static_cast<int>(rti) * 128 + (tid >> 4) + 16 * j;
+      sr[j] = (t >= total || r >= limit) ? -1 : (p.row_map ? p.row_map[r] : r);
+    }
+  };
+  auto fetch = [&](unsigned t, int buf, const int (&sr)[8]) {
+    if (t < total) {
+      const unsigned q = t / ctiles;
+      const int col = static_cast<int>(t - q * ctiles) * 128 + (tid & 15) * 8;
+      const uint16_t* s = p.src + static_cast<long long>(q / rtiles) * p.R * p.C;
+      uint8_t* dst = sm + buf * QT_IN_BYTES + (tid >> 4) * QT_IN_LD * 2 + (tid & 15) * 16;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool ok = sr[j] >= 0 && col < p.C;
+        const uint16_t* from = s + (ok ? static_cast<long long>(sr[j]) * p.C + col : 0);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(dst + 16 * j * QT_IN_LD * 2)), "l"(from),
+                     "r"(ok ? 16 : 0)
+                     : "memory");
+      }
+    }
+    copy_commit();
+  };
+
+  unsigned t = blockIdx.x;
+  int next[8];
+  rows_of(t, next);
+  fetch(t, 0, next);
+  rows_of(t + gridDim.x, next);
+  for (int it = 0; t < total; ++it, t += gridDim.x) {
+    fetch(t + gridDim.x, (it & 1) ^ 1, next);
+    rows_of(t + 2 * gridDim.x, next);
+    copy_wait<1>();
+    __syncthreads();
+    const uint16_t(*tile)[QT_IN_LD] = reinterpret_cast<const uint16_t(*)[QT_IN_LD]>(sm + (it & 1) * QT_IN_BYTES);
+    const unsigned qq = t / ctiles;
+    const int c0 = static_cast<int>(t - qq * ctiles) * 128, r0 = static_cast<int>(qq % rtiles) * 128;
+    const long long b = qq / rtiles;
+    // columns 2 cp and 2 cp + 1, rows 32 g to 32 g + 31; row rr, columns 64 hh to 64 hh + 63
+    const int cp = tid & 63, g = tid >> 6, rr = tid & 127, hh = tid >> 7;
+    uint32_t cw[32], rw[32];
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      cw[i] = *reinterpret_cast<const uint32_t*>(&tile[g * 32 + i][2 * cp]);
+      m = absmax_bf16x2(m, cw[i]);
+    }
+    float amax = max_halves(m);
+    if (!SQUARE) {
+      cmax[g * 128 + 2 * cp] = bf16_lo(m);
+      cmax[g * 128 + 2 * cp + 1] = bf16_hi(m);
+    }
+    m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 u = *reinterpret_cast<const uint4*>(&tile[rr][hh * 64 + 8 * i]);
+      rw[4 * i] = u.x; rw[4 * i + 1] = u.y; rw[4 * i + 2] = u.z; rw[4 * i + 3] = u.w;
+      if (!SQUARE) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) m = absmax_bf16x2(m, rw[4 * i + j]);
+      }
+    }
+    if (SQUARE) {
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+      if ((tid & 31) == 0) tmax[tid >> 5] = amax;
+    } else {
+      rmax[hh * 128 + rr] = max_halves(m);
+    }
+    __syncthreads();
+    float a0, a1, ar;
+    if (SQUARE) {
+      a0 = tmax[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) a0 = fmaxf(a0, tmax[i]);
+      a1 = ar = a0;
+    } else {
+      const int c = 2 * cp;
+      a0 = fmaxf(fmaxf(cmax[c], cmax[128 + c]), fmaxf(cmax[256 + c], cmax[384 + c]));
+      a1 = fmaxf(fmaxf(cmax[c + 1], cmax[129 + c]), fmaxf(cmax[257 + c], cmax[385 + c]));
+      ar = fmaxf(rmax[rr], rmax[128 + rr]);
+    }
+    if (p.codes_t) {
+      const F8Scale f0 = f8_scale(a0), f1 = SQUARE ? f0 : f8_scale(a1);
+      const f32x2 ns = pair(-f0.s, -f1.s), inv = pair(f0.inv, f1.inv);
+      uint32_t k0[8], k1[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float2 x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = unpair(f8_quotient(bf16_pair(cw[4 * i + j]), ns, inv));
+        k0[i] = cvt_e4m3x4(x[0].x, x[1].x, x[2].x, x[3].x);
+        k1[i] = cvt_e4m3x4(x[0].y, x[1].y, x[2].y, x[3].y);
+      }
+      // line cp holds column 2 cp, line 64 + cp column 2 cp + 1
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        *reinterpret_cast<uint4*>(ct + cp * QT_LD + g * 32 + 16 * i) = make_uint4(k0[4 * i], k0[4 * i + 1], k0[4 * i + 2], k0[4 * i + 3]);
+        *reinterpret_cast<uint4*>(ct + (64 + cp) * QT_LD + g * 32 + 16 * i) = make_uint4(k1[4 * i], k1[4 * i + 1], k1[4 * i + 2], k1[4 * i + 3]);
+      }
+      if (!SQUARE && g == 0 && c0 + 2 * cp < p.C) {
+        float* st = p.scales_t + static_cast<long long>(r0 >> 7) * p.C + c0 + 2 * cp;
+        st[0] = f0.s;
+        st[1] = f1.s;
+      }
+    }
+    if (p.codes) {
+      const F8Scale f = f8_scale(ar);
+      const f32x2 ns = pair(-f.s, -f.s), inv = pair(f.inv, f.inv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) k[j] = f8_codes4(bf16_pair(rw[8 * i + 2 * j]), bf16_pair(rw[8 * i + 2 * j + 1]), ns, inv);
+        *reinterpret_cast<uint4*>(rt + rr * QT_LD + hh * 64 + 16 * i) = make_uint4(k[0], k[1], k[2], k[3]);
+      }
+      if (!SQUARE && hh == 0 && r0 + rr < p.R) p.scales[static_cast<long long>(c0 >> 7) * p.R + r0 + rr] = f.s;
+    }
+    if (SQUARE && tid == 0) p.scales[(b * rtiles + (r0 >> 7)) * ctiles + (c0 >> 7)] = f8_scale(a0).s;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int line = (tid + 256 * j) >> 3, at = (tid & 7) * 16;
+      if (p.codes_t) {
+        const int col = c0 + (line < 64 ? 2 * line : 2 * (line - 64) + 1);
+        if (col < p.C && r0 + at < p.R_t)
+          *reinterpret_cast<uint4*>(p.codes_t + (b * p.C + col) * static_cast<long long>(p.R_t) + r0 + at) =
+              *reinterpret_cast<const uint4*>(ct + line * QT_LD + at);
+      }
+      if (p.codes && r0 + line < p.R && c0 + at < p.C)
+        *reinterpret_cast<uint4*>(p.codes + (b * p.R + r0 + line) * static_cast<long long>(p.C) + c0 + at) =
+            *reinterpret_cast<const uint4*>(rt + line * QT_LD + at);
+    }
+  }
+}
+
+template <bool SQUARE>
+static cudaError_t launch_f8_tiles(const F8Tiles& p, cudaStream_t s) {
+  const cudaError_t err = allow_smem<f8_tiles_kernel<SQUARE>>(QT_SMEM);
+  if (err != cudaSuccess) return err;
+  const long long tiles = static_cast<long long>(p.batch) * ((p.R + 127) / 128) * ((p.C + 127) / 128);
+  if (tiles >= (1ll << 31) - (1 << 20)) return cudaErrorInvalidValue;
+  const int grid = static_cast<int>(tiles < 2ll * num_sms() ? tiles : 2ll * num_sms());
+  f8_tiles_kernel<SQUARE><<<grid, 256, QT_SMEM, s>>>(p);
+  count_launch();
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------------ SwiGLU
+
+// w silu(g) u for two neighbours, silu through one exponential and one quotient in fp32.
+__device__ __forceinline__ float silu_exact(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
+
+// h = w silu(G) U of gu [rows][2f], a block of 128 columns of h on 16 lanes, quantised.
+__global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* __restrict__ gu, const float* __restrict__ w_rows, int rows,
+                                                        int f, const int32_t* __restrict__ nrows_dev,
+                                                        uint8_t* __restrict__ codes, float* __restrict__ scales) {
+  const int lane = threadIdx.x & 31;
+  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  const int groups = (f + 255) / 256;
+  const long long total = static_cast<long long>((limit + 1) / 2) * groups;
+  for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8ll) {
+    const int r0 = static_cast<int>(t / groups) * 2;
+    const int col = static_cast<int>(t % groups) * 256 + lane * 8;
+    const bool in = col < f;
+    uint4 g[2], u[2];
+    float w[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const bool ok = in && r0 + i < limit;
+      const uint16_t* at = gu + static_cast<long long>(r0 + i) * 2 * f + col;
+      g[i] = ok ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+      u[i] = ok ? *reinterpret_cast<const uint4*>(at + f) : make_uint4(0, 0, 0, 0);
+      w[i] = r0 + i >= limit ? 0.0f : (w_rows ? w_rows[r0 + i] : 1.0f);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t gw[4] = {g[i].x, g[i].y, g[i].z, g[i].w}, uw[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+      f32x2 v[4];
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float x = w[i] * silu_exact(bf16_lo(gw[j])) * bf16_lo(uw[j]);
+        const float y = w[i] * silu_exact(bf16_hi(gw[j])) * bf16_hi(uw[j]);
+        amax = fmaxf(amax, fmaxf(fabsf(x), fabsf(y)));
+        v[j] = pair(x, y);
+      }
+      float s;
+      const uint2 c = f8_block16(v, amax, s);
+      if (in && r0 + i < limit) {
+        *reinterpret_cast<uint2*>(codes + static_cast<long long>(r0 + i) * f + col) = c;
+        if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * rows + r0 + i] = s;
+      }
+    }
+  }
+}
+
+static int f8_row_grid(long long warps) {
+  const long long blocks = (warps + 7) / 8, most = 8ll * num_sms();
+  return static_cast<int>(blocks < most ? blocks : most);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+moe_status moe_fp8_quantize(const moe_bf16* src, int64_t rows, int32_t C, const int32_t* row_map, const int32_t* nrows_dev,
+                            uint8_t* codes, float* scales, uint8_t* codes_t, float* scales_t, void* stream) {
+  if (rows < 0 || C <= 0 || (rows > 0 && !src)) return MOE_ERR_INVALID_ARG;
+  if (!codes != !scales || !codes_t != !scales_t || (rows > 0 && !codes && !codes_t)) return MOE_ERR_INVALID_ARG;
+  if (C % 16 != 0 || rows > (1ll << 31) - 256) return MOE_ERR_UNSUPPORTED;
+  if (!f8_aligned(src) || !f8_aligned(codes) || !f8_aligned(codes_t)) return MOE_ERR_ALIGNMENT;
+  if (rows == 0) return MOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!codes_t) {
+    const long long warps = (rows + QR_ROWS - 1) / QR_ROWS * ((C + 255) / 256);
+    f8_rows_kernel<<<f8_row_grid(warps), 256, 0, s>>>(src, static_cast<int>(rows), C, row_map, nrows_dev, codes, scales);
+    count_launch();
+    return status_of(cudaGetLastError());
+  }
+  const F8Tiles p{src, row_map, nrows_dev, 1, static_cast<int>(rows), C, static_cast<int>(up128(rows)), codes, scales, codes_t, scales_t};
+  return status_of(launch_f8_tiles<false>(p, s));
+}
+
+moe_status moe_fp8_quantize_weights(const moe_bf16* src, int32_t E, int32_t N, int32_t K, uint8_t* codes, uint8_t* codes_t,
+                                    float* scales, void* stream) {
+  if (E <= 0 || N <= 0 || K <= 0 || !src || !scales || (!codes && !codes_t)) return MOE_ERR_INVALID_ARG;
+  if (N % 16 != 0 || K % 16 != 0) return MOE_ERR_UNSUPPORTED;
+  if (!f8_aligned(src) || !f8_aligned(codes) || !f8_aligned(codes_t)) return MOE_ERR_ALIGNMENT;
+  const F8Tiles p{src, nullptr, nullptr, E, N, K, N, codes, scales, codes_t, nullptr};
+  return status_of(launch_f8_tiles<true>(p, static_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows, int32_t f, const int32_t* nrows_dev, uint8_t* codes,
+                          float* scales, void* stream) {
+  if (rows < 0 || f <= 0 || (rows > 0 && (!gu || !codes || !scales))) return MOE_ERR_INVALID_ARG;
+  if (f % 16 != 0 || rows > (1ll << 31) - 256) return MOE_ERR_UNSUPPORTED;
+  if (!f8_aligned(gu) || !f8_aligned(codes)) return MOE_ERR_ALIGNMENT;
+  if (rows == 0) return MOE_OK;
+  const long long warps = (rows + 1) / 2 * ((f + 255) / 256);
+  f8_swiglu_kernel<<<f8_row_grid(warps), 256, 0, static_cast<cudaStream_t>(stream)>>>(gu, w_rows, static_cast<int>(rows), f, nrows_dev,
+                                                                                      codes, scales);
+  count_launch();
+  return status_of(cudaGetLastError());
+}
+
+}  // extern "C"

@@ -527,6 +527,64 @@ moe_status moe_gemm_bf16(const moe_bf16* A, const moe_bf16* B, moe_bf16* C, int3
                          int32_t* dev_status, void* stream);
 
 /*
+ * ---------------------------------------------------------------- blocks of 128
+ * Products of E4M3 codes whose fp32 scales each belong to 128 values, the form in which
+ * weights are published with one scale for each 128 x 128 block.  A block's scale is
+ *   s = max(largest |x|, 2^-64) / 448,  a code E4M3(x / s)   (both fp32 quotients, nearest;
+ * codes to nearest, ties to even, zeros of either sign 0); a code c stands for c * s.  A NaN is a NaN code; all
+ * values of a block that holds an infinity are NaN.
+ *   rows     codes [R][C], scales [ceil(C / 128)][R]: blocks along each row
+ *   columns  codes_t [C][R_t], scales_t [R_t / 128][C], R_t = R rounded up to 128: blocks of
+ *            128 rows down each column, rows from R on zeros (an operand of weight gradients)
+ *   weights  codes [E][N][K], scales [E][ceil(N / 128)][ceil(K / 128)]; codes_t [E][K][N] are
+ *            the same codes transposed (an operand of input gradients; the scales are shared)
+ */
+
+/*
+ * src bf16 [rows][C] (C % 16 == 0) -> the row form, the column form, or both from one read
+ * (each pair of codes and scales given, or both NULL).  row_map [rows] int32 or NULL: row r is
+ * src row row_map[r], zeros where that is negative (src then has any number of rows).
+ * nrows_dev (device int32, or NULL): 128-row blocks from *nrows_dev on are left as they were.
+ */
+moe_status moe_fp8_quantize(const moe_bf16* src, int64_t rows, int32_t C, const int32_t* row_map,
+                            const int32_t* nrows_dev, uint8_t* codes, float* scales, uint8_t* codes_t,
+                            float* scales_t, void* stream);
+
+/* src bf16 [E][N][K] (N, K % 16 == 0) -> weights; codes or codes_t may be NULL. */
+moe_status moe_fp8_quantize_weights(const moe_bf16* src, int32_t E, int32_t N, int32_t K, uint8_t* codes,
+                                    uint8_t* codes_t, float* scales, void* stream);
+
+/*
+ * out[r][n] = sum_k a(r, k) b_e(n, k), fp32 sums, one rounding to bf16.
+ *   a [rows][K], a_scales [ceil(K / 128)][rows]: the row form (K % 16 == 0)
+ *   b [E][N][K] codes (N % 8 == 0); b_scales [E][ceil(N / 128)][ceil(K / 128)], or with
+ *   b_transposed [E][ceil(K / 128)][ceil(N / 128)]: b is then the codes_t of weights
+ *   [E][K][N], and the product is a times them (an input gradient).
+ *   row_offsets [E + 1] int32, multiples of 128, ascending from 0: expert e multiplies rows
+ *   [row_offsets[e], row_offsets[e + 1]); NULL (E = 1): all rows.  Rows outside are left as
+ *   they were; offsets past `rows` count as the end.
+ */
+moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, int32_t K, const uint8_t* b,
+                        const float* b_scales, int32_t b_transposed, int32_t N, int32_t E,
+                        const int32_t* row_offsets, moe_bf16* out, int32_t* dev_status, void* stream);
+
+/*
+ * out[e][n][k] = sum over the rows r of expert e of dy(r, n) x(r, k), bf16 [E][N][K], from the
+ * column forms dy_t [N][rows], x_t [K][rows] (rows % 128 == 0, K % 8 == 0).  row_offsets as
+ * above; an expert without rows gets zeros.
+ */
+moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t, const float* x_scales,
+                         int64_t rows, int32_t N, int32_t K, int32_t E, const int32_t* row_offsets, moe_bf16* out,
+                         int32_t* dev_status, void* stream);
+
+/*
+ * h = w silu(G) U of gu bf16 [rows][2f] (G | U, f % 16 == 0), w_rows [rows] fp32 or NULL (= 1),
+ * in fp32, to the row form: codes [rows][f], scales [ceil(f / 128)][rows].  nrows_dev as above.
+ */
+moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows, int32_t f, const int32_t* nrows_dev,
+                          uint8_t* codes, float* scales, void* stream);
+
+/*
  * ---------------------------------------------------------------- around the layer
  * What a training step computes next to the layer: the norms and the residual merge of
  * the block the layer sits in, the router's balance loss, and the optimiser step.  The
