@@ -24,7 +24,7 @@ SCORE = {"softmax": 0, "sigmoid": 1}
 TYPE = {"bf16": 0, "fp32": 1}
 GATE = {"none": 0, "channel": 1, "token": 2}
 GATE_ACT = {"identity": 0, "sigmoid": 1}
-PREC = {"bf16": 0, "mxfp8": 1, "mxfp8-w4": 2}
+PREC = {"bf16": 0, "mxfp8": 1, "mxfp8-w4": 2, "fp8-block": 3}
 
 
 class MoeError(RuntimeError):
@@ -145,6 +145,8 @@ SIGNATURES = {
     "moe_fp8_gemm": (ctypes.c_int32, [_P, _P, ctypes.c_int64, _I, _P, _P, _I, _I, _I] + [_P] * 4),
     "moe_fp8_wgrad": (ctypes.c_int32, [_P] * 4 + [ctypes.c_int64, _I, _I, _I] + [_P] * 4),
     "moe_fp8_swiglu": (ctypes.c_int32, [_P, _P, ctypes.c_int64, _I] + [_P] * 4),
+    "moe_fp8_swiglu_bwd": (ctypes.c_int32, [_P] * 3 + [ctypes.c_int64, _I] + [_P] * 10),
+    "moe_permute_fp8": (ctypes.c_int32, [_D] + [_P] * 15),
     "moe_norm_check_dims": (ctypes.c_int32, [_N]),
     "moe_norm_workspace_size": (ctypes.c_size_t, [_N]),
     "moe_norm_fwd": (ctypes.c_int32, [_N] + [_P] * 4),
@@ -542,6 +544,20 @@ def moe_fp8_wgrad(dy_t, dy_scales, x_t, x_scales, rows, N, K, E, row_offsets, ou
 
 def moe_fp8_swiglu(gu, w_rows, rows, f, nrows_dev, codes, scales, stream=None):
     return _call("moe_fp8_swiglu", _ptr(gu), _ptr(w_rows), rows, f, _ptr(nrows_dev), _ptr(codes), _ptr(scales), _stream(stream))
+
+
+def moe_fp8_swiglu_bwd(gu, dh, w_rows, rows, f, nrows_dev, dgu_codes, dgu_scales, dgu_codes_t, dgu_scales_t, h_codes_t,
+                       h_scales_t, dw_rows, dw_part, stream=None):
+    return _call("moe_fp8_swiglu_bwd", _ptr(gu), _ptr(dh), _ptr(w_rows), rows, f, _ptr(nrows_dev), _ptr(dgu_codes),
+                 _ptr(dgu_scales), _ptr(dgu_codes_t), _ptr(dgu_scales_t), _ptr(h_codes_t), _ptr(h_scales_t), _ptr(dw_rows),
+                 _ptr(dw_part), _stream(stream))
+
+
+def moe_permute_fp8(dims, x, topk_idx, topk_w, split_sizes, row_offsets, workspace, codes, scales, codes_t, scales_t,
+                    row_to_token, token_to_row, w_rows, dev_status, stream=None):
+    return _call("moe_permute_fp8", _d(dims), _ptr(x), _ptr(topk_idx), _ptr(topk_w), _ptr(split_sizes), _ptr(row_offsets),
+                 _ptr(workspace), _ptr(codes), _ptr(scales), _ptr(codes_t), _ptr(scales_t), _ptr(row_to_token),
+                 _ptr(token_to_row), _ptr(w_rows), _ptr(dev_status), _stream(stream))
 
 
 # ------------------------------------------------------------------ around the layer

@@ -245,7 +245,7 @@ moe_status moe_check_dims(const moe_dims* dims) {
     return MOE_ERR_INVALID_ARG;
   if (d.k > d.E || d.k > 32) return MOE_ERR_INVALID_ARG;
   if (d.score != MOE_SCORE_SOFTMAX && d.score != MOE_SCORE_SIGMOID) return MOE_ERR_INVALID_ARG;
-  if (d.prec != MOE_PREC_BF16 && d.prec != MOE_PREC_MXFP8 && d.prec != MOE_PREC_MXFP8_W4) return MOE_ERR_INVALID_ARG;
+  if (d.prec < MOE_PREC_BF16 || d.prec > MOE_PREC_FP8_BLOCK) return MOE_ERR_INVALID_ARG;
   if (d.prec != MOE_PREC_BF16 && (d.f % 128 != 0 || d.f_shared % 128 != 0)) return MOE_ERR_UNSUPPORTED;
   if (d.E > MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
   if (d.d % 128 != 0 || d.f % 64 != 0 || d.f_shared % 64 != 0) return MOE_ERR_UNSUPPORTED;

@@ -293,6 +293,164 @@ __global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* __restri
   }
 }
 
+// The gradient of the SwiGLU, quantised both ways, and h again for the down weights' gradient:
+//   dA = w dH;  dG = dA U silu'(G);  dU = dA silu(G);  dw = sum silu(G) U dH
+// One 128 x 128 tile of h's columns at a time: a thread holds four rows of eight columns of G,
+// U and dH, the next tile's already on their way.  A row's block is on 16 lanes, as in the
+// forward; columns take their maxima through shared memory and their codes leave through a
+// transposing tile whose four-byte units are permuted so that neither side has bank conflicts.
+struct F8SwigluBwd {
+  const uint16_t *gu, *dh;    // [rows][2f], [rows][f]
+  const float* w_rows;        // NULL = 1
+  const int32_t* nrows_dev;
+  int rows, f, R_t;
+  uint8_t* dgu;               // [rows][2f]
+  float* dgu_s;               // [2f / 128][rows]
+  uint8_t* dgu_t;             // [2f][R_t]
+  float* dgu_ts;              // [R_t / 128][2f]
+  uint8_t* h_t;               // [f][R_t]
+  float* h_ts;                // [R_t / 128][f]
+  float* dw_part;             // [rows][f / 128], or NULL
+};
+constexpr int SB_THREADS = 512;
+
+__global__ void __launch_bounds__(SB_THREADS, 1) f8_swiglu_bwd_kernel(const F8SwigluBwd p) {
+  __shared__ __align__(16) uint32_t ct[128 * 32];    // codes of a tile's columns
+  __shared__ float cmax[32 * 128];
+  __shared__ float2 cscale[128];                     // -scale, 1 / scale of a tile's columns
+  const int tid = threadIdx.x, c = tid & 15, u = tid >> 4;
+  const int limit = p.nrows_dev ? min(p.rows, *p.nrows_dev) : p.rows;
+  const unsigned ctiles = p.f / 128, total = static_cast<unsigned>((limit + 127) / 128) * ctiles;
+
+  uint4 next[4][3];
+  auto fetch = [&](unsigned t) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = static_cast<int>(t / ctiles) * 128 + 4 * u + i;
+      const bool ok = t < total && r < limit;
+      const int col = static_cast<int>(t % ctiles) * 128 + 8 * c;
+      const uint16_t* gu = p.gu + (ok ? 2ll * r * p.f + col : 0);
+      next[i][0] = ok ? *reinterpret_cast<const uint4*>(gu) : make_uint4(0, 0, 0, 0);
+      next[i][1] = ok ? *reinterpret_cast<const uint4*>(gu + p.f) : make_uint4(0, 0, 0, 0);
+      next[i][2] = ok ? *reinterpret_cast<const uint4*>(p.dh + static_cast<long long>(r) * p.f + col) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  fetch(blockIdx.x);
+  for (unsigned t = blockIdx.x; t < total; t += gridDim.x) {
+    uint4 in[4][3];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 3; ++j) in[i][j] = next[i][j];
+    fetch(t + gridDim.x);
+    const int r0 = static_cast<int>(t / ctiles) * 128, c0 = static_cast<int>(t % ctiles) * 128;
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + 4 * u + i;
+      w[i] = r < limit ? (p.w_rows ? p.w_rows[r] : 1.0f) : 0.0f;
+    }
+#pragma unroll 1
+    for (int what = 0; what < 3; ++what) {           // dG, dU, h
+      f32x2 v[4][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t gw[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
+        const uint32_t uw[4] = {in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+        const uint32_t dw[4] = {in[i][2].x, in[i][2].y, in[i][2].z, in[i][2].w};
+        float sum = 0.0f, rmax = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float x[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float g = k ? bf16_hi(gw[j]) : bf16_lo(gw[j]), uu = k ? bf16_hi(uw[j]) : bf16_lo(uw[j]);
+            const float dh = k ? bf16_hi(dw[j]) : bf16_lo(dw[j]);
+            const float den = 1.0f + __expf(-g);
+            if (what == 0) {
+              const float sg = __fdividef(1.0f, den);
+              x[k] = w[i] * dh * uu * sg * (1.0f + g * (1.0f - sg));
+            } else {
+              const float silu = __fdividef(g, den);
+              x[k] = what == 1 ? w[i] * dh * silu : w[i] * silu * uu;
+              if (what == 2) sum += silu * uu * dh;
+            }
+          }
+          rmax = fmaxf(rmax, fmaxf(fabsf(x[0]), fabsf(x[1])));
+          v[i][j] = pair(x[0], x[1]);
+        }
+        const int r = r0 + 4 * u + i;
+        if (what < 2) {                              // the row's own block
+          float s;
+          const uint2 k = f8_block16(v[i], rmax, s);
+          const int col = what * p.f + c0 + 8 * c;
+          if (r < limit) {
+            *reinterpret_cast<uint2*>(p.dgu + 2ll * r * p.f + col) = k;
+            if (c == 0) p.dgu_s[static_cast<long long>(col >> 7) * p.rows + r] = s;
+          }
+        } else if (p.dw_part) {
+#pragma unroll
+          for (int off = 8; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+          if (c == 0 && r < limit) p.dw_part[static_cast<long long>(r) * ctiles + (c0 >> 7)] = sum;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float a = 0.0f, b = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 x = unpair(v[i][j]);
+          a = fmaxf(a, fabsf(x.x));
+          b = fmaxf(b, fabsf(x.y));
+        }
+        *reinterpret_cast<float2*>(&cmax[u * 128 + 8 * c + 2 * j]) = make_float2(a, b);
+      }
+      __syncthreads();
+      uint8_t* const out_t = what < 2 ? p.dgu_t : p.h_t;
+      const int width = what < 2 ? 2 * p.f : p.f, out_c = (what == 1 ? p.f : 0) + c0;
+      if (tid < 128) {
+        float a = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) a = fmaxf(a, cmax[i * 128 + tid]);
+        const F8Scale f = f8_scale(a);
+        cscale[tid] = make_float2(-f.s, f.inv);
+        (what < 2 ? p.dgu_ts : p.h_ts)[static_cast<long long>(r0 >> 7) * width + out_c + tid] = f.s;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 s0 = cscale[8 * c + 2 * j], s1 = cscale[8 * c + 2 * j + 1];
+        const f32x2 ns = pair(s0.x, s1.x), inv = pair(s0.y, s1.y);
+        float2 x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[i] = unpair(f8_quotient(v[i][j], ns, inv));
+        ct[(8 * c + 2 * j) * 32 + (u ^ (2 * c))] = cvt_e4m3x4(x[0].x, x[1].x, x[2].x, x[3].x);
+        ct[(8 * c + 2 * j + 1) * 32 + (u ^ (2 * c))] = cvt_e4m3x4(x[0].y, x[1].y, x[2].y, x[3].y);
+      }
+      __syncthreads();
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int i = tid + SB_THREADS * j, line = i >> 3, q = i & 7, cc = line >> 3;
+        uint4 k = *reinterpret_cast<const uint4*>(&ct[line * 32 + 4 * (q ^ (cc >> 1))]);
+        if (cc & 1) k = make_uint4(k.z, k.w, k.x, k.y);
+        *reinterpret_cast<uint4*>(out_t + static_cast<long long>(out_c + line) * p.R_t + r0 + 16 * q) = k;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+// dw [r] = its parts' sum, in order.
+__global__ void f8_dw_kernel(const float* __restrict__ part, int parts, int rows, const int32_t* __restrict__ nrows_dev,
+                             float* __restrict__ dw) {
+  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < limit; r += gridDim.x * blockDim.x) {
+    float s = 0.0f;
+    for (int i = 0; i < parts; ++i) s += part[static_cast<long long>(r) * parts + i];
+    dw[r] = s;
+  }
+}
+
 static int f8_row_grid(long long warps) {
   const long long blocks = (warps + 7) / 8, most = 8ll * num_sms();
   return static_cast<int>(blocks < most ? blocks : most);
@@ -342,6 +500,52 @@ moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows,
                                                                                       codes, scales);
   count_launch();
   return status_of(cudaGetLastError());
+}
+
+moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const float* w_rows, int64_t rows, int32_t f,
+                              const int32_t* nrows_dev, uint8_t* dgu_codes, float* dgu_scales, uint8_t* dgu_codes_t,
+                              float* dgu_scales_t, uint8_t* h_codes_t, float* h_scales_t, float* dw_rows, float* dw_part,
+                              void* stream) {
+  if (rows < 0 || f <= 0 || !dw_rows != !dw_part) return MOE_ERR_INVALID_ARG;
+  if (rows > 0 && (!gu || !dh || !dgu_codes || !dgu_scales || !dgu_codes_t || !dgu_scales_t || !h_codes_t || !h_scales_t))
+    return MOE_ERR_INVALID_ARG;
+  if (f % 128 != 0 || rows > (1ll << 31) - 256 || up128(rows) / 128 * (f / 128) >= (1ll << 31)) return MOE_ERR_UNSUPPORTED;
+  if (!f8_aligned(gu) || !f8_aligned(dh) || !f8_aligned(dgu_codes) || !f8_aligned(dgu_codes_t) || !f8_aligned(h_codes_t))
+    return MOE_ERR_ALIGNMENT;
+  if (rows == 0) return MOE_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const F8SwigluBwd p{gu, dh, w_rows, nrows_dev, static_cast<int>(rows), f, static_cast<int>(up128(rows)), dgu_codes, dgu_scales,
+                      dgu_codes_t, dgu_scales_t, h_codes_t, h_scales_t, dw_part};
+  const long long tiles = up128(rows) / 128 * (f / 128);
+  f8_swiglu_bwd_kernel<<<static_cast<int>(tiles < num_sms() ? tiles : num_sms()), SB_THREADS, 0, s>>>(p);
+  count_launch();
+  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  if (!dw_rows) return MOE_OK;
+  const long long blocks = (rows + 255) / 256;
+  f8_dw_kernel<<<static_cast<int>(blocks < 4 * num_sms() ? blocks : 4 * num_sms()), 256, 0, s>>>(dw_part, f / 128, static_cast<int>(rows),
+                                                                                               nrows_dev, dw_rows);
+  count_launch();
+  return status_of(cudaGetLastError());
+}
+
+moe_status moe_permute_fp8(const moe_dims* dims, const moe_bf16* x, const int32_t* topk_idx, const float* topk_w,
+                           const int32_t* split_sizes, const int32_t* row_offsets, const void* workspace, uint8_t* codes,
+                           float* scales, uint8_t* codes_t, float* scales_t, int32_t* row_to_token, int32_t* token_to_row,
+                           float* w_rows, int32_t* dev_status, void* stream) {
+  const moe_status st = moe_check_dims(dims);
+  if (st != MOE_OK) return st;
+  const moe_dims& d = *dims;
+  if (!split_sizes || !row_offsets || !codes || !scales || !row_to_token || !w_rows || !dev_status) return MOE_ERR_INVALID_ARG;
+  if (!codes_t != !scales_t || (d.T > 0 && (!x || !topk_idx || !topk_w || !token_to_row))) return MOE_ERR_INVALID_ARG;
+  if (!workspace) return MOE_ERR_WORKSPACE;
+  if (!f8_aligned(x) || !f8_aligned(codes) || !f8_aligned(codes_t)) return MOE_ERR_ALIGNMENT;
+  const int64_t rows = moe_row_capacity(dims);
+  const RouteScratch rs = route_scratch(d, const_cast<void*>(workspace));
+  if (launch_route_maps(d.T, d.E, d.k, topk_idx, topk_w, split_sizes, row_offsets, rs, row_to_token, token_to_row, w_rows,
+                        static_cast<int>(rows), dev_status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
+    return MOE_ERR_CUDA;
+  if (d.T == 0) return MOE_OK;
+  return moe_fp8_quantize(x, rows, d.d, row_to_token, row_offsets + d.E, codes, scales, codes_t, scales_t, stream);
 }
 
 }  // extern "C"

@@ -51,7 +51,7 @@ typedef uint16_t moe_bf16; /* bfloat16 bit pattern */
 typedef enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID_ARG = 1, /* bad size, NULL pointer, k > E, ... */
-  MOE_ERR_UNSUPPORTED = 2, /* valid but not supported (d % 128, f % 64 (% 128 for MXFP8), E > 1024, ...) */
+  MOE_ERR_UNSUPPORTED = 2, /* valid but not supported (d % 128, f % 64 (% 128 in 8 bits), E > 1024, ...) */
   MOE_ERR_ALIGNMENT = 3,   /* a pointer is not 16-byte aligned */
   MOE_ERR_WORKSPACE = 4,   /* workspace NULL while needed */
   MOE_ERR_CUDA = 5,        /* a CUDA runtime/driver call failed */
@@ -64,7 +64,8 @@ enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 /* MOE_PREC_MXFP8_W4: FP8 x FP4 experts -- activations and gradients MXFP8 (E4M3), the
  * expert weights MXFP4 (E2M1 codes with one E8M0 scale per 32 elements); see the MXFP8
  * layer calls below. */
-enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP8_W4 = 2 };
+/* MOE_PREC_FP8_BLOCK: E4M3 codes with fp32 scales for blocks of 128 ("blocks of 128" below). */
+enum { MOE_PREC_BF16 = 0, MOE_PREC_MXFP8 = 1, MOE_PREC_MXFP8_W4 = 2, MOE_PREC_FP8_BLOCK = 3 };
 enum { MOE_ROW_ALIGN = 128 };
 
 typedef struct moe_dims {
@@ -583,6 +584,28 @@ moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint
  */
 moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows, int32_t f, const int32_t* nrows_dev,
                           uint8_t* codes, float* scales, void* stream);
+
+/*
+ * Its gradient: from dh bf16 [rows][f] (f % 128 == 0)
+ *   dA = w dH;  dG = dA U silu'(G);  dU = dA silu(G);  dw[r] = sum_j silu(G) U dH
+ * dG | dU to the row form (dgu_codes [rows][2f]) and the column form (dgu_codes_t [2f][R_t]),
+ * h itself to the column form (h_codes_t [f][R_t]: the codes that moe_fp8_swiglu would have
+ * given columns).  dw_rows [rows] fp32 and its scratch dw_part [rows][f / 128], or both NULL.
+ */
+moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const float* w_rows, int64_t rows, int32_t f,
+                              const int32_t* nrows_dev, uint8_t* dgu_codes, float* dgu_scales, uint8_t* dgu_codes_t,
+                              float* dgu_scales_t, uint8_t* h_codes_t, float* h_scales_t, float* dw_rows,
+                              float* dw_part, void* stream);
+
+/*
+ * moe_permute for the layer in this form (MOE_PREC_FP8_BLOCK; dims->prec may be any value):
+ * the same maps, and the routed rows of x quantised as they are gathered, to the row form
+ * (codes [rows][d]) and, where codes_t is given, the column form.  rows = moe_row_capacity.
+ */
+moe_status moe_permute_fp8(const moe_dims* dims, const moe_bf16* x, const int32_t* topk_idx, const float* topk_w,
+                           const int32_t* split_sizes, const int32_t* row_offsets, const void* workspace,
+                           uint8_t* codes, float* scales, uint8_t* codes_t, float* scales_t, int32_t* row_to_token,
+                           int32_t* token_to_row, float* w_rows, int32_t* dev_status, void* stream);
 
 /*
  * ---------------------------------------------------------------- around the layer

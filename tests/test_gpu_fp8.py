@@ -217,3 +217,200 @@ def test_weight_grad(counts, N, K):
     fp8.check(da)
     ref, mag = ob.weight_grad(ob.rows_values(dc, ds).T, ob.rows_values(xc, xs).T, off)
     close(out, ref, mag, max(counts))
+
+
+# ------------------------------------------------------------------------------------ SwiGLU
+
+def stands_for(codes, scales, ref, mag=None):
+    """Codes and scales stand for ref within half a step of E4M3 (2^-4 of the value; 2^-10 of the scale among its
+    subnormals), the values computed in fp32 with exponentials good to 2^-20 of `mag` (default: of the value)."""
+    mag = np.abs(ref) if mag is None else mag
+
+    def top(a):
+        p = np.zeros((a.shape[0], ob.up(a.shape[1])))
+        p[:, :a.shape[1]] = a
+        return p.reshape(a.shape[0], -1, 128).max(2)
+
+    v = ob.rows_values(codes.cpu(), scales.cpu().numpy())
+    s = np.maximum(top(np.abs(ref)), ob.FLOOR) / ob.TOP
+    off = np.abs(scales.cpu().numpy().T - s) - (2.0 ** -18 * top(mag) / ob.TOP + 2.0 ** -23 * s)
+    assert np.all(off <= 0), np.max(off)
+    s = np.repeat(s, 128, 1)[:, :ref.shape[1]]
+    off = np.abs(v - ref) - (np.abs(ref) * 2.0 ** -4 + s * 2.0 ** -10 + 2.0 ** -16 * mag + 2.0 ** -17 * s)
+    assert np.all(off <= 0), np.max(off)
+
+
+def gradient_terms(g, u, w, dh):
+    """Sums of magnitudes of dG | dU: silu' = s (1 + g (1 - s)) is 0 near g = -1.28, where its terms cancel, so that dG is
+    exact to a part of s (1 + |g| (1 - s)) only."""
+    s, da = ob.sigmoid(g), np.abs(w[:, None] * dh)
+    return np.concatenate([da * np.abs(u) * s * (1 + np.abs(g) * (1 - s)), da * np.abs(g) * s], 1)
+
+
+@pytest.mark.parametrize("R,f", [(1, 16), (5, 272), (129, 128), (300, 640)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_swiglu(R, f, weighted):
+    from dropless_mixture_experts_warp_gb300 import binding as B, fp8
+    rng = np.random.default_rng(R + f)
+    gu = bf16(rng, R, 2 * f, scale=3.0)
+    gu[0, :4] = torch.tensor([90.0, -90.0, 300.0, -300.0])
+    w = torch.from_numpy(rng.random(R).astype(np.float32)) if weighted else None
+    h = fp8.allocate_rows(R, f)
+    B.moe_fp8_swiglu(gu.cuda(), None if w is None else w.cuda(), R, f, None, h.codes, h.scales)
+    v = gu.double().numpy()
+    ref = ob.swiglu(v[:, :f], v[:, f:], np.ones(R) if w is None else w.double().numpy())
+    stands_for(h.codes, h.scales, ref)
+
+
+@pytest.mark.parametrize("R,f,used", [(1, 128, None), (130, 256, None), (512, 384, 384), (256, 1024, 0)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_swiglu_gradient(R, f, used, weighted):
+    from dropless_mixture_experts_warp_gb300 import binding as B, fp8
+    rng = np.random.default_rng(R + f)
+    gu, dh = bf16(rng, R, 2 * f, scale=2.0), bf16(rng, R, f, scale=0.1)
+    gu[0, :4] = torch.tensor([90.0, -90.0, 300.0, -300.0])
+    w = torch.from_numpy(rng.random(R).astype(np.float32)) if weighted else None
+    dgu, h = fp8.allocate_rows(R, 2 * f, both=True), fp8.allocate_rows(R, f, both=True)
+    dw, part = (torch.full((R,), 7.0, device="cuda"), torch.empty(R, f // 128, device="cuda")) if weighted else (None, None)
+    for t in (dgu.codes, dgu.codes_t, h.codes_t):
+        t.view(torch.uint8).fill_(0x11)
+    for t in (dgu.scales, dgu.scales_t, h.scales_t):
+        t.fill_(7.0)
+    n = None if used is None else torch.tensor([used], dtype=torch.int32).cuda()
+    B.moe_fp8_swiglu_bwd(gu.cuda(), dh.cuda(), None if w is None else w.cuda(), R, f, n, dgu.codes, dgu.scales, dgu.codes_t,
+                         dgu.scales_t, h.codes_t, h.scales_t, dw, part)
+    k = R if used is None else used
+    v, d = gu.double().numpy()[:k], dh.double().numpy()[:k]
+    ww = np.ones(k) if w is None else w.double().numpy()[:k]
+    dG, dU, dws = ob.swiglu_bwd(v[:, :f], v[:, f:], ww, d)
+    ref, hr = np.concatenate([dG, dU], 1), ob.swiglu(v[:, :f], v[:, f:], ww)
+    if k:
+        mag = gradient_terms(v[:, :f], v[:, f:], ww, d)
+        stands_for(dgu.codes[:k], dgu.scales[:, :k], ref, mag)
+        pad = np.zeros((ob.up(k) - k, 2 * f))
+        kt = ob.up(k)
+        stands_for(dgu.codes_t[:, :kt], dgu.scales_t[: kt // 128], np.concatenate([ref, pad]).T, np.concatenate([mag, pad]).T)
+        stands_for(h.codes_t[:, :kt], h.scales_t[: kt // 128], np.concatenate([hr, pad[:, :f]]).T)
+        if weighted:
+            s = ob.sigmoid(v[:, :f])
+            mag = np.abs(v[:, :f] * s * v[:, f:] * d).sum(1)
+            assert np.all(np.abs(dw[:k].double().cpu().numpy() - dws) <= (f + 64) * ob.U32 * mag + 1e-30)
+    if used is not None:
+        assert (dgu.codes[k:].view(torch.uint8) == 0x11).all() and (dgu.scales[:, k:] == 7.0).all()
+        assert (h.codes_t[:, k:].contiguous().view(torch.uint8) == 0x11).all() and (h.scales_t[k // 128:] == 7.0).all()
+
+
+# ------------------------------------------------------------------------------------ the layer
+
+LAYERS = [dict(T=1, d=256, f=128, E=8, k=2, score="softmax"), dict(T=300, d=384, f=256, E=16, k=4, score="sigmoid"),
+          dict(T=129, d=128, f=384, E=5, k=5, score="softmax", f_shared=256), dict(T=0, d=128, f=128, E=4, k=2, score="softmax"),
+          dict(T=700, d=256, f=128, E=300, k=8, score="softmax")]
+
+
+@pytest.mark.parametrize("c", LAYERS, ids=lambda c: f"T{c['T']}E{c['E']}")
+def test_layer(c):
+    """Forward and backward, each step against float64 from what the step before left on the GPU."""
+    from dropless_mixture_experts_warp_gb300 import layer
+    c = dict(c)
+    T, d, f, E, k, fs = c["T"], c["d"], c["f"], c["E"], c["k"], c.get("f_shared", 0)
+    rng = np.random.default_rng(T + E)
+    x, dy = bf16(rng, T, d).cuda(), bf16(rng, T, d).cuda()
+    logits = torch.from_numpy((rng.standard_normal((T, E)) + rng.standard_normal(E)).astype(np.float32)).cuda()
+    w = {"gu": bf16(rng, E, 2 * f, d, scale=d ** -0.5).cuda(), "d": bf16(rng, E, d, f, scale=f ** -0.5).cuda()}
+    sh = {}
+    if fs:
+        sh = {"w_gu_s": bf16(rng, 2 * fs, d, scale=d ** -0.5).cuda(), "w_d_s": bf16(rng, d, fs, scale=fs ** -0.5).cuda()}
+    b = layer.allocate(layer.dims_of(T, d, f, E, k, f_shared=fs, score=c["score"], prec="fp8-block"))
+    layer.forward(b, x, logits, w["gu"], w["d"], **sh)
+    fwd_h = b.q.h.codes.clone(), b.q.h.scales.clone()
+    layer.backward(b, dy, logits, w["gu"], w["d"], x=x, **sh)
+    layer.check(b)
+    off = b.row_offsets.cpu().tolist()
+    n = off[-1]
+    idx = b.topk_idx.cpu().numpy()
+    assert b.split_sizes.sum() == T * k
+    tok = b.row_to_token[:n].cpu().numpy()
+    wr = b.w_rows[:n].double().cpu().numpy()
+
+    def routed(a):
+        return np.where(tok[:, None] >= 0, a.float().cpu().numpy()[np.maximum(tok, 0)], 0.0) if T else np.zeros((0, d), np.float32)
+
+    for q, src in ((b.q.x, x), (b.q.dy, dy)):
+        if n:
+            cc, ss = ob.quantize_rows(routed(src))
+            same_codes(q.codes[:n], cc)
+            assert np.array_equal(q.scales[:, :n].cpu().numpy(), ss)
+            cc, ss = ob.quantize_columns(routed(src))
+            same_codes(q.codes_t[:, :n].contiguous(), cc)
+            assert np.array_equal(q.scales_t[: n // 128].cpu().numpy(), ss)
+    vw = {n_: ob.weights_values(w_.codes.cpu(), w_.scales.cpu().numpy()) for n_, w_ in (("gu", b.q.gu), ("d", b.q.down))}
+    qc, qs = ob.quantize_weights(w["gu"].float().cpu().numpy())
+    same_codes(b.q.gu.codes, qc)
+
+    def val(r, codes=None, scales=None):
+        return ob.rows_values((r.codes if codes is None else codes)[:n].cpu(), (r.scales if scales is None else scales)[:, :n].cpu().numpy())
+
+    def cols(r):
+        return ob.rows_values(r.codes_t[:, :n].cpu(), r.scales_t[: n // 128].cpu().numpy()).T
+
+    ref, mag = ob.product(val(b.q.x), vw["gu"], off)
+    close(b.gu[:n], ref, mag, d)
+    gu = b.gu[:n].double().cpu().numpy()
+    hr = ob.swiglu(gu[:, :f], gu[:, f:], wr)
+    if n:
+        stands_for(fwd_h[0][:n], fwd_h[1][:, :n], hr)
+        stands_for(b.q.h.codes_t[:, :n], b.q.h.scales_t[: n // 128], hr.T)
+    ref, mag = ob.product(val(b.q.h, *fwd_h), vw["d"], off)
+    close(b.y_rows[:n], ref, mag, f)
+    rows_of = b.token_to_row.cpu().numpy()
+    yr = b.y_rows.float().cpu().numpy()
+    y = yr[rows_of].astype(np.float64).sum(1) if T else np.zeros((0, d))
+    extra = b.y_s.double().cpu().numpy() if fs else 0.0
+    close(b.y, y + extra, np.abs(y) + np.abs(extra) + np.abs(yr[rows_of]).sum(1) if T else y, k + 1)
+    # backward
+    ref, mag = ob.product(val(b.q.dy), vw["d"].transpose(0, 2, 1), off)
+    close(b.q.dh[:n], ref, mag, d)
+    dh = b.q.dh[:n].double().cpu().numpy()
+    dG, dU, dws = ob.swiglu_bwd(gu[:, :f], gu[:, f:], wr, dh)
+    if n:
+        stands_for(b.q.dgu.codes[:n], b.q.dgu.scales[:, :n], np.concatenate([dG, dU], 1), gradient_terms(gu[:, :f], gu[:, f:], wr, dh))
+        assert np.allclose(b.dw_rows[:n].cpu().numpy(), dws, rtol=0, atol=(f + 64) * ob.U32 * 50)
+    ref, mag = ob.product(val(b.q.dgu), vw["gu"].transpose(0, 2, 1), off)
+    close(b.dxp[:n], ref, mag, 2 * f)
+    for got, a, bb in ((b.dw_d, b.q.dy, b.q.h), (b.dw_gu, b.q.dgu, b.q.x)):
+        ref, mag = ob.weight_grad(cols(a), cols(bb), off)
+        close(got, ref, mag, max(128, max(np.diff(off))))
+    if fs and T:
+        q = b.q_s
+        cc, ss = ob.quantize_rows(x.float().cpu().numpy())
+        same_codes(q.x.codes, cc)
+        gs = b.gu_s.double().cpu().numpy()
+        ref, mag = ob.product(ob.rows_values(cc, ss), ob.weights_values(q.gu.codes.cpu(), q.gu.scales.cpu().numpy()))
+        close(b.gu_s, ref, mag, d)
+        ref, mag = ob.product(ob.rows_values(q.dgu.codes.cpu(), q.dgu.scales.cpu().numpy()),
+                              ob.weights_values(q.gu.codes.cpu(), q.gu.scales.cpu().numpy()).transpose(0, 2, 1))
+        close(b.dx_s, ref, mag, 2 * fs)
+        ref, mag = ob.weight_grad(ob.rows_values(q.dgu.codes_t.cpu(), q.dgu.scales_t.cpu().numpy()).T,
+                                  ob.rows_values(q.x.codes_t.cpu(), q.x.scales_t.cpu().numpy()).T)
+        close(b.dw_gu_s, ref[0], mag[0], T)
+        stands_for(q.h.codes_t, q.h.scales_t, np.concatenate([ob.swiglu(gs[:, :fs], gs[:, fs:], np.ones(T)), np.zeros((ob.up(T) - T, fs))]).T)
+    assert idx.shape == (T, k)
+
+
+def test_layer_serving_form():
+    """train=False with a checkpoint's weights gives the training form's output; backward is refused."""
+    from dropless_mixture_experts_warp_gb300 import fp8, layer
+    rng = np.random.default_rng(9)
+    T, d, f, E, k = 33, 256, 128, 8, 2
+    x = bf16(rng, T, d).cuda()
+    logits = torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    w_gu, w_d = bf16(rng, E, 2 * f, d, scale=0.06).cuda(), bf16(rng, E, d, f, scale=0.09).cuda()
+    dims = layer.dims_of(T, d, f, E, k, prec="fp8-block")
+    full, lean = layer.allocate(dims), layer.allocate(dims, train=False)
+    y = layer.forward(full, x, logits, w_gu, w_d).clone()
+    with pytest.raises(ValueError):
+        layer.forward(lean, x, logits, None, None, weights_cached=True)
+    layer.use_weights(lean, fp8.weights_of(full.q.gu.codes, full.q.gu.scales), fp8.weights_of(full.q.down.codes, full.q.down.scales))
+    assert torch.equal(layer.forward(lean, x, logits, None, None, weights_cached=True), y)
+    with pytest.raises(ValueError):
+        layer.backward(lean, x, logits, None, None)
