@@ -73,6 +73,20 @@ class moe_adamw_hyper(ctypes.Structure):
                 ("bits", ctypes.c_int32)]
 
 
+MUON_MAX_STEPS = 16
+
+
+class moe_muon_tensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("w", ctypes.c_void_p), ("w16", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("batch", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("weight_decay", ctypes.c_float), ("grad_type", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
+class moe_muon_hyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("momentum", ctypes.c_double), ("rms", ctypes.c_double),
+                ("nesterov", ctypes.c_int32), ("steps", ctypes.c_int32), ("coefficients", ctypes.c_float * (3 * MUON_MAX_STEPS))]
+
+
 def make_dims(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> moe_dims:
     return moe_dims(T, d, f, E, k, f_shared, SCORE[score] if isinstance(score, str) else score,
                     PREC[prec] if isinstance(prec, str) else prec)
@@ -85,6 +99,7 @@ _N = ctypes.POINTER(moe_norm_dims)
 _L = ctypes.POINTER(moe_balance_dims)
 _T = ctypes.POINTER(moe_adamw_tensor)
 _PP = ctypes.POINTER(ctypes.c_void_p)
+_U = ctypes.POINTER(moe_muon_tensor)
 
 # name -> (restype, argtypes)
 SIGNATURES = {
@@ -159,6 +174,8 @@ SIGNATURES = {
     "moe_balance_bwd": (ctypes.c_int32, [_L] + [_P] * 6 + [_I, _P, _P]),
     "moe_adamw_step": (ctypes.c_int32, [ctypes.POINTER(moe_adamw_hyper), _T, _I, _P, _P]),
     "moe_adamw_values": (ctypes.c_int32, [_T, _I, _I, _PP, _PP, _P]),
+    "moe_muon_workspace_size": (ctypes.c_size_t, [_U, _I, ctypes.c_size_t]),
+    "moe_muon_step": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, _P, ctypes.c_size_t, _P, _P, _P]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -621,3 +638,13 @@ def moe_adamw_step(hyper, tensors, count, control=None, stream=None):
 def moe_adamw_values(tensors, count, out_type, m_out, v_out, stream=None):
     """m_out, v_out: ctypes arrays of `count` device pointers."""
     return _call("moe_adamw_values", tensors, count, out_type, m_out, v_out, _stream(stream))
+
+
+def moe_muon_workspace_size(tensors, count, limit) -> int:
+    return lib().moe_muon_workspace_size(tensors, count, limit)
+
+
+def moe_muon_step(hyper, tensors, count, workspace, workspace_bytes, control=None, dev_status=None, stream=None):
+    """hyper: a moe_muon_hyper; tensors: a ctypes array of `count` moe_muon_tensor."""
+    return _call("moe_muon_step", None if hyper is None else ctypes.byref(hyper), tensors, count, _ptr(workspace),
+                 workspace_bytes, _ptr(control), _ptr(dev_status), _stream(stream))

@@ -17,7 +17,7 @@ OUT = os.path.join(HERE, "libmoe.so")
 BUILD_DIR = os.path.join(os.path.dirname(HERE), "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "route.cu", "gemm_fwd.cu", "gemm_bwd.cu", "noalloc.cu", "quant.cu", "gemm_mx.cu", "api_mx.cu", "gemm_pair.cu", "gemm_mx_pair.cu",
-           "norm.cu", "balance.cu", "adamw.cu", "fp8_quant.cu", "fp8_gemm.cu"]
+           "norm.cu", "balance.cu", "adamw.cu", "fp8_quant.cu", "fp8_gemm.cu", "muon.cu"]
 
 
 def nvcc() -> str:

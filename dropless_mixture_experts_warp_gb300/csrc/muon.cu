@@ -1,0 +1,604 @@
+// An update orthogonalised by Newton-Schulz products, for batches of matrices.
+//
+//   X_0 = U / |U|_F;   A = X X^T;  B = b A + c A A;  X' = a X + B X      (a, b, c of each step)
+//
+// on the side with fewer rows: X is [s][l], s <= l, in the workspace, transposed where the
+// tensor is tall, and padded with zeros to multiples of 128 (which the products keep at zero).
+//
+// Arithmetic: the products run on fp16 operands with fp32 sums.  Every matrix here is bounded (singular
+// values below 1.3), so fp16's 11 bits serve better than bf16's 8: on gaussian matrices the result is
+// 1.3e-3 off (bf16 operands: 1.1e-2).  X is held times a power of two near sqrt(l), so that its entries stay
+// normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
+// values, which later steps amplify by up to a each; for the first steps X is therefore kept in two fp16
+// parts, the second read for that addend alone (low-rank plus noise: 3.5e-3 off without, 5e-4 with three steps).
+// A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
+//
+// Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.
+#include "around.cuh"
+#include "kernels.h"
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <vector>
+
+namespace moe {
+
+constexpr int NS_STAGES = 5;
+constexpr int NS_EPI_WARPS = 8;
+constexpr int NS_THREADS = 64 + 32 * NS_EPI_WARPS;
+constexpr int NS_BOX = 2048;                       // a 32 x 32 box of 16-bit values
+constexpr int NS_EPI_BYTES = 4 * NS_BOX;           // a warp's boxes: two read, two written
+constexpr int NS_SMEM = NS_STAGES * P_STAGE_BYTES + NS_EPI_WARPS * NS_EPI_BYTES + 1024;
+
+enum { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };   // A = X X^T; B = b A + c A A; X' = a X + B X
+
+struct NsParams {
+  int batch, s, n, k;       // a matrix's padded rows, output columns, contraction
+  float alpha, beta;        // out = alpha * product + beta * in
+  int lo_in, lo_out;        // NS_APPLY: X's second part is read, written
+  int32_t* status;
+};
+
+// kind::f16 with fp16 A and B, fp32 D; see idesc_bf16.
+__host__ __device__ constexpr uint32_t idesc_fp16(int M, int N, int b_mn) {
+  return (1u << 4) | (static_cast<uint32_t>(b_mn) << 16) | (static_cast<uint32_t>(N >> 3) << 17) |
+         (static_cast<uint32_t>(M >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 half_pair(uint32_t w) { return __half22float2(*reinterpret_cast<const __half2*>(&w)); }
+
+struct NsTile {
+  int e, m, n;   // matrix, 256-row block, 256-column block
+};
+template <int KIND>
+__device__ __forceinline__ NsTile ns_tile(const NsParams& p, int t) {
+  const int mt = (p.s + 255) / 256, nt = (p.n + 255) / 256;
+  NsTile o;
+  if (KIND == NS_APPLY) {
+    const int per = mt * nt;
+    o.e = t / per;
+    const int r = t - o.e * per;
+    o.n = r / mt;
+    o.m = r - o.n * mt;
+  } else {                                          // n >= m, column by column
+    const int per = mt * (mt + 1) / 2;
+    o.e = t / per;
+    int r = t - o.e * per, n = 0;
+    while (r > n) r -= ++n;
+    o.n = n;
+    o.m = r;
+  }
+  return o;
+}
+
+// One CTA pair computes a 256 x 256 tile (tcgen05 cta_group::2), as in gemm2.cuh: warp 0 of each
+// CTA loads its halves, warp 1 of the leader multiplies, eight warps of each take its 128 rows out.
+// What the sum is added to arrives by tensor loads in a warp's boxes, a chunk ahead.
+template <int KIND>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
+    ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmIn, const __grid_constant__ CUtensorMap tmInLo,
+                   const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmOutLo, const NsParams p) {
+  constexpr bool B_MN = KIND == NS_APPLY;
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ __align__(8) uint64_t full_bar[NS_STAGES];
+  __shared__ __align__(8) uint64_t empty_bar[NS_STAGES];
+  __shared__ __align__(8) uint64_t tfull_bar[2];
+  __shared__ __align__(8) uint64_t tempty_bar[2];
+  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t in_bar[NS_EPI_WARPS];
+  __shared__ uint32_t s_tmem_base;
+  __shared__ int s_abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = static_cast<int>(cluster_ctarank());
+  const int pair_id = blockIdx.x >> 1, npairs = gridDim.x >> 1;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~static_cast<uintptr_t>(1023));
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < NS_STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], 1); }
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], 1); mbar_init(&tempty_bar[a], 2 * NS_EPI_WARPS); }
+    for (int w = 0; w < NS_EPI_WARPS; ++w) mbar_init(&in_bar[w], 1);
+    mbar_init(&drain_bar, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) { tmem_alloc_pair(&s_tmem_base, TMEM_COLS); tmem_relinquish_pair(); }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  wait_for_previous();
+  launch_dependents();
+  const uint32_t tmem_base = s_tmem_base;
+  const int mt = (p.s + 255) / 256;
+  const int total = p.batch * (KIND == NS_APPLY ? mt * ((p.n + 255) / 256) : mt * (mt + 1) / 2);
+  const int kblocks = p.k / BK;
+  volatile int* abort_flag = &s_abort;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0, armed = 0, armed_parity = 0;
+      bool ok = true;
+      for (int t = pair_id; ok && t < total; t += npairs) {
+        const NsTile c = ns_tile<KIND>(p, t);
+        // a half past the matrix's rows (or columns) reads the zero fill past the tensor
+        const int a_local = c.m * 256 + rank * 128, b_local = c.n * 256 + rank * 128;
+        const int a_row = a_local < p.s ? c.e * p.s + a_local : DEAD_ROW;
+        const int b_row = b_local < p.n ? c.e * p.s + b_local : DEAD_ROW;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
+          uint8_t* sa = smem + stage * P_STAGE_BYTES;
+          uint8_t* sb = sa + P_A_BYTES;
+          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+          if (rank == 0) {
+            mbar_arrive_expect_tx(&full_bar[stage], 2 * P_STAGE_BYTES);
+            armed |= 1u << stage;
+            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+          }
+          tma_load_2d_pair(sa, &tmA, bar, kb * BK, a_row);
+          if (!B_MN) {
+            tma_load_2d_pair(sb, &tmB, bar, kb * BK, b_row);
+          } else {
+            tma_load_2d_pair(sb, &tmB, bar, b_local, c.e * p.s + kb * BK);
+            tma_load_2d_pair(sb + 8192, &tmB, bar, b_local + 64, c.e * p.s + kb * BK);
+          }
+          if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
+        }
+      }
+      if (rank == 0)
+        for (int s = 0; s < NS_STAGES; ++s)
+          if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      constexpr uint32_t idesc = idesc_fp16(256, 256, B_MN ? 1 : 0);
+      int stage = 0, acc = 0;
+      uint32_t phase = 0, acc_phase = 0;
+      bool ok = true;
+      for (int t = pair_id; ok && t < total; t += npairs) {
+        if (!mbar_wait_bounded(&tempty_bar[acc], acc_phase ^ 1, abort_flag, p.status, WAIT_LIMIT_CYCLES)) break;
+        tc_fence_after();
+        const uint32_t d_tmem = tmem_base + acc * ACC_STRIDE;
+        for (int kb = 0; kb < kblocks; ++kb) {
+          if (!mbar_wait_bounded(&full_bar[stage], phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
+          tc_fence_after();
+          const uint32_t sa = smem_u32(smem + stage * P_STAGE_BYTES), sb = sa + P_A_BYTES;
+#pragma unroll
+          for (int kk = 0; kk < BK / UMMA_K; ++kk)
+            tc_mma_f16_pair(d_tmem, smem_desc_sw128(sa + kk * 32, 16, 1024),
+                            B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 16, 1024), idesc,
+                            (kb | kk) != 0 ? 1u : 0u);
+          tc_commit_pair_mc(&empty_bar[stage], 0x3);
+          if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
+        }
+        if (!ok) break;
+        tc_commit_pair_mc(&tfull_bar[acc], 0x3);
+        if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+      }
+      tc_commit_pair(&drain_bar);
+      mbar_drain(&drain_bar, 0, WAIT_LIMIT_CYCLES);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    uint8_t* in = smem + NS_STAGES * P_STAGE_BYTES + (warp - 2) * NS_EPI_BYTES;
+    uint8_t* out = in + 2 * NS_BOX;
+    uint64_t* ibar = &in_bar[warp - 2];
+    const int sw = (lane >> 1) & 3;                  // 64-byte swizzle of this lane's row of a box
+    const uint32_t in_row = smem_u32(in) + lane * 64, out_row = smem_u32(out) + lane * 64;
+    int acc = 0;
+    uint32_t acc_phase = 0, in_phase = 0;
+    bool inflight = false;
+    auto issue = [&](int x, int y) {                 // the boxes that the sum at (x, y) is added to
+      if (KIND == NS_GRAM) return;
+      if (lane == 0) {
+        fence_proxy_async_smem();
+        mbar_arrive_expect_tx(ibar, KIND == NS_APPLY && p.lo_in ? 2 * NS_BOX : NS_BOX);
+        tma_load_2d(in, &tmIn, ibar, x, y);
+        if (KIND == NS_APPLY && p.lo_in) tma_load_2d(in + NS_BOX, &tmInLo, ibar, x, y);
+      }
+      inflight = true;
+    };
+    for (int t = pair_id; t < total; t += npairs) {
+      const NsTile c = ns_tile<KIND>(p, t);
+      const int row0 = c.m * 256 + rank * 128 + q * 32;          // of the matrix
+      const int col0 = c.n * 256 + half * 128;
+      const bool live = row0 < p.s && col0 < p.n;                // 128-row and 128-column halves are whole
+      const int y = c.e * p.s + row0;
+      if (live) issue(col0, y);
+      if (!mbar_wait_bounded(&tfull_bar[acc], acc_phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) break;
+      tc_fence_after();
+      const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * ACC_STRIDE + half * 128;
+      bool ok = true;
+      if (live) {
+        for (int i = 0; i < 4; ++i) {
+          uint32_t r[32];
+          tmem_ld32(tbase + 32 * i, r);
+          uint32_t hi[16], lo[16];
+          if (KIND != NS_GRAM) {
+            if (!mbar_wait_bounded(ibar, in_phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
+            in_phase ^= 1u;
+            inflight = false;
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const uint4 x = ld_shared_v4(in_row + ((v ^ sw) << 4));
+              const uint4 z = KIND == NS_APPLY && p.lo_in ? ld_shared_v4(in_row + NS_BOX + ((v ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+              hi[4 * v] = x.x; hi[4 * v + 1] = x.y; hi[4 * v + 2] = x.z; hi[4 * v + 3] = x.w;
+              lo[4 * v] = z.x; lo[4 * v + 1] = z.y; lo[4 * v + 2] = z.z; lo[4 * v + 3] = z.w;
+            }
+            __syncwarp();
+            if (i < 3) issue(col0 + 32 * (i + 1), y);
+          }
+          tmem_wait_ld();
+          uint32_t oh[16], ol[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float a = p.alpha * __uint_as_float(r[2 * j]), b = p.alpha * __uint_as_float(r[2 * j + 1]);
+            if (KIND != NS_GRAM) {
+              const float2 x = half_pair(hi[j]), z = half_pair(lo[j]);
+              a = fmaf(p.beta, x.x + z.x, a);
+              b = fmaf(p.beta, x.y + z.y, b);
+            }
+            oh[j] = pack_half(a, b);
+            if (KIND == NS_APPLY) {
+              const float2 h = half_pair(oh[j]);
+              ol[j] = pack_half(a - h.x, b - h.y);
+            }
+          }
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            st_shared_v4(out_row + ((v ^ sw) << 4), oh[4 * v], oh[4 * v + 1], oh[4 * v + 2], oh[4 * v + 3]);
+            if (KIND == NS_APPLY && p.lo_out)
+              st_shared_v4(out_row + NS_BOX + ((v ^ sw) << 4), ol[4 * v], ol[4 * v + 1], ol[4 * v + 2], ol[4 * v + 3]);
+          }
+          const bool mirror = KIND != NS_APPLY && c.n > c.m;
+          if (mirror) {
+            // the box's transpose: two rows' values of a column meet in one word
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              const uint32_t other = __shfl_xor_sync(0xffffffffu, oh[j], 1);
+              // even lanes take column 2j of rows (lane, lane + 1), odd ones column 2j + 1 of (lane - 1, lane)
+              const uint32_t w = lane & 1 ? __byte_perm(other, oh[j], 0x7632) : __byte_perm(oh[j], other, 0x5410);
+              const int col = 2 * j + (lane & 1);
+              *reinterpret_cast<uint32_t*>(out + NS_BOX + col * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) = w;
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(&tmOut, out, col0 + 32 * i, y);
+            if (KIND == NS_APPLY && p.lo_out) tma_store_2d(&tmOutLo, out + NS_BOX, col0 + 32 * i, y);
+            if (mirror) tma_store_2d(&tmOut, out + NS_BOX, row0, c.e * p.s + col0 + 32 * i);
+            bulk_commit();
+          }
+        }
+      }
+      if (!ok) break;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+      if (++acc == 2) { acc = 0; acc_phase ^= 1; }
+    }
+    if (inflight) mbar_drain(ibar, in_phase, WAIT_LIMIT_CYCLES);
+    if (lane == 0) bulk_wait_all();
+  }
+  tc_fence_before();
+  cluster_sync_all();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, TMEM_COLS);
+}
+
+// ------------------------------------------------------------------------ around the products
+
+constexpr int NS_TENSORS = 32;       // of a launch
+constexpr int NS_PARTS = 64;         // blocks, and partial sums of squares, a matrix at most
+
+// Tensors of one shape, their matrices numbered through.
+struct NsTensors {
+  const void* grad[NS_TENSORS];
+  float* m[NS_TENSORS];              // NULL: the gradient itself is orthogonalised
+  float* w[NS_TENSORS];
+  moe_bf16* w16[NS_TENSORS];
+  void* out[NS_TENSORS];
+  float decay[NS_TENSORS];
+  int first[NS_TENSORS + 1];         // its first matrix
+  int skip0;                         // matrices of the first tensor that an earlier chunk had
+  int count;
+  int grad_type, out_type;
+  int rows, cols;                    // of a matrix
+  float momentum;
+  int nesterov;
+  const moe_adamw_control* control;
+};
+__device__ __forceinline__ int ns_find(const NsTensors& p, int e) {
+  int i = 0;
+  while (i + 1 < p.count && p.first[i + 1] <= e) ++i;
+  return i;
+}
+__device__ __forceinline__ long long ns_base(const NsTensors& p, int i, int e) {
+  return static_cast<long long>(e - p.first[i] + (i == 0 ? p.skip0 : 0)) * p.rows * p.cols;
+}
+__device__ __forceinline__ float ns_load(const void* g, int type, long long i) {
+  return type == MOE_TYPE_BF16 ? bf16_lo(static_cast<const uint16_t*>(g)[i]) : static_cast<const float*>(g)[i];
+}
+
+// m = momentum m + scale g; the sum of squares of what is orthogonalised, in NS_PARTS parts a matrix.
+__global__ void __launch_bounds__(256) ns_momentum_kernel(const NsTensors p, float* parts) {
+  wait_for_previous();
+  launch_dependents();
+  __shared__ float buf[32];
+  const int e = blockIdx.y, i = ns_find(p, e);
+  const bool skip = p.control && p.control->skip;
+  const float gs = p.control ? p.control->grad_scale : 1.0f;
+  const long long n = static_cast<long long>(p.rows) * p.cols, base = ns_base(p, i, e);
+  float s[1] = {0.0f};
+  float* m = p.m[i];
+  for (long long j = blockIdx.x * 256ll + threadIdx.x; j < n && !skip; j += gridDim.x * 256ll) {
+    float u = gs * ns_load(p.grad[i], p.grad_type, base + j);
+    if (m) {
+      const float v = fmaf(p.momentum, m[base + j], u);
+      m[base + j] = v;
+      u = p.nesterov ? fmaf(p.momentum, v, u) : v;
+    }
+    s[0] = fmaf(u, u, s[0]);
+  }
+  row_sums<false>(s, buf);
+  if (threadIdx.x == 0) parts[e * NS_PARTS + blockIdx.x] = s[0];
+}
+
+// X = scale U / |U| in two fp16 parts, [s][l] with zeros in the padding, transposed where the tensor is tall.
+// 32 x 32 tiles of X through shared memory.
+__global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const float* parts, int nparts, int s, int l, float scale,
+                                                      __half* hi, __half* lo) {
+  wait_for_previous();
+  launch_dependents();
+  __shared__ float tile[32][33];
+  const int e = blockIdx.z, i = ns_find(p, e);
+  const float gs = p.control ? p.control->grad_scale : 1.0f;
+  const bool tall = p.rows > p.cols;
+  float sum = 0.0f;
+  for (int j = 0; j < nparts; ++j) sum += parts[e * NS_PARTS + j];
+  // an overflowed sum makes NaNs rather than a silent zero
+  const float inv = sum > 0.0f ? (isinf(sum) ? __int_as_float(0x7fc00000) : scale / sqrtf(sum)) : (sum == 0.0f ? 0.0f : sum);
+  const long long base = ns_base(p, i, e);
+  const int x0 = blockIdx.x * 32, y0 = blockIdx.y * 32;       // of X
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = (tall ? x0 : y0) + ty + 8 * k, c = (tall ? y0 : x0) + tx;   // of the tensor
+    float u = 0.0f;
+    if (r < p.rows && c < p.cols) {
+      const long long at = base + static_cast<long long>(r) * p.cols + c;
+      u = gs * ns_load(p.grad[i], p.grad_type, at);
+      if (p.m[i]) u = p.nesterov ? fmaf(p.momentum, p.m[i][at], u) : p.m[i][at];
+    }
+    tile[ty + 8 * k][tx] = u * inv;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float v = tall ? tile[tx][ty + 8 * k] : tile[ty + 8 * k][tx];
+    const long long at = (static_cast<long long>(e) * s + y0 + ty + 8 * k) * l + x0 + tx;
+    const __half h = __float2half_rn(v);
+    hi[at] = h;
+    lo[at] = __float2half_rn(v - __half2float(h));
+  }
+}
+
+// w = w - lr (decay w + rms sqrt(max side) X), or out = X.
+__global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const __half* x, int s, int l, float unscale, float lr,
+                                                        float rms) {
+  wait_for_previous();
+  launch_dependents();
+  __shared__ float tile[32][33];
+  const int e = blockIdx.z, i = ns_find(p, e);
+  if (p.control && p.control->skip) return;
+  const float rate = p.control ? lr * p.control->lr_scale : lr;
+  const bool tall = p.rows > p.cols;
+  const int x0 = blockIdx.x * 32, y0 = blockIdx.y * 32;       // of the tensor
+  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = (tall ? x0 : y0) + ty + 8 * k, c = (tall ? y0 : x0) + tx;   // of X
+    tile[ty + 8 * k][tx] = r < s && c < l ? unscale * __half2float(x[(static_cast<long long>(e) * s + r) * l + c]) : 0.0f;
+  }
+  __syncthreads();
+  const long long base = ns_base(p, i, e);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int r = y0 + ty + 8 * k, c = x0 + tx;
+    if (r >= p.rows || c >= p.cols) continue;
+    const float v = tall ? tile[tx][ty + 8 * k] : tile[ty + 8 * k][tx];
+    const long long at = base + static_cast<long long>(r) * p.cols + c;
+    if (p.out[i]) {
+      if (p.out_type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(p.out[i])[at] = __float2bfloat16_rn(v);
+      else static_cast<float*>(p.out[i])[at] = v;
+    } else {
+      const float w = p.w[i][at];
+      const float nw = fmaf(-rate, fmaf(p.decay[i], w, rms * v), w);
+      p.w[i][at] = nw;
+      if (p.w16[i]) reinterpret_cast<__nv_bfloat16*>(p.w16[i])[at] = __float2bfloat16_rn(nw);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ host
+
+struct NsShape {
+  int s, l;                    // padded sides, s <= l
+  size_t x, a;                 // bytes of X (one part) and of A, a matrix
+};
+static NsShape ns_shape(int rows, int cols) {
+  NsShape o;
+  o.s = (std::min(rows, cols) + 127) / 128 * 128;
+  o.l = (std::max(rows, cols) + 127) / 128 * 128;
+  o.x = static_cast<size_t>(o.s) * o.l * 2;
+  o.a = static_cast<size_t>(o.s) * o.s * 2;
+  return o;
+}
+// X twice (a step reads one and writes the other), its second part, A, B, the partial sums
+static size_t ns_matrix_bytes(const NsShape& o) { return 3 * o.x + 2 * o.a + NS_PARTS * sizeof(float); }
+
+template <int KIND>
+static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_lo,
+                             const CUtensorMap& out, const CUtensorMap& out_lo, const NsParams& p, cudaStream_t s) {
+  auto kern = ns_gemm_kernel<KIND>;
+  const cudaError_t err = allow_smem<ns_gemm_kernel<KIND>>(NS_SMEM);
+  if (err != cudaSuccess) return err;
+  static const int most = pair_grid(reinterpret_cast<const void*>(kern), NS_THREADS, NS_SMEM);
+  const int mt = (p.s + 255) / 256;
+  const long long tiles = static_cast<long long>(p.batch) * (KIND == NS_APPLY ? mt * ((p.n + 255) / 256) : mt * (mt + 1) / 2);
+  const int grid = static_cast<int>(2 * tiles < most ? 2 * tiles : most);
+  return launch_early(kern, dim3(grid), dim3(NS_THREADS), NS_SMEM, s, a, b, in, in_lo, out, out_lo, p);
+}
+
+constexpr int NS_KEEP = 3;           // steps whose addend takes X in two parts
+
+// `batch` matrices of one shape: products, update.
+static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float lr, void* workspace, int32_t* status,
+                            cudaStream_t st) {
+  const NsShape o = ns_shape(t.rows, t.cols);
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  __half* x[2] = {reinterpret_cast<__half*>(w), reinterpret_cast<__half*>(w + batch * o.x)};
+  __half* lo = reinterpret_cast<__half*>(w + 2 * batch * o.x);
+  uint8_t* A = w + 3 * batch * o.x;
+  uint8_t* B = A + batch * o.a;
+  float* parts = reinterpret_cast<float*>(B + batch * o.a);
+  const long long n = static_cast<long long>(t.rows) * t.cols;
+  const int nparts = static_cast<int>(std::min<long long>(NS_PARTS, (n + 2047) / 2048));
+  float scale = 1.0f;
+  while (scale * scale * 4.0f <= o.l) scale *= 2.0f;
+  cudaError_t err = launch_early(ns_momentum_kernel, dim3(nparts, batch), dim3(256), 0, st, t, parts);
+  if (err != cudaSuccess) return err;
+  err = launch_early(ns_load_kernel, dim3(o.l / 32, o.s / 32, batch), dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo);
+  if (err != cudaSuccess) return err;
+  const uint64_t rows = static_cast<uint64_t>(batch) * o.s;
+  CUtensorMap xk[2], xn[2], xs[2], los, ak, as, bk, bs;
+  bool ok = make_tensor_map_store(&los, lo, o.l, o.l, rows) && make_tensor_map_bf16(&ak, A, o.s, rows, 64, 128) &&
+            make_tensor_map_store(&as, A, o.s, o.s, rows) && make_tensor_map_bf16(&bk, B, o.s, rows, 64, 128) &&
+            make_tensor_map_store(&bs, B, o.s, o.s, rows);
+  for (int i = 0; i < 2; ++i)
+    ok = ok && make_tensor_map_bf16(&xk[i], x[i], o.l, rows, 64, 128) && make_tensor_map_bf16(&xn[i], x[i], o.l, rows, 64, 64) &&
+         make_tensor_map_store(&xs[i], x[i], o.l, o.l, rows);
+  if (!ok) return cudaErrorInvalidValue;
+  int cur = 0;
+  for (int k = 0; k < h.steps; ++k, cur ^= 1) {
+    const float a = h.coefficients[3 * k], b = h.coefficients[3 * k + 1], c = h.coefficients[3 * k + 2];
+    NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, 0, 0, status};
+    err = launch_ns<NS_GRAM>(xk[cur], xk[cur], as, as, as, as, p, st);
+    if (err != cudaSuccess) return err;
+    p.k = o.s; p.alpha = c; p.beta = b;
+    err = launch_ns<NS_POLY>(ak, ak, as, as, bs, bs, p, st);
+    if (err != cudaSuccess) return err;
+    p.n = o.l; p.alpha = 1.0f; p.beta = a;
+    p.lo_in = k < NS_KEEP; p.lo_out = k + 1 < NS_KEEP && k + 1 < h.steps;
+    err = launch_ns<NS_APPLY>(bk, xn[cur], xs[cur], los, xs[cur ^ 1], los, p, st);
+    if (err != cudaSuccess) return err;
+  }
+  const float rms = static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(t.rows, t.cols))));
+  return launch_early(ns_update_kernel, dim3((t.cols + 31) / 32, (t.rows + 31) / 32, batch), dim3(256), 0, st, t, x[cur], o.s, o.l,
+                      1.0f / scale, lr, rms);
+}
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+static moe_status muon_check(const moe_muon_tensor* ts, int32_t count) {
+  if (count < 0 || (count > 0 && !ts)) return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < count; ++i) {
+    const moe_muon_tensor& t = ts[i];
+    if (t.batch < 0 || t.rows <= 0 || t.cols <= 0) return MOE_ERR_INVALID_ARG;
+    if (t.rows > 65536 || t.cols > 65536 || static_cast<int64_t>(t.batch) * ns_shape(t.rows, t.cols).s >= (1ll << 30)) return MOE_ERR_UNSUPPORTED;
+    if (t.grad_type != MOE_TYPE_BF16 && t.grad_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+    if (t.out_type != MOE_TYPE_BF16 && t.out_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+  }
+  return MOE_OK;
+}
+
+size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t limit) {
+  if (muon_check(tensors, count) != MOE_OK) return 0;
+  size_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    // tensors of one shape run together
+    size_t batch = 0;
+    for (int j = 0; j < count; ++j)
+      if (tensors[j].rows == tensors[i].rows && tensors[j].cols == tensors[i].cols) batch += tensors[j].batch;
+    const size_t one = ns_matrix_bytes(ns_shape(tensors[i].rows, tensors[i].cols));
+    most = std::max(most, one * std::min(batch, std::max<size_t>(1, limit / one)));
+  }
+  return most;
+}
+
+moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
+                         size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream) {
+  if (!hyper || !dev_status) return MOE_ERR_INVALID_ARG;
+  const moe_muon_hyper& h = *hyper;
+  const float lr = static_cast<float>(h.lr);
+  if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.momentum >= 0.0 && h.momentum < 1.0) || !(h.rms >= 0.0) || !std::isfinite(h.rms) ||
+      h.steps < 1 || h.steps > MOE_MUON_MAX_STEPS)
+    return MOE_ERR_INVALID_ARG;
+  for (int i = 0; i < 3 * h.steps; ++i)
+    if (!std::isfinite(h.coefficients[i])) return MOE_ERR_INVALID_ARG;
+  moe_status stc = muon_check(tensors, count);
+  if (stc != MOE_OK) return stc;
+  size_t need = 0;
+  for (int i = 0; i < count; ++i) {
+    const moe_muon_tensor& t = tensors[i];
+    if (t.batch == 0) continue;
+    if (!t.grad || (!t.out == !t.w) || (!t.w != !t.m) || (t.w16 && !t.w)) return MOE_ERR_INVALID_ARG;
+    need = std::max(need, ns_matrix_bytes(ns_shape(t.rows, t.cols)));
+  }
+  if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
+  if (!ptr_aligned16(workspace)) return MOE_ERR_ALIGNMENT;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  std::vector<char> done(static_cast<size_t>(std::max(count, 1)), 0);
+  for (int i = 0; i < count; ++i) {
+    if (done[i] || tensors[i].batch == 0) continue;
+    // the tensors like this one, in order, in chunks that fit the workspace
+    const moe_muon_tensor& f = tensors[i];
+    const int fit = static_cast<int>(std::min<size_t>(workspace_bytes / ns_matrix_bytes(ns_shape(f.rows, f.cols)), 65535));
+    NsTensors t{};
+    t.rows = f.rows; t.cols = f.cols; t.grad_type = f.grad_type; t.out_type = f.out_type;
+    t.momentum = static_cast<float>(h.momentum); t.nesterov = h.nesterov != 0; t.control = control;
+    int batch = 0;
+    auto flush = [&]() -> cudaError_t {
+      if (batch == 0) return cudaSuccess;
+      t.first[t.count] = batch;
+      const cudaError_t e = ns_chunk(t, batch, h, lr, workspace, dev_status, s);
+      t.count = 0; t.skip0 = 0; batch = 0;
+      return e;
+    };
+    for (int j = i; j < count; ++j) {
+      const moe_muon_tensor& g = tensors[j];
+      if (done[j] || g.batch == 0 || g.rows != f.rows || g.cols != f.cols || g.grad_type != f.grad_type || g.out_type != f.out_type ||
+          !g.out != !f.out)
+        continue;
+      done[j] = 1;
+      for (int at = 0; at < g.batch;) {
+        if (batch == fit || t.count == NS_TENSORS) {
+          if (flush() != cudaSuccess) return MOE_ERR_CUDA;
+        }
+        const int take = std::min(g.batch - at, fit - batch), k = t.count++;
+        t.grad[k] = g.grad; t.m[k] = g.m; t.w[k] = g.w; t.w16[k] = g.w16; t.out[k] = g.out; t.decay[k] = g.weight_decay;
+        t.first[k] = batch;
+        if (k == 0) t.skip0 = at;
+        batch += take;
+        at += take;
+      }
+    }
+    if (flush() != cudaSuccess) return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
+}  // extern "C"

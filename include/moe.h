@@ -796,6 +796,46 @@ moe_status moe_adamw_step(const moe_adamw_hyper* hyper, const moe_adamw_tensor* 
 moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int32_t out_type, void* const* m_out,
                             void* const* v_out, void* stream);
 
+/*
+ * An orthogonalised step over a list of tensors, each of `batch` matrices [rows][cols]:
+ *   m = momentum m + grad_scale grad;   U = grad_scale grad + momentum m (nesterov) or m
+ *   X_0 = U / |U|_F (0 where U is 0);   for each step's coefficients a, b, c
+ *     X = a X + b X X^T X + c X X^T X X^T X
+ *   w = w - lr (weight_decay w + rms sqrt(max(rows, cols)) X);   w16 = bf16(w)
+ * m, w and the sum of squares in fp32 (it must not overflow: U is 0 or NaN where it does);
+ * the products on fp16 operands with fp32 sums.  With `out` in place of m and w a tensor's
+ * gradient itself is orthogonalised: out = X, m, w and w16 NULL (momentum, lr and rms are not used).
+ * A gradient that is not finite reaches its whole matrix.
+ */
+enum { MOE_MUON_MAX_STEPS = 16 };
+typedef struct moe_muon_tensor {
+  const void* grad;    /* [batch][rows][cols] grad_type */
+  float* m;            /* momentum, updated */
+  float* w;            /* weights, updated */
+  moe_bf16* w16;       /* bf16 copy of the new weights, or NULL */
+  void* out;           /* out_type; given exactly when m and w are not */
+  int32_t batch, rows, cols;   /* batch >= 0; sides up to 65536 */
+  float weight_decay;
+  int32_t grad_type;   /* MOE_TYPE_* */
+  int32_t out_type;
+} moe_muon_tensor;
+
+typedef struct moe_muon_hyper {
+  double lr, momentum, rms;    /* lr, rms >= 0, 0 <= momentum < 1 */
+  int32_t nesterov;
+  int32_t steps;               /* 1 .. MOE_MUON_MAX_STEPS */
+  float coefficients[3 * MOE_MUON_MAX_STEPS];   /* a, b, c of each */
+} moe_muon_hyper;
+
+/* Scratch for running all matrices of a shape together, or as many as `limit` bytes hold (at
+ * least one). */
+size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t limit);
+
+/* tensors: HOST array (read before the call returns); workspace of workspace_bytes, at least
+ * what one matrix needs; control as in moe_adamw_step (its `step` is not used). */
+moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
+                         size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
