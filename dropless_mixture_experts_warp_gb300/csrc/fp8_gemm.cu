@@ -16,19 +16,34 @@
 // Rows and columns past the operands' ends are read as zeros and not stored.
 #include "fp8.cuh"
 #include "kernels.h"
+#include "pipe.cuh"
 
 namespace moe {
 
 constexpr int F8_K = 128;                                   // codes a stage, a scale block
 constexpr int F8_A_BYTES = BM * F8_K;                       // 16 KB
 constexpr int F8_B_BOX = 128;                               // rows of a B tensor load
-constexpr int F8_EPI_WARPS = 8;                             // two a lane quarter, half of the columns each
-constexpr int F8_THREADS = 64 + 32 * F8_EPI_WARPS;
-__host__ __device__ constexpr int f8_stages(int bn) { return bn == 256 ? 4 : 6; }
+constexpr int F8_EPI_WARPS = 16;                            // four a lane quarter, a quarter of the columns each
+// Warp 0 loads operands, warps 1 and 2 multiply every other block (a block's issue, its waits and commits
+// take one warp longer than its MMA takes), warp 3 loads scales.  The four hand registers to
+// those that hold the sums: 128 x 64 + 512 x 104 are the 640 x 96 of the launch.
+constexpr int F8_EPI_WARP0 = 4;
+constexpr int F8_THREADS = 32 * (F8_EPI_WARP0 + F8_EPI_WARPS);
+constexpr int F8_REGS_FEW = 64, F8_REGS_MANY = 104;
+static_assert(128 * F8_REGS_FEW + 512 * F8_REGS_MANY <= 640 * 96, "registers of the block at launch");
+// Operand stages: as many as shared memory holds beside the output's boxes.  A warp stages its
+// 32 rows at once (BR = 32), or 8 at a time (BR = 8), where a fourth stage is worth more.
+__host__ __device__ constexpr int f8_stages(int bn, int br) { return bn == 256 ? (br == 32 ? 3 : 4) : 5; }
 __host__ __device__ constexpr int f8_stage_bytes(int bn) { return F8_A_BYTES + bn * F8_K; }
-// operand stages, column scales a stage (SCHED_KGROUP), a 2 KB staging box a warp, alignment
-__host__ __device__ constexpr int f8_smem(int bn) {
-  return f8_stages(bn) * (f8_stage_bytes(bn) + bn * 4) + F8_EPI_WARPS * 2048 + 1024;
+__host__ __device__ constexpr int f8_box_bytes(int bn, int br) { return br * bn / 4 * 2; }
+// Scales of a block: the tile's 128 rows, then its columns (SCHED_KGROUP) or the columns' blocks.  The
+// loader is at most the operand stages ahead of the MMAs, these two blocks ahead of the sums, so
+// that with three slots more than stages it never writes one that is still read.
+__host__ __device__ constexpr int f8_slots(int bn, int br) { return f8_stages(bn, br) + 3; }
+__host__ __device__ constexpr int f8_slot_floats(int bn, bool col_scales) { return BM + (col_scales ? bn : 4); }
+__host__ __device__ constexpr int f8_smem(int bn, int br, bool col_scales) {
+  return f8_stages(bn, br) * f8_stage_bytes(bn) + F8_EPI_WARPS * f8_box_bytes(bn, br) +
+         f8_slots(bn, br) * f8_slot_floats(bn, col_scales) * 4 + 1024;
 }
 
 struct Fp8Params {
@@ -44,15 +59,6 @@ struct Fp8Params {
   int32_t* status;
 };
 
-__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                          uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
 // kind::f8f6f4, E4M3 A and B, both K-major, fp32 D: bits 4-5 D format (1 = f32), 7-9 and
 // 10-12 the operands' formats (0 = E4M3), 17-22 N >> 3, 24-28 M >> 4.
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
@@ -73,6 +79,15 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
+// acc += (x, y) * s, kept in its place among the loads: moved past the next ones, the registers that they
+// hold would not fit beside the sums.
+__device__ __forceinline__ void add_scaled(f32x2& acc, uint32_t x, uint32_t y, f32x2 s) {
+  asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(acc) : "r"(x), "r"(y), "l"(s));
+}
+// One fp32 to shared memory, asynchronously; zero where it is not valid.
+__device__ __forceinline__ void scale_async(float* dst, const float* src, bool valid) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
 __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int32_t x, int32_t y, int32_t z) {
   asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                    reinterpret_cast<uint64_t>(tmap)),
@@ -80,19 +95,18 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, 
                : "memory");
 }
 
-template <int SCHED, int BN>
+template <int SCHED, int BN, int BR>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
-  constexpr int STAGES = f8_stages(BN), STAGE_BYTES = f8_stage_bytes(BN);
-  constexpr int WC = BN / 2;       // columns of an epilogue warp
-  constexpr int NC = WC / 32;      // its 32-column boxes of the output
+  constexpr int STAGES = f8_stages(BN, BR), STAGE_BYTES = f8_stage_bytes(BN);
+  constexpr int WC = BN / 4;       // columns of an epilogue warp
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];
   __shared__ __align__(8) uint64_t empty_bar[STAGES];
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
-  __shared__ __align__(8) uint64_t drain_bar;
+  __shared__ __align__(8) uint64_t drain_bar[2];
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
   __shared__ int s_ro[MAX_EXPERTS + 1];
@@ -102,8 +116,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   const int lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* s_sb = reinterpret_cast<float*>(smem + STAGES * STAGE_BYTES);   // [STAGES][BN] column scales
-  uint8_t* s_stage = smem + STAGES * (STAGE_BYTES + BN * 4);
+  constexpr int SLOTS = f8_slots(BN, BR), SLOT = f8_slot_floats(BN, SCHED == SCHED_KGROUP);
+  uint8_t* s_box = smem + STAGES * STAGE_BYTES;
+  float* s_scales = reinterpret_cast<float*>(s_box + F8_EPI_WARPS * f8_box_bytes(BN, BR));
 
   const int E = p.row_offsets ? p.E : 1;
   const int all_rows = (p.rows + F8_K - 1) / F8_K * F8_K;
@@ -116,9 +131,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     snake = kgroup_order(s_ro, E, (p.g.M / BM) * n_tiles, gridDim.x, s_order);  // complete at the barrier below
   }
   if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1); mbar_init(&empty_bar[s], SCHED == SCHED_KGROUP ? F8_EPI_WARPS : 1); }
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1 + 32); mbar_init(&empty_bar[s], 1); }   // full: the tensor loads, the scale loader's lanes
     for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], 1); mbar_init(&tempty_bar[a], F8_EPI_WARPS); }
-    mbar_init(&drain_bar, 1);
+    for (int a = 0; a < 2; ++a) mbar_init(&drain_bar[a], 1);
     s_abort = 0;
     fence_mbar_init();
   }
@@ -133,108 +148,134 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   const int total = (SCHED == SCHED_ROWS) ? (s_ro[E] / BM) * n_tiles : E * (p.g.M / BM) * n_tiles;
-  volatile int* abort_flag = &s_abort;
+  volatile int* const aborted = &s_abort;
+  const uint32_t leader = lane == 0;
 
   if (warp == 0) {
     // ------------------------------------------------------------ TMA producer
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); ok && tile < total;
-           tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-        const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
-        const uint32_t sb_bytes = SCHED == SCHED_KGROUP ? static_cast<uint32_t>(min(BN, p.N - c.out_col)) * 4u : 0u;
-        for (int kb = 0; kb < c.kblocks; ++kb) {
-          if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
-          uint8_t* sa = smem + stage * STAGE_BYTES;
-          uint8_t* sb = sa + F8_A_BYTES;
-          uint64_t* bar = &full_bar[stage];
-          mbar_arrive_expect_tx(bar, STAGE_BYTES + sb_bytes);
-          armed |= 1u << stage;
-          armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          tma_load_2d(sa, &tmA, bar, c.a_k + kb * F8_K, c.a_m);
-#pragma unroll
-          for (int i = 0; i < BN / F8_B_BOX; ++i)
-            tma_load_2d(sb + i * F8_B_BOX * F8_K, &tmB, bar, c.b_k + kb * F8_K, c.b_n + i * F8_B_BOX);
-          if (SCHED == SCHED_KGROUP)
-            bulk_load(s_sb + stage * BN, p.sb + static_cast<long long>(c.b_k / F8_K + kb) * p.sb_k + c.out_col, sb_bytes, bar);
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
-        }
-      }
-      for (int s = 0; s < STAGES; ++s)
-        if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ------------------------------------------------------------ MMA issuer
-    if (lane == 0) {
-      constexpr uint32_t idesc = idesc_f8(BM, BN);
-      int stage = 0;
-      uint32_t phase = 0, it = 0;
-      bool ok = true;
-      for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); ok && tile < total;
-           tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-        const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
-        for (int kb = 0; kb < c.kblocks; ++kb, ++it) {
-          const uint32_t buf = it & 1u;
-          if (!mbar_wait_bounded(&tempty_bar[buf], ((it >> 1) & 1u) ^ 1u, abort_flag, p.status, WAIT_LIMIT_CYCLES) ||
-              !mbar_wait_bounded(&full_bar[stage], phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
-          tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * STAGE_BYTES);
-          const uint32_t sb = sa + F8_A_BYTES;
-#pragma unroll
-          for (int kk = 0; kk < F8_K / 32; ++kk)
-            tc_mma_f8(tmem_base + buf * 256, smem_desc_sw128(sa + kk * 32, 16, 1024), smem_desc_sw128(sb + kk * 32, 16, 1024),
-                      idesc, kk != 0 ? 1u : 0u);
-          // SCHED_KGROUP: the epilogue reads the stage's column scales, so it frees the stage
-          if (SCHED == SCHED_ROWS) tc_commit(&empty_bar[stage]);
-          tc_commit(&tfull_bar[buf]);
-          if (++stage == STAGES) { stage = 0; phase ^= 1; }
-        }
-      }
-      tc_commit(&drain_bar);
-      mbar_drain(&drain_bar, 0, WAIT_LIMIT_CYCLES);
-    }
-    __syncwarp();
-  } else {
-    // ------------------------------------------------------------ sums and stores
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    uint8_t* stg = s_stage + (warp - 2) * 2048;
-    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + half * WC;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
     int stage = 0;
-    uint32_t it = 0;
-    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
          tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
       const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
-      const int row = c.a_m + q * 32 + lane;
-      const int col = c.out_col + half * WC;
-      const bool row_ok = row < (SCHED == SCHED_ROWS ? p.rows : p.M);
-      const float* pa = p.sa + (row_ok ? row : 0) + static_cast<long long>(c.a_k / F8_K) * p.sa_ld;
-      const float* pb = p.sb;
-      if (SCHED == SCHED_ROWS) pb += c.e * p.sb_e + min(col / 128, (p.N - 1) / 128) * p.sb_n;
-      // this row's and (SCHED_ROWS) these columns' scales, two blocks ahead of their use
-      float sa0 = 0.f, sa1 = 0.f, sb0 = 1.f, sb1 = 1.f;
-      if (c.kblocks > 0) { sa0 = pa[0]; if (SCHED == SCHED_ROWS) sb0 = pb[0]; }
-      if (c.kblocks > 1) { sa1 = pa[p.sa_ld]; if (SCHED == SCHED_ROWS) sb1 = pb[p.sb_k]; }
+#pragma unroll 1
+      for (int kb = 0; kb < c.kblocks; ++kb) {
+        pipe_wait(&empty_bar[stage], phase ^ 1, &s_abort, p.status);
+        uint8_t* sa = smem + stage * STAGE_BYTES;
+        uint8_t* sb = sa + F8_A_BYTES;
+        uint64_t* bar = &full_bar[stage];
+        pipe_expect(bar, STAGE_BYTES, leader);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        pipe_load_2d(sa, &tmA, bar, c.a_k + kb * F8_K, c.a_m, leader);
+#pragma unroll
+        for (int i = 0; i < BN / F8_B_BOX; ++i)
+          pipe_load_2d(sb + i * F8_B_BOX * F8_K, &tmB, bar, c.b_k + kb * F8_K, c.b_n + i * F8_B_BOX, leader);
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (lane == 0)
+      for (int s = 0; s < STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
+    __syncwarp();
+  } else if (warp <= 2) {
+    // ------------------------------------------------------------ MMA issuers, a buffer each
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
+    constexpr uint32_t idesc = idesc_f8(BM, BN);
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(smem), 16, 1024);
+    const uint32_t buf = warp - 1, d_tmem = tmem_base + buf * 256;
+    int stage = 0;
+    uint32_t phase = 0, it = 0;
+    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
+      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+#pragma unroll 1
+      for (int kb = 0; kb < c.kblocks; ++kb, ++it) {
+        if ((it & 1u) == buf) {
+          pipe_wait(&tempty_bar[buf], ((it >> 1) & 1u) ^ 1u, &s_abort, p.status);
+          pipe_wait(&full_bar[stage], phase, &s_abort, p.status);
+          tc_fence_after();
+          const uint64_t ad = desc0 + static_cast<uint32_t>(stage * (STAGE_BYTES >> 4)), bd = ad + (F8_A_BYTES >> 4);
+#pragma unroll
+          for (int kk = 0; kk < F8_K / 32; ++kk) pipe_mma_f8(d_tmem, ad + 2 * kk, bd + 2 * kk, idesc, kk != 0 ? 1u : 0u, leader);
+          pipe_commit(&tfull_bar[buf], leader);
+          pipe_commit(&empty_bar[stage], leader);
+        }
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    if (lane == 0) {
+      tc_commit(&drain_bar[buf]);
+      mbar_drain(&drain_bar[buf], 0, WAIT_LIMIT_CYCLES);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ------------------------------------------------------------ scale loader
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
+    int stage = 0, slot = 0;
+    uint32_t phase = 0;
+    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
+      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+      const int rows = SCHED == SCHED_ROWS ? p.rows : p.M;
+      const float* pa = p.sa + static_cast<long long>(c.a_k / F8_K) * p.sa_ld;
+      // SCHED_ROWS: lanes 0 and 1 take the two halves' block scale
+      const float* pb = SCHED == SCHED_ROWS ? p.sb + c.e * p.sb_e + min(c.out_col / 128 + (lane & 1), (p.N - 1) / 128) * p.sb_n
+                                            : p.sb + static_cast<long long>(c.b_k / F8_K) * p.sb_k;
+#pragma unroll 1
+      for (int kb = 0; kb < c.kblocks; ++kb) {
+        pipe_wait(&empty_bar[stage], phase ^ 1, &s_abort, p.status);
+        float* to = s_scales + slot * SLOT;
+#pragma unroll
+        for (int i = 0; i < BM / 32; ++i) {
+          const int r = c.a_m + 32 * i + lane;
+          scale_async(to + 32 * i + lane, r < rows ? pa + r : p.sa, r < rows);
+        }
+        if (SCHED == SCHED_ROWS) {
+          if (lane < 2) scale_async(to + BM + lane, pb, true);
+        } else {
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i) {
+            const int n = c.out_col + 32 * i + lane;
+            scale_async(to + BM + 32 * i + lane, n < p.N ? pb + n : p.sb, n < p.N);
+          }
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&full_bar[stage])) : "memory");
+        pa += p.sa_ld;
+        pb += p.sb_k;
+        if (++slot == SLOTS) slot = 0;
+        if (++stage == STAGES) { stage = 0; phase ^= 1; }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+  } else {
+    // ------------------------------------------------------------ sums and stores
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_MANY));
+    const int q = warp & 3, part = (warp - F8_EPI_WARP0) >> 2;
+    uint8_t* box = s_box + (warp - F8_EPI_WARP0) * f8_box_bytes(BN, BR);
+    const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * WC;
+    int slot = 0;
+    uint32_t it = 0;
+    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
+      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+      const int col = c.out_col + part * WC;
       f32x2 acc[WC / 2];
 #pragma unroll
       for (int j = 0; j < WC / 2; ++j) acc[j] = 0;
-      bool ok = true;
+#pragma unroll 1
       for (int kb = 0; kb < c.kblocks; ++kb, ++it) {
         const uint32_t buf = it & 1u;
-        const float s = row_ok ? sa0 * sb0 : 0.f;
-        const f32x2 s2 = pair(s, s);
-        sa0 = sa1;
-        sb0 = sb1;
-        if (kb + 2 < c.kblocks) {
-          sa1 = pa[(kb + 2) * p.sa_ld];
-          if (SCHED == SCHED_ROWS) sb1 = pb[(kb + 2) * p.sb_k];
-        }
-        if (!mbar_wait_bounded(&tfull_bar[buf], (it >> 1) & 1u, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
+        pipe_wait(&tfull_bar[buf], (it >> 1) & 1u, &s_abort, p.status);
         tc_fence_after();
-        const ulonglong2* cs = reinterpret_cast<const ulonglong2*>(s_sb + stage * BN + half * WC);
-        // 16 columns at a time: beside 128 sums a thread 32 would not fit its 168 registers
+        const float* sc = s_scales + slot * SLOT;
+        if (++slot == SLOTS) slot = 0;
+        float s = sc[q * 32 + lane];
+        if (SCHED == SCHED_ROWS) s *= sc[BM + (part * WC) / 128];
+        const f32x2 s2 = pair(s, s);
+        const ulonglong2* cs = reinterpret_cast<const ulonglong2*>(sc + BM + part * WC);
+        // 16 columns at a time: beside the sums a thread has no registers for more
 #pragma unroll
         for (int i = 0; i < WC / 16; ++i) {
           uint32_t r[16];
@@ -243,49 +284,46 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           if (i == WC / 16 - 1) {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&tempty_bar[buf]);
+            pipe_arrive(&tempty_bar[buf], leader);
           }
-          if (SCHED == SCHED_ROWS) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-              acc[8 * i + j] = fma2(pair(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), s2, acc[8 * i + j]);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < 4; ++j) {
+            f32x2 a = s2, b = s2;
+            if (SCHED == SCHED_KGROUP) {
               const ulonglong2 v = cs[4 * i + j];
-              acc[8 * i + 2 * j] = fma2(pair(__uint_as_float(r[4 * j]), __uint_as_float(r[4 * j + 1])), mul2(s2, v.x),
-                                        acc[8 * i + 2 * j]);
-              acc[8 * i + 2 * j + 1] = fma2(pair(__uint_as_float(r[4 * j + 2]), __uint_as_float(r[4 * j + 3])),
-                                            mul2(s2, v.y), acc[8 * i + 2 * j + 1]);
+              a = mul2(s2, v.x);
+              b = mul2(s2, v.y);
             }
+            add_scaled(acc[8 * i + 2 * j], r[4 * j], r[4 * j + 1], a);
+            add_scaled(acc[8 * i + 2 * j + 1], r[4 * j + 2], r[4 * j + 3], b);
           }
-        }
-        if (SCHED == SCHED_KGROUP) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&empty_bar[stage]);
-          if (++stage == STAGES) stage = 0;
         }
       }
-      if (!ok) break;
-      // bf16 through the warp's staging box; 32-row and 32-column boxes past the ends are skipped
+      if (*aborted) break;
+      // bf16 through the warp's box (rows of WC values, 16-byte pieces swizzled as the tensor store
+      // expects them); boxes past the ends are skipped
       const int y0 = static_cast<int>(c.out_row) + q * 32;
       const int y_end = SCHED == SCHED_ROWS ? min(s_ro[c.e + 1], p.rows) : p.M;
+      const int swz = WC == 64 ? lane & 7 : (lane >> 1) & 3;
+      const uint32_t at = smem_u32(box) + (BR == 32 ? lane : lane & 7) * (WC * 2);
 #pragma unroll
-      for (int i = 0; i < NC; ++i) {
+      for (int g = 0; g < 32 / BR; ++g) {
         if (lane == 0) bulk_wait_read<0>();
         __syncwarp();
-        float v[32];
+        if (BR == 32 || (lane >> 3) == g) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const float2 x = unpair(acc[16 * i + j]);
-          v[2 * j] = x.x;
-          v[2 * j + 1] = x.y;
+          for (int j = 0; j < WC / 8; ++j) {
+            float2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = unpair(acc[4 * j + i]);
+            st_shared_v4(at + ((j ^ swz) << 4), pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
+                         pack_bf16(v[3].x, v[3].y));
+          }
         }
-        stage_row_bf16(stg, lane, v);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && y0 < y_end && col + 32 * i < p.N) {
-          tma_store_3d(&tmC, stg, col + 32 * i, y0, SCHED == SCHED_KGROUP ? c.e : 0);
+        if (lane == 0 && y0 + BR * g < y_end && col < p.N) {
+          tma_store_3d(&tmC, box, col, y0 + BR * g, SCHED == SCHED_KGROUP ? c.e : 0);
           bulk_commit();
         }
       }
@@ -299,17 +337,18 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <int SCHED, int BN>
-static cudaError_t launch_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& c, const Fp8Params& p,
+template <int SCHED, int BN, int BR>
+static cudaError_t launch_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const void* out, int groups, int out_rows, const Fp8Params& p,
                                 cudaStream_t stream) {
-  auto kern = fp8_gemm_kernel<SCHED, BN>;
-  const cudaError_t err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, f8_smem(BN));
+  CUtensorMap c;
+  if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups, BN / 4, BR)) return cudaErrorInvalidValue;
+  constexpr int smem = f8_smem(BN, BR, SCHED == SCHED_KGROUP);
+  const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, BR>>(smem);
   if (err != cudaSuccess) return err;
-  kern<<<num_sms(), F8_THREADS, f8_smem(BN), stream>>>(a, b, c, p);
+  fp8_gemm_kernel<SCHED, BN, BR><<<num_sms(), F8_THREADS, smem, stream>>>(a, b, c, p);
   count_launch();
   return cudaGetLastError();
 }
-
 
 }  // namespace moe
 
@@ -331,10 +370,9 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
   // BN = 128 where the rows make too few 256-wide tiles to fill the SMs evenly
   const int64_t wide = tiles * ((N + 255) / 256);
   const int bn = (N <= 128 || wide < num_sms()) ? 128 : 256;
-  CUtensorMap ta, tb, tc;
+  CUtensorMap ta, tb;
   if (!make_tensor_map_u8(&ta, a, K, rows, F8_K, BM) ||
-      !make_tensor_map_u8(&tb, b, K, static_cast<uint64_t>(E) * N, F8_K, F8_B_BOX) ||
-      !make_tensor_map_store3(&tc, out, N, rows, 1))
+      !make_tensor_map_u8(&tb, b, K, static_cast<uint64_t>(E) * N, F8_K, F8_B_BOX))
     return MOE_ERR_CUDA;
   Fp8Params p{};
   p.rows = static_cast<int>(rows); p.N = N; p.K = K; p.E = E; p.row_offsets = row_offsets;
@@ -345,7 +383,10 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
   p.g.band_krows = BAND_KROWS_E4M3;
   p.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = bn == 256 ? launch_fp8_t<SCHED_ROWS, 256>(ta, tb, tc, p, s) : launch_fp8_t<SCHED_ROWS, 128>(ta, tb, tc, p, s);
+  const int R = p.rows;
+  const cudaError_t e = bn == 128    ? launch_fp8_t<SCHED_ROWS, 128, 32>(ta, tb, out, 1, R, p, s)
+                        : K >= 4096 ? launch_fp8_t<SCHED_ROWS, 256, 8>(ta, tb, out, 1, R, p, s)
+                                    : launch_fp8_t<SCHED_ROWS, 256, 32>(ta, tb, out, 1, R, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -361,16 +402,15 @@ moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint
   if (rows == 0)
     return cudaMemsetAsync(out, 0, static_cast<size_t>(E) * N * K * sizeof(moe_bf16), s) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
   const int bn = K <= 128 || E * up128(N) / 128 * ((K + 255) / 256) < num_sms() ? 128 : 256;
-  CUtensorMap ta, tb, tc;
-  if (!make_tensor_map_u8(&ta, dy_t, rows, N, F8_K, BM) || !make_tensor_map_u8(&tb, x_t, rows, K, F8_K, F8_B_BOX) ||
-      !make_tensor_map_store3(&tc, out, K, N, E))
-    return MOE_ERR_CUDA;
+  CUtensorMap ta, tb;
+  if (!make_tensor_map_u8(&ta, dy_t, rows, N, F8_K, BM) || !make_tensor_map_u8(&tb, x_t, rows, K, F8_K, F8_B_BOX)) return MOE_ERR_CUDA;
   Fp8Params p{};
   p.rows = static_cast<int>(rows); p.M = N; p.N = K; p.E = E; p.row_offsets = row_offsets;
   p.sa = dy_scales; p.sa_ld = N; p.sb = x_scales; p.sb_k = K;
   p.g.BN = bn; p.g.M = static_cast<int>(up128(N)); p.g.N = K; p.g.m_fastest = N <= K ? 1 : 0;
   p.status = dev_status;
-  const cudaError_t e = bn == 256 ? launch_fp8_t<SCHED_KGROUP, 256>(ta, tb, tc, p, s) : launch_fp8_t<SCHED_KGROUP, 128>(ta, tb, tc, p, s);
+  const cudaError_t e = bn == 256 ? launch_fp8_t<SCHED_KGROUP, 256, 32>(ta, tb, out, E, N, p, s)
+                                  : launch_fp8_t<SCHED_KGROUP, 128, 32>(ta, tb, out, E, N, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -9,8 +9,8 @@
 // values below 1.3), so fp16's 11 bits serve better than bf16's 8: on gaussian matrices the result is
 // 1.3e-3 off (bf16 operands: 1.1e-2).  X is held times a power of two near sqrt(l), so that its entries stay
 // normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
-// values, which later steps amplify by up to a each; for the first steps X is therefore kept in two fp16
-// parts, the second read for that addend alone (low-rank plus noise: 3.5e-3 off without, 5e-4 with three steps).
+// values, which later steps amplify by up to a each; X is therefore kept in two fp16 parts, the second
+// read for that addend alone (low-rank plus noise: 3.4e-3 off without it, 2.4e-4 with it).
 // A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
 //
 // Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.
@@ -36,7 +36,7 @@ enum { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };   // A = X X^T; B = b A + c A A
 struct NsParams {
   int batch, s, n, k;       // a matrix's padded rows, output columns, contraction
   float alpha, beta;        // out = alpha * product + beta * in
-  int lo_in, lo_out;        // NS_APPLY: X's second part is read, written
+  int lo_out;               // NS_APPLY: X's second part is written
   int32_t* status;
 };
 
@@ -198,9 +198,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       if (KIND == NS_GRAM) return;
       if (lane == 0) {
         fence_proxy_async_smem();
-        mbar_arrive_expect_tx(ibar, KIND == NS_APPLY && p.lo_in ? 2 * NS_BOX : NS_BOX);
+        mbar_arrive_expect_tx(ibar, KIND == NS_APPLY ? 2 * NS_BOX : NS_BOX);
         tma_load_2d(in, &tmIn, ibar, x, y);
-        if (KIND == NS_APPLY && p.lo_in) tma_load_2d(in + NS_BOX, &tmInLo, ibar, x, y);
+        if (KIND == NS_APPLY) tma_load_2d(in + NS_BOX, &tmInLo, ibar, x, y);
       }
       inflight = true;
     };
@@ -227,7 +227,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               const uint4 x = ld_shared_v4(in_row + ((v ^ sw) << 4));
-              const uint4 z = KIND == NS_APPLY && p.lo_in ? ld_shared_v4(in_row + NS_BOX + ((v ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+              const uint4 z = KIND == NS_APPLY ? ld_shared_v4(in_row + NS_BOX + ((v ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
               hi[4 * v] = x.x; hi[4 * v + 1] = x.y; hi[4 * v + 2] = x.z; hi[4 * v + 3] = x.w;
               lo[4 * v] = z.x; lo[4 * v + 1] = z.y; lo[4 * v + 2] = z.z; lo[4 * v + 3] = z.w;
             }
@@ -459,8 +459,6 @@ static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const C
   return launch_early(kern, dim3(grid), dim3(NS_THREADS), NS_SMEM, s, a, b, in, in_lo, out, out_lo, p);
 }
 
-constexpr int NS_KEEP = 3;           // steps whose addend takes X in two parts
-
 // `batch` matrices of one shape: products, update.
 static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float lr, void* workspace, int32_t* status,
                             cudaStream_t st) {
@@ -491,14 +489,14 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   int cur = 0;
   for (int k = 0; k < h.steps; ++k, cur ^= 1) {
     const float a = h.coefficients[3 * k], b = h.coefficients[3 * k + 1], c = h.coefficients[3 * k + 2];
-    NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, 0, 0, status};
+    NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, 0, status};
     err = launch_ns<NS_GRAM>(xk[cur], xk[cur], as, as, as, as, p, st);
     if (err != cudaSuccess) return err;
     p.k = o.s; p.alpha = c; p.beta = b;
     err = launch_ns<NS_POLY>(ak, ak, as, as, bs, bs, p, st);
     if (err != cudaSuccess) return err;
     p.n = o.l; p.alpha = 1.0f; p.beta = a;
-    p.lo_in = k < NS_KEEP; p.lo_out = k + 1 < NS_KEEP && k + 1 < h.steps;
+    p.lo_out = k + 1 < h.steps;
     err = launch_ns<NS_APPLY>(bk, xn[cur], xs[cur], los, xs[cur ^ 1], los, p, st);
     if (err != cudaSuccess) return err;
   }

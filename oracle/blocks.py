@@ -116,9 +116,9 @@ def muon_step(w, m, grad, lr, momentum, decay, rms, nesterov=True, coefficients=
     return w - lr * (decay * w + rms * np.sqrt(max(w.shape)) * o), m, o
 
 
-def newton_schulz_rounded(x, coefficients=COEFFICIENTS, keep=3):
-    """newton_schulz as the kernels round it: products on fp16 operands, X in two parts in the addend of the first
-    `keep` steps, everything else exact.  How far it is from newton_schulz is what that arithmetic costs."""
+def newton_schulz_rounded(x, coefficients=COEFFICIENTS):
+    """newton_schulz as the kernels round it: products on fp16 operands, X in two parts in the addend, everything else
+    exact.  How far it is from newton_schulz is what that arithmetic costs."""
     h = lambda v: v.astype(np.float16).astype(np.float64)  # noqa: E731
     x = x.T if x.shape[0] > x.shape[1] else x
     n = np.linalg.norm(x)
@@ -129,10 +129,10 @@ def newton_schulz_rounded(x, coefficients=COEFFICIENTS, keep=3):
     x = scale * x / n if n > 0 else np.zeros_like(x)
     hi = h(x)
     lo = h(x - hi)
-    for k, (a, b, c) in enumerate(coefficients):
+    for a, b, c in coefficients:
         A = h(hi @ hi.T / scale ** 2)
         B = h(b * A + c * (A @ A))
-        v = a * (hi + lo if k < keep else hi) + B @ hi
+        v = a * (hi + lo) + B @ hi
         hi = h(v)
         lo = h(v - hi)
     return hi / scale
