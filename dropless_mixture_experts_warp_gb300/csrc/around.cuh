@@ -42,20 +42,27 @@ inline moe_status status_of(cudaError_t e) { return e == cudaSuccess ? MOE_OK : 
 __device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 template <typename... Params, typename... Args>
-static cudaError_t launch_early(void (*kern)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, const Args&... args) {
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+static cudaError_t launch_early_clusters(void (*kern)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, int cluster, const Args&... args) {
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;    // of blocks along x, where it is not 0
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
   const cudaError_t err = cudaLaunchKernelEx(&cfg, kern, static_cast<Params>(args)...);
   if (err == cudaSuccess) count_launch();
   return err;
+}
+template <typename... Params, typename... Args>
+static cudaError_t launch_early(void (*kern)(Params...), dim3 grid, dim3 block, int smem, cudaStream_t s, const Args&... args) {
+  return launch_early_clusters(kern, grid, block, smem, s, 0, args...);
 }
 
 // Asynchronous copies of 16, 8 or 4 bytes from global to shared memory, in groups.

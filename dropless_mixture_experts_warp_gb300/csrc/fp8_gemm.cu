@@ -46,6 +46,9 @@ __host__ __device__ constexpr int f8_smem(int bn, int br, bool col_scales) {
          f8_slots(bn, br) * f8_slot_floats(bn, col_scales) * 4 + 1024;
 }
 
+constexpr int F8_INFOS = 4;
+constexpr int F8_SPLIT_LD = 128 + 4;     // floats of a row of a part
+
 struct Fp8Params {
   int rows;                    // rows of A (SCHED_ROWS), or along the contraction (SCHED_KGROUP)
   int M, N, K;                 // SCHED_KGROUP: out [E][M][N]; SCHED_ROWS: out [rows][N], K long
@@ -55,6 +58,8 @@ struct Fp8Params {
   long long sa_ld;
   const float* sb;             // SCHED_ROWS: block scales with these strides; SCHED_KGROUP: [kb][N]
   long long sb_e, sb_n, sb_k;
+  int split;                   // SPLIT: CTAs of a tile, a power of two
+  moe_bf16* out;               // SPLIT
   GemmParams g;                // what the shared schedules read
   int32_t* status;
 };
@@ -95,7 +100,8 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, 
                : "memory");
 }
 
-template <int SCHED, int BN, int BR>
+// SPLIT: one tile a cluster of CTAs, each a part of the contraction; their sums meet in shared memory.
+template <int SCHED, int BN, int BR, bool SPLIT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
@@ -107,6 +113,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   __shared__ __align__(8) uint64_t tfull_bar[2];
   __shared__ __align__(8) uint64_t tempty_bar[2];
   __shared__ __align__(8) uint64_t drain_bar[2];
+  __shared__ __align__(8) uint64_t ifull_bar[F8_INFOS];
+  __shared__ __align__(8) uint64_t iempty_bar[F8_INFOS];
+  __shared__ int4 s_info[F8_INFOS];       // of the tiles on their way to the sums: see below
   __shared__ uint32_t s_tmem_base;
   __shared__ int s_abort;
   __shared__ int s_ro[MAX_EXPERTS + 1];
@@ -120,6 +129,22 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   uint8_t* s_box = smem + STAGES * STAGE_BYTES;
   float* s_scales = reinterpret_cast<float*>(s_box + F8_EPI_WARPS * f8_box_bytes(BN, BR));
 
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1 + 32); mbar_init(&empty_bar[s], 1); }   // full: the tensor loads, the scale loader's lanes
+    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], 1); mbar_init(&tempty_bar[a], F8_EPI_WARPS); }
+    for (int a = 0; a < 2; ++a) mbar_init(&drain_bar[a], 1);
+    for (int i = 0; i < F8_INFOS; ++i) { mbar_init(&ifull_bar[i], 1); mbar_init(&iempty_bar[i], F8_EPI_WARPS); }
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+    tma_prefetch_desc(&tmC);
+  }
+  if (warp == 1) { tmem_alloc(&s_tmem_base, TMEM_COLS); tmem_relinquish(); }
+  wait_for_previous();
+  launch_dependents();
   const int E = p.row_offsets ? p.E : 1;
   const int all_rows = (p.rows + F8_K - 1) / F8_K * F8_K;
   for (int i = threadIdx.x; i <= E; i += blockDim.x)
@@ -130,25 +155,25 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     __syncthreads();
     snake = kgroup_order(s_ro, E, (p.g.M / BM) * n_tiles, gridDim.x, s_order);  // complete at the barrier below
   }
-  if (threadIdx.x == 0) {
-    for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1 + 32); mbar_init(&empty_bar[s], 1); }   // full: the tensor loads, the scale loader's lanes
-    for (int a = 0; a < 2; ++a) { mbar_init(&tfull_bar[a], 1); mbar_init(&tempty_bar[a], F8_EPI_WARPS); }
-    for (int a = 0; a < 2; ++a) mbar_init(&drain_bar[a], 1);
-    s_abort = 0;
-    fence_mbar_init();
-  }
-  if (warp == 0 && lane == 0) {
-    tma_prefetch_desc(&tmA);
-    tma_prefetch_desc(&tmB);
-    tma_prefetch_desc(&tmC);
-  }
-  if (warp == 1) { tmem_alloc(&s_tmem_base, TMEM_COLS); tmem_relinquish(); }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = s_tmem_base;
   const int total = (SCHED == SCHED_ROWS) ? (s_ro[E] / BM) * n_tiles : E * (p.g.M / BM) * n_tiles;
   volatile int* const aborted = &s_abort;
+  // tiles of this CTA: every `step`-th from its own; a split tile's contraction from block kb0 on
+  const int rank = SPLIT ? static_cast<int>(cluster_ctarank()) : 0;
+  const int mine = SPLIT ? blockIdx.x / p.split : blockIdx.x, step = SPLIT ? total : gridDim.x;
+  auto coord = [&](int tile) {
+    TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+    if (SPLIT) {
+      const int per = (c.kblocks + p.split - 1) / p.split, kb0 = min(rank * per, c.kblocks);
+      c.a_k += kb0 * F8_K;
+      c.b_k += kb0 * F8_K;
+      c.kblocks = min(per, c.kblocks - kb0);
+    }
+    return c;
+  };
   const uint32_t leader = lane == 0;
 
   if (warp == 0) {
@@ -156,9 +181,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
     int stage = 0;
     uint32_t phase = 0, armed = 0, armed_parity = 0;
-    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
-         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+    for (int rnd = 0, tile = sched_tile(0, mine, step, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, mine, step, snake)) {
+      const TileCoord c = coord(tile);
 #pragma unroll 1
       for (int kb = 0; kb < c.kblocks; ++kb) {
         pipe_wait(&empty_bar[stage], phase ^ 1, &s_abort, p.status);
@@ -179,6 +204,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       for (int s = 0; s < STAGES; ++s)
         if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
     __syncwarp();
+    if (SPLIT) { cluster_sync_all(); cluster_sync_all(); }   // the summing warps' two
   } else if (warp <= 2) {
     // ------------------------------------------------------------ MMA issuers, a buffer each
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
@@ -187,9 +213,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     const uint32_t buf = warp - 1, d_tmem = tmem_base + buf * 256;
     int stage = 0;
     uint32_t phase = 0, it = 0;
-    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
-         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+    for (int rnd = 0, tile = sched_tile(0, mine, step, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, mine, step, snake)) {
+      const TileCoord c = coord(tile);
 #pragma unroll 1
       for (int kb = 0; kb < c.kblocks; ++kb, ++it) {
         if ((it & 1u) == buf) {
@@ -210,18 +236,28 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       mbar_drain(&drain_bar[buf], 0, WAIT_LIMIT_CYCLES);
     }
     __syncwarp();
+    if (SPLIT) { cluster_sync_all(); cluster_sync_all(); }   // the summing warps' two
   } else if (warp == 3) {
     // ------------------------------------------------------------ scale loader
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(F8_REGS_FEW));
-    int stage = 0, slot = 0;
-    uint32_t phase = 0;
-    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
-         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
+    int stage = 0, slot = 0, info = 0;
+    uint32_t phase = 0, info_phase = 0;
+    for (int rnd = 0, tile = sched_tile(0, mine, step, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, mine, step, snake)) {
+      const TileCoord c = coord(tile);
       const int rows = SCHED == SCHED_ROWS ? p.rows : p.M;
+      // the tile for the summing warps, to whom its coordinates would cost 1100 cycles a tile: columns, rows
+      // and their end, blocks, expert
+      pipe_wait(&iempty_bar[info], info_phase ^ 1, &s_abort, p.status);
+      if (lane == 0) {
+        s_info[info] = make_int4(c.out_col, static_cast<int>(c.out_row), SCHED == SCHED_ROWS ? min(s_ro[c.e + 1], p.rows) : c.e, c.kblocks);
+        mbar_arrive(&ifull_bar[info]);
+      }
+      __syncwarp();
+      if (++info == F8_INFOS) { info = 0; info_phase ^= 1; }
       const float* pa = p.sa + static_cast<long long>(c.a_k / F8_K) * p.sa_ld;
       // SCHED_ROWS: lanes 0 and 1 take the two halves' block scale
-      const float* pb = SCHED == SCHED_ROWS ? p.sb + c.e * p.sb_e + min(c.out_col / 128 + (lane & 1), (p.N - 1) / 128) * p.sb_n
+      const float* pb = SCHED == SCHED_ROWS ? p.sb + c.e * p.sb_e + min(c.out_col / 128 + (lane & 1), (p.N - 1) / 128) * p.sb_n + c.b_k / F8_K * p.sb_k
                                             : p.sb + static_cast<long long>(c.b_k / F8_K) * p.sb_k;
 #pragma unroll 1
       for (int kb = 0; kb < c.kblocks; ++kb) {
@@ -249,23 +285,29 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    __syncwarp();
+    if (SPLIT) { cluster_sync_all(); cluster_sync_all(); }   // the summing warps' two
   } else {
     // ------------------------------------------------------------ sums and stores
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_MANY));
     const int q = warp & 3, part = (warp - F8_EPI_WARP0) >> 2;
     uint8_t* box = s_box + (warp - F8_EPI_WARP0) * f8_box_bytes(BN, BR);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * WC;
-    int slot = 0;
-    uint32_t it = 0;
-    for (int rnd = 0, tile = sched_tile(0, blockIdx.x, gridDim.x, snake); tile < total && !*aborted;
-         tile = sched_tile(++rnd, blockIdx.x, gridDim.x, snake)) {
-      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, tile);
-      const int col = c.out_col + part * WC;
+    int slot = 0, info = 0;
+    uint32_t it = 0, info_phase = 0;
+    for (int rnd = 0, tile = sched_tile(0, mine, step, snake); tile < total && !*aborted;
+         tile = sched_tile(++rnd, mine, step, snake)) {
+      pipe_wait(&ifull_bar[info], info_phase, &s_abort, p.status);
+      const int4 c = s_info[info];
+      __syncwarp();
+      pipe_arrive(&iempty_bar[info], leader);
+      if (++info == F8_INFOS) { info = 0; info_phase ^= 1; }
+      const int col = c.x + part * WC, kblocks = c.w;
       f32x2 acc[WC / 2];
 #pragma unroll
       for (int j = 0; j < WC / 2; ++j) acc[j] = 0;
 #pragma unroll 1
-      for (int kb = 0; kb < c.kblocks; ++kb, ++it) {
+      for (int kb = 0; kb < kblocks; ++kb, ++it) {
         const uint32_t buf = it & 1u;
         pipe_wait(&tfull_bar[buf], (it >> 1) & 1u, &s_abort, p.status);
         tc_fence_after();
@@ -299,11 +341,17 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
           }
         }
       }
+      if (SPLIT) {                        // the part's sums, for the cluster
+        float* to = reinterpret_cast<float*>(smem) + (q * 32 + lane) * F8_SPLIT_LD + part * WC;
+        // the stage that this overwrites is read: every block's product has been taken out
+#pragma unroll
+        for (int j = 0; j < WC / 4; ++j) *reinterpret_cast<ulonglong2*>(to + 4 * j) = make_ulonglong2(acc[2 * j], acc[2 * j + 1]);
+        break;
+      }
       if (*aborted) break;
       // bf16 through the warp's box (rows of WC values, 16-byte pieces swizzled as the tensor store
       // expects them); boxes past the ends are skipped
-      const int y0 = static_cast<int>(c.out_row) + q * 32;
-      const int y_end = SCHED == SCHED_ROWS ? min(s_ro[c.e + 1], p.rows) : p.M;
+      const int y0 = c.y + q * 32, y_end = SCHED == SCHED_ROWS ? c.z : p.M;
       const int swz = WC == 64 ? lane & 7 : (lane >> 1) & 3;
       const uint32_t at = smem_u32(box) + (BR == 32 ? lane : lane & 7) * (WC * 2);
 #pragma unroll
@@ -323,12 +371,38 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0 && y0 + BR * g < y_end && col < p.N) {
-          tma_store_3d(&tmC, box, col, y0 + BR * g, SCHED == SCHED_KGROUP ? c.e : 0);
+          tma_store_3d(&tmC, box, col, y0 + BR * g, SCHED == SCHED_KGROUP ? c.z : 0);
           bulk_commit();
         }
       }
     }
     if (lane == 0) bulk_wait_all();
+    if (SPLIT) {
+      // each CTA adds the parts of its share of the tile's columns, in the order of the contraction
+      __syncwarp();
+      cluster_sync_all();
+      const TileCoord c = tile_coord<SCHED, EPI_STORE, false, F8_K>(p.g, s_ro, s_order, E, n_tiles, mine);
+      const int rows = min(BM, p.rows - c.a_m), cols = BN / p.split, col0 = rank * cols;
+      for (int i = threadIdx.x - 32 * F8_EPI_WARP0; i < rows * (cols / 4) && !*aborted; i += 32 * F8_EPI_WARPS) {
+        const int r = i / (cols / 4), n = col0 + (i - r * (cols / 4)) * 4;
+        if (c.out_col + n >= p.N) continue;
+        const uint32_t at = smem_u32(smem) + (r * F8_SPLIT_LD + n) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int k = 0; k < p.split; ++k) {
+          float x[4];
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                       : "r"(mapa_shared(at, k))
+                       : "memory");
+#pragma unroll
+          for (int j = 0; j < 4; ++j) v[j] += x[j];
+        }
+        *reinterpret_cast<uint2*>(p.out + static_cast<long long>(c.a_m + r) * p.N + c.out_col + n) =
+            make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+      }
+      __syncwarp();
+      cluster_sync_all();        // no CTA leaves while another may read its parts
+    }
   }
 
   tc_fence_before();
@@ -337,17 +411,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <int SCHED, int BN, int BR>
+template <int SCHED, int BN, int BR, bool SPLIT = false>
 static cudaError_t launch_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const void* out, int groups, int out_rows, const Fp8Params& p,
-                                cudaStream_t stream) {
+                                cudaStream_t stream, int tiles = 0) {
   CUtensorMap c;
   if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups, BN / 4, BR)) return cudaErrorInvalidValue;
   constexpr int smem = f8_smem(BN, BR, SCHED == SCHED_KGROUP);
-  const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, BR>>(smem);
+  const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, BR, SPLIT>>(smem);
   if (err != cudaSuccess) return err;
-  fp8_gemm_kernel<SCHED, BN, BR><<<num_sms(), F8_THREADS, smem, stream>>>(a, b, c, p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early_clusters(fp8_gemm_kernel<SCHED, BN, BR, SPLIT>, dim3(SPLIT ? tiles * p.split : num_sms()), dim3(F8_THREADS), smem, stream,
+                      SPLIT ? p.split : 0, a, b, c, p);
 }
 
 }  // namespace moe
@@ -384,8 +457,17 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
   p.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int R = p.rows;
+  // One matrix and few tiles: the contraction over up to eight SMs a tile, four blocks each at least (5 x 4096 x 7168,
+  // bound by reading the weights: 22 us on 32 SMs).
+  const int64_t few = tiles * ((N + 127) / 128);
+  if (!row_offsets) {
+    p.split = 1;
+    while (p.split < 8 && few * p.split * 2 <= num_sms() && kb >= 8ll * p.split) p.split *= 2;
+    p.out = out;
+    if (p.split > 1) return status_of(launch_fp8_t<SCHED_ROWS, 128, 32, true>(ta, tb, out, 1, R, p, s, static_cast<int>(few)));
+  }
   const cudaError_t e = bn == 128    ? launch_fp8_t<SCHED_ROWS, 128, 32>(ta, tb, out, 1, R, p, s)
-                        : K >= 4096 ? launch_fp8_t<SCHED_ROWS, 256, 8>(ta, tb, out, 1, R, p, s)
+                        : rows <= 256ll * E ? launch_fp8_t<SCHED_ROWS, 256, 8>(ta, tb, out, 1, R, p, s)
                                     : launch_fp8_t<SCHED_ROWS, 256, 32>(ta, tb, out, 1, R, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }

@@ -24,10 +24,12 @@ __device__ __forceinline__ uint2 f8_block16(const f32x2 (&v)[4], float amax, flo
 // A warp takes QR_ROWS rows x 256 columns: 16 lanes of 16 bytes a block, every row's load
 // issued before the first is used.  row_map: row r reads src row row_map[r], zeros where that
 // is negative.
-__global__ void __launch_bounds__(256) f8_rows_kernel(const uint16_t* __restrict__ src, int rows, int C,
-                                                      const int32_t* __restrict__ row_map,
-                                                      const int32_t* __restrict__ nrows_dev, uint8_t* __restrict__ codes,
-                                                      float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) f8_rows_kernel(const uint16_t* src, int rows, int C,
+                                                      const int32_t* row_map,
+                                                      const int32_t* nrows_dev, uint8_t* codes,
+                                                      float* scales) {
+  wait_for_previous();
+  launch_dependents();
   const int lane = threadIdx.x & 31;
   const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
   const int groups = (C + 255) / 256;
@@ -52,6 +54,33 @@ __global__ void __launch_bounds__(256) f8_rows_kernel(const uint16_t* __restrict
       if (in && r0 + i < limit) {
         *reinterpret_cast<uint2*>(codes + static_cast<long long>(r0 + i) * C + col) = c;
         if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * rows + r0 + i] = s;
+      }
+    }
+  }
+}
+
+// Each token's row quantised once, its codes written to the k rows that the routing gave it: a
+// warp takes 256 columns of a token.  Rows without a token are left as they were.
+__global__ void __launch_bounds__(256) f8_scatter_kernel(const uint16_t* x, int T, int C, int k, const int32_t* token_to_row, int rows,
+                                                         uint8_t* codes, float* scales) {
+  wait_for_previous();
+  launch_dependents();
+  const int lane = threadIdx.x & 31, groups = (C + 255) / 256;
+  const long long total = static_cast<long long>(T) * groups;
+  for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8ll) {
+    const int tok = static_cast<int>(t / groups), col = static_cast<int>(t - static_cast<long long>(tok) * groups) * 256 + lane * 8;
+    const bool in = col < C;
+    const int mine = lane < k ? token_to_row[static_cast<long long>(tok) * k + lane] : -1;
+    const uint4 w = in ? *reinterpret_cast<const uint4*>(x + static_cast<long long>(tok) * C + col) : make_uint4(0, 0, 0, 0);
+    const uint32_t m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(0u, w.x), w.y), w.z), w.w);
+    const f32x2 v[4] = {bf16_pair(w.x), bf16_pair(w.y), bf16_pair(w.z), bf16_pair(w.w)};
+    float s;
+    const uint2 c = f8_block16(v, max_halves(m), s);
+    for (int j = 0; j < k; ++j) {
+      const int r = __shfl_sync(0xffffffffu, mine, j);
+      if (in && r >= 0 && r < rows) {
+        *reinterpret_cast<uint2*>(codes + static_cast<long long>(r) * C + col) = c;
+        if ((lane & 15) == 0) scales[static_cast<long long>(col >> 7) * rows + r] = s;
       }
     }
   }
@@ -90,6 +119,8 @@ __global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
   float* rmax = cmax + 4 * 128;                    // [2][128]
   float* tmax = rmax + 2 * 128;                    // [8]
   const int tid = threadIdx.x;
+  wait_for_previous();
+  launch_dependents();
   const int limit = p.nrows_dev ? min(p.R, *p.nrows_dev) : p.R;
   const unsigned ctiles = (p.C + 127) / 128, rtiles = (limit + 127) / 128;
   const unsigned total = p.batch * rtiles * ctiles;
@@ -239,9 +270,7 @@ static cudaError_t launch_f8_tiles(const F8Tiles& p, cudaStream_t s) {
   const long long tiles = static_cast<long long>(p.batch) * ((p.R + 127) / 128) * ((p.C + 127) / 128);
   if (tiles >= (1ll << 31) - (1 << 20)) return cudaErrorInvalidValue;
   const int grid = static_cast<int>(tiles < 2ll * num_sms() ? tiles : 2ll * num_sms());
-  f8_tiles_kernel<SQUARE><<<grid, 256, QT_SMEM, s>>>(p);
-  count_launch();
-  return cudaGetLastError();
+  return launch_early(f8_tiles_kernel<SQUARE>, dim3(grid), dim3(256), QT_SMEM, s, p);
 }
 
 // ------------------------------------------------------------------------ SwiGLU
@@ -250,9 +279,11 @@ static cudaError_t launch_f8_tiles(const F8Tiles& p, cudaStream_t s) {
 __device__ __forceinline__ float silu_exact(float g) { return __fdividef(g, 1.0f + __expf(-g)); }
 
 // h = w silu(G) U of gu [rows][2f], a block of 128 columns of h on 16 lanes, quantised.
-__global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* __restrict__ gu, const float* __restrict__ w_rows, int rows,
-                                                        int f, const int32_t* __restrict__ nrows_dev,
-                                                        uint8_t* __restrict__ codes, float* __restrict__ scales) {
+__global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* gu, const float* w_rows, int rows,
+                                                        int f, const int32_t* nrows_dev,
+                                                        uint8_t* codes, float* scales) {
+  wait_for_previous();
+  launch_dependents();
   const int lane = threadIdx.x & 31;
   const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
   const int groups = (f + 255) / 256;
@@ -265,11 +296,11 @@ __global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* __restri
     float w[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const bool ok = in && r0 + i < limit;
+      w[i] = r0 + i >= limit ? 0.0f : (w_rows ? w_rows[r0 + i] : 1.0f);
+      const bool ok = in && w[i] != 0.0f;       // padding rows weigh 0
       const uint16_t* at = gu + static_cast<long long>(r0 + i) * 2 * f + col;
       g[i] = ok ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
       u[i] = ok ? *reinterpret_cast<const uint4*>(at + f) : make_uint4(0, 0, 0, 0);
-      w[i] = r0 + i >= limit ? 0.0f : (w_rows ? w_rows[r0 + i] : 1.0f);
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -318,6 +349,8 @@ __global__ void __launch_bounds__(SB_THREADS, 1) f8_swiglu_bwd_kernel(const F8Sw
   __shared__ __align__(16) uint32_t ct[128 * 32];    // codes of a tile's columns
   __shared__ float cmax[32 * 128];
   __shared__ float2 cscale[128];                     // -scale, 1 / scale of a tile's columns
+  wait_for_previous();
+  launch_dependents();
   const int tid = threadIdx.x, c = tid & 15, u = tid >> 4;
   const int limit = p.nrows_dev ? min(p.rows, *p.nrows_dev) : p.rows;
   const unsigned ctiles = p.f / 128, total = static_cast<unsigned>((limit + 127) / 128) * ctiles;
@@ -441,8 +474,10 @@ __global__ void __launch_bounds__(SB_THREADS, 1) f8_swiglu_bwd_kernel(const F8Sw
 }
 
 // dw [r] = its parts' sum, in order.
-__global__ void f8_dw_kernel(const float* __restrict__ part, int parts, int rows, const int32_t* __restrict__ nrows_dev,
-                             float* __restrict__ dw) {
+__global__ void f8_dw_kernel(const float* part, int parts, int rows, const int32_t* nrows_dev,
+                             float* dw) {
+  wait_for_previous();
+  launch_dependents();
   const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
   for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < limit; r += gridDim.x * blockDim.x) {
     float s = 0.0f;
@@ -472,9 +507,8 @@ moe_status moe_fp8_quantize(const moe_bf16* src, int64_t rows, int32_t C, const 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (!codes_t) {
     const long long warps = (rows + QR_ROWS - 1) / QR_ROWS * ((C + 255) / 256);
-    f8_rows_kernel<<<f8_row_grid(warps), 256, 0, s>>>(src, static_cast<int>(rows), C, row_map, nrows_dev, codes, scales);
-    count_launch();
-    return status_of(cudaGetLastError());
+    return status_of(launch_early(f8_rows_kernel, dim3(f8_row_grid(warps)), dim3(256), 0, s, src, static_cast<int>(rows), C, row_map,
+                                  nrows_dev, codes, scales));
   }
   const F8Tiles p{src, row_map, nrows_dev, 1, static_cast<int>(rows), C, static_cast<int>(up128(rows)), codes, scales, codes_t, scales_t};
   return status_of(launch_f8_tiles<false>(p, s));
@@ -496,10 +530,8 @@ moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows,
   if (!f8_aligned(gu) || !f8_aligned(codes)) return MOE_ERR_ALIGNMENT;
   if (rows == 0) return MOE_OK;
   const long long warps = (rows + 1) / 2 * ((f + 255) / 256);
-  f8_swiglu_kernel<<<f8_row_grid(warps), 256, 0, static_cast<cudaStream_t>(stream)>>>(gu, w_rows, static_cast<int>(rows), f, nrows_dev,
-                                                                                      codes, scales);
-  count_launch();
-  return status_of(cudaGetLastError());
+  return status_of(launch_early(f8_swiglu_kernel, dim3(f8_row_grid(warps)), dim3(256), 0, static_cast<cudaStream_t>(stream), gu, w_rows,
+                                static_cast<int>(rows), f, nrows_dev, codes, scales));
 }
 
 moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const float* w_rows, int64_t rows, int32_t f,
@@ -517,15 +549,12 @@ moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const floa
   const F8SwigluBwd p{gu, dh, w_rows, nrows_dev, static_cast<int>(rows), f, static_cast<int>(up128(rows)), dgu_codes, dgu_scales,
                       dgu_codes_t, dgu_scales_t, h_codes_t, h_scales_t, dw_part};
   const long long tiles = up128(rows) / 128 * (f / 128);
-  f8_swiglu_bwd_kernel<<<static_cast<int>(tiles < num_sms() ? tiles : num_sms()), SB_THREADS, 0, s>>>(p);
-  count_launch();
-  if (cudaGetLastError() != cudaSuccess) return MOE_ERR_CUDA;
+  const int grid = static_cast<int>(tiles < num_sms() ? tiles : num_sms());
+  if (launch_early(f8_swiglu_bwd_kernel, dim3(grid), dim3(SB_THREADS), 0, s, p) != cudaSuccess) return MOE_ERR_CUDA;
   if (!dw_rows) return MOE_OK;
   const long long blocks = (rows + 255) / 256;
-  f8_dw_kernel<<<static_cast<int>(blocks < 4 * num_sms() ? blocks : 4 * num_sms()), 256, 0, s>>>(dw_part, f / 128, static_cast<int>(rows),
-                                                                                               nrows_dev, dw_rows);
-  count_launch();
-  return status_of(cudaGetLastError());
+  return status_of(launch_early(f8_dw_kernel, dim3(static_cast<int>(blocks < 4 * num_sms() ? blocks : 4 * num_sms())), dim3(256), 0, s,
+                                dw_part, f / 128, static_cast<int>(rows), nrows_dev, dw_rows));
 }
 
 moe_status moe_permute_fp8(const moe_dims* dims, const moe_bf16* x, const int32_t* topk_idx, const float* topk_w,
@@ -545,6 +574,11 @@ moe_status moe_permute_fp8(const moe_dims* dims, const moe_bf16* x, const int32_
                         static_cast<int>(rows), dev_status, static_cast<cudaStream_t>(stream)) != cudaSuccess)
     return MOE_ERR_CUDA;
   if (d.T == 0) return MOE_OK;
+  if (!codes_t) {
+    const long long warps = static_cast<long long>(d.T) * ((d.d + 255) / 256);
+    return status_of(launch_early(f8_scatter_kernel, dim3(f8_row_grid(warps)), dim3(256), 0, static_cast<cudaStream_t>(stream), x, d.T, d.d,
+                                  d.k, token_to_row, static_cast<int>(rows), codes, scales));
+  }
   return moe_fp8_quantize(x, rows, d.d, row_to_token, row_offsets + d.E, codes, scales, codes_t, scales_t, stream);
 }
 

@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(256) scatter_rows_kernel(
 // ============================================================================ combine
 
 // Warp per token: out[t] = sum_j rows[token_to_row[t][j]] (+ shared[t]) in fp32,
-// slot order, one rounding to bf16.
+// slot order, one rounding to bf16.  Few tokens are spread over gridDim.y warps each, every
+// gridDim.y-th 32 pieces of 16 bytes a warp (4 tokens of 7168: 117 us with one).
 __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ rows, int T, int d8,
                                                       int k, const int32_t* __restrict__ token_to_row,
                                                       const uint4* __restrict__ shared,
@@ -303,7 +304,7 @@ __global__ void __launch_bounds__(256) combine_kernel(const uint4* __restrict__ 
     s_rows[wib][lane] = (r >= 0 && r < rows_cap) ? r : -1;
   }
   __syncwarp();
-  for (int c = lane; c < d8; c += 32) {
+  for (int c = blockIdx.y * 32 + lane; c < d8; c += 32 * gridDim.y) {
     float acc[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) acc[i] = 0.0f;
@@ -434,9 +435,9 @@ cudaError_t launch_combine_bwd(const void* dy, int T, int d, int E, int k, const
 cudaError_t launch_combine(const void* rows, int T, int d, int k, const int32_t* token_to_row,
                            const void* shared, void* out, int rows_cap, cudaStream_t stream) {
   if (T == 0) return cudaSuccess;
-  combine_kernel<<<(T + 7) / 8, 256, 0, stream>>>(static_cast<const uint4*>(rows), T, d / 8, k,
-                                                  token_to_row, static_cast<const uint4*>(shared),
-                                                  static_cast<uint4*>(out), rows_cap);
+  const int blocks = (T + 7) / 8, parts = max(1, min((d / 8 + 31) / 32, 2 * num_sms() / blocks));
+  combine_kernel<<<dim3(blocks, parts), 256, 0, stream>>>(static_cast<const uint4*>(rows), T, d / 8, k, token_to_row,
+                                                          static_cast<const uint4*>(shared), static_cast<uint4*>(out), rows_cap);
   count_launch();
   return cudaGetLastError();
 }

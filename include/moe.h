@@ -581,6 +581,7 @@ moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint
 /*
  * h = w silu(G) U of gu bf16 [rows][2f] (G | U, f % 16 == 0), w_rows [rows] fp32 or NULL (= 1),
  * in fp32, to the row form: codes [rows][f], scales [ceil(f / 128)][rows].  nrows_dev as above.
+ * A row of weight 0 gives zeros whatever its G and U are (they are not read).
  */
 moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows, int32_t f, const int32_t* nrows_dev,
                           uint8_t* codes, float* scales, void* stream);
@@ -601,6 +602,8 @@ moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const floa
  * moe_permute for the layer in this form (MOE_PREC_FP8_BLOCK; dims->prec may be any value):
  * the same maps, and the routed rows of x quantised as they are gathered, to the row form
  * (codes [rows][d]) and, where codes_t is given, the column form.  rows = moe_row_capacity.
+ * Padding rows are zeros where codes_t is given (weight gradients sum over them); without it
+ * they are left as they were, and what the products make of them is not to be used.
  */
 moe_status moe_permute_fp8(const moe_dims* dims, const moe_bf16* x, const int32_t* topk_idx, const float* topk_w,
                            const int32_t* split_sizes, const int32_t* row_offsets, const void* workspace,

@@ -151,7 +151,8 @@ def cuda(x):
 
 
 @pytest.mark.parametrize("R,N,K", [(1, 16, 16), (1, 4096, 7168), (5, 128, 128), (127, 144, 272), (128, 256, 256), (129, 272, 400),
-                                   (300, 2064, 1456), (1237, 640, 144)])
+                                   (300, 2064, 1456), (1237, 640, 144),
+                                   (5, 4096, 2064), (130, 272, 1040), (64, 16, 4096), (17, 1040, 7168)])
 @pytest.mark.parametrize("transposed", [False, True])
 def test_product(R, N, K, transposed):
     from dropless_mixture_experts_warp_gb300 import fp8
