@@ -300,6 +300,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 constexpr int NS_TENSORS = 32;       // of a launch
 constexpr int NS_PARTS = 64;         // blocks, and partial sums of squares, a matrix at most
 
+struct NsSteps {
+  int steps;
+  float c[3 * MOE_MUON_MAX_STEPS];
+};
+
 // Tensors of one shape, their matrices numbered through.
 struct NsTensors {
   const void* grad[NS_TENSORS];
@@ -313,6 +318,7 @@ struct NsTensors {
   int count;
   int grad_type, out_type;
   int rows, cols;                    // of a matrix
+  int vec;                           // every tensor starts at 16 bytes
   float momentum;
   int nesterov;
   const moe_adamw_control* control;
@@ -325,11 +331,40 @@ __device__ __forceinline__ int ns_find(const NsTensors& p, int e) {
 __device__ __forceinline__ long long ns_base(const NsTensors& p, int i, int e) {
   return static_cast<long long>(e - p.first[i] + (i == 0 ? p.skip0 : 0)) * p.rows * p.cols;
 }
-__device__ __forceinline__ float ns_load(const void* g, int type, long long i) {
-  return type == MOE_TYPE_BF16 ? bf16_lo(static_cast<const uint16_t*>(g)[i]) : static_cast<const float*>(g)[i];
+// Eight values from element i on, one by one where rows do not start at whole vectors (`n` of them are there).
+__device__ __forceinline__ void ns_get8(float (&v)[8], const void* g, int type, long long i, bool vec, int n) {
+  if (vec) {
+    if (type == MOE_TYPE_BF16) {
+      const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(g) + i);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) { v[2 * j] = bf16_lo(u[j]); v[2 * j + 1] = bf16_hi(u[j]); }
+    } else {
+      const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(g) + i);
+      const float4 x = f[0], y = f[1];
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      v[j] = j >= n ? 0.0f : type == MOE_TYPE_BF16 ? bf16_lo(static_cast<const uint16_t*>(g)[i + j]) : static_cast<const float*>(g)[i + j];
+  }
+}
+__device__ __forceinline__ void ns_put8(const float (&v)[8], void* o, int type, long long i, bool vec, int n) {
+  if (vec) {
+    if (type == MOE_TYPE_BF16) store8(static_cast<moe_bf16*>(o) + i, v);
+    else store8(static_cast<float*>(o) + i, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (j >= n) continue;
+      if (type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(o)[i + j] = __float2bfloat16_rn(v[j]);
+      else static_cast<float*>(o)[i + j] = v[j];
+    }
+  }
 }
 
-// m = momentum m + scale g; the sum of squares of what is orthogonalised, in NS_PARTS parts a matrix.
+// m = momentum m + scale g; the sum of squares of what is orthogonalised, in at most NS_PARTS parts a matrix.
 __global__ void __launch_bounds__(256) ns_momentum_kernel(const NsTensors p, float* parts) {
   wait_for_previous();
   launch_dependents();
@@ -338,93 +373,331 @@ __global__ void __launch_bounds__(256) ns_momentum_kernel(const NsTensors p, flo
   const bool skip = p.control && p.control->skip;
   const float gs = p.control ? p.control->grad_scale : 1.0f;
   const long long n = static_cast<long long>(p.rows) * p.cols, base = ns_base(p, i, e);
+  const bool vec = p.vec && n % 8 == 0;
   float s[1] = {0.0f};
   float* m = p.m[i];
-  for (long long j = blockIdx.x * 256ll + threadIdx.x; j < n && !skip; j += gridDim.x * 256ll) {
-    float u = gs * ns_load(p.grad[i], p.grad_type, base + j);
-    if (m) {
-      const float v = fmaf(p.momentum, m[base + j], u);
-      m[base + j] = v;
-      u = p.nesterov ? fmaf(p.momentum, v, u) : v;
+#pragma unroll 2
+  for (long long j = (blockIdx.x * 256ll + threadIdx.x) * 8; j < n && !skip; j += gridDim.x * 2048ll) {
+    const int left = static_cast<int>(n - j < 8 ? n - j : 8);
+    float g[8], v[8];
+    ns_get8(g, p.grad[i], p.grad_type, base + j, vec, left);
+    if (m) ns_get8(v, m, MOE_TYPE_FP32, base + j, vec, left);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      float u = gs * g[k];
+      if (m) {
+        v[k] = fmaf(p.momentum, v[k], u);
+        u = p.nesterov ? fmaf(p.momentum, v[k], u) : v[k];
+      }
+      s[0] = fmaf(u, u, s[0]);
     }
-    s[0] = fmaf(u, u, s[0]);
+    if (m) ns_put8(v, m, MOE_TYPE_FP32, base + j, vec, left);
   }
   row_sums<false>(s, buf);
   if (threadIdx.x == 0) parts[e * NS_PARTS + blockIdx.x] = s[0];
 }
 
-// X = scale U / |U| in two fp16 parts, [s][l] with zeros in the padding, transposed where the tensor is tall.
-// 32 x 32 tiles of X through shared memory.
+// The two kernels below move 64 x 64 tiles between a tensor and X, a thread eight columns of two rows on
+// either side, through shared memory where the tensor is tall and X its transpose.
+constexpr int NS_LD = 65;
+template <bool TALL>
+__device__ __forceinline__ void ns_turn(float (&v)[2][8], float* tile, int r, int c) {
+  if (!TALL) return;
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) tile[(r + 32 * k) * NS_LD + c + j] = v[k][j];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 2; ++k)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[k][j] = tile[(c + j) * NS_LD + r + 32 * k];
+}
+
+// X = scale U / |U| in two fp16 parts, [s][l] with zeros in the padding.
+template <bool TALL>
 __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const float* parts, int nparts, int s, int l, float scale,
                                                       __half* hi, __half* lo) {
   wait_for_previous();
   launch_dependents();
-  __shared__ float tile[32][33];
+  __shared__ float tile[TALL ? 64 * NS_LD : 1];
   const int e = blockIdx.z, i = ns_find(p, e);
   const float gs = p.control ? p.control->grad_scale : 1.0f;
-  const bool tall = p.rows > p.cols;
   float sum = 0.0f;
   for (int j = 0; j < nparts; ++j) sum += parts[e * NS_PARTS + j];
   // an overflowed sum makes NaNs rather than a silent zero
   const float inv = sum > 0.0f ? (isinf(sum) ? __int_as_float(0x7fc00000) : scale / sqrtf(sum)) : (sum == 0.0f ? 0.0f : sum);
   const long long base = ns_base(p, i, e);
-  const int x0 = blockIdx.x * 32, y0 = blockIdx.y * 32;       // of X
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
+  const int x0 = blockIdx.x * 64, y0 = blockIdx.y * 64;          // of X
+  float v[2][8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = (tall ? x0 : y0) + ty + 8 * k, c = (tall ? y0 : x0) + tx;   // of the tensor
-    float u = 0.0f;
-    if (r < p.rows && c < p.cols) {
-      const long long at = base + static_cast<long long>(r) * p.cols + c;
-      u = gs * ns_load(p.grad[i], p.grad_type, at);
-      if (p.m[i]) u = p.nesterov ? fmaf(p.momentum, p.m[i][at], u) : p.m[i][at];
+  for (int k = 0; k < 2; ++k) {
+    const int row = (TALL ? x0 : y0) + r + 32 * k, col = (TALL ? y0 : x0) + c;
+    const int left = row < p.rows ? max(0, min(8, p.cols - col)) : 0;
+    const bool vec = p.vec && p.cols % 8 == 0 && left == 8;
+    const long long at = base + static_cast<long long>(row) * p.cols + col;
+    float g[8], m[8];
+    ns_get8(g, p.grad[i], p.grad_type, at, vec, left);
+    if (p.m[i]) ns_get8(m, p.m[i], MOE_TYPE_FP32, at, vec, left);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float u = gs * g[j];
+      if (p.m[i]) u = p.nesterov ? fmaf(p.momentum, m[j], u) : m[j];
+      v[k][j] = u * inv;
     }
-    tile[ty + 8 * k][tx] = u * inv;
   }
-  __syncthreads();
+  ns_turn<TALL>(v, tile, r, c);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float v = tall ? tile[tx][ty + 8 * k] : tile[ty + 8 * k][tx];
-    const long long at = (static_cast<long long>(e) * s + y0 + ty + 8 * k) * l + x0 + tx;
-    const __half h = __float2half_rn(v);
-    hi[at] = h;
-    lo[at] = __float2half_rn(v - __half2float(h));
+  for (int k = 0; k < 2; ++k) {
+    const long long at = (static_cast<long long>(e) * s + y0 + r + 32 * k) * l + x0 + c;
+    uint32_t h[4], w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[j] = pack_half(v[k][2 * j], v[k][2 * j + 1]);
+      const float2 f = half_pair(h[j]);
+      w[j] = pack_half(v[k][2 * j] - f.x, v[k][2 * j + 1] - f.y);
+    }
+    *reinterpret_cast<uint4*>(hi + at) = make_uint4(h[0], h[1], h[2], h[3]);
+    *reinterpret_cast<uint4*>(lo + at) = make_uint4(w[0], w[1], w[2], w[3]);
   }
 }
 
 // w = w - lr (decay w + rms sqrt(max side) X), or out = X.
+template <bool TALL>
 __global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const __half* x, int s, int l, float unscale, float lr,
                                                         float rms) {
   wait_for_previous();
   launch_dependents();
-  __shared__ float tile[32][33];
+  __shared__ float tile[TALL ? 64 * NS_LD : 1];
   const int e = blockIdx.z, i = ns_find(p, e);
   if (p.control && p.control->skip) return;
   const float rate = p.control ? lr * p.control->lr_scale : lr;
-  const bool tall = p.rows > p.cols;
-  const int x0 = blockIdx.x * 32, y0 = blockIdx.y * 32;       // of the tensor
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
+  const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
+  const int x0 = blockIdx.x * 64, y0 = blockIdx.y * 64;          // of the tensor
+  float v[2][8];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = (tall ? x0 : y0) + ty + 8 * k, c = (tall ? y0 : x0) + tx;   // of X
-    tile[ty + 8 * k][tx] = r < s && c < l ? unscale * __half2float(x[(static_cast<long long>(e) * s + r) * l + c]) : 0.0f;
+  for (int k = 0; k < 2; ++k) {                                  // X's padding holds whole tiles
+    const long long at = (static_cast<long long>(e) * s + (TALL ? x0 : y0) + r + 32 * k) * l + (TALL ? y0 : x0) + c;
+    const uint4 h = *reinterpret_cast<const uint4*>(x + at);
+    const uint32_t u[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 f = half_pair(u[j]);
+      v[k][2 * j] = unscale * f.x;
+      v[k][2 * j + 1] = unscale * f.y;
+    }
   }
-  __syncthreads();
+  ns_turn<TALL>(v, tile, r, c);
   const long long base = ns_base(p, i, e);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int r = y0 + ty + 8 * k, c = x0 + tx;
-    if (r >= p.rows || c >= p.cols) continue;
-    const float v = tall ? tile[tx][ty + 8 * k] : tile[ty + 8 * k][tx];
-    const long long at = base + static_cast<long long>(r) * p.cols + c;
+  for (int k = 0; k < 2; ++k) {
+    const int row = y0 + r + 32 * k, col = x0 + c;
+    const int left = row < p.rows ? max(0, min(8, p.cols - col)) : 0;
+    if (left == 0) continue;
+    const bool vec = p.vec && p.cols % 8 == 0 && left == 8;
+    const long long at = base + static_cast<long long>(row) * p.cols + col;
     if (p.out[i]) {
-      if (p.out_type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(p.out[i])[at] = __float2bfloat16_rn(v);
-      else static_cast<float*>(p.out[i])[at] = v;
+      ns_put8(v[k], p.out[i], p.out_type, at, vec, left);
     } else {
-      const float w = p.w[i][at];
-      const float nw = fmaf(-rate, fmaf(p.decay[i], w, rms * v), w);
-      p.w[i][at] = nw;
-      if (p.w16[i]) reinterpret_cast<__nv_bfloat16*>(p.w16[i])[at] = __float2bfloat16_rn(nw);
+      float w[8];
+      ns_get8(w, p.w[i], MOE_TYPE_FP32, at, vec, left);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = fmaf(-rate, fmaf(p.decay[i], w[j], rms * v[k][j]), w[j]);
+      ns_put8(w, p.w[i], MOE_TYPE_FP32, at, vec, left);
+      if (p.w16[i]) ns_put8(w, p.w16[i], MOE_TYPE_BF16, at, vec, left);
+    }
+  }
+}
+
+// ------------------------------------------------------------------------ small matrices
+//
+// A matrix of at most 128 x 256 goes through the whole step in one block: X in fp32 registers (a thread has a
+// row, half of the columns), its fp16 form, A and B in shared memory, products in tensor memory.  Fifteen products of
+// one tile each are latency: 18 launches took 98 us for six matrices of 131 x 72.
+// X's fp16 form lies in blocks of 64 columns, 128 rows of 128 bytes each (128-byte swizzle), which the MMA reads
+// K-major in X X^T and MN-major in B X.
+
+constexpr int SM_BLOCK = 128 * 128;                  // bytes of 128 rows x 64 columns
+// X, A and B lie where X's fp32 form was before them and is after.
+__host__ __device__ constexpr int small_smem(int l) {
+  return (128 * (l + 1) * 4 > (l / 64 + 4) * SM_BLOCK ? 128 * (l + 1) * 4 : (l / 64 + 4) * SM_BLOCK) + 1024;
+}
+
+__device__ __forceinline__ void small_put(uint32_t block0, int row, int col, const float* v) {   // eight columns
+  const uint32_t at = block0 + (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+  st_shared_v4(at, pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
+}
+
+template <int L>
+__global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, const NsSteps h, float scale, float lr, float rms, int32_t* status) {
+  constexpr int HALF = L / 2;                        // X's columns of a thread
+  extern __shared__ uint8_t dyn_smem[];
+  __shared__ __align__(8) uint64_t bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort;
+  __shared__ float buf[32];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~static_cast<uintptr_t>(1023));
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    mbar_init(&bar, 1);
+    s_abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0) { tmem_alloc(&s_tmem, TMEM_COLS); tmem_relinquish(); }
+  float* stage = reinterpret_cast<float*>(smem);     // [128][L + 1]
+  for (int i = tid; i < 128 * (L + 1); i += 256) stage[i] = 0.0f;
+  tc_fence_before();
+  wait_for_previous();
+  launch_dependents();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  const int e = blockIdx.x, ti = ns_find(p, e);
+  const bool skip = p.control && p.control->skip;
+  const float gs = p.control ? p.control->grad_scale : 1.0f;
+  const bool tall = p.rows > p.cols;
+  const int n = p.rows * p.cols;
+  const long long base = ns_base(p, ti, e);
+  float* m = p.m[ti];
+  float sq[1] = {0.0f};
+  for (int i = tid; i < n && !skip; i += 256) {
+    const int r = i / p.cols, c = i - r * p.cols;
+    float u = gs * (p.grad_type == MOE_TYPE_BF16 ? bf16_lo(static_cast<const uint16_t*>(p.grad[ti])[base + i])
+                                                 : static_cast<const float*>(p.grad[ti])[base + i]);
+    if (m) {
+      const float v = fmaf(p.momentum, m[base + i], u);
+      m[base + i] = v;
+      u = p.nesterov ? fmaf(p.momentum, v, u) : v;
+    }
+    sq[0] = fmaf(u, u, sq[0]);
+    stage[(tall ? c : r) * (L + 1) + (tall ? r : c)] = u;
+  }
+  row_sums<false>(sq, buf);
+  __syncthreads();
+  const float inv = sq[0] > 0.0f ? (isinf(sq[0]) ? __int_as_float(0x7fc00000) : scale / sqrtf(sq[0])) : (sq[0] == 0.0f ? 0.0f : sq[0]);
+  const int row = (warp & 3) * 32 + lane, col0 = (warp >> 2) * HALF;
+  float x[HALF];
+#pragma unroll
+  for (int j = 0; j < HALF; ++j) x[j] = stage[row * (L + 1) + col0 + j] * inv;
+  __syncthreads();
+
+  const uint32_t sx = smem_u32(smem), sa = sx + (L / 64) * SM_BLOCK, sb = sa + 2 * SM_BLOCK;
+  const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  uint32_t phase = 0;
+  // products: the writers' shared memory is handed to the tensor core, one thread issues, all wait
+  auto hand = [&]() {
+    fence_proxy_async_smem();
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  };
+  auto take = [&]() {
+    mbar_wait_bounded(&bar, phase, &s_abort, status, WAIT_LIMIT_CYCLES);
+    phase ^= 1u;
+    __syncwarp();
+    tc_fence_after();
+  };
+#pragma unroll 1
+  for (int k = 0; k < h.steps; ++k) {
+    const float a = h.c[3 * k], b = h.c[3 * k + 1], c = h.c[3 * k + 2];
+#pragma unroll
+    for (int j = 0; j < HALF; j += 8) small_put(sx, row, col0 + j, x + j);
+    hand();
+    if (tid == 0) {                                  // A = X X^T
+#pragma unroll
+      for (int kk = 0; kk < L / 16; ++kk) {
+        const uint64_t d = smem_desc_sw128(sx + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
+        tc_mma_f16(tmem, d, d, idesc_fp16(128, 128, 0), kk != 0);
+      }
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    take();
+    const int ac = (warp >> 2) * 64;                 // A's and B's columns of a thread
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r[32];
+      tmem_ld32(tmem + lanes + ac + 32 * i, r);
+      tmem_wait_ld();
+      float v[32];
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / (scale * scale));
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) small_put(sa, row, ac + 32 * i + j, v + j);
+    }
+    hand();
+    if (tid == 0) {                                  // A A
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint64_t d = smem_desc_sw128(sa + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
+        tc_mma_f16(tmem + 128, d, d, idesc_fp16(128, 128, 0), kk != 0);
+      }
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    take();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      uint32_t r[32];
+      tmem_ld32(tmem + lanes + 128 + ac + 32 * i, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; j += 8) {
+        const int col = ac + 32 * i + j;
+        const uint4 q = ld_shared_v4(sa + (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4));
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        float v[8];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const float2 f = half_pair(u[t]);
+          v[2 * t] = fmaf(b, f.x, c * __uint_as_float(r[j + 2 * t]));
+          v[2 * t + 1] = fmaf(b, f.y, c * __uint_as_float(r[j + 2 * t + 1]));
+        }
+        small_put(sb, row, col, v);
+      }
+    }
+    hand();
+    if (tid == 0) {                                  // B X
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk)
+        tc_mma_f16(tmem + 256, smem_desc_sw128(sb + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024),
+                   smem_desc_sw128(sx + kk * 2048, SM_BLOCK, 1024), idesc_fp16(128, L, 1), kk != 0);
+      tc_commit(&bar);
+    }
+    __syncwarp();
+    take();
+#pragma unroll
+    for (int i = 0; i < HALF / 32; ++i) {
+      uint32_t r[32];
+      tmem_ld32(tmem + lanes + 256 + col0 + 32 * i, r);
+      tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) x[32 * i + j] = fmaf(a, x[32 * i + j], __uint_as_float(r[j]));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < HALF; ++j) stage[row * (L + 1) + col0 + j] = x[j] * (1.0f / scale);
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
+  if (skip) return;
+  const float rate = p.control ? lr * p.control->lr_scale : lr;
+  for (int i = tid; i < n; i += 256) {
+    const int r = i / p.cols, c = i - r * p.cols;
+    const float v = stage[(tall ? c : r) * (L + 1) + (tall ? r : c)];
+    const long long at = base + i;
+    if (p.out[ti]) {
+      if (p.out_type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(p.out[ti])[at] = __float2bfloat16_rn(v);
+      else static_cast<float*>(p.out[ti])[at] = v;
+    } else {
+      const float w = p.w[ti][at];
+      const float nw = fmaf(-rate, fmaf(p.decay[ti], w, rms * v), w);
+      p.w[ti][at] = nw;
+      if (p.w16[ti]) reinterpret_cast<__nv_bfloat16*>(p.w16[ti])[at] = __float2bfloat16_rn(nw);
     }
   }
 }
@@ -473,9 +746,28 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   const int nparts = static_cast<int>(std::min<long long>(NS_PARTS, (n + 2047) / 2048));
   float scale = 1.0f;
   while (scale * scale * 4.0f <= o.l) scale *= 2.0f;
+  const bool tall = t.rows > t.cols;
+  const float rms = static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(t.rows, t.cols))));
+  if (o.s == 128 && o.l <= 256) {
+    NsSteps steps;
+    steps.steps = h.steps;
+    for (int i = 0; i < 3 * h.steps; ++i) steps.c[i] = h.coefficients[i];
+    const int smem = small_smem(o.l);
+    const cudaError_t err = o.l == 128 ? allow_smem<ns_small_kernel<128>>(smem) : allow_smem<ns_small_kernel<256>>(smem);
+    if (err != cudaSuccess) return err;
+    return o.l == 128 ? launch_early(ns_small_kernel<128>, dim3(batch), dim3(256), smem, st, t, steps, scale, lr, rms, status)
+                      : launch_early(ns_small_kernel<256>, dim3(batch), dim3(256), smem, st, t, steps, scale, lr, rms, status);
+  }
+  t.vec = 1;
+  for (int i = 0; i < t.count; ++i)
+    for (const void* q : {t.grad[i], static_cast<const void*>(t.m[i]), static_cast<const void*>(t.w[i]), static_cast<const void*>(t.w16[i]),
+                          static_cast<const void*>(t.out[i])})
+      t.vec = t.vec && ptr_aligned16(q);
   cudaError_t err = launch_early(ns_momentum_kernel, dim3(nparts, batch), dim3(256), 0, st, t, parts);
   if (err != cudaSuccess) return err;
-  err = launch_early(ns_load_kernel, dim3(o.l / 32, o.s / 32, batch), dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo);
+  const dim3 tiles_x(o.l / 64, o.s / 64, batch), tiles_t((t.cols + 63) / 64, (t.rows + 63) / 64, batch);
+  err = tall ? launch_early(ns_load_kernel<true>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo)
+             : launch_early(ns_load_kernel<false>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo);
   if (err != cudaSuccess) return err;
   const uint64_t rows = static_cast<uint64_t>(batch) * o.s;
   CUtensorMap xk[2], xn[2], xs[2], los, ak, as, bk, bs;
@@ -500,9 +792,8 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
     err = launch_ns<NS_APPLY>(bk, xn[cur], xs[cur], los, xs[cur ^ 1], los, p, st);
     if (err != cudaSuccess) return err;
   }
-  const float rms = static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(t.rows, t.cols))));
-  return launch_early(ns_update_kernel, dim3((t.cols + 31) / 32, (t.rows + 31) / 32, batch), dim3(256), 0, st, t, x[cur], o.s, o.l,
-                      1.0f / scale, lr, rms);
+  return tall ? launch_early(ns_update_kernel<true>, tiles_t, dim3(256), 0, st, t, x[cur], o.s, o.l, 1.0f / scale, lr, rms)
+              : launch_early(ns_update_kernel<false>, tiles_t, dim3(256), 0, st, t, x[cur], o.s, o.l, 1.0f / scale, lr, rms);
 }
 
 }  // namespace moe
