@@ -11,6 +11,10 @@
 // normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
 // values, which later steps amplify by up to a each; X is therefore kept in two fp16 parts, the second
 // read for that addend alone (low-rank plus noise: 3.4e-3 off without it, 2.4e-4 with it).
+// In the last two steps X is near orthogonal, A near a multiple of I and B near a negative one; taking the
+// multiples off first, A' = A - u I and X' = (a - t) X + (B + t I) X with u = 1/2, t = a - 1, leaves fp16 less to
+// round (the same polynomial in other terms: 1.3e-3 -> 5.2e-4 on strong directions under noise).  (A second
+// part of A for its addend alone does not help: A's rounding in b A and in c A A partly cancels.)
 // A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
 //
 // Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.
@@ -35,7 +39,7 @@ enum { NS_GRAM = 0, NS_POLY = 1, NS_APPLY = 2 };   // A = X X^T; B = b A + c A A
 
 struct NsParams {
   int batch, s, n, k;       // a matrix's padded rows, output columns, contraction
-  float alpha, beta;        // out = alpha * product + beta * in
+  float alpha, beta, diag;  // out = alpha * product + beta * in + diag I (not NS_APPLY)
   int lo_out;               // NS_APPLY: X's second part is written
   int32_t* status;
 };
@@ -236,9 +240,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
           tmem_wait_ld();
           uint32_t oh[16], ol[16];
+          const float diag = KIND != NS_APPLY && row0 == col0 + 32 * i ? p.diag : 0.0f;
 #pragma unroll
           for (int j = 0; j < 16; ++j) {
             float a = p.alpha * __uint_as_float(r[2 * j]), b = p.alpha * __uint_as_float(r[2 * j + 1]);
+            if (KIND != NS_APPLY) {
+              a += lane == 2 * j ? diag : 0.0f;
+              b += lane == 2 * j + 1 ? diag : 0.0f;
+            }
             if (KIND != NS_GRAM) {
               const float2 x = half_pair(hi[j]), z = half_pair(lo[j]);
               a = fmaf(p.beta, x.x + z.x, a);
@@ -300,10 +309,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 constexpr int NS_TENSORS = 32;       // of a launch
 constexpr int NS_PARTS = 64;         // blocks, and partial sums of squares, a matrix at most
 
+// A step as the kernels take it: A' = X X^T - u I;  B = c A' A' + b A' + d I;  X' = a X + B X.
+struct NsStep {
+  float u, a, b, c, d;
+};
 struct NsSteps {
   int steps;
-  float c[3 * MOE_MUON_MAX_STEPS];
+  NsStep s[MOE_MUON_MAX_STEPS];
 };
+static NsSteps ns_steps(const moe_muon_hyper& h) {
+  NsSteps o{};
+  o.steps = h.steps;
+  for (int k = 0; k < h.steps; ++k) {
+    const double a = h.coefficients[3 * k], b = h.coefficients[3 * k + 1], c = h.coefficients[3 * k + 2];
+    const bool late = k >= 1 && k >= h.steps - 2;
+    const double u = late ? 0.5 : 0.0, t = late ? a - 1.0 : 0.0;
+    o.s[k] = NsStep{static_cast<float>(u), static_cast<float>(a - t), static_cast<float>(b + 2 * u * c), static_cast<float>(c),
+                    static_cast<float>(b * u + c * u * u + t)};
+  }
+  return o;
+}
 
 // Tensors of one shape, their matrices numbered through.
 struct NsTensors {
@@ -601,7 +626,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   };
 #pragma unroll 1
   for (int k = 0; k < h.steps; ++k) {
-    const float a = h.c[3 * k], b = h.c[3 * k + 1], c = h.c[3 * k + 2];
+    const NsStep q = h.s[k];
 #pragma unroll
     for (int j = 0; j < HALF; j += 8) small_put(sx, row, col0 + j, x + j);
     hand();
@@ -623,7 +648,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
       tmem_wait_ld();
       float v[32];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / (scale * scale));
+      for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / (scale * scale)) - (row == ac + 32 * i + j ? q.u : 0.0f);
 #pragma unroll
       for (int j = 0; j < 32; j += 8) small_put(sa, row, ac + 32 * i + j, v + j);
     }
@@ -646,14 +671,14 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const int col = ac + 32 * i + j;
-        const uint4 q = ld_shared_v4(sa + (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4));
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        const uint4 w = ld_shared_v4(sa + (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4));
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
         float v[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const float2 f = half_pair(u[t]);
-          v[2 * t] = fmaf(b, f.x, c * __uint_as_float(r[j + 2 * t]));
-          v[2 * t + 1] = fmaf(b, f.y, c * __uint_as_float(r[j + 2 * t + 1]));
+          v[2 * t] = fmaf(q.b, f.x, q.c * __uint_as_float(r[j + 2 * t])) + (row == col + 2 * t ? q.d : 0.0f);
+          v[2 * t + 1] = fmaf(q.b, f.y, q.c * __uint_as_float(r[j + 2 * t + 1])) + (row == col + 2 * t + 1 ? q.d : 0.0f);
         }
         small_put(sb, row, col, v);
       }
@@ -674,7 +699,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
       tmem_ld32(tmem + lanes + 256 + col0 + 32 * i, r);
       tmem_wait_ld();
 #pragma unroll
-      for (int j = 0; j < 32; ++j) x[32 * i + j] = fmaf(a, x[32 * i + j], __uint_as_float(r[j]));
+      for (int j = 0; j < 32; ++j) x[32 * i + j] = fmaf(q.a, x[32 * i + j], __uint_as_float(r[j]));
     }
   }
   tc_fence_before();
@@ -747,11 +772,9 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   float scale = 1.0f;
   while (scale * scale * 4.0f <= o.l) scale *= 2.0f;
   const bool tall = t.rows > t.cols;
+  const NsSteps steps = ns_steps(h);
   const float rms = static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(t.rows, t.cols))));
   if (o.s == 128 && o.l <= 256) {
-    NsSteps steps;
-    steps.steps = h.steps;
-    for (int i = 0; i < 3 * h.steps; ++i) steps.c[i] = h.coefficients[i];
     const int smem = small_smem(o.l);
     const cudaError_t err = o.l == 128 ? allow_smem<ns_small_kernel<128>>(smem) : allow_smem<ns_small_kernel<256>>(smem);
     if (err != cudaSuccess) return err;
@@ -780,14 +803,14 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   if (!ok) return cudaErrorInvalidValue;
   int cur = 0;
   for (int k = 0; k < h.steps; ++k, cur ^= 1) {
-    const float a = h.coefficients[3 * k], b = h.coefficients[3 * k + 1], c = h.coefficients[3 * k + 2];
-    NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, 0, status};
+    const NsStep& q = steps.s[k];
+    NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, -q.u, 0, status};
     err = launch_ns<NS_GRAM>(xk[cur], xk[cur], as, as, as, as, p, st);
     if (err != cudaSuccess) return err;
-    p.k = o.s; p.alpha = c; p.beta = b;
+    p.k = o.s; p.alpha = q.c; p.beta = q.b; p.diag = q.d;
     err = launch_ns<NS_POLY>(ak, ak, as, as, bs, bs, p, st);
     if (err != cudaSuccess) return err;
-    p.n = o.l; p.alpha = 1.0f; p.beta = a;
+    p.n = o.l; p.alpha = 1.0f; p.beta = q.a;
     p.lo_out = k + 1 < h.steps;
     err = launch_ns<NS_APPLY>(bk, xn[cur], xs[cur], los, xs[cur ^ 1], los, p, st);
     if (err != cudaSuccess) return err;

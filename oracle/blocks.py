@@ -117,8 +117,8 @@ def muon_step(w, m, grad, lr, momentum, decay, rms, nesterov=True, coefficients=
 
 
 def newton_schulz_rounded(x, coefficients=COEFFICIENTS):
-    """newton_schulz as the kernels round it: products on fp16 operands, X in two parts in the addend, everything else
-    exact.  How far it is from newton_schulz is what that arithmetic costs."""
+    """newton_schulz as the kernels round it: products on fp16 operands, X in two parts in the addend, multiples of I
+    taken off A and B in the last two steps, everything else exact.  How far it is from newton_schulz is what that arithmetic costs."""
     h = lambda v: v.astype(np.float16).astype(np.float64)  # noqa: E731
     x = x.T if x.shape[0] > x.shape[1] else x
     n = np.linalg.norm(x)
@@ -129,10 +129,12 @@ def newton_schulz_rounded(x, coefficients=COEFFICIENTS):
     x = scale * x / n if n > 0 else np.zeros_like(x)
     hi = h(x)
     lo = h(x - hi)
-    for a, b, c in coefficients:
-        A = h(hi @ hi.T / scale ** 2)
-        B = h(b * A + c * (A @ A))
-        v = a * (hi + lo) + B @ hi
+    for k, (a, b, c) in enumerate(coefficients):
+        late = k >= 1 and k >= len(coefficients) - 2
+        u, t, eye = 0.5 * late, (a - 1) * late, np.eye(x.shape[0])
+        A = h(hi @ hi.T / scale ** 2 - u * eye)
+        B = h(c * (A @ A) + (b + 2 * u * c) * A + (b * u + c * u * u + t) * eye)
+        v = (a - t) * (hi + lo) + B @ hi
         hi = h(v)
         lo = h(v - hi)
     return hi / scale
