@@ -20,6 +20,7 @@
 // Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.
 #include "around.cuh"
 #include "kernels.h"
+#include "pipe.cuh"
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -81,7 +82,9 @@ __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int t) {
 
 // One CTA pair computes a 256 x 256 tile (tcgen05 cta_group::2), as in gemm2.cuh: warp 0 of each
 // CTA loads its halves, warp 1 of the leader multiplies, eight warps of each take its 128 rows out.
-// What the sum is added to arrives by tensor loads in a warp's boxes, a chunk ahead.
+// What the sum is added to arrives by tensor loads in a warp's boxes, a chunk of 32 columns ahead, across
+// tiles.  The MMA warp looks for two stages at a time: a wait's latency, 130 cycles, comes on top of the
+// 512 that a stage's MMAs take.
 template <int KIND>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
@@ -120,72 +123,74 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const int mt = (p.s + 255) / 256;
   const int total = p.batch * (KIND == NS_APPLY ? mt * ((p.n + 255) / 256) : mt * (mt + 1) / 2);
   const int kblocks = p.k / BK;
-  volatile int* abort_flag = &s_abort;
+  volatile int* const aborted = &s_abort;
+  const uint32_t leader = lane == 0;
 
   if (warp == 0) {
-    if (lane == 0) {
-      int stage = 0;
-      uint32_t phase = 0, armed = 0, armed_parity = 0;
-      bool ok = true;
-      for (int t = pair_id; ok && t < total; t += npairs) {
-        const NsTile c = ns_tile<KIND>(p, t);
-        // a half past the matrix's rows (or columns) reads the zero fill past the tensor
-        const int a_local = c.m * 256 + rank * 128, b_local = c.n * 256 + rank * 128;
-        const int a_row = a_local < p.s ? c.e * p.s + a_local : DEAD_ROW;
-        const int b_row = b_local < p.n ? c.e * p.s + b_local : DEAD_ROW;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait_bounded(&empty_bar[stage], phase ^ 1, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
-          uint8_t* sa = smem + stage * P_STAGE_BYTES;
-          uint8_t* sb = sa + P_A_BYTES;
-          const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&full_bar[stage], 2 * P_STAGE_BYTES);
-            armed |= 1u << stage;
-            armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-          }
-          tma_load_2d_pair(sa, &tmA, bar, kb * BK, a_row);
-          if (!B_MN) {
-            tma_load_2d_pair(sb, &tmB, bar, kb * BK, b_row);
-          } else {
-            tma_load_2d_pair(sb, &tmB, bar, b_local, c.e * p.s + kb * BK);
-            tma_load_2d_pair(sb + 8192, &tmB, bar, b_local + 64, c.e * p.s + kb * BK);
-          }
-          if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
+    int stage = 0;
+    uint32_t phase = 0, armed = 0, armed_parity = 0;
+    for (int t = pair_id; t < total && !*aborted; t += npairs) {
+      const NsTile c = ns_tile<KIND>(p, t);
+      // a half past the matrix's rows (or columns) reads the zero fill past the tensor
+      const int a_local = c.m * 256 + rank * 128, b_local = c.n * 256 + rank * 128;
+      const int a_row = a_local < p.s ? c.e * p.s + a_local : DEAD_ROW;
+      const int b_row = b_local < p.n ? c.e * p.s + b_local : DEAD_ROW;
+#pragma unroll 1
+      for (int kb = 0; kb < kblocks; ++kb) {
+        pipe_wait(&empty_bar[stage], phase ^ 1, &s_abort, p.status);
+        uint8_t* sa = smem + stage * P_STAGE_BYTES;
+        uint8_t* sb = sa + P_A_BYTES;
+        const uint32_t bar = mapa_shared(smem_u32(&full_bar[stage]), 0);
+        pipe_expect(&full_bar[stage], 2 * P_STAGE_BYTES, leader && rank == 0);
+        armed |= 1u << stage;
+        armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
+        pipe_load_2d_pair(sa, &tmA, bar, kb * BK, a_row, leader);
+        if (!B_MN) {
+          pipe_load_2d_pair(sb, &tmB, bar, kb * BK, b_row, leader);
+        } else {
+          pipe_load_2d_pair(sb, &tmB, bar, b_local, c.e * p.s + kb * BK, leader);
+          pipe_load_2d_pair(sb + 8192, &tmB, bar, b_local + 64, c.e * p.s + kb * BK, leader);
         }
+        if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
       }
-      if (rank == 0)
-        for (int s = 0; s < NS_STAGES; ++s)
-          if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
     }
+    if (lane == 0 && rank == 0)
+      for (int s = 0; s < NS_STAGES; ++s)
+        if ((armed >> s) & 1u) mbar_drain(&full_bar[s], (armed_parity >> s) & 1u, WAIT_LIMIT_CYCLES);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       constexpr uint32_t idesc = idesc_fp16(256, 256, B_MN ? 1 : 0);
+      const uint64_t desc_a = smem_desc_sw128(smem_u32(smem), 16, 1024);
+      const uint64_t desc_b = B_MN ? smem_desc_sw128(smem_u32(smem) + P_A_BYTES, 8192, 1024) : smem_desc_sw128(smem_u32(smem) + P_A_BYTES, 16, 1024);
       int stage = 0, acc = 0;
       uint32_t phase = 0, acc_phase = 0;
-      bool ok = true;
-      for (int t = pair_id; ok && t < total; t += npairs) {
-        if (!mbar_wait_bounded(&tempty_bar[acc], acc_phase ^ 1, abort_flag, p.status, WAIT_LIMIT_CYCLES)) break;
+      for (int t = pair_id; t < total && !*aborted; t += npairs) {
+        pipe_wait(&tempty_bar[acc], acc_phase ^ 1, &s_abort, p.status);
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC_STRIDE;
-        for (int kb = 0; kb < kblocks; ++kb) {
-          if (!mbar_wait_bounded(&full_bar[stage], phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
+#pragma unroll 1
+        for (int kb = 0; kb < kblocks; kb += 2) {    // the contraction is a multiple of 128
+          const int next = stage + 1 == NS_STAGES ? 0 : stage + 1;
+          pipe_wait_two(&full_bar[stage], phase, &full_bar[next], phase ^ (next == 0), &s_abort, p.status);
           tc_fence_after();
-          const uint32_t sa = smem_u32(smem + stage * P_STAGE_BYTES), sb = sa + P_A_BYTES;
 #pragma unroll
-          for (int kk = 0; kk < BK / UMMA_K; ++kk)
-            tc_mma_f16_pair(d_tmem, smem_desc_sw128(sa + kk * 32, 16, 1024),
-                            B_MN ? smem_desc_sw128(sb + kk * 2048, 8192, 1024) : smem_desc_sw128(sb + kk * 32, 16, 1024), idesc,
-                            (kb | kk) != 0 ? 1u : 0u);
-          tc_commit_pair_mc(&empty_bar[stage], 0x3);
-          if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
+          for (int two = 0; two < 2; ++two) {
+            const uint32_t at = static_cast<uint32_t>(stage * (P_STAGE_BYTES >> 4));
+#pragma unroll
+            for (int kk = 0; kk < BK / UMMA_K; ++kk)
+              pipe_mma_f16_pair(d_tmem, desc_a + at + 2 * kk, desc_b + at + (B_MN ? 128 : 2) * kk, idesc, (kb | two | kk) != 0 ? 1u : 0u, leader);
+            pipe_commit_pair_mc(&empty_bar[stage], 0x3, leader);
+            if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
+          }
         }
-        if (!ok) break;
-        tc_commit_pair_mc(&tfull_bar[acc], 0x3);
+        pipe_commit_pair_mc(&tfull_bar[acc], 0x3, leader);
         if (++acc == 2) { acc = 0; acc_phase ^= 1; }
       }
-      tc_commit_pair(&drain_bar);
-      mbar_drain(&drain_bar, 0, WAIT_LIMIT_CYCLES);
+      if (lane == 0) {
+        tc_commit_pair(&drain_bar);
+        mbar_drain(&drain_bar, 0, WAIT_LIMIT_CYCLES);
+      }
     }
     __syncwarp();
   } else {
@@ -196,38 +201,60 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     const int sw = (lane >> 1) & 3;                  // 64-byte swizzle of this lane's row of a box
     const uint32_t in_row = smem_u32(in) + lane * 64, out_row = smem_u32(out) + lane * 64;
     int acc = 0;
-    uint32_t acc_phase = 0, in_phase = 0;
-    bool inflight = false;
-    auto issue = [&](int x, int y) {                 // the boxes that the sum at (x, y) is added to
-      if (KIND == NS_GRAM) return;
-      if (lane == 0) {
-        fence_proxy_async_smem();
-        mbar_arrive_expect_tx(ibar, KIND == NS_APPLY ? 2 * NS_BOX : NS_BOX);
-        tma_load_2d(in, &tmIn, ibar, x, y);
-        if (KIND == NS_APPLY) tma_load_2d(in + NS_BOX, &tmInLo, ibar, x, y);
-      }
-      inflight = true;
+    uint32_t acc_phase = 0, taken = 0, asked = 0;    // chunks
+    // the chunks to ask for: of this warp's tiles (a warp whose rows or columns lie past a matrix has none there)
+    struct Place {
+      int row0, col0, y;
+      bool live;
     };
-    for (int t = pair_id; t < total; t += npairs) {
+    auto place = [&](int t) {
       const NsTile c = ns_tile<KIND>(p, t);
-      const int row0 = c.m * 256 + rank * 128 + q * 32;          // of the matrix
-      const int col0 = c.n * 256 + half * 128;
-      const bool live = row0 < p.s && col0 < p.n;                // 128-row and 128-column halves are whole
-      const int y = c.e * p.s + row0;
-      if (live) issue(col0, y);
-      if (!mbar_wait_bounded(&tfull_bar[acc], acc_phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) break;
+      Place o;
+      o.row0 = c.m * 256 + rank * 128 + q * 32;      // of the matrix
+      o.col0 = c.n * 256 + half * 128;
+      o.live = o.row0 < p.s && o.col0 < p.n;         // 128-row and 128-column halves are whole
+      o.y = c.e * p.s + o.row0;
+      return o;
+    };
+    int ask_t = pair_id, ask_i = 0;
+    Place ask{0, 0, 0, false};
+    auto next_live = [&]() {
+      while (ask_t < total && !(ask = place(ask_t)).live) ask_t += npairs;
+    };
+    auto issue = [&]() {                             // the next chunk's boxes
+      if (KIND == NS_GRAM || ask_t >= total) return;
+      const int x = ask.col0 + 32 * ask_i;
+      if (lane == 0) fence_proxy_async_smem();
+      pipe_expect(ibar, KIND == NS_APPLY ? 2 * NS_BOX : NS_BOX, leader);
+      pipe_load_2d(in, &tmIn, ibar, x, ask.y, leader);
+      if (KIND == NS_APPLY) pipe_load_2d(in + NS_BOX, &tmInLo, ibar, x, ask.y, leader);
+      ++asked;
+      if (++ask_i == 4) {
+        ask_i = 0;
+        ask_t += npairs;
+        next_live();
+      }
+    };
+    if (KIND != NS_GRAM) {
+      next_live();
+      issue();
+    }
+    for (int t = pair_id; t < total && !*aborted; t += npairs) {
+      const NsTile c = ns_tile<KIND>(p, t);
+      const Place at = place(t);
+      const int row0 = at.row0, col0 = at.col0, y = at.y;
+      pipe_wait(&tfull_bar[acc], acc_phase, &s_abort, p.status);
       tc_fence_after();
       const uint32_t tbase = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * ACC_STRIDE + half * 128;
-      bool ok = true;
-      if (live) {
+      if (at.live) {
         for (int i = 0; i < 4; ++i) {
           uint32_t r[32];
           tmem_ld32(tbase + 32 * i, r);
           uint32_t hi[16], lo[16];
           if (KIND != NS_GRAM) {
-            if (!mbar_wait_bounded(ibar, in_phase, abort_flag, p.status, WAIT_LIMIT_CYCLES)) { ok = false; break; }
-            in_phase ^= 1u;
-            inflight = false;
+            pipe_wait(ibar, taken & 1u, &s_abort, p.status);
+            if (*aborted) break;
+            ++taken;
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               const uint4 x = ld_shared_v4(in_row + ((v ^ sw) << 4));
@@ -236,7 +263,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
               lo[4 * v] = z.x; lo[4 * v + 1] = z.y; lo[4 * v + 2] = z.z; lo[4 * v + 3] = z.w;
             }
             __syncwarp();
-            if (i < 3) issue(col0 + 32 * (i + 1), y);
+            issue();
           }
           tmem_wait_ld();
           uint32_t oh[16], ol[16];
@@ -289,13 +316,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
           }
         }
       }
-      if (!ok) break;
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0));
+      pipe_arrive_cluster(mapa_shared(smem_u32(&tempty_bar[acc]), 0), leader);
       if (++acc == 2) { acc = 0; acc_phase ^= 1; }
     }
-    if (inflight) mbar_drain(ibar, in_phase, WAIT_LIMIT_CYCLES);
+    for (; taken < asked; ++taken) mbar_drain(ibar, taken & 1u, WAIT_LIMIT_CYCLES);   // after an abort
     if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();

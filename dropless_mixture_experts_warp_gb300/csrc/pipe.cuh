@@ -36,6 +36,23 @@ __device__ __forceinline__ void pipe_wait(uint64_t* bar, uint32_t parity, int* a
       : "memory");
 }
 
+// Both of two barriers, asked together: their latencies overlap.
+__device__ __forceinline__ void pipe_wait_two(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1, int* abort_flag,
+                                              int32_t* status) {
+  uint32_t both;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 q, [%3], %4;\n\t"
+      "and.pred p, p, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(both)
+      : "r"(smem_u32(bar0)), "r"(parity0), "r"(smem_u32(bar1)), "r"(parity1)
+      : "memory");
+  if (__all_sync(0xffffffffu, both)) return;
+  pipe_wait(bar0, parity0, abort_flag, status);
+  pipe_wait(bar1, parity1, abort_flag, status);
+}
+
 // The lane with `act` not 0 does it.
 __device__ __forceinline__ void pipe_arrive(uint64_t* bar, uint32_t act) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_u32(bar)),
