@@ -23,19 +23,19 @@ namespace moe {
 constexpr int F8_K = 128;                                   // codes a stage, a scale block
 constexpr int F8_A_BYTES = BM * F8_K;                       // 16 KB
 constexpr int F8_B_BOX = 128;                               // rows of a B tensor load
-constexpr int F8_EPI_WARPS = 16;                            // four a lane quarter, a quarter of the columns each
+constexpr int F8_EPI_WARPS = 8;                             // two a lane quarter, half of the columns each
 // Warp 0 loads operands, warps 1 and 2 multiply every other block (a block's issue, its waits and commits
 // take one warp longer than its MMA takes), warp 3 loads scales.  The four hand registers to
-// those that hold the sums: 128 x 64 + 512 x 104 are the 640 x 96 of the launch.
+// those that hold the sums: 128 x 64 + 256 x 216 of the 384 x 168 of the launch.
 constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_THREADS = 32 * (F8_EPI_WARP0 + F8_EPI_WARPS);
-constexpr int F8_REGS_FEW = 64, F8_REGS_MANY = 104;
-static_assert(128 * F8_REGS_FEW + 512 * F8_REGS_MANY <= 640 * 96, "registers of the block at launch");
+constexpr int F8_REGS_FEW = 64, F8_REGS_MANY = 216;
+static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_MANY <= 384 * 168, "registers of the block at launch");
 // Operand stages: as many as shared memory holds beside the output's boxes.  A warp stages its
 // 32 rows at once (BR = 32), or 8 at a time (BR = 8), where a fourth stage is worth more.
 __host__ __device__ constexpr int f8_stages(int bn, int br) { return bn == 256 ? (br == 32 ? 3 : 4) : 5; }
 __host__ __device__ constexpr int f8_stage_bytes(int bn) { return F8_A_BYTES + bn * F8_K; }
-__host__ __device__ constexpr int f8_box_bytes(int bn, int br) { return br * bn / 4 * 2; }
+__host__ __device__ constexpr int f8_box_bytes(int bn, int br) { return br * bn / 2 * 2; }
 // Scales of a block: the tile's 128 rows, then its columns (SCHED_KGROUP) or the columns' blocks.  The
 // loader is at most the operand stages ahead of the MMAs, these two blocks ahead of the sums, so
 // that with three slots more than stages it never writes one that is still read.
@@ -69,20 +69,14 @@ struct Fp8Params {
 __host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
   return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
-// 32 lanes x 16 consecutive fp32 columns.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr));
-}
-// The wait for such a load; it hands the registers on, so that nothing uses them before it.
-__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+// The wait for loads of 32 columns; it hands the registers on, so that nothing uses them before it.
+__device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
-                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]),
+                 "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]),
+                 "+r"(r[28]), "+r"(r[29])::"memory");
+  asm volatile("" : "+r"(r[30]), "+r"(r[31])::"memory");
 }
 // acc += (x, y) * s, kept in its place among the loads: moved past the next ones, the registers that they
 // hold would not fit beside the sums.
@@ -106,7 +100,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
   constexpr int STAGES = f8_stages(BN, BR), STAGE_BYTES = f8_stage_bytes(BN);
-  constexpr int WC = BN / 4;       // columns of an epilogue warp
+  constexpr int WC = BN / 2;       // columns of an epilogue warp
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];
   __shared__ __align__(8) uint64_t empty_bar[STAGES];
@@ -317,27 +311,32 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         if (SCHED == SCHED_ROWS) s *= sc[BM + (part * WC) / 128];
         const f32x2 s2 = pair(s, s);
         const ulonglong2* cs = reinterpret_cast<const ulonglong2*>(sc + BM + part * WC);
-        // 16 columns at a time: beside the sums a thread has no registers for more
+        // 64 columns at a time (32 where they have scales of their own); the last are out of tensor memory
+        // before they are added
+        constexpr int CH = SCHED == SCHED_ROWS ? 64 : 32;
 #pragma unroll
-        for (int i = 0; i < WC / 16; ++i) {
-          uint32_t r[16];
-          tmem_ld16(lane_base + buf * 256 + 16 * i, r);
-          tmem_wait_ld16(r);
-          if (i == WC / 16 - 1) {
+        for (int i = 0; i < WC / CH; ++i) {
+          uint32_t r[CH / 32][32];
+#pragma unroll
+          for (int k = 0; k < CH / 32; ++k) tmem_ld32(lane_base + buf * 256 + CH * i + 32 * k, r[k]);
+#pragma unroll
+          for (int k = 0; k < CH / 32; ++k) tmem_wait_ld32(r[k]);
+          if (i == WC / CH - 1) {
             tc_fence_before();
             __syncwarp();
             pipe_arrive(&tempty_bar[buf], leader);
           }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
+          for (int j = 0; j < CH / 4; ++j) {
             f32x2 a = s2, b = s2;
             if (SCHED == SCHED_KGROUP) {
-              const ulonglong2 v = cs[4 * i + j];
+              const ulonglong2 v = cs[CH / 4 * i + j];
               a = mul2(s2, v.x);
               b = mul2(s2, v.y);
             }
-            add_scaled(acc[8 * i + 2 * j], r[4 * j], r[4 * j + 1], a);
-            add_scaled(acc[8 * i + 2 * j + 1], r[4 * j + 2], r[4 * j + 3], b);
+            const uint32_t* w = &r[j >> 3][4 * (j & 7)];
+            add_scaled(acc[CH / 2 * i + 2 * j], w[0], w[1], a);
+            add_scaled(acc[CH / 2 * i + 2 * j + 1], w[2], w[3], b);
           }
         }
       }
@@ -349,11 +348,10 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         break;
       }
       if (*aborted) break;
-      // bf16 through the warp's box (rows of WC values, 16-byte pieces swizzled as the tensor store
-      // expects them); boxes past the ends are skipped
+      // bf16 through the warp's boxes of 64 columns (16-byte pieces swizzled as the tensor store expects
+      // them); boxes past the ends are skipped
       const int y0 = c.y + q * 32, y_end = SCHED == SCHED_ROWS ? c.z : p.M;
-      const int swz = WC == 64 ? lane & 7 : (lane >> 1) & 3;
-      const uint32_t at = smem_u32(box) + (BR == 32 ? lane : lane & 7) * (WC * 2);
+      const uint32_t at = smem_u32(box) + (BR == 32 ? lane : lane & 7) * 128;
 #pragma unroll
       for (int g = 0; g < 32 / BR; ++g) {
         if (lane == 0) bulk_wait_read<0>();
@@ -364,14 +362,16 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             float2 v[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] = unpair(acc[4 * j + i]);
-            st_shared_v4(at + ((j ^ swz) << 4), pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y), pack_bf16(v[2].x, v[2].y),
-                         pack_bf16(v[3].x, v[3].y));
+            st_shared_v4(at + (j >> 3) * (BR * 128) + (((j & 7) ^ (lane & 7)) << 4), pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                         pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0 && y0 + BR * g < y_end && col < p.N) {
-          tma_store_3d(&tmC, box, col, y0 + BR * g, SCHED == SCHED_KGROUP ? c.z : 0);
+        if (lane == 0 && y0 + BR * g < y_end) {
+#pragma unroll
+          for (int j = 0; j < WC / 64; ++j)
+            if (col + 64 * j < p.N) tma_store_3d(&tmC, box + j * BR * 128, col + 64 * j, y0 + BR * g, SCHED == SCHED_KGROUP ? c.z : 0);
           bulk_commit();
         }
       }
@@ -415,7 +415,7 @@ template <int SCHED, int BN, int BR, bool SPLIT = false>
 static cudaError_t launch_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const void* out, int groups, int out_rows, const Fp8Params& p,
                                 cudaStream_t stream, int tiles = 0) {
   CUtensorMap c;
-  if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups, BN / 4, BR)) return cudaErrorInvalidValue;
+  if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups, 64, BR)) return cudaErrorInvalidValue;
   constexpr int smem = f8_smem(BN, BR, SCHED == SCHED_KGROUP);
   const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, BR, SPLIT>>(smem);
   if (err != cudaSuccess) return err;
