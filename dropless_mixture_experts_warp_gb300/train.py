@@ -1,14 +1,16 @@
-"""A stack of MoE blocks trained end to end: norms, router, balance loss, MoE layer, merge, AdamW.
+"""A stack of MoE blocks trained end to end: norms, router, balance loss, MoE layer, merge, AdamW or Muon.
 
     x_0 = norm(h_0)                                    moe_norm_fwd
     y_i = MoE layer(x_i, logits = x_i W_r^T)           layer.forward; balance.forward on its routing
     h_{i+1} = h_i + gate_i norm(y_i);  x_{i+1} = norm(h_{i+1})          moe_merge_fwd, one pass
     loss = mean (x_L - target)^2 + sum of the blocks' balance and z-losses
 
-The gradient is the chain of the backward calls; the update is one optim.step over every weight.  The router's
+The gradient is the chain of the backward calls; the update is one optim.step over every weight, or with
+optimizer="muon" one muon.step over the expert and router matrices and one optim.step over the rest.  The router's
 projection (logits, its gradients) is a library GEMM in fp32, outside the layer as everywhere in this package.
 
     python -m dropless_mixture_experts_warp_gb300.train --steps 30 --bits 8
+    python -m dropless_mixture_experts_warp_gb300.train --steps 30 --optimizer muon --prec fp8-block
 """
 from __future__ import annotations
 
@@ -18,20 +20,22 @@ from typing import Optional
 
 import torch
 
-from . import balance, block, layer, optim
+from . import balance, block, layer, muon, optim
 
 
 class Stack:
     """L blocks of one shape for T tokens a step: weights, buffers and the calls of a step."""
 
     def __init__(self, T, d, f, E, k, blocks=2, score="softmax", stream="bf16", sequences=1, coef=1e-2, z_coef=1e-3,
-                 bits=32, seed=0, device="cuda"):
+                 bits=32, seed=0, device="cuda", prec="bf16", optimizer="adamw"):
+        if optimizer not in ("adamw", "muon"):
+            raise ValueError('optimizer: "adamw" or "muon"')
         self.T, self.L, self.coef, self.z_coef = T, blocks, coef, z_coef
         self.stream = torch.bfloat16 if stream == "bf16" else torch.float32
         g = torch.Generator(device=device)
         g.manual_seed(seed)
         rand = lambda *s, fan: torch.randn(*s, generator=g, device=device) / math.sqrt(fan)  # noqa: E731
-        dims = layer.dims_of(T, d, f, E, k, score=score)
+        dims = layer.dims_of(T, d, f, E, k, score=score, prec=prec)
         norm = block.dims_of(T, d, stream=stream, gate="channel")
         # norms[i] belongs to x_i: one before each block, one after the last
         self.norms = [torch.ones(d, device=device) for _ in range(blocks + 1)]
@@ -46,19 +50,30 @@ class Stack:
         self.d_router = [torch.empty(E, d, device=device) for _ in range(blocks)]
         self.logits = [None] * blocks
         weights, grads, copies, decay = [], [], [], []
+        matrices = [], [], [], []                  # the same for Muon
 
         def add(w, grad, copy=None, wd=0.0):
             weights.append(w), grads.append(grad), copies.append(copy), decay.append(wd)
 
+        def add_matrix(w, grad, copy=None, wd=0.0):
+            if optimizer == "adamw":
+                return add(w, grad, copy, wd)
+            for to, x in zip(matrices, (w, grad, copy, wd)):
+                to.append(x)
+
+        halves = lambda x: x.view(2 * E, f, d)  # gate and up are matrices of their own  # noqa: E731
         for i, b in enumerate(self.blocks):
-            add(b["gu"], self.bufs[i].dw_gu, self.low[i]["gu"], 0.1)
-            add(b["down"], self.bufs[i].dw_d, self.low[i]["down"], 0.1)
-            add(b["router"], self.d_router[i], wd=0.1)
+            add_matrix(halves(b["gu"]), halves(self.bufs[i].dw_gu), halves(self.low[i]["gu"]), 0.1)
+            add_matrix(b["down"], self.bufs[i].dw_d, self.low[i]["down"], 0.1)
+            add_matrix(b["router"], self.d_router[i], wd=0.1)
             add(b["post"], self.merges[i].dw_post)
             add(b["gate"], self.merges[i].dgate)
             add(self.norms[i], self.pre.dw if i == 0 else self.merges[i - 1].dw)
         add(self.norms[-1], self.merges[-1].dw)
         self.plan = optim.plan(weights, grads, copies=copies, bits=bits, weight_decay=decay)
+        self.matrices = None
+        if optimizer == "muon":
+            self.matrices = muon.plan(matrices[0], matrices[1], copies=matrices[2], weight_decay=matrices[3])
 
     def forward(self, h, seq_offsets: Optional[torch.Tensor] = None, mask: Optional[torch.Tensor] = None):
         """The stream h [T, d] -> x_L [T, d] bf16; the blocks' losses are in self.balances[i].losses."""
@@ -81,16 +96,18 @@ class Stack:
             b, m, bufs = self.blocks[i], self.merges[i], self.bufs[i]
             dh = block.merge_backward(m, dh, dx, m.h_out, bufs.y, w_post=b["post"], gate=b["gate"],
                                       w_next=self.norms[i + 1])
-            dxe = layer.backward(bufs, m.dy, self.logits[i], self.low[i]["gu"], self.low[i]["down"])
+            x = self.pre.x if i == 0 else self.merges[i - 1].x
+            dxe = layer.backward(bufs, m.dy, self.logits[i], self.low[i]["gu"], self.low[i]["down"], x=x)
             dl = balance.backward(self.balances[i], self.logits[i], bufs.d_logits, seq_offsets=self.seqs, mask=self.mask,
                                   coef=self.coef, z_coef=self.z_coef)
-            x = self.pre.x if i == 0 else self.merges[i - 1].x
             torch.mm(dl.t(), x.float(), out=self.d_router[i])
             dx = (dxe.float() + dl @ b["router"]).bfloat16()
         return block.norm_backward(self.pre, dx, self.h0, self.norms[0], dh_add=dh)
 
     def update(self, step, lr):
         optim.step(self.plan, lr=lr, step=step, seed=step)
+        if self.matrices is not None:
+            muon.step(self.matrices, lr=lr)
 
     def check(self):
         """Raise on an error found on the device."""
@@ -98,6 +115,8 @@ class Stack:
             layer.check(b)
         for b in self.balances:
             balance.check(b)
+        if self.matrices is not None:
+            muon.check(self.matrices)
 
 
 def main():
@@ -105,9 +124,11 @@ def main():
     ap.add_argument("--steps", type=int, default=30)
     ap.add_argument("--bits", type=int, choices=(32, 8), default=32, help="of the optimiser's states")
     ap.add_argument("--score", choices=("softmax", "sigmoid"), default="softmax")
+    ap.add_argument("--optimizer", choices=("adamw", "muon"), default="adamw", help="of the matrices")
+    ap.add_argument("--prec", choices=("bf16", "mxfp8", "mxfp8-w4", "fp8-block"), default="bf16", help="of the experts' products")
     a = ap.parse_args()
     T, d, f, E, k = 2048, 512, 256, 16, 2
-    model = Stack(T, d, f, E, k, score=a.score, sequences=4, bits=a.bits)
+    model = Stack(T, d, f, E, k, score=a.score, sequences=4, bits=a.bits, prec=a.prec, optimizer=a.optimizer)
     g = torch.Generator(device="cuda")
     g.manual_seed(1)
     h = torch.randn(T, d, generator=g, device="cuda").bfloat16()
