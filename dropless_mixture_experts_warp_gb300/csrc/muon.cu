@@ -613,17 +613,39 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   const long long base = ns_base(p, ti, e);
   float* m = p.m[ti];
   float sq[1] = {0.0f};
-  for (int i = tid; i < n && !skip; i += 256) {
-    const int r = i / p.cols, c = i - r * p.cols;
-    float u = gs * (p.grad_type == MOE_TYPE_BF16 ? bf16_lo(static_cast<const uint16_t*>(p.grad[ti])[base + i])
-                                                 : static_cast<const float*>(p.grad[ti])[base + i]);
-    if (m) {
-      const float v = fmaf(p.momentum, m[base + i], u);
-      m[base + i] = v;
-      u = p.nesterov ? fmaf(p.momentum, v, u) : v;
+  constexpr int WAYS = 8;                            // elements of a thread on their way together
+  for (int i0 = tid; i0 < n && !skip; i0 += 256 * WAYS) {
+    float g[WAYS], v[WAYS];
+    if (p.grad_type == MOE_TYPE_BF16) {
+      const uint16_t* from = static_cast<const uint16_t*>(p.grad[ti]) + base;
+      uint16_t b[WAYS];
+#pragma unroll
+      for (int j = 0; j < WAYS; ++j) b[j] = from[min(i0 + 256 * j, n - 1)];
+#pragma unroll
+      for (int j = 0; j < WAYS; ++j) g[j] = bf16_lo(b[j]);
+    } else {
+      const float* from = static_cast<const float*>(p.grad[ti]) + base;
+#pragma unroll
+      for (int j = 0; j < WAYS; ++j) g[j] = from[min(i0 + 256 * j, n - 1)];
     }
-    sq[0] = fmaf(u, u, sq[0]);
-    stage[(tall ? c : r) * (L + 1) + (tall ? r : c)] = u;
+    if (m) {
+#pragma unroll
+      for (int j = 0; j < WAYS; ++j) v[j] = m[base + min(i0 + 256 * j, n - 1)];
+    }
+#pragma unroll
+    for (int j = 0; j < WAYS; ++j) {
+      const int i = i0 + 256 * j;
+      if (i >= n) break;
+      float u = gs * g[j];
+      if (m) {
+        const float w = fmaf(p.momentum, v[j], u);
+        m[base + i] = w;
+        u = p.nesterov ? fmaf(p.momentum, w, u) : w;
+      }
+      sq[0] = fmaf(u, u, sq[0]);
+      const int r = i / p.cols, c = i - r * p.cols;
+      stage[(tall ? c : r) * (L + 1) + (tall ? r : c)] = u;
+    }
   }
   row_sums<false>(sq, buf);
   __syncthreads();
@@ -636,6 +658,9 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
 
   const uint32_t sx = smem_u32(smem), sa = sx + (L / 64) * SM_BLOCK, sb = sa + 2 * SM_BLOCK;
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+  // steps of 16 that the matrix's own rows and columns reach; what lies past them is not multiplied, and what
+  // tensor memory and X's registers hold there is not used
+  const int ks = (min(p.rows, p.cols) + 15) / 16, kl = (max(p.rows, p.cols) + 15) / 16;
   uint32_t phase = 0;
   // products: the writers' shared memory is handed to the tensor core, one thread issues, all wait
   auto hand = [&]() {
@@ -654,11 +679,13 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   for (int k = 0; k < h.steps; ++k) {
     const NsStep q = h.s[k];
 #pragma unroll
-    for (int j = 0; j < HALF; j += 8) small_put(sx, row, col0 + j, x + j);
+    for (int j = 0; j < HALF; j += 8)
+      if (col0 + j < 16 * kl) small_put(sx, row, col0 + j, x + j);
     hand();
     if (tid == 0) {                                  // A = X X^T
 #pragma unroll
       for (int kk = 0; kk < L / 16; ++kk) {
+        if (kk >= kl) break;
         const uint64_t d = smem_desc_sw128(sx + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
         tc_mma_f16(tmem, d, d, idesc_fp16(128, 128, 0), kk != 0);
       }
@@ -669,6 +696,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
     const int ac = (warp >> 2) * 64;                 // A's and B's columns of a thread
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (ac + 32 * i >= 16 * ks) break;
       uint32_t r[32];
       tmem_ld32(tmem + lanes + ac + 32 * i, r);
       tmem_wait_ld();
@@ -682,6 +710,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
     if (tid == 0) {                                  // A A
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
+        if (kk >= ks) break;
         const uint64_t d = smem_desc_sw128(sa + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
         tc_mma_f16(tmem + 128, d, d, idesc_fp16(128, 128, 0), kk != 0);
       }
@@ -691,6 +720,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
     take();
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
+      if (ac + 32 * i >= 16 * ks) break;
       uint32_t r[32];
       tmem_ld32(tmem + lanes + 128 + ac + 32 * i, r);
       tmem_wait_ld();
@@ -712,15 +742,18 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
     hand();
     if (tid == 0) {                                  // B X
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk)
+      for (int kk = 0; kk < 8; ++kk) {
+        if (kk >= ks) break;
         tc_mma_f16(tmem + 256, smem_desc_sw128(sb + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024),
-                   smem_desc_sw128(sx + kk * 2048, SM_BLOCK, 1024), idesc_fp16(128, L, 1), kk != 0);
+                   smem_desc_sw128(sx + kk * 2048, SM_BLOCK, 1024), idesc_fp16(128, 16 * kl, 1), kk != 0);
+      }
       tc_commit(&bar);
     }
     __syncwarp();
     take();
 #pragma unroll
     for (int i = 0; i < HALF / 32; ++i) {
+      if (col0 + 32 * i >= 16 * kl) break;
       uint32_t r[32];
       tmem_ld32(tmem + lanes + 256 + col0 + 32 * i, r);
       tmem_wait_ld();
@@ -737,18 +770,26 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   if (warp == 0) tmem_dealloc(tmem, TMEM_COLS);
   if (skip) return;
   const float rate = p.control ? lr * p.control->lr_scale : lr;
-  for (int i = tid; i < n; i += 256) {
-    const int r = i / p.cols, c = i - r * p.cols;
-    const float v = stage[(tall ? c : r) * (L + 1) + (tall ? r : c)];
-    const long long at = base + i;
-    if (p.out[ti]) {
-      if (p.out_type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(p.out[ti])[at] = __float2bfloat16_rn(v);
-      else static_cast<float*>(p.out[ti])[at] = v;
-    } else {
-      const float w = p.w[ti][at];
-      const float nw = fmaf(-rate, fmaf(p.decay[ti], w, rms * v), w);
-      p.w[ti][at] = nw;
-      if (p.w16[ti]) reinterpret_cast<__nv_bfloat16*>(p.w16[ti])[at] = __float2bfloat16_rn(nw);
+  float* const weights = p.w[ti];
+  for (int i0 = tid; i0 < n; i0 += 256 * WAYS) {
+    float w[WAYS];
+#pragma unroll
+    for (int j = 0; j < WAYS; ++j) w[j] = weights ? weights[base + min(i0 + 256 * j, n - 1)] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < WAYS; ++j) {
+      const int i = i0 + 256 * j;
+      if (i >= n) break;
+      const int r = i / p.cols, c = i - r * p.cols;
+      const float v = stage[(tall ? c : r) * (L + 1) + (tall ? r : c)];
+      const long long at = base + i;
+      if (!weights) {
+        if (p.out_type == MOE_TYPE_BF16) static_cast<__nv_bfloat16*>(p.out[ti])[at] = __float2bfloat16_rn(v);
+        else static_cast<float*>(p.out[ti])[at] = v;
+      } else {
+        const float nw = fmaf(-rate, fmaf(p.decay[ti], w[j], rms * v), w[j]);
+        weights[at] = nw;
+        if (p.w16[ti]) reinterpret_cast<__nv_bfloat16*>(p.w16[ti])[at] = __float2bfloat16_rn(nw);
+      }
     }
   }
 }
