@@ -133,16 +133,15 @@ bool make_tensor_map_store(CUtensorMap* m, const void* base, uint64_t cols, uint
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_tensor_map_store3(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t groups, uint32_t box_cols,
-                            uint32_t box_rows) {
+bool make_tensor_map_store3(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t groups) {
   auto fn = encode_fn();
   if (!fn) return false;
   cuuint64_t dims[3] = {cols, rows, groups};
   cuuint64_t strides[2] = {cols * 2, rows * cols * 2};
-  cuuint32_t box[3] = {box_cols, box_rows, 1};
+  cuuint32_t box[3] = {64, 32, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

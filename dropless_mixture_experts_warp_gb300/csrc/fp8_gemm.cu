@@ -31,19 +31,19 @@ constexpr int F8_EPI_WARP0 = 4;
 constexpr int F8_THREADS = 32 * (F8_EPI_WARP0 + F8_EPI_WARPS);
 constexpr int F8_REGS_FEW = 64, F8_REGS_MANY = 216;
 static_assert(128 * F8_REGS_FEW + 256 * F8_REGS_MANY <= 384 * 168, "registers of the block at launch");
-// Operand stages: as many as shared memory holds beside the output's boxes.  A warp stages its
-// 32 rows at once (BR = 32), or 8 at a time (BR = 8), where a fourth stage is worth more.
-__host__ __device__ constexpr int f8_stages(int bn, int br) { return bn == 256 ? (br == 32 ? 3 : 4) : 5; }
+// Operand stages: as many as shared memory holds beside boxes for a whole tile of the output (with boxes of a
+// quarter and a fourth stage, a tile's store took 3700 cycles instead of 1300).
+__host__ __device__ constexpr int f8_stages(int bn) { return bn == 256 ? 3 : 5; }
 __host__ __device__ constexpr int f8_stage_bytes(int bn) { return F8_A_BYTES + bn * F8_K; }
-__host__ __device__ constexpr int f8_box_bytes(int bn, int br) { return br * bn / 2 * 2; }
+__host__ __device__ constexpr int f8_box_bytes(int bn) { return 32 * bn / 2 * 2; }
 // Scales of a block: the tile's 128 rows, then its columns (SCHED_KGROUP) or the columns' blocks.  The
 // loader is at most the operand stages ahead of the MMAs, these two blocks ahead of the sums, so
 // that with three slots more than stages it never writes one that is still read.
-__host__ __device__ constexpr int f8_slots(int bn, int br) { return f8_stages(bn, br) + 3; }
+__host__ __device__ constexpr int f8_slots(int bn) { return f8_stages(bn) + 3; }
 __host__ __device__ constexpr int f8_slot_floats(int bn, bool col_scales) { return BM + (col_scales ? bn : 4); }
-__host__ __device__ constexpr int f8_smem(int bn, int br, bool col_scales) {
-  return f8_stages(bn, br) * f8_stage_bytes(bn) + F8_EPI_WARPS * f8_box_bytes(bn, br) +
-         f8_slots(bn, br) * f8_slot_floats(bn, col_scales) * 4 + 1024;
+__host__ __device__ constexpr int f8_smem(int bn, bool col_scales) {
+  return f8_stages(bn) * f8_stage_bytes(bn) + F8_EPI_WARPS * f8_box_bytes(bn) +
+         f8_slots(bn) * f8_slot_floats(bn, col_scales) * 4 + 1024;
 }
 
 constexpr int F8_INFOS = 4;
@@ -95,11 +95,11 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, 
 }
 
 // SPLIT: one tile a cluster of CTAs, each a part of the contraction; their sums meet in shared memory.
-template <int SCHED, int BN, int BR, bool SPLIT>
+template <int SCHED, int BN, bool SPLIT>
 __global__ void __launch_bounds__(F8_THREADS, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                     const __grid_constant__ CUtensorMap tmC, const Fp8Params p) {
-  constexpr int STAGES = f8_stages(BN, BR), STAGE_BYTES = f8_stage_bytes(BN);
+  constexpr int STAGES = f8_stages(BN), STAGE_BYTES = f8_stage_bytes(BN);
   constexpr int WC = BN / 2;       // columns of an epilogue warp
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t full_bar[STAGES];
@@ -119,9 +119,9 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   const int lane = threadIdx.x & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~static_cast<uintptr_t>(1023));
-  constexpr int SLOTS = f8_slots(BN, BR), SLOT = f8_slot_floats(BN, SCHED == SCHED_KGROUP);
+  constexpr int SLOTS = f8_slots(BN), SLOT = f8_slot_floats(BN, SCHED == SCHED_KGROUP);
   uint8_t* s_box = smem + STAGES * STAGE_BYTES;
-  float* s_scales = reinterpret_cast<float*>(s_box + F8_EPI_WARPS * f8_box_bytes(BN, BR));
+  float* s_scales = reinterpret_cast<float*>(s_box + F8_EPI_WARPS * f8_box_bytes(BN));
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) { mbar_init(&full_bar[s], 1 + 32); mbar_init(&empty_bar[s], 1); }   // full: the tensor loads, the scale loader's lanes
@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
     // ------------------------------------------------------------ sums and stores
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(F8_REGS_MANY));
     const int q = warp & 3, part = (warp - F8_EPI_WARP0) >> 2;
-    uint8_t* box = s_box + (warp - F8_EPI_WARP0) * f8_box_bytes(BN, BR);
+    uint8_t* box = s_box + (warp - F8_EPI_WARP0) * f8_box_bytes(BN);
     const uint32_t lane_base = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + part * WC;
     int slot = 0, info = 0;
     uint32_t it = 0, info_phase = 0;
@@ -351,29 +351,24 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       // bf16 through the warp's boxes of 64 columns (16-byte pieces swizzled as the tensor store expects
       // them); boxes past the ends are skipped
       const int y0 = c.y + q * 32, y_end = SCHED == SCHED_ROWS ? c.z : p.M;
-      const uint32_t at = smem_u32(box) + (BR == 32 ? lane : lane & 7) * 128;
+      const uint32_t at = smem_u32(box) + lane * 128;
+      if (lane == 0) bulk_wait_read<0>();
+      __syncwarp();
 #pragma unroll
-      for (int g = 0; g < 32 / BR; ++g) {
-        if (lane == 0) bulk_wait_read<0>();
-        __syncwarp();
-        if (BR == 32 || (lane >> 3) == g) {
+      for (int j = 0; j < WC / 8; ++j) {
+        float2 v[4];
 #pragma unroll
-          for (int j = 0; j < WC / 8; ++j) {
-            float2 v[4];
+        for (int i = 0; i < 4; ++i) v[i] = unpair(acc[4 * j + i]);
+        st_shared_v4(at + (j >> 3) * 4096 + (((j & 7) ^ (lane & 7)) << 4), pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
+                     pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && y0 < y_end) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = unpair(acc[4 * j + i]);
-            st_shared_v4(at + (j >> 3) * (BR * 128) + (((j & 7) ^ (lane & 7)) << 4), pack_bf16(v[0].x, v[0].y), pack_bf16(v[1].x, v[1].y),
-                         pack_bf16(v[2].x, v[2].y), pack_bf16(v[3].x, v[3].y));
-          }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && y0 + BR * g < y_end) {
-#pragma unroll
-          for (int j = 0; j < WC / 64; ++j)
-            if (col + 64 * j < p.N) tma_store_3d(&tmC, box + j * BR * 128, col + 64 * j, y0 + BR * g, SCHED == SCHED_KGROUP ? c.z : 0);
-          bulk_commit();
-        }
+        for (int j = 0; j < WC / 64; ++j)
+          if (col + 64 * j < p.N) tma_store_3d(&tmC, box + j * 4096, col + 64 * j, y0, SCHED == SCHED_KGROUP ? c.z : 0);
+        bulk_commit();
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -411,15 +406,15 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
   if (warp == 1) tmem_dealloc(tmem_base, TMEM_COLS);
 }
 
-template <int SCHED, int BN, int BR, bool SPLIT = false>
+template <int SCHED, int BN, bool SPLIT = false>
 static cudaError_t launch_fp8_t(const CUtensorMap& a, const CUtensorMap& b, const void* out, int groups, int out_rows, const Fp8Params& p,
                                 cudaStream_t stream, int tiles = 0) {
   CUtensorMap c;
-  if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups, 64, BR)) return cudaErrorInvalidValue;
-  constexpr int smem = f8_smem(BN, BR, SCHED == SCHED_KGROUP);
-  const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, BR, SPLIT>>(smem);
+  if (!make_tensor_map_store3(&c, out, p.N, out_rows, groups)) return cudaErrorInvalidValue;
+  constexpr int smem = f8_smem(BN, SCHED == SCHED_KGROUP);
+  const cudaError_t err = allow_smem<fp8_gemm_kernel<SCHED, BN, SPLIT>>(smem);
   if (err != cudaSuccess) return err;
-  return launch_early_clusters(fp8_gemm_kernel<SCHED, BN, BR, SPLIT>, dim3(SPLIT ? tiles * p.split : num_sms()), dim3(F8_THREADS), smem, stream,
+  return launch_early_clusters(fp8_gemm_kernel<SCHED, BN, SPLIT>, dim3(SPLIT ? tiles * p.split : num_sms()), dim3(F8_THREADS), smem, stream,
                       SPLIT ? p.split : 0, a, b, c, p);
 }
 
@@ -440,9 +435,11 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
   if (!f8_aligned(a) || !f8_aligned(b) || !f8_aligned(out)) return MOE_ERR_ALIGNMENT;
   if (rows == 0) return MOE_OK;
   const int64_t tiles = up128(rows) / 128;
-  // BN = 128 where the rows make too few 256-wide tiles to fill the SMs evenly
+  // 256 columns a tile; 128 where those are too few to fill the SMs, and where experts have about a tile of rows or
+  // less: reading the weights bounds those, and tiles of half the width spread over the SMs more evenly (4 tokens
+  // through a layer of 256 experts: 268 us with 256, 249 with 128).
   const int64_t wide = tiles * ((N + 255) / 256);
-  const int bn = (N <= 128 || wide < num_sms()) ? 128 : 256;
+  const int bn = N <= 128 || wide < num_sms() || rows <= 256ll * E ? 128 : 256;
   CUtensorMap ta, tb;
   if (!make_tensor_map_u8(&ta, a, K, rows, F8_K, BM) ||
       !make_tensor_map_u8(&tb, b, K, static_cast<uint64_t>(E) * N, F8_K, F8_B_BOX))
@@ -464,11 +461,9 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
     p.split = 1;
     while (p.split < 8 && few * p.split * 2 <= num_sms() && kb >= 8ll * p.split) p.split *= 2;
     p.out = out;
-    if (p.split > 1) return status_of(launch_fp8_t<SCHED_ROWS, 128, 32, true>(ta, tb, out, 1, R, p, s, static_cast<int>(few)));
+    if (p.split > 1) return status_of(launch_fp8_t<SCHED_ROWS, 128, true>(ta, tb, out, 1, R, p, s, static_cast<int>(few)));
   }
-  const cudaError_t e = bn == 128    ? launch_fp8_t<SCHED_ROWS, 128, 32>(ta, tb, out, 1, R, p, s)
-                        : rows <= 256ll * E ? launch_fp8_t<SCHED_ROWS, 256, 8>(ta, tb, out, 1, R, p, s)
-                                    : launch_fp8_t<SCHED_ROWS, 256, 32>(ta, tb, out, 1, R, p, s);
+  const cudaError_t e = bn == 128 ? launch_fp8_t<SCHED_ROWS, 128>(ta, tb, out, 1, R, p, s) : launch_fp8_t<SCHED_ROWS, 256>(ta, tb, out, 1, R, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
@@ -491,8 +486,8 @@ moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint
   p.sa = dy_scales; p.sa_ld = N; p.sb = x_scales; p.sb_k = K;
   p.g.BN = bn; p.g.M = static_cast<int>(up128(N)); p.g.N = K; p.g.m_fastest = N <= K ? 1 : 0;
   p.status = dev_status;
-  const cudaError_t e = bn == 256 ? launch_fp8_t<SCHED_KGROUP, 256, 32>(ta, tb, out, E, N, p, s)
-                                  : launch_fp8_t<SCHED_KGROUP, 128, 32>(ta, tb, out, E, N, p, s);
+  const cudaError_t e = bn == 256 ? launch_fp8_t<SCHED_KGROUP, 256>(ta, tb, out, E, N, p, s)
+                                  : launch_fp8_t<SCHED_KGROUP, 128>(ta, tb, out, E, N, p, s);
   return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 

@@ -132,9 +132,8 @@ RouteScratch route_scratch(const moe_dims& d, void* ws);
 float* workspace_dw_part(const moe_dims& d, void* ws);
 bool make_tensor_map_sf(CUtensorMap* m, const void* base, uint64_t bytes, uint32_t box_rows = 2);
 bool make_tensor_map_store(CUtensorMap* m, const void* base, uint64_t cols, uint64_t ld, uint64_t rows);
-// The same for [groups][rows][cols]: boxes of 32 columns (64-byte swizzle) or 64 (128-byte), clipped at each group's rows.
-bool make_tensor_map_store3(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t groups, uint32_t box_cols,
-                            uint32_t box_rows);
+// The same for [groups][rows][cols]: boxes of 32 rows and 64 columns (128-byte swizzle), clipped at each group's rows.
+bool make_tensor_map_store3(CUtensorMap* m, const void* base, uint64_t cols, uint64_t rows, uint64_t groups);
 bool make_tensor_map_bf16(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
                           uint32_t box_inner, uint32_t box_outer);
 bool make_tensor_map_u8(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
