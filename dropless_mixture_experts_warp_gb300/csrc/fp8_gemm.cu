@@ -78,6 +78,21 @@ __device__ __forceinline__ void tmem_wait_ld32(uint32_t (&r)[32]) {
                  "+r"(r[28]), "+r"(r[29])::"memory");
   asm volatile("" : "+r"(r[30]), "+r"(r[31])::"memory");
 }
+// 16 lanes x 32 columns, spread as an MMA's result: registers 4 g and the next are columns 8 g + 2 (lane % 4) and
+// the next of row lane / 4, registers 4 g + 2 and the next those of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_rows4(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                 "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
 // acc += (x, y) * s, kept in its place among the loads: moved past the next ones, the registers that they
 // hold would not fit beside the sums.
 __device__ __forceinline__ void add_scaled(f32x2& acc, uint32_t x, uint32_t y, f32x2 s) {
@@ -307,36 +322,55 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
         tc_fence_after();
         const float* sc = s_scales + slot * SLOT;
         if (++slot == SLOTS) slot = 0;
-        float s = sc[q * 32 + lane];
-        if (SCHED == SCHED_ROWS) s *= sc[BM + (part * WC) / 128];
-        const f32x2 s2 = pair(s, s);
-        const ulonglong2* cs = reinterpret_cast<const ulonglong2*>(sc + BM + part * WC);
-        // 64 columns at a time (32 where they have scales of their own); the last are out of tensor memory
-        // before they are added
-        constexpr int CH = SCHED == SCHED_ROWS ? 64 : 32;
+        if constexpr (SCHED == SCHED_ROWS) {
+          // a thread has a row: 64 columns at a time, the last out of tensor memory before they are added
+          const float s = sc[q * 32 + lane] * sc[BM + (part * WC) / 128];
+          const f32x2 s2 = pair(s, s);
 #pragma unroll
-        for (int i = 0; i < WC / CH; ++i) {
-          uint32_t r[CH / 32][32];
-#pragma unroll
-          for (int k = 0; k < CH / 32; ++k) tmem_ld32(lane_base + buf * 256 + CH * i + 32 * k, r[k]);
-#pragma unroll
-          for (int k = 0; k < CH / 32; ++k) tmem_wait_ld32(r[k]);
-          if (i == WC / CH - 1) {
-            tc_fence_before();
-            __syncwarp();
-            pipe_arrive(&tempty_bar[buf], leader);
-          }
-#pragma unroll
-          for (int j = 0; j < CH / 4; ++j) {
-            f32x2 a = s2, b = s2;
-            if (SCHED == SCHED_KGROUP) {
-              const ulonglong2 v = cs[CH / 4 * i + j];
-              a = mul2(s2, v.x);
-              b = mul2(s2, v.y);
+          for (int i = 0; i < WC / 64; ++i) {
+            uint32_t r[2][32];
+            tmem_ld32(lane_base + buf * 256 + 64 * i, r[0]);
+            tmem_ld32(lane_base + buf * 256 + 64 * i + 32, r[1]);
+            tmem_wait_ld32(r[0]);
+            tmem_wait_ld32(r[1]);
+            if (i == WC / 64 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              pipe_arrive(&tempty_bar[buf], leader);
             }
-            const uint32_t* w = &r[j >> 3][4 * (j & 7)];
-            add_scaled(acc[CH / 2 * i + 2 * j], w[0], w[1], a);
-            add_scaled(acc[CH / 2 * i + 2 * j + 1], w[2], w[3], b);
+#pragma unroll
+            for (int j = 0; j < 32; ++j) add_scaled(acc[32 * i + j], r[j >> 4][2 * (j & 15)], r[j >> 4][2 * (j & 15) + 1], s2);
+          }
+        } else {
+          // a thread has columns 2 (lane % 4) and the next of every eight, in rows lane / 4 + 0, 8, 16, 24: a
+          // column's scale serves four rows.  With a row a thread it served one, and the scales' way from shared
+          // memory to the registers bound (1600 cycles a block).
+          f32x2 rs[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float v = sc[q * 32 + 8 * i + (lane >> 2)];
+            rs[i] = pair(v, v);
+          }
+          const f32x2* cs = reinterpret_cast<const f32x2*>(sc + BM + part * WC + 2 * (lane & 3));
+#pragma unroll
+          for (int i = 0; i < WC / 32; ++i) {
+            uint32_t r[2][16];
+            tmem_ld_rows4(lane_base + buf * 256 + 32 * i, r[0]);
+            tmem_ld_rows4(lane_base + (16u << 16) + buf * 256 + 32 * i, r[1]);
+            tmem_wait_ld16(r[0]);
+            tmem_wait_ld16(r[1]);
+            if (i == WC / 32 - 1) {
+              tc_fence_before();
+              __syncwarp();
+              pipe_arrive(&tempty_bar[buf], leader);
+            }
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+              const f32x2 c2 = cs[4 * (4 * i + g)];
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                add_scaled(acc[4 * (4 * i + g) + k], r[k >> 1][4 * g + 2 * (k & 1)], r[k >> 1][4 * g + 2 * (k & 1) + 1], mul2(rs[k], c2));
+            }
           }
         }
       }
@@ -354,6 +388,19 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
       const uint32_t at = smem_u32(box) + lane * 128;
       if (lane == 0) bulk_wait_read<0>();
       __syncwarp();
+      if constexpr (SCHED == SCHED_KGROUP) {
+#pragma unroll
+        for (int g = 0; g < WC / 8; ++g) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int row = 8 * k + (lane >> 2);
+            const float2 v = unpair(acc[4 * g + k]);
+            asm volatile("st.shared.b32 [%0], %1;" ::"r"(smem_u32(box) + (g >> 3) * 4096 + row * 128 + (((g & 7) ^ (row & 7)) << 4) + 4 * (lane & 3)),
+                         "r"(pack_bf16(v.x, v.y))
+                         : "memory");
+          }
+        }
+      } else
 #pragma unroll
       for (int j = 0; j < WC / 8; ++j) {
         float2 v[4];
