@@ -93,6 +93,11 @@ __device__ __forceinline__ void tmem_wait_ld16(uint32_t (&r)[16]) {
                : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
                  "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
+__device__ __forceinline__ f32x2 ld_shared_pair(uint32_t addr) {
+  f32x2 v;
+  asm volatile("ld.shared.b64 %0, [%1];" : "=l"(v) : "r"(addr));
+  return v;
+}
 // acc += (x, y) * s, kept in its place among the loads: moved past the next ones, the registers that they
 // hold would not fit beside the sums.
 __device__ __forceinline__ void add_scaled(f32x2& acc, uint32_t x, uint32_t y, f32x2 s) {
@@ -351,7 +356,11 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             const float v = sc[q * 32 + 8 * i + (lane >> 2)];
             rs[i] = pair(v, v);
           }
-          const f32x2* cs = reinterpret_cast<const f32x2*>(sc + BM + part * WC + 2 * (lane & 3));
+          // scales of the next 32 columns are read ahead: each read where it is used, their latencies add up
+          const uint32_t cs = smem_u32(sc + BM + part * WC + 2 * (lane & 3));
+          f32x2 c2[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) c2[g] = ld_shared_pair(cs + 32 * g);
 #pragma unroll
           for (int i = 0; i < WC / 32; ++i) {
             uint32_t r[2][16];
@@ -366,10 +375,13 @@ __global__ void __launch_bounds__(F8_THREADS, 1)
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-              const f32x2 c2 = cs[4 * (4 * i + g)];
+              f32x2 s4[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) s4[k] = mul2(rs[k], c2[g]);
+              if (i + 1 < WC / 32) c2[g] = ld_shared_pair(cs + 32 * (4 * (i + 1) + g));
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                add_scaled(acc[4 * (4 * i + g) + k], r[k >> 1][4 * g + 2 * (k & 1)], r[k >> 1][4 * g + 2 * (k & 1) + 1], mul2(rs[k], c2));
+                add_scaled(acc[4 * (4 * i + g) + k], r[k >> 1][4 * g + 2 * (k & 1)], r[k >> 1][4 * g + 2 * (k & 1) + 1], s4[k]);
             }
           }
         }
