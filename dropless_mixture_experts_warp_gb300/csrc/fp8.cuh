@@ -35,10 +35,10 @@ __device__ __forceinline__ f32x2 bf16_pair(uint32_t w) { return pair(bf16_lo(w),
 // Per half, the larger magnitude (a NaN gives way to a number: its code is NaN by itself).
 __device__ __forceinline__ uint32_t absmax_bf16x2(uint32_t a, uint32_t b) {
   uint32_t r;
-  asm("{\n\t.reg .b32 x;\n\tabs.bf16x2 x, %2;\n\tmax.bf16x2 %0, %1, x;\n\t}" : "=r"(r) : "r"(a), "r"(b));
+  asm("max.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));   // the signs' product comes along
   return r;
 }
-__device__ __forceinline__ float max_halves(uint32_t w) { return fmaxf(bf16_lo(w), bf16_hi(w)); }
+__device__ __forceinline__ float max_halves(uint32_t w) { return fmaxf(fabsf(bf16_lo(w)), fabsf(bf16_hi(w))); }
 
 inline bool f8_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 inline long long up128(long long x) { return (x + 127) / 128 * 128; }

@@ -91,7 +91,7 @@ __global__ void __launch_bounds__(256) f8_scatter_kernel(const uint16_t* x, int 
 constexpr int QT_IN_LD = 128 + 8;     // padded bf16 input rows
 constexpr int QT_LD = 128 + 16;       // padded code rows (bytes)
 constexpr int QT_IN_BYTES = 128 * QT_IN_LD * 2;
-constexpr int QT_SMEM = 2 * QT_IN_BYTES + 2 * 128 * QT_LD + (4 * 128 + 2 * 128 + 8) * 4;
+constexpr int QT_SMEM = QT_IN_BYTES + 2 * 128 * QT_LD + (4 * 128 + 2 * 128 + 8) * 4;
 
 // What a tile kernel writes.  Rows: codes [batch][R][C] and scales; columns: codes_t
 // [batch][C][R_t] (R_t >= R: rows from R on are zeros) and scales_t.  Either may be NULL.
@@ -106,14 +106,14 @@ struct F8Tiles {
   float* scales_t;             // [ceil(R / 128)][C]; SQUARE: not used
 };
 
-// 128 x 128 tiles, persistent blocks with the next tile's rows on their way (cp.async) while
-// one is quantised.  A thread holds 32 rows of two columns and 64 columns of one row in
-// registers, as they were loaded from shared memory for the maxima; codes are assembled in
-// shared memory and leave as whole lines.  SQUARE: one scale a tile.
+// 128 x 128 tiles, three persistent blocks an SM; a tile's rows are asked for (cp.async) as soon as the codes of the
+// one before have left its buffer.  A thread takes 32 rows of two columns and 64 columns of one row,
+// first for the maxima, then for the codes, which are assembled in shared memory and leave as whole lines.  Bound by
+// instruction issue (16384 x 7168, both forms: 94 us, 60 % of the issue slots, 5.06 TB/s).  SQUARE: one scale a tile.
 template <bool SQUARE>
-__global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
+__global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
   extern __shared__ __align__(16) uint8_t sm[];
-  uint8_t* ct = sm + 2 * QT_IN_BYTES;              // column codes [128 columns][QT_LD]
+  uint8_t* ct = sm + QT_IN_BYTES;              // column codes [128 columns][QT_LD]
   uint8_t* rt = ct + 128 * QT_LD;                  // row codes [128 rows][QT_LD]
   float* cmax = reinterpret_cast<float*>(rt + 128 * QT_LD);   // [4][128]
   float* rmax = cmax + 4 * 128;                    // [2][128]
@@ -156,38 +156,30 @@ __global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
   rows_of(t, next);
   fetch(t, 0, next);
   rows_of(t + gridDim.x, next);
-  for (int it = 0; t < total; ++it, t += gridDim.x) {
-    fetch(t + gridDim.x, (it & 1) ^ 1, next);
-    rows_of(t + 2 * gridDim.x, next);
-    copy_wait<1>();
+  for (; t < total; t += gridDim.x) {
+    copy_wait<0>();
     __syncthreads();
-    const uint16_t(*tile)[QT_IN_LD] = reinterpret_cast<const uint16_t(*)[QT_IN_LD]>(sm + (it & 1) * QT_IN_BYTES);
+    const uint16_t(*tile)[QT_IN_LD] = reinterpret_cast<const uint16_t(*)[QT_IN_LD]>(sm);
     const unsigned qq = t / ctiles;
     const int c0 = static_cast<int>(t - qq * ctiles) * 128, r0 = static_cast<int>(qq % rtiles) * 128;
     const long long b = qq / rtiles;
     // columns 2 cp and 2 cp + 1, rows 32 g to 32 g + 31; row rr, columns 64 hh to 64 hh + 63
     const int cp = tid & 63, g = tid >> 6, rr = tid & 127, hh = tid >> 7;
-    uint32_t cw[32], rw[32];
     uint32_t m = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      cw[i] = *reinterpret_cast<const uint32_t*>(&tile[g * 32 + i][2 * cp]);
-      m = absmax_bf16x2(m, cw[i]);
+      m = absmax_bf16x2(m, *reinterpret_cast<const uint32_t*>(&tile[g * 32 + i][2 * cp]));
     }
     float amax = max_halves(m);
     if (!SQUARE) {
-      cmax[g * 128 + 2 * cp] = bf16_lo(m);
-      cmax[g * 128 + 2 * cp + 1] = bf16_hi(m);
+      cmax[g * 128 + 2 * cp] = fabsf(bf16_lo(m));
+      cmax[g * 128 + 2 * cp + 1] = fabsf(bf16_hi(m));
     }
     m = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint4 u = *reinterpret_cast<const uint4*>(&tile[rr][hh * 64 + 8 * i]);
-      rw[4 * i] = u.x; rw[4 * i + 1] = u.y; rw[4 * i + 2] = u.z; rw[4 * i + 3] = u.w;
-      if (!SQUARE) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = absmax_bf16x2(m, rw[4 * i + j]);
-      }
+      if (!SQUARE) m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, u.x), u.y), u.z), u.w);
     }
     if (SQUARE) {
 #pragma unroll
@@ -197,27 +189,40 @@ __global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
       rmax[hh * 128 + rr] = max_halves(m);
     }
     __syncthreads();
-    float a0, a1, ar;
-    if (SQUARE) {
-      a0 = tmax[0];
+    {
+      // one column's (the first 128 threads) or row's scale a thread, - scale and 1 / scale over two of the maxima that
+      // only this thread reads
+      float top;
+      if (SQUARE) {
+        top = tmax[0];
 #pragma unroll
-      for (int i = 1; i < 8; ++i) a0 = fmaxf(a0, tmax[i]);
-      a1 = ar = a0;
-    } else {
-      const int c = 2 * cp;
-      a0 = fmaxf(fmaxf(cmax[c], cmax[128 + c]), fmaxf(cmax[256 + c], cmax[384 + c]));
-      a1 = fmaxf(fmaxf(cmax[c + 1], cmax[129 + c]), fmaxf(cmax[257 + c], cmax[385 + c]));
-      ar = fmaxf(rmax[rr], rmax[128 + rr]);
+        for (int i = 1; i < 8; ++i) top = fmaxf(top, tmax[i]);
+      } else if (tid < 128) {
+        top = fmaxf(fmaxf(cmax[tid], cmax[128 + tid]), fmaxf(cmax[256 + tid], cmax[384 + tid]));
+      } else {
+        top = fmaxf(rmax[tid - 128], rmax[tid]);
+      }
+      const F8Scale f = f8_scale(top);
+      float* ends = tid < 128 ? cmax + tid : rmax + tid - 128;
+      ends[0] = -f.s;
+      ends[128] = f.inv;
+      if (SQUARE) {
+        if (tid == 0) p.scales[(b * rtiles + (r0 >> 7)) * ctiles + (c0 >> 7)] = f.s;
+      } else if (tid < 128) {
+        if (p.codes_t && c0 + tid < p.C) p.scales_t[static_cast<long long>(r0 >> 7) * p.C + c0 + tid] = f.s;
+      } else {
+        if (p.codes && r0 + tid - 128 < p.R) p.scales[static_cast<long long>(c0 >> 7) * p.R + r0 + tid - 128] = f.s;
+      }
     }
+    __syncthreads();
     if (p.codes_t) {
-      const F8Scale f0 = f8_scale(a0), f1 = SQUARE ? f0 : f8_scale(a1);
-      const f32x2 ns = pair(-f0.s, -f1.s), inv = pair(f0.inv, f1.inv);
+      const f32x2 ns = *reinterpret_cast<const f32x2*>(cmax + 2 * cp), inv = *reinterpret_cast<const f32x2*>(cmax + 128 + 2 * cp);
       uint32_t k0[8], k1[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float2 x[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[j] = unpair(f8_quotient(bf16_pair(cw[4 * i + j]), ns, inv));
+        for (int j = 0; j < 4; ++j) x[j] = unpair(f8_quotient(bf16_pair(*reinterpret_cast<const uint32_t*>(&tile[g * 32 + 4 * i + j][2 * cp])), ns, inv));
         k0[i] = cvt_e4m3x4(x[0].x, x[1].x, x[2].x, x[3].x);
         k1[i] = cvt_e4m3x4(x[0].y, x[1].y, x[2].y, x[3].y);
       }
@@ -227,26 +232,24 @@ __global__ void __launch_bounds__(256, 2) f8_tiles_kernel(const F8Tiles p) {
         *reinterpret_cast<uint4*>(ct + cp * QT_LD + g * 32 + 16 * i) = make_uint4(k0[4 * i], k0[4 * i + 1], k0[4 * i + 2], k0[4 * i + 3]);
         *reinterpret_cast<uint4*>(ct + (64 + cp) * QT_LD + g * 32 + 16 * i) = make_uint4(k1[4 * i], k1[4 * i + 1], k1[4 * i + 2], k1[4 * i + 3]);
       }
-      if (!SQUARE && g == 0 && c0 + 2 * cp < p.C) {
-        float* st = p.scales_t + static_cast<long long>(r0 >> 7) * p.C + c0 + 2 * cp;
-        st[0] = f0.s;
-        st[1] = f1.s;
-      }
     }
     if (p.codes) {
-      const F8Scale f = f8_scale(ar);
-      const f32x2 ns = pair(-f.s, -f.s), inv = pair(f.inv, f.inv);
+      const f32x2 ns = pair(rmax[rr], rmax[rr]), inv = pair(rmax[128 + rr], rmax[128 + rr]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t k[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = f8_codes4(bf16_pair(rw[8 * i + 2 * j]), bf16_pair(rw[8 * i + 2 * j + 1]), ns, inv);
+        for (int j = 0; j < 2; ++j) {
+          const uint4 u = *reinterpret_cast<const uint4*>(&tile[rr][hh * 64 + 16 * i + 8 * j]);
+          k[2 * j] = f8_codes4(bf16_pair(u.x), bf16_pair(u.y), ns, inv);
+          k[2 * j + 1] = f8_codes4(bf16_pair(u.z), bf16_pair(u.w), ns, inv);
+        }
         *reinterpret_cast<uint4*>(rt + rr * QT_LD + hh * 64 + 16 * i) = make_uint4(k[0], k[1], k[2], k[3]);
       }
-      if (!SQUARE && hh == 0 && r0 + rr < p.R) p.scales[static_cast<long long>(c0 >> 7) * p.R + r0 + rr] = f.s;
     }
-    if (SQUARE && tid == 0) p.scales[(b * rtiles + (r0 >> 7)) * ctiles + (c0 >> 7)] = f8_scale(a0).s;
     __syncthreads();
+    fetch(t + gridDim.x, 0, next);
+    rows_of(t + 2 * gridDim.x, next);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int line = (tid + 256 * j) >> 3, at = (tid & 7) * 16;
@@ -269,7 +272,7 @@ static cudaError_t launch_f8_tiles(const F8Tiles& p, cudaStream_t s) {
   if (err != cudaSuccess) return err;
   const long long tiles = static_cast<long long>(p.batch) * ((p.R + 127) / 128) * ((p.C + 127) / 128);
   if (tiles >= (1ll << 31) - (1 << 20)) return cudaErrorInvalidValue;
-  const int grid = static_cast<int>(tiles < 2ll * num_sms() ? tiles : 2ll * num_sms());
+  const int grid = static_cast<int>(tiles < 3ll * num_sms() ? tiles : 3ll * num_sms());
   return launch_early(f8_tiles_kernel<SQUARE>, dim3(grid), dim3(256), QT_SMEM, s, p);
 }
 
