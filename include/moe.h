@@ -56,7 +56,7 @@ typedef enum moe_status {
   MOE_ERR_WORKSPACE = 4,   /* workspace NULL while needed */
   MOE_ERR_CUDA = 5,        /* a CUDA runtime/driver call failed */
   MOE_ERR_TIMEOUT = 6,     /* a bounded device wait gave up (written to dev_status) */
-  MOE_ERR_INVARIANT = 7,   /* sum(split_sizes) != T*k seen on the device */
+  MOE_ERR_INVARIANT = 7,   /* sum(split_sizes) != T*k, or offsets out of order, seen on the device */
   MOE_ERR_SCRATCH_LIMIT = 8 /* too large for moe_gemm_down_dgrad_noalloc's static scratch */
 } moe_status;
 
@@ -563,7 +563,8 @@ moe_status moe_fp8_quantize_weights(const moe_bf16* src, int32_t E, int32_t N, i
  *   [E][K][N], and the product is a times them (an input gradient).
  *   row_offsets [E + 1] int32, multiples of 128, ascending from 0: expert e multiplies rows
  *   [row_offsets[e], row_offsets[e + 1]); NULL (E = 1): all rows.  Rows outside are left as
- *   they were; offsets past `rows` count as the end.
+ *   they were; offsets past `rows` count as the end.  Offsets that are not so give dev_status
+ *   MOE_ERR_INVARIANT and count as no rows.
  */
 moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, int32_t K, const uint8_t* b,
                         const float* b_scales, int32_t b_transposed, int32_t N, int32_t E,

@@ -301,6 +301,23 @@ def test_swiglu_gradient(R, f, used, weighted):
         assert (h.codes_t[:, k:].contiguous().view(torch.uint8) == 0x11).all() and (h.scales_t[k // 128:] == 7.0).all()
 
 
+@pytest.mark.parametrize("offsets", [[0, 256, 128], [128, 256, 384], [0, 100, 256], [0, -128, 256], [-128, 0, 128]])
+def test_offsets_out_of_order(offsets):
+    from dropless_mixture_experts_warp_gb300 import binding as B, fp8
+    rng = np.random.default_rng(5)
+    o = torch.tensor(offsets, dtype=torch.int32).cuda()
+    a, x = (fp8.quantize(fp8.allocate_rows(384, C, both=True), activations(rng, 384, C).cuda()) for C in (144, 256))
+    w = fp8.weights_of(*map(cuda, weights(rng, 2, 272, 144)))
+    out, grad = torch.full((384, 272), 7.0, device="cuda").bfloat16(), torch.full((2, 144, 256), 7.0, device="cuda").bfloat16()
+    for call in (lambda: fp8.matmul(a, w, out, o), lambda: fp8.weight_grad(a, x, grad, o)):
+        call()
+        with pytest.raises(B.MoeError) as e:
+            fp8.check(a)
+        assert e.value.status == 7
+        a.status.zero_()
+    assert (out == 7.0).all() and (grad == 0.0).all()
+
+
 # ------------------------------------------------------------------------------------ the layer
 
 LAYERS = [dict(T=1, d=256, f=128, E=8, k=2, score="softmax"), dict(T=300, d=384, f=256, E=16, k=4, score="sigmoid"),
