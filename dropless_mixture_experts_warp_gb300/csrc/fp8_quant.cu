@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1) f8_swiglu_bwd_kernel(const F8Sw
               x[k] = what == 1 ? w[i] * dh * silu : w[i] * silu * uu;
               if (what == 2) sum += silu * uu * dh;
             }
+            if (w[i] == 0.0f) x[k] = 0.0f;           // as the forward, which does not read such a row
           }
           rmax = fmaxf(rmax, fmaxf(fabsf(x[0]), fabsf(x[1])));
           v[i][j] = pair(x[0], x[1]);

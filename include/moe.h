@@ -592,7 +592,8 @@ moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows,
  *   dA = w dH;  dG = dA U silu'(G);  dU = dA silu(G);  dw[r] = sum_j silu(G) U dH
  * dG | dU to the row form (dgu_codes [rows][2f]) and the column form (dgu_codes_t [2f][R_t]),
  * h itself to the column form (h_codes_t [f][R_t]: the codes that moe_fp8_swiglu would have
- * given columns).  dw_rows [rows] fp32 and its scratch dw_part [rows][f / 128], or both NULL.
+ * given columns).  A row of weight 0 gives zeros to all three whatever it holds; its dw is as
+ * above.  dw_rows [rows] fp32 and its scratch dw_part [rows][f / 128], or both NULL.
  */
 moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const float* w_rows, int64_t rows, int32_t f,
                               const int32_t* nrows_dev, uint8_t* dgu_codes, float* dgu_scales, uint8_t* dgu_codes_t,

@@ -318,6 +318,30 @@ def test_offsets_out_of_order(offsets):
     assert (out == 7.0).all() and (grad == 0.0).all()
 
 
+def test_swiglu_gradient_of_rows_that_weigh_nothing():
+    """A row of weight 0 is zeros in all forms, infinities and NaN in it included; columns keep the other rows' scales."""
+    from dropless_mixture_experts_warp_gb300 import binding as B, fp8
+    R, f = 130, 256
+    rng = np.random.default_rng(8)
+    gu, dh, w = bf16(rng, R, 2 * f), bf16(rng, R, f), torch.rand(R) + 0.5
+    none = [0, 77, 129]
+    w[none] = 0.0
+    got = []
+    for fill in (0.0, float("inf"), float("nan")):
+        g, d = gu.clone(), dh.clone()
+        g[none], d[none] = fill, fill
+        dgu, h = fp8.allocate_rows(R, 2 * f, both=True), fp8.allocate_rows(R, f, both=True)
+        dw, part = torch.empty(R, device="cuda"), torch.empty(R, f // 128, device="cuda")
+        B.moe_fp8_swiglu_bwd(g.cuda(), d.cuda(), w.cuda(), R, f, None, dgu.codes, dgu.scales, dgu.codes_t, dgu.scales_t, h.codes_t, h.scales_t,
+                             dw, part)
+        keep = [i for i in range(R) if i not in none]
+        got.append([t.cpu() for t in (dgu.codes.view(torch.uint8), dgu.scales, dgu.codes_t.view(torch.uint8), dgu.scales_t,
+                                      h.codes_t.view(torch.uint8), h.scales_t, dw[keep])])
+        assert (got[-1][0][none] == 0).all()
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
 # ------------------------------------------------------------------------------------ the layer
 
 LAYERS = [dict(T=1, d=256, f=128, E=8, k=2, score="softmax"), dict(T=300, d=384, f=256, E=16, k=4, score="sigmoid"),
