@@ -73,6 +73,7 @@ class Blocks:
     dgu: fp8.Rows = None       # [rows, 2f]
     dh: torch.Tensor = None    # [rows, f] bf16
     dw_part: torch.Tensor = None
+    given: bool = False        # the weights are the caller's: never written
 
 
 def dims_of(T, d, f, E, k, f_shared=0, score="softmax", prec="bf16") -> B.moe_dims:
@@ -147,24 +148,28 @@ def use_weights(b: Buffers, gu: fp8.Weights, down: fp8.Weights, gu_s: fp8.Weight
     if dm.f_shared:
         check(gu_s, 1, 2 * dm.f_shared, dm.d)
         check(down_s, 1, dm.d, dm.f_shared)
-        b.q_s.gu, b.q_s.down = gu_s, down_s
-    b.q.gu, b.q.down = gu, down
+        b.q_s.gu, b.q_s.down, b.q_s.given = gu_s, down_s, True
+    b.q.gu, b.q.down, b.q.given = gu, down, True
 
 
 def quantize_weights(b: Buffers, w_gu, w_d, stream=None, w_gu_s=None, w_d_s=None):
     """MXFP8: the 16-bit master weights -> b.wq (and b.wq_s for the shared expert), codes and
     scales in both contraction orientations.  The weights change once per optimiser step, so a
     step of several micro-batches quantises them once and passes weights_cached=True to every
-    forward() of the step.  fp8-block: to b.q's weights (and b.q_s's), allocated at the first call."""
+    forward() of the step.  fp8-block: to b.q's weights (and b.q_s's), allocated at the first call and in
+    place of those that use_weights() gave, which stay as they are."""
     dm = b.dims
     if dm.prec == FP8_BLOCK:
         for q, E, f, gu, down in ((b.q, dm.E, dm.f, w_gu, w_d), (b.q_s, 1, dm.f_shared, w_gu_s, w_d_s)):
             if q is None:
                 continue
-            if q.gu is None:
+            if gu is None or down is None:
+                raise ValueError("quantize_weights: no 16-bit weights (weights_cached=True after use_weights())")
+            if q.gu is None or q.given:
                 both, dev = q.dy is not None, b.y.device
                 q.gu = fp8.allocate_weights(E, 2 * f, dm.d, both=both, device=dev)
                 q.down = fp8.allocate_weights(E, dm.d, f, both=both, device=dev)
+                q.given = False
             fp8.quantize_weights(q.gu, gu.view(E, 2 * f, dm.d), stream)
             fp8.quantize_weights(q.down, down.view(E, dm.d, f), stream)
         return

@@ -456,3 +456,25 @@ def test_layer_serving_form():
     assert torch.equal(layer.forward(lean, x, logits, None, None, weights_cached=True), y)
     with pytest.raises(ValueError):
         layer.backward(lean, x, logits, None, None)
+
+
+def test_given_weights_are_not_written():
+    """quantize_weights() after use_weights() takes weights of its own."""
+    from dropless_mixture_experts_warp_gb300 import fp8, layer
+    rng = np.random.default_rng(10)
+    T, d, f, E, k = 9, 128, 128, 4, 2
+    x, logits = bf16(rng, T, d).cuda(), torch.from_numpy(rng.standard_normal((T, E)).astype(np.float32)).cuda()
+    first, second = ([bf16(rng, E, 2 * f, d, scale=0.06).cuda(), bf16(rng, E, d, f, scale=0.09).cuda()] for _ in range(2))
+    given = [fp8.quantize_weights(fp8.allocate_weights(*w.shape), w) for w in first]
+    kept = [(w.codes.clone().view(torch.uint8), w.scales.clone()) for w in given]
+    dims = layer.dims_of(T, d, f, E, k, prec="fp8-block")
+    b, other = layer.allocate(dims), layer.allocate(dims)
+    layer.use_weights(b, *given)
+    with pytest.raises(ValueError):
+        layer.forward(b, x, logits, None, None)
+    y = layer.forward(b, x, logits, *second)
+    assert torch.equal(y, layer.forward(other, x, logits, *second))
+    layer.backward(b, x, logits, *second)
+    layer.check(b)
+    for w, (codes, scales) in zip(given, kept):
+        assert torch.equal(w.codes.view(torch.uint8), codes) and torch.equal(w.scales, scales)
