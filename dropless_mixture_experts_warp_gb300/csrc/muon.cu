@@ -25,7 +25,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <vector>
 
 namespace moe {
 
@@ -940,9 +939,14 @@ moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* ten
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   if (!ptr_aligned16(workspace)) return MOE_ERR_ALIGNMENT;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  std::vector<char> done(static_cast<size_t>(std::max(count, 1)), 0);
+  const auto alike = [&](int i, int j) {
+    const moe_muon_tensor &f = tensors[i], &g = tensors[j];
+    return g.batch > 0 && g.rows == f.rows && g.cols == f.cols && g.grad_type == f.grad_type && g.out_type == f.out_type && !g.out == !f.out;
+  };
   for (int i = 0; i < count; ++i) {
-    if (done[i] || tensors[i].batch == 0) continue;
+    bool done = tensors[i].batch == 0;
+    for (int j = 0; j < i && !done; ++j) done = alike(i, j);
+    if (done) continue;
     // the tensors like this one, in order, in chunks that fit the workspace
     const moe_muon_tensor& f = tensors[i];
     const int fit = static_cast<int>(std::min<size_t>(workspace_bytes / ns_matrix_bytes(ns_shape(f.rows, f.cols)), 65535));
@@ -959,10 +963,7 @@ moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* ten
     };
     for (int j = i; j < count; ++j) {
       const moe_muon_tensor& g = tensors[j];
-      if (done[j] || g.batch == 0 || g.rows != f.rows || g.cols != f.cols || g.grad_type != f.grad_type || g.out_type != f.out_type ||
-          !g.out != !f.out)
-        continue;
-      done[j] = 1;
+      if (!alike(i, j)) continue;
       for (int at = 0; at < g.batch;) {
         if (batch == fit || t.count == NS_TENSORS) {
           if (flush() != cudaSuccess) return MOE_ERR_CUDA;

@@ -71,7 +71,8 @@ def _allocate(table, n, limit, device):
 
 def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COEFFICIENTS, workspace=WORKSPACE) -> Plan:
     """weights: fp32; grads: bf16 or fp32; copies: bf16 or None; weight_decay: one number or one a tensor.  The
-    momentum starts at zero, or is the one given (a resumed run's, fp32).  workspace: bytes of scratch at most."""
+    momentum starts at zero, or is the one given (a resumed run's, fp32).  workspace: bytes of scratch at most; a plan's
+    steps share it, so they follow one another, also as replays of captured graphs."""
     weights, grads = list(weights), list(grads)
     n = len(weights)
     copies = [None] * n if copies is None else list(copies)
@@ -84,6 +85,8 @@ def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COE
     device = weights[0].device if n else torch.device("cuda")
     if any(w.device != device for w in weights):
         raise ValueError("weights on more than one device")
+    if any(len({t.data_ptr() for t in x if t.numel()}) < sum(t.numel() > 0 for t in x) for x in (weights, m)):
+        raise ValueError("a tensor is in the list twice")
     table = (B.moe_muon_tensor * max(1, n))()
     for i, w in enumerate(weights):
         low = grads[i].dtype == torch.bfloat16

@@ -836,7 +836,7 @@ typedef struct moe_muon_hyper {
  * least one). */
 size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t limit);
 
-/* tensors: HOST array (read before the call returns); workspace of workspace_bytes, at least
+/* tensors: HOST array (read before the call returns), none overlapping another; workspace of workspace_bytes, at least
  * what one matrix needs; control as in moe_adamw_step (its `step` is not used). */
 moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
                          size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream);

@@ -153,6 +153,8 @@ def test_python_checks():
         muon.plan(g, g, copies=[g[0]])
     with pytest.raises(ValueError):
         muon.plan(g, g, m=[None])
+    with pytest.raises(ValueError):
+        muon.plan(g * 2, [torch.zeros(3, 4, 5) for _ in range(2)])          # a weight twice
     b = layer.allocate(layer.dims_of(4, 128, 128, 4, 2, prec="fp8-block"), device="cpu", train=False)
     with pytest.raises(ValueError):
         layer.use_weights(b, w, w)
