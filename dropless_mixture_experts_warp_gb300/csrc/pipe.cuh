@@ -86,13 +86,6 @@ __device__ __forceinline__ void pipe_load_2d_pair(void* dst, const void* tmap, u
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(mbar_cluster), "r"(x), "r"(y), "r"(act)
       : "memory");
 }
-__device__ __forceinline__ void pipe_bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint32_t act) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "@p cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n\t}" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar)), "r"(act)
-      : "memory");
-}
 __device__ __forceinline__ void pipe_commit(uint64_t* bar, uint32_t act) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t"
