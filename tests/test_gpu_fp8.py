@@ -201,6 +201,42 @@ def test_grouped_product(counts, N, K, transposed):
     assert (out[n:] == 7.0).all()
 
 
+@pytest.mark.parametrize("counts", [[5000], [1300, 0, 640, 1, 129, 3000, 257], [0, 0, 5000, 128, 0], [4000] + [100] * 9 + [1024]])
+@pytest.mark.parametrize("N,K,transposed", [(1040, 144, False), (1296, 400, False), (528, 1296, True)])
+def test_product_of_many_rows(counts, N, K, transposed):
+    """Tiles of 256 rows and columns: experts with odd numbers of 128 rows, ends inside a tile, none at all."""
+    from dropless_mixture_experts_warp_gb300 import fp8
+    rng = np.random.default_rng(sum(counts) + N)
+    off = segments(counts)
+    R, E = off[-1] + 130, len(counts)
+    codes, scales = rows(rng, R, N if transposed else K)
+    wc, ws = weights(rng, E, N, K)
+    w = fp8.weights_of(cuda(wc), cuda(ws), cuda(wc.transpose(1, 2).contiguous()) if transposed else None)
+    a = fp8.rows_of(cuda(codes), cuda(scales))
+    out = torch.full((R, K if transposed else N), 7.0, dtype=torch.bfloat16, device="cuda")
+    fp8.matmul(a, w, out, offsets=torch.tensor(off, dtype=torch.int32).cuda(), transposed=transposed)
+    fp8.check(a)
+    v = ob.weights_values(wc, ws)
+    ref, mag = ob.product(ob.rows_values(codes, scales), v.transpose(0, 2, 1) if transposed else v, off)
+    n = off[-1]
+    close(out[:n], ref[:n], mag[:n], N if transposed else K)
+    assert (out[n:] == 7.0).all()
+
+
+def test_product_of_many_rows_one_matrix():
+    from dropless_mixture_experts_warp_gb300 import fp8
+    rng = np.random.default_rng(4)
+    R, N, K = 4997, 1040, 272
+    codes, scales = rows(rng, R, K)
+    wc, ws = torch.from_numpy(rng.standard_normal((1, N, K)).astype(np.float32)).to(ob.E4M3), (0.5 + rng.random((1, 9, 3))).astype(np.float32)
+    a, w = fp8.rows_of(cuda(codes), cuda(scales)), fp8.weights_of(cuda(wc), cuda(ws))
+    out = torch.empty(R, N, dtype=torch.bfloat16, device="cuda")
+    fp8.matmul(a, w, out)
+    fp8.check(a)
+    ref, mag = ob.product(ob.rows_values(codes, scales), ob.weights_values(wc, ws), [0, R])
+    close(out, ref, mag, K)
+
+
 @pytest.mark.parametrize("counts", COUNTS + [[300]])
 @pytest.mark.parametrize("N,K", [(16, 16), (256, 384), (144, 272), (400, 1040)])
 def test_weight_grad(counts, N, K):
