@@ -17,7 +17,9 @@
 // part of A for its addend alone does not help: A's rounding in b A and in c A A partly cancels.)
 // A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
 //
-// Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.
+// Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.  48 matrices of 1536 x 4096, five
+// steps: 7.9 ms, of which the products 6.3 (64 % of the measured bf16 rate; operands from shared memory and the power
+// limit), the passes over momenta, weights and X 1.6.
 #include "around.cuh"
 #include "kernels.h"
 #include "pipe.cuh"
@@ -564,7 +566,7 @@ __global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const
 //
 // A matrix of at most 128 x 256 goes through the whole step in one block: X in fp32 registers (a thread has a
 // row, half of the columns), its fp16 form, A and B in shared memory, products in tensor memory.  Fifteen products of
-// one tile each are latency: 18 launches took 98 us for six matrices of 131 x 72.
+// one tile each are latency: 26 us for six matrices of 131 x 72, 98 with 18 launches.
 // X's fp16 form lies in blocks of 64 columns, 128 rows of 128 bytes each (128-byte swizzle), which the MMA reads
 // K-major in X X^T and MN-major in B X.
 
