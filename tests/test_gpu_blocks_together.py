@@ -193,3 +193,55 @@ def test_many_experts_and_wide_rows():
     v = ob.rows_values(cc, cs).T
     ref, mag = ob.weight_grad(v, v, off)
     assert np.all(np.abs(g.double().cpu().numpy() - ref) <= ob.BF16_HALF * np.abs(ref) + 4 * 400 * ob.U32 * mag + 1e-37)
+
+
+def test_two_streams_at_once():
+    """Two sets of buffers on two streams at once, called and as graphs, give what each gives alone."""
+    from dropless_mixture_experts_warp_gb300 import fp8, muon
+    g = torch.Generator("cuda").manual_seed(0)
+    r = lambda *s: torch.randn(*s, device="cuda", generator=g).bfloat16()  # noqa: E731
+
+    def chain(R, N, K, E):
+        x, dy, w16 = r(R, K), r(R, N), r(E, N, K)
+        off = torch.arange(E + 1, device="cuda", dtype=torch.int32) * (R // E // 128 * 128)
+        a, b, w = fp8.allocate_rows(R, K, both=True), fp8.allocate_rows(R, N, both=True), fp8.allocate_weights(E, N, K, both=True)
+        out, dx, dw = torch.zeros_like(dy), torch.zeros_like(x), torch.zeros_like(w16)
+        o, ws = torch.empty_like(dw), muon.workspace([dw.shape])
+
+        def run(s=None):
+            fp8.quantize(a, x, stream=s), fp8.quantize(b, dy, stream=s), fp8.quantize_weights(w, w16, stream=s)
+            fp8.matmul(a, w, out, off, stream=s)
+            fp8.matmul(b, w, dx, off, transposed=True, stream=s)
+            fp8.weight_grad(b, a, dw, off, stream=s)
+            muon.orthogonalize([dw], [o], ws, stream=s)
+            return out, dx, dw, o, a, b, ws
+        return run
+
+    chains = [chain(4096, 1536, 768, 8), chain(1000, 528, 2064, 3)]
+    alone = [[t.clone() for t in run()[:4]] for run in chains]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in chains]
+    graphs = []
+    for run, s in zip(chains, streams):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            run(s.cuda_stream)
+
+    def compare(outs):
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for got, want in zip(outs, alone) for x, y in zip(got, want))
+
+    for _ in range(20):
+        outs = [run(s.cuda_stream) for run, s in zip(chains, streams)]
+    compare(outs)
+    for got in outs:
+        for t in got[:4]:
+            t.zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for graph, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                graph.replay()
+    compare(outs)
+    for got in outs:
+        fp8.check(got[4]), fp8.check(got[5]), muon.check(got[6])
