@@ -416,17 +416,40 @@ __device__ __forceinline__ void ns_put8(const float (&v)[8], void* o, int type, 
   }
 }
 
-// m = momentum m + scale g; the sum of squares of what is orthogonalised, in at most NS_PARTS parts a matrix.
+// |U|_F from two sums of squares: of U, and of U times 2^100, which keeps what underflows in the first. The second
+// serves where the first is below 2^-80: there no element reaches 2^-40 and the second cannot overflow (2^120), and above it
+// the squares lost below 2^-149 are no part of the sum (2^32 of them are 2^-37 of it). fp32's smallest numbers
+// are 2^-49 times 2^100, their squares normal numbers.
+constexpr float NS_TINY = 8.271806125530277e-25f;          // 2^-80
+constexpr float NS_UP = 1.2676506002282294e30f;            // 2^100
+__device__ __forceinline__ void ns_add_square(float (&s)[2], float u) {
+  const float t = u * NS_UP;
+  s[0] = fmaf(u, u, s[0]);
+  s[1] = fmaf(t, t, s[1]);
+}
+// What takes U to X_0: times `up`, a power of two, then times `inv`. Zeros stay zeros; a sum that overflowed, or a NaN in it,
+// makes NaNs rather than a silent zero.
+struct NsNorm {
+  float up, inv;
+};
+__device__ __forceinline__ NsNorm ns_norm(const float (&s)[2], float scale) {
+  if (!(s[0] < __int_as_float(0x7f800000))) return {1.0f, __int_as_float(0x7fc00000)};
+  const bool tiny = s[0] < NS_TINY;
+  const float norm = sqrtf(tiny ? s[1] : s[0]);
+  return {tiny ? NS_UP : 1.0f, norm > 0.0f ? scale / norm : 0.0f};
+}
+
+// m = momentum m + scale g; the sums of squares of what is orthogonalised, in at most NS_PARTS parts a matrix.
 __global__ void __launch_bounds__(256) ns_momentum_kernel(const NsTensors p, float* parts) {
   wait_for_previous();
   launch_dependents();
-  __shared__ float buf[32];
+  __shared__ float buf[64];
   const int e = blockIdx.y, i = ns_find(p, e);
   const bool skip = p.control && p.control->skip;
   const float gs = p.control ? p.control->grad_scale : 1.0f;
   const long long n = static_cast<long long>(p.rows) * p.cols, base = ns_base(p, i, e);
   const bool vec = p.vec && n % 8 == 0;
-  float s[1] = {0.0f};
+  float s[2] = {0.0f, 0.0f};
   float* m = p.m[i];
 #pragma unroll 2
   for (long long j = (blockIdx.x * 256ll + threadIdx.x) * 8; j < n && !skip; j += gridDim.x * 2048ll) {
@@ -441,12 +464,15 @@ __global__ void __launch_bounds__(256) ns_momentum_kernel(const NsTensors p, flo
         v[k] = fmaf(p.momentum, v[k], u);
         u = p.nesterov ? fmaf(p.momentum, v[k], u) : v[k];
       }
-      s[0] = fmaf(u, u, s[0]);
+      ns_add_square(s, u);
     }
     if (m) ns_put8(v, m, MOE_TYPE_FP32, base + j, vec, left);
   }
   row_sums<false>(s, buf);
-  if (threadIdx.x == 0) parts[e * NS_PARTS + blockIdx.x] = s[0];
+  if (threadIdx.x == 0) {
+    parts[2 * (e * NS_PARTS + blockIdx.x)] = s[0];
+    parts[2 * (e * NS_PARTS + blockIdx.x) + 1] = s[1];
+  }
 }
 
 // The two kernels below move 64 x 64 tiles between a tensor and X, a thread eight columns of two rows on
@@ -475,10 +501,12 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const f
   __shared__ float tile[TALL ? 64 * NS_LD : 1];
   const int e = blockIdx.z, i = ns_find(p, e);
   const float gs = p.control ? p.control->grad_scale : 1.0f;
-  float sum = 0.0f;
-  for (int j = 0; j < nparts; ++j) sum += parts[e * NS_PARTS + j];
-  // an overflowed sum makes NaNs rather than a silent zero
-  const float inv = sum > 0.0f ? (isinf(sum) ? __int_as_float(0x7fc00000) : scale / sqrtf(sum)) : (sum == 0.0f ? 0.0f : sum);
+  float sum[2] = {0.0f, 0.0f};
+  for (int j = 0; j < nparts; ++j) {
+    sum[0] += parts[2 * (e * NS_PARTS + j)];
+    sum[1] += parts[2 * (e * NS_PARTS + j) + 1];
+  }
+  const NsNorm norm = ns_norm(sum, scale);
   const long long base = ns_base(p, i, e);
   const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
   const int x0 = blockIdx.x * 64, y0 = blockIdx.y * 64;          // of X
@@ -496,7 +524,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const f
     for (int j = 0; j < 8; ++j) {
       float u = gs * g[j];
       if (p.m[i]) u = p.nesterov ? fmaf(p.momentum, m[j], u) : m[j];
-      v[k][j] = u * inv;
+      v[k][j] = u * norm.up * norm.inv;
     }
   }
   ns_turn<TALL>(v, tile, r, c);
@@ -588,7 +616,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   __shared__ __align__(8) uint64_t bar;
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
-  __shared__ float buf[32];
+  __shared__ float buf[64];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(dyn_smem) + 1023) & ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
@@ -613,7 +641,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   const int n = p.rows * p.cols;
   const long long base = ns_base(p, ti, e);
   float* m = p.m[ti];
-  float sq[1] = {0.0f};
+  float sq[2] = {0.0f, 0.0f};
   constexpr int WAYS = 8;                            // elements of a thread on their way together
   for (int i0 = tid; i0 < n && !skip; i0 += 256 * WAYS) {
     float g[WAYS], v[WAYS];
@@ -643,18 +671,18 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
         m[base + i] = w;
         u = p.nesterov ? fmaf(p.momentum, w, u) : w;
       }
-      sq[0] = fmaf(u, u, sq[0]);
+      ns_add_square(sq, u);
       const int r = i / p.cols, c = i - r * p.cols;
       stage[(tall ? c : r) * (L + 1) + (tall ? r : c)] = u;
     }
   }
   row_sums<false>(sq, buf);
   __syncthreads();
-  const float inv = sq[0] > 0.0f ? (isinf(sq[0]) ? __int_as_float(0x7fc00000) : scale / sqrtf(sq[0])) : (sq[0] == 0.0f ? 0.0f : sq[0]);
+  const NsNorm norm = ns_norm(sq, scale);
   const int row = (warp & 3) * 32 + lane, col0 = (warp >> 2) * HALF;
   float x[HALF];
 #pragma unroll
-  for (int j = 0; j < HALF; ++j) x[j] = stage[row * (L + 1) + col0 + j] * inv;
+  for (int j = 0; j < HALF; ++j) x[j] = stage[row * (L + 1) + col0 + j] * norm.up * norm.inv;
   __syncthreads();
 
   const uint32_t sx = smem_u32(smem), sa = sx + (L / 64) * SM_BLOCK, sb = sa + 2 * SM_BLOCK;
@@ -810,7 +838,7 @@ static NsShape ns_shape(int rows, int cols) {
   return o;
 }
 // X twice (a step reads one and writes the other), its second part, A, B, the partial sums
-static size_t ns_matrix_bytes(const NsShape& o) { return 3 * o.x + 2 * o.a + NS_PARTS * sizeof(float); }
+static size_t ns_matrix_bytes(const NsShape& o) { return 3 * o.x + 2 * o.a + 2 * NS_PARTS * sizeof(float); }
 
 template <int KIND>
 static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_lo,

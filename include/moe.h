@@ -809,8 +809,9 @@ moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int3
  *   X_0 = U / |U|_F (0 where U is 0);   for each step's coefficients a, b, c
  *     X = a X + b X X^T X + c X X^T X X^T X
  *   w = w - lr (weight_decay w + rms sqrt(max(rows, cols)) X);   w16 = bf16(w)
- * m, w and the sum of squares in fp32 (it must not overflow: U is 0 or NaN where it does);
- * the products on fp16 operands with fp32 sums.  With `out` in place of m and w a tensor's
+ * m, w and the sums of squares in fp32.  |U|_F is right for every U whose sum of squares does not
+ * overflow, fp32's smallest numbers included; where it overflows (|U|_F from 2^64 on) X is NaN.
+ * The products on fp16 operands with fp32 sums.  With `out` in place of m and w a tensor's
  * gradient itself is orthogonalised: out = X, m, w and w16 NULL (momentum, lr and rms are not used).
  * A gradient that is not finite reaches its whole matrix.
  */

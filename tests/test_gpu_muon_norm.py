@@ -1,0 +1,84 @@
+"""The norm that Muon's matrices are divided by, over the range of fp32: gradients and momenta of any size, idle experts.
+
+Bounds: those of test_gpu_muon.py (its `near`), whose derivation stands there; and equal bits where inputs differ by a
+power of two, which no rounding of the kernels sees.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import need_gpu
+from oracle import blocks as ob
+from test_gpu_muon import matrices, near
+
+pytestmark = pytest.mark.gpu
+SHAPES = [(96, 160), (40, 7), (300, 200), (129, 257)]      # the first two in one block, the others through the workspace
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    need_gpu()
+
+
+def orthogonal(x):
+    from dropless_mixture_experts_warp_gb300 import muon
+    w = muon.workspace([x.shape])
+    o = torch.empty(x.shape, device="cuda")
+    muon.orthogonalize([x.cuda()], [o], w)
+    muon.check(w)
+    return o
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+@pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
+def test_any_scale(m, n, kind):
+    """x times a power of two has x's orthogonal factor, bit for bit, also where squares of its elements are below fp32."""
+    x = matrices(np.random.default_rng(m), 1, m, n, kind, scale=1.0)
+    want = orthogonal(x)
+    near(want[0], x[0].double().numpy(), torch.float32)
+    for e in (30, -20, -45, -55, -62, -66, -70, -75, -90):
+        y = x * 2.0 ** e
+        assert torch.equal(y.double(), x.double() * 2.0 ** e)      # nothing of x is lost
+        assert torch.equal(orthogonal(y), want), e
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+def test_subnormal_elements(m, n):
+    x = matrices(np.random.default_rng(n), 1, m, n, torch.float32, scale=2.0 ** -136)
+    assert 0 < x.abs().max() < 2.0 ** -126
+    near(orthogonal(x)[0], x[0].double().numpy(), torch.float32)
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+def test_matrices_of_different_sizes_together(m, n):
+    """Each matrix of a batch by its own norm."""
+    x = matrices(np.random.default_rng(3), 5, m, n, torch.float32, scale=1.0)
+    for i, e in enumerate((0, -70, -100, 20, -60)):
+        x[i] *= 2.0 ** e
+    x[2] = 0.0
+    o = orthogonal(x)
+    assert (o[2] == 0).all()
+    for i in (0, 1, 3, 4):
+        near(o[i], x[i].double().numpy(), torch.float32)
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+@pytest.mark.parametrize("rank", [1, 4, None])
+def test_idle_expert(m, n, rank):
+    """An expert without tokens has gradients of zeros: its momentum shrinks by 0.95 a step until it is gone, and its
+    weights stay finite."""
+    from dropless_mixture_experts_warp_gb300 import muon
+    rng = np.random.default_rng(5)
+    if rank is None:
+        mom = matrices(rng, 2, m, n, torch.float32)
+    else:
+        mom = torch.from_numpy(1e-4 * rng.standard_normal((2, m, rank)) @ rng.standard_normal((2, rank, n))).float()
+    w = torch.from_numpy(rng.standard_normal((2, m, n)).astype(np.float32) * 0.02).cuda()
+    low = w.bfloat16()
+    p = muon.plan([w], [torch.zeros(2, m, n, device="cuda")], copies=[low], m=[mom.cuda()])
+    for t in range(1, 2101):
+        muon.step(p, lr=1e-3)
+        if t % 25 == 0:
+            assert torch.isfinite(w).all() and torch.isfinite(p.m[0]).all(), t
+    muon.check(p)
+    assert torch.isfinite(low).all()
