@@ -175,6 +175,7 @@ SIGNATURES = {
     "moe_adamw_step": (ctypes.c_int32, [ctypes.POINTER(moe_adamw_hyper), _T, _I, _P, _P]),
     "moe_adamw_values": (ctypes.c_int32, [_T, _I, _I, _PP, _PP, _P]),
     "moe_muon_workspace_size": (ctypes.c_size_t, [_U, _I, ctypes.c_size_t]),
+    "moe_muon_step_floor": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, ctypes.c_double, _P, ctypes.c_size_t, _P, _P, _P]),
     "moe_muon_step": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, _P, ctypes.c_size_t, _P, _P, _P]),
 }
 
@@ -642,6 +643,12 @@ def moe_adamw_values(tensors, count, out_type, m_out, v_out, stream=None):
 
 def moe_muon_workspace_size(tensors, count, limit) -> int:
     return lib().moe_muon_workspace_size(tensors, count, limit)
+
+
+def moe_muon_step_floor(hyper, tensors, count, norm_floor, workspace, workspace_bytes, control=None, dev_status=None, stream=None):
+    """moe_muon_step() with norms of at least norm_floor."""
+    return _call("moe_muon_step_floor", None if hyper is None else ctypes.byref(hyper), tensors, count, norm_floor, _ptr(workspace),
+                 workspace_bytes, _ptr(control), _ptr(dev_status), _stream(stream))
 
 
 def moe_muon_step(hyper, tensors, count, workspace, workspace_bytes, control=None, dev_status=None, stream=None):

@@ -427,16 +427,16 @@ __device__ __forceinline__ void ns_add_square(float (&s)[2], float u) {
   s[0] = fmaf(u, u, s[0]);
   s[1] = fmaf(t, t, s[1]);
 }
-// What takes U to X_0: times `up`, a power of two, then times `inv`. Zeros stay zeros; a sum that overflowed, or a NaN in it,
+// What takes U to X_0, over a norm of at least `floor`: times `up`, a power of two, then times `inv`. Zeros stay zeros; a sum that overflowed, or a NaN in it,
 // makes NaNs rather than a silent zero.
 struct NsNorm {
   float up, inv;
 };
-__device__ __forceinline__ NsNorm ns_norm(const float (&s)[2], float scale) {
+__device__ __forceinline__ NsNorm ns_norm(const float (&s)[2], float scale, float floor) {
   if (!(s[0] < __int_as_float(0x7f800000))) return {1.0f, __int_as_float(0x7fc00000)};
   const bool tiny = s[0] < NS_TINY;
-  const float norm = sqrtf(tiny ? s[1] : s[0]);
-  return {tiny ? NS_UP : 1.0f, norm > 0.0f ? scale / norm : 0.0f};
+  const float up = tiny ? NS_UP : 1.0f, norm = fmaxf(sqrtf(tiny ? s[1] : s[0]), floor * up);
+  return {up, norm > 0.0f ? scale / norm : 0.0f};
 }
 
 // m = momentum m + scale g; the sums of squares of what is orthogonalised, in at most NS_PARTS parts a matrix.
@@ -492,10 +492,10 @@ __device__ __forceinline__ void ns_turn(float (&v)[2][8], float* tile, int r, in
     for (int j = 0; j < 8; ++j) v[k][j] = tile[(c + j) * NS_LD + r + 32 * k];
 }
 
-// X = scale U / |U| in two fp16 parts, [s][l] with zeros in the padding.
+// X = scale U / max(|U|, floor) in two fp16 parts, [s][l] with zeros in the padding.
 template <bool TALL>
 __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const float* parts, int nparts, int s, int l, float scale,
-                                                      __half* hi, __half* lo) {
+                                                      float floor, __half* hi, __half* lo) {
   wait_for_previous();
   launch_dependents();
   __shared__ float tile[TALL ? 64 * NS_LD : 1];
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const f
     sum[0] += parts[2 * (e * NS_PARTS + j)];
     sum[1] += parts[2 * (e * NS_PARTS + j) + 1];
   }
-  const NsNorm norm = ns_norm(sum, scale);
+  const NsNorm norm = ns_norm(sum, scale, floor);
   const long long base = ns_base(p, i, e);
   const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
   const int x0 = blockIdx.x * 64, y0 = blockIdx.y * 64;          // of X
@@ -610,7 +610,8 @@ __device__ __forceinline__ void small_put(uint32_t block0, int row, int col, con
 }
 
 template <int L>
-__global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, const NsSteps h, float scale, float lr, float rms, int32_t* status) {
+__global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, const NsSteps h, float scale, float floor, float lr, float rms,
+                                                          int32_t* status) {
   constexpr int HALF = L / 2;                        // X's columns of a thread
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t bar;
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   }
   row_sums<false>(sq, buf);
   __syncthreads();
-  const NsNorm norm = ns_norm(sq, scale);
+  const NsNorm norm = ns_norm(sq, scale, floor);
   const int row = (warp & 3) * 32 + lane, col0 = (warp >> 2) * HALF;
   float x[HALF];
 #pragma unroll
@@ -854,7 +855,7 @@ static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const C
 }
 
 // `batch` matrices of one shape: products, update.
-static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float lr, void* workspace, int32_t* status,
+static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float floor, float lr, void* workspace, int32_t* status,
                             cudaStream_t st) {
   const NsShape o = ns_shape(t.rows, t.cols);
   uint8_t* w = static_cast<uint8_t*>(workspace);
@@ -874,8 +875,8 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
     const int smem = small_smem(o.l);
     const cudaError_t err = o.l == 128 ? allow_smem<ns_small_kernel<128>>(smem) : allow_smem<ns_small_kernel<256>>(smem);
     if (err != cudaSuccess) return err;
-    return o.l == 128 ? launch_early(ns_small_kernel<128>, dim3(batch), dim3(256), smem, st, t, steps, scale, lr, rms, status)
-                      : launch_early(ns_small_kernel<256>, dim3(batch), dim3(256), smem, st, t, steps, scale, lr, rms, status);
+    return o.l == 128 ? launch_early(ns_small_kernel<128>, dim3(batch), dim3(256), smem, st, t, steps, scale, floor, lr, rms, status)
+                      : launch_early(ns_small_kernel<256>, dim3(batch), dim3(256), smem, st, t, steps, scale, floor, lr, rms, status);
   }
   t.vec = 1;
   for (int i = 0; i < t.count; ++i)
@@ -885,8 +886,8 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   cudaError_t err = launch_early(ns_momentum_kernel, dim3(nparts, batch), dim3(256), 0, st, t, parts);
   if (err != cudaSuccess) return err;
   const dim3 tiles_x(o.l / 64, o.s / 64, batch), tiles_t((t.cols + 63) / 64, (t.rows + 63) / 64, batch);
-  err = tall ? launch_early(ns_load_kernel<true>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo)
-             : launch_early(ns_load_kernel<false>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, x[0], lo);
+  err = tall ? launch_early(ns_load_kernel<true>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, floor, x[0], lo)
+             : launch_early(ns_load_kernel<false>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, floor, x[0], lo);
   if (err != cudaSuccess) return err;
   const uint64_t rows = static_cast<uint64_t>(batch) * o.s;
   CUtensorMap xk[2], xn[2], xs[2], los, ak, as, bk, bs;
@@ -949,9 +950,16 @@ size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, si
 
 moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
                          size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream) {
+  return moe_muon_step_floor(hyper, tensors, count, 0.0, workspace, workspace_bytes, control, dev_status, stream);
+}
+
+moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
+                               void* workspace, size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status,
+                               void* stream) {
   if (!hyper || !dev_status) return MOE_ERR_INVALID_ARG;
   const moe_muon_hyper& h = *hyper;
-  const float lr = static_cast<float>(h.lr);
+  const float lr = static_cast<float>(h.lr), floor = static_cast<float>(norm_floor);
+  if (!(floor >= 0.0f) || !std::isfinite(floor)) return MOE_ERR_INVALID_ARG;
   if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.momentum >= 0.0 && h.momentum < 1.0) || !(h.rms >= 0.0) || !std::isfinite(h.rms) ||
       h.steps < 1 || h.steps > MOE_MUON_MAX_STEPS)
     return MOE_ERR_INVALID_ARG;
@@ -987,7 +995,7 @@ moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* ten
     auto flush = [&]() -> cudaError_t {
       if (batch == 0) return cudaSuccess;
       t.first[t.count] = batch;
-      const cudaError_t e = ns_chunk(t, batch, h, lr, workspace, dev_status, s);
+      const cudaError_t e = ns_chunk(t, batch, h, floor, lr, workspace, dev_status, s);
       t.count = 0; t.skip0 = 0; batch = 0;
       return e;
     };

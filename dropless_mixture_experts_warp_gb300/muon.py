@@ -103,16 +103,18 @@ def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COE
                 _hyper(0.0, 0.0, 0.0, True, coefficients), device)
 
 
-def step(p: Plan, lr, momentum=0.95, rms=0.2, nesterov=True, control=None, stream=None):
+def step(p: Plan, lr, momentum=0.95, rms=0.2, nesterov=True, control=None, stream=None, eps=1e-7):
     """Updates p's momenta, weights and copies.  rms: root mean square of the update's elements at lr = 1 (of a full
-    orthogonal factor).  control: an optim.Control, whose scales and skip the kernels then read on the device."""
+    orthogonal factor).  control: an optim.Control, whose scales and skip the kernels then read on the device.  eps:
+    a matrix whose update's norm is below it is divided by eps instead, so that the steps of an expert without tokens fade
+    with its momentum (0: every matrix that is not 0 takes full steps)."""
     B.check_device(p.device, stream)
     raw = None if control is None else control.raw
     if p.weights:
         B.check_tensor(raw, torch.int32, (4,), p.device)
     h = p.hyper
     h.lr, h.momentum, h.rms, h.nesterov = lr, momentum, rms, int(nesterov)
-    B.moe_muon_step(h, p.table, len(p.weights), p.workspace, p.workspace.numel(), raw, p.status, stream)
+    B.moe_muon_step_floor(h, p.table, len(p.weights), eps, p.workspace, p.workspace.numel(), raw, p.status, stream)
 
 
 def workspace(shapes, coefficients=COEFFICIENTS, limit=WORKSPACE, device="cuda") -> Workspace:

@@ -844,6 +844,15 @@ size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, si
 moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
                          size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream);
 
+/*
+ * The same with X_0 = U / max(|U|_F, norm_floor) (finite, >= 0; 0 is moe_muon_step): matrices
+ * whose U has all but gone, an expert's without tokens for a while, take steps that fade with
+ * it instead of full ones along what is left of its direction.
+ */
+moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
+                               void* workspace, size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status,
+                               void* stream);
+
 #ifdef __cplusplus
 }
 #endif

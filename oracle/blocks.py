@@ -98,9 +98,9 @@ def swiglu_bwd(g, u, w, dh):
 COEFFICIENTS = [(3.4445, -4.7750, 2.0315)] * 5
 
 
-def newton_schulz(x, coefficients=COEFFICIENTS):
-    """x [m, n] float64 -> a_i X + b_i X X^T X + c_i X X^T X X^T X, step by step, from X / |X|_F."""
-    n = np.linalg.norm(x)
+def newton_schulz(x, coefficients=COEFFICIENTS, eps=0.0):
+    """x [m, n] float64 -> a_i X + b_i X X^T X + c_i X X^T X X^T X, step by step, from X / max(|X|_F, eps)."""
+    n = max(np.linalg.norm(x), eps)
     x = x / n if n > 0 else np.zeros_like(x)
     for a, b, c in coefficients:
         x3 = x @ (x.T @ x) if x.shape[0] > x.shape[1] else (x @ x.T) @ x
@@ -109,19 +109,19 @@ def newton_schulz(x, coefficients=COEFFICIENTS):
     return x
 
 
-def muon_step(w, m, grad, lr, momentum, decay, rms, nesterov=True, coefficients=COEFFICIENTS):
+def muon_step(w, m, grad, lr, momentum, decay, rms, nesterov=True, coefficients=COEFFICIENTS, eps=0.0):
     """One matrix: (w', m', update)."""
     m = momentum * m + grad
-    o = newton_schulz(grad + momentum * m if nesterov else m, coefficients)
+    o = newton_schulz(grad + momentum * m if nesterov else m, coefficients, eps)
     return w - lr * (decay * w + rms * np.sqrt(max(w.shape)) * o), m, o
 
 
-def newton_schulz_rounded(x, coefficients=COEFFICIENTS):
+def newton_schulz_rounded(x, coefficients=COEFFICIENTS, eps=0.0):
     """newton_schulz as the kernels round it: products on fp16 operands, X in two parts in the addend, multiples of I
     taken off A and B in the last two steps, everything else exact.  How far it is from newton_schulz is what that arithmetic costs."""
     h = lambda v: v.astype(np.float16).astype(np.float64)  # noqa: E731
     x = x.T if x.shape[0] > x.shape[1] else x
-    n = np.linalg.norm(x)
+    n = max(np.linalg.norm(x), eps)
     length = up(x.shape[1])
     scale = 1.0
     while scale * scale * 4 <= length:

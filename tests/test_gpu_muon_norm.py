@@ -82,3 +82,51 @@ def test_idle_expert(m, n, rank):
             assert torch.isfinite(w).all() and torch.isfinite(p.m[0]).all(), t
     muon.check(p)
     assert torch.isfinite(low).all()
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+def test_idle_expert_comes_to_rest(m, n):
+    """The steps of an expert without tokens fade below eps, as the definition's do."""
+    from dropless_mixture_experts_warp_gb300 import muon
+    rng = np.random.default_rng(6)
+    mom = matrices(rng, 2, m, n, torch.float32)
+    w = torch.from_numpy(rng.standard_normal((2, m, n)).astype(np.float32) * 0.02).cuda()
+    p = muon.plan([w], [torch.zeros(2, m, n, device="cuda")], m=[mom.cuda()])
+    for _ in range(800):
+        muon.step(p, lr=1e-3)
+    rest = w.clone()
+    for _ in range(400):
+        muon.step(p, lr=1e-3)
+    muon.check(p)
+    # |U| started below 0.1 and is below 0.1 x 0.95^800 = 2^-62 after 800 steps, 2^-38 of eps; five steps make a
+    # singular value at most 3.4445^5 < 2^9 times as large, so an update's norm is below lr rms sqrt(max side)
+    # 2^-29, and all that follow add up to 20 of them, for each of two matrices; adding them rounds w below half a step
+    assert mom.norm() < 0.1
+    size = 1e-3 * 0.2 * np.sqrt(max(m, n))
+    assert (w - rest).norm().item() <= 2 * 20 * size * 2.0 ** -29
+
+
+@pytest.mark.parametrize("m,n", SHAPES)
+@pytest.mark.parametrize("times", [0.0, 0.3, 1.0, 5.0, 1e4])
+def test_floor(m, n, times):
+    """X_0 = U / max(|U|, eps), against float64."""
+    from dropless_mixture_experts_warp_gb300 import muon
+    rng = np.random.default_rng(m + 1)
+    g = matrices(rng, 1, m, n, torch.float32)[0]
+    w0 = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32) * 0.02)
+    eps = times * g.double().norm().item()
+    w = w0.cuda()
+    p = muon.plan([w], [g.cuda()])
+    lr, rms = 2e-2, 0.2
+    muon.step(p, lr=lr, momentum=0.0, rms=rms, nesterov=False, eps=eps)
+    muon.check(p)
+    u = g.double().numpy()
+    ref, _, o = ob.muon_step(w0.double().numpy(), np.zeros((m, n)), u, lr, 0.0, 0.0, rms, False, eps=eps)
+    low = ob.newton_schulz_rounded(u, eps=eps)
+    e = np.linalg.norm((low.T if m > n else low) - o)
+    size = lr * rms * np.sqrt(max(m, n))
+    off = np.linalg.norm(w.double().cpu().numpy() - ref)
+    # as in test_gpu_muon.py's test_step, and fp16's smallest steps, 2^-25 of an element of X_0 in its second
+    # part, which five steps make at most 2^9 times as large: they count where X_0 is small
+    fine = 2.0 ** -16 * np.sqrt(m * n)
+    assert off <= size * (1.5 * e + 2.0 ** -11 * np.linalg.norm(o) + fine) + 4 * ob.U32 * np.linalg.norm(np.abs(ref) + size * np.abs(o))
