@@ -55,6 +55,19 @@ def _sides(shape):
     return batch, shape[-2], shape[-1]
 
 
+def _apart(written, read):
+    """Refuse tensors of which one is written and shares memory with another: the matrices of a call run in no order."""
+    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w) for w, ts in ((True, written), (False, read))
+                   for t in ts if t is not None and t.numel())
+    end = end_written = 0
+    for start, stop, w in spans:
+        if start < (end if w else end_written):
+            raise ValueError("a tensor that is written shares memory with another of the call")
+        end = max(end, stop)
+        if w:
+            end_written = max(end_written, stop)
+
+
 def _hyper(lr, momentum, rms, nesterov, coefficients):
     coefficients = [tuple(c) for c in coefficients]
     if not 1 <= len(coefficients) <= B.MUON_MAX_STEPS or any(len(c) != 3 for c in coefficients):
@@ -71,7 +84,8 @@ def _allocate(table, n, limit, device):
 
 def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COEFFICIENTS, workspace=WORKSPACE) -> Plan:
     """weights: fp32; grads: bf16 or fp32; copies: bf16 or None; weight_decay: one number or one a tensor.  The
-    momentum starts at zero, or is the one given (a resumed run's, fp32).  workspace: bytes of scratch at most; a plan's
+    momentum starts at zero, or is the one given (a resumed run's, fp32).  No tensor may share memory with another, but
+    gradients with each other.  workspace: bytes of scratch at most; a plan's
     steps share it, so they follow one another, also as replays of captured graphs."""
     weights, grads = list(weights), list(grads)
     n = len(weights)
@@ -99,6 +113,7 @@ def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COE
         t.grad, t.m, t.w = grads[i].data_ptr(), m[i].data_ptr(), w.data_ptr()
         t.w16 = None if copies[i] is None else copies[i].data_ptr()
         t.weight_decay, t.grad_type = decay[i], B.TYPE["bf16" if low else "fp32"]
+    _apart(weights + m + copies, grads)
     return Plan(weights, grads, copies, m, table, *_allocate(table, n, workspace, device),
                 _hyper(0.0, 0.0, 0.0, True, coefficients), device)
 
@@ -128,7 +143,8 @@ def workspace(shapes, coefficients=COEFFICIENTS, limit=WORKSPACE, device="cuda")
 
 
 def orthogonalize(xs, outs, w: Workspace, stream=None):
-    """outs[i] (bf16 or fp32) = the orthogonal factor of xs[i] (bf16 or fp32) as the steps approximate it."""
+    """outs[i] (bf16 or fp32) = the orthogonal factor of xs[i] (bf16 or fp32) as the steps approximate it.  outs[i] may be
+    xs[i] itself; no output may share memory otherwise."""
     B.check_device(w.device, stream)
     if len(xs) != len(w.shapes) or len(outs) != len(w.shapes):
         raise ValueError(f"expected {len(w.shapes)} tensors, got {len(xs)} and {len(outs)}")
@@ -138,6 +154,7 @@ def orthogonalize(xs, outs, w: Workspace, stream=None):
         B.check_tensor(o, kind[1], s, w.device)
         t.grad, t.out = x.data_ptr(), o.data_ptr()
         t.grad_type, t.out_type = (B.TYPE["bf16" if k == torch.bfloat16 else "fp32"] for k in kind)
+    _apart(outs, [x for x, o in zip(xs, outs) if x.data_ptr() != o.data_ptr() or x.dtype != o.dtype])
     B.moe_muon_step(w.hyper, w.table, len(xs), w.workspace, w.workspace.numel(), None, w.status, stream)
     return outs
 
