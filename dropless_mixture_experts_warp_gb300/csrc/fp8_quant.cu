@@ -8,6 +8,11 @@
 
 namespace moe {
 
+// Rows that a call works on: *nrows_dev of them, where it is given; none where that is negative.
+__device__ __forceinline__ int rows_in_use(int rows, const int32_t* nrows_dev) {
+  return nrows_dev ? max(0, min(rows, *nrows_dev)) : rows;
+}
+
 // ------------------------------------------------------------------------ rows
 
 constexpr int QR_ROWS = 4;   // rows under way in a warp
@@ -32,7 +37,7 @@ __global__ void __launch_bounds__(256) f8_rows_kernel(const uint16_t* src, int r
   wait_for_previous();
   launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  const int limit = rows_in_use(rows, nrows_dev);
   const int groups = (C + 255) / 256;
   const long long total = static_cast<long long>((limit + QR_ROWS - 1) / QR_ROWS) * groups;
   for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8ll) {
@@ -122,7 +127,7 @@ __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
   const int tid = threadIdx.x;
   wait_for_previous();
   launch_dependents();
-  const int limit = p.nrows_dev ? min(p.R, *p.nrows_dev) : p.R;
+  const int limit = rows_in_use(p.R, p.nrows_dev);
   const unsigned ctiles = (p.C + 127) / 128, rtiles = (limit + 127) / 128;
   const unsigned total = p.batch * rtiles * ctiles;
 
@@ -291,7 +296,7 @@ __global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* gu, cons
   wait_for_previous();
   launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  const int limit = rows_in_use(rows, nrows_dev);
   const int groups = (f + 255) / 256;
   const long long total = static_cast<long long>((limit + 1) / 2) * groups;
   for (long long t = static_cast<long long>(blockIdx.x) * 8 + (threadIdx.x >> 5); t < total; t += gridDim.x * 8ll) {
@@ -364,7 +369,7 @@ __global__ void __launch_bounds__(SB_THREADS, 1) f8_swiglu_bwd_kernel(const F8Sw
   wait_for_previous();
   launch_dependents();
   const int tid = threadIdx.x, c = tid & 15, u = tid >> 4;
-  const int limit = p.nrows_dev ? min(p.rows, *p.nrows_dev) : p.rows;
+  const int limit = rows_in_use(p.rows, p.nrows_dev);
   const unsigned ctiles = p.f / 128, total = static_cast<unsigned>((limit + 127) / 128) * ctiles;
 
   auto fetch = [&](unsigned t) {
@@ -518,7 +523,7 @@ __global__ void f8_dw_kernel(const float* part, int parts, int rows, const int32
                              float* dw) {
   wait_for_previous();
   launch_dependents();
-  const int limit = nrows_dev ? min(rows, *nrows_dev) : rows;
+  const int limit = rows_in_use(rows, nrows_dev);
   for (int r = blockIdx.x * blockDim.x + threadIdx.x; r < limit; r += gridDim.x * blockDim.x) {
     float s = 0.0f;
     for (int i = 0; i < parts; ++i) s += part[static_cast<long long>(r) * parts + i];

@@ -545,9 +545,9 @@ moe_status moe_gemm_bf16(const moe_bf16* A, const moe_bf16* B, moe_bf16* C, int3
  * src bf16 [rows][C] (C % 16 == 0) -> the row form, the column form, or both from one read
  * (each pair of codes and scales given, or both NULL).  row_map [rows] int32 or NULL: row r is
  * src row row_map[r], zeros where that is negative (src then has any number of rows; an index
- * past them is not looked for).  nrows_dev (device int32, or NULL): 128-row blocks from *nrows_dev
- * on are left as they were; rows from there to the end of its block are zeros in the column form,
- * and zeros or left in the row form.
+ * past them is not looked for).  nrows_dev (device int32, or NULL; above rows it counts as rows,
+ * below 0 as 0): 128-row blocks from *nrows_dev on are left as they were; rows from there to the
+ * end of its block are zeros in the column form, and zeros or left in the row form.
  */
 moe_status moe_fp8_quantize(const moe_bf16* src, int64_t rows, int32_t C, const int32_t* row_map,
                             const int32_t* nrows_dev, uint8_t* codes, float* scales, uint8_t* codes_t,

@@ -37,3 +37,21 @@ def test_h_of_the_gradient_is_the_forward_h(weighted):
     assert torch.equal(rows, rows[:, :, :1].expand_as(rows))
     different = h.codes.view(torch.uint8) != ht.codes_t.view(torch.uint8).t()
     assert not different.any(), int(different.sum())
+
+
+@pytest.mark.parametrize("count", [-1, -128, -300, -(1 << 31), 0])
+def test_counts_below_zero_are_no_rows(count):
+    """A count of rows that is negative counts as none: every buffer stays as it was."""
+    from dropless_mixture_experts_warp_gb300 import binding as B, fp8
+    R, f = 300, 256
+    n = torch.tensor([count], dtype=torch.int32).cuda()
+    x, dh = torch.randn(R, 2 * f, device="cuda").bfloat16(), torch.randn(R, f, device="cuda").bfloat16()
+    a, d, h = fp8.allocate_rows(R, 2 * f, both=True), fp8.allocate_rows(R, 2 * f, both=True), fp8.allocate_rows(R, f, both=True)
+    dw, part, w = torch.full((R,), 7.0, device="cuda"), torch.full((R, f // 128), 7.0, device="cuda"), torch.ones(R, device="cuda")
+    codes = [t.view(torch.uint8).fill_(0x11) for r in (a, d, h) for t in (r.codes, r.codes_t)]
+    scales = [t.fill_(7.0) for r in (a, d, h) for t in (r.scales, r.scales_t)]
+    B.moe_fp8_quantize(x, R, 2 * f, None, n, a.codes, a.scales, a.codes_t, a.scales_t)
+    B.moe_fp8_quantize(x, R, 2 * f, None, n, a.codes, a.scales, None, None)
+    B.moe_fp8_swiglu(x, w, R, f, n, h.codes, h.scales)
+    B.moe_fp8_swiglu_bwd(x, dh, w, R, f, n, d.codes, d.scales, d.codes_t, d.scales_t, h.codes_t, h.scales_t, dw, part)
+    assert all((t == 0x11).all() for t in codes) and all((t == 7.0).all() for t in scales + [dw, part])
