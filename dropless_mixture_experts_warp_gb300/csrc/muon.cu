@@ -854,6 +854,11 @@ static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const C
   return launch_early(kern, dim3(grid), dim3(NS_THREADS), NS_SMEM, s, a, b, in, in_lo, out, out_lo, p);
 }
 
+// What X is multiplied by in an update.
+static float ns_rms(const moe_muon_hyper& h, int rows, int cols) {
+  return static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(rows, cols))));
+}
+
 // `batch` matrices of one shape: products, update.
 static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float floor, float lr, void* workspace, int32_t* status,
                             cudaStream_t st) {
@@ -870,7 +875,7 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   while (scale * scale * 4.0f <= o.l) scale *= 2.0f;
   const bool tall = t.rows > t.cols;
   const NsSteps steps = ns_steps(h);
-  const float rms = static_cast<float>(h.rms * std::sqrt(static_cast<double>(std::max(t.rows, t.cols))));
+  const float rms = ns_rms(h, t.rows, t.cols);
   if (o.s == 128 && o.l <= 256) {
     const int smem = small_smem(o.l);
     const cudaError_t err = o.l == 128 ? allow_smem<ns_small_kernel<128>>(smem) : allow_smem<ns_small_kernel<256>>(smem);
@@ -960,8 +965,8 @@ moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tenso
   const moe_muon_hyper& h = *hyper;
   const float lr = static_cast<float>(h.lr), floor = static_cast<float>(norm_floor);
   if (!(floor >= 0.0f) || !std::isfinite(floor)) return MOE_ERR_INVALID_ARG;
-  if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.momentum >= 0.0 && h.momentum < 1.0) || !(h.rms >= 0.0) || !std::isfinite(h.rms) ||
-      h.steps < 1 || h.steps > MOE_MUON_MAX_STEPS)
+  if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.momentum >= 0.0 && static_cast<float>(h.momentum) < 1.0f) || !(h.rms >= 0.0) ||
+      !std::isfinite(h.rms) || h.steps < 1 || h.steps > MOE_MUON_MAX_STEPS)
     return MOE_ERR_INVALID_ARG;
   for (int i = 0; i < 3 * h.steps; ++i)
     if (!std::isfinite(h.coefficients[i])) return MOE_ERR_INVALID_ARG;
@@ -972,6 +977,7 @@ moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tenso
     const moe_muon_tensor& t = tensors[i];
     if (t.batch == 0) continue;
     if (!t.grad || (!t.out == !t.w) || (!t.w != !t.m) || (t.w16 && !t.w)) return MOE_ERR_INVALID_ARG;
+    if (t.w && (!std::isfinite(t.weight_decay) || !std::isfinite(ns_rms(h, t.rows, t.cols)))) return MOE_ERR_INVALID_ARG;
     need = std::max(need, ns_matrix_bytes(ns_shape(t.rows, t.cols)));
   }
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;

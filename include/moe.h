@@ -829,7 +829,7 @@ typedef struct moe_muon_tensor {
 } moe_muon_tensor;
 
 typedef struct moe_muon_hyper {
-  double lr, momentum, rms;    /* lr, rms >= 0, 0 <= momentum < 1 */
+  double lr, momentum, rms;    /* lr, rms >= 0, 0 <= momentum < 1; momentum, and rms sqrt(side), as fp32 numbers */
   int32_t nesterov;
   int32_t steps;               /* 1 .. MOE_MUON_MAX_STEPS */
   float coefficients[3 * MOE_MUON_MAX_STEPS];   /* a, b, c of each */

@@ -14,6 +14,15 @@ def test_floor(B):  # noqa: F811
     assert B.moe_muon_step_floor(muon_hyper(B), muon_table(B), 0, 1e-7, None, 0, None, P, stream=0) == 0
 
 
+def test_numbers_as_the_kernels_use_them(B):  # noqa: F811
+    """A momentum that is 1 in fp32, decays and lengths of updates that are not finite there."""
+    run = lambda h, t: status(B, "moe_muon_step", h, t, 1, P, 1 << 30, None, P)  # noqa: E731
+    assert run(muon_hyper(B, momentum=1.0 - 1e-12), muon_table(B)) == 1
+    assert run(muon_hyper(B, rms=3e38), muon_table(B)) == 1                  # times sqrt(16)
+    for decay in (float("nan"), float("inf"), 1e39):
+        assert run(muon_hyper(B), muon_table(B, weight_decay=decay)) == 1
+
+
 def test_plans_of_tensors_that_share_memory(B):  # noqa: F811
     """Steps write weights, momenta and copies: none may share memory with anything, gradients only with each other."""
     from dropless_mixture_experts_warp_gb300 import muon
