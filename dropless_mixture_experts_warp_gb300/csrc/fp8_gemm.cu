@@ -56,7 +56,7 @@ constexpr int F8_SPLIT_LD = 128 + 4;     // floats of a row of a part
 
 struct Fp8Params {
   int rows;                    // rows of A (SCHED_ROWS), or along the contraction (SCHED_KGROUP)
-  int M, N, K;                 // SCHED_KGROUP: out [E][M][N]; SCHED_ROWS: out [rows][N], K long
+  int M, N;                    // SCHED_KGROUP: out [E][M][N]; SCHED_ROWS: out [rows][N]
   int E;
   const int32_t* row_offsets;  // [E + 1] multiples of 128, or NULL: one group
   const float* sa;             // [kb][rows or M]
@@ -523,7 +523,7 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
       !make_tensor_map_u8(&tb, b, K, static_cast<uint64_t>(E) * N, F8_K, F8_B_BOX))
     return MOE_ERR_CUDA;
   Fp8Params p{};
-  p.rows = static_cast<int>(rows); p.N = N; p.K = K; p.E = E; p.row_offsets = row_offsets;
+  p.rows = static_cast<int>(rows); p.N = N; p.E = E; p.row_offsets = row_offsets;
   p.sa = a_scales; p.sa_ld = rows;
   const long long nb = (N + 127) / 128, kb = (K + 127) / 128;
   p.sb = b_scales; p.sb_e = nb * kb; p.sb_n = b_transposed ? 1 : kb; p.sb_k = b_transposed ? nb : 1;
@@ -532,7 +532,8 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
   p.status = dev_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int R = p.rows;
-  // One matrix and few tiles: the contraction over up to eight SMs a tile, four blocks each at least (5 x 4096 x 7168,
+  // One matrix and few tiles: the contraction over up to eight SMs a tile, four blocks each or more but for the last
+  // ones, which take what is left (33 blocks over eight: five each, three, none).  (5 x 4096 x 7168,
   // bound by reading the weights: 13 us on 128 SMs, 22 on 32).
   const int64_t few = tiles * ((N + 127) / 128);
   if (!row_offsets) {

@@ -139,12 +139,12 @@ __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
       sr[j] = (t >= total || r >= limit) ? -1 : (p.row_map ? p.row_map[r] : r);
     }
   };
-  auto fetch = [&](unsigned t, int buf, const int (&sr)[8]) {
+  auto fetch = [&](unsigned t, const int (&sr)[8]) {
     if (t < total) {
       const unsigned q = t / ctiles;
       const int col = static_cast<int>(t - q * ctiles) * 128 + (tid & 15) * 8;
       const uint16_t* s = p.src + static_cast<long long>(q / rtiles) * p.R * p.C;
-      uint8_t* dst = sm + buf * QT_IN_BYTES + (tid >> 4) * QT_IN_LD * 2 + (tid & 15) * 16;
+      uint8_t* dst = sm + (tid >> 4) * QT_IN_LD * 2 + (tid & 15) * 16;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         const bool ok = sr[j] >= 0 && col < p.C;
@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
   unsigned t = blockIdx.x;
   int next[8];
   rows_of(t, next);
-  fetch(t, 0, next);
+  fetch(t, next);
   rows_of(t + gridDim.x, next);
   for (; t < total; t += gridDim.x) {
     copy_wait<0>();
@@ -181,17 +181,17 @@ __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
       cmax[g * 128 + 2 * cp] = fabsf(bf16_lo(m));
       cmax[g * 128 + 2 * cp + 1] = fabsf(bf16_hi(m));
     }
-    m = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint4 u = *reinterpret_cast<const uint4*>(&tile[rr][hh * 64 + 8 * i]);
-      if (!SQUARE) m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, u.x), u.y), u.z), u.w);
-    }
     if (SQUARE) {
 #pragma unroll
       for (int off = 16; off > 0; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
       if ((tid & 31) == 0) tmax[tid >> 5] = amax;
     } else {
+      m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint4 u = *reinterpret_cast<const uint4*>(&tile[rr][hh * 64 + 8 * i]);
+        m = absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(absmax_bf16x2(m, u.x), u.y), u.z), u.w);
+      }
       rmax[hh * 128 + rr] = max_halves(m);
     }
     __syncthreads();
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
       }
     }
     __syncthreads();
-    fetch(t + gridDim.x, 0, next);
+    fetch(t + gridDim.x, next);
     rows_of(t + 2 * gridDim.x, next);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
