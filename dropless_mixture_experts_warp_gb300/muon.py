@@ -55,17 +55,21 @@ def _sides(shape):
     return batch, shape[-2], shape[-1]
 
 
-def _apart(written, read):
-    """Refuse tensors of which one is written and shares memory with another: the matrices of a call run in no order."""
-    spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), w) for w, ts in ((True, written), (False, read))
-                   for t in ts if t is not None and t.numel())
+def _apart(spans):
+    """Refuse memory that is written and shared: the matrices of a call run in no order.  spans: (start, stop, written)."""
     end = end_written = 0
-    for start, stop, w in spans:
-        if start < (end if w else end_written):
+    for start, stop, written in sorted(spans):
+        if start < (end if written else end_written) and start < stop:
             raise ValueError("a tensor that is written shares memory with another of the call")
-        end = max(end, stop)
-        if w:
-            end_written = max(end_written, stop)
+        if stop > end:
+            end = stop
+        if written and stop > end_written:
+            end_written = stop
+
+
+def _span(t, written):
+    at = t.data_ptr()
+    return at, at + t.numel() * t.element_size(), written
 
 
 def _hyper(lr, momentum, rms, nesterov, coefficients):
@@ -113,7 +117,7 @@ def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COE
         t.grad, t.m, t.w = grads[i].data_ptr(), m[i].data_ptr(), w.data_ptr()
         t.w16 = None if copies[i] is None else copies[i].data_ptr()
         t.weight_decay, t.grad_type = decay[i], B.TYPE["bf16" if low else "fp32"]
-    _apart(weights + m + copies, grads)
+    _apart([_span(t, True) for t in weights + m + copies if t is not None] + [_span(t, False) for t in grads])
     return Plan(weights, grads, copies, m, table, *_allocate(table, n, workspace, device),
                 _hyper(0.0, 0.0, 0.0, True, coefficients), device)
 
@@ -148,13 +152,17 @@ def orthogonalize(xs, outs, w: Workspace, stream=None):
     B.check_device(w.device, stream)
     if len(xs) != len(w.shapes) or len(outs) != len(w.shapes):
         raise ValueError(f"expected {len(w.shapes)} tensors, got {len(xs)} and {len(outs)}")
+    spans = []
     for t, s, x, o in zip(w.table, w.shapes, xs, outs):
         kind = [torch.bfloat16 if y.dtype == torch.bfloat16 else torch.float32 for y in (x, o)]
         B.check_tensor(x, kind[0], s, w.device)
         B.check_tensor(o, kind[1], s, w.device)
         t.grad, t.out = x.data_ptr(), o.data_ptr()
         t.grad_type, t.out_type = (B.TYPE["bf16" if k == torch.bfloat16 else "fp32"] for k in kind)
-    _apart(outs, [x for x, o in zip(xs, outs) if x.data_ptr() != o.data_ptr() or x.dtype != o.dtype])
+        spans.append(_span(o, True))
+        if t.grad != t.out or t.grad_type != t.out_type:
+            spans.append(_span(x, False))
+    _apart(spans)
     B.moe_muon_step(w.hyper, w.table, len(xs), w.workspace, w.workspace.numel(), None, w.status, stream)
     return outs
 
