@@ -12,8 +12,9 @@
 // tensor-memory reads 256, the multiply-adds 256 (column scales: 512), operands 48 KB.
 // Measured, 32768 rows over 32 experts, 4096 x 7168: 719 us where they are equal (2.68 PFLOP/s; 562 with operands that are
 // already there, 708 with codes of 0 at a higher clock: operands from L2, 52 bytes a cycle and SM, and the way of a block
-// through two buffers bound, under the power limit), 822 where they are skewed.  Weight gradients, 7168 x 2048: 585 us,
-// by the column scales' multiply-adds.  (CTA pairs with 32 KB of operands a block: 675 and 831 us, as odd numbers of
+// through two buffers bound, under the power limit), 822 to 850 where they are skewed.  Weight gradients, 7168 x 2048: 585
+// to 600 us, about 1400 cycles a block where the MMA and the multiply-adds take 512 each and nothing is full (tensor
+// pipe 37 %, issue 47 %): a chunk's load from tensor memory, the wait for it and its arithmetic follow one another.  (CTA pairs with 32 KB of operands a block: 675 and 831 us, as odd numbers of
 // 128-row tiles leave half a pair idle.)
 //
 // Schedules and tile order are those of the other grouped products (gemm.cuh): SCHED_ROWS

@@ -1,8 +1,9 @@
 // The quantiser of the 8-bit products with blocks of 128: bf16 rows to E4M3 codes with fp32
 // scales, blocks along rows, down columns (codes transposed, the operand of weight gradients)
 // or square (weights); and the SwiGLU between the experts' two products, quantised as it is
-// computed.  The row forms and the weights are bound by memory (SwiGLU of 131072 rows of 768: 98 us,
-// 5.1 TB/s; 128 x 1536 x 2048 weights both ways: 291 us, 5.5 TB/s), the column forms by instruction issue.
+// computed.  The row forms and the weights are bound by memory (SwiGLU of 131072 rows of 768: 93 us,
+// 5.4 TB/s; 128 x 1536 x 2048 weights both ways: 291 us, 5.5 TB/s); the column forms fill neither memory nor
+// the issue slots: a tile's steps follow one another.
 #include "fp8.cuh"
 #include "kernels.h"
 
@@ -114,8 +115,9 @@ struct F8Tiles {
 
 // 128 x 128 tiles, three persistent blocks an SM; a tile's rows are asked for (cp.async) as soon as the codes of the
 // one before have left its buffer.  A thread takes 32 rows of two columns and 64 columns of one row,
-// first for the maxima, then for the codes, which are assembled in shared memory and leave as whole lines.  Bound by
-// instruction issue (16384 x 7168, both forms: 94 us, 60 % of the issue slots, 5.06 TB/s).  SQUARE: one scale a tile.
+// first for the maxima, then for the codes, which are assembled in shared memory and leave as whole lines.  16384 x 7168,
+// both forms: 94 us, 5.06 TB/s (75 % of a copy) and 60 % of the issue slots; three blocks an SM cover each other's barriers and
+// loads, but not all of them.  SQUARE: one scale a tile.
 template <bool SQUARE>
 __global__ void __launch_bounds__(256, 3) f8_tiles_kernel(const F8Tiles p) {
   extern __shared__ __align__(16) uint8_t sm[];
@@ -284,9 +286,10 @@ static cudaError_t launch_f8_tiles(const F8Tiles& p, cudaStream_t s) {
 
 // ------------------------------------------------------------------------ SwiGLU
 
-// The sigmoid of a gate: a fast exponential and an approximate reciprocal, good to 2^-20 of silu(g) and cheaper than the
-// exact ones, which three bits of a code would not show.  The forward and the gradient compute silu(g) = g sigmoid(g)
-// and h = (w silu(g)) u with these operations in this order, so that both quantise the same numbers.
+// The sigmoid of a gate: a fast exponential and an approximate reciprocal.  The exponential is off by 2 + 1.2 |g| units
+// in the last place: 2^-19 of silu(g) at g = -12, 2^-16 at -88, where half a step of a code is 2^-4.  The forward and the
+// gradient compute silu(g) = g sigmoid(g) and h = (w silu(g)) u with these operations in this order, so that both quantise the
+// same numbers.
 __device__ __forceinline__ float f8_sigmoid(float g) { return rcp_fast(1.0f + __expf(-g)); }
 
 // h = w silu(G) U of gu [rows][2f], a block of 128 columns of h on 16 lanes, quantised.
@@ -341,7 +344,8 @@ __global__ void __launch_bounds__(256) f8_swiglu_kernel(const uint16_t* gu, cons
 // quantised.  A thread holds dG, dU and h of four rows and eight columns in registers, so that nothing is computed
 // twice.  A row's block is on 16 lanes, as in the forward; columns take their maxima through shared memory and their
 // codes leave through transposing tiles whose four-byte units are permuted so that neither side has bank conflicts.
-// 131072 rows of 768: 335 us, 3.3 TB/s; bound by instruction issue and the four barriers of a tile.  (A pass for each
+// 131072 rows of 768: 332 us, 3.3 TB/s.  Bound by latency: the one block of an SM stands still at each of a tile's four
+// barriers (issue slots 50 %, DRAM 35 %).  (A pass for each
 // of the three, with its sigmoids and the next tile's operands in registers: 653 us.)
 struct F8SwigluBwd {
   const uint16_t *gu, *dh;    // [rows][2f], [rows][f]

@@ -1,24 +1,24 @@
 // An update orthogonalised by Newton-Schulz products, for batches of matrices.
 //
-//   X_0 = U / |U|_F;   A = X X^T;  B = b A + c A A;  X' = a X + B X      (a, b, c of each step)
+//   X_0 = U / max(|U|_F, floor);   A = X X^T;  B = b A + c A A;  X' = a X + B X      (a, b, c of each step)
 //
 // on the side with fewer rows: X is [s][l], s <= l, in the workspace, transposed where the
 // tensor is tall, and padded with zeros to multiples of 128 (which the products keep at zero).
 //
 // Arithmetic: the products run on fp16 operands with fp32 sums.  Every matrix here is bounded (singular
-// values below 1.3), so fp16's 11 bits serve better than bf16's 8: on gaussian matrices the result is
-// 1.3e-3 off (bf16 operands: 1.1e-2).  X is held times a power of two near sqrt(l), so that its entries stay
-// normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
+// values below 1.3), so fp16's 11 bits serve better than bf16's 8: on gaussian matrices with
+// 128 rows or more the result is 0.8e-3 to 1.2e-3 off, relative to its norm (bf16 operands: 1.1e-2); with fewer, up to
+// 3e-3, and up to 8e-3 below 16.  X is held times a power of two near sqrt(l), so that its entries stay normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
 // values, which later steps amplify by up to a each; X is therefore kept in two fp16 parts, the second
 // read for that addend alone (low-rank plus noise: 3.4e-3 off without it, 2.4e-4 with it).
 // In the last two steps X is near orthogonal, A near a multiple of I and B near a negative one; taking the
 // multiples off first, A' = A - u I and X' = (a - t) X + (B + t I) X with u = 1/2, t = a - 1, leaves fp16 less to
-// round (the same polynomial in other terms: 1.3e-3 -> 5.2e-4 on strong directions under noise).  (A second
+// round (the same polynomial in other terms: 1.3e-3 -> 5.2e-4 on strong directions under noise, 300 x 700).  (A second
 // part of A for its addend alone does not help: A's rounding in b A and in c A A partly cancels.)
 // A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
 //
 // Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.  48 matrices of 1536 x 4096, five
-// steps: 7.9 ms, of which the products 6.3 (64 % of the measured bf16 rate; operands from shared memory and the power
+// steps: 7.9 to 8.0 ms, of which the products 6.3 (64 % of the measured bf16 rate; operands from shared memory and the power
 // limit), the passes over momenta, weights and X 1.6.
 #include "around.cuh"
 #include "kernels.h"
@@ -427,8 +427,8 @@ __device__ __forceinline__ void ns_add_square(float (&s)[2], float u) {
   s[0] = fmaf(u, u, s[0]);
   s[1] = fmaf(t, t, s[1]);
 }
-// What takes U to X_0, over a norm of at least `floor`: times `up`, a power of two, then times `inv`. Zeros stay zeros; a sum that overflowed, or a NaN in it,
-// makes NaNs rather than a silent zero.
+// What takes U to X_0, over a norm of at least `floor`: times `up`, a power of two, then times `inv`. Zeros stay zeros; a
+// sum that overflowed, or a NaN in it, makes NaNs rather than a silent zero.
 struct NsNorm {
   float up, inv;
 };

@@ -574,8 +574,8 @@ moe_status moe_fp8_gemm(const uint8_t* a, const float* a_scales, int64_t rows, i
 
 /*
  * out[e][n][k] = sum over the rows r of expert e of dy(r, n) x(r, k), bf16 [E][N][K], from the
- * column forms dy_t [N][rows], x_t [K][rows] (rows % 128 == 0, K % 8 == 0).  row_offsets as
- * above; an expert without rows gets zeros.
+ * column forms dy_t [N][rows], x_t [K][rows] (rows % 128 == 0, K % 8 == 0; x_scales starts at
+ * 16 bytes, as codes and out do).  row_offsets as above; an expert without rows gets zeros.
  */
 moe_status moe_fp8_wgrad(const uint8_t* dy_t, const float* dy_scales, const uint8_t* x_t, const float* x_scales,
                          int64_t rows, int32_t N, int32_t K, int32_t E, const int32_t* row_offsets, moe_bf16* out,
@@ -593,8 +593,8 @@ moe_status moe_fp8_swiglu(const moe_bf16* gu, const float* w_rows, int64_t rows,
  * Its gradient: from dh bf16 [rows][f] (f % 128 == 0)
  *   dA = w dH;  dG = dA U silu'(G);  dU = dA silu(G);  dw[r] = sum_j silu(G) U dH
  * dG | dU to the row form (dgu_codes [rows][2f]) and the column form (dgu_codes_t [2f][R_t]),
- * h itself to the column form (h_codes_t [f][R_t]: the codes that moe_fp8_swiglu would have
- * given columns).  A row of weight 0 gives zeros to all three whatever it holds; its dw is as
+ * h itself to the column form (h_codes_t [f][R_t]: of the numbers that moe_fp8_swiglu quantises,
+ * to the last bit).  A row of weight 0 gives zeros to all three whatever it holds; its dw is as
  * above.  dw_rows [rows] fp32 and its scratch dw_part [rows][f / 128], or both NULL.
  */
 moe_status moe_fp8_swiglu_bwd(const moe_bf16* gu, const moe_bf16* dh, const float* w_rows, int64_t rows, int32_t f,
@@ -811,7 +811,9 @@ moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int3
  *   w = w - lr (weight_decay w + rms sqrt(max(rows, cols)) X);   w16 = bf16(w)
  * m, w and the sums of squares in fp32.  |U|_F is right for every U whose sum of squares does not
  * overflow, fp32's smallest numbers included; where it overflows (|U|_F from 2^64 on) X is NaN.
- * The products on fp16 operands with fp32 sums.  With `out` in place of m and w a tensor's
+ * The products on fp16 operands with fp32 sums.  With the coefficients 3.4445, -4.7750, 2.0315 five
+ * times X is off by less than 1.5e-3 of its norm where the shorter side is 128 or more, 4e-3 from 16
+ * on, 1e-2 below (gaussian matrices and strong directions under noise).  With `out` in place of m and w a tensor's
  * gradient itself is orthogonalised: out = X, m, w and w16 NULL (momentum, lr and rms are not used).
  * A gradient that is not finite reaches its whole matrix.
  */
