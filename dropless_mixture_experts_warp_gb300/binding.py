@@ -74,6 +74,7 @@ class moe_adamw_hyper(ctypes.Structure):
 
 
 MUON_MAX_STEPS = 16
+MUON_PRODUCTS = {"fp16": 0, "fp32": 1}
 
 
 class moe_muon_tensor(ctypes.Structure):
@@ -175,7 +176,8 @@ SIGNATURES = {
     "moe_adamw_step": (ctypes.c_int32, [ctypes.POINTER(moe_adamw_hyper), _T, _I, _P, _P]),
     "moe_adamw_values": (ctypes.c_int32, [_T, _I, _I, _PP, _PP, _P]),
     "moe_muon_workspace_size": (ctypes.c_size_t, [_U, _I, ctypes.c_size_t]),
-    "moe_muon_step_floor": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, ctypes.c_double, _P, ctypes.c_size_t, _P, _P, _P]),
+    "moe_muon_workspace_size_with": (ctypes.c_size_t, [_U, _I, ctypes.c_size_t, _I]),
+    "moe_muon_step_with": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, ctypes.c_double, _I, _P, ctypes.c_size_t, _P, _P, _P]),
     "moe_muon_step": (ctypes.c_int32, [ctypes.POINTER(moe_muon_hyper), _U, _I, _P, ctypes.c_size_t, _P, _P, _P]),
 }
 
@@ -645,10 +647,15 @@ def moe_muon_workspace_size(tensors, count, limit) -> int:
     return lib().moe_muon_workspace_size(tensors, count, limit)
 
 
-def moe_muon_step_floor(hyper, tensors, count, norm_floor, workspace, workspace_bytes, control=None, dev_status=None, stream=None):
-    """moe_muon_step() with norms of at least norm_floor."""
-    return _call("moe_muon_step_floor", None if hyper is None else ctypes.byref(hyper), tensors, count, norm_floor, _ptr(workspace),
-                 workspace_bytes, _ptr(control), _ptr(dev_status), _stream(stream))
+def moe_muon_workspace_size_with(tensors, count, limit, products) -> int:
+    return lib().moe_muon_workspace_size_with(tensors, count, limit, products)
+
+
+def moe_muon_step_with(hyper, tensors, count, norm_floor, products, workspace, workspace_bytes, control=None, dev_status=None,
+                       stream=None):
+    """moe_muon_step() with norms of at least norm_floor and products of MUON_PRODUCTS."""
+    return _call("moe_muon_step_with", None if hyper is None else ctypes.byref(hyper), tensors, count, norm_floor, products,
+                 _ptr(workspace), workspace_bytes, _ptr(control), _ptr(dev_status), _stream(stream))
 
 
 def moe_muon_step(hyper, tensors, count, workspace, workspace_bytes, control=None, dev_status=None, stream=None):

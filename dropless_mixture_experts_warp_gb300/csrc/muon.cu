@@ -5,12 +5,15 @@
 // on the side with fewer rows: X is [s][l], s <= l, in the workspace, transposed where the
 // tensor is tall, and padded with zeros to multiples of 128 (which the products keep at zero).
 //
-// Arithmetic: the products run on fp16 operands with fp32 sums.  Every matrix here is bounded (singular
-// values below 1.3), so fp16's 11 bits serve better than bf16's 8: on gaussian matrices with
-// 128 rows or more the result is 0.8e-3 to 1.2e-3 off, relative to its norm (bf16 operands: 1.1e-2); with fewer, up to
-// 3e-3, and up to 8e-3 below 16.  X is held times a power of two near sqrt(l), so that its entries stay normal numbers.  The addend a X would carry X's rounding past the products straight into the small singular
-// values, which later steps amplify by up to a each; X is therefore kept in two fp16 parts, the second
-// read for that addend alone (low-rank plus noise: 3.4e-3 off without it, 2.4e-4 with it).
+// Arithmetic: tensor-core products of fp16 operands with fp32 sums.  Every matrix here is bounded (singular
+// values below 1.3), so fp16's 11 bits serve better than bf16's 8.  The caller chooses between
+//   SPLIT: X, A and B each in two fp16 parts, 22 bits, and three products (lo hi + hi lo + hi hi) for each: what fp32
+//     products give (the roundings cost 3e-6 of the factor's norm at 1024 x 1024, less for smaller matrices);
+//   one part, a third of the multiplying: on gaussian matrices with 128 rows or more the result is 0.8e-3 to 1.2e-3 off,
+//     relative to its norm (bf16 operands: 1.1e-2); with fewer, up to 3e-3, and up to 8e-3 below 16.
+// X is held times a power of two near sqrt(l), so that its entries stay normal numbers.  The addend a X would carry X's
+// rounding past the products straight into the small singular values, which later steps amplify by up to a each; X is
+// therefore kept in two fp16 parts also where its products take one (low-rank plus noise: 3.4e-3 off without, 2.4e-4 with it).
 // In the last two steps X is near orthogonal, A near a multiple of I and B near a negative one; taking the
 // multiples off first, A' = A - u I and X' = (a - t) X + (B + t I) X with u = 1/2, t = a - 1, leaves fp16 less to
 // round (the same polynomial in other terms: 1.3e-3 -> 5.2e-4 on strong directions under noise, 300 x 700).  (A second
@@ -86,12 +89,17 @@ __device__ __forceinline__ NsTile ns_tile(const NsParams& p, int t) {
 // What the sum is added to arrives by tensor loads in a warp's boxes, a chunk of 32 columns ahead, across
 // tiles.  The MMA warp looks for two stages at a time: a wait's latency, 130 cycles, comes on top of the
 // 512 that a stage's MMAs take.
-template <int KIND>
+// SPLIT: the contraction runs three times into one sum, over A's second parts and B's first, A's first and B's second, and
+// both first; results leave in two parts.  The first parts come last: tensor-core sums lose up to a unit in the last place
+// at each step of 16, which counts for most where the sum is large.
+template <int KIND, bool SPLIT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
     ns_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                   const __grid_constant__ CUtensorMap tmALo, const __grid_constant__ CUtensorMap tmBLo,
                    const __grid_constant__ CUtensorMap tmIn, const __grid_constant__ CUtensorMap tmInLo,
                    const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmOutLo, const NsParams p) {
   constexpr bool B_MN = KIND == NS_APPLY;
+  constexpr bool TWO_IN = KIND == NS_APPLY || (SPLIT && KIND == NS_POLY);   // what is added is in two parts
   extern __shared__ uint8_t dyn_smem[];
   __shared__ __align__(8) uint64_t full_bar[NS_STAGES];
   __shared__ __align__(8) uint64_t empty_bar[NS_STAGES];
@@ -123,7 +131,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
   const uint32_t tmem_base = s_tmem_base;
   const int mt = (p.s + 255) / 256;
   const int total = p.batch * (KIND == NS_APPLY ? mt * ((p.n + 255) / 256) : mt * (mt + 1) / 2);
-  const int kblocks = p.k / BK;
+  const int kblocks = p.k / BK, all_kblocks = SPLIT ? 3 * kblocks : kblocks;
   volatile int* const aborted = &s_abort;
   const uint32_t leader = lane == 0;
 
@@ -136,8 +144,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       const int a_local = c.m * 256 + rank * 128, b_local = c.n * 256 + rank * 128;
       const int a_row = a_local < p.s ? c.e * p.s + a_local : DEAD_ROW;
       const int b_row = b_local < p.n ? c.e * p.s + b_local : DEAD_ROW;
+      int part = 0, kb = 0;
 #pragma unroll 1
-      for (int kb = 0; kb < kblocks; ++kb) {
+      for (int i = 0; i < all_kblocks; ++i) {
+        const CUtensorMap* ma = SPLIT && part == 0 ? &tmALo : &tmA;
+        const CUtensorMap* mb = SPLIT && part == 1 ? &tmBLo : &tmB;
         pipe_wait(&empty_bar[stage], phase ^ 1, &s_abort, p.status);
         uint8_t* sa = smem + stage * P_STAGE_BYTES;
         uint8_t* sb = sa + P_A_BYTES;
@@ -145,13 +156,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
         pipe_expect(&full_bar[stage], 2 * P_STAGE_BYTES, leader && rank == 0);
         armed |= 1u << stage;
         armed_parity = (armed_parity & ~(1u << stage)) | (phase << stage);
-        pipe_load_2d_pair(sa, &tmA, bar, kb * BK, a_row, leader);
+        pipe_load_2d_pair(sa, ma, bar, kb * BK, a_row, leader);
         if (!B_MN) {
-          pipe_load_2d_pair(sb, &tmB, bar, kb * BK, b_row, leader);
+          pipe_load_2d_pair(sb, mb, bar, kb * BK, b_row, leader);
         } else {
-          pipe_load_2d_pair(sb, &tmB, bar, b_local, c.e * p.s + kb * BK, leader);
-          pipe_load_2d_pair(sb + 8192, &tmB, bar, b_local + 64, c.e * p.s + kb * BK, leader);
+          pipe_load_2d_pair(sb, mb, bar, b_local, c.e * p.s + kb * BK, leader);
+          pipe_load_2d_pair(sb + 8192, mb, bar, b_local + 64, c.e * p.s + kb * BK, leader);
         }
+        if (++kb == kblocks) { kb = 0; ++part; }
         if (++stage == NS_STAGES) { stage = 0; phase ^= 1; }
       }
     }
@@ -171,7 +183,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + acc * ACC_STRIDE;
 #pragma unroll 1
-        for (int kb = 0; kb < kblocks; kb += 2) {    // the contraction is a multiple of 128
+        for (int kb = 0; kb < all_kblocks; kb += 2) {    // the contraction is a multiple of 128
           const int next = stage + 1 == NS_STAGES ? 0 : stage + 1;
           pipe_wait_two(&full_bar[stage], phase, &full_bar[next], phase ^ (next == 0), &s_abort, p.status);
           tc_fence_after();
@@ -226,9 +238,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
       if (KIND == NS_GRAM || ask_t >= total) return;
       const int x = ask.col0 + 32 * ask_i;
       if (lane == 0) fence_proxy_async_smem();
-      pipe_expect(ibar, KIND == NS_APPLY ? 2 * NS_BOX : NS_BOX, leader);
+      pipe_expect(ibar, TWO_IN ? 2 * NS_BOX : NS_BOX, leader);
       pipe_load_2d(in, &tmIn, ibar, x, ask.y, leader);
-      if (KIND == NS_APPLY) pipe_load_2d(in + NS_BOX, &tmInLo, ibar, x, ask.y, leader);
+      if (TWO_IN) pipe_load_2d(in + NS_BOX, &tmInLo, ibar, x, ask.y, leader);
       ++asked;
       if (++ask_i == 4) {
         ask_i = 0;
@@ -259,7 +271,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               const uint4 x = ld_shared_v4(in_row + ((v ^ sw) << 4));
-              const uint4 z = KIND == NS_APPLY ? ld_shared_v4(in_row + NS_BOX + ((v ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
+              const uint4 z = TWO_IN ? ld_shared_v4(in_row + NS_BOX + ((v ^ sw) << 4)) : make_uint4(0, 0, 0, 0);
               hi[4 * v] = x.x; hi[4 * v + 1] = x.y; hi[4 * v + 2] = x.z; hi[4 * v + 3] = x.w;
               lo[4 * v] = z.x; lo[4 * v + 1] = z.y; lo[4 * v + 2] = z.z; lo[4 * v + 3] = z.w;
             }
@@ -282,38 +294,43 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(NS_THREADS, 1)
               b = fmaf(p.beta, x.y + z.y, b);
             }
             oh[j] = pack_half(a, b);
-            if (KIND == NS_APPLY) {
+            if (KIND == NS_APPLY || SPLIT) {
               const float2 h = half_pair(oh[j]);
               ol[j] = pack_half(a - h.x, b - h.y);
             }
           }
-          if (lane == 0) bulk_wait_read<0>();
-          __syncwarp();
-#pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            st_shared_v4(out_row + ((v ^ sw) << 4), oh[4 * v], oh[4 * v + 1], oh[4 * v + 2], oh[4 * v + 3]);
-            if (KIND == NS_APPLY && p.lo_out)
-              st_shared_v4(out_row + NS_BOX + ((v ^ sw) << 4), ol[4 * v], ol[4 * v + 1], ol[4 * v + 2], ol[4 * v + 3]);
-          }
           const bool mirror = KIND != NS_APPLY && c.n > c.m;
-          if (mirror) {
-            // the box's transpose: two rows' values of a column meet in one word
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              const uint32_t other = __shfl_xor_sync(0xffffffffu, oh[j], 1);
-              // even lanes take column 2j of rows (lane, lane + 1), odd ones column 2j + 1 of (lane - 1, lane)
-              const uint32_t w = lane & 1 ? __byte_perm(other, oh[j], 0x7632) : __byte_perm(oh[j], other, 0x5410);
-              const int col = 2 * j + (lane & 1);
-              *reinterpret_cast<uint32_t*>(out + NS_BOX + col * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) = w;
+          for (int part = 0; part < (SPLIT && KIND != NS_APPLY ? 2 : 1); ++part) {   // A and B in two parts: one after the other
+            uint32_t(&o)[16] = part == 0 ? oh : ol;
+            if (lane == 0) bulk_wait_read<0>();
+            __syncwarp();
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              st_shared_v4(out_row + ((v ^ sw) << 4), o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+              if (KIND == NS_APPLY && p.lo_out)
+                st_shared_v4(out_row + NS_BOX + ((v ^ sw) << 4), ol[4 * v], ol[4 * v + 1], ol[4 * v + 2], ol[4 * v + 3]);
             }
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) {
-            tma_store_2d(&tmOut, out, col0 + 32 * i, y);
-            if (KIND == NS_APPLY && p.lo_out) tma_store_2d(&tmOutLo, out + NS_BOX, col0 + 32 * i, y);
-            if (mirror) tma_store_2d(&tmOut, out + NS_BOX, row0, c.e * p.s + col0 + 32 * i);
-            bulk_commit();
+            if (mirror) {
+              // the box's transpose: two rows' values of a column meet in one word
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, o[j], 1);
+                // even lanes take column 2j of rows (lane, lane + 1), odd ones column 2j + 1 of (lane - 1, lane)
+                const uint32_t w = lane & 1 ? __byte_perm(other, o[j], 0x7632) : __byte_perm(o[j], other, 0x5410);
+                const int col = 2 * j + (lane & 1);
+                *reinterpret_cast<uint32_t*>(out + NS_BOX + col * 64 + (((lane >> 3) ^ ((col >> 1) & 3)) << 4) + ((lane >> 1) & 3) * 4) = w;
+              }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              const CUtensorMap* to = part == 0 ? &tmOut : &tmOutLo;
+              tma_store_2d(to, out, col0 + 32 * i, y);
+              if (KIND == NS_APPLY && p.lo_out) tma_store_2d(&tmOutLo, out + NS_BOX, col0 + 32 * i, y);
+              if (mirror) tma_store_2d(to, out + NS_BOX, row0, c.e * p.s + col0 + 32 * i);
+              bulk_commit();
+            }
           }
         }
       }
@@ -542,10 +559,10 @@ __global__ void __launch_bounds__(256) ns_load_kernel(const NsTensors p, const f
   }
 }
 
-// w = w - lr (decay w + rms sqrt(max side) X), or out = X.
+// w = w - lr (decay w + rms sqrt(max side) X), or out = X; lo: X's second part, or NULL.
 template <bool TALL>
-__global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const __half* x, int s, int l, float unscale, float lr,
-                                                        float rms) {
+__global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const __half* x, const __half* lo, int s, int l, float unscale,
+                                                        float lr, float rms) {
   wait_for_previous();
   launch_dependents();
   __shared__ float tile[TALL ? 64 * NS_LD : 1];
@@ -559,12 +576,13 @@ __global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const
   for (int k = 0; k < 2; ++k) {                                  // X's padding holds whole tiles
     const long long at = (static_cast<long long>(e) * s + (TALL ? x0 : y0) + r + 32 * k) * l + (TALL ? y0 : x0) + c;
     const uint4 h = *reinterpret_cast<const uint4*>(x + at);
-    const uint32_t u[4] = {h.x, h.y, h.z, h.w};
+    const uint4 g = lo ? *reinterpret_cast<const uint4*>(lo + at) : make_uint4(0, 0, 0, 0);
+    const uint32_t u[4] = {h.x, h.y, h.z, h.w}, d[4] = {g.x, g.y, g.z, g.w};
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float2 f = half_pair(u[j]);
-      v[k][2 * j] = unscale * f.x;
-      v[k][2 * j + 1] = unscale * f.y;
+      const float2 f = half_pair(u[j]), z = lo ? half_pair(d[j]) : make_float2(0.0f, 0.0f);
+      v[k][2 * j] = unscale * (f.x + z.x);
+      v[k][2 * j + 1] = unscale * (f.y + z.y);
     }
   }
   ns_turn<TALL>(v, tile, r, c);
@@ -598,9 +616,11 @@ __global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const
 // K-major in X X^T and MN-major in B X.
 
 constexpr int SM_BLOCK = 128 * 128;                  // bytes of 128 rows x 64 columns
-// X, A and B lie where X's fp32 form was before them and is after.
-__host__ __device__ constexpr int small_smem(int l) {
-  return (128 * (l + 1) * 4 > (l / 64 + 4) * SM_BLOCK ? 128 * (l + 1) * 4 : (l / 64 + 4) * SM_BLOCK) + 1024;
+// X, A and B lie where X's fp32 form was before them and is after.  SPLIT: two parts of X, then two of A, which B's
+// take the place of.
+__host__ __device__ constexpr int small_smem(int l, bool split) {
+  const int stage = 128 * (l + 1) * 4, operands = (split ? 2 * (l / 64) + 4 : l / 64 + 4) * SM_BLOCK;
+  return (stage > operands ? stage : operands) + 1024;
 }
 
 __device__ __forceinline__ void small_put(uint32_t block0, int row, int col, const float* v) {   // eight columns
@@ -608,7 +628,21 @@ __device__ __forceinline__ void small_put(uint32_t block0, int row, int col, con
   st_shared_v4(at, pack_half(v[0], v[1]), pack_half(v[2], v[3]), pack_half(v[4], v[5]), pack_half(v[6], v[7]));
 }
 
-template <int L>
+// The same in two fp16 parts.
+__device__ __forceinline__ void small_put_split(uint32_t hi0, uint32_t lo0, int row, int col, const float* v) {
+  const uint32_t at = (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+  uint32_t h[4], d[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    h[j] = pack_half(v[2 * j], v[2 * j + 1]);
+    const float2 f = half_pair(h[j]);
+    d[j] = pack_half(v[2 * j] - f.x, v[2 * j + 1] - f.y);
+  }
+  st_shared_v4(hi0 + at, h[0], h[1], h[2], h[3]);
+  st_shared_v4(lo0 + at, d[0], d[1], d[2], d[3]);
+}
+
+template <int L, bool SPLIT>
 __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, const NsSteps h, float scale, float floor, float lr, float rms,
                                                           int32_t* status) {
   constexpr int HALF = L / 2;                        // X's columns of a thread
@@ -685,7 +719,9 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
   for (int j = 0; j < HALF; ++j) x[j] = stage[row * (L + 1) + col0 + j] * norm.up * norm.inv;
   __syncthreads();
 
-  const uint32_t sx = smem_u32(smem), sa = sx + (L / 64) * SM_BLOCK, sb = sa + 2 * SM_BLOCK;
+  const uint32_t sx = smem_u32(smem), sx_lo = sx + (L / 64) * SM_BLOCK, sa = sx_lo + (SPLIT ? (L / 64) * SM_BLOCK : 0), sa_lo = sa + 2 * SM_BLOCK;
+  const uint32_t sb = SPLIT ? sa : sa_lo, sb_lo = sa_lo;   // one part: A's second place is B's
+  constexpr int PART0 = SPLIT ? 0 : 2;               // lo hi, hi lo, hi hi
   const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
   // steps of 16 that the matrix's own rows and columns reach; what lies past them is not multiplied, and what
   // tensor memory and X's registers hold there is not used
@@ -709,15 +745,21 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
     const NsStep q = h.s[k];
 #pragma unroll
     for (int j = 0; j < HALF; j += 8)
-      if (col0 + j < 16 * kl) small_put(sx, row, col0 + j, x + j);
+      if (col0 + j < 16 * kl) {
+        if (SPLIT) small_put_split(sx, sx_lo, row, col0 + j, x + j);
+        else small_put(sx, row, col0 + j, x + j);
+      }
     hand();
     if (tid == 0) {                                  // A = X X^T
 #pragma unroll
-      for (int kk = 0; kk < L / 16; ++kk) {
-        if (kk >= kl) break;
-        const uint64_t d = smem_desc_sw128(sx + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
-        tc_mma_f16(tmem, d, d, idesc_fp16(128, 128, 0), kk != 0);
-      }
+      for (int part = PART0; part < 3; ++part)
+#pragma unroll
+        for (int kk = 0; kk < L / 16; ++kk) {
+          if (kk >= kl) break;
+          const uint32_t at = (kk >> 2) * SM_BLOCK + (kk & 3) * 32;
+          tc_mma_f16(tmem, smem_desc_sw128((part == 0 ? sx_lo : sx) + at, 16, 1024), smem_desc_sw128((part == 1 ? sx_lo : sx) + at, 16, 1024),
+                     idesc_fp16(128, 128, 0), part != PART0 || kk != 0);
+        }
       tc_commit(&bar);
     }
     __syncwarp();
@@ -733,16 +775,22 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = __uint_as_float(r[j]) * (1.0f / (scale * scale)) - (row == ac + 32 * i + j ? q.u : 0.0f);
 #pragma unroll
-      for (int j = 0; j < 32; j += 8) small_put(sa, row, ac + 32 * i + j, v + j);
+      for (int j = 0; j < 32; j += 8) {
+        if (SPLIT) small_put_split(sa, sa_lo, row, ac + 32 * i + j, v + j);
+        else small_put(sa, row, ac + 32 * i + j, v + j);
+      }
     }
     hand();
     if (tid == 0) {                                  // A A
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        if (kk >= ks) break;
-        const uint64_t d = smem_desc_sw128(sa + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024);
-        tc_mma_f16(tmem + 128, d, d, idesc_fp16(128, 128, 0), kk != 0);
-      }
+      for (int part = PART0; part < 3; ++part)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          if (kk >= ks) break;
+          const uint32_t at = (kk >> 2) * SM_BLOCK + (kk & 3) * 32;
+          tc_mma_f16(tmem + 128, smem_desc_sw128((part == 0 ? sa_lo : sa) + at, 16, 1024), smem_desc_sw128((part == 1 ? sa_lo : sa) + at, 16, 1024),
+                     idesc_fp16(128, 128, 0), part != PART0 || kk != 0);
+        }
       tc_commit(&bar);
     }
     __syncwarp();
@@ -756,26 +804,35 @@ __global__ void __launch_bounds__(256, 1) ns_small_kernel(const NsTensors p, con
 #pragma unroll
       for (int j = 0; j < 32; j += 8) {
         const int col = ac + 32 * i + j;
-        const uint4 w = ld_shared_v4(sa + (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4));
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        const uint32_t at = (col >> 6) * SM_BLOCK + row * 128 + ((((col & 63) >> 3) ^ (row & 7)) << 4);
+        const uint4 w = ld_shared_v4(sa + at), z = SPLIT ? ld_shared_v4(sa_lo + at) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {w.x, w.y, w.z, w.w}, d[4] = {z.x, z.y, z.z, z.w};
         float v[8];
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const float2 f = half_pair(u[t]);
+          float2 f = half_pair(u[t]);
+          if (SPLIT) {
+            const float2 g = half_pair(d[t]);
+            f.x += g.x;
+            f.y += g.y;
+          }
           v[2 * t] = fmaf(q.b, f.x, q.c * __uint_as_float(r[j + 2 * t])) + (row == col + 2 * t ? q.d : 0.0f);
           v[2 * t + 1] = fmaf(q.b, f.y, q.c * __uint_as_float(r[j + 2 * t + 1])) + (row == col + 2 * t + 1 ? q.d : 0.0f);
         }
-        small_put(sb, row, col, v);
+        if (SPLIT) small_put_split(sb, sb_lo, row, col, v);   // over the elements of A that this thread alone reads
+        else small_put(sb, row, col, v);
       }
     }
     hand();
     if (tid == 0) {                                  // B X
 #pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        if (kk >= ks) break;
-        tc_mma_f16(tmem + 256, smem_desc_sw128(sb + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024),
-                   smem_desc_sw128(sx + kk * 2048, SM_BLOCK, 1024), idesc_fp16(128, 16 * kl, 1), kk != 0);
-      }
+      for (int part = PART0; part < 3; ++part)
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          if (kk >= ks) break;
+          tc_mma_f16(tmem + 256, smem_desc_sw128((part == 0 ? sb_lo : sb) + (kk >> 2) * SM_BLOCK + (kk & 3) * 32, 16, 1024),
+                     smem_desc_sw128((part == 1 ? sx_lo : sx) + kk * 2048, SM_BLOCK, 1024), idesc_fp16(128, 16 * kl, 1), part != PART0 || kk != 0);
+        }
       tc_commit(&bar);
     }
     __syncwarp();
@@ -837,20 +894,44 @@ static NsShape ns_shape(int rows, int cols) {
   o.a = static_cast<size_t>(o.s) * o.s * 2;
   return o;
 }
-// X twice (a step reads one and writes the other), its second part, A, B, the partial sums
-static size_t ns_matrix_bytes(const NsShape& o) { return 3 * o.x + 2 * o.a + 2 * NS_PARTS * sizeof(float); }
+// X twice (a step reads one and writes the other), its second part, A, B, the partial sums; split: the second parts of
+// both X, of A and of B
+static size_t ns_matrix_bytes(const NsShape& o, bool split) {
+  return (split ? 4 * o.x + 4 * o.a : 3 * o.x + 2 * o.a) + 2 * NS_PARTS * sizeof(float);
+}
 
-template <int KIND>
-static cudaError_t launch_ns(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& in, const CUtensorMap& in_lo,
-                             const CUtensorMap& out, const CUtensorMap& out_lo, const NsParams& p, cudaStream_t s) {
-  auto kern = ns_gemm_kernel<KIND>;
-  const cudaError_t err = allow_smem<ns_gemm_kernel<KIND>>(NS_SMEM);
+// A matrix in the workspace and its second part, as operands (K-major, MN-major) and in 32 x 32 boxes.
+struct NsMaps {
+  CUtensorMap k[2], n[2], box[2];
+};
+static bool ns_maps(NsMaps& m, const void* hi, const void* lo, uint64_t cols, uint64_t rows) {
+  for (int i = 0; i < 2; ++i) {
+    const void* at = i == 0 ? hi : lo;
+    if (!make_tensor_map_bf16(&m.k[i], at, cols, rows, 64, 128) || !make_tensor_map_bf16(&m.n[i], at, cols, rows, 64, 64) ||
+        !make_tensor_map_store(&m.box[i], at, cols, cols, rows))
+      return false;
+  }
+  return true;
+}
+
+template <int KIND, bool SPLIT>
+static cudaError_t launch_ns(const CUtensorMap (&a)[2], const CUtensorMap (&b)[2], const NsMaps& in, const NsMaps& out, const NsParams& p,
+                             cudaStream_t s) {
+  auto kern = ns_gemm_kernel<KIND, SPLIT>;
+  const cudaError_t err = allow_smem<ns_gemm_kernel<KIND, SPLIT>>(NS_SMEM);
   if (err != cudaSuccess) return err;
   static const int most = pair_grid(reinterpret_cast<const void*>(kern), NS_THREADS, NS_SMEM);
   const int mt = (p.s + 255) / 256;
   const long long tiles = static_cast<long long>(p.batch) * (KIND == NS_APPLY ? mt * ((p.n + 255) / 256) : mt * (mt + 1) / 2);
   const int grid = static_cast<int>(2 * tiles < most ? 2 * tiles : most);
-  return launch_early(kern, dim3(grid), dim3(NS_THREADS), NS_SMEM, s, a, b, in, in_lo, out, out_lo, p);
+  return launch_early(kern, dim3(grid), dim3(NS_THREADS), NS_SMEM, s, a[0], b[0], a[1], b[1], in.box[0], in.box[1], out.box[0], out.box[1], p);
+}
+template <int L, bool SPLIT>
+static cudaError_t launch_small(const NsTensors& t, int batch, const NsSteps& steps, float scale, float floor, float lr, float rms,
+                                int32_t* status, cudaStream_t st) {
+  const cudaError_t err = allow_smem<ns_small_kernel<L, SPLIT>>(small_smem(L, SPLIT));
+  if (err != cudaSuccess) return err;
+  return launch_early(ns_small_kernel<L, SPLIT>, dim3(batch), dim3(256), small_smem(L, SPLIT), st, t, steps, scale, floor, lr, rms, status);
 }
 
 // What X is multiplied by in an update.
@@ -859,15 +940,25 @@ static float ns_rms(const moe_muon_hyper& h, int rows, int cols) {
 }
 
 // `batch` matrices of one shape: products, update.
+template <bool SPLIT>
 static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, float floor, float lr, void* workspace, int32_t* status,
                             cudaStream_t st) {
   const NsShape o = ns_shape(t.rows, t.cols);
   uint8_t* w = static_cast<uint8_t*>(workspace);
-  __half* x[2] = {reinterpret_cast<__half*>(w), reinterpret_cast<__half*>(w + batch * o.x)};
-  __half* lo = reinterpret_cast<__half*>(w + 2 * batch * o.x);
-  uint8_t* A = w + 3 * batch * o.x;
-  uint8_t* B = A + batch * o.a;
-  float* parts = reinterpret_cast<float*>(B + batch * o.a);
+  const auto take = [&](size_t bytes) {
+    uint8_t* at = w;
+    w += batch * bytes;
+    return at;
+  };
+  // X's second part is an operand where it is split, so that a step may not write over it; A and B have none otherwise
+  uint8_t* const x[2] = {take(o.x), take(o.x)};
+  uint8_t* const lo0 = take(o.x);
+  uint8_t* const lo[2] = {lo0, SPLIT ? take(o.x) : lo0};
+  uint8_t* const A = take(o.a);
+  uint8_t* const B = take(o.a);
+  uint8_t* const A_lo = SPLIT ? take(o.a) : A;
+  uint8_t* const B_lo = SPLIT ? take(o.a) : B;
+  float* parts = reinterpret_cast<float*>(w);
   const long long n = static_cast<long long>(t.rows) * t.cols;
   const int nparts = static_cast<int>(std::min<long long>(NS_PARTS, (n + 2047) / 2048));
   float scale = 1.0f;
@@ -875,13 +966,9 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   const bool tall = t.rows > t.cols;
   const NsSteps steps = ns_steps(h);
   const float rms = ns_rms(h, t.rows, t.cols);
-  if (o.s == 128 && o.l <= 256) {
-    const int smem = small_smem(o.l);
-    const cudaError_t err = o.l == 128 ? allow_smem<ns_small_kernel<128>>(smem) : allow_smem<ns_small_kernel<256>>(smem);
-    if (err != cudaSuccess) return err;
-    return o.l == 128 ? launch_early(ns_small_kernel<128>, dim3(batch), dim3(256), smem, st, t, steps, scale, floor, lr, rms, status)
-                      : launch_early(ns_small_kernel<256>, dim3(batch), dim3(256), smem, st, t, steps, scale, floor, lr, rms, status);
-  }
+  if (o.s == 128 && o.l <= 256)
+    return o.l == 128 ? launch_small<128, SPLIT>(t, batch, steps, scale, floor, lr, rms, status, st)
+                      : launch_small<256, SPLIT>(t, batch, steps, scale, floor, lr, rms, status, st);
   t.vec = 1;
   for (int i = 0; i < t.count; ++i)
     for (const void* q : {t.grad[i], static_cast<const void*>(t.m[i]), static_cast<const void*>(t.w[i]), static_cast<const void*>(t.w16[i]),
@@ -890,34 +977,32 @@ static cudaError_t ns_chunk(NsTensors& t, int batch, const moe_muon_hyper& h, fl
   cudaError_t err = launch_early(ns_momentum_kernel, dim3(nparts, batch), dim3(256), 0, st, t, parts);
   if (err != cudaSuccess) return err;
   const dim3 tiles_x(o.l / 64, o.s / 64, batch), tiles_t((t.cols + 63) / 64, (t.rows + 63) / 64, batch);
-  err = tall ? launch_early(ns_load_kernel<true>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, floor, x[0], lo)
-             : launch_early(ns_load_kernel<false>, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, floor, x[0], lo);
+  const auto load = tall ? ns_load_kernel<true> : ns_load_kernel<false>;
+  err = launch_early(load, tiles_x, dim3(256), 0, st, t, parts, nparts, o.s, o.l, scale, floor, reinterpret_cast<__half*>(x[0]),
+                     reinterpret_cast<__half*>(lo[0]));
   if (err != cudaSuccess) return err;
   const uint64_t rows = static_cast<uint64_t>(batch) * o.s;
-  CUtensorMap xk[2], xn[2], xs[2], los, ak, as, bk, bs;
-  bool ok = make_tensor_map_store(&los, lo, o.l, o.l, rows) && make_tensor_map_bf16(&ak, A, o.s, rows, 64, 128) &&
-            make_tensor_map_store(&as, A, o.s, o.s, rows) && make_tensor_map_bf16(&bk, B, o.s, rows, 64, 128) &&
-            make_tensor_map_store(&bs, B, o.s, o.s, rows);
-  for (int i = 0; i < 2; ++i)
-    ok = ok && make_tensor_map_bf16(&xk[i], x[i], o.l, rows, 64, 128) && make_tensor_map_bf16(&xn[i], x[i], o.l, rows, 64, 64) &&
-         make_tensor_map_store(&xs[i], x[i], o.l, o.l, rows);
-  if (!ok) return cudaErrorInvalidValue;
+  NsMaps mx[2], ma, mb;
+  if (!ns_maps(mx[0], x[0], lo[0], o.l, rows) || !ns_maps(mx[1], x[1], lo[1], o.l, rows) || !ns_maps(ma, A, A_lo, o.s, rows) ||
+      !ns_maps(mb, B, B_lo, o.s, rows))
+    return cudaErrorInvalidValue;
   int cur = 0;
   for (int k = 0; k < h.steps; ++k, cur ^= 1) {
     const NsStep& q = steps.s[k];
     NsParams p{batch, o.s, o.s, o.l, 1.0f / (scale * scale), 0.0f, -q.u, 0, status};
-    err = launch_ns<NS_GRAM>(xk[cur], xk[cur], as, as, as, as, p, st);
+    err = launch_ns<NS_GRAM, SPLIT>(mx[cur].k, mx[cur].k, ma, ma, p, st);
     if (err != cudaSuccess) return err;
     p.k = o.s; p.alpha = q.c; p.beta = q.b; p.diag = q.d;
-    err = launch_ns<NS_POLY>(ak, ak, as, as, bs, bs, p, st);
+    err = launch_ns<NS_POLY, SPLIT>(ma.k, ma.k, ma, mb, p, st);
     if (err != cudaSuccess) return err;
     p.n = o.l; p.alpha = 1.0f; p.beta = q.a;
-    p.lo_out = k + 1 < h.steps;
-    err = launch_ns<NS_APPLY>(bk, xn[cur], xs[cur], los, xs[cur ^ 1], los, p, st);
+    p.lo_out = SPLIT || k + 1 < h.steps;
+    err = launch_ns<NS_APPLY, SPLIT>(mb.k, mx[cur].n, mx[cur], mx[cur ^ 1], p, st);
     if (err != cudaSuccess) return err;
   }
-  return tall ? launch_early(ns_update_kernel<true>, tiles_t, dim3(256), 0, st, t, x[cur], o.s, o.l, 1.0f / scale, lr, rms)
-              : launch_early(ns_update_kernel<false>, tiles_t, dim3(256), 0, st, t, x[cur], o.s, o.l, 1.0f / scale, lr, rms);
+  const auto update = tall ? ns_update_kernel<true> : ns_update_kernel<false>;
+  return launch_early(update, tiles_t, dim3(256), 0, st, t, reinterpret_cast<const __half*>(x[cur]),
+                      SPLIT ? reinterpret_cast<const __half*>(lo[cur]) : nullptr, o.s, o.l, 1.0f / scale, lr, rms);
 }
 
 }  // namespace moe
@@ -939,14 +1024,18 @@ static moe_status muon_check(const moe_muon_tensor* ts, int32_t count) {
 }
 
 size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, size_t limit) {
-  if (muon_check(tensors, count) != MOE_OK) return 0;
+  return moe_muon_workspace_size_with(tensors, count, limit, MOE_MUON_FP16);
+}
+
+size_t moe_muon_workspace_size_with(const moe_muon_tensor* tensors, int32_t count, size_t limit, int32_t products) {
+  if (muon_check(tensors, count) != MOE_OK || (products != MOE_MUON_FP16 && products != MOE_MUON_FP32)) return 0;
   size_t most = 0;
   for (int i = 0; i < count; ++i) {
     // tensors of one shape run together
     size_t batch = 0;
     for (int j = 0; j < count; ++j)
       if (tensors[j].rows == tensors[i].rows && tensors[j].cols == tensors[i].cols) batch += tensors[j].batch;
-    const size_t one = ns_matrix_bytes(ns_shape(tensors[i].rows, tensors[i].cols));
+    const size_t one = ns_matrix_bytes(ns_shape(tensors[i].rows, tensors[i].cols), products == MOE_MUON_FP32);
     most = std::max(most, one * std::min(batch, std::max<size_t>(1, limit / one)));
   }
   return most;
@@ -954,16 +1043,17 @@ size_t moe_muon_workspace_size(const moe_muon_tensor* tensors, int32_t count, si
 
 moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, void* workspace,
                          size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream) {
-  return moe_muon_step_floor(hyper, tensors, count, 0.0, workspace, workspace_bytes, control, dev_status, stream);
+  return moe_muon_step_with(hyper, tensors, count, 0.0, MOE_MUON_FP16, workspace, workspace_bytes, control, dev_status, stream);
 }
 
-moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
-                               void* workspace, size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status,
-                               void* stream) {
+moe_status moe_muon_step_with(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
+                              int32_t products, void* workspace, size_t workspace_bytes, const moe_adamw_control* control,
+                              int32_t* dev_status, void* stream) {
   if (!hyper || !dev_status) return MOE_ERR_INVALID_ARG;
   const moe_muon_hyper& h = *hyper;
   const float lr = static_cast<float>(h.lr), floor = static_cast<float>(norm_floor);
-  if (!(floor >= 0.0f) || !std::isfinite(floor)) return MOE_ERR_INVALID_ARG;
+  if (!(floor >= 0.0f) || !std::isfinite(floor) || (products != MOE_MUON_FP16 && products != MOE_MUON_FP32)) return MOE_ERR_INVALID_ARG;
+  const bool split = products == MOE_MUON_FP32;
   if (!(lr >= 0.0f) || !std::isfinite(lr) || !(h.momentum >= 0.0 && static_cast<float>(h.momentum) < 1.0f) || !(h.rms >= 0.0) ||
       !std::isfinite(h.rms) || h.steps < 1 || h.steps > MOE_MUON_MAX_STEPS)
     return MOE_ERR_INVALID_ARG;
@@ -977,7 +1067,7 @@ moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tenso
     if (t.batch == 0) continue;
     if (!t.grad || (!t.out == !t.w) || (!t.w != !t.m) || (t.w16 && !t.w)) return MOE_ERR_INVALID_ARG;
     if (t.w && (!std::isfinite(t.weight_decay) || !std::isfinite(ns_rms(h, t.rows, t.cols)))) return MOE_ERR_INVALID_ARG;
-    need = std::max(need, ns_matrix_bytes(ns_shape(t.rows, t.cols)));
+    need = std::max(need, ns_matrix_bytes(ns_shape(t.rows, t.cols), split));
   }
   if (need > 0 && (!workspace || workspace_bytes < need)) return MOE_ERR_WORKSPACE;
   if (!ptr_aligned16(workspace)) return MOE_ERR_ALIGNMENT;
@@ -992,7 +1082,7 @@ moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tenso
     if (done) continue;
     // the tensors like this one, in order, in chunks that fit the workspace
     const moe_muon_tensor& f = tensors[i];
-    const int fit = static_cast<int>(std::min<size_t>(workspace_bytes / ns_matrix_bytes(ns_shape(f.rows, f.cols)), 65535));
+    const int fit = static_cast<int>(std::min<size_t>(workspace_bytes / ns_matrix_bytes(ns_shape(f.rows, f.cols), split), 65535));
     NsTensors t{};
     t.rows = f.rows; t.cols = f.cols; t.grad_type = f.grad_type; t.out_type = f.out_type;
     t.momentum = static_cast<float>(h.momentum); t.nesterov = h.nesterov != 0; t.control = control;
@@ -1000,7 +1090,8 @@ moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tenso
     auto flush = [&]() -> cudaError_t {
       if (batch == 0) return cudaSuccess;
       t.first[t.count] = batch;
-      const cudaError_t e = ns_chunk(t, batch, h, floor, lr, workspace, dev_status, s);
+      const cudaError_t e = split ? ns_chunk<true>(t, batch, h, floor, lr, workspace, dev_status, s)
+                                  : ns_chunk<false>(t, batch, h, floor, lr, workspace, dev_status, s);
       t.count = 0; t.skip0 = 0; batch = 0;
       return e;
     };

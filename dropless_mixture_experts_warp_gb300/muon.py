@@ -5,7 +5,9 @@
 
 Every tensor is a matrix [m, n] or a batch of them [..., m, n] (an expert weight [E, 2f, d] holds a gate and an up
 matrix: pass its view(2 * E, f, d)).  The momentum is orthogonalised by Newton-Schulz products and taken off the fp32
-weights; `copies` (each or any None) get them rounded to bf16.  orthogonalize() does that alone.  The steps run in
+weights; `copies` (each or any None) get them rounded to bf16.  orthogonalize() does that alone.  The products are as good
+as fp32's (operands in two fp16 parts), or with products="fp16" take a third of the multiplying and leave the orthogonal
+factor some 1e-3 off (include/moe.h says how far), a step's fp32 weights some 1e-6.  The steps run in
 libmoe.so's kernels (moe_muon_* of include/moe.h, where the formulas are); norms, routers' biases and other vectors
 are optim.py's.
 """
@@ -34,6 +36,7 @@ class Plan:
     status: torch.Tensor
     hyper: B.moe_muon_hyper
     device: torch.device
+    products: int
 
 
 @dataclass
@@ -44,6 +47,7 @@ class Workspace:
     status: torch.Tensor
     hyper: B.moe_muon_hyper
     device: torch.device
+    products: int
 
 
 def _sides(shape):
@@ -81,12 +85,19 @@ def _hyper(lr, momentum, rms, nesterov, coefficients):
     return h
 
 
-def _allocate(table, n, limit, device):
-    return (torch.empty(max(16, B.moe_muon_workspace_size(table, n, limit)), dtype=torch.uint8, device=device),
+def _products(name):
+    if name not in B.MUON_PRODUCTS:
+        raise ValueError('products: "fp32" or "fp16"')
+    return B.MUON_PRODUCTS[name]
+
+
+def _allocate(table, n, limit, device, products):
+    return (torch.empty(max(16, B.moe_muon_workspace_size_with(table, n, limit, products)), dtype=torch.uint8, device=device),
             torch.zeros(1, dtype=torch.int32, device=device))
 
 
-def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COEFFICIENTS, workspace=WORKSPACE) -> Plan:
+def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COEFFICIENTS, workspace=WORKSPACE,
+         products="fp32") -> Plan:
     """weights: fp32; grads: bf16 or fp32; copies: bf16 or None; weight_decay: one number or one a tensor.  The
     momentum starts at zero, or is the one given (a resumed run's, fp32).  No tensor may share memory with another, but
     gradients with each other.  workspace: bytes of scratch at most; a plan's
@@ -118,8 +129,9 @@ def plan(weights, grads, copies=None, weight_decay=0.0, m=None, coefficients=COE
         t.w16 = None if copies[i] is None else copies[i].data_ptr()
         t.weight_decay, t.grad_type = decay[i], B.TYPE["bf16" if low else "fp32"]
     _apart([_span(t, True) for t in weights + m + copies if t is not None] + [_span(t, False) for t in grads])
-    return Plan(weights, grads, copies, m, table, *_allocate(table, n, workspace, device),
-                _hyper(0.0, 0.0, 0.0, True, coefficients), device)
+    kind = _products(products)
+    return Plan(weights, grads, copies, m, table, *_allocate(table, n, workspace, device, kind),
+                _hyper(0.0, 0.0, 0.0, True, coefficients), device, kind)
 
 
 def step(p: Plan, lr, momentum=0.95, rms=0.2, nesterov=True, control=None, stream=None, eps=1e-7):
@@ -133,17 +145,18 @@ def step(p: Plan, lr, momentum=0.95, rms=0.2, nesterov=True, control=None, strea
         B.check_tensor(raw, torch.int32, (4,), p.device)
     h = p.hyper
     h.lr, h.momentum, h.rms, h.nesterov = lr, momentum, rms, int(nesterov)
-    B.moe_muon_step_floor(h, p.table, len(p.weights), eps, p.workspace, p.workspace.numel(), raw, p.status, stream)
+    B.moe_muon_step_with(h, p.table, len(p.weights), eps, p.products, p.workspace, p.workspace.numel(), raw, p.status, stream)
 
 
-def workspace(shapes, coefficients=COEFFICIENTS, limit=WORKSPACE, device="cuda") -> Workspace:
-    """What orthogonalize() needs for tensors of these shapes."""
+def workspace(shapes, coefficients=COEFFICIENTS, limit=WORKSPACE, device="cuda", products="fp32") -> Workspace:
+    """What orthogonalize() needs for tensors of these shapes, and how it multiplies."""
     shapes = [torch.Size(s) for s in shapes]
     table = (B.moe_muon_tensor * max(1, len(shapes)))()
     for t, s in zip(table, shapes):
         t.batch, t.rows, t.cols = _sides(s)
-    ws, status = _allocate(table, len(shapes), limit, device)
-    return Workspace(shapes, table, ws, status, _hyper(0.0, 0.0, 0.0, False, coefficients), ws.device)
+    kind = _products(products)
+    ws, status = _allocate(table, len(shapes), limit, device, kind)
+    return Workspace(shapes, table, ws, status, _hyper(0.0, 0.0, 0.0, False, coefficients), ws.device, kind)
 
 
 def orthogonalize(xs, outs, w: Workspace, stream=None):
@@ -163,7 +176,7 @@ def orthogonalize(xs, outs, w: Workspace, stream=None):
         if t.grad != t.out or t.grad_type != t.out_type:
             spans.append(_span(x, False))
     _apart(spans)
-    B.moe_muon_step(w.hyper, w.table, len(xs), w.workspace, w.workspace.numel(), None, w.status, stream)
+    B.moe_muon_step_with(w.hyper, w.table, len(xs), 0.0, w.products, w.workspace, w.workspace.numel(), None, w.status, stream)
     return outs
 
 

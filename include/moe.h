@@ -847,13 +847,20 @@ moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* ten
                          size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status, void* stream);
 
 /*
- * The same with X_0 = U / max(|U|_F, norm_floor) (finite, >= 0; 0 is moe_muon_step): matrices
- * whose U has all but gone, an expert's without tokens for a while, take steps that fade with
- * it instead of full ones along what is left of its direction.
+ * The same with what the caller chooses:
+ *   norm_floor (finite, >= 0; moe_muon_step: 0): X_0 = U / max(|U|_F, norm_floor).  Matrices whose U
+ *     has all but gone, an expert's without tokens for a while, then take steps that fade with it
+ *     instead of full ones along what is left of its direction.
+ *   products (moe_muon_step: MOE_MUON_FP16): MOE_MUON_FP32 holds the operands of all products in
+ *     two fp16 parts and leaves out the second parts' product alone, so that X is as fp32 products
+ *     give it (the roundings cost 3e-6 of its norm at 1024 x 1024, less for smaller matrices); it
+ *     takes three times the multiplying and its own workspace size.
  */
-moe_status moe_muon_step_floor(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
-                               void* workspace, size_t workspace_bytes, const moe_adamw_control* control, int32_t* dev_status,
-                               void* stream);
+enum { MOE_MUON_FP16 = 0, MOE_MUON_FP32 = 1 };
+size_t moe_muon_workspace_size_with(const moe_muon_tensor* tensors, int32_t count, size_t limit, int32_t products);
+moe_status moe_muon_step_with(const moe_muon_hyper* hyper, const moe_muon_tensor* tensors, int32_t count, double norm_floor,
+                              int32_t products, void* workspace, size_t workspace_bytes, const moe_adamw_control* control,
+                              int32_t* dev_status, void* stream);
 
 #ifdef __cplusplus
 }

@@ -138,3 +138,32 @@ def newton_schulz_rounded(x, coefficients=COEFFICIENTS, eps=0.0):
         hi = h(v)
         lo = h(v - hi)
     return hi / scale
+
+
+def newton_schulz_split(x, coefficients=COEFFICIENTS, eps=0.0, step=2.0 ** -23):
+    """newton_schulz as the kernels round it with operands in two fp16 parts, and with what their fp32 sums may lose: at
+    every step of 16 along a contraction up to a unit in the last place of the largest value that the sum reaches, here
+    always towards 0 (step=0: the operands' roundings alone)."""
+    def two(v):
+        hi = v.astype(np.float16).astype(np.float64)
+        return hi, (v - hi).astype(np.float16).astype(np.float64)
+
+    def product(a, b):
+        v = a[0] @ b[0] + a[0] @ b[1] + a[1] @ b[0]
+        lost = (-(-a[0].shape[1] // 16) + 2) * step
+        return v - np.sign(v) * np.minimum(lost * (np.abs(a[0]) @ np.abs(b[0])), np.abs(v)) if step else v
+
+    x = x.T if x.shape[0] > x.shape[1] else x
+    n = max(np.linalg.norm(x), eps)
+    length = up(x.shape[1])
+    scale = 1.0
+    while scale * scale * 4 <= length:
+        scale *= 2
+    x = two(scale * x / n if n > 0 else np.zeros_like(x))
+    for k, (a, b, c) in enumerate(coefficients):
+        late = k >= 1 and k >= len(coefficients) - 2
+        u, t, eye = 0.5 * late, (a - 1) * late, np.eye(x[0].shape[0])
+        A = two(product(x, (x[0].T, x[1].T)) / scale ** 2 - u * eye)
+        B = two(c * product(A, A) + (b + 2 * u * c) * (A[0] + A[1]) + (b * u + c * u * u + t) * eye)
+        x = two((a - t) * (x[0] + x[1]) + product(B, x))
+    return (x[0] + x[1]) / scale

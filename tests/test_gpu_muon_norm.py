@@ -12,6 +12,7 @@ from oracle import blocks as ob
 from test_gpu_muon import matrices, near
 
 pytestmark = pytest.mark.gpu
+both = pytest.mark.parametrize("products", ["fp32", "fp16"])
 SHAPES = [(96, 160), (40, 7), (300, 200), (129, 257)]      # the first two in one block, the others through the workspace
 
 
@@ -20,51 +21,55 @@ def _gpu():
     need_gpu()
 
 
-def orthogonal(x):
+def orthogonal(x, products):
     from dropless_mixture_experts_warp_gb300 import muon
-    w = muon.workspace([x.shape])
+    w = muon.workspace([x.shape], products=products)
     o = torch.empty(x.shape, device="cuda")
     muon.orthogonalize([x.cuda()], [o], w)
     muon.check(w)
     return o
 
 
+@both
 @pytest.mark.parametrize("m,n", SHAPES)
 @pytest.mark.parametrize("kind", [torch.float32, torch.bfloat16])
-def test_any_scale(m, n, kind):
+def test_any_scale(m, n, kind, products):
     """x times a power of two has x's orthogonal factor, bit for bit, also where squares of its elements are below fp32."""
     x = matrices(np.random.default_rng(m), 1, m, n, kind, scale=1.0)
-    want = orthogonal(x)
+    want = orthogonal(x, products)
     near(want[0], x[0].double().numpy(), torch.float32)
     for e in (30, -20, -45, -55, -62, -66, -70, -75, -90):
         y = x * 2.0 ** e
         assert torch.equal(y.double(), x.double() * 2.0 ** e)      # nothing of x is lost
-        assert torch.equal(orthogonal(y), want), e
+        assert torch.equal(orthogonal(y, products), want), e
 
 
+@both
 @pytest.mark.parametrize("m,n", SHAPES)
-def test_subnormal_elements(m, n):
+def test_subnormal_elements(m, n, products):
     x = matrices(np.random.default_rng(n), 1, m, n, torch.float32, scale=2.0 ** -136)
     assert 0 < x.abs().max() < 2.0 ** -126
-    near(orthogonal(x)[0], x[0].double().numpy(), torch.float32)
+    near(orthogonal(x, products)[0], x[0].double().numpy(), torch.float32)
 
 
+@both
 @pytest.mark.parametrize("m,n", SHAPES)
-def test_matrices_of_different_sizes_together(m, n):
+def test_matrices_of_different_sizes_together(m, n, products):
     """Each matrix of a batch by its own norm."""
     x = matrices(np.random.default_rng(3), 5, m, n, torch.float32, scale=1.0)
     for i, e in enumerate((0, -70, -100, 20, -60)):
         x[i] *= 2.0 ** e
     x[2] = 0.0
-    o = orthogonal(x)
+    o = orthogonal(x, products)
     assert (o[2] == 0).all()
     for i in (0, 1, 3, 4):
         near(o[i], x[i].double().numpy(), torch.float32)
 
 
+@both
 @pytest.mark.parametrize("m,n", SHAPES)
 @pytest.mark.parametrize("rank", [1, 4, None])
-def test_idle_expert(m, n, rank):
+def test_idle_expert(m, n, rank, products):
     """An expert without tokens has gradients of zeros: its momentum shrinks by 0.95 a step until it is gone, and its
     weights stay finite."""
     from dropless_mixture_experts_warp_gb300 import muon
@@ -75,7 +80,7 @@ def test_idle_expert(m, n, rank):
         mom = torch.from_numpy(1e-4 * rng.standard_normal((2, m, rank)) @ rng.standard_normal((2, rank, n))).float()
     w = torch.from_numpy(rng.standard_normal((2, m, n)).astype(np.float32) * 0.02).cuda()
     low = w.bfloat16()
-    p = muon.plan([w], [torch.zeros(2, m, n, device="cuda")], copies=[low], m=[mom.cuda()])
+    p = muon.plan([w], [torch.zeros(2, m, n, device="cuda")], copies=[low], m=[mom.cuda()], products=products)
     for t in range(1, 2101):
         muon.step(p, lr=1e-3)
         if t % 25 == 0:
@@ -106,9 +111,10 @@ def test_idle_expert_comes_to_rest(m, n):
     assert (w - rest).norm().item() <= 2 * 20 * size * 2.0 ** -29
 
 
+@both
 @pytest.mark.parametrize("m,n", SHAPES)
 @pytest.mark.parametrize("times", [0.0, 0.3, 1.0, 5.0, 1e4])
-def test_floor(m, n, times):
+def test_floor(m, n, times, products):
     """X_0 = U / max(|U|, eps), against float64."""
     from dropless_mixture_experts_warp_gb300 import muon
     rng = np.random.default_rng(m + 1)
@@ -116,7 +122,7 @@ def test_floor(m, n, times):
     w0 = torch.from_numpy(rng.standard_normal((m, n)).astype(np.float32) * 0.02)
     eps = times * g.double().norm().item()
     w = w0.cuda()
-    p = muon.plan([w], [g.cuda()])
+    p = muon.plan([w], [g.cuda()], products=products)
     lr, rms = 2e-2, 0.2
     muon.step(p, lr=lr, momentum=0.0, rms=rms, nesterov=False, eps=eps)
     muon.check(p)

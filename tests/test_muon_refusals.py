@@ -7,11 +7,29 @@ from test_blocks_refusals import B, P, muon_hyper, muon_table, status  # noqa: F
 
 
 def test_floor(B):  # noqa: F811
-    run = lambda floor: status(B, "moe_muon_step_floor", muon_hyper(B), muon_table(B), 1, floor, P, 1 << 30, None, P)  # noqa: E731
+    run = lambda floor: status(B, "moe_muon_step_with", muon_hyper(B), muon_table(B), 1, floor, 1, P, 1 << 30, None, P)  # noqa: E731
     for floor in (-1e-9, float("nan"), float("inf"), 1e39):
         assert run(floor) == 1, floor
-    assert status(B, "moe_muon_step_floor", muon_hyper(B), muon_table(B, batch=-1), 1, 1e-7, P, 1 << 30, None, P) == 1
-    assert B.moe_muon_step_floor(muon_hyper(B), muon_table(B), 0, 1e-7, None, 0, None, P, stream=0) == 0
+    assert status(B, "moe_muon_step_with", muon_hyper(B), muon_table(B, batch=-1), 1, 1e-7, 1, P, 1 << 30, None, P) == 1
+    assert B.moe_muon_step_with(muon_hyper(B), muon_table(B), 0, 1e-7, 1, None, 0, None, P, stream=0) == 0
+
+
+def test_products(B):  # noqa: F811
+    """Operands in two parts need a workspace of their own size; other kinds are refused."""
+    from dropless_mixture_experts_warp_gb300 import muon
+    t = muon_table(B)
+    need = [B.moe_muon_workspace_size_with(t, 1, 0, kind) for kind in (0, 1)]
+    assert need[0] == B.moe_muon_workspace_size(t, 1, 0) < need[1]
+    for kind in (0, 1):
+        assert status(B, "moe_muon_step_with", muon_hyper(B), t, 1, 0.0, kind, P, need[kind] - 1, None, P) == 4
+        assert B.moe_muon_workspace_size_with(t, 1, 1 << 30, kind) == 2 * need[kind]
+    for kind in (-1, 2):
+        assert status(B, "moe_muon_step_with", muon_hyper(B), t, 1, 0.0, kind, P, 1 << 30, None, P) == 1
+        assert B.moe_muon_workspace_size_with(t, 1, 0, kind) == 0
+    z = [torch.zeros(4, 5)]
+    for make in (lambda: muon.plan(z, [torch.zeros(4, 5)], products="bf16"), lambda: muon.workspace([(4, 5)], device="cpu", products=1)):
+        with pytest.raises(ValueError, match="products"):
+            make()
 
 
 def test_numbers_as_the_kernels_use_them(B):  # noqa: F811
@@ -43,7 +61,7 @@ def test_outputs_that_share_memory(B, monkeypatch):  # noqa: F811
     from dropless_mixture_experts_warp_gb300 import muon
     calls = []
     monkeypatch.setattr(muon.B, "check_device", lambda *a: None)
-    monkeypatch.setattr(muon.B, "moe_muon_step", lambda *a: calls.append(a))
+    monkeypatch.setattr(muon.B, "moe_muon_step_with", lambda *a: calls.append(a))
     both = torch.zeros(3, 4, 5)
     ws = muon.workspace([(2, 4, 5), (2, 4, 5)], device="cpu")
     x, o = ([torch.zeros(2, 4, 5) for _ in range(2)] for _ in range(2))
