@@ -7,8 +7,10 @@
 //
 // Arithmetic: tensor-core products of fp16 operands with fp32 sums.  Every matrix here is bounded (singular
 // values below 1.3), so fp16's 11 bits serve better than bf16's 8.  The caller chooses between
-//   SPLIT: X, A and B each in two fp16 parts, 22 bits, and three products (lo hi + hi lo + hi hi) for each: what fp32
-//     products give (the roundings cost 3e-6 of the factor's norm at 1024 x 1024, less for smaller matrices);
+//   SPLIT: X, A and B each in two fp16 parts, 22 bits, and three products (lo hi + hi lo + hi hi) for each.  The roundings
+//     cost 3e-6 of the factor's norm at 1024 x 1024 and less for smaller matrices; what tensor-core sums lose comes on
+//     top of it with long contractions (1e-6 to 2e-6 off up to 128 x 256, where fp32 products are too, 7e-6 at 1024 x 1024,
+//     4e-5 at 1536 x 4096);
 //   one part, a third of the multiplying: on gaussian matrices with 128 rows or more the result is 0.8e-3 to 1.2e-3 off,
 //     relative to its norm (bf16 operands: 1.1e-2); with fewer, up to 3e-3, and up to 8e-3 below 16.
 // X is held times a power of two near sqrt(l), so that its entries stay normal numbers.  The addend a X would carry X's
@@ -21,8 +23,8 @@
 // A and B are symmetric: only tiles on and above the diagonal are computed, the others mirrored.
 //
 // Bound: tensor cores, s s l / 2 + s s s / 2 + s s l multiply-adds a step and matrix.  48 matrices of 1536 x 4096, five
-// steps: 7.9 to 8.0 ms, of which the products 6.3 (64 % of the measured bf16 rate; operands from shared memory and the power
-// limit), the passes over momenta, weights and X 1.6.
+// steps: 18.2 ms, of which the products 16.4 (73 % of the measured bf16 rate for three products each; operands from shared
+// memory and the power limit), the passes over momenta, weights and X 1.8; with one part 7.9 to 8.0 ms, 6.3 (64 %) and 1.6.
 #include "around.cuh"
 #include "kernels.h"
 #include "pipe.cuh"
@@ -611,7 +613,7 @@ __global__ void __launch_bounds__(256) ns_update_kernel(const NsTensors p, const
 //
 // A matrix of at most 128 x 256 goes through the whole step in one block: X in fp32 registers (a thread has a
 // row, half of the columns), its fp16 form, A and B in shared memory, products in tensor memory.  Fifteen products of
-// one tile each are latency: 26 us for six matrices of 131 x 72, 98 with 18 launches.
+// one tile each are latency: 39 us for six matrices of 131 x 72 (one part: 26; 98 with 18 launches).
 // X's fp16 form lies in blocks of 64 columns, 128 rows of 128 bytes each (128-byte swizzle), which the MMA reads
 // K-major in X X^T and MN-major in B X.
 

@@ -811,10 +811,11 @@ moe_status moe_adamw_values(const moe_adamw_tensor* tensors, int32_t count, int3
  *   w = w - lr (weight_decay w + rms sqrt(max(rows, cols)) X);   w16 = bf16(w)
  * m, w and the sums of squares in fp32.  |U|_F is right for every U whose sum of squares does not
  * overflow, fp32's smallest numbers included; where it overflows (|U|_F from 2^64 on) X is NaN.
- * The products on fp16 operands with fp32 sums.  With the coefficients 3.4445, -4.7750, 2.0315 five
- * times X is off by less than 1.5e-3 of its norm where the shorter side is 128 or more, 4e-3 from 16
- * on, 1e-2 below (gaussian matrices and strong directions under noise).  With `out` in place of m and w a tensor's
- * gradient itself is orthogonalised: out = X, m, w and w16 NULL (momentum, lr and rms are not used).
+ * The products on fp16 operands with fp32 sums (moe_muon_step_with has better ones).  With the
+ * coefficients 3.4445, -4.7750, 2.0315 five times X is off by less than 1.5e-3 of its norm where the
+ * shorter side is 128 or more, 4e-3 from 16 on, 1e-2 below (gaussian matrices and strong directions
+ * under noise).  With `out` in place of m and w a tensor's gradient itself is orthogonalised:
+ * out = X, m, w and w16 NULL (momentum, lr and rms are not used).
  * A gradient that is not finite reaches its whole matrix.
  */
 enum { MOE_MUON_MAX_STEPS = 16 };
@@ -852,9 +853,10 @@ moe_status moe_muon_step(const moe_muon_hyper* hyper, const moe_muon_tensor* ten
  *     has all but gone, an expert's without tokens for a while, then take steps that fade with it
  *     instead of full ones along what is left of its direction.
  *   products (moe_muon_step: MOE_MUON_FP16): MOE_MUON_FP32 holds the operands of all products in
- *     two fp16 parts and leaves out the second parts' product alone, so that X is as fp32 products
- *     give it (the roundings cost 3e-6 of its norm at 1024 x 1024, less for smaller matrices); it
- *     takes three times the multiplying and its own workspace size.
+ *     two fp16 parts (22 bits) and leaves out the second parts' product alone: X is off by less than
+ *     1e-5 + 7.5e-8 max(rows, cols) of its norm (the sums' share grows with their length; seen: 2e-6
+ *     up to 128 x 256, 7e-6 at 1024 x 1024, 4e-5 at 1536 x 4096).  It takes three times the
+ *     multiplying and its own workspace size.
  */
 enum { MOE_MUON_FP16 = 0, MOE_MUON_FP32 = 1 };
 size_t moe_muon_workspace_size_with(const moe_muon_tensor* tensors, int32_t count, size_t limit, int32_t products);
